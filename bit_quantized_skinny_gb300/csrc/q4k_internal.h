@@ -3,6 +3,8 @@
 #include <cstdint>
 #include <cuda_runtime_api.h>
 
+#include "qmm.h"
+
 namespace q4k {
 
 // Weight formats (the qmm_format codes of the C ABI).
@@ -80,6 +82,19 @@ cudaError_t launch_pack_dev(const float* W, int64_t N, int64_t K, void* out, cud
 cudaError_t read_and_clear_pack_status(unsigned* out);
 cudaError_t read_and_clear_fma_status(unsigned* out);
 cudaError_t read_and_clear_tc_status(unsigned* out);
+
+// The attention half of a layer (argument structs of the C ABI, checked by the caller).  Each
+// file keeps a status word; kErrIndex: a device-side index was out of range.
+constexpr unsigned kErrIndex = 4u;
+cudaError_t launch_norm_rope(const qmm_norm_rope_args& a, cudaStream_t stream);
+cudaError_t read_and_clear_norm_rope_status(unsigned* out);
+cudaError_t launch_attn(const qmm_attn_args& a, void* workspace, cudaStream_t stream);
+size_t attn_workspace_bytes(const qmm_attn_args& a);
+cudaError_t read_and_clear_attn_status(unsigned* out);
+cudaError_t launch_lora(const qmm_lora_entry* entries, int count, const int32_t* ids, int M, int rank_max,
+                        void* workspace, cudaStream_t stream);
+size_t lora_workspace_bytes(const qmm_lora_entry* entries, int count, int M, int rank_max);
+cudaError_t read_and_clear_lora_status(unsigned* out);
 
 // Host packers (qmm_pack.cpp).  Return 0, or 6 on non-finite input / fp16 overflow.
 int pack_q4k(const float* W, int64_t N, int64_t K, uint8_t* out, int threads);

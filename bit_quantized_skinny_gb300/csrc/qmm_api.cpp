@@ -33,6 +33,23 @@ qmm_status check_shape(int64_t N, int64_t K) {
   return QMM_OK;
 }
 
+bool valid_dtype(int t) { return t >= QMM_F32 && t <= QMM_F16; }
+bool half_type(int t) { return t == QMM_BF16 || t == QMM_F16; }
+
+// Sizes and types of a qmm_attn_shared call.
+qmm_status check_attn_shape(const qmm_attn_args& a) {
+  if (a.T < 0 || a.T >= (1 << 20) || a.B < 0 || a.B > QMM_ATTN_MAX_STREAMS) return QMM_ERR_SHAPE;
+  if (a.D != 64 && a.D != 128) return QMM_ERR_SHAPE;
+  if (a.Hk < 1 || a.Hq < 1 || a.Hq > 1024 || a.Hq % a.Hk != 0 || a.Hq / a.Hk > 64) return QMM_ERR_SHAPE;
+  if (a.page_size < 16 || a.page_size > 4096 || (a.page_size & (a.page_size - 1))) return QMM_ERR_SHAPE;
+  if (a.n_slots < a.page_size || a.n_slots % a.page_size || a.n_slots >= (int64_t(1) << 31)) return QMM_ERR_SHAPE;
+  if (a.prefix_len < 0 || a.prefix_len >= (1 << 30)) return QMM_ERR_SHAPE;
+  if (a.pages_per_stream < 0 || a.pages_per_stream >= (1 << 30) / a.page_size) return QMM_ERR_SHAPE;
+  const int64_t w = (int64_t)a.Hq * a.D;
+  if (a.ldq < w || a.ldo < w) return QMM_ERR_SHAPE;
+  return half_type(a.type) ? QMM_OK : QMM_ERR_TYPE;
+}
+
 bool valid_format(int fmt) { return fmt >= QMM_FMT_Q4K && fmt <= QMM_FMT_Q6K; }
 
 qmm_status check_job(const void* W, int64_t N, int64_t K, const uint16_t* X, const float* Y) {
@@ -388,6 +405,87 @@ int qmm_select_variant_batched(const qmm_entry* entries_host, int count, int M) 
   return select_variant_jobs(jobs, count, M);
 }
 
+qmm_status qmm_norm_rope(const qmm_norm_rope_args* args_host, cudaStream_t stream) {
+  if (!args_host) return QMM_ERR_NULL;
+  const qmm_norm_rope_args& a = *args_host;
+  if (a.T < 0 || a.Hq < 1 || a.Hk < 0 || a.Hq > 65535 || a.Hk > 32767 || a.Hq + 2 * a.Hk > 65535) return QMM_ERR_SHAPE;
+  if (a.D != 64 && a.D != 128 && a.D != 256) return QMM_ERR_SHAPE;
+  if (a.rot < 0 || a.rot > a.D || a.rot % 16 != 0) return QMM_ERR_SHAPE;
+  if (!valid_dtype(a.in_type) || !half_type(a.out_type)) return QMM_ERR_TYPE;
+  if (a.T == 0) return QMM_OK;
+  const bool keys = a.Hk > 0, values = keys && a.V;
+  if (!a.Q || !a.Q_out || (keys && (!a.K || !a.K_cache || !a.slots)) || (values && !a.V_cache)) return QMM_ERR_NULL;
+  if (a.rot > 0 && (!a.cos_sin || !a.positions)) return QMM_ERR_NULL;
+  if (a.rot > 0 && a.max_pos < 1) return QMM_ERR_SHAPE;
+  const int64_t wq = (int64_t)a.Hq * a.D, wk = (int64_t)a.Hk * a.D;
+  if (a.ldq < wq || a.ldqo < wq || (keys && (a.ldk < wk || a.n_slots < 1)) || (values && a.ldv < wk)) return QMM_ERR_SHAPE;
+  const int64_t in_step = a.in_type == QMM_F32 ? 4 : 8;   // elements in 16 bytes
+  if (!aligned(a.Q, 16) || !aligned(a.Q_out, 16) || !aligned(a.q_weight, 16) || a.ldq % in_step || a.ldqo % 8)
+    return QMM_ERR_ALIGN;
+  if (keys && (!aligned(a.K, 16) || !aligned(a.K_cache, 16) || !aligned(a.k_weight, 16) || !aligned(a.slots, 8) ||
+               a.ldk % in_step))
+    return QMM_ERR_ALIGN;
+  if (values && (!aligned(a.V, 16) || !aligned(a.V_cache, 16) || a.ldv % in_step)) return QMM_ERR_ALIGN;
+  if (a.rot > 0 && (!aligned(a.cos_sin, 16) || !aligned(a.positions, 4))) return QMM_ERR_ALIGN;
+  const cudaError_t e = q4k::launch_norm_rope(a, stream);
+  return e == cudaSuccess ? QMM_OK : cuda_fail(e);
+}
+
+size_t qmm_attn_workspace_bytes(const qmm_attn_args* args_host) {
+  if (!args_host || check_attn_shape(*args_host) != QMM_OK) return 0;
+  return q4k::attn_workspace_bytes(*args_host);
+}
+
+qmm_status qmm_attn_shared(const qmm_attn_args* args_host, void* workspace_dev, size_t workspace_bytes,
+                           cudaStream_t stream) {
+  if (!args_host) return QMM_ERR_NULL;
+  const qmm_attn_args& a = *args_host;
+  const qmm_status s = check_attn_shape(a);
+  if (s != QMM_OK) return s;
+  if (a.T == 0) return QMM_OK;
+  if (!a.Q || !a.O || !a.K_cache || !a.V_cache || !a.row_starts || !workspace_dev) return QMM_ERR_NULL;
+  if ((a.prefix_len > 0 && !a.prefix_pages) || (a.B > 0 && (!a.kv_lens || (a.pages_per_stream > 0 && !a.pages))))
+    return QMM_ERR_NULL;
+  if (!aligned(a.Q, 16) || !aligned(a.O, 16) || !aligned(a.K_cache, 16) || !aligned(a.V_cache, 16) || a.ldq % 8 ||
+      a.ldo % 8 || !aligned(workspace_dev, 16))
+    return QMM_ERR_ALIGN;
+  if (!aligned(a.prefix_pages, 4) || !aligned(a.pages, 4) || !aligned(a.kv_lens, 4) || !aligned(a.row_starts, 4) ||
+      !aligned(a.lse, 4))
+    return QMM_ERR_ALIGN;
+  if (workspace_bytes < q4k::attn_workspace_bytes(a)) return QMM_ERR_BUFSIZE;
+  const cudaError_t e = q4k::launch_attn(a, workspace_dev, stream);
+  return e == cudaSuccess ? QMM_OK : cuda_fail(e);
+}
+
+size_t qmm_lora_workspace_bytes(const qmm_lora_entry* entries_host, int count, int M, int rank_max) {
+  if (!entries_host || count < 1 || count > QMM_LORA_MAX_ENTRIES || M < 1 || M > QMM_MAX_M || rank_max < 1 ||
+      rank_max > QMM_LORA_MAX_RANK)
+    return 0;
+  for (int k = 0; k < count; ++k)
+    if (check_shape(entries_host[k].N, entries_host[k].K) != QMM_OK) return 0;
+  return q4k::lora_workspace_bytes(entries_host, count, M, rank_max);
+}
+
+qmm_status qmm_run_lora(const qmm_lora_entry* entries_host, int count, const int32_t* ids_dev, int M, int rank_max,
+                        void* workspace_dev, size_t workspace_bytes, cudaStream_t stream) {
+  if (!entries_host || !ids_dev || !workspace_dev) return QMM_ERR_NULL;
+  if (count < 1 || count > QMM_LORA_MAX_ENTRIES) return QMM_ERR_COUNT;
+  if (M < 1 || M > QMM_MAX_M) return QMM_ERR_M_RANGE;
+  if (rank_max < 1 || rank_max > QMM_LORA_MAX_RANK) return QMM_ERR_SHAPE;
+  for (int k = 0; k < count; ++k) {
+    const qmm_lora_entry& e = entries_host[k];
+    if (!e.adapters || !e.X || !e.Y0 || !e.Y) return QMM_ERR_NULL;
+    const qmm_status s = check_shape(e.N, e.K);
+    if (s != QMM_OK) return s;
+    if (e.n_adapters < 1) return QMM_ERR_SHAPE;
+    if (!aligned(e.adapters, 8) || !aligned(e.X, 16) || !aligned(e.Y0, 4) || !aligned(e.Y, 4)) return QMM_ERR_ALIGN;
+  }
+  if (!aligned(ids_dev, 4) || !aligned(workspace_dev, 16)) return QMM_ERR_ALIGN;
+  if (workspace_bytes < q4k::lora_workspace_bytes(entries_host, count, M, rank_max)) return QMM_ERR_BUFSIZE;
+  const cudaError_t e = q4k::launch_lora(entries_host, count, ids_dev, M, rank_max, workspace_dev, stream);
+  return e == cudaSuccess ? QMM_OK : cuda_fail(e);
+}
+
 size_t qmm_stream_read_sink_words(void) {
   const int g = q4k::stream_read_grid();
   return g > 0 ? (size_t)g : 0;
@@ -412,11 +510,14 @@ size_t qmm_workspace_bytes_held(void) { return q4k::workspace_bytes_held(); }
 
 qmm_status qmm_device_status(unsigned* status_out) {
   if (!status_out) return QMM_ERR_NULL;
-  unsigned a = 0, b = 0, c = 0;
+  unsigned a = 0, b = 0, c = 0, d = 0, f = 0, g = 0;
   cudaError_t e = q4k::read_and_clear_fma_status(&a);
   if (e == cudaSuccess) e = q4k::read_and_clear_tc_status(&b);
   if (e == cudaSuccess) e = q4k::read_and_clear_pack_status(&c);
-  *status_out = a | b | c;
+  if (e == cudaSuccess) e = q4k::read_and_clear_norm_rope_status(&d);
+  if (e == cudaSuccess) e = q4k::read_and_clear_attn_status(&f);
+  if (e == cudaSuccess) e = q4k::read_and_clear_lora_status(&g);
+  *status_out = a | b | c | d | f | g;
   return e == cudaSuccess ? QMM_OK : cuda_fail(e);
 }
 
@@ -434,6 +535,7 @@ const char* qmm_strerror(qmm_status status) {
     case QMM_ERR_VARIANT: return "the requested kernel variant cannot run this shape";
     case QMM_ERR_SCRATCH: return "qmm_run_noalloc: the problem needs more than QMM_NOALLOC_SCRATCH_BYTES of scratch";
     case QMM_ERR_FORMAT: return "unknown weight format code";
+    case QMM_ERR_TYPE: return "element type not taken by this call";
   }
   return "unknown status";
 }

@@ -24,9 +24,11 @@ VARIANT_NAMES = {VARIANT_FMA: "fma", VARIANT_TC: "tc"}
 
 STATUS = {0: "QMM_OK", 1: "QMM_ERR_NULL", 2: "QMM_ERR_SHAPE", 3: "QMM_ERR_M_RANGE",
           4: "QMM_ERR_ALIGN", 5: "QMM_ERR_BUFSIZE", 6: "QMM_ERR_NONFINITE", 7: "QMM_ERR_CUDA",
-          8: "QMM_ERR_COUNT", 9: "QMM_ERR_VARIANT", 10: "QMM_ERR_SCRATCH", 11: "QMM_ERR_FORMAT"}
+          8: "QMM_ERR_COUNT", 9: "QMM_ERR_VARIANT", 10: "QMM_ERR_SCRATCH", 11: "QMM_ERR_FORMAT",
+          12: "QMM_ERR_TYPE"}
 
 FMT_Q4K, FMT_Q5K, FMT_NVFP4, FMT_INT4, FMT_Q6K = 0, 1, 2, 3, 4
+F32, BF16, F16 = 0, 1, 2   # element types of the attention half (qmm_dtype)
 FORMATS = {"q4k": FMT_Q4K, "q5k": FMT_Q5K, "q6k": FMT_Q6K, "nvfp4": FMT_NVFP4, "int4": FMT_INT4}
 
 # Every symbol include/qmm.h declares.
@@ -36,7 +38,9 @@ EXPORTS = ["qmm_packed_bytes", "qmm_pack", "qmm_run", "qmm_run_batched", "qmm_de
            "qmm_ffn_workspace_bytes", "qmm_run_ffn", "qmm_indexed_workspace_bytes", "qmm_run_indexed",
            "qmm_fmt_packed_bytes", "qmm_fmt_pack", "qmm_fmt_run", "qmm_fmt_dequant", "qmm_fmt_run_batched",
            "qmm_ffn_fused_workspace_bytes", "qmm_run_ffn_fused", "qmm_release", "qmm_workspace_bytes_held",
-           "qmm_stream_read", "qmm_stream_read_sink_words", "qmm_set_wait_limit", "qmm_pack_dev"]
+           "qmm_stream_read", "qmm_stream_read_sink_words", "qmm_set_wait_limit", "qmm_pack_dev",
+           "qmm_norm_rope", "qmm_attn_workspace_bytes", "qmm_attn_shared", "qmm_lora_workspace_bytes",
+           "qmm_run_lora"]
 NOALLOC_SCRATCH_BYTES = 4 << 20
 
 
@@ -58,6 +62,34 @@ class _Entry(ctypes.Structure):
 class _FmtEntry(ctypes.Structure):
     _fields_ = [("fmt", ctypes.c_int), ("Wq", ctypes.c_void_p), ("X", ctypes.c_void_p), ("Y", ctypes.c_void_p),
                 ("N", ctypes.c_int64), ("K", ctypes.c_int64)]
+
+
+class _NormRopeArgs(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int) for n in ("T", "Hq", "Hk", "D", "rot", "interleaved", "in_type", "out_type")] + [
+        ("eps", ctypes.c_float), ("Q", ctypes.c_void_p), ("K", ctypes.c_void_p), ("V", ctypes.c_void_p),
+        ("ldq", ctypes.c_int64), ("ldk", ctypes.c_int64), ("ldv", ctypes.c_int64),
+        ("q_weight", ctypes.c_void_p), ("k_weight", ctypes.c_void_p), ("cos_sin", ctypes.c_void_p),
+        ("max_pos", ctypes.c_int64), ("positions", ctypes.c_void_p), ("slots", ctypes.c_void_p),
+        ("Q_out", ctypes.c_void_p), ("ldqo", ctypes.c_int64), ("K_cache", ctypes.c_void_p),
+        ("V_cache", ctypes.c_void_p), ("n_slots", ctypes.c_int64)]
+
+
+class _AttnArgs(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int) for n in ("T", "B", "Hq", "Hk", "D", "page_size", "type")] + [
+        ("scale", ctypes.c_float), ("Q", ctypes.c_void_p), ("ldq", ctypes.c_int64), ("K_cache", ctypes.c_void_p),
+        ("V_cache", ctypes.c_void_p), ("n_slots", ctypes.c_int64), ("prefix_pages", ctypes.c_void_p),
+        ("prefix_len", ctypes.c_int64), ("pages", ctypes.c_void_p), ("pages_per_stream", ctypes.c_int64),
+        ("kv_lens", ctypes.c_void_p), ("row_starts", ctypes.c_void_p), ("O", ctypes.c_void_p),
+        ("ldo", ctypes.c_int64), ("lse", ctypes.c_void_p)]
+
+
+class _LoraAdapter(ctypes.Structure):
+    _fields_ = [("A", ctypes.c_void_p), ("Bt", ctypes.c_void_p), ("scale", ctypes.c_float), ("rank", ctypes.c_int)]
+
+
+class _LoraEntry(ctypes.Structure):
+    _fields_ = [("adapters", ctypes.c_void_p), ("n_adapters", ctypes.c_int), ("X", ctypes.c_void_p),
+                ("Y0", ctypes.c_void_p), ("Y", ctypes.c_void_p), ("N", ctypes.c_int64), ("K", ctypes.c_int64)]
 
 
 _lib = None
@@ -126,6 +158,16 @@ def load(path: str | None = None):
     lib.qmm_fmt_run_batched.restype = i32
     lib.qmm_fmt_dequant.argtypes = [i32, vp, i64, i64, vp, vp]
     lib.qmm_fmt_dequant.restype = i32
+    lib.qmm_norm_rope.argtypes = [ctypes.POINTER(_NormRopeArgs), vp]
+    lib.qmm_norm_rope.restype = i32
+    lib.qmm_attn_workspace_bytes.argtypes = [ctypes.POINTER(_AttnArgs)]
+    lib.qmm_attn_workspace_bytes.restype = ctypes.c_size_t
+    lib.qmm_attn_shared.argtypes = [ctypes.POINTER(_AttnArgs), vp, ctypes.c_size_t, vp]
+    lib.qmm_attn_shared.restype = i32
+    lib.qmm_lora_workspace_bytes.argtypes = [ctypes.POINTER(_LoraEntry), i32, i32, i32]
+    lib.qmm_lora_workspace_bytes.restype = ctypes.c_size_t
+    lib.qmm_run_lora.argtypes = [ctypes.POINTER(_LoraEntry), i32, vp, i32, i32, vp, ctypes.c_size_t, vp]
+    lib.qmm_run_lora.restype = i32
     lib.qmm_device_status.argtypes = [ctypes.POINTER(u32)]
     lib.qmm_device_status.restype = i32
     lib.qmm_strerror.argtypes = [i32]
@@ -326,6 +368,159 @@ def fmt_run_batched(entries, M: int, stream=None):
 def fmt_dequant(fmt: int, Wq, N: int, K: int, out, stream=None):
     _check(load().qmm_fmt_dequant(fmt, ctypes.c_void_p(Wq.data_ptr()), N, K, ctypes.c_void_p(out.data_ptr()),
                                   _stream_handle(stream)), "qmm_fmt_dequant")
+
+
+def _dtype_code(t) -> int:
+    import torch
+    code = {torch.float32: F32, torch.bfloat16: BF16, torch.float16: F16}.get(t.dtype)
+    if code is None:
+        raise QmmError(12, f"dtype {t.dtype}")
+    return code
+
+
+def _rows(t, what: str) -> int:
+    """Elements between the rows of a T x H x D tensor whose rows are dense (H x D contiguous)."""
+    if t.dim() != 3 or t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != t.shape[2]):
+        raise QmmError(2, what)
+    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1] * t.shape[2])
+
+
+def _dense(t, dtype, what: str) -> int:
+    """Data pointer of a contiguous tensor of that dtype (0 for None)."""
+    if t is None:
+        return 0
+    if t.dtype != dtype:
+        raise QmmError(12, what)
+    if not t.is_contiguous():
+        raise QmmError(2, what)
+    return t.data_ptr()
+
+
+def make_norm_rope(Q, K, V, q_weight, k_weight, cos_sin, positions, slots, Q_out, K_cache, V_cache,
+                   eps: float = 1e-6, interleaved: bool = False):
+    """Arguments of norm_rope().  Q: T x Hq x D, K and V: T x Hk x D (rows may be strided), one of
+    fp32, bf16 and fp16; Q_out: T x Hq x D and the caches n_slots x Hk x D, bf16 or fp16; weights
+    fp32 D or None; cos_sin fp32 max_pos x rot or None (no rotation); positions int32 T, slots int64
+    T.  K, V, slots and the caches may be None together, and V with V_cache.  The tensors are kept
+    alive by what is returned."""
+    import torch
+    T, Hq, D = Q.shape
+    a = _NormRopeArgs(T=T, Hq=Hq, Hk=0 if K is None else K.shape[1], D=D, rot=0 if cos_sin is None else cos_sin.shape[1],
+                      interleaved=int(interleaved), in_type=_dtype_code(Q), out_type=_dtype_code(Q_out), eps=eps)
+    a.Q, a.ldq, a.Q_out, a.ldqo = Q.data_ptr(), _rows(Q, "Q"), Q_out.data_ptr(), _rows(Q_out, "Q_out")
+    if tuple(Q_out.shape) != (T, Hq, D):
+        raise QmmError(2, "Q_out")
+    for t, cache, name in ((K, K_cache, "K"), (V, V_cache, "V")):
+        if t is None:
+            continue
+        if tuple(t.shape) != (T, a.Hk, D) or cache.shape[1:] != (a.Hk, D):
+            raise QmmError(2, name)
+        if t.dtype != Q.dtype:
+            raise QmmError(12, name)
+        setattr(a, name, t.data_ptr())
+        setattr(a, "ldk" if name == "K" else "ldv", _rows(t, name))
+        setattr(a, name + "_cache", _dense(cache, Q_out.dtype, name + "_cache"))
+    if K is not None:
+        a.n_slots = K_cache.shape[0]
+        if V is not None and V_cache.shape[0] != a.n_slots:
+            raise QmmError(2, "V_cache")
+        a.slots = _dense(slots, torch.int64, "slots")
+    for w, name in ((q_weight, "q_weight"), (k_weight, "k_weight")):
+        if w is not None and w.numel() != D:
+            raise QmmError(2, name)
+        setattr(a, name, _dense(w, torch.float32, name))
+    if cos_sin is not None:
+        a.cos_sin, a.max_pos = _dense(cos_sin, torch.float32, "cos_sin"), cos_sin.shape[0]
+        a.positions = _dense(positions, torch.int32, "positions")
+    for t, name in ((positions if cos_sin is not None else None, "positions"), (slots if K is not None else None, "slots")):
+        if t is not None and t.numel() != T:
+            raise QmmError(2, name)
+    a._keep = (Q, K, V, q_weight, k_weight, cos_sin, positions, slots, Q_out, K_cache, V_cache)
+    return a
+
+
+def norm_rope(args, stream=None) -> None:
+    """qmm_norm_rope: norm and rotation of every query and key head, keys and values to their cache
+    slots.  `args` from make_norm_rope()."""
+    _check(load().qmm_norm_rope(args, _stream_handle(stream)), "qmm_norm_rope")
+
+
+def make_attn(Q, K_cache, V_cache, page_size: int, prefix_pages, prefix_len: int, pages, kv_lens, row_starts, O,
+              scale: float, lse=None):
+    """Arguments of attn_shared().  Q, O: T x Hq x D (rows may be strided), caches n_slots x Hk x D, all
+    bf16 or all fp16; prefix_pages int32 (None without a prefix), pages int32 B x pages_per_stream,
+    kv_lens int32 B, row_starts int32 B + 1; lse fp32 T x Hq or None.  The tensors are kept alive by
+    what is returned."""
+    import torch
+    T, Hq, D = Q.shape
+    n_slots, Hk, Dk = K_cache.shape
+    B, per_stream = pages.shape
+    if Dk != D or V_cache.shape != K_cache.shape or O.shape != Q.shape:
+        raise QmmError(2, "make_attn")
+    if kv_lens.numel() != B or row_starts.numel() != B + 1 or (lse is not None and tuple(lse.shape) != (T, Hq)):
+        raise QmmError(2, "make_attn")
+    if prefix_len > 0 and (prefix_pages is None or prefix_pages.numel() * page_size < prefix_len):
+        raise QmmError(2, "prefix_pages")
+    if O.dtype != Q.dtype:
+        raise QmmError(12, "O")
+    a = _AttnArgs(T=T, B=B, Hq=Hq, Hk=Hk, D=D, page_size=page_size, type=_dtype_code(Q), scale=scale,
+                  n_slots=n_slots, prefix_len=prefix_len, pages_per_stream=per_stream)
+    a.Q, a.ldq, a.O, a.ldo = Q.data_ptr(), _rows(Q, "Q"), O.data_ptr(), _rows(O, "O")
+    a.K_cache, a.V_cache = _dense(K_cache, Q.dtype, "K_cache"), _dense(V_cache, Q.dtype, "V_cache")
+    a.prefix_pages = _dense(prefix_pages, torch.int32, "prefix_pages")
+    a.pages, a.kv_lens = _dense(pages, torch.int32, "pages"), _dense(kv_lens, torch.int32, "kv_lens")
+    a.row_starts, a.lse = _dense(row_starts, torch.int32, "row_starts"), _dense(lse, torch.float32, "lse")
+    a._keep = (Q, K_cache, V_cache, prefix_pages, pages, kv_lens, row_starts, O, lse)
+    return a
+
+
+def attn_workspace_bytes(args) -> int:
+    return load().qmm_attn_workspace_bytes(args)
+
+
+def attn_shared(args, workspace, stream=None) -> None:
+    """qmm_attn_shared: attention of every stream's rows over the shared prefix and the stream's own
+    keys.  `args` from make_attn(); `workspace`: a device tensor of >= attn_workspace_bytes(args)
+    bytes."""
+    _check(load().qmm_attn_shared(args, workspace.data_ptr(), workspace.numel() * workspace.element_size(),
+                                  _stream_handle(stream)), "qmm_attn_shared")
+
+
+def make_lora_adapters(items):
+    """Device table of one projection's adapters.  items: sequence of (A, Bt, scale) with bf16 CUDA
+    tensors A rank x K and Bt rank x N (B transposed), both contiguous; they must outlive the table."""
+    import torch
+    arr = (_LoraAdapter * len(items))()
+    for k, (A, Bt, scale) in enumerate(items):
+        if A.shape[0] != Bt.shape[0]:
+            raise QmmError(2, "make_lora_adapters")
+        arr[k] = _LoraAdapter(_dense(A, torch.bfloat16, "A"), _dense(Bt, torch.bfloat16, "Bt"), scale, A.shape[0])
+        if (arr[k].A or 0) % 16:
+            raise QmmError(4, "make_lora_adapters")
+    return torch.frombuffer(bytearray(bytes(arr)), dtype=torch.uint8).to(items[0][0].device)
+
+
+def make_lora_entries(items):
+    """items: sequence of (adapters, X, Y0, Y, N, K): the table of make_lora_adapters(), X bf16 M x K, Y0
+    and Y fp32 M x N (they may be one tensor).  The tensors are kept alive by what is returned."""
+    arr = (_LoraEntry * len(items))()
+    for k, (table, X, Y0, Y, N, K) in enumerate(items):
+        arr[k] = _LoraEntry(table.data_ptr(), table.numel() // ctypes.sizeof(_LoraAdapter), X.data_ptr(),
+                            Y0.data_ptr(), Y.data_ptr(), N, K)
+    arr._keep = tuple(items)
+    return arr
+
+
+def lora_workspace_bytes(entries, M: int, rank_max: int) -> int:
+    return load().qmm_lora_workspace_bytes(entries, len(entries), M, rank_max)
+
+
+def run_lora(entries, ids, M: int, rank_max: int, workspace, stream=None) -> None:
+    """qmm_run_lora: Y[i] = Y0[i] + scale * B (A x_i) with the adapter ids[i] (int32 device tensor, -1:
+    none) for each projection of `entries` (make_lora_entries()).  rank_max: at least every rank in
+    use; `workspace`: a device tensor of >= lora_workspace_bytes(entries, M, rank_max) bytes."""
+    _check(load().qmm_run_lora(entries, len(entries), ids.data_ptr(), M, rank_max, workspace.data_ptr(),
+                               workspace.numel() * workspace.element_size(), _stream_handle(stream)), "qmm_run_lora")
 
 
 def select_variant(M: int, N: int, K: int) -> int:

@@ -105,7 +105,8 @@ typedef enum {
   QMM_ERR_COUNT = 8,      /* qmm_run_batched: count outside [1, QMM_MAX_BATCH]              */
   QMM_ERR_VARIANT = 9,    /* an explicitly requested kernel variant cannot run this shape  */
   QMM_ERR_SCRATCH = 10,   /* qmm_run_noalloc: problem larger than its fixed device buffer  */
-  QMM_ERR_FORMAT = 11     /* qmm_fmt_*: unknown weight format code                         */
+  QMM_ERR_FORMAT = 11,    /* qmm_fmt_*: unknown weight format code                         */
+  QMM_ERR_TYPE = 12       /* an element type (qmm_dtype) that the call does not take       */
 } qmm_status;
 
 /* Bytes of the packed form of an N x K weight matrix: N * (K/256) * 144.
@@ -361,6 +362,141 @@ qmm_status qmm_fmt_run_batched(const qmm_fmt_entry* entries_host, int count, int
 qmm_status qmm_fmt_dequant(int fmt, const void* Wq_dev, int64_t N, int64_t K, float* out_dev,
                            cudaStream_t stream);
 
+/* ------------------------------------------------------------------------------------------
+ * The attention half of a layer: the operators between the quantized projections of a verify
+ * pass.  qmm_run_lora adds the rows' adapters to a projection's result, qmm_norm_rope takes the
+ * q, k and v results to the attention's queries and into the key/value cache, and
+ * qmm_attn_shared reads that cache; its bf16 output is the X of the o projection.  The
+ * conventions above hold (caller-owned buffers, host-side checks before anything is enqueued,
+ * asynchronous on `stream`, status codes); these calls allocate nothing and keep nothing.  The
+ * argument structs are read during the call only.
+ *
+ * Indices that live on the device (positions, slots, page tables, lengths, adapter ids) cannot be
+ * checked on the host.  The kernels check every one before they use it: one that is out of range
+ * reads and writes nothing out of bounds, sets bit 2 of the device status word
+ * (qmm_device_status), and leaves the rows that depend on it with unspecified values.
+ *
+ * The cache: K_cache and V_cache are n_slots x Hk x D each, row-major, one slot per cached token.
+ * Pages are runs of page_size slots: token j of a sequence whose page list is p is in slot
+ * p[j / page_size] * page_size + j % page_size. */
+typedef enum { QMM_F32 = 0, QMM_BF16 = 1, QMM_F16 = 2 } qmm_dtype;
+
+/* Norm of every query and key head, position rotation, and the write into the cache, in one pass
+ * over the projections' results.  For a head x of row t:
+ *     y = x / sqrt(mean(x^2) + eps) * weight
+ *     (a, b) -> (a c - b s, b c + a s)  for the rot/2 pairs of the first rot values of y,
+ * c and s from row positions[t] of cos_sin, a max_pos x rot table (rot/2 cosines, then rot/2
+ * sines).  Pair i is (y[i], y[i + rot/2]), or (y[2i], y[2i+1]) with `interleaved`.  Queries go to
+ * Q_out (row t, Hq x D), keys and the values (converted only) to slot slots[t] of the caches;
+ * a negative slot writes neither key nor value (a padding row).  Slots of one call are distinct.
+ * Arithmetic in fp32, one rounding to out_type at the end.
+ *   T >= 0 rows, 0 <= Hk, 1 <= Hq, Hq + 2 Hk <= 65535, D 64, 128 or 256, rot a multiple of 16 in
+ *   [0, D].  in_type: QMM_F32 (what the products write), QMM_BF16 or QMM_F16; out_type: QMM_BF16
+ *   or QMM_F16.  ldq, ldk, ldv, ldqo: elements between rows.  q_weight, k_weight: D fp32, or NULL
+ *   for ones.  V may be NULL (no values are written); K, V and the caches are not used if Hk = 0;
+ *   cos_sin and positions are not used if rot = 0.
+ *   Every buffer is 16-byte aligned (positions 4, slots 8), every row stride a multiple of 16
+ *   bytes.  Q_out and the caches must not overlap an input or each other.
+ * Errors: QMM_ERR_NULL, QMM_ERR_SHAPE, QMM_ERR_TYPE, QMM_ERR_ALIGN, QMM_ERR_CUDA. */
+typedef struct {
+  int T, Hq, Hk, D, rot, interleaved;
+  int in_type, out_type;
+  float eps;
+  const void *Q, *K, *V;
+  int64_t ldq, ldk, ldv;
+  const float *q_weight, *k_weight;
+  const float* cos_sin;
+  int64_t max_pos;
+  const int32_t* positions;
+  const int64_t* slots;
+  void* Q_out;
+  int64_t ldqo;
+  void *K_cache, *V_cache;
+  int64_t n_slots;
+} qmm_norm_rope_args;
+qmm_status qmm_norm_rope(const qmm_norm_rope_args* args_host, cudaStream_t stream);
+
+/* Attention of the rows of B streams that share a prefix.  Stream b owns rows
+ * row_starts[b] .. row_starts[b+1]-1 of Q (m_b rows) and kv_lens[b] keys of its own behind the
+ * prefix_len keys of the prefix; its rows are the last m_b of its own keys, so row i of the stream
+ * sees the whole prefix and its own keys j <= kv_lens[b] - m_b + i.  For each row and each of its
+ * Hq heads (head h reads key/value head h / (Hq/Hk)):
+ *     O = sum_j softmax_j(scale * q . k_j) v_j,    lse = log sum_j exp(scale * q . k_j).
+ * A row that sees no key gets O = 0 and lse = -inf, and so does a row of Q behind
+ * row_starts[B] (padding).  The prefix's keys are read once for all streams, not once each.
+ * Cache slots that no row may see are never part of a result, whatever they hold.
+ *   Q, O: T rows of Hq x D, type `type` (QMM_BF16 or QMM_F16, as the caches), ldq, ldo elements
+ *   between rows.  lse: T x Hq fp32, or NULL.
+ *   prefix_pages: device, ceil(prefix_len / page_size) page numbers.  pages: device, B rows of
+ *   pages_per_stream page numbers.  kv_lens: device, B.  row_starts: device, B + 1, from 0, not
+ *   decreasing, at most T.
+ *   0 <= T < 2^20, 0 <= B <= QMM_ATTN_MAX_STREAMS, D 64 or 128, Hq a multiple of Hk with
+ *   Hq/Hk <= 64, Hq <= 1024, page_size a power of two in [16, 4096], n_slots a multiple of
+ *   page_size below 2^31, 0 <= prefix_len < 2^30, pages_per_stream * page_size < 2^30.
+ *   Q, O and the caches are 16-byte aligned, row strides multiples of 8; the int arrays and lse
+ *   4-byte aligned.
+ * Scores, softmax statistics and sums are fp32; the weights of the values are rounded to `type` for
+ * the tensor cores, and O is rounded once.  The result does not depend on the other calls of the
+ * stream, and the same arguments give the same bits.
+ *   workspace_dev: at least qmm_attn_workspace_bytes(args) bytes (it depends on T, B, Hq, Hk and D
+ *   only), 16-byte aligned; calls that may overlap need one each.  It needs no initialisation.
+ * Errors: QMM_ERR_NULL, QMM_ERR_SHAPE, QMM_ERR_TYPE, QMM_ERR_ALIGN, QMM_ERR_BUFSIZE, QMM_ERR_CUDA. */
+#define QMM_ATTN_MAX_STREAMS 1024
+typedef struct {
+  int T, B, Hq, Hk, D, page_size;
+  int type;
+  float scale;
+  const void* Q;
+  int64_t ldq;
+  const void *K_cache, *V_cache;
+  int64_t n_slots;
+  const int32_t* prefix_pages;
+  int64_t prefix_len;
+  const int32_t* pages;
+  int64_t pages_per_stream;
+  const int32_t *kv_lens, *row_starts;
+  void* O;
+  int64_t ldo;
+  float* lse;
+} qmm_attn_args;
+size_t qmm_attn_workspace_bytes(const qmm_attn_args* args_host);   /* 0: invalid arguments */
+qmm_status qmm_attn_shared(const qmm_attn_args* args_host, void* workspace_dev, size_t workspace_bytes,
+                           cudaStream_t stream);
+
+/* Low-rank adapters of the rows' requests beside shared projections:
+ *     Y[i] = Y0[i] + scale_a * B_a (A_a x_i),   a = ids_dev[i]   (Y[i] = Y0[i] for ids[i] = -1)
+ * for the M rows of X and each of `count` projections that share the rows' ids (q, k and v of a
+ * layer in one call).  Y0 is the projection's own result (qmm_run), Y may be the same buffer.
+ * Sums are fp32 throughout, in an order that depends on the shapes only.
+ *   entries_host: count entries, 1 <= count <= QMM_LORA_MAX_ENTRIES.  adapters: device table of
+ *   n_adapters adapters of that projection (qmm_lora_adapter: A rank x K and Bt rank x N bf16,
+ *   row-major, Bt being B transposed; A 16-byte aligned, Bt 2-byte).  X: M x K bf16, Y0 and Y: M x N
+ *   fp32.  0 <= rank <= rank_max for every adapter in use (rank 0 adds nothing), 1 <= rank_max <=
+ *   QMM_LORA_MAX_RANK.  Shapes and alignment as qmm_run; the table is 8-byte aligned; ids_dev: M int32.
+ *   workspace_dev: at least qmm_lora_workspace_bytes(entries, count, M, rank_max) bytes, 16-byte
+ *   aligned; calls that may overlap need one each.  It needs no initialisation.
+ * Errors: as qmm_run_batched, QMM_ERR_COUNT (count), QMM_ERR_SHAPE (n_adapters, rank_max),
+ * QMM_ERR_BUFSIZE (workspace). */
+#define QMM_LORA_MAX_ENTRIES 16
+#define QMM_LORA_MAX_RANK 256
+typedef struct {
+  const uint16_t* A;    /* device, rank x K */
+  const uint16_t* Bt;   /* device, rank x N */
+  float scale;
+  int rank;
+} qmm_lora_adapter;
+typedef struct {
+  const qmm_lora_adapter* adapters;   /* device table */
+  int n_adapters;
+  const uint16_t* X;
+  const float* Y0;
+  float* Y;
+  int64_t N, K;
+} qmm_lora_entry;
+size_t qmm_lora_workspace_bytes(const qmm_lora_entry* entries_host, int count, int M, int rank_max);
+qmm_status qmm_run_lora(const qmm_lora_entry* entries_host, int count, const int32_t* ids_dev, int M, int rank_max,
+                        void* workspace_dev, size_t workspace_bytes, cudaStream_t stream);
+
 /* Measurement probe: read bytes (a multiple of 16) of device memory at buf_dev exactly once,
  * with 16-byte loads that bypass L1 and are marked evict-first in L2, and write one word per CTA
  * (an XOR of what it read) to sink_dev, which holds qmm_stream_read_sink_words() words.  Timed
@@ -398,7 +534,8 @@ void qmm_set_wait_limit(uint32_t polls, uint32_t suspend_ns);
  * (a synchronous call: it waits for the device).  0: no kernel reported a problem since the
  * last read.  Bit 0: a kernel stopped waiting for its own weight copies after a bounded number
  * of polls; the outputs of the calls since the last read are then invalid.  Bit 1: qmm_pack_dev
- * met a non-finite weight or an fp16 scale overflow and wrote zeros for that super-block. */
+ * met a non-finite weight or an fp16 scale overflow and wrote zeros for that super-block.  Bit 2:
+ * qmm_norm_rope, qmm_attn_shared or qmm_run_lora met a device-side index out of range. */
 qmm_status qmm_device_status(unsigned* status_out);
 
 /* Human-readable text of a status code (static storage). */
