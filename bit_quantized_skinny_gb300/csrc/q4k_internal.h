@@ -68,6 +68,12 @@ size_t workspace_bytes_held();
 // Failure-detection hook: bound the tensor-core kernel's pipeline waits to `polls` polls of at
 // most suspend_ns each (0, 0: the kernel's own bound) in launches made from now on.
 void set_wait_limit(uint32_t polls, uint32_t suspend_ns);
+void get_wait_limit(uint32_t* polls, uint32_t* suspend_ns);
+
+// cuTensorMapEncodeTiled (a driver entry point, looked up through the runtime; nullptr: not found),
+// and the current device's SM count (0: no device).
+void* tensor_map_encoder();
+int sm_count();
 
 // The read-only streaming probe: read `bytes` (a multiple of 16) at buf once; sink holds
 // stream_read_grid() words.

@@ -1869,6 +1869,13 @@ cudaError_t launch_tc_noalloc_t(const Job& job, int M, cudaStream_t stream, uint
 
 cudaError_t release_workspaces() { return Workspace::release(); }
 
+void* tensor_map_encoder() { return reinterpret_cast<void*>(encode_fn()); }
+int sm_count() { return num_sms(); }
+void get_wait_limit(uint32_t* polls, uint32_t* suspend_ns) {
+  *polls = g_wait_polls.load(std::memory_order_relaxed);
+  *suspend_ns = g_wait_ns.load(std::memory_order_relaxed);
+}
+
 void set_wait_limit(uint32_t polls, uint32_t suspend_ns) {
   g_wait_polls.store(polls, std::memory_order_relaxed);
   g_wait_ns.store(suspend_ns, std::memory_order_relaxed);

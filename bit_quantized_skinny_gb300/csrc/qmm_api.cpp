@@ -38,7 +38,7 @@ bool half_type(int t) { return t == QMM_BF16 || t == QMM_F16; }
 
 // Sizes and types of a qmm_attn_shared call.
 qmm_status check_attn_shape(const qmm_attn_args& a) {
-  if (a.T < 0 || a.T >= (1 << 20) || a.B < 0 || a.B > QMM_ATTN_MAX_STREAMS) return QMM_ERR_SHAPE;
+  if (a.T < 0 || a.T > QMM_ATTN_MAX_ROWS || a.B < 0 || a.B > QMM_ATTN_MAX_STREAMS) return QMM_ERR_SHAPE;
   if (a.D != 64 && a.D != 128) return QMM_ERR_SHAPE;
   if (a.Hk < 1 || a.Hq < 1 || a.Hq > 1024 || a.Hq % a.Hk != 0 || a.Hq / a.Hk > 64) return QMM_ERR_SHAPE;
   if (a.page_size < 16 || a.page_size > 4096 || (a.page_size & (a.page_size - 1))) return QMM_ERR_SHAPE;
@@ -47,6 +47,7 @@ qmm_status check_attn_shape(const qmm_attn_args& a) {
   if (a.pages_per_stream < 0 || a.pages_per_stream >= (1 << 30) / a.page_size) return QMM_ERR_SHAPE;
   const int64_t w = (int64_t)a.Hq * a.D;
   if (a.ldq < w || a.ldo < w) return QMM_ERR_SHAPE;
+  if (!(a.scale > 0.0f) || std::isinf(a.scale)) return QMM_ERR_SHAPE;
   return half_type(a.type) ? QMM_OK : QMM_ERR_TYPE;
 }
 

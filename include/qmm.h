@@ -430,7 +430,7 @@ qmm_status qmm_norm_rope(const qmm_norm_rope_args* args_host, cudaStream_t strea
  *   prefix_pages: device, ceil(prefix_len / page_size) page numbers.  pages: device, B rows of
  *   pages_per_stream page numbers.  kv_lens: device, B.  row_starts: device, B + 1, from 0, not
  *   decreasing, at most T.
- *   0 <= T < 2^20, 0 <= B <= QMM_ATTN_MAX_STREAMS, D 64 or 128, Hq a multiple of Hk with
+ *   0 <= T <= QMM_ATTN_MAX_ROWS, 0 <= B <= QMM_ATTN_MAX_STREAMS, scale > 0 and finite, D 64 or 128, Hq a multiple of Hk with
  *   Hq/Hk <= 64, Hq <= 1024, page_size a power of two in [16, 4096], n_slots a multiple of
  *   page_size below 2^31, 0 <= prefix_len < 2^30, pages_per_stream * page_size < 2^30.
  *   Q, O and the caches are 16-byte aligned, row strides multiples of 8; the int arrays and lse
@@ -442,6 +442,7 @@ qmm_status qmm_norm_rope(const qmm_norm_rope_args* args_host, cudaStream_t strea
  *   only), 16-byte aligned; calls that may overlap need one each.  It needs no initialisation.
  * Errors: QMM_ERR_NULL, QMM_ERR_SHAPE, QMM_ERR_TYPE, QMM_ERR_ALIGN, QMM_ERR_BUFSIZE, QMM_ERR_CUDA. */
 #define QMM_ATTN_MAX_STREAMS 1024
+#define QMM_ATTN_MAX_ROWS 65536
 typedef struct {
   int T, B, Hq, Hk, D, page_size;
   int type;

@@ -53,7 +53,7 @@ def attn_args(qmm, **change):
 
 
 @pytest.mark.parametrize("change,status", [
-    (dict(T=-1), SHAPE), (dict(T=1 << 20), SHAPE), (dict(B=-1), SHAPE), (dict(B=1025), SHAPE), (dict(D=256), SHAPE),
+    (dict(T=-1), SHAPE), (dict(T=65537), SHAPE), (dict(scale=0.0), SHAPE), (dict(scale=float('nan')), SHAPE), (dict(scale=float('inf')), SHAPE), (dict(B=-1), SHAPE), (dict(B=1025), SHAPE), (dict(D=256), SHAPE),
     (dict(Hk=0), SHAPE), (dict(Hk=3), SHAPE), (dict(Hq=130, Hk=2, ldq=1 << 16, ldo=1 << 16), SHAPE),
     (dict(page_size=8), SHAPE), (dict(page_size=48, n_slots=480), SHAPE), (dict(page_size=8192, n_slots=8192), SHAPE),
     (dict(n_slots=100), SHAPE), (dict(n_slots=1 << 31), SHAPE), (dict(prefix_len=-1), SHAPE),
