@@ -4,19 +4,22 @@
 // Work.  A group is a block of rows that see the same keys, with one key/value head: for the prefix
 // the rows of all streams, for own keys the rows of one stream; the G query heads of a key/value
 // head are rows of the same block, so a key is read once for all of them.  A row tile is 128 rows
-// (128 / G tokens) and a block up to two tiles; a key tile is 128 keys.  The key tiles of all
-// groups form one list, cut into equal pieces, one per CTA (one CTA an SM): every SM streams
-// the same number of bytes whatever the lengths, and the lengths stay on the device.  A piece holds
-// one or several segments (runs of one group's key tiles).  Each segment leaves its sums
-// unnormalised in the workspace, with the running maximum and weight sum of each row, and
-// attn_combine_kernel joins a row's segments in their order.
+// (128 / G tokens) and a block up to two tiles; a key tile is 64 keys.  The key tiles of all groups
+// form one list, each group led by kLead units for what a segment costs besides its tiles, cut into
+// equal pieces, one per CTA (one CTA an SM): every SM has the same work whatever the lengths, and the
+// lengths stay on the device.  A piece holds one or several segments (runs of one group's key tiles).
+// Each segment leaves its sums unnormalised in the workspace, with the running maximum and weight sum
+// of each row, and attn_combine_kernel joins a row's segments in their order.
 //
-// One segment.  Two lanes of flash attention share the tensor cores: with more than one row tile
-// each lane has a row tile and both read every key tile; with one, the lanes take the key tiles in
-// turn and are joined at the segment's end.  Per lane and key tile:
+// One segment.  Two lanes of flash attention take turns on the tensor cores: with more than one row
+// tile each lane has a row tile and both read every key tile; with one, the lanes take the key tiles
+// in turn and are joined at the segment's end.  Per lane and key tile:
 //     S = Q K^T              tcgen05, both operands in shared memory (TMA, 128-byte swizzle)
-//     p = 2^(c S - m)        a thread per row: S from tensor memory into registers, c = scale log2 e
+//     p = 2^(c S - m)        a thread per row, S from tensor memory, c = scale log2 e
 //     O += p V               tcgen05, p (16 bits, rounded once) from tensor memory, V MN-major
+// Each lane has two S, so the scores of its next item are formed during the softmax of this one: 64
+// keys a tile make room for them in tensor memory (2 lanes x (2 x 64 + 128 columns)).  The lanes take
+// items (key tiles) in turn across segments, and a warp each issues their products.
 // m is the maximum when it was last moved: it moves, and O is rescaled, only when the row's maximum
 // grew by more than 8 (2^8 in a 16-bit p costs no precision), so O stays in tensor memory.
 //
@@ -25,6 +28,7 @@
 // non-finite values among the keys that only some rows of the block see (a draft's last keys);
 // attn_combine_kernel then adds those back, from the cache, to the rows that see them.
 #include <cstdint>
+#include <type_traits>
 #include <cuda.h>
 #include <cudaTypedefs.h>
 #include <cuda_bf16.h>
@@ -40,12 +44,14 @@ namespace {
 
 __device__ unsigned g_status;   // this file's kernels' status word
 
-constexpr int kTile = 128;           // rows of a row tile, keys of a key tile
+constexpr int kRows = 128;           // rows of a row tile
+constexpr int kTile = 64;            // keys of a key tile
+constexpr int kLead = 3;             // units of a group besides its key tiles
 constexpr int kMaxCtas = 152;
 constexpr int kLaneWarps = 4;
-constexpr int kLoadWarp = 8, kMmaWarp = 9, kQWarp = 10;
-constexpr int kThreads = 11 * 32;
-constexpr uint32_t kTmemCols = 512;   // S and p of the lanes at 128 L, O at 256 + 128 L
+constexpr int kLoadWarp = 8, kMmaWarp = 9 /* and 10 */, kQWarp = 11;
+constexpr int kThreads = 12 * 32;
+constexpr uint32_t kTmemCols = 512;   // lane L: S and p at 128 L and 128 L + 64, O at 256 + 128 L
 constexpr float kGrow = 8.0f;
 constexpr uint32_t kWaitLimit = 1u << 17;
 constexpr float kLog2e = 1.44269504088896340736f, kLn2 = 0.69314718055994530942f;
@@ -62,29 +68,36 @@ struct Params {
   CUtensorMap mapQ, mapK, mapV;
   float* o_rows;      // [2][T * Hq][D]: first segments, of the prefix and of own keys
   RowStat* s_rows;
-  float* o_cta;       // [kMaxCtas][2 * 128][D]: a CTA's first segment that begins inside a group
+  float* o_cta;       // [kMaxCtas][2 * kRows][D]: a CTA's first segment that begins inside a group
   RowStat* s_cta;
-  int64_t* plan;      // [0] tiles, [1] CTAs with work, [2 + b] first own tile of stream b
+  int64_t* plan;      // [0] units, [1] CTAs with work, [2 + b] first unit of stream b's own keys
   int tokens;         // of a row tile
+  int n_pages, page_shift;
   uint32_t wait_polls, wait_ns;
 };
 
 template <int D>
 struct Smem {
-  static constexpr int kHalf = kTile * 128;              // 128 rows of 64 values
+  static constexpr int kHalf = kTile * 128;              // 64 keys of 64 values
   static constexpr int kTileBytes = kTile * D * 2;
-  static constexpr int kStages = D == 128 ? 5 : 10;
+  static constexpr int kQHalf = kRows * 128;
+  static constexpr int kQBytes = kRows * D * 2;
+  static constexpr int kStages = 5;                      // of keys, and of values
   static constexpr int kQ = 0;
-  static constexpr int kKV = 2 * kTileBytes;
-  static constexpr int kStats = kKV + kStages * kTileBytes;   // (top, sum) of the two lanes' rows
-  static constexpr int kMisc = kStats + 2 * kTile * 8;
+  static constexpr int kK = 2 * kQBytes;
+  static constexpr int kV = kK + kStages * kTileBytes;
+  static constexpr int kStats = kV + kStages * kTileBytes;   // (top, sum) of the two lanes' rows
+  static constexpr int kMisc = kStats + 2 * kRows * 8;
   static constexpr int kTotal = kMisc + 1024;
 };
 static_assert(Smem<128>::kTotal <= 227 * 1024 && Smem<64>::kTotal <= 227 * 1024, "shared memory");
 
-enum : int {   // barriers
-  kBarFull = 0, kBarEmpty = 10, kBarQFull = 20, kBarQEmpty = 22, kBarS = 24, kBarP = 26, kBarO = 28, kBarJoin = 30,
-  kBarDrain = 31, kBars = 32
+// Barriers.  A wait tells a phase from the one after it only, so a barrier is waited on by threads that
+// see all of its phases, or that know the phase before to be over and the one after not begun: a stage of keys or values has a full barrier for each set of users (lane
+// 0, lane 1, both), and a query tile is waited for and released by both lanes whoever uses it.
+enum : int {
+  kBarFullK = 0 /* 5 users + stage */, kBarFullV = 15, kBarEmptyK = 30, kBarEmptyV = 35, kBarQFull = 40, kBarQEmpty = 42,
+  kBarS = 44 /* 2 lane + S */, kBarP = 48, kBarO = 52, kBarEnd = 56, kBarJoin = 58, kBarDrain = 59, kBars = 61
 };
 
 struct Misc {
@@ -92,7 +105,7 @@ struct Misc {
   int64_t total, prefix_tiles, w0, w1;
   int64_t scan[kThreads / 32];
   int b, rb, h;
-  int64_t tile;       // first tile within its group
+  int64_t unit;       // first unit within its group
   uint32_t tmem;
   int abort;
   uint32_t odd[8];    // [s % 8]: s, if values were taken out in segment s (the lanes drift a few apart)
@@ -120,6 +133,16 @@ __device__ __forceinline__ int keys_of(const Stream& s, int rb, int block) {
   return clampi(s.len - s.m + min(s.m, (rb + 1) * block), 0, s.len);
 }
 __device__ __forceinline__ int tiles_of(int keys) { return (keys + kTile - 1) / kTile; }
+__device__ __forceinline__ int units_of(int tiles) { return tiles > 0 ? tiles + kLead : 0; }
+
+// First unit of the c-th of C pieces of W units, and the first piece that does not begin before unit x.
+// (32-bit division where it holds: c <= 152.)
+__device__ __forceinline__ int64_t piece_start(int64_t c, int64_t W, int64_t C) {
+  return W < (1 << 24) ? (int64_t)((uint32_t)c * (uint32_t)W / (uint32_t)C) : c * W / C;
+}
+__device__ __forceinline__ int64_t piece_from(int64_t x, int64_t W, int64_t C) {
+  return W < (1 << 24) ? (int64_t)(((uint32_t)x * (uint32_t)C + (uint32_t)W - 1) / (uint32_t)W) : (x * C + W - 1) / W;
+}
 
 // A run of key tiles of one group.
 struct Seg {
@@ -135,20 +158,19 @@ struct Seg {
 // Steps through a CTA's segments; every role has its own.
 struct Walker {
   int64_t left;
-  int b, rb, h, j;
+  int b, rb, h, j;   // group, unit within it
   Stream s;
   int block;
 
   __device__ __forceinline__ void start(const Params& P, const Misc& m) {
     left = m.w1 - m.w0;
-    b = m.b; rb = m.rb; h = m.h; j = (int)m.tile;
+    b = m.b; rb = m.rb; h = m.h; j = (int)m.unit;
     block = 2 * P.tokens;
     if (b >= 0 && left > 0) s = stream_of(P.a, b);
   }
   __device__ __forceinline__ bool next(const Params& P, Seg& g) {
     const qmm_attn_args& a = P.a;
     while (left > 0) {
-      int tiles;
       if (b < 0) {
         const int rows = a.B > 0 ? clampi(a.row_starts[a.B], 0, a.T) : 0;
         if (rb * (int64_t)block >= rows) { b = 0; rb = h = j = 0; s = stream_of(a, 0); continue; }
@@ -171,22 +193,20 @@ struct Walker {
         g.first_keys = s.len - s.m + rb * block + 1;
         g.pages = a.pages + b * a.pages_per_stream;
       }
-      tiles = tiles_of(g.keys);
-      if (j >= tiles) { j = 0; if (tiles == 0 || ++h == a.Hk) { h = 0; ++rb; } continue; }
+      const int tiles = tiles_of(g.keys), units = units_of(tiles);
+      if (j >= units) { j = 0; if (units == 0 || ++h == a.Hk) { h = 0; ++rb; } continue; }
       g.h = h;
-      g.j0 = j;
-      g.j1 = (int)min((int64_t)tiles, j + left);
-      left -= g.j1 - g.j0;
-      j = g.j1;
+      g.j0 = max(0, j - kLead);
+      const int take = (int)min((int64_t)(units - j), left);
+      j += take;
+      left -= take;
+      g.j1 = j - kLead;
+      if (g.j1 <= g.j0) continue;   // the piece ends with the group's lead
       return true;
     }
     return false;
   }
 };
-
-// Order of a segment's n key tiles in the ring: K0, then K1, V0, K2, V1, ...
-__device__ __forceinline__ uint32_t pos_k(int i) { return i == 0 ? 0u : 2u * i - 1; }
-__device__ __forceinline__ uint32_t pos_v(int i, int n) { return i == n - 1 ? 2u * n - 1 : 2u * i + 2; }
 
 __device__ __forceinline__ void tma_3d(uint32_t dst, const CUtensorMap* map, int x, int y, int z, uint32_t bar) {
   asm volatile(
@@ -232,12 +252,21 @@ __device__ __forceinline__ void store8(float* p, const uint32_t* v) {
                : "memory");
 }
 
+// The wait for a phase that has not completed yet (out of line: the roles' loops stay short).
+__device__ __noinline__ bool wait_slowly(uint32_t bar, uint32_t parity, uint32_t polls, uint32_t ns,
+                                         volatile int* abort_flag) {
+  if (*abort_flag) return false;
+  if (mbar_wait(bar, parity, polls, ns)) return true;
+  atomicOr(&g_status, kErrWaitTimeout);
+  *abort_flag = 1;
+  return false;
+}
+
 template <int D, int TYPE>
 __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant__ Params P) {
   extern __shared__ __align__(1024) uint8_t smem[];
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   using L = Smem<D>;
-  constexpr int kS = L::kStages;
+  constexpr uint32_t kS = L::kStages;
   const qmm_attn_args& a = P.a;
   Misc& M = *reinterpret_cast<Misc*>(smem + L::kMisc);
   volatile int* abort_flag = &M.abort;
@@ -248,16 +277,26 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
 
   // ---- barriers, tensor memory, and this CTA's piece of the list of key tiles
   if (threadIdx.x == 0) {
-    for (int k = 0; k < kS; ++k) { mbar_init(bar(kBarFull + k), 1); mbar_init(bar(kBarEmpty + k), 1); }
+    for (int k = 0; k < 3 * kS; ++k) {
+      mbar_init(bar(kBarFullK + k), 1);
+      mbar_init(bar(kBarFullV + k), 1);
+    }
+    for (int k = 0; k < kS; ++k) {
+      mbar_init(bar(kBarEmptyK + k), 2);
+      mbar_init(bar(kBarEmptyV + k), 2);
+    }
     for (int k = 0; k < 2; ++k) {
       mbar_init(bar(kBarQFull + k), 1);
-      mbar_init(bar(kBarQEmpty + k), 1);
+      mbar_init(bar(kBarQEmpty + k), 2);
+      mbar_init(bar(kBarEnd + k), 1);
+      mbar_init(bar(kBarDrain + k), 1);
+    }
+    for (int k = 0; k < 4; ++k) {
       mbar_init(bar(kBarS + k), 1);
       mbar_init(bar(kBarP + k), kLaneWarps);
       mbar_init(bar(kBarO + k), 1);
     }
     mbar_init(bar(kBarJoin), 2 * kLaneWarps);
-    mbar_init(bar(kBarDrain), 1);
     M.abort = 0;
     for (int k = 0; k < 8; ++k) M.odd[k] = 0;
     fence_barrier_init();
@@ -266,7 +305,19 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
     tc::tmem_alloc(smem_addr(&M.tmem), kTmemCols);
     tc::tmem_relinquish();
   }
+  if (threadIdx.x < 3)
+    asm volatile("prefetch.tensormap [%0];" :: "l"(threadIdx.x == 0 ? &P.mapK : threadIdx.x == 1 ? &P.mapV : &P.mapQ)
+                 : "memory");
+  // Launched early (behind a launch that allows it), this grid reads what was written before it from
+  // here on; the combine launch, which reads the lengths before its own wait, may start from here on.
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   {
+    // the page tables towards L2 while the pieces are worked out: one 128-byte line a thread
+    const int64_t line = ((int64_t)blockIdx.x * kThreads + threadIdx.x) * 32;
+    const int64_t n_pre = (a.prefix_len + a.page_size - 1) / a.page_size, n_own = a.B * a.pages_per_stream;
+    if (line < n_pre) asm volatile("prefetch.global.L2 [%0];" :: "l"(a.prefix_pages + line));
+    if (line < n_own) asm volatile("prefetch.global.L2 [%0];" :: "l"(a.pages + line));
     constexpr int kPer = (QMM_ATTN_MAX_STREAMS + kThreads - 1) / kThreads;
     int64_t mine[kPer], sum = 0;
     bool wrong = false;
@@ -278,7 +329,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
         bool bad;
         const Stream s = stream_of(a, b, &bad);
         wrong |= bad;
-        for (int rb = 0; rb * (int64_t)block < s.m; ++rb) mine[q] += (int64_t)a.Hk * tiles_of(keys_of(s, rb, block));
+        for (int rb = 0; rb * (int64_t)block < s.m; ++rb) mine[q] += (int64_t)a.Hk * units_of(tiles_of(keys_of(s, rb, block)));
       }
       sum += mine[q];
     }
@@ -297,21 +348,21 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
       if (w < warp) before += M.scan[w];
       own += M.scan[w];
     }
-    const int ptiles = tiles_of((int)a.prefix_len);
+    const int punits = units_of(tiles_of((int)a.prefix_len));
     const int rows = a.B > 0 ? clampi(a.row_starts[a.B], 0, a.T) : 0;
-    const int64_t prefix = (int64_t)((rows + block - 1) / block) * a.Hk * ptiles;
+    const int64_t prefix = (int64_t)((rows + block - 1) / block) * a.Hk * punits;
     const int64_t W = prefix + own, C = min((int64_t)gridDim.x, W);
-    const int64_t w0 = C > 0 && blockIdx.x < C ? blockIdx.x * W / C : 0;
-    const int64_t w1 = C > 0 && blockIdx.x < C ? (blockIdx.x + 1) * W / C : 0;
+    const int64_t w0 = blockIdx.x < C ? piece_start(blockIdx.x, W, C) : 0;
+    const int64_t w1 = blockIdx.x < C ? piece_start(blockIdx.x + 1, W, C) : 0;
     if (threadIdx.x == 0) {
       M.w0 = w0;
       M.w1 = w1;
       if (w0 < prefix) {
-        const int64_t g = w0 / ptiles;
+        const int64_t g = w0 < (1 << 24) ? (int64_t)((uint32_t)w0 / (uint32_t)punits) : w0 / punits;
         M.b = -1;
-        M.rb = (int)(g / a.Hk);
-        M.h = (int)(g % a.Hk);
-        M.tile = w0 % ptiles;
+        M.rb = (int)((uint32_t)g / (uint32_t)a.Hk);
+        M.h = (int)((uint32_t)g % (uint32_t)a.Hk);
+        M.unit = w0 - g * punits;
       }
       if (blockIdx.x == 0) { P.plan[0] = W; P.plan[1] = C; }
     }
@@ -324,12 +375,13 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
         if (w0 >= before && w0 < before + mine[q]) {
           const Stream s = stream_of(a, b);
           int64_t at = w0 - before;
-          int rb = 0, n = tiles_of(keys_of(s, 0, block));
-          while (at >= (int64_t)a.Hk * n) { at -= (int64_t)a.Hk * n; n = tiles_of(keys_of(s, ++rb, block)); }
+          int rb = 0, n = units_of(tiles_of(keys_of(s, 0, block)));
+          while (at >= (int64_t)a.Hk * n) { at -= (int64_t)a.Hk * n; n = units_of(tiles_of(keys_of(s, ++rb, block))); }
           M.b = b;
           M.rb = rb;
-          M.h = (int)(at / n);
-          M.tile = at % n;
+          M.h = 0;
+          while (at >= n) { at -= n; ++M.h; }
+          M.unit = at;
         }
       }
       before += mine[q];
@@ -343,12 +395,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
   // A bounded wait for a phase of a barrier; false: this wait, or another one, gave up.
   auto wait = [&](int k, uint32_t parity) -> bool {
     if (mbar_try(bar(k), parity)) return true;
-    if (*abort_flag) return false;
-    if (mbar_wait(bar(k), parity, P.wait_polls ? P.wait_polls : kWaitLimit, P.wait_ns ? P.wait_ns : kSuspendNs))
-      return true;
-    atomicOr(&g_status, kErrWaitTimeout);
-    *abort_flag = 1;
-    return false;
+    return wait_slowly(bar(k), parity, P.wait_polls ? P.wait_polls : kWaitLimit, P.wait_ns ? P.wait_ns : kSuspendNs,
+                       abort_flag);
   };
   auto wait_w = [&](int k, uint32_t parity) -> bool { return __all_sync(0xffffffffu, wait(k, parity)); };
 
@@ -358,51 +406,71 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
 
   if (warp == kLoadWarp) {
     // ------------------------------------------------------------------ keys and values
-    // A tile is one box per page (or 128 keys of a longer page) and half of 64 values; lane k copies
+    // A tile is one box per page (or 64 keys of a longer page) and half of 64 values; lane k copies
     // box k / halves of half k % halves.  Pages behind the last key are not read.
     constexpr int kHalves = D / 64;
     const int per_box = min(a.page_size, kTile);
     const uint32_t box_bytes = per_box * 128;
-    const int64_t n_pages = a.n_slots / a.page_size;
-    uint32_t pos = 0, filled = 0;   // stages ever filled
+    const int my_key = lane / kHalves * per_box;          // of the tile; behind it for lanes without a box
+    struct Ring {
+      uint32_t filled = 0;    // stages ever filled
+      uint32_t parity = 0;    // bit kS * users + stage: of the next phase of its full barrier
+      uint32_t users = 0;     // 2 bits a stage: of its last copy
+    } rk, rv;
+    uint32_t items = 0;
     bool ok = true;
     auto slot_of = [&](const Seg& s, int tile) -> int {   // first slot of this lane's box
-      const int key = tile * kTile + lane / kHalves * per_box;
-      if (lane >= kHalves * (kTile / per_box) || key >= s.keys) return -1;
-      const int page = s.pages[key / a.page_size];
-      if (page < 0 || page >= n_pages) {
+      const int key = tile * kTile + my_key;
+      if (my_key >= kTile || key >= s.keys) return -1;
+      const int page = s.pages[key >> P.page_shift];
+      if (page < 0 || page >= P.n_pages) {
         atomicOr(&g_status, kErrIndex);
         return (int)a.n_slots;   // outside the map: reads as zeros
       }
-      return page * a.page_size + key % a.page_size;
+      return (page << P.page_shift) + (key & (a.page_size - 1));
     };
-    auto copy = [&](const CUtensorMap* map, const Seg& s, int slot) {
-      const uint32_t st = pos % kS, use = pos / kS;
-      ++pos;
-      ok = ok && (use == 0 || wait_w(kBarEmpty + st, (use - 1) & 1));
+    auto copy = [&](const CUtensorMap* map, const Seg& s, int slot, uint32_t users, Ring& r, int full, int empty, int base) {
+      const uint32_t st = r.filled % kS, use = r.filled / kS;
+      ok = ok && (use == 0 || wait_w(empty + st, (use - 1) & 1));
       if (!ok) return;
-      const uint32_t n = __popc(__ballot_sync(0xffffffffu, slot >= 0));
-      if (lane == 0) mbar_arrive_expect_tx(bar(kBarFull + st), n * box_bytes);
+      const uint32_t n = __popc(__ballot_sync(0xffffffffu, slot >= 0)), at = kS * users + st;
+      if (lane == 0) mbar_arrive_expect_tx(bar(full + at), n * box_bytes);
       __syncwarp();
-      filled = pos;
+      ++r.filled;
+      r.parity ^= 1u << at;
+      r.users = (r.users & ~(3u << 2 * st)) | users << 2 * st;
       const int half = lane % kHalves;
       if (slot >= 0)
-        tma_3d(smem_addr(smem + L::kKV) + st * L::kTileBytes + half * L::kHalf + lane / kHalves * box_bytes, map,
-               64 * half, s.h, slot, bar(kBarFull + st));
+        tma_3d(smem_addr(smem) + base + st * L::kTileBytes + half * L::kHalf + my_key * 128, map, 64 * half, s.h, slot,
+               bar(full + at));
     };
     while (ok && walk.next(P, g)) {
-      int slot = slot_of(g, g.j0);
-      copy(&P.mapK, g, slot);
-      for (int t = g.j0; ok && t < g.j1; ++t) {
-        const int next = t + 1 < g.j1 ? slot_of(g, t + 1) : -1;
-        if (t + 1 < g.j1) copy(&P.mapK, g, next);
-        if (ok) copy(&P.mapV, g, slot);
-        slot = next;
+      // K0, K1, K2, V0, K3, V1, ...: the order in which they are used
+      const int n = g.j1 - g.j0;
+      const bool pair = g.rows > P.tokens;
+      auto users = [&](int t) -> uint32_t { return pair ? 2 : (items + t) & 1; };
+      int slots[3] = {slot_of(g, g.j0), n > 1 ? slot_of(g, g.j0 + 1) : -1, n > 2 ? slot_of(g, g.j0 + 2) : -1};
+      copy(&P.mapK, g, slots[0], users(0), rk, kBarFullK, kBarEmptyK, L::kK);
+      if (n > 1) copy(&P.mapK, g, slots[1], users(1), rk, kBarFullK, kBarEmptyK, L::kK);
+      for (int t = 0; ok && t < n; ++t) {
+        const int next = t + 3 < n ? slot_of(g, g.j0 + t + 3) : -1;
+        if (t + 2 < n) copy(&P.mapK, g, slots[2], users(t + 2), rk, kBarFullK, kBarEmptyK, L::kK);
+        copy(&P.mapV, g, slots[0], users(t), rv, kBarFullV, kBarEmptyV, L::kV);
+        slots[0] = slots[1];
+        slots[1] = slots[2];
+        slots[2] = next;
       }
+      items += pair ? 2 * n : n;
     }
     // no copy of this CTA is in flight when it ends
-    for (uint32_t k = filled > (uint32_t)kS ? filled - kS : 0; k < filled; ++k)
-      mbar_wait(bar(kBarFull + k % kS), (k / kS) & 1, kWaitLimit);
+    auto land = [&](const Ring& r, int full) {
+      for (uint32_t st = 0; st < kS && st < r.filled; ++st) {
+        const uint32_t at = kS * (r.users >> 2 * st & 3) + st;
+        mbar_wait(bar(full + at), (r.parity >> at & 1) ^ 1, kWaitLimit);
+      }
+    };
+    land(rk, kBarFullK);
+    land(rv, kBarFullV);
   } else if (warp == kQWarp) {
     // ------------------------------------------------------------------ query tiles
     if (elect_one()) {
@@ -418,7 +486,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
           mbar_arrive_expect_tx(bar(kBarQFull + st), bytes * (D / 64));
           filled = pos + 1;
           for (int half = 0; half < D / 64; ++half)
-            tma_3d(smem_addr(smem + L::kQ) + st * L::kTileBytes + half * L::kHalf, &P.mapQ, 64 * half, g.h * G,
+            tma_3d(smem_addr(smem + L::kQ) + st * L::kQBytes + half * L::kQHalf, &P.mapQ, 64 * half, g.h * G,
                    g.t0 + k * P.tokens, bar(kBarQFull + st));
         }
       }
@@ -426,71 +494,118 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
         mbar_wait(bar(kBarQFull + (k & 1)), (k >> 1) & 1, kWaitLimit);
     }
     __syncwarp();
-  } else if (warp == kMmaWarp) {
+  } else if (warp == kMmaWarp || warp == kMmaWarp + 1) {
     // ------------------------------------------------------------------ tensor cores
+    // A warp for each lane, one elected thread of it: the lanes' waits and issue overlap each other's
+    // products.  Item j of the lane uses S j % 2; the scores of item j + 1 are issued ahead of the
+    // values of item j.  The empty barriers of keys and values count two arrivals, and the only user of a
+    // tile makes both; those of query tiles count one of each lane.
     if (elect_one()) {
       constexpr bool kBf16 = TYPE == QMM_BF16;
       constexpr uint32_t kIdS = tc::idesc_16_f32(128, kTile, kBf16, false);
       constexpr uint32_t kIdO = tc::idesc_16_f32(128, D, kBf16, true);
       const uint64_t dq = tc::smem_desc_sw128(smem_addr(smem + L::kQ), 16, 1024);
-      const uint64_t dk = tc::smem_desc_sw128(smem_addr(smem + L::kKV), 16, 1024);
-      const uint64_t dv = tc::smem_desc_sw128(smem_addr(smem + L::kKV), L::kHalf, 1024);
-      uint32_t pos = 0, qpos = 0;
-      uint32_t done[2] = {0, 0};   // products p V issued for each lane
+      const uint64_t dk = tc::smem_desc_sw128(smem_addr(smem + L::kK), 16, 1024);
+      const uint64_t dv = tc::smem_desc_sw128(smem_addr(smem + L::kV), L::kHalf, 1024);
+      const uint32_t l = warp - kMmaWarp;
+      const uint32_t tS = tmem + 2 * kTile * l, tO = tmem + 4 * kTile + kRows * l;
+      const int barS = kBarS + 2 * l, barP = kBarP + 2 * l, barO = kBarO + 2 * l;
+      struct Pass {
+        Walker w;
+        int left = 0;                  // the lane's items left of the segment
+        bool pair = false, fresh = false;   // two row tiles; no item of the segment yet
+        uint32_t users = 0;            // kS * users of the segment's tiles
+        uint32_t step = 1;             // key tiles from item to item
+        uint32_t st = 0, parity = 0;   // stage of the next item's key tile; of its full barriers' next phases
+        uint32_t tiles = 0, items = 0, q = 0;   // key tiles, items and query tiles up to the segment's end
+      } qk, pv;
+      qk.w = pv.w = walk;
       bool ok = true;
-      while (ok && walk.next(P, g)) {
-        const int n = g.j1 - g.j0;
-        const bool pair = g.rows > P.tokens;
-        const int steps[2] = {pair ? n : (n + 1) / 2, pair ? n : n / 2};
-        auto tile_of = [&](int l, int i) { return pair ? i : 2 * i + l; };
-        auto scores = [&](int l, int i) {
-          const uint32_t q = pair ? qpos + l : qpos;
-          const int t = tile_of(l, i);
-          const uint32_t kp = pos + pos_k(t), st = kp % kS;
-          if (i == 0) ok = ok && wait(kBarQFull + (q & 1), (q >> 1) & 1);
-          ok = ok && wait(kBarFull + st, (kp / kS) & 1);
-          // the lane's p of the tile before sits where S goes: its product must have read it
-          if (done[l] > 0) ok = ok && wait(kBarO + l, (done[l] - 1) & 1);
-          if (!ok) return;
-          tc::fence_after_sync();
+      auto begin = [&](Pass& p) -> bool {   // the next segment that has items of this lane
+        while (ok && p.w.next(P, g)) {
+          const uint32_t n = g.j1 - g.j0;
+          p.pair = g.rows > P.tokens;
+          const uint32_t first = p.pair ? 0 : (p.items + l) & 1, at = p.tiles + first;
+          p.step = p.pair ? 1 : 2;
+          p.users = kS * (p.pair ? 2 : l);
+          p.left = p.pair ? n : (n + 1 - first) / 2;
+          p.st = at % kS;
+          p.tiles += n;
+          p.items += p.pair ? 2 * n : n;
+          p.q += p.pair ? 2 : 1;
+          p.fresh = true;
+          if (p.left > 0) return true;
+          if (&p == &qk) {   // no item: the segment's query tile passes by
+            ok = wait(kBarQFull + ((p.q - 1) & 1), ((p.q - 1) >> 1) & 1);
+            if (ok) mbar_arrive(bar(kBarQEmpty + ((p.q - 1) & 1)));
+          }
+        }
+        return false;
+      };
+      auto full = [&](Pass& p, int k) -> bool {   // wait for the item's keys or values
+        const uint32_t at = p.users + p.st;
+        const bool yes = wait(k + at, p.parity >> at & 1);
+        p.parity ^= 1u << at;
+        return yes;
+      };
+      auto step = [&](Pass& p, int empty) {   // behind an item's products
+        tc::commit(bar(empty + p.st));
+        if (!p.pair) tc::commit(bar(empty + p.st));
+        --p.left;
+        p.fresh = false;
+        p.st += p.step;
+        if (p.st >= kS) p.st -= kS;
+      };
+      bool more = true;   // scores are left to issue
+      auto scores = [&](auto b_, int reuse) {   // reuse: the phase of the product that read S's last p, or -1
+        constexpr int b = decltype(b_)::value;
+        if (qk.left == 0) more = more && begin(qk);
+        if (!more || !ok) return;
+        const uint32_t q = qk.q - (qk.pair ? 2 - l : 1), slot = q & 1;
+        if (qk.fresh) {
+          ok = wait(kBarQFull + ((qk.q - 1) & 1), ((qk.q - 1) >> 1) & 1);
+          if (qk.pair) ok = ok && wait(kBarQFull + (qk.q & 1), ((qk.q - 2) >> 1) & 1);
+        }
+        ok = ok && full(qk, kBarFullK);
+        if (reuse >= 0) ok = ok && wait(barO + b, reuse);   // the p of two items before sits where S goes
+        if (!ok) return;
+        tc::fence_after_sync();
 #pragma unroll
-          for (int k = 0; k < D / 16; ++k) {
-            const uint32_t off = (k / 4) * L::kHalf + (k % 4) * 32;
-            tc::mma_f16_ss(tmem + kTile * l, dq + (((q & 1) * L::kTileBytes + off) >> 4),
-                           dk + ((st * L::kTileBytes + off) >> 4), kIdS, k > 0);
-          }
-          tc::commit(bar(kBarS + l));
-          if (!pair || l == 1) tc::commit(bar(kBarEmpty + st));
-          const bool last_q = i + 1 == steps[l] && (pair || t == n - 1);
-          if (last_q) tc::commit(bar(kBarQEmpty + (q & 1)));
-        };
-        auto values = [&](int l, int i) {
-          const int t = tile_of(l, i);
-          const uint32_t vp = pos + pos_v(t, n), st = vp % kS;
-          ok = ok && wait(kBarFull + st, (vp / kS) & 1) && wait(kBarP + l, done[l] & 1);
-          if (!ok) return;
-          tc::fence_after_sync();
-          const int keys = min(kTile, g.keys - (g.j0 + t) * kTile);
-          for (int k = 0; k * 16 < keys; ++k)
-            tc::mma_f16_ts(tmem + 2 * kTile + kTile * l, tmem + kTile * l + 8 * k,
-                           dv + ((st * L::kTileBytes + k * 2048) >> 4), kIdO, i > 0 || k > 0);
-          tc::commit(bar(kBarO + l));
-          ++done[l];
-          if (!pair || l == 1) tc::commit(bar(kBarEmpty + st));
-        };
-        for (int l = 0; l < 2; ++l)
-          if (ok && steps[l] > 0) scores(l, 0);
-        for (int i = 0; ok && i < steps[0]; ++i)
-          for (int l = 0; l < 2; ++l) {
-            if (ok && i < steps[l]) values(l, i);
-            if (ok && i + 1 < steps[l]) scores(l, i + 1);
-          }
-        pos += 2 * n;
-        qpos += pair ? 2 : 1;
+        for (int k = 0; k < D / 64; ++k)   // 64 values of the head: 4 MMAs, 32 bytes of each row further
+          tc::mma_f16_ss_x4(tS + kTile * b, dq + ((slot * L::kQBytes + k * L::kQHalf) >> 4),
+                            dk + ((qk.st * L::kTileBytes + k * L::kHalf) >> 4), 2, kIdS, k > 0);
+        tc::commit(bar(barS + b));
+        if (qk.left == 1) {
+          tc::commit(bar(kBarQEmpty + slot));
+          if (qk.pair) tc::commit(bar(kBarQEmpty + (slot ^ 1)));
+        }
+        step(qk, kBarEmptyK);
+      };
+      auto values = [&](auto b_, uint32_t parity) {
+        constexpr int b = decltype(b_)::value;
+        if (pv.left == 0 && !begin(pv)) return false;
+        ok = full(pv, kBarFullV) && wait(barP + b, parity);
+        if (!ok) return false;
+        tc::fence_after_sync();
+        tc::mma_f16_ts_x4(tO, tS + kTile * b, dv + ((pv.st * L::kTileBytes) >> 4), 128, kIdO,
+                          !pv.fresh);   // 16 rows of V an MMA; the segment's first item begins O
+        tc::commit(bar(barO + b));
+        if (pv.left == 1) tc::commit(bar(kBarEnd + l));
+        step(pv, kBarEmptyV);
+        return true;
+      };
+      using S0 = std::integral_constant<int, 0>;
+      using S1 = std::integral_constant<int, 1>;
+      scores(S0{}, -1);
+      for (uint32_t r = 0; ok; ++r) {   // two items
+        scores(S1{}, r > 0 ? (r - 1) & 1 : -1);
+        if (!ok || !values(S0{}, r & 1)) break;
+        scores(S0{}, r & 1);
+        if (!ok || !values(S1{}, r & 1)) break;
       }
       // no tensor-core operation of this CTA is in flight when it ends
-      tc::commit(bar(kBarDrain));
-      mbar_wait(bar(kBarDrain), 0, kWaitLimit);
+      tc::commit(bar(kBarDrain + l));
+      mbar_wait(bar(kBarDrain + l), 0, kWaitLimit);
     }
     __syncwarp();
   } else {
@@ -498,15 +613,16 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
     const int l = warp / kLaneWarps;                 // this warp's lane of flash attention
     const int row = (warp % kLaneWarps) * 32 + lane;
     const uint32_t lanes = (uint32_t)(warp % kLaneWarps) << 21;   // first TMEM lane << 16
-    const uint32_t tS = tmem + lanes + kTile * l, tO = tmem + lanes + 2 * kTile;
+    const uint32_t tS = tmem + lanes + 2 * kTile * l, tO = tmem + lanes + 4 * kTile;
     const float c = a.scale * kLog2e;
     float2* stats = reinterpret_cast<float2*>(smem + L::kStats);
-    uint32_t pos = 0, seen = 0, joins = 0, segs = 0;
+    uint32_t parity = 0;   // of the next phases of the value stages' full barriers (single, both)
+    uint32_t pos = 0, seen = 0, joins = 0, segs = 0, items = 0, ends = 0;
     bool ok = true;
     while (ok && walk.next(P, g)) {
       const int n = g.j1 - g.j0;
       const bool pair = g.rows > P.tokens;
-      const int steps = pair ? n : (n + 1 - l) / 2;
+      const int first = pair ? 0 : (items + l) & 1;               // the lane's first key tile of the segment
       const int tok0 = pair ? l * P.tokens : 0;                   // the lane's rows of the block
       const int live = min(P.tokens, g.rows - tok0) * G;          // rows of the tile in use
       const int tok = tok0 + row / G;
@@ -514,64 +630,22 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
       const int clean_from = g.own ? clampi(g.first_keys + tok0, 0, g.keys) : g.keys;   // keys that not every row sees
       const bool idle = (warp % kLaneWarps) * 32 >= live;
       ++segs;
+      items += pair ? 2 * n : n;
       float top = -INFINITY, sum = 0.0f;
-      for (int i = 0; i < steps; ++i) {
-        const int t = g.j0 + (pair ? i : 2 * i + l);
-        ok = ok && wait_w(kBarS + l, seen & 1);
-        if (!ok) break;
-        ++seen;
-        tc::fence_after_sync();
-        const int base = t * kTile;
-        if (!idle) {
-          uint32_t s[128];
-          tc::ld_wait_x128(tS, s);
-          const int vis = sees - base;
-          if (__any_sync(0xffffffffu, vis < kTile)) {
-#pragma unroll
-            for (int k = 0; k < kTile; ++k)
-              if (k >= vis) s[k] = 0xFF800000u;   // -inf
-          }
-          float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-          for (int k = 0; k < kTile; ++k) mx[k & 3] = fmaxf(mx[k & 3], __uint_as_float(s[k]));
-          const float now = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c;
-          const bool grew = now > top + kGrow || (top == -INFINITY && now > -INFINITY);
-          if (i > 0 && __any_sync(0xffffffffu, grew)) {
-            const float keep = grew ? exp2_fast(top - now) : 1.0f;
-            sum *= keep;
-#pragma unroll 1
-            for (int k = 0; k < D; k += 32) {
-              uint32_t o[32];
-              tc::ld_wait_x32(tO + kTile * l + k, o);
-#pragma unroll
-              for (int q = 0; q < 32; ++q) o[q] = __float_as_uint(__uint_as_float(o[q]) * keep);
-              tc::st_x32(tO + kTile * l + k, o);
-            }
-          }
-          if (grew) top = now;
-          const float off = top == -INFINITY ? 0.0f : -top;
-          float part[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-          for (int k = 0; k < kTile; k += 2) {
-            const float p0 = exp2_fast(__fmaf_rn(__uint_as_float(s[k]), c, off));
-            const float p1 = exp2_fast(__fmaf_rn(__uint_as_float(s[k + 1]), c, off));
-            part[k & 3] += p0;
-            part[(k & 3) + 1] += p1;
-            s[k / 2] = pack2<TYPE>(p0, p1);
-          }
-          sum += (part[0] + part[1]) + (part[2] + part[3]);
-          tc::st_x32(tS, s);
-          tc::st_x32(tS + 32, s + 32);
-          tc::wait_st();
-        }
+      uint32_t st = (pos + first) % kS;   // stage of the item's values
+      for (int i = first; i < n; i += pair ? 1 : 2) {
+        const int base = (g.j0 + i) * kTile;
+        const int buf = seen & 1;   // which S of the lane
+        const uint32_t at = pair ? kS + st : st;
+        parity ^= 1u << at;
+        ok = wait_w(kBarS + 2 * l + buf, (seen >> 1) & 1);
         // value rows that a weight of 0 must not meet
         const int upto = min(g.keys, base + kTile) - base;
-        if (clean_from < base + kTile && (upto < kTile || g.own)) {
-          const uint32_t vp = pos + pos_v(t - g.j0, n), st = vp % kS;
-          ok = wait_w(kBarFull + st, (vp / kS) & 1);
+        if (ok && clean_from < base + kTile && (upto < kTile || g.own)) {
+          ok = wait_w(kBarFullV + kS * (pair ? 2 : l) + st, !(parity >> at & 1));
           if (!ok) break;
-          uint8_t* V = smem + L::kKV + st * L::kTileBytes;
-          const int from = max(0, clean_from - base), end = (upto + 15) & ~15;
+          uint8_t* V = smem + L::kV + st * L::kTileBytes;
+          const int from = max(0, clean_from - base), end = (upto + 63) & ~63;
           for (int v = (warp % kLaneWarps) * 32 + lane; v < (end - from) * (D / 8); v += 32 * kLaneWarps) {
             const int r = from + v / (D / 8), piece = v % (D / 8);
             uint4* at = reinterpret_cast<uint4*>(V + (piece / 8) * L::kHalf + r * 128 + (piece % 8) * 16);
@@ -592,69 +666,156 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
           }
           fence_proxy_async_smem();
         }
+        if (!ok) break;
+        tc::fence_after_sync();
+        if (!idle) {
+          uint32_t s[kTile];
+          tc::ld_wait_x64(tS + kTile * buf, s);
+          const int vis = sees - base;
+          if (__any_sync(0xffffffffu, vis < kTile)) {
+#pragma unroll
+            for (int k = 0; k < kTile; ++k)
+              if (k >= vis) s[k] = 0xFF800000u;   // -inf
+          }
+          float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+          for (int k = 0; k < kTile; k += 8)
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+              mx[q] = fmaxf(mx[q], fmaxf(__uint_as_float(s[k + 2 * q]), __uint_as_float(s[k + 2 * q + 1])));
+          const float now = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c;
+          const bool grew = now > top + kGrow || (top == -INFINITY && now > -INFINITY);
+          if (i > first && __any_sync(0xffffffffu, grew)) {
+            // the item before is in O (S, formed after the one before that was, says so much of that one)
+            ok = wait_w(kBarO + 2 * l + (buf ^ 1), ((seen - 1) >> 1) & 1);
+            if (!ok) break;
+            tc::fence_after_sync();
+            const float keep = grew ? exp2_fast(top - now) : 1.0f;
+            sum *= keep;
+#pragma unroll 1
+            for (int k = 0; k < D; k += 32) {
+              uint32_t o[32];
+              tc::ld_wait_x32(tO + kRows * l + k, o);
+#pragma unroll
+              for (int q = 0; q < 32; ++q) o[q] = __float_as_uint(__uint_as_float(o[q]) * keep);
+              tc::st_x32(tO + kRows * l + k, o);
+            }
+          }
+          if (grew) top = now;
+          const float off = top == -INFINITY ? 0.0f : -top;
+          const uint64_t cc = f2pack(c, c), oo = f2pack(off, off);
+          uint64_t part0 = 0, part1 = 0;   // sums of weights, two fp32 each
+#pragma unroll
+          for (int k = 0; k < kTile; k += 4) {
+            const float2 x = f2unpack(fma2(f2pack(__uint_as_float(s[k]), __uint_as_float(s[k + 1])), cc, oo));
+            const float2 y = f2unpack(fma2(f2pack(__uint_as_float(s[k + 2]), __uint_as_float(s[k + 3])), cc, oo));
+            const float p0 = exp2_fast(x.x), p1 = exp2_fast(x.y), p2 = exp2_fast(y.x), p3 = exp2_fast(y.y);
+            part0 = add2(part0, f2pack(p0, p1));
+            part1 = add2(part1, f2pack(p2, p3));
+            s[k / 2] = pack2<TYPE>(p0, p1);
+            s[k / 2 + 1] = pack2<TYPE>(p2, p3);
+          }
+          tc::st_x32(tS + kTile * buf, s);
+          const float2 u = f2unpack(part0), v = f2unpack(part1);
+          sum += (u.x + u.y) + (v.x + v.y);
+          tc::wait_st();
+        }
         tc::fence_before_sync();
         __syncwarp();
-        if (lane == 0) mbar_arrive(bar(kBarP + l));
+        if (lane == 0) mbar_arrive(bar(kBarP + 2 * l + buf));
+        ++seen;
+        st += pair ? 1 : 2;
+        if (st >= kS) st -= kS;
       }
-      pos += 2 * n;
+      pos += n;   // value tiles before the next segment's
       if (!ok) break;
 
       // ---- the segment's sums to the workspace
-      if (steps > 0) ok = wait_w(kBarO + l, (seen - 1) & 1);
+      const bool some = first < n;   // the lane had key tiles
+      if (some) ok = wait_w(kBarEnd + l, ends++ & 1);
       if (!pair) {   // the other lane's state of the same rows
-        stats[l * kTile + row] = make_float2(top, steps > 0 ? sum : -1.0f);
+        stats[l * kRows + row] = make_float2(top, some ? sum : -1.0f);
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(kBarJoin));
         ok = ok && wait_w(kBarJoin, joins++ & 1);
       }
       if (!ok) break;
       tc::fence_after_sync();
-      const int64_t head = (int64_t)g.h * G + row % G;
-      const bool mine = row < live;
       const bool inside = g.j0 > 0;   // not the first segment of its group: the CTA's own record
-      int64_t rec = inside ? (int64_t)blockIdx.x * 2 * kTile + (pair ? l * kTile : 0) + row
-                           : ((int64_t)(g.own ? a.T : 0) + g.t0 + tok) * a.Hq + head;
-      float* out = (inside ? P.o_cta : P.o_rows) + rec * D;
-      RowStat* stat = (inside ? P.s_cta : P.s_rows) + rec;
       const uint32_t odd = *reinterpret_cast<volatile uint32_t*>(&M.odd[segs & 7]) == segs;
-      if (pair) {
-        if (!idle) {
-#pragma unroll 1
-          for (int k = 0; k < D; k += 32) {
-            uint32_t o[32];
-            tc::ld_wait_x32(tO + kTile * l + k, o);
-            if (mine)
-#pragma unroll
-              for (int q = 0; q < 32; q += 8) store8(out + k + q, o + q);
-          }
-          if (mine) *stat = RowStat{top, sum, odd, 0u};
+      auto record = [&](int r) -> int64_t {   // of row r of the tile
+        return inside ? (int64_t)blockIdx.x * 2 * kRows + (pair ? l * kRows : 0) + r
+                      : ((int64_t)(g.own ? a.T : 0) + g.t0 + tok0 + r / G) * a.Hq + (int64_t)g.h * G + r % G;
+      };
+      float* out = inside ? P.o_cta : P.o_rows;
+      if (row < live && (pair || l == 0)) {
+        RowStat st{top, sum, odd, 0u};
+        if (!pair) {
+          const float2 s0 = stats[row], s1 = stats[kRows + row];
+          const bool b0 = !(s0.y < 0.0f), b1 = !(s1.y < 0.0f);
+          st.top = fmaxf(b0 ? s0.x : -INFINITY, b1 ? s1.x : -INFINITY);
+          st.sum = (b0 && !(s0.x == -INFINITY && s0.y == 0.0f) ? s0.y * exp2_fast(s0.x - st.top) : 0.0f) +
+                   (b1 && !(s1.x == -INFINITY && s1.y == 0.0f) ? s1.y * exp2_fast(s1.x - st.top) : 0.0f);
         }
-      } else {
-        const float2 s0 = stats[row], s1 = stats[kTile + row];
-        const bool two = s1.y >= 0.0f || s1.y != s1.y;   // lane 1 had key tiles
-        const float best = two ? fmaxf(s0.x, s1.x) : s0.x;
-        const float f0 = s0.x == -INFINITY && s0.y == 0.0f ? 0.0f : exp2_fast(s0.x - best);
-        const float f1 = !two || (s1.x == -INFINITY && s1.y == 0.0f) ? 0.0f : exp2_fast(s1.x - best);
-        if (!idle) {
+        (inside ? P.s_cta : P.s_rows)[record(row)] = st;
+      }
+      // O: 16 rows x 32 columns at a time; the four threads of a row write 128 bytes of it.  A row's
+      // values are kept in the order the load gives them (column_of).
+      if (!idle) {
+        const int c0 = pair ? 0 : l * (D / 2), c1 = pair ? D : c0 + D / 2;   // one tile: half of O for each lane's warps
 #pragma unroll 1
-          for (int k = l * (D / 2); k < (l + 1) * (D / 2); k += 32) {   // half of O for each lane's warps
-            uint32_t o[32];
-            tc::ld_wait_x32(tO + k, o);
+        for (int hh = 0; hh < 2 && (warp % kLaneWarps) * 32 + 16 * hh < live; ++hh) {
+          float f[2][2] = {{1.0f, 1.0f}, {1.0f, 1.0f}};   // [row][lane]
+          bool has[2] = {true, true};
+          float* dst[2];
+          bool mine[2];
 #pragma unroll
-            for (int q = 0; q < 32; ++q) o[q] = __float_as_uint(__uint_as_float(o[q]) * f0);
-            if (two) {
-              uint32_t o1[32];
-              tc::ld_wait_x32(tO + kTile + k, o1);
-#pragma unroll
-              for (int q = 0; q < 32; ++q)
-                o[q] = __float_as_uint(__fmaf_rn(__uint_as_float(o1[q]), f1, __uint_as_float(o[q])));
+          for (int k = 0; k < 2; ++k) {
+            const int r = (warp % kLaneWarps) * 32 + 16 * hh + 8 * k + lane / 4;
+            mine[k] = r < live;
+            dst[k] = out + record(r) * D + 8 * (lane & 3);
+            if (!pair) {
+              const float2 s0 = stats[r], s1 = stats[kRows + r];
+              has[0] = !(s0.y < 0.0f);
+              has[1] = !(s1.y < 0.0f);
+              const float best = fmaxf(has[0] ? s0.x : -INFINITY, has[1] ? s1.x : -INFINITY);
+              f[k][0] = s0.x == -INFINITY && s0.y == 0.0f ? 0.0f : exp2_fast(s0.x - best);
+              f[k][1] = s1.x == -INFINITY && s1.y == 0.0f ? 0.0f : exp2_fast(s1.x - best);
             }
-            if (mine)
-#pragma unroll
-              for (int q = 0; q < 32; q += 8) store8(out + k + q, o + q);
           }
-          if (mine && l == 0) *stat = RowStat{best, two ? __fmaf_rn(s1.y, f1, s0.y * f0) : s0.y * f0, odd, 0u};
+#pragma unroll 1
+          for (int k = c0; k < c1; k += 32) {
+            const uint32_t at = tmem + lanes + ((uint32_t)hh << 20) + 4 * kTile + k;
+            uint32_t o[16];
+            if (pair) {
+              tc::ld_wait_16x32(at + kRows * l, o);
+            } else {
+              if (has[0]) {
+                tc::ld_wait_16x32(at, o);
+#pragma unroll
+                for (int q = 0; q < 16; ++q) o[q] = __float_as_uint(__uint_as_float(o[q]) * f[(q >> 1) & 1][0]);
+              } else {
+#pragma unroll
+                for (int q = 0; q < 16; ++q) o[q] = 0u;
+              }
+              if (has[1]) {
+                uint32_t o1[16];
+                tc::ld_wait_16x32(at + kRows, o1);
+#pragma unroll
+                for (int q = 0; q < 16; ++q)
+                  o[q] = __float_as_uint(__fmaf_rn(__uint_as_float(o1[q]), f[(q >> 1) & 1][1], __uint_as_float(o[q])));
+              }
+            }
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+              const uint32_t w[8] = {o[2 * q], o[2 * q + 1], o[2 * q + 4], o[2 * q + 5],
+                                     o[2 * q + 8], o[2 * q + 9], o[2 * q + 12], o[2 * q + 13]};
+              if (mine[q]) store8(dst[q] + k, w);
+            }
+          }
         }
+      }
+      if (!pair) {
         // both lanes have read both sums before either lane's next product writes one
         tc::fence_before_sync();
         __syncwarp();
@@ -676,69 +837,119 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
 // it (in the row's own record) and those of the CTAs whose piece begins inside it.
 constexpr int kCombineWarps = 8;
 
+// Column of the value at position p of a row's record: the epilogue keeps columns 8k + 2q, 8k + 2q + 1
+// (k = 0..3) of each 32 together, as the 8 values of thread q of four.
+__device__ __forceinline__ int column_of(int p) {
+  return (p & ~31) + 8 * ((p & 7) >> 1) + 2 * ((p & 31) >> 3) + (p & 1);
+}
+
 template <int D, int TYPE>
 __global__ void __launch_bounds__(32 * kCombineWarps) attn_combine_kernel(const __grid_constant__ Params P) {
-  constexpr int kV = D / 32;
+  constexpr int kV = D / 32;   // values of a lane: positions kV * lane and on
   const qmm_attn_args& a = P.a;
   __shared__ int stream;
+  __shared__ unsigned long long units_before;   // units of the stream's row blocks before the row's
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int t = blockIdx.x, lane = threadIdx.x & 31;
   const int head = blockIdx.y * kCombineWarps + (threadIdx.x >> 5);
-  if (threadIdx.x == 0) stream = -1;
+  if (threadIdx.x == 0) { stream = -1; units_before = 0; }
   __syncthreads();
   for (int b = threadIdx.x; b < a.B; b += blockDim.x) {
     const Stream s = stream_of(a, b);
     if (t >= s.t0 && t < s.t0 + s.m) stream = b;   // one stream, if the starts do not decrease
   }
-  asm volatile("griddepcontrol.wait;" ::: "memory");
   __syncthreads();
-  if (head >= a.Hq) return;
   const int b = stream, G = a.Hq / a.Hk, block = 2 * P.tokens, h = head / G;
-  const int64_t W = P.plan[0], C = P.plan[1];
-  float o[kV] = {}, top = -INFINITY, sum = 0.0f;
-  uint32_t odd = 0;
-
-  auto add = [&](const float* rec_o, const RowStat& r) {
-    if (r.top == -INFINITY && r.sum == 0.0f) return;   // the row saw none of the segment's keys
-    const float best = fmaxf(top, r.top);
-    const float f0 = top == -INFINITY && sum == 0.0f ? 0.0f : exp2_fast(top - best), f1 = exp2_fast(r.top - best);
-    float x[kV];
-    if constexpr (kV == 4) {
-      const float4 v = *reinterpret_cast<const float4*>(rec_o + 4 * lane);
-      x[0] = v.x; x[1] = v.y; x[2] = v.z; x[3] = v.w;
-    } else {
-      const float2 v = *reinterpret_cast<const float2*>(rec_o + 2 * lane);
-      x[0] = v.x; x[1] = v.y;
-    }
-#pragma unroll
-    for (int k = 0; k < kV; ++k) o[k] = __fmaf_rn(x[k], f1, o[k] * f0);
-    sum = __fmaf_rn(r.sum, f1, sum * f0);
-    top = best;
-  };
-  // the segments of the group whose first tile is `first` in the list and that has `tiles` tiles
-  auto group = [&](int own, int64_t first, int tiles, int tok) {
-    if (tiles == 0) return;
-    const int64_t rec = ((int64_t)(own ? a.T : 0) + t) * a.Hq + head;
-    const RowStat r = P.s_rows[rec];
-    odd |= r.odd;
-    add(P.o_rows + rec * D, r);
-    const int row = (tok < P.tokens ? tok * G : kTile + (tok - P.tokens) * G) + head % G;
-    for (int64_t cta = ((first + 1) * C + W - 1) / W; cta < C && cta * W / C < first + tiles; ++cta) {
-      const int64_t at = cta * 2 * kTile + row;
-      const RowStat q = P.s_cta[at];
-      odd |= q.odd;
-      add(P.o_cta + at * D, q);
-    }
-  };
   Stream s{};
   if (b >= 0) {
     s = stream_of(a, b);
-    const int ptiles = tiles_of((int)a.prefix_len);
-    group(0, ((int64_t)(t / block) * a.Hk + h) * ptiles, ptiles, t % block);
     const int rb = (t - s.t0) / block;
-    int64_t first = P.plan[2 + b];
-    for (int k = 0; k < rb; ++k) first += (int64_t)a.Hk * tiles_of(keys_of(s, k, block));
-    const int tiles = tiles_of(keys_of(s, rb, block));
-    group(1, first + (int64_t)h * tiles, tiles, (t - s.t0) % block);
+    if (rb > 0) {
+      unsigned long long mine = 0;
+      for (int k = threadIdx.x; k < rb; k += blockDim.x) mine += (unsigned long long)a.Hk * units_of(tiles_of(keys_of(s, k, block)));
+      atomicAdd(&units_before, mine);
+      __syncthreads();
+    }
+  }
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (head >= a.Hq) return;
+  float o[kV] = {}, top = -INFINITY, sum = 0.0f;
+  uint32_t odd = 0;
+  if (b >= 0) {
+    const int64_t W = P.plan[0], C = P.plan[1];
+    const int64_t first = P.plan[2 + b] + (int64_t)units_before;
+    // the records of the row: of the prefix's group, then of the own keys' group
+    int64_t cta[2];
+    int n[2], row[2];
+#pragma unroll
+    for (int own = 0; own < 2; ++own) {
+      const int tok = own ? t - s.t0 : t, rb = tok / block, in = tok % block;
+      int tiles = tiles_of((int)a.prefix_len);
+      int64_t at = ((int64_t)rb * a.Hk + h) * units_of(tiles) + kLead;   // unit of the group's first tile
+      if (own) {
+        tiles = tiles_of(keys_of(s, rb, block));
+        at = first + (int64_t)h * units_of(tiles) + kLead;
+      }
+      row[own] = (in < P.tokens ? in * G : kRows + (in - P.tokens) * G) + head % G;
+      n[own] = 0;
+      cta[own] = 0;
+      if (tiles > 0) {
+        cta[own] = piece_from(at + 1, W, C);
+        n[own] = 1 + (int)max((int64_t)0, min(C, piece_from(at + tiles, W, C)) - cta[own]);
+      }
+    }
+    const int all = n[0] + n[1];
+    for (int r0 = 0; r0 < all; r0 += 32) {
+      // one record a lane: its weight
+      const int r = r0 + lane, own = r >= n[0], k = own ? r - n[0] : r;
+      const bool live = r < all;
+      const int64_t at = k == 0 ? ((int64_t)(own ? a.T : 0) + t) * a.Hq + head
+                                : ((own ? cta[1] : cta[0]) + k - 1) * 2 * kRows + (own ? row[1] : row[0]);
+      RowStat st{-INFINITY, 0.0f, 0u, 0u};
+      if (live) st = (k == 0 ? P.s_rows : P.s_cta)[at];
+      const float* src = (k == 0 ? P.o_rows : P.o_cta) + at * D;
+      float best = st.top;
+#pragma unroll
+      for (int off = 16; off >= 1; off >>= 1) best = fmaxf(best, __shfl_xor_sync(0xffffffffu, best, off));
+      best = fmaxf(best, top);
+      const bool saw = !(st.top == -INFINITY && st.sum == 0.0f);   // the row saw some of the segment's keys
+      const float w = saw ? exp2_fast(st.top - best) : 0.0f;
+      float part = saw ? st.sum * w : 0.0f;
+#pragma unroll
+      for (int off = 16; off >= 1; off >>= 1) part += __shfl_xor_sync(0xffffffffu, part, off);
+      const float keep = r0 > 0 && !(top == -INFINITY && sum == 0.0f) ? exp2_fast(top - best) : 0.0f;
+      sum = __fmaf_rn(sum, keep, part);
+      top = best;
+      odd |= __any_sync(0xffffffffu, st.odd != 0);
+#pragma unroll
+      for (int q = 0; q < kV; ++q) o[q] *= keep;
+      const unsigned who = __ballot_sync(0xffffffffu, live && saw);
+      constexpr int kAhead = 8;
+      for (int j0 = 0; j0 < 32 && (who >> j0) != 0; j0 += kAhead) {
+        float x[kAhead][kV];
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j) {
+          const float* p = reinterpret_cast<const float*>(__shfl_sync(0xffffffffu, (unsigned long long)src, j0 + j));
+#pragma unroll
+          for (int q = 0; q < kV; ++q) x[j][q] = 0.0f;
+          if (who >> (j0 + j) & 1) {
+            if constexpr (kV == 4) {
+              const float4 v = *reinterpret_cast<const float4*>(p + 4 * lane);
+              x[j][0] = v.x; x[j][1] = v.y; x[j][2] = v.z; x[j][3] = v.w;
+            } else {
+              const float2 v = *reinterpret_cast<const float2*>(p + 2 * lane);
+              x[j][0] = v.x; x[j][1] = v.y;
+            }
+          }
+        }
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j) {
+          const float f = __shfl_sync(0xffffffffu, w, j0 + j);
+#pragma unroll
+          for (int q = 0; q < kV; ++q) o[q] = __fmaf_rn(x[j][q], f, o[q]);
+        }
+      }
+    }
   }
   const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
 #pragma unroll
@@ -750,10 +961,10 @@ __global__ void __launch_bounds__(32 * kCombineWarps) attn_combine_kernel(const 
     for (int j = max(0, s.len - s.m); j < sees; ++j) {
       const int page = a.pages[b * a.pages_per_stream + j / a.page_size];
       if (page < 0 || page >= a.n_slots / a.page_size) continue;
-      const int64_t at = (((int64_t)page * a.page_size + j % a.page_size) * a.Hk + h) * D + kV * lane;
+      const int64_t at = (((int64_t)page * a.page_size + j % a.page_size) * a.Hk + h) * D;
 #pragma unroll
       for (int k = 0; k < kV; ++k) {
-        const uint16_t raw = static_cast<const uint16_t*>(a.V_cache)[at + k];
+        const uint16_t raw = static_cast<const uint16_t*>(a.V_cache)[at + column_of(kV * lane + k)];
         const float v = TYPE == QMM_BF16 ? __uint_as_float((uint32_t)raw << 16) : __half2float(__ushort_as_half(raw));
         if (!(fabsf(v) < INFINITY)) extra[k] += v;
       }
@@ -761,12 +972,10 @@ __global__ void __launch_bounds__(32 * kCombineWarps) attn_combine_kernel(const 
 #pragma unroll
     for (int k = 0; k < kV; ++k) o[k] += extra[k];
   }
-  uint32_t w[kV / 2];
+  uint16_t* out = static_cast<uint16_t*>(a.O) + (int64_t)t * a.ldo + (int64_t)head * D;
 #pragma unroll
-  for (int k = 0; k < kV / 2; ++k) w[k] = pack2<TYPE>(o[2 * k], o[2 * k + 1]);
-  uint16_t* out = static_cast<uint16_t*>(a.O) + (int64_t)t * a.ldo + (int64_t)head * D + kV * lane;
-  if constexpr (kV == 4) *reinterpret_cast<uint2*>(out) = make_uint2(w[0], w[1]);
-  else *reinterpret_cast<uint32_t*>(out) = w[0];
+  for (int k = 0; k < kV; k += 2)
+    *reinterpret_cast<uint32_t*>(out + column_of(kV * lane + k)) = pack2<TYPE>(o[k], o[k + 1]);
   if (a.lse && lane == 0) a.lse[(int64_t)t * a.Hq + head] = sum == 0.0f ? -INFINITY : __fmaf_rn(top, kLn2, logf(sum));
 }
 
@@ -777,7 +986,7 @@ size_t up(size_t n) { return (n + 255) & ~(size_t)255; }
 struct Space {
   size_t o_rows, s_rows, o_cta, s_cta, plan, total;
   explicit Space(const qmm_attn_args& a) {
-    const size_t rows = 2 * (size_t)a.T * a.Hq, cta = (size_t)kMaxCtas * 2 * kTile;
+    const size_t rows = 2 * (size_t)a.T * a.Hq, cta = (size_t)kMaxCtas * 2 * kRows;
     o_rows = 0;
     o_cta = o_rows + up(rows * a.D * sizeof(float));
     s_rows = o_cta + up(cta * a.D * sizeof(float));
@@ -817,7 +1026,9 @@ cudaError_t launch(const qmm_attn_args& a, void* workspace, cudaStream_t stream)
   const int G = a.Hq / a.Hk;
   Params P;
   P.a = a;
-  P.tokens = kTile / G;
+  P.tokens = kRows / G;
+  P.n_pages = (int)(a.n_slots / a.page_size);
+  P.page_shift = 31 - __builtin_clz((unsigned)a.page_size);
   const Space sp(a);
   uint8_t* ws = reinterpret_cast<uint8_t*>(up(reinterpret_cast<uintptr_t>(workspace)));
   P.o_rows = reinterpret_cast<float*>(ws + sp.o_rows);
@@ -835,18 +1046,23 @@ cudaError_t launch(const qmm_attn_args& a, void* workspace, cudaStream_t stream)
   if (e != cudaSuccess) return e;
   const int sms = sm_count();
   if (sms < 1) return cudaErrorNoDevice;
-  attn_kernel<D, TYPE><<<sms < kMaxCtas ? sms : kMaxCtas, kThreads, Smem<D>::kTotal, stream>>>(P);
-  e = cudaGetLastError();
-  if (e != cudaSuccess) return e;
+  // Both launches may be scheduled while the one before them finishes (programmatic dependent launch);
+  // each waits for it before it reads or writes memory.
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(a.T, (a.Hq + kCombineWarps - 1) / kCombineWarps);
-  cfg.blockDim = dim3(32 * kCombineWarps);
+  cfg.gridDim = dim3(sms < kMaxCtas ? sms : kMaxCtas);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = Smem<D>::kTotal;
   cfg.stream = stream;
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
+  e = cudaLaunchKernelEx(&cfg, attn_kernel<D, TYPE>, P);
+  if (e != cudaSuccess) return e;
+  cfg.gridDim = dim3(a.T, (a.Hq + kCombineWarps - 1) / kCombineWarps);
+  cfg.blockDim = dim3(32 * kCombineWarps);
+  cfg.dynamicSmemBytes = 0;
   return cudaLaunchKernelEx(&cfg, attn_combine_kernel<D, TYPE>, P);
 }
 
