@@ -17,9 +17,10 @@
 //     S = Q K^T              tcgen05, both operands in shared memory (TMA, 128-byte swizzle)
 //     p = 2^(c S - m)        a thread per row, S from tensor memory, c = scale log2 e
 //     O += p V               tcgen05, p (16 bits, rounded once) from tensor memory, V MN-major
-// Each lane has two S, so the scores of its next item are formed during the softmax of this one: 64
-// keys a tile make room for them in tensor memory (2 lanes x (2 x 64 + 128 columns)).  The lanes take
-// items (key tiles) in turn across segments, and a warp each issues their products.
+// A softmax frees S as soon as it has it in registers, and p has two places of its own, so the scores of
+// the next item are formed during the softmax of this one: 64 keys a tile make room for that in
+// tensor memory (2 lanes x (64 + 2 x 32 + 128 columns)).  The lanes take items (key tiles) in turn
+// across segments, and a warp each issues their products.
 // m is the maximum when it was last moved: it moves, and O is rescaled, only when the row's maximum
 // grew by more than 8 (2^8 in a 16-bit p costs no precision), so O stays in tensor memory.
 //
@@ -51,16 +52,17 @@ constexpr int kMaxCtas = 152;
 constexpr int kLaneWarps = 4;
 constexpr int kLoadWarp = 8, kMmaWarp = 9 /* and 10 */, kQWarp = 11;
 constexpr int kThreads = 12 * 32;
-constexpr uint32_t kTmemCols = 512;   // lane L: S and p at 128 L and 128 L + 64, O at 256 + 128 L
+constexpr uint32_t kTmemCols = 512;   // lane L: S at 64 L, p at 128 + 64 L and 160 + 64 L, O at 256 + 128 L
 constexpr float kGrow = 8.0f;
 constexpr uint32_t kWaitLimit = 1u << 17;
 constexpr float kLog2e = 1.44269504088896340736f, kLn2 = 0.69314718055994530942f;
 
-// One row's state beside its O: the maximum in units of log2, the weight sum, and whether values
-// were taken out of the block (nonzero).
+// One row's state beside its O: the maximum in units of log2, the weight sum, whether values were
+// taken out of the block (nonzero), and, in the record of a group's first segment, the CTAs that hold
+// the others: their number << 16 | the first of them.
 struct RowStat {
   float top, sum;
-  uint32_t odd, unused;
+  uint32_t odd, rest;
 };
 
 struct Params {
@@ -70,7 +72,6 @@ struct Params {
   RowStat* s_rows;
   float* o_cta;       // [kMaxCtas][2 * kRows][D]: a CTA's first segment that begins inside a group
   RowStat* s_cta;
-  int64_t* plan;      // [0] units, [1] CTAs with work, [2 + b] first unit of stream b's own keys
   int tokens;         // of a row tile
   int n_pages, page_shift;
   uint32_t wait_polls, wait_ns;
@@ -97,15 +98,22 @@ static_assert(Smem<128>::kTotal <= 227 * 1024 && Smem<64>::kTotal <= 227 * 1024,
 // 0, lane 1, both), and a query tile is waited for and released by both lanes whoever uses it.
 enum : int {
   kBarFullK = 0 /* 5 users + stage */, kBarFullV = 15, kBarEmptyK = 30, kBarEmptyV = 35, kBarQFull = 40, kBarQEmpty = 42,
-  kBarS = 44 /* 2 lane + S */, kBarP = 48, kBarO = 52, kBarEnd = 56, kBarJoin = 58, kBarDrain = 59, kBars = 61
+  kBarS = 44, kBarFree = 46, kBarP = 48 /* 2 lane + item % 2 */, kBarO = 52, kBarEnd = 56, kBarJoin = 58, kBarDrain = 59,
+  kBars = 61
+};
+
+// Rows and own keys of a stream.
+struct Stream {
+  int t0, m, len;
 };
 
 struct Misc {
   uint64_t bars[kBars];
-  int64_t total, prefix_tiles, w0, w1;
+  int64_t w0, w1, per;   // this CTA's units, units of a CTA
   int64_t scan[kThreads / 32];
-  int b, rb, h;
-  int64_t unit;       // first unit within its group
+  int b, rb, h, rows;
+  Stream s;           // stream b, if b >= 0
+  int64_t unit;       // end of the CTA's units within that group
   uint32_t tmem;
   int abort;
   uint32_t odd[8];    // [s % 8]: s, if values were taken out in segment s (the lanes drift a few apart)
@@ -114,10 +122,7 @@ static_assert(sizeof(Misc) <= 1024, "misc");
 
 __device__ __forceinline__ int clampi(int v, int lo, int hi) { return v < lo ? lo : (v > hi ? hi : v); }
 
-// Rows and own keys of stream b, whatever the arrays hold.
-struct Stream {
-  int t0, m, len;
-};
+// Stream b, whatever the arrays hold.
 __device__ __forceinline__ Stream stream_of(const qmm_attn_args& a, int b, bool* bad = nullptr) {
   const int r0 = a.row_starts[b], r1 = a.row_starts[b + 1], n = a.kv_lens[b];
   const int cap = (int)(a.pages_per_stream * a.page_size);
@@ -135,15 +140,6 @@ __device__ __forceinline__ int keys_of(const Stream& s, int rb, int block) {
 __device__ __forceinline__ int tiles_of(int keys) { return (keys + kTile - 1) / kTile; }
 __device__ __forceinline__ int units_of(int tiles) { return tiles > 0 ? tiles + kLead : 0; }
 
-// First unit of the c-th of C pieces of W units, and the first piece that does not begin before unit x.
-// (32-bit division where it holds: c <= 152.)
-__device__ __forceinline__ int64_t piece_start(int64_t c, int64_t W, int64_t C) {
-  return W < (1 << 24) ? (int64_t)((uint32_t)c * (uint32_t)W / (uint32_t)C) : c * W / C;
-}
-__device__ __forceinline__ int64_t piece_from(int64_t x, int64_t W, int64_t C) {
-  return W < (1 << 24) ? (int64_t)(((uint32_t)x * (uint32_t)C + (uint32_t)W - 1) / (uint32_t)W) : (x * C + W - 1) / W;
-}
-
 // A run of key tiles of one group.
 struct Seg {
   bool own;
@@ -152,57 +148,64 @@ struct Seg {
   int keys;         // keys that its last row sees
   int first_keys;   // keys that its first row sees (below 0: rows further on see none either)
   int j0, j1;       // key tiles
+  int rest;         // units of the group in the CTAs behind this one
   const int32_t* pages;
 };
 
-// Steps through a CTA's segments; every role has its own.
+// Steps through a CTA's segments, the last one first; every role has its own.  (A piece usually ends with
+// the beginning of a group and begins with the end of another: from the last one, the CTAs of the row
+// blocks of a long prefix read its keys from the front at about the same time, and find them in L2.
+// From the first one, each began elsewhere: 64 x 16 rows over 32768 keys read 1.9 GB from memory, not
+// 0.48 GB.)
 struct Walker {
   int64_t left;
-  int b, rb, h, j;   // group, unit within it
+  int b, rb, h, j;   // group, end of what is left of it in units (-1: all)
   Stream s;
-  int block;
+  int block, rows;   // rows of a block, rows in streams
 
   __device__ __forceinline__ void start(const Params& P, const Misc& m) {
     left = m.w1 - m.w0;
     b = m.b; rb = m.rb; h = m.h; j = (int)m.unit;
     block = 2 * P.tokens;
-    if (b >= 0 && left > 0) s = stream_of(P.a, b);
+    rows = m.rows;
+    s = m.s;
   }
   __device__ __forceinline__ bool next(const Params& P, Seg& g) {
     const qmm_attn_args& a = P.a;
-    while (left > 0) {
-      if (b < 0) {
-        const int rows = a.B > 0 ? clampi(a.row_starts[a.B], 0, a.T) : 0;
-        if (rb * (int64_t)block >= rows) { b = 0; rb = h = j = 0; s = stream_of(a, 0); continue; }
-        g.own = false;
-        g.t0 = rb * block;
-        g.rows = min(block, rows - g.t0);
+    while (left > 0 && b >= -1) {
+      if (rb < 0) {   // no group left of this stream
+        if (--b < -1) return false;
+        if (b >= 0) s = stream_of(a, b);
+        rb = ((b >= 0 ? s.m : rows) + block - 1) / block - 1;
+        h = a.Hk - 1;
+        j = -1;
+        continue;
+      }
+      g.own = b >= 0;
+      g.t0 = rb * block;
+      g.rows = min(block, (g.own ? s.m : rows) - g.t0);
+      if (g.own) {
+        g.keys = keys_of(s, rb, block);
+        g.first_keys = s.len - s.m + g.t0 + 1;
+        g.pages = a.pages + b * a.pages_per_stream;
+        g.t0 += s.t0;
+      } else {
         g.keys = g.first_keys = (int)a.prefix_len;
         g.pages = a.prefix_pages;
-      } else {
-        if (rb * (int64_t)block >= s.m) {
-          rb = h = j = 0;
-          if (++b >= a.B) return false;
-          s = stream_of(a, b);
-          continue;
-        }
-        g.own = true;
-        g.t0 = s.t0 + rb * block;
-        g.rows = min(block, s.m - rb * block);
-        g.keys = keys_of(s, rb, block);
-        g.first_keys = s.len - s.m + rb * block + 1;
-        g.pages = a.pages + b * a.pages_per_stream;
       }
-      const int tiles = tiles_of(g.keys), units = units_of(tiles);
-      if (j >= units) { j = 0; if (units == 0 || ++h == a.Hk) { h = 0; ++rb; } continue; }
       g.h = h;
-      g.j0 = max(0, j - kLead);
-      const int take = (int)min((int64_t)(units - j), left);
-      j += take;
+      const int units = units_of(tiles_of(g.keys)), end = j < 0 ? units : j;
+      const int take = (int)min((int64_t)end, left);
       left -= take;
-      g.j1 = j - kLead;
-      if (g.j1 <= g.j0) continue;   // the piece ends with the group's lead
-      return true;
+      g.j0 = max(0, end - take - kLead);
+      g.j1 = end - kLead;
+      g.rest = units - end;
+      j = -1;
+      if (--h < 0) {
+        h = a.Hk - 1;
+        --rb;
+      }
+      if (g.j1 > g.j0) return true;   // (else the piece holds only some of the group's lead)
     }
     return false;
   }
@@ -276,30 +279,14 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
   const int G = a.Hq / a.Hk, block = 2 * P.tokens;
 
   // ---- barriers, tensor memory, and this CTA's piece of the list of key tiles
-  if (threadIdx.x == 0) {
-    for (int k = 0; k < 3 * kS; ++k) {
-      mbar_init(bar(kBarFullK + k), 1);
-      mbar_init(bar(kBarFullV + k), 1);
-    }
-    for (int k = 0; k < kS; ++k) {
-      mbar_init(bar(kBarEmptyK + k), 2);
-      mbar_init(bar(kBarEmptyV + k), 2);
-    }
-    for (int k = 0; k < 2; ++k) {
-      mbar_init(bar(kBarQFull + k), 1);
-      mbar_init(bar(kBarQEmpty + k), 2);
-      mbar_init(bar(kBarEnd + k), 1);
-      mbar_init(bar(kBarDrain + k), 1);
-    }
-    for (int k = 0; k < 4; ++k) {
-      mbar_init(bar(kBarS + k), 1);
-      mbar_init(bar(kBarP + k), kLaneWarps);
-      mbar_init(bar(kBarO + k), 1);
-    }
-    mbar_init(bar(kBarJoin), 2 * kLaneWarps);
+  if (threadIdx.x < kBars) {
+    const int k = threadIdx.x;
+    const bool two = (k >= kBarEmptyK && k < kBarQFull) || (k >= kBarQEmpty && k < kBarS);
+    mbar_init(bar(k), two ? 2 : (k >= kBarFree && k < kBarO) ? kLaneWarps : k == kBarJoin ? 2 * kLaneWarps : 1);
+    fence_barrier_init();
+  } else if (threadIdx.x == kBars) {
     M.abort = 0;
     for (int k = 0; k < 8; ++k) M.odd[k] = 0;
-    fence_barrier_init();
   }
   if (warp == kMmaWarp) {
     tc::tmem_alloc(smem_addr(&M.tmem), kTmemCols);
@@ -315,21 +302,24 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
   {
     // the page tables towards L2 while the pieces are worked out: one 128-byte line a thread
     const int64_t line = ((int64_t)blockIdx.x * kThreads + threadIdx.x) * 32;
-    const int64_t n_pre = (a.prefix_len + a.page_size - 1) / a.page_size, n_own = a.B * a.pages_per_stream;
+    const int64_t n_pre = (a.prefix_len + a.page_size - 1) >> P.page_shift, n_own = a.B * a.pages_per_stream;
     if (line < n_pre) asm volatile("prefetch.global.L2 [%0];" :: "l"(a.prefix_pages + line));
     if (line < n_own) asm volatile("prefetch.global.L2 [%0];" :: "l"(a.pages + line));
     constexpr int kPer = (QMM_ATTN_MAX_STREAMS + kThreads - 1) / kThreads;
+    Stream str[kPer];
     int64_t mine[kPer], sum = 0;
     bool wrong = false;
+    const int rows = a.B > 0 ? clampi(a.row_starts[a.B], 0, a.T) : 0;
 #pragma unroll
     for (int q = 0; q < kPer; ++q) {
       const int b = threadIdx.x * kPer + q;
       mine[q] = 0;
       if (b < a.B) {
         bool bad;
-        const Stream s = stream_of(a, b, &bad);
+        str[q] = stream_of(a, b, &bad);
         wrong |= bad;
-        for (int rb = 0; rb * (int64_t)block < s.m; ++rb) mine[q] += (int64_t)a.Hk * units_of(tiles_of(keys_of(s, rb, block)));
+        for (int rb = 0; rb * block < str[q].m; ++rb)
+          mine[q] += (int64_t)a.Hk * units_of(tiles_of(keys_of(str[q], rb, block)));
       }
       sum += mine[q];
     }
@@ -349,40 +339,40 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
       own += M.scan[w];
     }
     const int punits = units_of(tiles_of((int)a.prefix_len));
-    const int rows = a.B > 0 ? clampi(a.row_starts[a.B], 0, a.T) : 0;
     const int64_t prefix = (int64_t)((rows + block - 1) / block) * a.Hk * punits;
-    const int64_t W = prefix + own, C = min((int64_t)gridDim.x, W);
-    const int64_t w0 = blockIdx.x < C ? piece_start(blockIdx.x, W, C) : 0;
-    const int64_t w1 = blockIdx.x < C ? piece_start(blockIdx.x + 1, W, C) : 0;
+    const int64_t W = prefix + own;
+    // equal pieces: no CTA has more than ceil(W / CTAs), whichever way the remainder falls
+    const int64_t per = W < (int64_t(1) << 31) ? (int64_t)(((uint32_t)W + gridDim.x - 1) / gridDim.x)
+                                               : (W + gridDim.x - 1) / gridDim.x;
+    const int64_t w0 = min(W, blockIdx.x * per), w1 = min(W, w0 + per);
+    const int64_t last = w1 - 1;   // its group is the first one the CTA works on
     if (threadIdx.x == 0) {
       M.w0 = w0;
       M.w1 = w1;
-      if (w0 < prefix) {
-        const int64_t g = w0 < (1 << 24) ? (int64_t)((uint32_t)w0 / (uint32_t)punits) : w0 / punits;
+      M.per = per;
+      M.rows = rows;
+      if (w0 < w1 && last < prefix) {
+        const int64_t g = prefix < (int64_t(1) << 31) ? (int64_t)((uint32_t)last / (uint32_t)punits) : last / punits;
         M.b = -1;
         M.rb = (int)((uint32_t)g / (uint32_t)a.Hk);
-        M.h = (int)((uint32_t)g % (uint32_t)a.Hk);
-        M.unit = w0 - g * punits;
+        M.h = (int)((uint32_t)g - (uint32_t)M.rb * (uint32_t)a.Hk);
+        M.unit = last - g * punits + 1;
       }
-      if (blockIdx.x == 0) { P.plan[0] = W; P.plan[1] = C; }
     }
     before += prefix;
 #pragma unroll
     for (int q = 0; q < kPer; ++q) {
       const int b = threadIdx.x * kPer + q;
-      if (b < a.B) {
-        if (blockIdx.x == 0) P.plan[2 + b] = before;
-        if (w0 >= before && w0 < before + mine[q]) {
-          const Stream s = stream_of(a, b);
-          int64_t at = w0 - before;
-          int rb = 0, n = units_of(tiles_of(keys_of(s, 0, block)));
-          while (at >= (int64_t)a.Hk * n) { at -= (int64_t)a.Hk * n; n = units_of(tiles_of(keys_of(s, ++rb, block))); }
-          M.b = b;
-          M.rb = rb;
-          M.h = 0;
-          while (at >= n) { at -= n; ++M.h; }
-          M.unit = at;
-        }
+      if (b < a.B && w0 < w1 && last >= before && last < before + mine[q]) {
+        int64_t at = last - before;
+        int rb = 0, h = 0, n = units_of(tiles_of(keys_of(str[q], 0, block)));
+        while (at >= (int64_t)a.Hk * n) { at -= (int64_t)a.Hk * n; n = units_of(tiles_of(keys_of(str[q], ++rb, block))); }
+        while (at >= n) { at -= n; ++h; }
+        M.s = str[q];
+        M.b = b;
+        M.rb = rb;
+        M.h = h;
+        M.unit = at + 1;
       }
       before += mine[q];
     }
@@ -497,8 +487,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
   } else if (warp == kMmaWarp || warp == kMmaWarp + 1) {
     // ------------------------------------------------------------------ tensor cores
     // A warp for each lane, one elected thread of it: the lanes' waits and issue overlap each other's
-    // products.  Item j of the lane uses S j % 2; the scores of item j + 1 are issued ahead of the
-    // values of item j.  The empty barriers of keys and values count two arrivals, and the only user of a
+    // products.  The scores of item j + 1 are issued ahead of the values of item j.  The empty barriers of keys and values count two arrivals, and the only user of a
     // tile makes both; those of query tiles count one of each lane.
     if (elect_one()) {
       constexpr bool kBf16 = TYPE == QMM_BF16;
@@ -508,8 +497,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
       const uint64_t dk = tc::smem_desc_sw128(smem_addr(smem + L::kK), 16, 1024);
       const uint64_t dv = tc::smem_desc_sw128(smem_addr(smem + L::kV), L::kHalf, 1024);
       const uint32_t l = warp - kMmaWarp;
-      const uint32_t tS = tmem + 2 * kTile * l, tO = tmem + 4 * kTile + kRows * l;
-      const int barS = kBarS + 2 * l, barP = kBarP + 2 * l, barO = kBarO + 2 * l;
+      const uint32_t tS = tmem + kTile * l, tP = tmem + 2 * kTile + kTile * l, tO = tmem + 4 * kTile + kRows * l;
+      const int barP = kBarP + 2 * l, barO = kBarO + 2 * l;
       struct Pass {
         Walker w;
         int left = 0;                  // the lane's items left of the segment
@@ -557,8 +546,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
         if (p.st >= kS) p.st -= kS;
       };
       bool more = true;   // scores are left to issue
-      auto scores = [&](auto b_, int reuse) {   // reuse: the phase of the product that read S's last p, or -1
-        constexpr int b = decltype(b_)::value;
+      auto scores = [&](int freed) {   // freed: the phase in which the softmax of the item before frees S, or -1
         if (qk.left == 0) more = more && begin(qk);
         if (!more || !ok) return;
         const uint32_t q = qk.q - (qk.pair ? 2 - l : 1), slot = q & 1;
@@ -567,14 +555,14 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
           if (qk.pair) ok = ok && wait(kBarQFull + (qk.q & 1), ((qk.q - 2) >> 1) & 1);
         }
         ok = ok && full(qk, kBarFullK);
-        if (reuse >= 0) ok = ok && wait(barO + b, reuse);   // the p of two items before sits where S goes
+        if (freed >= 0) ok = ok && wait(kBarFree + l, freed);
         if (!ok) return;
         tc::fence_after_sync();
 #pragma unroll
         for (int k = 0; k < D / 64; ++k)   // 64 values of the head: 4 MMAs, 32 bytes of each row further
-          tc::mma_f16_ss_x4(tS + kTile * b, dq + ((slot * L::kQBytes + k * L::kQHalf) >> 4),
+          tc::mma_f16_ss_x4(tS, dq + ((slot * L::kQBytes + k * L::kQHalf) >> 4),
                             dk + ((qk.st * L::kTileBytes + k * L::kHalf) >> 4), 2, kIdS, k > 0);
-        tc::commit(bar(barS + b));
+        tc::commit(bar(kBarS + l));
         if (qk.left == 1) {
           tc::commit(bar(kBarQEmpty + slot));
           if (qk.pair) tc::commit(bar(kBarQEmpty + (slot ^ 1)));
@@ -587,7 +575,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
         ok = full(pv, kBarFullV) && wait(barP + b, parity);
         if (!ok) return false;
         tc::fence_after_sync();
-        tc::mma_f16_ts_x4(tO, tS + kTile * b, dv + ((pv.st * L::kTileBytes) >> 4), 128, kIdO,
+        tc::mma_f16_ts_x4(tO, tP + kTile / 2 * b, dv + ((pv.st * L::kTileBytes) >> 4), 128, kIdO,
                           !pv.fresh);   // 16 rows of V an MMA; the segment's first item begins O
         tc::commit(bar(barO + b));
         if (pv.left == 1) tc::commit(bar(kBarEnd + l));
@@ -596,11 +584,11 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
       };
       using S0 = std::integral_constant<int, 0>;
       using S1 = std::integral_constant<int, 1>;
-      scores(S0{}, -1);
+      scores(-1);
       for (uint32_t r = 0; ok; ++r) {   // two items
-        scores(S1{}, r > 0 ? (r - 1) & 1 : -1);
+        scores(0);
         if (!ok || !values(S0{}, r & 1)) break;
-        scores(S0{}, r & 1);
+        scores(1);
         if (!ok || !values(S1{}, r & 1)) break;
       }
       // no tensor-core operation of this CTA is in flight when it ends
@@ -613,7 +601,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
     const int l = warp / kLaneWarps;                 // this warp's lane of flash attention
     const int row = (warp % kLaneWarps) * 32 + lane;
     const uint32_t lanes = (uint32_t)(warp % kLaneWarps) << 21;   // first TMEM lane << 16
-    const uint32_t tS = tmem + lanes + 2 * kTile * l, tO = tmem + lanes + 4 * kTile;
+    const uint32_t tS = tmem + lanes + kTile * l, tP = tmem + lanes + 2 * kTile + kTile * l;
+    const uint32_t tO = tmem + lanes + 4 * kTile;
     const float c = a.scale * kLog2e;
     float2* stats = reinterpret_cast<float2*>(smem + L::kStats);
     uint32_t parity = 0;   // of the next phases of the value stages' full barriers (single, both)
@@ -623,6 +612,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
       const int n = g.j1 - g.j0;
       const bool pair = g.rows > P.tokens;
       const int first = pair ? 0 : (items + l) & 1;               // the lane's first key tile of the segment
+      const bool has[2] = {pair || n > (int)(items & 1), pair || n > (int)((items + 1) & 1)};   // lanes with key tiles
       const int tok0 = pair ? l * P.tokens : 0;                   // the lane's rows of the block
       const int live = min(P.tokens, g.rows - tok0) * G;          // rows of the tile in use
       const int tok = tok0 + row / G;
@@ -635,10 +625,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
       uint32_t st = (pos + first) % kS;   // stage of the item's values
       for (int i = first; i < n; i += pair ? 1 : 2) {
         const int base = (g.j0 + i) * kTile;
-        const int buf = seen & 1;   // which S of the lane
+        const int buf = seen & 1;   // which p of the lane
         const uint32_t at = pair ? kS + st : st;
         parity ^= 1u << at;
-        ok = wait_w(kBarS + 2 * l + buf, (seen >> 1) & 1);
+        ok = wait_w(kBarS + l, buf);   // (and with S the products of two items before, the last readers of this p)
         // value rows that a weight of 0 must not meet
         const int upto = min(g.keys, base + kTile) - base;
         if (ok && clean_from < base + kTile && (upto < kTile || g.own)) {
@@ -670,7 +660,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
         tc::fence_after_sync();
         if (!idle) {
           uint32_t s[kTile];
-          tc::ld_wait_x64(tS + kTile * buf, s);
+          tc::ld_wait_x64(tS, s);
+          tc::fence_before_sync();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(kBarFree + l));
           const int vis = sees - base;
           if (__any_sync(0xffffffffu, vis < kTile)) {
 #pragma unroll
@@ -686,7 +679,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
           const float now = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c;
           const bool grew = now > top + kGrow || (top == -INFINITY && now > -INFINITY);
           if (i > first && __any_sync(0xffffffffu, grew)) {
-            // the item before is in O (S, formed after the one before that was, says so much of that one)
+            // the item before is in O (the one before that is, with S)
             ok = wait_w(kBarO + 2 * l + (buf ^ 1), ((seen - 1) >> 1) & 1);
             if (!ok) break;
             tc::fence_after_sync();
@@ -715,10 +708,12 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
             s[k / 2] = pack2<TYPE>(p0, p1);
             s[k / 2 + 1] = pack2<TYPE>(p2, p3);
           }
-          tc::st_x32(tS + kTile * buf, s);
+          tc::st_x32(tP + kTile / 2 * buf, s);
           const float2 u = f2unpack(part0), v = f2unpack(part1);
           sum += (u.x + u.y) + (v.x + v.y);
           tc::wait_st();
+        } else if (lane == 0) {
+          mbar_arrive(bar(kBarFree + l));
         }
         tc::fence_before_sync();
         __syncwarp();
@@ -734,7 +729,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
       const bool some = first < n;   // the lane had key tiles
       if (some) ok = wait_w(kBarEnd + l, ends++ & 1);
       if (!pair) {   // the other lane's state of the same rows
-        stats[l * kRows + row] = make_float2(top, some ? sum : -1.0f);
+        stats[l * kRows + row] = make_float2(top, sum);
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(kBarJoin));
         ok = ok && wait_w(kBarJoin, joins++ & 1);
@@ -749,13 +744,14 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
       };
       float* out = inside ? P.o_cta : P.o_rows;
       if (row < live && (pair || l == 0)) {
-        RowStat st{top, sum, odd, 0u};
+        const uint32_t per = (uint32_t)min(M.per, (int64_t)0x7fffffff);
+        const uint32_t others = g.rest > 0 ? ((uint32_t)g.rest + per - 1) / per : 0;
+        RowStat st{top, sum, odd, others << 16 | (blockIdx.x + 1)};
         if (!pair) {
           const float2 s0 = stats[row], s1 = stats[kRows + row];
-          const bool b0 = !(s0.y < 0.0f), b1 = !(s1.y < 0.0f);
-          st.top = fmaxf(b0 ? s0.x : -INFINITY, b1 ? s1.x : -INFINITY);
-          st.sum = (b0 && !(s0.x == -INFINITY && s0.y == 0.0f) ? s0.y * exp2_fast(s0.x - st.top) : 0.0f) +
-                   (b1 && !(s1.x == -INFINITY && s1.y == 0.0f) ? s1.y * exp2_fast(s1.x - st.top) : 0.0f);
+          st.top = fmaxf(s0.x, s1.x);
+          st.sum = (!(s0.x == -INFINITY && s0.y == 0.0f) ? s0.y * exp2_fast(s0.x - st.top) : 0.0f) +
+                   (!(s1.x == -INFINITY && s1.y == 0.0f) ? s1.y * exp2_fast(s1.x - st.top) : 0.0f);
         }
         (inside ? P.s_cta : P.s_rows)[record(row)] = st;
       }
@@ -766,7 +762,6 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
 #pragma unroll 1
         for (int hh = 0; hh < 2 && (warp % kLaneWarps) * 32 + 16 * hh < live; ++hh) {
           float f[2][2] = {{1.0f, 1.0f}, {1.0f, 1.0f}};   // [row][lane]
-          bool has[2] = {true, true};
           float* dst[2];
           bool mine[2];
 #pragma unroll
@@ -776,9 +771,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
             dst[k] = out + record(r) * D + 8 * (lane & 3);
             if (!pair) {
               const float2 s0 = stats[r], s1 = stats[kRows + r];
-              has[0] = !(s0.y < 0.0f);
-              has[1] = !(s1.y < 0.0f);
-              const float best = fmaxf(has[0] ? s0.x : -INFINITY, has[1] ? s1.x : -INFINITY);
+              const float best = fmaxf(s0.x, s1.x);
               f[k][0] = s0.x == -INFINITY && s0.y == 0.0f ? 0.0f : exp2_fast(s0.x - best);
               f[k][1] = s1.x == -INFINITY && s1.y == 0.0f ? 0.0f : exp2_fast(s1.x - best);
             }
@@ -843,110 +836,112 @@ __device__ __forceinline__ int column_of(int p) {
   return (p & ~31) + 8 * ((p & 7) >> 1) + 2 * ((p & 31) >> 3) + (p & 1);
 }
 
-template <int D, int TYPE>
+template <int D, int TYPE, int AHEAD>
 __global__ void __launch_bounds__(32 * kCombineWarps) attn_combine_kernel(const __grid_constant__ Params P) {
   constexpr int kV = D / 32;   // values of a lane: positions kV * lane and on
   const qmm_attn_args& a = P.a;
   __shared__ int stream;
-  __shared__ unsigned long long units_before;   // units of the stream's row blocks before the row's
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int t = blockIdx.x, lane = threadIdx.x & 31;
   const int head = blockIdx.y * kCombineWarps + (threadIdx.x >> 5);
-  if (threadIdx.x == 0) { stream = -1; units_before = 0; }
+  if (threadIdx.x == 0) stream = -1;
   __syncthreads();
   for (int b = threadIdx.x; b < a.B; b += blockDim.x) {
     const Stream s = stream_of(a, b);
     if (t >= s.t0 && t < s.t0 + s.m) stream = b;   // one stream, if the starts do not decrease
   }
   __syncthreads();
-  const int b = stream, G = a.Hq / a.Hk, block = 2 * P.tokens, h = head / G;
+  if (head >= a.Hq) return;
+  const int b = stream, G = a.Hq / a.Hk, block = 2 * P.tokens;
   Stream s{};
+  bool has[2] = {b >= 0 && a.prefix_len > 0 && t < a.row_starts[a.B], false};   // key tiles of the prefix, of own keys
   if (b >= 0) {
     s = stream_of(a, b);
-    const int rb = (t - s.t0) / block;
-    if (rb > 0) {
-      unsigned long long mine = 0;
-      for (int k = threadIdx.x; k < rb; k += blockDim.x) mine += (unsigned long long)a.Hk * units_of(tiles_of(keys_of(s, k, block)));
-      atomicAdd(&units_before, mine);
-      __syncthreads();
-    }
+    has[1] = keys_of(s, (t - s.t0) / block, block) > 0;
   }
+  const int64_t rec = (int64_t)t * a.Hq + head;
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  if (head >= a.Hq) return;
-  float o[kV] = {}, top = -INFINITY, sum = 0.0f;
-  uint32_t odd = 0;
-  if (b >= 0) {
-    const int64_t W = P.plan[0], C = P.plan[1];
-    const int64_t first = P.plan[2 + b] + (int64_t)units_before;
-    // the records of the row: of the prefix's group, then of the own keys' group
-    int64_t cta[2];
-    int n[2], row[2];
-#pragma unroll
-    for (int own = 0; own < 2; ++own) {
-      const int tok = own ? t - s.t0 : t, rb = tok / block, in = tok % block;
-      int tiles = tiles_of((int)a.prefix_len);
-      int64_t at = ((int64_t)rb * a.Hk + h) * units_of(tiles) + kLead;   // unit of the group's first tile
-      if (own) {
-        tiles = tiles_of(keys_of(s, rb, block));
-        at = first + (int64_t)h * units_of(tiles) + kLead;
-      }
-      row[own] = (in < P.tokens ? in * G : kRows + (in - P.tokens) * G) + head % G;
-      n[own] = 0;
-      cta[own] = 0;
-      if (tiles > 0) {
-        cta[own] = piece_from(at + 1, W, C);
-        n[own] = 1 + (int)max((int64_t)0, min(C, piece_from(at + tiles, W, C)) - cta[own]);
-      }
+
+  auto load = [&](const float* p, float (&x)[kV]) {
+    if constexpr (kV == 4) {
+      const float4 v = *reinterpret_cast<const float4*>(p + 4 * lane);
+      x[0] = v.x; x[1] = v.y; x[2] = v.z; x[3] = v.w;
+    } else {
+      const float2 v = *reinterpret_cast<const float2*>(p + 2 * lane);
+      x[0] = v.x; x[1] = v.y;
     }
-    const int all = n[0] + n[1];
+  };
+  // a row that saw none of a segment's keys has no part in it
+  auto saw = [](const RowStat& r) { return !(r.top == -INFINITY && r.sum == 0.0f); };
+  RowStat st[2] = {{-INFINITY, 0.0f, 0u, 0u}, {-INFINITY, 0.0f, 0u, 0u}};
+  float x[2][kV] = {};
+#pragma unroll
+  for (int k = 0; k < 2; ++k)
+    if (has[k]) {
+      const int64_t at = k ? (int64_t)a.T * a.Hq + rec : rec;
+      st[k] = P.s_rows[at];
+      load(P.o_rows + at * D, x[k]);
+    }
+  float top = fmaxf(st[0].top, st[1].top), sum = 0.0f, o[kV] = {};
+  uint32_t odd = st[0].odd | st[1].odd;
+#pragma unroll
+  for (int k = 0; k < 2; ++k)
+    if (saw(st[k])) {
+      const float w = exp2_fast(st[k].top - top);
+      sum = __fmaf_rn(st[k].sum, w, sum);
+#pragma unroll
+      for (int q = 0; q < kV; ++q) o[q] = __fmaf_rn(x[k][q], w, o[q]);
+    }
+  // the other segments of the two groups, one a lane
+  const int n0 = st[0].rest >> 16, all = n0 + (int)(st[1].rest >> 16);
+  if (all > 0) {
+    int row[2];   // of the tiles of each group's block
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const int in = (k ? t - s.t0 : t) % block;
+      row[k] = (in < P.tokens ? in * G : kRows + (in - P.tokens) * G) + head % G;
+    }
     for (int r0 = 0; r0 < all; r0 += 32) {
-      // one record a lane: its weight
-      const int r = r0 + lane, own = r >= n[0], k = own ? r - n[0] : r;
-      const bool live = r < all;
-      const int64_t at = k == 0 ? ((int64_t)(own ? a.T : 0) + t) * a.Hq + head
-                                : ((own ? cta[1] : cta[0]) + k - 1) * 2 * kRows + (own ? row[1] : row[0]);
-      RowStat st{-INFINITY, 0.0f, 0u, 0u};
-      if (live) st = (k == 0 ? P.s_rows : P.s_cta)[at];
-      const float* src = (k == 0 ? P.o_rows : P.o_cta) + at * D;
-      float best = st.top;
+      const int r = r0 + lane;
+      const bool own = r >= n0, live = r < all;
+      const int cta = min((int)((own ? st[1].rest : st[0].rest) & 0xFFFFu) + (own ? r - n0 : r), kMaxCtas - 1);
+      const int at = cta * 2 * kRows + (own ? row[1] : row[0]);
+      RowStat q{-INFINITY, 0.0f, 0u, 0u};
+      if (live) q = P.s_cta[at];
+      // their O, AHEAD at a time, asked for before the statistics are there
+      float best = top, keep = 1.0f, w = 0.0f;
+#pragma unroll 1
+      for (int j0 = 0; j0 < 32 && r0 + j0 < all; j0 += AHEAD) {
+        float y[AHEAD][kV];
 #pragma unroll
-      for (int off = 16; off >= 1; off >>= 1) best = fmaxf(best, __shfl_xor_sync(0xffffffffu, best, off));
-      best = fmaxf(best, top);
-      const bool saw = !(st.top == -INFINITY && st.sum == 0.0f);   // the row saw some of the segment's keys
-      const float w = saw ? exp2_fast(st.top - best) : 0.0f;
-      float part = saw ? st.sum * w : 0.0f;
+        for (int j = 0; j < AHEAD; ++j) {
+          const int from = __shfl_sync(0xffffffffu, at, j0 + j);
 #pragma unroll
-      for (int off = 16; off >= 1; off >>= 1) part += __shfl_xor_sync(0xffffffffu, part, off);
-      const float keep = r0 > 0 && !(top == -INFINITY && sum == 0.0f) ? exp2_fast(top - best) : 0.0f;
-      sum = __fmaf_rn(sum, keep, part);
-      top = best;
-      odd |= __any_sync(0xffffffffu, st.odd != 0);
+          for (int k = 0; k < kV; ++k) y[j][k] = 0.0f;
+          if (j0 + j < 32 && r0 + j0 + j < all) load(P.o_cta + (int64_t)from * D, y[j]);
+        }
+        if (j0 == 0) {
+          best = q.top;
 #pragma unroll
-      for (int q = 0; q < kV; ++q) o[q] *= keep;
-      const unsigned who = __ballot_sync(0xffffffffu, live && saw);
-      constexpr int kAhead = 8;
-      for (int j0 = 0; j0 < 32 && (who >> j0) != 0; j0 += kAhead) {
-        float x[kAhead][kV];
+          for (int off = 16; off >= 1; off >>= 1) best = fmaxf(best, __shfl_xor_sync(0xffffffffu, best, off));
+          best = fmaxf(best, top);
+          w = saw(q) ? exp2_fast(q.top - best) : 0.0f;
+          float part = saw(q) ? q.sum * w : 0.0f;
 #pragma unroll
-        for (int j = 0; j < kAhead; ++j) {
-          const float* p = reinterpret_cast<const float*>(__shfl_sync(0xffffffffu, (unsigned long long)src, j0 + j));
+          for (int off = 16; off >= 1; off >>= 1) part += __shfl_xor_sync(0xffffffffu, part, off);
+          keep = top == -INFINITY && sum == 0.0f ? 0.0f : exp2_fast(top - best);
+          sum = __fmaf_rn(sum, keep, part);
+          top = best;
+          odd |= __any_sync(0xffffffffu, q.odd != 0);
 #pragma unroll
-          for (int q = 0; q < kV; ++q) x[j][q] = 0.0f;
-          if (who >> (j0 + j) & 1) {
-            if constexpr (kV == 4) {
-              const float4 v = *reinterpret_cast<const float4*>(p + 4 * lane);
-              x[j][0] = v.x; x[j][1] = v.y; x[j][2] = v.z; x[j][3] = v.w;
-            } else {
-              const float2 v = *reinterpret_cast<const float2*>(p + 2 * lane);
-              x[j][0] = v.x; x[j][1] = v.y;
-            }
-          }
+          for (int k = 0; k < kV; ++k) o[k] *= keep;
         }
 #pragma unroll
-        for (int j = 0; j < kAhead; ++j) {
+        for (int j = 0; j < AHEAD; ++j) {
           const float f = __shfl_sync(0xffffffffu, w, j0 + j);
+          if (j0 + j < 32 && f != 0.0f)   // (of a segment none of whose keys the row saw, O means nothing)
 #pragma unroll
-          for (int q = 0; q < kV; ++q) o[q] = __fmaf_rn(x[j][q], f, o[q]);
+            for (int k = 0; k < kV; ++k) o[k] = __fmaf_rn(y[j][k], f, o[k]);
         }
       }
     }
@@ -961,7 +956,7 @@ __global__ void __launch_bounds__(32 * kCombineWarps) attn_combine_kernel(const 
     for (int j = max(0, s.len - s.m); j < sees; ++j) {
       const int page = a.pages[b * a.pages_per_stream + j / a.page_size];
       if (page < 0 || page >= a.n_slots / a.page_size) continue;
-      const int64_t at = (((int64_t)page * a.page_size + j % a.page_size) * a.Hk + h) * D;
+      const int64_t at = (((int64_t)page * a.page_size + j % a.page_size) * a.Hk + head / G) * D;
 #pragma unroll
       for (int k = 0; k < kV; ++k) {
         const uint16_t raw = static_cast<const uint16_t*>(a.V_cache)[at + column_of(kV * lane + k)];
@@ -984,15 +979,14 @@ __global__ void __launch_bounds__(32 * kCombineWarps) attn_combine_kernel(const 
 size_t up(size_t n) { return (n + 255) & ~(size_t)255; }
 
 struct Space {
-  size_t o_rows, s_rows, o_cta, s_cta, plan, total;
+  size_t o_rows, s_rows, o_cta, s_cta, total;
   explicit Space(const qmm_attn_args& a) {
     const size_t rows = 2 * (size_t)a.T * a.Hq, cta = (size_t)kMaxCtas * 2 * kRows;
     o_rows = 0;
     o_cta = o_rows + up(rows * a.D * sizeof(float));
     s_rows = o_cta + up(cta * a.D * sizeof(float));
     s_cta = s_rows + up(rows * sizeof(RowStat));
-    plan = s_cta + up(cta * sizeof(RowStat));
-    total = plan + up((2 + (size_t)a.B) * sizeof(int64_t)) + 256;   // the base may be 16-byte aligned only
+    total = s_cta + up(cta * sizeof(RowStat)) + 256;   // the base may be 16-byte aligned only
   }
 };
 
@@ -1035,7 +1029,6 @@ cudaError_t launch(const qmm_attn_args& a, void* workspace, cudaStream_t stream)
   P.o_cta = reinterpret_cast<float*>(ws + sp.o_cta);
   P.s_rows = reinterpret_cast<RowStat*>(ws + sp.s_rows);
   P.s_cta = reinterpret_cast<RowStat*>(ws + sp.s_cta);
-  P.plan = reinterpret_cast<int64_t*>(ws + sp.plan);
   get_wait_limit(&P.wait_polls, &P.wait_ns);
   const int per_box = a.page_size < kTile ? a.page_size : kTile;
   if (!tensor_map(&P.mapQ, a.Q, D, a.Hq, a.T, a.ldq, G, P.tokens, TYPE) ||
@@ -1063,7 +1056,10 @@ cudaError_t launch(const qmm_attn_args& a, void* workspace, cudaStream_t stream)
   cfg.gridDim = dim3(a.T, (a.Hq + kCombineWarps - 1) / kCombineWarps);
   cfg.blockDim = dim3(32 * kCombineWarps);
   cfg.dynamicSmemBytes = 0;
-  return cudaLaunchKernelEx(&cfg, attn_combine_kernel<D, TYPE>, P);
+  // A row's other records are read 24 at a time where the grid is one CTA an SM at most (179 registers;
+  // 160 CTAs of 19 records each: 2.6 us, 4.2 us with 8), 8 at a time where more CTAs share an SM.
+  if ((int64_t)cfg.gridDim.x * cfg.gridDim.y <= 2 * sms) return cudaLaunchKernelEx(&cfg, attn_combine_kernel<D, TYPE, 24>, P);
+  return cudaLaunchKernelEx(&cfg, attn_combine_kernel<D, TYPE, 8>, P);
 }
 
 }  // namespace

@@ -438,8 +438,8 @@ qmm_status qmm_norm_rope(const qmm_norm_rope_args* args_host, cudaStream_t strea
  * Scores, softmax statistics and sums are fp32; the weights of the values are rounded to `type` for
  * the tensor cores, and O is rounded once.  The result does not depend on the other calls of the
  * stream, and the same arguments give the same bits.
- *   workspace_dev: at least qmm_attn_workspace_bytes(args) bytes (it depends on T, B, Hq, Hk and D
- *   only), 16-byte aligned; calls that may overlap need one each.  It needs no initialisation.
+ *   workspace_dev: at least qmm_attn_workspace_bytes(args) bytes (it depends on T, Hq and D only),
+ *   16-byte aligned; calls that may overlap need one each.  It needs no initialisation.
  * Errors: QMM_ERR_NULL, QMM_ERR_SHAPE, QMM_ERR_TYPE, QMM_ERR_ALIGN, QMM_ERR_BUFSIZE, QMM_ERR_CUDA. */
 #define QMM_ATTN_MAX_STREAMS 1024
 #define QMM_ATTN_MAX_ROWS 65536
