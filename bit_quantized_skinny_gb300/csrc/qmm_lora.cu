@@ -1,12 +1,14 @@
 // qmm_lora.cu — low-rank adapters beside shared projections (qmm_run_lora):
 //     Y[i] = Y0[i] + scale_a * B_a (A_a x_i),  a = ids[i].
 //
-// Two launches.  lora_shrink_kernel forms t_i = A_a x_i: one warp per (adapter in use, 4 ranks, a
-// piece of K), partial sums of the pieces kept apart.  lora_expand_kernel sums the pieces and adds
-// scale * t_i Bt_a to Y0: one CTA per (adapter in use, 256 columns), its warps sharing the ranks.
-// An adapter is read once for all the rows that use it: the rows of one adapter are found by a warp
-// match over the (at most 32) ids.
+// Two launches.  lora_shrink_kernel forms t_i = A_a x_i: one warp per (adapter in use, 4 ranks, 512
+// values of K), the partial sums of the pieces of K kept apart.  lora_expand_kernel sums the pieces
+// and adds scale * t_i Bt_a to Y0, 256 columns a warp.  Both are bound by the adapters' bytes: an
+// adapter is read once for all the rows that use it (found by a warp match over the at most 32 ids),
+// A stays in registers over the rows and B over up to 4 rows.  The expand launch starts while the
+// shrink launch runs and has its first B values in flight before it waits for t.
 #include <cstdint>
+#include <type_traits>
 #include <cuda_runtime.h>
 
 #include "q4k_device.cuh"
@@ -17,11 +19,21 @@ namespace {
 
 __device__ unsigned g_status;   // this file's kernels' status word
 
-constexpr int kWarps = 8;
+constexpr int kShrinkWarps = 4;
 constexpr int kRanks = 4;        // ranks of one shrink warp
-constexpr int kPiece = 1024;     // values of K of one shrink warp (a multiple of 256)
-constexpr int kCols = 256;       // columns of one expand CTA, 8 a lane
-constexpr int kRows = 4;         // rows of one adapter worked on together
+constexpr int kChunk = 512;      // values of K that a shrink warp holds at a time
+constexpr int kPieces = 64;      // pieces of K at most
+constexpr int64_t kAhead = 16 << 20;   // bytes of B that the shrink launch asks into L2
+constexpr int kCols = 256;       // columns of one expand warp, 8 a lane
+constexpr int kStep = 4;         // ranks that an expand warp loads together
+// The two forms of the expand kernel.  kSplit: 8 warps share the ranks of one block of columns and join
+// their sums in shared memory; up to 4 rows are worked on together.  kStream: a block of columns for
+// each of 2 warps, up to 2 rows together, few enough registers that every warp of 32 adapters
+// beside 34816 columns is resident at once (28.6 an SM; in CTAs of 8 warps the last ones waited for a
+// second round: 45 us, not 37).
+enum Form { kSplit, kStream };
+__host__ __device__ constexpr int warps_of(Form f) { return f == kSplit ? 8 : 2; }
+__host__ __device__ constexpr int rows_of(Form f) { return f == kSplit ? 4 : 2; }
 
 struct Entry {
   const qmm_lora_adapter* adapters;
@@ -31,18 +43,20 @@ struct Entry {
   float* t;          // pieces x M x rank_max
   int64_t N, K;
   int n_adapters;
-  int pieces;
+  int pieces, chunks;   // of K, and of a piece
   int first;         // first block of this entry in the expand grid's x
 };
 struct Params {
   Entry e[QMM_LORA_MAX_ENTRIES];
   const int32_t* ids;
   int count, M, rank_max;
+  int rank_groups;   // of kRanks in rank_max
 };
 
 // The rows of the g-th distinct adapter of the M ids (in order of first row) as a mask of rows; 0
-// past the last.  All lanes of a warp call this; `id` comes back as that adapter's id.
-__device__ __forceinline__ unsigned group_rows(const int32_t* ids, int M, int n_adapters, int g, int& id) {
+// past the last.  All lanes of a warp call this; `id` comes back as that adapter's id, `groups` as the
+// number of distinct ones.
+__device__ __forceinline__ unsigned group_rows(const int32_t* ids, int M, int n_adapters, int g, int& id, int& groups) {
   const int lane = threadIdx.x & 31;
   int mine = lane < M ? ids[lane] : -2;
   if (mine >= n_adapters || mine < -2 || (mine == -2 && lane < M)) {
@@ -52,7 +66,8 @@ __device__ __forceinline__ unsigned group_rows(const int32_t* ids, int M, int n_
   const unsigned same = __match_any_sync(0xffffffffu, mine);
   const bool leader = lane < M && (same & ((1u << lane) - 1)) == 0;
   unsigned leaders = __ballot_sync(0xffffffffu, leader);
-  if (g >= __popc(leaders)) return 0;
+  groups = __popc(leaders);
+  if (g >= groups) return 0;
   for (int k = 0; k < g; ++k) leaders &= leaders - 1;
   const int at = __ffs(leaders) - 1;
   id = __shfl_sync(0xffffffffu, mine, at);
@@ -81,126 +96,262 @@ __device__ __forceinline__ void unpack8(uint4 v, float (&x)[8]) {
   }
 }
 
-// Grid (rank groups of kWarps * kRanks x pieces, adapters in use, entries).
-__global__ void __launch_bounds__(32 * kWarps) lora_shrink_kernel(const __grid_constant__ Params P) {
+// Grid (rank groups x pieces in units of kShrinkWarps, adapters in use, entries).
+__global__ void __launch_bounds__(32 * kShrinkWarps, 4) lora_shrink_kernel(const __grid_constant__ Params P) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const Entry& e = P.e[blockIdx.z];
-  const int piece = blockIdx.x % e.pieces;
-  const int r0 = (blockIdx.x / e.pieces * kWarps + (threadIdx.x >> 5)) * kRanks;
   const int lane = threadIdx.x & 31;
-  if (piece * (int64_t)kPiece >= e.K) return;
-  int id = -1;
-  unsigned rows = group_rows(P.ids, P.M, e.n_adapters, blockIdx.y, id);
-  if (!rows || id < 0) return;
+  const int unit = blockIdx.x * kShrinkWarps + (threadIdx.x >> 5);
+  const int piece = unit / P.rank_groups, r0 = (unit - piece * P.rank_groups) * kRanks;
+  if (piece >= e.pieces) return;
+  int id = -1, groups;
+  const unsigned all = group_rows(P.ids, P.M, e.n_adapters, blockIdx.y, id, groups);
+  if (!all || id < 0) return;
   const qmm_lora_adapter a = adapter_of(e, id, P.rank_max);
   if (r0 >= a.rank) return;
-  const int64_t k0 = piece * (int64_t)kPiece;
-  const int64_t k1 = k0 + kPiece < e.K ? k0 + kPiece : e.K;
-  while (rows) {
-    int row[kRows], n = 0;
+  constexpr int kV = kChunk / 256;   // 16-byte loads of a lane in a chunk
+  for (int chunk = 0; chunk < e.chunks; ++chunk) {
+    const int64_t k0 = ((int64_t)piece * e.chunks + chunk) * kChunk + 8 * lane;
+    if (k0 - 8 * lane >= e.K) break;
+    uint4 raw[kRanks][kV];
 #pragma unroll
-    for (int j = 0; j < kRows; ++j) {
-      row[j] = rows ? __ffs(rows) - 1 : row[0];
-      if (rows) { rows &= rows - 1; ++n; }
-    }
-    float acc[kRows * kRanks] = {};
-    for (int64_t k = k0 + 8 * lane; k < k1; k += 256) {
-      float w[kRanks][8];
+    for (int r = 0; r < kRanks; ++r)
 #pragma unroll
-      for (int r = 0; r < kRanks; ++r) {
-        const int rr = r0 + r < a.rank ? r0 + r : r0;
-        unpack8(*reinterpret_cast<const uint4*>(a.A + rr * e.K + k), w[r]);
+      for (int v = 0; v < kV; ++v) {
+        const bool in = r0 + r < a.rank && k0 + 256 * v < e.K;
+        raw[r][v] = in ? ldg_nc_v4(a.A + (r0 + r) * e.K + k0 + 256 * v) : make_uint4(0u, 0u, 0u, 0u);
       }
+    if (chunk == 0) {
+      // The expand launch's first B towards L2, this warp's share of the adapter's (its units are the live
+      // rank groups by the pieces), so that memory is not idle while t is formed.
+      const int64_t bytes = min((int64_t)a.rank * e.N * 2, kAhead / groups / P.count) & ~(int64_t)127;
+      const int64_t lines = bytes / 128, units = (int64_t)((a.rank + kRanks - 1) / kRanks) * e.pieces;
+      const int64_t mine = ((int64_t)piece * ((a.rank + kRanks - 1) / kRanks) + r0 / kRanks) * 32 + lane;
+      for (int64_t k = mine; k < lines; k += 32 * units)
+        asm volatile("prefetch.global.L2 [%0];" :: "l"(reinterpret_cast<const uint8_t*>(a.Bt) + 128 * k));
+    }
+    // a row's x is asked for while the row before is worked on
+    uint4 x[kV];
+    auto ask = [&](int row) {
 #pragma unroll
-      for (int j = 0; j < kRows; ++j) {
-        if (j >= n) break;
-        float x[8];
-        unpack8(*reinterpret_cast<const uint4*>(e.X + row[j] * e.K + k), x);
+      for (int v = 0; v < kV; ++v)
+        x[v] = k0 + 256 * v < e.K ? *reinterpret_cast<const uint4*>(e.X + row * e.K + k0 + 256 * v) : make_uint4(0u, 0u, 0u, 0u);
+    };
+    ask(__ffs(all) - 1);
+    for (unsigned rows = all; rows;) {
+      const int row = __ffs(rows) - 1;
+      rows &= rows - 1;
+      uint4 now[kV];
 #pragma unroll
-        for (int r = 0; r < kRanks; ++r)
+      for (int v = 0; v < kV; ++v) now[v] = x[v];
+      if (rows) ask(__ffs(rows) - 1);
+      float acc[kRanks] = {};
 #pragma unroll
-          for (int c = 0; c < 8; ++c) acc[j * kRanks + r] = __fmaf_rn(w[r][c], x[c], acc[j * kRanks + r]);
+      for (int v = 0; v < kV; ++v) {
+        float xs[8];
+        unpack8(now[v], xs);
+#pragma unroll
+        for (int r = 0; r < kRanks; ++r) {
+          float w[8];
+          unpack8(raw[r][v], w);
+#pragma unroll
+          for (int c = 0; c < 8; ++c) acc[r] = __fmaf_rn(w[c], xs[c], acc[r]);
+        }
+      }
+      butterfly_reduce<kRanks>(acc, lane);   // lane l: rank l / 4
+      const int r = r0 + lane / (32 / kRanks);
+      if (lane % (32 / kRanks) == 0 && r < a.rank) {
+        float* t = e.t + ((int64_t)piece * P.M + row) * P.rank_max + r;
+        *t = chunk == 0 ? acc[0] : *t + acc[0];
       }
     }
-    butterfly_reduce<kRows * kRanks>(acc, lane);   // lane l: value l / (32 / values)
-    constexpr int kPer = 32 / (kRows * kRanks);
-    const int v = lane / kPer, j = v / kRanks, r = v % kRanks;
-    int mine = row[0];
-#pragma unroll
-    for (int q = 0; q < kRows; ++q) mine = j == q ? row[q] : mine;
-    if (lane % kPer == 0 && j < n && r0 + r < a.rank)
-      e.t[((int64_t)piece * P.M + mine) * P.rank_max + r0 + r] = acc[0];
   }
 }
 
-// Grid (blocks of kCols columns over all entries, adapters in use).
-__global__ void __launch_bounds__(32 * kWarps) lora_expand_kernel(const __grid_constant__ Params P) {
-  __shared__ float ts[kRows][QMM_LORA_MAX_RANK];
-  __shared__ float part[kWarps][kRows][kCols];
-  int k = 0;
-  while (k + 1 < P.count && (int)blockIdx.x >= P.e[k + 1].first) ++k;
-  const Entry& e = P.e[k];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  int id = -1;
-  unsigned rows = group_rows(P.ids, P.M, e.n_adapters, blockIdx.y, id);
-  if (!rows) return;
-  const qmm_lora_adapter a = adapter_of(e, id, P.rank_max);
-  const int64_t n0 = (int64_t)(blockIdx.x - e.first) * kCols;
-  const int64_t n = n0 + 8 * lane;
-  const bool wide = (reinterpret_cast<uintptr_t>(a.Bt) & 15) == 0 && e.N % 8 == 0;
-  while (rows) {
-    int row[kRows], m = 0;
+// The column of value c of a lane: 8 neighbouring ones, or (rows of Bt that are not 16-byte aligned)
+// every 32nd.
+template <bool WIDE>
+__device__ __forceinline__ int column(int lane, int c) { return WIDE ? 8 * lane + c : lane + 32 * c; }
+
+// kStep rows of Bt from rank r on, the lane's 8 columns of 256 from column n0 on; zeros outside.
+template <bool WIDE>
+__device__ __forceinline__ void load_b(const qmm_lora_adapter& a, int64_t N, int64_t n0, int r, int r1, int lane,
+                                       uint4 (&b)[kStep]) {
 #pragma unroll
-    for (int j = 0; j < kRows; ++j) {
+  for (int q = 0; q < kStep; ++q) {
+    b[q] = make_uint4(0u, 0u, 0u, 0u);
+    if (r + q >= r1) continue;
+    const uint16_t* src = a.Bt + (int64_t)(r + q) * N + n0;
+    if constexpr (WIDE) {
+      if (n0 + 8 * lane < N) b[q] = ldg_nc_v4(src + 8 * lane);
+    } else {
+      uint32_t v[8];
+#pragma unroll
+      for (int c = 0; c < 8; ++c) v[c] = n0 + lane + 32 * c < N ? src[lane + 32 * c] : 0u;
+      b[q] = make_uint4(v[0] | v[1] << 16, v[2] | v[3] << 16, v[4] | v[5] << 16, v[6] | v[7] << 16);
+    }
+  }
+}
+
+// acc[j][c] += sum over ranks [r0, r1) of ts[j][r] Bt[r][column c] for R rows; `b` holds the first
+// kStep ranks' values already.
+template <int R, bool WIDE>
+__device__ __forceinline__ void accumulate(const qmm_lora_adapter& a, int64_t N, int64_t n0, int r0, int r1, int lane,
+                                           const float (*ts)[QMM_LORA_MAX_RANK], const uint4 (&first)[kStep],
+                                           float (&acc)[R][8]) {
+  uint4 b[kStep];
+#pragma unroll
+  for (int q = 0; q < kStep; ++q) b[q] = first[q];
+#pragma unroll 1
+  for (int r = r0; r < r1; r += kStep) {
+    uint4 ahead[kStep];
+    load_b<WIDE>(a, N, n0, r + kStep, r1, lane, ahead);
+#pragma unroll
+    for (int q = 0; q < kStep; ++q) {
+      float x[8];
+      unpack8(b[q], x);
+#pragma unroll
+      for (int j = 0; j < R; ++j) {
+        const float t = r + q < r1 ? ts[j][r + q] : 0.0f;
+#pragma unroll
+        for (int c = 0; c < 8; ++c) acc[j][c] = __fmaf_rn(x[c], t, acc[j][c]);
+      }
+    }
+#pragma unroll
+    for (int q = 0; q < kStep; ++q) b[q] = ahead[q];
+  }
+}
+
+// One CTA: one block (kSplit) or a block a warp (kStream) of columns for one adapter in use.
+template <Form FORM, bool WIDE>
+__device__ __forceinline__ void expand(const Params& P, const Entry& e, unsigned rows, const qmm_lora_adapter& a,
+                                       int64_t block0, float (*ts)[QMM_LORA_MAX_RANK], float (*part)[rows_of(FORM)][kCols]) {
+  constexpr bool SPLIT = FORM == kSplit;
+  constexpr int kWarps = warps_of(FORM), kRows = rows_of(FORM);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int64_t n0 = SPLIT ? block0 : block0 + kCols * warp;
+  int r0 = 0, r1 = a.rank;
+  if constexpr (SPLIT) {   // an equal share of the ranks, in steps
+    const int share = (a.rank + kStep * kWarps - 1) / (kStep * kWarps) * kStep;
+    r0 = min(a.rank, warp * share);
+    r1 = min(a.rank, r0 + share);
+  }
+  uint4 first[kStep];
+  load_b<WIDE>(a, e.N, n0, r0, r1, lane, first);
+  const bool vec = WIDE && e.N % 4 == 0 && ((reinterpret_cast<uintptr_t>(e.Y) | reinterpret_cast<uintptr_t>(e.Y0)) & 15) == 0;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  auto work = [&](auto r_) {   // the next R rows (or fewer) of the group
+    constexpr int R = decltype(r_)::value;
+    int row[R], m = 0;
+#pragma unroll
+    for (int j = 0; j < R; ++j) {
       row[j] = rows ? __ffs(rows) - 1 : row[0];
       if (rows) { rows &= rows - 1; ++m; }
     }
-    __syncthreads();
-    for (int v = threadIdx.x; v < m * a.rank; v += blockDim.x) {
-      const int j = v / a.rank, r = v % a.rank;
+    __syncthreads();   // the rows before are done with ts
+    for (int v = threadIdx.x; v < R * a.rank; v += 32 * kWarps) {
+      const int j = v / a.rank, r = v - j * a.rank;
       int mine = row[0];
 #pragma unroll
-      for (int q = 0; q < kRows; ++q) mine = j == q ? row[q] : mine;
+      for (int q = 1; q < R; ++q) mine = j == q ? row[q] : mine;
       float s = 0.0f;
-      for (int p = 0; p < e.pieces; ++p) s += e.t[((int64_t)p * P.M + mine) * P.rank_max + r];
-      ts[j][r] = s * a.scale;
+#pragma unroll 8
+      for (int p = 0; p < e.pieces; ++p) s += __ldcg(e.t + ((int64_t)p * P.M + mine) * P.rank_max + r);
+      ts[j][r] = j < m ? s * a.scale : 0.0f;
     }
     __syncthreads();
-    float acc[kRows][8] = {};
-    for (int r = warp; r < a.rank; r += kWarps) {
-      float b[8] = {};
-      const uint16_t* src = a.Bt + (int64_t)r * e.N + n;
-      if (wide && n < e.N) unpack8(*reinterpret_cast<const uint4*>(src), b);
-      else
-#pragma unroll
-        for (int c = 0; c < 8; ++c)
-          if (n + c < e.N) b[c] = __uint_as_float((uint32_t)src[c] << 16);
-#pragma unroll
-      for (int j = 0; j < kRows; ++j)
-        if (j < m)
-#pragma unroll
-          for (int c = 0; c < 8; ++c) acc[j][c] = __fmaf_rn(b[c], ts[j][r], acc[j][c]);
+    float acc[R][8] = {};
+    float4 y0[2];   // one row: its Y0 is asked for ahead of the sums
+    const bool early = R == 1 && !SPLIT && vec && n0 + 8 * lane < e.N;
+    if (early) {
+      y0[0] = *reinterpret_cast<const float4*>(e.Y0 + row[0] * e.N + n0 + 8 * lane);
+      y0[1] = *reinterpret_cast<const float4*>(e.Y0 + row[0] * e.N + n0 + 8 * lane + 4);
     }
+    accumulate<R, WIDE>(a, e.N, n0, r0, r1, lane, ts, first, acc);
+    if constexpr (SPLIT) {
 #pragma unroll
-    for (int j = 0; j < kRows; ++j)
+      for (int j = 0; j < R; ++j)
 #pragma unroll
-      for (int c = 0; c < 8; ++c) part[warp][j][8 * lane + c] = acc[j][c];
-    __syncthreads();
-    for (int v = threadIdx.x; v < m * kCols; v += blockDim.x) {
-      const int j = v / kCols, c = v % kCols;
-      int mine = row[0];
+        for (int c = 0; c < 8; ++c) part[warp][j][column<WIDE>(lane, c)] = acc[j][c];
+      __syncthreads();
+      for (int v = threadIdx.x; v < m * kCols; v += 32 * kWarps) {
+        const int j = v / kCols, c = v % kCols;
+        int mine = row[0];
 #pragma unroll
-      for (int q = 0; q < kRows; ++q) mine = j == q ? row[q] : mine;
-      float s = 0.0f;
+        for (int q = 1; q < R; ++q) mine = j == q ? row[q] : mine;
+        float s = 0.0f;
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) s += part[w][j][c];
-      if (n0 + c < e.N) e.Y[mine * e.N + n0 + c] = e.Y0[mine * e.N + n0 + c] + s;
+        for (int w = 0; w < kWarps; ++w) s += part[w][j][c];
+        const int64_t at = mine * e.N + n0 + c;
+        if (n0 + c < e.N) e.Y[at] = e.Y0[at] + s;
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < R; ++j) {
+        if (j >= m) break;
+        const int64_t at = row[j] * e.N + n0;
+        if (vec && n0 + 8 * lane < e.N) {
+          const float4* src = reinterpret_cast<const float4*>(e.Y0 + at + 8 * lane);
+          float4* y = reinterpret_cast<float4*>(e.Y + at + 8 * lane);
+          const float4 u = early ? y0[0] : src[0], v = early ? y0[1] : src[1];
+          y[0] = make_float4(u.x + acc[j][0], u.y + acc[j][1], u.z + acc[j][2], u.w + acc[j][3]);
+          y[1] = make_float4(v.x + acc[j][4], v.y + acc[j][5], v.z + acc[j][6], v.w + acc[j][7]);
+        } else if (!vec) {
+#pragma unroll
+          for (int c = 0; c < 8; ++c) {
+            const int col = column<WIDE>(lane, c);
+            if (n0 + col < e.N) e.Y[at + col] = e.Y0[at + col] + acc[j][c];
+          }
+        }
+      }
     }
+  };
+  while (rows) {
+    if (__popc(rows) == 1) work(std::integral_constant<int, 1>{});
+    else work(std::integral_constant<int, kRows>{});
   }
 }
 
-int pieces_of(int64_t K) { return (int)((K + kPiece - 1) / kPiece); }
+// Grid (blocks of columns over all entries, adapters in use).
+template <Form FORM>
+__global__ void __launch_bounds__(32 * warps_of(FORM), FORM == kSplit ? 2 : 16) lora_expand_kernel(const __grid_constant__ Params P) {
+  __shared__ float ts[rows_of(FORM)][QMM_LORA_MAX_RANK];
+  __shared__ float part[FORM == kSplit ? warps_of(FORM) : 1][rows_of(FORM)][kCols];
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  int k = 0;
+  while (k + 1 < P.count && (int)blockIdx.x >= P.e[k + 1].first) ++k;
+  const Entry& e = P.e[k];
+  int id = -1, groups;
+  const unsigned rows = group_rows(P.ids, P.M, e.n_adapters, blockIdx.y, id, groups);
+  if (!rows) return;
+  const qmm_lora_adapter a = adapter_of(e, id, P.rank_max);
+  const int64_t n0 = (int64_t)(blockIdx.x - e.first) * (FORM == kSplit ? kCols : kCols * warps_of(FORM));
+  if ((reinterpret_cast<uintptr_t>(a.Bt) & 15) == 0 && e.N % 8 == 0) expand<FORM, true>(P, e, rows, a, n0, ts, part);
+  else expand<FORM, false>(P, e, rows, a, n0, ts, part);
+}
+
+int chunks_of(int64_t K) { return (int)((K + (int64_t)kChunk * kPieces - 1) / ((int64_t)kChunk * kPieces)); }
+int pieces_of(int64_t K) {
+  const int64_t piece = (int64_t)kChunk * chunks_of(K);
+  return (int)((K + piece - 1) / piece);
+}
 
 size_t entry_floats(int64_t K, int M, int rank_max) { return ((size_t)pieces_of(K) * M * rank_max + 3) & ~(size_t)3; }
+
+template <class F>
+cudaError_t launch_early(F* kernel, dim3 grid, int warps, const Params& P, cudaStream_t stream) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(32 * warps);
+  cfg.stream = stream;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, P);
+}
 
 }  // namespace
 
@@ -217,23 +368,36 @@ cudaError_t launch_lora(const qmm_lora_entry* entries, int count, const int32_t*
   P.count = count;
   P.M = M;
   P.rank_max = rank_max;
-  float* t = static_cast<float*>(workspace);
-  int64_t blocks = 0;
+  P.rank_groups = (rank_max + kRanks - 1) / kRanks;
+  // kStream where the blocks of columns alone make 16 warps an SM and the rows of an adapter are few (each
+  // two read it again).
+  int64_t warps = 0;
   int pieces = 0, groups = 1;
   for (int k = 0; k < count; ++k) {
     const qmm_lora_entry& e = entries[k];
-    P.e[k] = Entry{e.adapters, e.X, e.Y0, e.Y, t, e.N, e.K, e.n_adapters, pieces_of(e.K), (int)blocks};
-    t += entry_floats(e.K, M, rank_max);
-    blocks += (e.N + kCols - 1) / kCols;
-    pieces = pieces > P.e[k].pieces ? pieces : P.e[k].pieces;
     const int g = e.n_adapters < M ? e.n_adapters + 1 : M;   // adapters in use, and no adapter
-    groups = groups > g ? groups : (g < M ? g : M);
+    groups = groups > g ? groups : g;
+    pieces = pieces > pieces_of(e.K) ? pieces : pieces_of(e.K);
+    warps += (e.N + kCols - 1) / kCols * g;
+  }
+  const bool split = warps < 16 * (int64_t)sm_count() || M > 2 * entries[0].n_adapters;
+  const int64_t cols = split ? kCols : (int64_t)kCols * warps_of(kStream);
+  float* t = static_cast<float*>(workspace);
+  int64_t blocks = 0;
+  for (int k = 0; k < count; ++k) {
+    const qmm_lora_entry& e = entries[k];
+    P.e[k] = Entry{e.adapters, e.X, e.Y0, e.Y, t, e.N, e.K, e.n_adapters, pieces_of(e.K), chunks_of(e.K), (int)blocks};
+    t += entry_floats(e.K, M, rank_max);
+    blocks += (e.N + cols - 1) / cols;
   }
   if (blocks > 0x7fffffff) return cudaErrorInvalidValue;
-  const int rank_groups = (rank_max + kWarps * kRanks - 1) / (kWarps * kRanks);
-  lora_shrink_kernel<<<dim3(pieces * rank_groups, groups, count), 32 * kWarps, 0, stream>>>(P);
-  lora_expand_kernel<<<dim3((unsigned)blocks, groups), 32 * kWarps, 0, stream>>>(P);
-  return cudaGetLastError();
+  cudaError_t err = launch_early(lora_shrink_kernel,
+                                 dim3((pieces * P.rank_groups + kShrinkWarps - 1) / kShrinkWarps, groups, count),
+                                 kShrinkWarps, P, stream);
+  if (err != cudaSuccess) return err;
+  const dim3 grid((unsigned)blocks, groups);
+  return split ? launch_early(lora_expand_kernel<kSplit>, grid, warps_of(kSplit), P, stream)
+               : launch_early(lora_expand_kernel<kStream>, grid, warps_of(kStream), P, stream);
 }
 
 cudaError_t read_and_clear_lora_status(unsigned* out) {
