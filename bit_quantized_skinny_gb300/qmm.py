@@ -183,10 +183,17 @@ def _check(status: int, what: str):
         raise QmmError(status, what)
 
 
-def _stream_handle(stream):
+def _current_stream() -> int:
+    """Handle of torch's current stream on the current device.  (Without the Stream object that
+    torch.cuda.current_stream() makes: 0.4 us a call, not 3.3.)"""
     import torch
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    return raw(torch.cuda.current_device()) if raw else torch.cuda.current_stream().cuda_stream
+
+
+def _stream_handle(stream):
     if stream is None:
-        stream = torch.cuda.current_stream()
+        return _current_stream()
     return ctypes.c_void_p(stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream))
 
 
