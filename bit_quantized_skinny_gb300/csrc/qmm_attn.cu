@@ -893,7 +893,7 @@ __global__ void __launch_bounds__(32 * kCombineWarps) attn_combine_kernel(const 
       for (int q = 0; q < kV; ++q) o[q] = __fmaf_rn(x[k][q], w, o[q]);
     }
   // the other segments of the two groups, one a lane
-  const int n0 = st[0].rest >> 16, all = n0 + (int)(st[1].rest >> 16);
+  const int n0 = min((int)(st[0].rest >> 16), kMaxCtas), all = n0 + min((int)(st[1].rest >> 16), kMaxCtas);
   if (all > 0) {
     int row[2];   // of the tiles of each group's block
 #pragma unroll

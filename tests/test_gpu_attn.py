@@ -268,3 +268,57 @@ def test_random_shapes(qmm):
         if c.T:
             c.run(qmm).check()
     assert qmm.device_status() == 0
+
+
+def test_many_calls_of_ragged_streams(qmm):
+    """Short and long segments of one and two row tiles in turn, call after call behind each other: every wait
+    ends (bit 0 of the status word) and every call gives the same bits."""
+    import random
+    r = random.Random(3)
+    for D, dtype, G in ((64, F16, 8), (128, BF16, 5), (128, BF16, 64)):
+        cases = [Case([r.randint(0, 2 * (128 // G) + 3) for _ in range(29)], [r.choice([0, 1, 40, 64, 65, 300, 900]) for _ in range(29)],
+                      p, 2 * G, 2, D, 32, dtype, seed=k) for k, p in enumerate((0, 60, 1700))]
+        first = []
+        for c in cases:
+            c.run(qmm).check()
+            first.append(c.O.clone())
+        args = [c.args(qmm) for c in cases]
+        ws = torch.empty(max(qmm.attn_workspace_bytes(a) for a in args), dtype=torch.uint8, device="cuda")
+        for _ in range(60):
+            for a in args:
+                qmm.attn_shared(a, ws)
+        torch.cuda.synchronize()
+        assert qmm.device_status() == 0
+        for c, f in zip(cases, first):
+            assert torch.equal(c.O, f)
+
+
+def test_a_wait_that_runs_out_is_reported(qmm):
+    """With a bound far below a memory access's latency the first waits give up: the call ends, sets bit 0, and
+    the next call (default bound) is right."""
+    c = Case([8] * 4, [90, 8, 500, 129], 2050, 10, 2, 128, 64)
+    qmm.set_wait_limit(2, 50)
+    try:
+        c.run(qmm)
+    finally:
+        qmm.set_wait_limit(0, 0)
+    assert qmm.device_status() & 1 and qmm.device_status() == 0
+    c.run(qmm).check()
+    assert qmm.device_status() == 0
+
+
+def test_concurrent_streams(qmm):
+    """Calls on two streams with a workspace each do not disturb each other."""
+    a = Case([2] * 8, [300 + k for k in range(8)], 900, 10, 2, 128, 32)
+    b = Case([5] * 6, [70 * k + 9 for k in range(6)], 400, 24, 3, 64, 16, F16)
+    a.run(qmm)
+    b.run(qmm)
+    want = a.O.clone(), b.O.clone()
+    args = [a.args(qmm), b.args(qmm)]
+    ws = [torch.empty(qmm.attn_workspace_bytes(x), dtype=torch.uint8, device="cuda") for x in args]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for _ in range(20):
+        for x, w, st in zip(args, ws, streams):
+            qmm.attn_shared(x, w, stream=st)
+    torch.cuda.synchronize()
+    assert torch.equal(a.O, want[0]) and torch.equal(b.O, want[1]) and qmm.device_status() == 0
