@@ -47,7 +47,7 @@ __device__ unsigned g_status;   // this file's kernels' status word
 
 constexpr int kRows = 128;           // rows of a row tile
 constexpr int kTile = 64;            // keys of a key tile
-constexpr int kLead = 3;             // units of a group besides its key tiles
+constexpr int kLead = 4;             // units of a group besides its key tiles (2, 3, 6: 10, 6, 2 % slower for 16 streams)
 constexpr int kMaxCtas = 152;
 constexpr int kLaneWarps = 4;
 constexpr int kLoadWarp = 8, kMmaWarp = 9 /* and 10 */, kQWarp = 11;
@@ -826,7 +826,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
 }
 
 // ------------------------------------------------------------------------------------------
-// Joins a row's segments: one warp per (row, head).  The segments of a group are the one that begins
+// Joins a row's segments: SHARE warps per (row, head).  The segments of a group are the one that begins
 // it (in the row's own record) and those of the CTAs whose piece begins inside it.
 constexpr int kCombineWarps = 8;
 
@@ -836,14 +836,15 @@ __device__ __forceinline__ int column_of(int p) {
   return (p & ~31) + 8 * ((p & 7) >> 1) + 2 * ((p & 31) >> 3) + (p & 1);
 }
 
-template <int D, int TYPE, int AHEAD>
+template <int D, int TYPE, int SHARE>
 __global__ void __launch_bounds__(32 * kCombineWarps) attn_combine_kernel(const __grid_constant__ Params P) {
   constexpr int kV = D / 32;   // values of a lane: positions kV * lane and on
+  constexpr int kAhead = 8;    // records whose O a warp has in flight
   const qmm_attn_args& a = P.a;
   __shared__ int stream;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int t = blockIdx.x, lane = threadIdx.x & 31;
-  const int head = blockIdx.y * kCombineWarps + (threadIdx.x >> 5);
+  const int head = (blockIdx.y * kCombineWarps + (threadIdx.x >> 5)) / SHARE, share = (threadIdx.x >> 5) % SHARE;
   if (threadIdx.x == 0) stream = -1;
   __syncthreads();
   for (int b = threadIdx.x; b < a.B; b += blockDim.x) {
@@ -851,8 +852,8 @@ __global__ void __launch_bounds__(32 * kCombineWarps) attn_combine_kernel(const 
     if (t >= s.t0 && t < s.t0 + s.m) stream = b;   // one stream, if the starts do not decrease
   }
   __syncthreads();
-  if (head >= a.Hq) return;
-  const int b = stream, G = a.Hq / a.Hk, block = 2 * P.tokens;
+  if (SHARE == 1 && head >= a.Hq) return;
+  const int b = head < a.Hq ? stream : -1, G = a.Hq / a.Hk, block = 2 * P.tokens;
   Stream s{};
   bool has[2] = {b >= 0 && a.prefix_len > 0 && t < a.row_starts[a.B], false};   // key tiles of the prefix, of own keys
   if (b >= 0) {
@@ -880,13 +881,13 @@ __global__ void __launch_bounds__(32 * kCombineWarps) attn_combine_kernel(const 
     if (has[k]) {
       const int64_t at = k ? (int64_t)a.T * a.Hq + rec : rec;
       st[k] = P.s_rows[at];
-      load(P.o_rows + at * D, x[k]);
+      if (share == 0) load(P.o_rows + at * D, x[k]);
     }
-  float top = fmaxf(st[0].top, st[1].top), sum = 0.0f, o[kV] = {};
+  float top = share == 0 ? fmaxf(st[0].top, st[1].top) : -INFINITY, sum = 0.0f, o[kV] = {};
   uint32_t odd = st[0].odd | st[1].odd;
 #pragma unroll
   for (int k = 0; k < 2; ++k)
-    if (saw(st[k])) {
+    if (share == 0 && saw(st[k])) {
       const float w = exp2_fast(st[k].top - top);
       sum = __fmaf_rn(st[k].sum, w, sum);
 #pragma unroll
@@ -894,31 +895,32 @@ __global__ void __launch_bounds__(32 * kCombineWarps) attn_combine_kernel(const 
     }
   // the other segments of the two groups, one a lane
   const int n0 = min((int)(st[0].rest >> 16), kMaxCtas), all = n0 + min((int)(st[1].rest >> 16), kMaxCtas);
-  if (all > 0) {
+  const int part = (all + SHARE - 1) / SHARE, end = min(all, (share + 1) * part);   // this warp's of them
+  if (share * part < end) {
     int row[2];   // of the tiles of each group's block
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
       const int in = (k ? t - s.t0 : t) % block;
       row[k] = (in < P.tokens ? in * G : kRows + (in - P.tokens) * G) + head % G;
     }
-    for (int r0 = 0; r0 < all; r0 += 32) {
+    for (int r0 = share * part; r0 < end; r0 += 32) {
       const int r = r0 + lane;
-      const bool own = r >= n0, live = r < all;
+      const bool own = r >= n0, live = r < end;
       const int cta = min((int)((own ? st[1].rest : st[0].rest) & 0xFFFFu) + (own ? r - n0 : r), kMaxCtas - 1);
       const int at = cta * 2 * kRows + (own ? row[1] : row[0]);
       RowStat q{-INFINITY, 0.0f, 0u, 0u};
       if (live) q = P.s_cta[at];
-      // their O, AHEAD at a time, asked for before the statistics are there
+      // their O, some at a time, asked for before the statistics are there
       float best = top, keep = 1.0f, w = 0.0f;
 #pragma unroll 1
-      for (int j0 = 0; j0 < 32 && r0 + j0 < all; j0 += AHEAD) {
-        float y[AHEAD][kV];
+      for (int j0 = 0; j0 < 32 && r0 + j0 < end; j0 += kAhead) {
+        float y[kAhead][kV];
 #pragma unroll
-        for (int j = 0; j < AHEAD; ++j) {
+        for (int j = 0; j < kAhead; ++j) {
           const int from = __shfl_sync(0xffffffffu, at, j0 + j);
 #pragma unroll
           for (int k = 0; k < kV; ++k) y[j][k] = 0.0f;
-          if (j0 + j < 32 && r0 + j0 + j < all) load(P.o_cta + (int64_t)from * D, y[j]);
+          if (r0 + j0 + j < end) load(P.o_cta + (int64_t)from * D, y[j]);
         }
         if (j0 == 0) {
           best = q.top;
@@ -937,14 +939,42 @@ __global__ void __launch_bounds__(32 * kCombineWarps) attn_combine_kernel(const 
           for (int k = 0; k < kV; ++k) o[k] *= keep;
         }
 #pragma unroll
-        for (int j = 0; j < AHEAD; ++j) {
+        for (int j = 0; j < kAhead; ++j) {
           const float f = __shfl_sync(0xffffffffu, w, j0 + j);
-          if (j0 + j < 32 && f != 0.0f)   // (of a segment none of whose keys the row saw, O means nothing)
+          if (f != 0.0f)   // (of a segment none of whose keys the row saw, O means nothing)
 #pragma unroll
             for (int k = 0; k < kV; ++k) o[k] = __fmaf_rn(y[j][k], f, o[k]);
         }
       }
     }
+  }
+  if constexpr (SHARE > 1) {   // the warps of a row, joined by the first
+    __shared__ float o_s[kCombineWarps][D];
+    __shared__ float4 stat_s[kCombineWarps];
+    const int w0 = threadIdx.x >> 5;
+#pragma unroll
+    for (int k = 0; k < kV; ++k) o_s[w0][kV * lane + k] = o[k];
+    if (lane == 0) stat_s[w0] = make_float4(top, sum, __uint_as_float(odd), 0.0f);
+    __syncthreads();
+    if (share != 0 || head >= a.Hq) return;
+    float best = top;
+#pragma unroll
+    for (int w = 1; w < SHARE; ++w) best = fmaxf(best, stat_s[w0 + w].x);
+    const float keep = top == -INFINITY && sum == 0.0f ? 0.0f : exp2_fast(top - best);
+    sum *= keep;
+#pragma unroll
+    for (int k = 0; k < kV; ++k) o[k] *= keep;
+#pragma unroll
+    for (int w = 1; w < SHARE; ++w) {
+      const float4 q = stat_s[w0 + w];
+      odd |= __float_as_uint(q.z);
+      if (q.x == -INFINITY && q.y == 0.0f) continue;
+      const float f = exp2_fast(q.x - best);
+      sum = __fmaf_rn(q.y, f, sum);
+#pragma unroll
+      for (int k = 0; k < kV; ++k) o[k] = __fmaf_rn(o_s[w0 + w][kV * lane + k], f, o[k]);
+    }
+    top = best;
   }
   const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
 #pragma unroll
@@ -1056,10 +1086,13 @@ cudaError_t launch(const qmm_attn_args& a, void* workspace, cudaStream_t stream)
   cfg.gridDim = dim3(a.T, (a.Hq + kCombineWarps - 1) / kCombineWarps);
   cfg.blockDim = dim3(32 * kCombineWarps);
   cfg.dynamicSmemBytes = 0;
-  // A row's other records are read 24 at a time where the grid is one CTA an SM at most (179 registers;
-  // 160 CTAs of 19 records each: 2.6 us, 4.2 us with 8), 8 at a time where more CTAs share an SM.
-  if ((int64_t)cfg.gridDim.x * cfg.gridDim.y <= 2 * sms) return cudaLaunchKernelEx(&cfg, attn_combine_kernel<D, TYPE, 24>, P);
-  return cudaLaunchKernelEx(&cfg, attn_combine_kernel<D, TYPE, 8>, P);
+  // Four warps share a row's records where one warp a row is nine an SM at most (1280 rows of 21 records:
+  // the call takes 43.7 us, 46.3 with one; 1824 rows of a few: 21.1, 18.5 with one).
+  if ((int64_t)a.T * a.Hq <= 9 * sms) {
+    cfg.gridDim.y = (a.Hq * 4 + kCombineWarps - 1) / kCombineWarps;
+    return cudaLaunchKernelEx(&cfg, attn_combine_kernel<D, TYPE, 4>, P);
+  }
+  return cudaLaunchKernelEx(&cfg, attn_combine_kernel<D, TYPE, 1>, P);
 }
 
 }  // namespace
