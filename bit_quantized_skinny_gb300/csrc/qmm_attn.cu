@@ -382,9 +382,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
   tc::fence_after_sync();
   const uint32_t tmem = M.tmem;
 
-  // A bounded wait for a phase of a barrier; false: this wait, or another one, gave up.
+  // A bounded wait for a phase of a barrier; false: this wait, or another one, gave up.  (A suspended try
+  // from the start: polls take issue slots from the softmax; 32 of them first cost 14 %.)
   auto wait = [&](int k, uint32_t parity) -> bool {
-    if (mbar_try(bar(k), parity)) return true;
+    if (mbar_wait(bar(k), parity, 1, P.wait_ns ? P.wait_ns : kSuspendNs)) return true;
     return wait_slowly(bar(k), parity, P.wait_polls ? P.wait_polls : kWaitLimit, P.wait_ns ? P.wait_ns : kSuspendNs,
                        abort_flag);
   };
@@ -896,13 +897,41 @@ __global__ void __launch_bounds__(32 * kCombineWarps) attn_combine_kernel(const 
   // the other segments of the two groups, one a lane
   const int n0 = min((int)(st[0].rest >> 16), kMaxCtas), all = n0 + min((int)(st[1].rest >> 16), kMaxCtas);
   const int part = (all + SHARE - 1) / SHARE, end = min(all, (share + 1) * part);   // this warp's of them
-  if (share * part < end) {
-    int row[2];   // of the tiles of each group's block
+  int row[2] = {0, 0};   // of the tiles of each group's block
+  if (all > 0) {
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
       const int in = (k ? t - s.t0 : t) % block;
       row[k] = (in < P.tokens ? in * G : kRows + (in - P.tokens) * G) + head % G;
     }
+  }
+  constexpr int kFew = 3;
+  if (SHARE == 1 && all > 0 && all <= kFew) {   // few of them, as a rule where rows are many: one after the other
+    RowStat q[kFew];
+    float y[kFew][kV];
+#pragma unroll
+    for (int r = 0; r < kFew; ++r) {
+      q[r] = RowStat{-INFINITY, 0.0f, 0u, 0u};
+      if (r < all) {
+        const bool own = r >= n0;
+        const int cta = min((int)((own ? st[1].rest : st[0].rest) & 0xFFFFu) + (own ? r - n0 : r), kMaxCtas - 1);
+        const int at = cta * 2 * kRows + (own ? row[1] : row[0]);
+        q[r] = P.s_cta[at];
+        load(P.o_cta + (int64_t)at * D, y[r]);
+      }
+    }
+#pragma unroll
+    for (int r = 0; r < kFew; ++r) {
+      if (!saw(q[r])) continue;
+      const float best = fmaxf(top, q[r].top), f = exp2_fast(q[r].top - best);
+      const float keep = top == -INFINITY && sum == 0.0f ? 0.0f : exp2_fast(top - best);
+      sum = __fmaf_rn(sum, keep, q[r].sum * f);
+      top = best;
+      odd |= q[r].odd;
+#pragma unroll
+      for (int k = 0; k < kV; ++k) o[k] = __fmaf_rn(y[r][k], f, o[k] * keep);
+    }
+  } else if (share * part < end) {
     for (int r0 = share * part; r0 < end; r0 += 32) {
       const int r = r0 + lane;
       const bool own = r >= n0, live = r < end;
