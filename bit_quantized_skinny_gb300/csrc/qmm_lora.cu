@@ -25,7 +25,6 @@ constexpr int kChunk = 512;      // values of K that a shrink warp holds at a ti
 constexpr int kPieces = 64;      // pieces of K at most
 constexpr int64_t kAhead = 16 << 20;   // bytes of B that the shrink launch asks into L2
 constexpr int kCols = 256;       // columns of one expand warp, 8 a lane
-constexpr int kStep = 4;         // ranks that an expand warp loads together
 // The two forms of the expand kernel.  kSplit: 8 warps share the ranks of one block of columns and join
 // their sums in shared memory; up to 4 rows are worked on together.  kStream: a block of columns for
 // each of 2 warps, up to 2 rows together, few enough registers that every warp of 32 adapters
@@ -34,6 +33,7 @@ constexpr int kStep = 4;         // ranks that an expand warp loads together
 enum Form { kSplit, kStream };
 __host__ __device__ constexpr int warps_of(Form f) { return f == kSplit ? 8 : 2; }
 __host__ __device__ constexpr int rows_of(Form f) { return f == kSplit ? 4 : 2; }
+__host__ __device__ constexpr int step_of(Form f, bool wide) { return f == kSplit && wide ? 8 : 4; }   // ranks loaded together
 
 struct Entry {
   const qmm_lora_adapter* adapters;
@@ -169,46 +169,72 @@ __global__ void __launch_bounds__(32 * kShrinkWarps, 4) lora_shrink_kernel(const
   }
 }
 
-// The column of value c of a lane: 8 neighbouring ones, or (rows of Bt that are not 16-byte aligned)
-// every 32nd.
-template <bool WIDE>
-__device__ __forceinline__ int column(int lane, int c) { return WIDE ? 8 * lane + c : lane + 32 * c; }
+// The 16 bytes at p (16-byte aligned), as far as they lie in [lo, hi); zeros for the rest.  (The first and
+// the last of a matrix only: out of line.)
+__device__ __noinline__ uint4 load_edge(const uint16_t* p, const uint16_t* lo, const uint16_t* hi) {
+  uint32_t v[8];
+#pragma unroll
+  for (int c = 0; c < 8; ++c) v[c] = p + c >= lo && p + c < hi ? p[c] : 0u;
+  return make_uint4(v[0] | v[1] << 16, v[2] | v[3] << 16, v[4] | v[5] << 16, v[6] | v[7] << 16);
+}
 
-// kStep rows of Bt from rank r on, the lane's 8 columns of 256 from column n0 on; zeros outside.
-template <bool WIDE>
+__device__ __forceinline__ uint4 load_within(const uint16_t* p, const uint16_t* lo, const uint16_t* hi) {
+  if (p >= lo && p + 8 <= hi) return __ldg(reinterpret_cast<const uint4*>(p));
+  return load_edge(p, lo, hi);
+}
+
+// The 8 values that begin `skip` values (0..7) into a and go on in b.
+__device__ __forceinline__ uint4 shifted(uint4 a, uint4 b, int skip) {
+  uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+  if (skip & 4)
+#pragma unroll
+    for (int k = 0; k < 6; ++k) w[k] = w[k + 2];
+  if (skip & 2)
+#pragma unroll
+    for (int k = 0; k < 5; ++k) w[k] = w[k + 1];
+  if (skip & 1)
+#pragma unroll
+    for (int k = 0; k < 4; ++k) w[k] = w[k] >> 16 | w[k + 1] << 16;
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// STEP rows of Bt from rank r on, the lane's 8 columns n0 + 8 lane ..; zeros for ranks from r1 on.  (Columns
+// behind N are never stored; what stands in their place is the next row's.)  WIDE: every row is 16-byte
+// aligned; else a row's values are cut out of the two aligned words that hold them.
+template <int STEP, bool WIDE>
 __device__ __forceinline__ void load_b(const qmm_lora_adapter& a, int64_t N, int64_t n0, int r, int r1, int lane,
-                                       uint4 (&b)[kStep]) {
+                                       uint4 (&b)[STEP]) {
 #pragma unroll
-  for (int q = 0; q < kStep; ++q) {
+  for (int q = 0; q < STEP; ++q) {
     b[q] = make_uint4(0u, 0u, 0u, 0u);
-    if (r + q >= r1) continue;
-    const uint16_t* src = a.Bt + (int64_t)(r + q) * N + n0;
+    if (r + q >= r1 || n0 + 8 * lane >= N) continue;
+    const uint16_t* src = a.Bt + (int64_t)(r + q) * N + n0 + 8 * lane;
     if constexpr (WIDE) {
-      if (n0 + 8 * lane < N) b[q] = ldg_nc_v4(src + 8 * lane);
+      b[q] = ldg_nc_v4(src);
     } else {
-      uint32_t v[8];
-#pragma unroll
-      for (int c = 0; c < 8; ++c) v[c] = n0 + lane + 32 * c < N ? src[lane + 32 * c] : 0u;
-      b[q] = make_uint4(v[0] | v[1] << 16, v[2] | v[3] << 16, v[4] | v[5] << 16, v[6] | v[7] << 16);
+      const int skip = (int)(reinterpret_cast<uintptr_t>(src) & 15) / 2;   // the same for all lanes of a row
+      const uint16_t* hi = a.Bt + (int64_t)a.rank * N;
+      const uint4 u = load_within(src - skip, a.Bt, hi);
+      b[q] = skip ? shifted(u, load_within(src - skip + 8, a.Bt, hi), skip) : u;
     }
   }
 }
 
 // acc[j][c] += sum over ranks [r0, r1) of ts[j][r] Bt[r][column c] for R rows; `b` holds the first
-// kStep ranks' values already.
-template <int R, bool WIDE>
+// STEP ranks' values already.
+template <int R, int STEP, bool WIDE>
 __device__ __forceinline__ void accumulate(const qmm_lora_adapter& a, int64_t N, int64_t n0, int r0, int r1, int lane,
-                                           const float (*ts)[QMM_LORA_MAX_RANK], const uint4 (&first)[kStep],
+                                           const float (*ts)[QMM_LORA_MAX_RANK], const uint4 (&first)[STEP],
                                            float (&acc)[R][8]) {
-  uint4 b[kStep];
+  uint4 b[STEP];
 #pragma unroll
-  for (int q = 0; q < kStep; ++q) b[q] = first[q];
+  for (int q = 0; q < STEP; ++q) b[q] = first[q];
 #pragma unroll 1
-  for (int r = r0; r < r1; r += kStep) {
-    uint4 ahead[kStep];
-    load_b<WIDE>(a, N, n0, r + kStep, r1, lane, ahead);
+  for (int r = r0; r < r1; r += STEP) {
+    uint4 ahead[STEP];
+    load_b<STEP, WIDE>(a, N, n0, r + STEP, r1, lane, ahead);
 #pragma unroll
-    for (int q = 0; q < kStep; ++q) {
+    for (int q = 0; q < STEP; ++q) {
       float x[8];
       unpack8(b[q], x);
 #pragma unroll
@@ -219,7 +245,7 @@ __device__ __forceinline__ void accumulate(const qmm_lora_adapter& a, int64_t N,
       }
     }
 #pragma unroll
-    for (int q = 0; q < kStep; ++q) b[q] = ahead[q];
+    for (int q = 0; q < STEP; ++q) b[q] = ahead[q];
   }
 }
 
@@ -228,7 +254,7 @@ template <Form FORM, bool WIDE>
 __device__ __forceinline__ void expand(const Params& P, const Entry& e, unsigned rows, const qmm_lora_adapter& a,
                                        int64_t block0, float (*ts)[QMM_LORA_MAX_RANK], float (*part)[rows_of(FORM)][kCols]) {
   constexpr bool SPLIT = FORM == kSplit;
-  constexpr int kWarps = warps_of(FORM), kRows = rows_of(FORM);
+  constexpr int kWarps = warps_of(FORM), kRows = rows_of(FORM), kStep = step_of(FORM, WIDE);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int64_t n0 = SPLIT ? block0 : block0 + kCols * warp;
   int r0 = 0, r1 = a.rank;
@@ -238,8 +264,8 @@ __device__ __forceinline__ void expand(const Params& P, const Entry& e, unsigned
     r1 = min(a.rank, r0 + share);
   }
   uint4 first[kStep];
-  load_b<WIDE>(a, e.N, n0, r0, r1, lane, first);
-  const bool vec = WIDE && e.N % 4 == 0 && ((reinterpret_cast<uintptr_t>(e.Y) | reinterpret_cast<uintptr_t>(e.Y0)) & 15) == 0;
+  load_b<kStep, WIDE>(a, e.N, n0, r0, r1, lane, first);
+  const bool vec = e.N % 8 == 0 && ((reinterpret_cast<uintptr_t>(e.Y) | reinterpret_cast<uintptr_t>(e.Y0)) & 15) == 0;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   auto work = [&](auto r_) {   // the next R rows (or fewer) of the group
     constexpr int R = decltype(r_)::value;
@@ -249,6 +275,11 @@ __device__ __forceinline__ void expand(const Params& P, const Entry& e, unsigned
       row[j] = rows ? __ffs(rows) - 1 : row[0];
       if (rows) { rows &= rows - 1; ++m; }
     }
+    float ys[R];   // kSplit: Y0 of the thread's column, asked for ahead of the sums
+    if constexpr (SPLIT)
+#pragma unroll
+      for (int j = 0; j < R; ++j)
+        ys[j] = j < m && n0 + threadIdx.x < e.N ? e.Y0[row[j] * e.N + n0 + threadIdx.x] : 0.0f;
     __syncthreads();   // the rows before are done with ts
     for (int v = threadIdx.x; v < R * a.rank; v += 32 * kWarps) {
       const int j = v / a.rank, r = v - j * a.rank;
@@ -256,9 +287,16 @@ __device__ __forceinline__ void expand(const Params& P, const Entry& e, unsigned
 #pragma unroll
       for (int q = 1; q < R; ++q) mine = j == q ? row[q] : mine;
       float s = 0.0f;
-#pragma unroll 8
-      for (int p = 0; p < e.pieces; ++p) s += __ldcg(e.t + ((int64_t)p * P.M + mine) * P.rank_max + r);
-      ts[j][r] = j < m ? s * a.scale : 0.0f;
+      const float* t = e.t + (int64_t)mine * P.rank_max + r;
+      constexpr int kTogether = 16;
+      for (int p0 = 0; j < m && p0 < e.pieces; p0 += kTogether) {
+        float x[kTogether];
+#pragma unroll
+        for (int p = 0; p < kTogether; ++p) x[p] = p0 + p < e.pieces ? __ldcg(t + (int64_t)(p0 + p) * P.M * P.rank_max) : 0.0f;
+#pragma unroll
+        for (int p = 0; p < kTogether; ++p) s += x[p];
+      }
+      ts[j][r] = s * a.scale;
     }
     __syncthreads();
     float acc[R][8] = {};
@@ -268,23 +306,20 @@ __device__ __forceinline__ void expand(const Params& P, const Entry& e, unsigned
       y0[0] = *reinterpret_cast<const float4*>(e.Y0 + row[0] * e.N + n0 + 8 * lane);
       y0[1] = *reinterpret_cast<const float4*>(e.Y0 + row[0] * e.N + n0 + 8 * lane + 4);
     }
-    accumulate<R, WIDE>(a, e.N, n0, r0, r1, lane, ts, first, acc);
+    accumulate<R, kStep, WIDE>(a, e.N, n0, r0, r1, lane, ts, first, acc);
     if constexpr (SPLIT) {
 #pragma unroll
       for (int j = 0; j < R; ++j)
 #pragma unroll
-        for (int c = 0; c < 8; ++c) part[warp][j][column<WIDE>(lane, c)] = acc[j][c];
+        for (int c = 0; c < 8; ++c) part[warp][j][8 * lane + c] = acc[j][c];
       __syncthreads();
-      for (int v = threadIdx.x; v < m * kCols; v += 32 * kWarps) {
-        const int j = v / kCols, c = v % kCols;
-        int mine = row[0];
+      static_assert(!SPLIT || kCols == 32 * kWarps, "a column a thread");
 #pragma unroll
-        for (int q = 1; q < R; ++q) mine = j == q ? row[q] : mine;
+      for (int j = 0; j < R; ++j) {
         float s = 0.0f;
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w) s += part[w][j][c];
-        const int64_t at = mine * e.N + n0 + c;
-        if (n0 + c < e.N) e.Y[at] = e.Y0[at] + s;
+        for (int w = 0; w < kWarps; ++w) s += part[w][j][threadIdx.x];
+        if (j < m && n0 + threadIdx.x < e.N) e.Y[row[j] * e.N + n0 + threadIdx.x] = ys[j] + s;
       }
     } else {
 #pragma unroll
@@ -300,7 +335,7 @@ __device__ __forceinline__ void expand(const Params& P, const Entry& e, unsigned
         } else if (!vec) {
 #pragma unroll
           for (int c = 0; c < 8; ++c) {
-            const int col = column<WIDE>(lane, c);
+            const int col = 8 * lane + c;
             if (n0 + col < e.N) e.Y[at + col] = e.Y0[at + col] + acc[j][c];
           }
         }
