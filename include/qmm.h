@@ -528,7 +528,8 @@ size_t qmm_workspace_bytes_held(void);
  * outputs of that call are invalid and the context stays usable.  This call sets the bound of
  * the launches made from now on to `polls` polls of at most `suspend_ns` nanoseconds each
  * (0, 0 restores the default), for every thread and stream of the process: a test hook, which
- * with a bound far below a memory access's latency makes the first wait run out. */
+ * with a bound far below a memory access's latency makes the first wait run out.  The
+ * waits of qmm_attn_shared are bounded in the same way and by the same call. */
 void qmm_set_wait_limit(uint32_t polls, uint32_t suspend_ns);
 
 /* Read and clear the status word that the kernels of this library keep on the current device
