@@ -1,15 +1,18 @@
 // qmm_lora.cu — low-rank adapters beside shared projections (qmm_run_lora):
 //     Y[i] = Y0[i] + scale_a * B_a (A_a x_i),  a = ids[i].
 //
-// Two launches.  lora_shrink_kernel forms t_i = A_a x_i: one warp per (adapter in use, 4 ranks, 512
-// values of K), the partial sums of the pieces of K kept apart.  lora_expand_kernel sums the pieces
-// and adds scale * t_i Bt_a to Y0, 256 columns a warp.  Both are bound by the adapters' bytes: an
-// adapter is read once for all the rows that use it (found by a warp match over the at most 32 ids),
-// A stays in registers over the rows and B over up to 4 rows.  The expand launch starts while the
-// shrink launch runs and has its first B values in flight before it waits for t.
+// Two launches.  lora_shrink_kernel forms t_i = A_a x_i: one warp per (adapter in use, up to 4 of its
+// rows, 4 ranks, run of pieces of K), the partial sums of the pieces of 512 values kept apart.
+// lora_expand_kernel sums the pieces and adds scale * t_i Bt_a to Y0, 256 columns a warp, for up to 4 (2)
+// rows of an adapter.  Both are bound by the adapters' bytes, which the rows of an item share (rows are
+// matched to adapters by a warp match over the at most 32 ids); an adapter with more rows is read again
+// from L2 by its next item, side by side: 32 rows of one adapter beside 34816 columns 20 us, one item
+// after the other 41.  The expand launch starts while the shrink launch runs and has its first B values in
+// flight before it waits for t.
 //
-// Measured: 32 rows of 32 adapters beside 34816 x 5120, 173 MB: 31.3 us, 5.5 TB/s over both launches;
-// one row beside q, k and v 4.5 us: two launches' chains of dependent loads.
+// Measured: 32 rows of 32 adapters of rank 64 beside 34816 x 5120, 173 MB: 31.8 us, 5.4 TB/s over both
+// launches; the same rows beside q, k and v (7168 columns of 5120, 94 MB) 28.4 us; one row beside q, k and
+// v 4.4 us: two launches' chains of dependent loads.
 #include <cstdint>
 #include <type_traits>
 #include <cuda_runtime.h>
@@ -24,8 +27,10 @@ __device__ unsigned g_status;   // this file's kernels' status word
 
 constexpr int kShrinkWarps = 4;
 constexpr int kRanks = 4;        // ranks of one shrink warp
+constexpr int kShrinkRows = 4;   // rows of one shrink warp (8 rows an adapter, K 17408: 13.0 us; 2: 15.0, 8: 16.4)
 constexpr int kChunk = 512;      // values of K that a shrink warp holds at a time
 constexpr int kPieces = 64;      // pieces of K at most
+constexpr int kResident = 16;    // shrink warps an SM holds
 constexpr int64_t kAhead = 16 << 20;   // bytes of B that the shrink launch asks into L2
 constexpr int kCols = 256;       // columns of one expand warp, 8 a lane
 // The two forms of the expand kernel.  kSplit: 8 warps share the ranks of one block of columns and join
@@ -54,12 +59,16 @@ struct Params {
   const int32_t* ids;
   int count, M, rank_max;
   int rank_groups;   // of kRanks in rank_max
+  int run;           // pieces of K of one shrink warp
 };
 
-// The rows of the g-th distinct adapter of the M ids (in order of first row) as a mask of rows; 0
-// past the last.  All lanes of a warp call this; `id` comes back as that adapter's id, `groups` as the
-// number of distinct ones.
-__device__ __forceinline__ unsigned group_rows(const int32_t* ids, int M, int n_adapters, int g, int& id, int& groups) {
+// The work of item g: the rows of one adapter in use, R at most, as a mask; an adapter with more rows has
+// several items (in the order of their first rows); 0 past the last.  All lanes of a warp call this; `id`
+// comes back as the adapter's id, `groups` as the number of adapters in use, `nth` as the item's place
+// among those of its adapter.
+template <int R>
+__device__ __forceinline__ unsigned item_rows(const int32_t* ids, int M, int n_adapters, int g, int& id, int& groups,
+                                              int& nth) {
   const int lane = threadIdx.x & 31;
   int mine = lane < M ? ids[lane] : -2;
   if (mine >= n_adapters || mine < -2 || (mine == -2 && lane < M)) {
@@ -67,14 +76,15 @@ __device__ __forceinline__ unsigned group_rows(const int32_t* ids, int M, int n_
     mine = -1;
   }
   const unsigned same = __match_any_sync(0xffffffffu, mine);
-  const bool leader = lane < M && (same & ((1u << lane) - 1)) == 0;
-  unsigned leaders = __ballot_sync(0xffffffffu, leader);
-  groups = __popc(leaders);
-  if (g >= groups) return 0;
-  for (int k = 0; k < g; ++k) leaders &= leaders - 1;
-  const int at = __ffs(leaders) - 1;
+  const int before = __popc(same & ((1u << lane) - 1));   // rows of the same adapter
+  groups = __popc(__ballot_sync(0xffffffffu, lane < M && before == 0));
+  unsigned firsts = __ballot_sync(0xffffffffu, lane < M && before % R == 0);
+  if (g >= __popc(firsts)) return 0;
+  for (int k = 0; k < g; ++k) firsts &= firsts - 1;
+  const int at = __ffs(firsts) - 1;
   id = __shfl_sync(0xffffffffu, mine, at);
-  return __shfl_sync(0xffffffffu, same, at);
+  nth = __shfl_sync(0xffffffffu, before / R, at);
+  return __ballot_sync(0xffffffffu, mine == id && before / R == nth);
 }
 
 // Adapter `id` of entry e; rank 0 for none, or for one whose rank or alignment is not allowed.
@@ -99,56 +109,63 @@ __device__ __forceinline__ void unpack8(uint4 v, float (&x)[8]) {
   }
 }
 
-// Grid (rank groups x pieces in units of kShrinkWarps, adapters in use, entries).
+// Grid (rank groups x runs of pieces in units of kShrinkWarps, items, entries).
 __global__ void __launch_bounds__(32 * kShrinkWarps, 4) lora_shrink_kernel(const __grid_constant__ Params P) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const Entry& e = P.e[blockIdx.z];
   const int lane = threadIdx.x & 31;
   const int unit = blockIdx.x * kShrinkWarps + (threadIdx.x >> 5);
-  const int piece = unit / P.rank_groups, r0 = (unit - piece * P.rank_groups) * kRanks;
-  if (piece >= e.pieces) return;
-  int id = -1, groups;
-  const unsigned all = group_rows(P.ids, P.M, e.n_adapters, blockIdx.y, id, groups);
+  const int run = unit / P.rank_groups, r0 = (unit - run * P.rank_groups) * kRanks;
+  const int runs = (e.pieces + P.run - 1) / P.run;
+  if (run >= runs) return;
+  int id = -1, groups, nth;
+  const unsigned all = item_rows<kShrinkRows>(P.ids, P.M, e.n_adapters, blockIdx.y, id, groups, nth);
   if (!all || id < 0) return;
   const qmm_lora_adapter a = adapter_of(e, id, P.rank_max);
   if (r0 >= a.rank) return;
   constexpr int kV = kChunk / 256;   // 16-byte loads of a lane in a chunk
-  for (int chunk = 0; chunk < e.chunks; ++chunk) {
-    const int64_t k0 = ((int64_t)piece * e.chunks + chunk) * kChunk + 8 * lane;
-    if (k0 - 8 * lane >= e.K) break;
-    uint4 raw[kRanks][kV];
+  const int64_t end = min(e.K, (int64_t)(run + 1) * P.run * e.chunks * kChunk);
+  int64_t k0 = (int64_t)run * P.run * e.chunks * kChunk;
+  uint4 raw[kRanks][kV], x[kV];
+  auto ask_a = [&](int64_t from, uint4 (&to)[kRanks][kV]) {
 #pragma unroll
     for (int r = 0; r < kRanks; ++r)
 #pragma unroll
       for (int v = 0; v < kV; ++v) {
-        const bool in = r0 + r < a.rank && k0 + 256 * v < e.K;
-        raw[r][v] = in ? ldg_nc_v4(a.A + (r0 + r) * e.K + k0 + 256 * v) : make_uint4(0u, 0u, 0u, 0u);
+        const bool in = r0 + r < a.rank && from + 256 * v < end;
+        to[r][v] = in ? ldg_nc_v4(a.A + (r0 + r) * e.K + from + 256 * v + 8 * lane) : make_uint4(0u, 0u, 0u, 0u);
       }
-    if (chunk == 0) {
-      // The expand launch's first B towards L2, this warp's share of the adapter's (its units are the live
-      // rank groups by the pieces), so that memory is not idle while t is formed.
-      const int64_t bytes = min((int64_t)a.rank * e.N * 2, kAhead / groups / P.count) & ~(int64_t)127;
-      const int64_t lines = bytes / 128, units = (int64_t)((a.rank + kRanks - 1) / kRanks) * e.pieces;
-      const int64_t mine = ((int64_t)piece * ((a.rank + kRanks - 1) / kRanks) + r0 / kRanks) * 32 + lane;
-      for (int64_t k = mine; k < lines; k += 32 * units)
-        asm volatile("prefetch.global.L2 [%0];" :: "l"(reinterpret_cast<const uint8_t*>(a.Bt) + 128 * k));
-    }
-    // a row's x is asked for while the row before is worked on
-    uint4 x[kV];
-    auto ask = [&](int row) {
+  };
+  auto ask_x = [&](int row, int64_t from) {
 #pragma unroll
-      for (int v = 0; v < kV; ++v)
-        x[v] = k0 + 256 * v < e.K ? *reinterpret_cast<const uint4*>(e.X + row * e.K + k0 + 256 * v) : make_uint4(0u, 0u, 0u, 0u);
-    };
-    ask(__ffs(all) - 1);
+    for (int v = 0; v < kV; ++v)
+      x[v] = from + 256 * v < end ? *reinterpret_cast<const uint4*>(e.X + row * e.K + from + 256 * v + 8 * lane)
+                                  : make_uint4(0u, 0u, 0u, 0u);
+  };
+  const int first = __ffs(all) - 1;
+  ask_a(k0, raw);
+  ask_x(first, k0);
+  if (nth == 0) {
+    // The expand launch's first B towards L2, this warp's share of the adapter's (its units are the live
+    // rank groups by the runs), so that memory is not idle while t is formed.
+    const int live = (a.rank + kRanks - 1) / kRanks;
+    const int64_t bytes = min((int64_t)a.rank * e.N * 2, kAhead / groups / P.count) & ~(int64_t)127;
+    for (int64_t k = ((int64_t)run * live + r0 / kRanks) * 32 + lane; k < bytes / 128; k += 32 * (int64_t)live * runs)
+      asm volatile("prefetch.global.L2 [%0];" :: "l"(reinterpret_cast<const uint8_t*>(a.Bt) + 128 * k));
+  }
+  int piece = run * P.run, part = 0;   // of the piece's chunks
+  for (; k0 < end; k0 += kChunk) {
+    uint4 next[kRanks][kV];   // the next chunk's A and a row's x are asked for while the ones before are worked on
+    if (k0 + kChunk < end) ask_a(k0 + kChunk, next);
     for (unsigned rows = all; rows;) {
       const int row = __ffs(rows) - 1;
       rows &= rows - 1;
       uint4 now[kV];
 #pragma unroll
       for (int v = 0; v < kV; ++v) now[v] = x[v];
-      if (rows) ask(__ffs(rows) - 1);
+      if (rows) ask_x(__ffs(rows) - 1, k0);
+      else if (k0 + kChunk < end) ask_x(first, k0 + kChunk);
       float acc[kRanks] = {};
 #pragma unroll
       for (int v = 0; v < kV; ++v) {
@@ -166,9 +183,18 @@ __global__ void __launch_bounds__(32 * kShrinkWarps, 4) lora_shrink_kernel(const
       const int r = r0 + lane / (32 / kRanks);
       if (lane % (32 / kRanks) == 0 && r < a.rank) {
         float* t = e.t + ((int64_t)piece * P.M + row) * P.rank_max + r;
-        *t = chunk == 0 ? acc[0] : *t + acc[0];
+        *t = part == 0 ? acc[0] : *t + acc[0];
       }
     }
+    if (k0 + kChunk >= end) break;
+    if (++part == e.chunks) {
+      part = 0;
+      ++piece;
+    }
+#pragma unroll
+    for (int r = 0; r < kRanks; ++r)
+#pragma unroll
+      for (int v = 0; v < kV; ++v) raw[r][v] = next[r][v];
   }
 }
 
@@ -252,7 +278,7 @@ __device__ __forceinline__ void accumulate(const qmm_lora_adapter& a, int64_t N,
   }
 }
 
-// One CTA: one block (kSplit) or a block a warp (kStream) of columns for one adapter in use.
+// One CTA: one block (kSplit) or a block a warp (kStream) of columns for one item.
 template <Form FORM, bool WIDE>
 __device__ __forceinline__ void expand(const Params& P, const Entry& e, unsigned rows, const qmm_lora_adapter& a,
                                        int64_t block0, float (*ts)[QMM_LORA_MAX_RANK], float (*part)[rows_of(FORM)][kCols]) {
@@ -270,7 +296,7 @@ __device__ __forceinline__ void expand(const Params& P, const Entry& e, unsigned
   load_b<kStep, WIDE>(a, e.N, n0, r0, r1, lane, first);
   const bool vec = e.N % 8 == 0 && ((reinterpret_cast<uintptr_t>(e.Y) | reinterpret_cast<uintptr_t>(e.Y0)) & 15) == 0;
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  auto work = [&](auto r_) {   // the next R rows (or fewer) of the group
+  auto work = [&](auto r_) {   // R rows or fewer
     constexpr int R = decltype(r_)::value;
     int row[R], m = 0;
 #pragma unroll
@@ -278,12 +304,11 @@ __device__ __forceinline__ void expand(const Params& P, const Entry& e, unsigned
       row[j] = rows ? __ffs(rows) - 1 : row[0];
       if (rows) { rows &= rows - 1; ++m; }
     }
-    float ys[R];   // kSplit: Y0 of the thread's column, asked for ahead of the sums
+    [[maybe_unused]] float ys[R];   // kSplit: Y0 of the thread's column, asked for ahead of the sums
     if constexpr (SPLIT)
 #pragma unroll
       for (int j = 0; j < R; ++j)
         ys[j] = j < m && n0 + threadIdx.x < e.N ? e.Y0[row[j] * e.N + n0 + threadIdx.x] : 0.0f;
-    __syncthreads();   // the rows before are done with ts
     for (int v = threadIdx.x; v < R * a.rank; v += 32 * kWarps) {
       const int j = v / a.rank, r = v - j * a.rank;
       int mine = row[0];
@@ -345,13 +370,11 @@ __device__ __forceinline__ void expand(const Params& P, const Entry& e, unsigned
       }
     }
   };
-  while (rows) {
-    if (__popc(rows) == 1) work(std::integral_constant<int, 1>{});
-    else work(std::integral_constant<int, kRows>{});
-  }
+  if (__popc(rows) == 1) work(std::integral_constant<int, 1>{});
+  else work(std::integral_constant<int, kRows>{});
 }
 
-// Grid (blocks of columns over all entries, adapters in use).
+// Grid (blocks of columns over all entries, items).
 template <Form FORM>
 __global__ void __launch_bounds__(32 * warps_of(FORM), FORM == kSplit ? 2 : 16) lora_expand_kernel(const __grid_constant__ Params P) {
   __shared__ float ts[rows_of(FORM)][QMM_LORA_MAX_RANK];
@@ -360,8 +383,8 @@ __global__ void __launch_bounds__(32 * warps_of(FORM), FORM == kSplit ? 2 : 16) 
   int k = 0;
   while (k + 1 < P.count && (int)blockIdx.x >= P.e[k + 1].first) ++k;
   const Entry& e = P.e[k];
-  int id = -1, groups;
-  const unsigned rows = group_rows(P.ids, P.M, e.n_adapters, blockIdx.y, id, groups);
+  int id = -1, groups, nth;
+  const unsigned rows = item_rows<rows_of(FORM)>(P.ids, P.M, e.n_adapters, blockIdx.y, id, groups, nth);
   if (!rows) return;
   const qmm_lora_adapter a = adapter_of(e, id, P.rank_max);
   const int64_t n0 = (int64_t)(blockIdx.x - e.first) * (FORM == kSplit ? kCols : kCols * warps_of(FORM));
@@ -407,18 +430,18 @@ cudaError_t launch_lora(const qmm_lora_entry* entries, int count, const int32_t*
   P.M = M;
   P.rank_max = rank_max;
   P.rank_groups = (rank_max + kRanks - 1) / kRanks;
-  // kStream where the blocks of columns alone make 16 warps an SM and the rows of an adapter are few (each
-  // two read it again).
+  // kStream where the blocks of columns alone make 16 warps an SM.  With 32 adapters of rank 64: 34816
+  // columns (29 an SM) 32 us, kSplit 51; 7168 columns (6 an SM) 37 us, kSplit 28.
   int64_t warps = 0;
-  int pieces = 0, groups = 1;
+  int pieces = 0, groups = 1;   // groups: adapters in use at most, no adapter among them
   for (int k = 0; k < count; ++k) {
     const qmm_lora_entry& e = entries[k];
-    const int g = e.n_adapters < M ? e.n_adapters + 1 : M;   // adapters in use, and no adapter
+    const int g = e.n_adapters < M ? e.n_adapters + 1 : M;
     groups = groups > g ? groups : g;
     pieces = pieces > pieces_of(e.K) ? pieces : pieces_of(e.K);
     warps += (e.N + kCols - 1) / kCols * g;
   }
-  const bool split = warps < 16 * (int64_t)sm_count() || M > 2 * entries[0].n_adapters;
+  const bool split = warps < 16 * (int64_t)sm_count();
   const int64_t cols = split ? kCols : (int64_t)kCols * warps_of(kStream);
   float* t = static_cast<float*>(workspace);
   int64_t blocks = 0;
@@ -429,11 +452,21 @@ cudaError_t launch_lora(const qmm_lora_entry* entries, int count, const int32_t*
     blocks += (e.N + cols - 1) / cols;
   }
   if (blocks > 0x7fffffff) return cudaErrorInvalidValue;
+  // A warp takes as many pieces as bring the launch into one round of resident warps, with the next
+  // chunk's A in flight (16 adapters of rank 64, 7168 columns of 5120: 15.5 us; a piece a warp 18.7;
+  // half or double the warps 21.3, 16.4).  Each piece keeps its own sum, so the result does not depend on this.
+  const int64_t resident = (int64_t)kResident * sm_count();
+  const int64_t each = (int64_t)P.rank_groups * groups * count;
+  const int64_t fit = resident / each;   // runs
+  P.run = fit >= pieces ? 1 : fit <= 1 ? pieces : (int)((pieces + fit - 1) / fit);
+  const int runs = (pieces + P.run - 1) / P.run;
+  // items of R rows at most: each of the groups has one, and one more for every R rows beside its first
+  auto items = [&](int R) { return (unsigned)(groups + (M - groups) / R); };
   cudaError_t err = launch_early(lora_shrink_kernel,
-                                 dim3((pieces * P.rank_groups + kShrinkWarps - 1) / kShrinkWarps, groups, count),
+                                 dim3((runs * P.rank_groups + kShrinkWarps - 1) / kShrinkWarps, items(kShrinkRows), count),
                                  kShrinkWarps, P, stream);
   if (err != cudaSuccess) return err;
-  const dim3 grid((unsigned)blocks, groups);
+  const dim3 grid((unsigned)blocks, items(split ? rows_of(kSplit) : rows_of(kStream)));
   return split ? launch_early(lora_expand_kernel<kSplit>, grid, warps_of(kSplit), P, stream)
                : launch_early(lora_expand_kernel<kStream>, grid, warps_of(kStream), P, stream);
 }
