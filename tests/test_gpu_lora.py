@@ -144,3 +144,53 @@ def test_ids_change_between_graph_replays(qmm):
         torch.cuda.synchronize()
         for y, y0, a in zip(Y, Y0, adapters):
             check(y, y0, X, now, a)
+
+
+@pytest.mark.parametrize("M,widths,K,ranks,ids", [
+    # wide projections and many adapters in the table: a block of columns to each warp
+    (32, [20480], 256, [5] * 32, [7] * 32),
+    (32, [20481], 256, [1 + k % 7 for k in range(32)], [k // 3 for k in range(32)]),
+    (32, [20483, 264], 512, [9] * 40, [39, 0] * 16),
+    (17, [65544], 256, [4] * 20, [-1] * 3 + [19] * 5 + list(range(9))),
+    # adapters with more rows than a warp takes at a time, in runs that alternate
+    (31, [1032, 8], 17408, [64] * 4, [0, 1, 2, 3, 0, 0, 1] * 4 + [-1, 3, 3]),
+    # warps that take several pieces of K, the last run and the last chunk shorter; chunks in pieces
+    (16, [96, 40, 33], 8960 + 256, [40] * 16, list(range(16))),
+    (24, [72], 33024, [61, 64] * 12, list(range(24))),
+    (32, [24], 66560, [130] * 32, list(range(32))),
+])
+def test_many_rows_and_many_adapters(qmm, M, widths, K, ranks, ids):
+    X, adapters, Y0 = make(M, widths, K, ranks, seed=M + K + 1)
+    Y = [torch.full_like(y, 7.0) for y in Y0]
+    call(qmm, X, adapters, Y0, Y, ids, max(ranks))
+    assert qmm.device_status() == 0
+    for y, y0, a in zip(Y, Y0, adapters):
+        check(y, y0, X, ids, a)
+
+
+def test_rows_do_not_depend_on_the_adapters_in_use(qmm):
+    """A row of a call with many adapters has the bits of the same row alone with its own."""
+    X, adapters, Y0 = make(32, [1000], 8704, [48] * 32, seed=11)
+    Y, one = [torch.empty_like(Y0[0])], [torch.empty_like(Y0[0][:1])]
+    call(qmm, X, adapters, Y0, Y, list(range(32)), 48)
+    for i in (0, 13, 31):
+        call(qmm, X[i:i + 1].clone(), [adapters[0][i:i + 1]], [Y0[0][i:i + 1].clone()], one, [0], 48)
+        assert torch.equal(one[0][0], Y[0][i])
+
+
+def test_a_table_with_a_misaligned_adapter(qmm):
+    """A on an 8-byte boundary in a table built by hand: reported, its rows get Y0."""
+    X, adapters, Y0 = make(3, [256], 512, [8, 8], seed=12)
+    Y = [torch.full_like(Y0[0], 7.0)]
+    table = qmm.make_lora_adapters(adapters[0])
+    raw = torch.zeros(8 * 512 + 4, dtype=BF16, device="cuda")
+    host = table.cpu()
+    host.view(torch.int64)[host.numel() // 16] = raw.data_ptr() + 8   # the second adapter's first word
+    table.copy_(host)
+    entries = qmm.make_lora_entries([(table, X, Y0[0], Y[0], 256, 512)])
+    ws = torch.empty(qmm.lora_workspace_bytes(entries, 3, 8), dtype=torch.uint8, device="cuda")
+    qmm.run_lora(entries, torch.tensor([0, 1, 0], dtype=torch.int32, device="cuda"), 3, 8, ws)
+    torch.cuda.synchronize()
+    assert qmm.device_status() == 4
+    check(Y[0][[0, 2]], Y0[0][[0, 2]], X[[0, 2]], [0, 0], adapters[0])
+    assert torch.equal(Y[0][1], Y0[0][1])
