@@ -441,7 +441,8 @@ cudaError_t launch_lora(const qmm_lora_entry* entries, int count, const int32_t*
     pieces = pieces > pieces_of(e.K) ? pieces : pieces_of(e.K);
     warps += (e.N + kCols - 1) / kCols * g;
   }
-  const bool split = warps < 16 * (int64_t)sm_count();
+  const int64_t sms = sm_count();
+  const bool split = warps < 16 * sms;
   const int64_t cols = split ? kCols : (int64_t)kCols * warps_of(kStream);
   float* t = static_cast<float*>(workspace);
   int64_t blocks = 0;
@@ -455,7 +456,7 @@ cudaError_t launch_lora(const qmm_lora_entry* entries, int count, const int32_t*
   // A warp takes as many pieces as bring the launch into one round of resident warps, with the next
   // chunk's A in flight (16 adapters of rank 64, 7168 columns of 5120: 15.5 us; a piece a warp 18.7;
   // half or double the warps 21.3, 16.4).  Each piece keeps its own sum, so the result does not depend on this.
-  const int64_t resident = (int64_t)kResident * sm_count();
+  const int64_t resident = kResident * sms;
   const int64_t each = (int64_t)P.rank_groups * groups * count;
   const int64_t fit = resident / each;   // runs
   P.run = fit >= pieces ? 1 : fit <= 1 ? pieces : (int)((pieces + fit - 1) / fit);
