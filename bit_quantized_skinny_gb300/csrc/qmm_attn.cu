@@ -625,7 +625,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
       const int live = min(P.tokens, g.rows - tok0) * G;          // rows of the tile in use
       const int tok = tok0 + row / G;
       const int sees = g.own ? clampi(g.first_keys + tok, 0, g.keys) : g.keys;
-      const int clean_from = g.own ? clampi(g.first_keys + tok0, 0, g.keys) : g.keys;   // keys that not every row sees
+      // Keys that not every row of the block sees.  The same ones for both lanes, also where each has a row
+      // tile and they share the value tiles: whichever takes a value out first, the other one's product
+      // follows its own pass over the same values, and what it may still write is what is there already.
+      const int clean_from = g.own ? clampi(g.first_keys, 0, g.keys) : g.keys;
       const bool idle = (warp % kLaneWarps) * 32 >= live;
       ++segs;
       items += pair ? 2 * n : n;

@@ -159,6 +159,33 @@ def test_later_rows_values_do_not_reach_earlier_rows(qmm, D, dtype):
     assert bool((err <= (u * O[10:12].abs() + (u + 2.0 ** -11) * S[10:12])[rest]).all())
 
 
+@pytest.mark.parametrize("D,dtype,special", [(128, F16, math.inf), (128, BF16, -math.inf), (64, F16, math.nan)])
+def test_an_early_draft_value_in_a_block_of_two_row_tiles(qmm, D, dtype, special):
+    """An infinity or NaN in the value of the fifth of 40 drafted rows, whose key is far below the others in
+    score (its weight is 0 in 16 bits): the rows of both row tiles that see it get it, whichever lane takes
+    it out of the tile they share, and every call gives the same bits."""
+    c = Case([40], [150], 70, 5, 1, D, 16, dtype=dtype)          # 25 rows a tile
+    c.Q = c.Q.abs()
+    at = int(c.pages[0, 114 // 16]) * 16 + 114 % 16
+    c.K[at] = -8.0                                               # score about -8 * 1.2 * sqrt(D): below -70
+    c.V[at, 0, 3] = special
+    c.run(qmm)
+    assert bool(c.O[4:, :, 3].isnan().all() if math.isnan(special) else (c.O[4:, :, 3] == special).all())
+    rest = [d for d in range(D) if d != 3]
+    O, lse, S = c.plain()
+    u = plain.UNIT[dtype]
+    err = (c.O.double() - O).abs()
+    ok = err <= u * O.abs() + (u + 2.0 ** -11) * S + 2.0 ** -24
+    assert bool(ok[:, :, rest].all()) and bool(ok[:4].all())
+    first = c.O.clone()
+    args, ws = c.args(qmm), torch.empty(qmm.attn_workspace_bytes(c.args(qmm)), dtype=torch.uint8, device="cuda")
+    for _ in range(200):
+        c.O.fill_(3.0)
+        qmm.attn_shared(args, ws)
+        assert torch.equal(c.O.view(torch.int16), first.view(torch.int16))
+    assert qmm.device_status() == 0
+
+
 def test_large_and_equal_scores(qmm):
     """Scores near the exponential's range: one key far above the rest, and all keys equal."""
     c = Case([2, 2], [300, 300], 500, 4, 2, 128, 32)
