@@ -28,16 +28,18 @@ struct Params {
   int parts;   // CTAs of one row
 };
 
-// 8 values of in_type at p as fp32.
+// 8 values of in_type at p as fp32.  Plain loads throughout this kernel: it starts while the kernel ahead
+// may still be writing these buffers, so they are not read-only for its lifetime, and only a load that
+// is not taken for invariant stays behind the wait for that kernel.
 template <int IN>
 __device__ __forceinline__ void load8(const void* base, int64_t at, float (&x)[8]) {
   if constexpr (IN == QMM_F32) {
     const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(base) + at);
-    const float4 u = __ldg(p), v = __ldg(p + 1);
+    const float4 u = p[0], v = p[1];
     x[0] = u.x; x[1] = u.y; x[2] = u.z; x[3] = u.w;
     x[4] = v.x; x[5] = v.y; x[6] = v.z; x[7] = v.w;
   } else {
-    const uint4 u = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(base) + at));
+    const uint4 u = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(base) + at);
     const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
@@ -119,8 +121,8 @@ __global__ void __launch_bounds__(kThreads, AHEAD == 2 ? 16 : 0) norm_rope_kerne
     if (a.interleaved) {
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
-        c[2 * k] = c[2 * k + 1] = __ldg(row + 4 * l + k);
-        s[2 * k + 1] = __ldg(row + half + 4 * l + k);
+        c[2 * k] = c[2 * k + 1] = row[4 * l + k];
+        s[2 * k + 1] = row[half + 4 * l + k];
         s[2 * k] = -s[2 * k + 1];
       }
     } else {

@@ -1,0 +1,21 @@
+"""CPU test of the kernels that start while the launch ahead of them still runs (programmatic dependent
+launch): what that launch may be writing is read with loads that stay behind the wait for it.  A load
+marked read-only for the kernel's lifetime (__ldg, ld.global.nc) may be taken for invariant and moved
+ahead, and the memory is not read-only for that long."""
+import os
+import re
+
+import pytest
+
+CSRC = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "bit_quantized_skinny_gb300", "csrc")
+
+
+@pytest.mark.parametrize("source,forbidden", [
+    ("qmm_norm_rope.cu", r"__ldg\(|\.nc\b|ldg_nc"),      # Q, K, V, positions, slots, weights and table
+])
+def test_loads_stay_behind_the_wait(source, forbidden):
+    with open(os.path.join(CSRC, source), encoding="utf-8") as fh:
+        code = re.sub(r"//[^\n]*", "", fh.read())
+    assert "griddepcontrol.wait" in code
+    found = [line.strip() for line in code.split("\n") if re.search(forbidden, line)]
+    assert not found, found

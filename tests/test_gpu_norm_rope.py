@@ -139,3 +139,45 @@ def test_other_stream_and_graph(qmm):
     graph.replay()
     torch.cuda.synchronize()
     check(out, *plain.norm_rope(Q, None, 1e-6, cs, pos, False), D)
+
+
+def test_behind_the_launch_that_writes_its_inputs(qmm):
+    """Call after call behind adapters that write q, k and v in place, with nothing between them: the bits
+    of the same calls one at a time."""
+    T, Hq, Hk, D, width = 32, 40, 8, 128, 512
+    g = torch.Generator(device="cuda").manual_seed(9)
+    rnd = lambda *s: torch.randn(*s, generator=g, device="cuda")
+    widths = [Hq * D, Hk * D, Hk * D]
+    X = [rnd(T, width).to(BF16) for _ in range(8)]
+    adapters = [[((rnd(16, width) * width ** -0.5).to(BF16), rnd(16, N).to(BF16), 1.0) for _ in range(4)] for N in widths]
+    tables = [qmm.make_lora_adapters(a) for a in adapters]
+    y0, y = [rnd(T, N) for N in widths], [torch.empty(T, N, device="cuda") for N in widths]
+    ids = torch.arange(T, dtype=torch.int32, device="cuda") % 4
+    cs, pos = table(256, D), torch.arange(T, dtype=torch.int32, device="cuda")
+    slots = torch.arange(T, device="cuda")
+    calls = []
+    for x in X:
+        entries = qmm.make_lora_entries([(t, x, a, b, N, width) for t, a, b, N in zip(tables, y0, y, widths)])
+        out = torch.zeros(T, Hq, D, dtype=BF16, device="cuda")
+        Kc, Vc = (torch.zeros(T, Hk, D, dtype=BF16, device="cuda") for _ in range(2))
+        args = qmm.make_norm_rope(y[0].view(T, Hq, D), y[1].view(T, Hk, D), y[2].view(T, Hk, D), None, None, cs, pos, slots,
+                                  out, Kc, Vc)
+        calls.append((entries, args, (out, Kc, Vc)))
+    ws = torch.empty(qmm.lora_workspace_bytes(calls[0][0], T, 16), dtype=torch.uint8, device="cuda")
+    want = []
+    for entries, args, outs in calls:
+        qmm.run_lora(entries, ids, T, 16, ws)
+        torch.cuda.synchronize()
+        qmm.norm_rope(args)
+        torch.cuda.synchronize()
+        want.append([t.clone() for t in outs])
+    for _ in range(20):
+        for _, _, outs in calls:
+            for t in outs:
+                t.zero_()
+        for entries, args, _ in calls:
+            qmm.run_lora(entries, ids, T, 16, ws)
+            qmm.norm_rope(args)
+        for w, (_, _, outs) in zip(want, calls):
+            assert all(torch.equal(a, b) for a, b in zip(w, outs))
+    assert qmm.device_status() == 0
