@@ -181,3 +181,34 @@ def test_behind_the_launch_that_writes_its_inputs(qmm):
         for w, (_, _, outs) in zip(want, calls):
             assert all(torch.equal(a, b) for a, b in zip(w, outs))
     assert qmm.device_status() == 0
+
+
+@pytest.mark.parametrize("T,Hq,Hk,D,rot,interleaved,src,dst", [
+    # more than 2048 fp32 rows: two heads at a time; heads that leave the last step half or all but empty
+    (2049, 13, 3, 64, 32, False, F32, BF16),
+    (2050, 5, 1, 64, 64, True, F32, F16),
+    (4099, 7, 1, 128, 128, False, F32, BF16),
+    (2301, 9, 2, 128, 48, True, F32, F16),
+    (2111, 3, 2, 256, 256, False, F32, F16),
+    (2051, 2, 1, 256, 64, True, F32, BF16),
+    # as many rows of 16 bits: one head at a time
+    (4099, 7, 1, 128, 128, True, BF16, BF16),
+])
+def test_many_rows_against_the_formula(qmm, T, Hq, Hk, D, rot, interleaved, src, dst):
+    test_against_the_formula(qmm, T, Hq, Hk, D, rot, interleaved, src, dst)
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_many_rows_without_values_or_rotation(qmm, D):
+    T, Hq, Hk = 2500, 5, 2
+    Q, K = torch.randn(T, Hq, D, device="cuda"), torch.randn(T, Hk, D, device="cuda")
+    out, Kc = torch.empty(T, Hq, D, dtype=BF16, device="cuda"), torch.full((T + 1, Hk, D), 5.0, dtype=BF16, device="cuda")
+    slots = torch.randperm(T + 1, device="cuda")[:T].clone()
+    slots[::7] = -1
+    qmm.norm_rope(qmm.make_norm_rope(Q, K, None, None, None, None, None, slots, out, Kc, None))
+    check(out, *plain.norm_rope(Q, None, 1e-6, None, None, False), D)
+    live = slots >= 0
+    check(Kc[slots[live]], *(v[live] for v in plain.norm_rope(K, None, 1e-6, None, None, False)), D)
+    rest = torch.ones(T + 1, dtype=torch.bool, device="cuda")
+    rest[slots[live]] = False
+    assert bool((Kc[rest] == 5.0).all())
