@@ -205,6 +205,15 @@ __device__ __forceinline__ uint4 ldg_nc_v4(const void* p) {
   return v;
 }
 
+// 16-byte global load that does not allocate in L1, of memory that the launch ahead may have been writing
+// when this one started: not marked read-only, and volatile, so that it stays behind the wait for it.
+__device__ __forceinline__ uint4 ld_v4(const void* p) {
+  uint4 v;
+  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+  return v;
+}
+
 // ---------------------------------------------------------------- warp butterfly ---------
 // v[0..V) per lane (V a power of two <= 32).  Afterwards lane l holds, in v[0], the sum over
 // all 32 lanes of value index l / (32/V).  The additions form the same tree for every index

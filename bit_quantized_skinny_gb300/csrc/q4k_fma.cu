@@ -166,7 +166,7 @@ q4k_fma_kernel(const __grid_constant__ FmaParams<MAXE> P) {
           if (lane_valid && i0 + i < P.M) {
             const uint16_t* xr = E.X + (int64_t)(i0 + i) * E.K + k0;
 #pragma unroll
-            for (int g = 0; g < 4; ++g) v[g] = ldg_nc_v4(xr + 8 * g);
+            for (int g = 0; g < 4; ++g) v[g] = ld_v4(xr + 8 * g);
           } else {
 #pragma unroll
             for (int g = 0; g < 4; ++g) v[g] = make_uint4(0, 0, 0, 0);

@@ -11,6 +11,7 @@ CSRC = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))),
 
 
 @pytest.mark.parametrize("source,forbidden", [
+    ("q4k_fma.cu", r"__ldg\(|ldg_nc_v4\(xr|\.nc\b"),          # X
     ("qmm_norm_rope.cu", r"__ldg\(|\.nc\b|ldg_nc"),      # Q, K, V, positions, slots, weights and table
 ])
 def test_loads_stay_behind_the_wait(source, forbidden):
