@@ -100,6 +100,13 @@ __device__ __forceinline__ qmm_lora_adapter adapter_of(const Entry& e, int id, i
   return a;
 }
 
+// A word that the shrink launch wrote, from L2.  volatile: behind the wait for that launch.
+__device__ __forceinline__ float ld_cg(const float* p) {
+  float v;
+  asm volatile("ld.global.cg.f32 %0, [%1];" : "=f"(v) : "l"(p));
+  return v;
+}
+
 __device__ __forceinline__ void unpack8(uint4 v, float (&x)[8]) {
   const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
@@ -320,7 +327,7 @@ __device__ __forceinline__ void expand(const Params& P, const Entry& e, unsigned
       for (int p0 = 0; j < m && p0 < e.pieces; p0 += kTogether) {
         float x[kTogether];
 #pragma unroll
-        for (int p = 0; p < kTogether; ++p) x[p] = p0 + p < e.pieces ? __ldcg(t + (int64_t)(p0 + p) * P.M * P.rank_max) : 0.0f;
+        for (int p = 0; p < kTogether; ++p) x[p] = p0 + p < e.pieces ? ld_cg(t + (int64_t)(p0 + p) * P.M * P.rank_max) : 0.0f;
 #pragma unroll
         for (int p = 0; p < kTogether; ++p) s += x[p];
       }
