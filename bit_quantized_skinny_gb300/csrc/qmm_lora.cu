@@ -10,7 +10,7 @@
 // after the other 41.  The expand launch starts while the shrink launch runs and has its first B values in
 // flight before it waits for t.
 //
-// Measured: 32 rows of 32 adapters of rank 64 beside 34816 x 5120, 173 MB: 31.8 us, 5.4 TB/s over both
+// Measured: 32 rows of 32 adapters of rank 64 beside 34816 x 5120, 173 MB: 32.4 us, 5.3 TB/s over both
 // launches; the same rows beside q, k and v (7168 columns of 5120, 94 MB) 28.4 us; one row beside q, k and
 // v 4.4 us: two launches' chains of dependent loads.
 #include <cstdint>
@@ -38,9 +38,15 @@ constexpr int kCols = 256;       // columns of one expand warp, 8 a lane
 // each of 2 warps, up to 2 rows together, few enough registers that every warp of 32 adapters
 // beside 34816 columns is resident at once (28.6 an SM; in CTAs of 8 warps the last ones waited for a
 // second round: 45 us, not 37).
+// In both, and on every boundary, a value is the sum of its ranks in shares (share_of), each share summed in
+// order and the shares added up in order: its bits depend on K and the adapter's rank, not on
+// the form, the batch, the table or where Bt lies.  (Two sums a value in kStream: 32 adapters beside 34816
+// columns 32.4 us, one sum 32.0; shares of 4 instead of 8 ranks where a row of Bt is aligned: 32 of rank 32
+// beside 5120 columns 12.8 us, 12.2.)
 enum Form { kSplit, kStream };
 __host__ __device__ constexpr int warps_of(Form f) { return f == kSplit ? 8 : 2; }
 __host__ __device__ constexpr int rows_of(Form f) { return f == kSplit ? 4 : 2; }
+__host__ __device__ constexpr int share_of(int rank) { return (rank + 31) / 32 * 4; }   // ranks of one of 8 sums
 __host__ __device__ constexpr int step_of(Form f, bool wide) { return f == kSplit && wide ? 8 : 4; }   // ranks loaded together
 
 struct Entry {
@@ -256,12 +262,14 @@ __device__ __forceinline__ void load_b(const qmm_lora_adapter& a, int64_t N, int
   }
 }
 
-// acc[j][c] += sum over ranks [r0, r1) of ts[j][r] Bt[r][column c] for R rows; `b` holds the first
-// STEP ranks' values already.
-template <int R, int STEP, bool WIDE>
-__device__ __forceinline__ void accumulate(const qmm_lora_adapter& a, int64_t N, int64_t n0, int r0, int r1, int lane,
-                                           const float (*ts)[QMM_LORA_MAX_RANK], const uint4 (&first)[STEP],
+// acc[j][c] = sum over ranks [r0, r1) of ts[j][r] Bt[r][column c] for R rows: in one sum, or (SHARES) a sum
+// for each `share` ranks and those added up in order.  `first` holds the first STEP ranks' values already.
+template <int R, int STEP, bool WIDE, bool SHARES>
+__device__ __forceinline__ void accumulate(const qmm_lora_adapter& a, int64_t N, int64_t n0, int r0, int r1, int share,
+                                           int lane, const float (*ts)[QMM_LORA_MAX_RANK], const uint4 (&first)[STEP],
                                            float (&acc)[R][8]) {
+  [[maybe_unused]] float total[R][8] = {};
+  [[maybe_unused]] int left = share;
   uint4 b[STEP];
 #pragma unroll
   for (int q = 0; q < STEP; ++q) b[q] = first[q];
@@ -280,9 +288,27 @@ __device__ __forceinline__ void accumulate(const qmm_lora_adapter& a, int64_t N,
         for (int c = 0; c < 8; ++c) acc[j][c] = __fmaf_rn(x[c], t, acc[j][c]);
       }
     }
+    if constexpr (SHARES) {
+      left -= STEP;
+      if (left == 0 || r + STEP >= r1) {
+        left = share;
+#pragma unroll
+        for (int j = 0; j < R; ++j)
+#pragma unroll
+          for (int c = 0; c < 8; ++c) {
+            total[j][c] += acc[j][c];
+            acc[j][c] = 0.0f;
+          }
+      }
+    }
 #pragma unroll
     for (int q = 0; q < STEP; ++q) b[q] = ahead[q];
   }
+  if constexpr (SHARES)
+#pragma unroll
+    for (int j = 0; j < R; ++j)
+#pragma unroll
+      for (int c = 0; c < 8; ++c) acc[j][c] = total[j][c];
 }
 
 // One CTA: one block (kSplit) or a block a warp (kStream) of columns for one item.
@@ -293,9 +319,9 @@ __device__ __forceinline__ void expand(const Params& P, const Entry& e, unsigned
   constexpr int kWarps = warps_of(FORM), kRows = rows_of(FORM), kStep = step_of(FORM, WIDE);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int64_t n0 = SPLIT ? block0 : block0 + kCols * warp;
+  const int share = share_of(a.rank);
   int r0 = 0, r1 = a.rank;
-  if constexpr (SPLIT) {   // an equal share of the ranks, in steps
-    const int share = (a.rank + kStep * kWarps - 1) / (kStep * kWarps) * kStep;
+  if constexpr (SPLIT) {   // a share a warp
     r0 = min(a.rank, warp * share);
     r1 = min(a.rank, r0 + share);
   }
@@ -341,7 +367,7 @@ __device__ __forceinline__ void expand(const Params& P, const Entry& e, unsigned
       y0[0] = *reinterpret_cast<const float4*>(e.Y0 + row[0] * e.N + n0 + 8 * lane);
       y0[1] = *reinterpret_cast<const float4*>(e.Y0 + row[0] * e.N + n0 + 8 * lane + 4);
     }
-    accumulate<R, kStep, WIDE>(a, e.N, n0, r0, r1, lane, ts, first, acc);
+    accumulate<R, kStep, WIDE, !SPLIT>(a, e.N, n0, r0, r1, share, lane, ts, first, acc);
     if constexpr (SPLIT) {
 #pragma unroll
       for (int j = 0; j < R; ++j)

@@ -468,7 +468,8 @@ qmm_status qmm_attn_shared(const qmm_attn_args* args_host, void* workspace_dev, 
  *     Y[i] = Y0[i] + scale_a * B_a (A_a x_i),   a = ids_dev[i]   (Y[i] = Y0[i] for ids[i] = -1)
  * for the M rows of X and each of `count` projections that share the rows' ids (q, k and v of a
  * layer in one call).  Y0 is the projection's own result (qmm_run), Y may be the same buffer.
- * Sums are fp32 throughout, in an order that depends on the shapes only.
+ * Sums are fp32 throughout, in an order that K and the adapter's rank give: a row's bits depend on
+ * neither the other rows, nor the table's size, nor where Bt lies.
  *   entries_host: count entries, 1 <= count <= QMM_LORA_MAX_ENTRIES.  adapters: device table of
  *   n_adapters adapters of that projection (qmm_lora_adapter: A rank x K and Bt rank x N bf16,
  *   row-major, Bt being B transposed; A 16-byte aligned, Bt 2-byte).  X: M x K bf16, Y0 and Y: M x N

@@ -194,3 +194,32 @@ def test_a_table_with_a_misaligned_adapter(qmm):
     assert qmm.device_status() == 4
     check(Y[0][[0, 2]], Y0[0][[0, 2]], X[[0, 2]], [0, 0], adapters[0])
     assert torch.equal(Y[0][1], Y0[0][1])
+
+
+@pytest.mark.parametrize("N,K,rank", [(512, 512, 16), (520, 1280, 72), (1000, 768, 32), (264, 512, 200)])
+def test_bits_do_not_depend_on_where_bt_lies(qmm, N, K, rank):
+    """The same adapter with Bt on 16-byte and on 2-byte boundaries."""
+    X, adapters, Y0 = make(3, [N], K, [rank], seed=13)
+    A, Bt, scale = adapters[0][0]
+    Y = [torch.empty_like(Y0[0])]
+    call(qmm, X, [[(A, Bt, scale)]], Y0, Y, [0, -1, 0], rank)
+    for shift in (1, 4, 7):
+        raw = torch.empty(rank * N + shift, dtype=BF16, device="cuda")
+        raw[shift:] = Bt.reshape(-1)
+        other = [torch.empty_like(Y0[0])]
+        call(qmm, X, [[(A, raw[shift:].view(rank, N), scale)]], Y0, other, [0, -1, 0], rank)
+        assert torch.equal(other[0], Y[0])
+
+
+def test_bits_do_not_depend_on_table_batch_or_form(qmm):
+    """A row beside a wide projection: alone (the ranks shared by warps), and among 32 rows with a table of 40
+    adapters (a block of columns to each warp)."""
+    N, K = 20480, 512
+    X, adapters, Y0 = make(32, [N], K, [72] * 4 + [9] * 36, seed=14)
+    ids = [0, 1, 2, 3, 0, 0] + list(range(4, 30))
+    Y, one = [torch.empty_like(Y0[0])], [torch.empty_like(Y0[0][:1])]
+    call(qmm, X, adapters, Y0, Y, ids, 72)
+    check(Y[0], Y0[0], X, ids, adapters[0])
+    for i in (0, 3, 5, 17):
+        call(qmm, X[i:i + 1].clone(), [adapters[0][ids[i]:ids[i] + 1]], [Y0[0][i:i + 1].clone()], one, [0], 72)
+        assert torch.equal(one[0][0], Y[0][i])
