@@ -495,26 +495,46 @@ def attn_shared(args, workspace, stream=None) -> None:
 
 def make_lora_adapters(items):
     """Device table of one projection's adapters.  items: sequence of (A, Bt, scale) with bf16 CUDA
-    tensors A rank x K and Bt rank x N (B transposed), both contiguous; they must outlive the table."""
+    tensors A rank x K and Bt rank x N (B transposed), both contiguous, K and N those of the projection.
+    The tensors are kept alive by what is returned."""
     import torch
+    if not items:
+        raise QmmError(8, "make_lora_adapters")
     arr = (_LoraAdapter * len(items))()
+    first = items[0][0], items[0][1]
     for k, (A, Bt, scale) in enumerate(items):
-        if A.shape[0] != Bt.shape[0]:
+        if A.dim() != 2 or Bt.dim() != 2 or A.shape[0] != Bt.shape[0]:
             raise QmmError(2, "make_lora_adapters")
+        if A.shape[1] != first[0].shape[1] or Bt.shape[1] != first[1].shape[1]:
+            raise QmmError(2, "make_lora_adapters: adapters of different projections")
         arr[k] = _LoraAdapter(_dense(A, torch.bfloat16, "A"), _dense(Bt, torch.bfloat16, "Bt"), scale, A.shape[0])
         if (arr[k].A or 0) % 16:
             raise QmmError(4, "make_lora_adapters")
-    return torch.frombuffer(bytearray(bytes(arr)), dtype=torch.uint8).to(items[0][0].device)
+    table = torch.frombuffer(bytearray(bytes(arr)), dtype=torch.uint8).to(first[0].device)
+    table.lora_shape = first[1].shape[1], first[0].shape[1]   # N, K, for make_lora_entries()
+    table._keep = tuple(items)
+    return table
 
 
 def make_lora_entries(items):
     """items: sequence of (adapters, X, Y0, Y, N, K): the table of make_lora_adapters(), X bf16 M x K, Y0
-    and Y fp32 M x N (they may be one tensor).  The tensors are kept alive by what is returned."""
+    and Y fp32 M x N (they may be one tensor), all contiguous.  The tensors are kept alive by what is
+    returned."""
+    import torch
     arr = (_LoraEntry * len(items))()
     for k, (table, X, Y0, Y, N, K) in enumerate(items):
-        arr[k] = _LoraEntry(table.data_ptr(), table.numel() // ctypes.sizeof(_LoraAdapter), X.data_ptr(),
-                            Y0.data_ptr(), Y.data_ptr(), N, K)
+        if getattr(table, "lora_shape", (N, K)) != (N, K):
+            raise QmmError(2, "make_lora_entries: adapters of another projection")
+        if X.dim() != 2 or X.shape[1] != K:
+            raise QmmError(2, "X")
+        for t, name in ((Y0, "Y0"), (Y, "Y")):
+            if t.dim() != 2 or t.shape[0] != X.shape[0] or t.shape[1] != N:
+                raise QmmError(2, name)
+        arr[k] = _LoraEntry(_dense(table, torch.uint8, "adapters"), table.numel() // ctypes.sizeof(_LoraAdapter),
+                            _dense(X, torch.bfloat16, "X"), _dense(Y0, torch.float32, "Y0"), _dense(Y, torch.float32, "Y"),
+                            N, K)
     arr._keep = tuple(items)
+    arr._rows, arr._ids_type = min((item[1].shape[0] for item in items), default=0), torch.int32   # for run_lora()
     return arr
 
 
@@ -526,6 +546,10 @@ def run_lora(entries, ids, M: int, rank_max: int, workspace, stream=None) -> Non
     """qmm_run_lora: Y[i] = Y0[i] + scale * B (A x_i) with the adapter ids[i] (int32 device tensor, -1:
     none) for each projection of `entries` (make_lora_entries()).  rank_max: at least every rank in
     use; `workspace`: a device tensor of >= lora_workspace_bytes(entries, M, rank_max) bytes."""
+    if ids.dtype is not entries._ids_type:
+        raise QmmError(12, "ids")
+    if M > entries._rows or ids.numel() < M or not ids.is_contiguous():
+        raise QmmError(2, "run_lora: M rows, M dense ids")
     _check(load().qmm_run_lora(entries, len(entries), ids.data_ptr(), M, rank_max, workspace.data_ptr(),
                                workspace.numel() * workspace.element_size(), _stream_handle(stream)), "qmm_run_lora")
 

@@ -134,3 +134,35 @@ def test_python_checks(qmm):
                 dict(O=Q), dict(K_cache=K.half()), dict(lse=torch.zeros(2, 3))):
         with pytest.raises(qmm.QmmError):
             qmm.make_attn(**dict(kw, **bad))
+
+
+def test_python_checks_of_adapters(qmm):
+    """What the adapters' calls read through raw pointers has the type, shape and layout that they take."""
+    import torch
+    bf16 = torch.bfloat16
+    A, Bt = torch.zeros(8, 512, dtype=bf16), torch.zeros(8, 40, dtype=bf16)
+    table = qmm.make_lora_adapters([(A, Bt, 1.0), (A[:3], Bt[:3], 0.5)])
+    assert table.numel() == 2 * ctypes.sizeof(qmm._LoraAdapter)
+    for bad in ([], [(A[:4], Bt, 1.0)], [(A.float(), Bt, 1.0)], [(A, Bt.half(), 1.0)], [(A[:, ::2], Bt, 1.0)],
+                [(A, Bt.T.contiguous().T, 1.0)], [(A, Bt, 1.0), (A, torch.zeros(8, 48, dtype=bf16), 1.0)],
+                [(A, Bt, 1.0), (torch.zeros(8, 256, dtype=bf16), Bt, 1.0)], [(A[0], Bt[0], 1.0)]):
+        with pytest.raises(qmm.QmmError):
+            qmm.make_lora_adapters(bad)
+    X, Y = torch.zeros(4, 512, dtype=bf16), torch.zeros(4, 40)
+    good = dict(adapters=table, X=X, Y0=Y, Y=Y, N=40, K=512)
+    entries = qmm.make_lora_entries([tuple(good.values())])
+    for bad in (dict(X=X.float()), dict(X=X[:, :256]), dict(X=torch.zeros(512, 4, dtype=bf16).T), dict(Y0=Y.half()),
+                dict(Y=Y[:3]), dict(Y=torch.zeros(4, 41)), dict(Y0=torch.zeros(40, 4).T), dict(N=48), dict(K=256),
+                dict(adapters=table.view(torch.int64)), dict(X=X[0])):
+        with pytest.raises(qmm.QmmError):
+            qmm.make_lora_entries([tuple(dict(good, **bad).values())])
+    # an adapter's widths are those of its projection, also where X and Y fit another one
+    with pytest.raises(qmm.QmmError):
+        qmm.make_lora_entries([(table, X[:, :256].contiguous(), Y, Y, 40, 256)])
+    ws = torch.zeros(1 << 16, dtype=torch.uint8)
+    i32 = torch.zeros(4, dtype=torch.int32)
+    for bad in (dict(ids=i32.long()), dict(ids=i32[:3]), dict(ids=torch.zeros(8, dtype=torch.int32)[::2]),
+                dict(ids=torch.zeros(5, dtype=torch.int32), M=5)):
+        kw = dict(dict(ids=i32, M=4), **bad)
+        with pytest.raises(qmm.QmmError):
+            qmm.run_lora(entries, kw["ids"], kw["M"], 8, ws, stream=0)
