@@ -420,6 +420,8 @@ def make_norm_rope(Q, K, V, q_weight, k_weight, cos_sin, positions, slots, Q_out
     for t, cache, name in ((K, K_cache, "K"), (V, V_cache, "V")):
         if t is None:
             continue
+        if cache is None:
+            raise QmmError(1, name + "_cache")
         if tuple(t.shape) != (T, a.Hk, D) or cache.shape[1:] != (a.Hk, D):
             raise QmmError(2, name)
         if t.dtype != Q.dtype:
@@ -459,6 +461,8 @@ def make_attn(Q, K_cache, V_cache, page_size: int, prefix_pages, prefix_len: int
     kv_lens int32 B, row_starts int32 B + 1; lse fp32 T x Hq or None.  The tensors are kept alive by
     what is returned."""
     import torch
+    if any(t is None for t in (K_cache, V_cache, pages, kv_lens, row_starts, O)):
+        raise QmmError(1, "make_attn")
     T, Hq, D = Q.shape
     n_slots, Hk, Dk = K_cache.shape
     B, per_stream = pages.shape

@@ -166,3 +166,21 @@ def test_python_checks_of_adapters(qmm):
         kw = dict(dict(ids=i32, M=4), **bad)
         with pytest.raises(qmm.QmmError):
             qmm.run_lora(entries, kw["ids"], kw["M"], 8, ws, stream=0)
+
+
+def test_python_checks_of_missing_tensors(qmm):
+    import torch
+    bf16, i32 = torch.bfloat16, lambda *v: torch.tensor(v, dtype=torch.int32)
+    Q, K, out, cache = torch.zeros(2, 4, 64), torch.zeros(2, 1, 64), torch.zeros(2, 4, 64, dtype=bf16), torch.zeros(16, 1, 64, dtype=bf16)
+    kw = dict(Q=Q, K=K, V=K, q_weight=None, k_weight=None, cos_sin=None, positions=None, slots=torch.arange(2), Q_out=out,
+              K_cache=cache, V_cache=cache.clone())
+    qmm.make_norm_rope(**kw)
+    for name in ("K_cache", "V_cache"):
+        with pytest.raises(qmm.QmmError):
+            qmm.make_norm_rope(**dict(kw, **{name: None}))
+    kw = dict(Q=out, K_cache=cache, V_cache=cache, page_size=16, prefix_pages=None, prefix_len=0, pages=i32(0)[None],
+              kv_lens=i32(3), row_starts=i32(0, 2), O=out.clone(), scale=0.1)
+    qmm.make_attn(**kw)
+    for name in ("K_cache", "V_cache", "pages", "kv_lens", "row_starts", "O"):
+        with pytest.raises(qmm.QmmError):
+            qmm.make_attn(**dict(kw, **{name: None}))
