@@ -89,6 +89,7 @@
 #include <cuda_fp16.h>
 
 #include "q4k_device.cuh"
+#include "q4k_device_once.h"
 #include "q4k_formats.cuh"
 #include "q4k_internal.h"
 #include "q4k_tcgen05.cuh"
@@ -1566,15 +1567,14 @@ cudaError_t weight_map(const void* W, int64_t N, int64_t K, int fmt, CUtensorMap
 
 template <int FMT, int MPAD, int MT, int MAXE, bool GATED, int NG>
 cudaError_t set_smem_attr() {
-  static bool done[64] = {};
+  static DeviceOnce once;
   int dev = 0;
-  cudaError_t err = cudaGetDevice(&dev);
+  const cudaError_t err = cudaGetDevice(&dev);
   if (err != cudaSuccess) return err;
-  if (dev >= 0 && dev < 64 && done[dev]) return cudaSuccess;
-  err = cudaFuncSetAttribute(q4k_tc_kernel<FMT, MPAD, MT, MAXE, GATED, NG>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             TcSmem<MPAD, FMT, MT, NG>::kTotal);
-  if (err == cudaSuccess && dev >= 0 && dev < 64) done[dev] = true;
-  return err;
+  return once.run(dev, cudaSuccess, [] {
+    return cudaFuncSetAttribute(q4k_tc_kernel<FMT, MPAD, MT, MAXE, GATED, NG>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                TcSmem<MPAD, FMT, MT, NG>::kTotal);
+  });
 }
 
 // One instance of the kernel: its shared memory attribute, block size and launch.

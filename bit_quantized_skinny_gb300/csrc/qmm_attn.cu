@@ -44,6 +44,7 @@
 #include <cuda_runtime.h>
 
 #include "q4k_device.cuh"
+#include "q4k_device_once.h"
 #include "q4k_internal.h"
 #include "q4k_tcgen05.cuh"
 
@@ -1075,13 +1076,13 @@ bool tensor_map(CUtensorMap* m, const void* p, int D, int H, int64_t n, int64_t 
 
 template <int D, int TYPE>
 cudaError_t set_smem_attr() {
-  static bool done[64] = {};
+  static DeviceOnce once;
   int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess || (dev < 64 && done[dev])) return e;
-  e = cudaFuncSetAttribute(attn_kernel<D, TYPE>, cudaFuncAttributeMaxDynamicSharedMemorySize, Smem<D>::kTotal);
-  if (e == cudaSuccess && dev < 64) done[dev] = true;
-  return e;
+  const cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  return once.run(dev, cudaSuccess, [] {
+    return cudaFuncSetAttribute(attn_kernel<D, TYPE>, cudaFuncAttributeMaxDynamicSharedMemorySize, Smem<D>::kTotal);
+  });
 }
 
 template <int D, int TYPE>
