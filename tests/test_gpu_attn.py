@@ -349,3 +349,20 @@ def test_concurrent_streams(qmm):
             qmm.attn_shared(x, w, stream=st)
     torch.cuda.synchronize()
     assert torch.equal(a.O, want[0]) and torch.equal(b.O, want[1]) and qmm.device_status() == 0
+
+
+@pytest.mark.parametrize("rows,lens,prefix,Hq,Hk,D,page,dtype", [
+    # prompts: many blocks of rows, whose last keys differ, behind a prefix and without one
+    ([1500], [2100], 513, 10, 2, 128, 64, BF16),
+    ([700, 900], [700, 1300], 0, 3, 3, 64, 128, F16),
+    ([333], [5000], 0, 64, 1, 128, 256, BF16),
+    # more rows than four warps each take in the combine launch, each with many pieces to join
+    ([5] * 8, [40 + 9 * k for k in range(8)], 9000, 40, 8, 128, 64, BF16),
+    ([4] * 20, [1500 + 70 * k for k in range(20)], 6000, 20, 2, 64, 16, F16),
+])
+def test_long_streams_against_the_formula(qmm, rows, lens, prefix, Hq, Hk, D, page, dtype):
+    c = Case(rows, lens, prefix, Hq, Hk, D, page, dtype).run(qmm)
+    c.check()
+    first = c.O.clone()
+    assert torch.equal(c.run(qmm).O, first)
+    assert qmm.device_status() == 0
