@@ -105,3 +105,54 @@ def test_chain_of_verify_passes(qmm, oracle_lib):
         torch.cuda.synchronize()
         check(lens, *before)
     assert qmm.device_status() == 0
+
+
+def test_a_full_verify_pass(qmm, oracle_lib):
+    """4 requests of 8 drafted rows with an adapter each, 8 query heads to a key/value head: 32 rows are two row
+    tiles for the prefix.  Per row, the root mean square of the error is at most 2^-5 of the row's (the bound
+    above), and no value is off by more than four of those (a bell curve's 16384 values)."""
+    from bit_quantized_skinny_gb300.attention_half import AttentionHalf
+
+    width, Hq, Hk, D, page, prefix, B, m = 512, 16, 2, 128, 32, 700, 4, 8
+    T = B * m
+    shape = {"q": (Hq * D, width), "k": (Hk * D, width), "v": (Hk * D, width), "o": (width, Hq * D)}
+    g = torch.Generator(device="cuda").manual_seed(6)
+    rnd = lambda *s: torch.randn(*s, generator=g, device="cuda")
+    packed = {n: oracle_lib.pack(inputs.weights_f32(N, K, 60 + k)) for k, (n, (N, K)) in enumerate(shape.items())}
+    dense = {n: torch.from_numpy(oracle_lib.dequant(packed[n], *shape[n])).cuda().double() for n in shape}
+    items = {n: [((rnd(r, K) * K ** -0.5).to(BF16), (0.2 * rnd(r, N)).to(BF16), 1.0) for r in (16, 64, 8, 33)]
+             for n, (N, K) in shape.items()}
+    lens, starts = [8, 40, 130, 95], [0, 8, 16, 24, 32]
+    n_pages = 80
+    order = torch.randperm(n_pages, generator=g, device="cuda").int()
+    prefix_pages, own = order[:22].contiguous(), order[22:62].view(B, 10).contiguous()
+    Kc, Vc = (rnd(n_pages * page, Hk, D).to(BF16) for _ in range(2))
+    q_norm, k_norm = 1 + 0.1 * rnd(D), 1 + 0.1 * rnd(D)
+    inv = 10000.0 ** (-torch.arange(0, D, 2, dtype=torch.float64, device="cuda") / D)
+    angle = torch.arange(1024, dtype=torch.float64, device="cuda")[:, None] * inv
+    cos_sin = torch.cat([angle.cos(), angle.sin()], 1).float().contiguous()
+    half = AttentionHalf({n: torch.from_numpy(p).cuda() for n, p in packed.items()}, width, Hq, Hk, D, T, B, Kc, Vc, page, 10,
+                         q_norm, k_norm, cos_sin, prefix_pages, prefix,
+                         adapters={n: qmm.make_lora_adapters(v) for n, v in items.items()}, rank_max=64)
+    ids = [t // m for t in range(T)]
+    own_at = [lens[t // m] - m + t % m for t in range(T)]
+    half.ids.copy_(torch.tensor(ids))
+    half.pages.copy_(own)
+    half.row_starts.copy_(torch.tensor(starts))
+    half.kv_lens.copy_(torch.tensor(lens))
+    half.positions.copy_(torch.tensor([prefix + j for j in own_at]))
+    half.slots.copy_(torch.tensor([int(own[t // m, j // page]) * page + j % page for t, j in enumerate(own_at)]))
+    half.X.copy_(rnd(T, width))
+    Kp, Vp = Kc.double(), Vc.double()
+    half.run()
+    torch.cuda.synchronize()
+    assert qmm.device_status() == 0
+    X = half.X.double()
+    y = {n: plain.lora(half.X, X @ dense[n].T, ids, items[n])[0] for n in "qkv"}
+    q, _ = plain.norm_rope(y["q"].view(T, Hq, D), q_norm, 1e-6, cos_sin, half.positions, False)
+    k, _ = plain.norm_rope(y["k"].view(T, Hk, D), k_norm, 1e-6, cos_sin, half.positions, False)
+    Kp[half.slots], Vp[half.slots] = k, y["v"].view(T, Hk, D)
+    O, _, _ = plain.attention(q, Kp, Vp, page, prefix_pages, prefix, own, lens, starts, D ** -0.5)
+    want, _ = plain.lora(O.view(T, Hq * D), O.view(T, Hq * D) @ dense["o"].T, ids, items["o"])
+    err = (half.Y.double() - want).abs() / want.square().mean(-1, keepdim=True).sqrt()
+    assert bool((err.square().mean(-1).sqrt() <= 2.0 ** -5).all()) and err.max().item() <= 2.0 ** -3
