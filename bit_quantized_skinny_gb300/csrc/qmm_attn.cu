@@ -1126,9 +1126,11 @@ cudaError_t launch(const qmm_attn_args& a, void* workspace, cudaStream_t stream)
   cfg.gridDim = dim3(a.T, (a.Hq + kCombineWarps - 1) / kCombineWarps);
   cfg.blockDim = dim3(32 * kCombineWarps);
   cfg.dynamicSmemBytes = 0;
-  // Four warps share a row's records where one warp a row is nine an SM at most (1280 rows of 21 records:
-  // the call takes 43.7 us, 46.3 with one; 1824 rows of a few: 21.1, 18.5 with one).
-  if ((int64_t)a.T * a.Hq <= 9 * sms) {
+  // Four warps share a row's records where all of their CTAs, three an SM, run at once; with more rows, one
+  // warp a row.  The limit shows at any number of records.  Behind 32768 shared keys, some 19 records a row:
+  // 800 rows 35.7 us (one warp a row 37.5), 960 rows 38.4 (37.8), 1280 rows 44.5 (43.7).  Behind 8192: 800 rows
+  // 26.8 (27.0), 960 rows 31.4 (29.0).  640 rows of 8 streams' own 3000 to 6000 keys 15.0 (17.4).
+  if ((int64_t)a.T * a.Hq * 4 <= 3 * kCombineWarps * (int64_t)sms) {
     cfg.gridDim.y = (a.Hq * 4 + kCombineWarps - 1) / kCombineWarps;
     return cudaLaunchKernelEx(&cfg, attn_combine_kernel<D, TYPE, 4>, P);
   }
