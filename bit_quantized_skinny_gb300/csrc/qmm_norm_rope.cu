@@ -202,12 +202,20 @@ cudaError_t launch_ahead(const qmm_norm_rope_args& a, cudaStream_t stream) {
   return cudaLaunchKernelEx(&cfg, norm_rope_kernel<D, IN, OUT, AHEAD>, P);
 }
 
-// Two heads at a time for many fp32 rows (16384 rows: 104 us, one at a time 109; 1500 rows: 17.0, one 15.9);
-// one at a time for few rows and for 16-bit ones, which are bound by instructions.
+// Two heads at a time for many fp32 rows, unless a group's last pair would stand half empty after few pairs:
+// a row's heads take `steps` of a CTA's groups.  Heads of 128: 16384 rows of 56 heads (14 steps) 104 us, one at
+// a time 114; 3000 rows 25.6 (28.0); 1024 rows 10.7 (10.2); 16384 rows of 8 heads (2) 29.2 (30.7).  Heads of 64:
+// 24000 rows of 56 (7) 81 (87); 2049 rows of 24 (3) 5.1 (4.5), 16384 rows 33.0 (32.3).  Heads of 256: 4000
+// rows of 10 (5) 15.4 (14.6).  Rows of 16 bits take one at a time (16384 rows of 56 heads of 128 117 us, two
+// 124; 2311 rows of 30 heads of 64 5.8, 6.3): twice the instructions a byte, which fill half the issue slots,
+// and the waits for loads between them (two would gain 5 to 7 % with 8 heads a row).
 template <int D, int IN, int OUT>
 cudaError_t launch(const qmm_norm_rope_args& a, cudaStream_t stream) {
-  if constexpr (IN == QMM_F32)
-    if (a.T > 2048) return launch_ahead<D, IN, OUT, 2>(a, stream);
+  if constexpr (IN == QMM_F32) {
+    constexpr int kGroups = kThreads / (D / 8);
+    const int steps = (a.Hq + (a.V ? 2 : 1) * a.Hk + kGroups - 1) / kGroups;
+    if (a.T > 2048 && (steps % 2 == 0 || steps >= 7)) return launch_ahead<D, IN, OUT, 2>(a, stream);
+  }
   return launch_ahead<D, IN, OUT, 1>(a, stream);
 }
 

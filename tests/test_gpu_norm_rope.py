@@ -212,3 +212,15 @@ def test_many_rows_without_values_or_rotation(qmm, D):
     rest = torch.ones(T + 1, dtype=torch.bool, device="cuda")
     rest[slots[live]] = False
     assert bool((Kc[rest] == 5.0).all())
+
+
+@pytest.mark.parametrize("T,Hq,Hk,D,rot,interleaved,dst", [
+    # heads that fill an even number of steps, the last one partly; seven steps, the last pair half empty
+    (2049, 9, 3, 64, 64, False, BF16),
+    (2050, 45, 2, 64, 16, True, F16),
+    (2111, 21, 2, 128, 128, True, BF16),
+    (2053, 5, 1, 128, 64, False, F16),
+    (2049, 9, 2, 256, 128, False, BF16),
+])
+def test_many_rows_in_pairs_of_heads(qmm, T, Hq, Hk, D, rot, interleaved, dst):
+    test_against_the_formula(qmm, T, Hq, Hk, D, rot, interleaved, F32, dst)
