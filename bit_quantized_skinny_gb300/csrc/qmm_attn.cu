@@ -29,12 +29,14 @@
 // non-finite values among the keys that only some rows of the block see (a draft's last keys);
 // attn_combine_kernel then adds those back, from the cache, to the rows that see them.
 //
-// Measured (heads of 128, bf16, 40 query and 8 key/value heads; the SM clock at 2070 MHz): 4 streams of
-// 8 rows over 32768 shared keys 42 us, the keys and values at 5.8 TB/s while they stream, the rest the
-// start, the pieces' sums through memory and the combine launch; 64 streams of 16 rows over the same
-// keys 565 us, 1.24 PFLOP/s: held by the tensor cores' reads of shared memory (a score product of 64
-// keys takes 48 clocks where its arithmetic takes 32; without any softmax the kernel takes 496 us).  One
-// row 10.8 us: start, first copies, combine, nothing but latency.
+// Measured (heads of 128, bf16, 40 query and 8 key/value heads; graph replays, the SM clock sampled at 2070
+// MHz): 4 streams of 8 rows over 32768 shared keys 42 us, the keys and values at 5.8 TB/s while they stream,
+// the rest the start, the pieces' sums through memory and the combine launch.  64 streams of 16 rows over the
+// same keys 560 to 565 us, 1.25 PFLOP/s; 580 in runs so long that the power cap takes the clock to 1995 MHz.
+// Its products take 354 us of that by their own rates (a score product of 64 keys 48 clocks where its
+// arithmetic takes 32, Q being read from shared memory for each; a value product 64); without any softmax the
+// kernel takes 496 us, and what holds it between the two has not been found.  A prompt of 4096 rows over
+// its 8192 own keys 446 us, 1.16 PFLOP/s.  One row 10.8 us: start, first copies, combine, nothing but latency.
 #include <cstdint>
 #include <type_traits>
 #include <cuda.h>

@@ -425,6 +425,9 @@ qmm_status qmm_norm_rope(const qmm_norm_rope_args* args_host, cudaStream_t strea
  * A row that sees no key gets O = 0 and lse = -inf, and so does a row of Q behind
  * row_starts[B] (padding).  The prefix's keys are read once for all streams, not once each.
  * Cache slots that no row may see are never part of a result, whatever they hold.
+ * An infinity or NaN in a value that a row sees makes that value of its O infinite or NaN.  An infinity whose
+ * weight rounds to 0 in `type` gives an infinity where the kernel works on the row beside an earlier one that
+ * does not see it, and NaN (0 times infinity) elsewhere.
  *   Q, O: T rows of Hq x D, type `type` (QMM_BF16 or QMM_F16, as the caches), ldq, ldo elements
  *   between rows.  lse: T x Hq fp32, or NULL.
  *   prefix_pages: device, ceil(prefix_len / page_size) page numbers.  pages: device, B rows of
