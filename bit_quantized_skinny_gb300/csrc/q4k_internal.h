@@ -97,10 +97,20 @@ cudaError_t read_and_clear_norm_rope_status(unsigned* out);
 cudaError_t launch_attn(const qmm_attn_args& a, void* workspace, cudaStream_t stream);
 size_t attn_workspace_bytes(const qmm_attn_args& a);
 cudaError_t read_and_clear_attn_status(unsigned* out);
+cudaError_t launch_norm_rope_fp4(const qmm_norm_rope_fp4_args& a, cudaStream_t stream);
+cudaError_t launch_kv_fp4_read(const qmm_kv_fp4_read_args& a, cudaStream_t stream);
+cudaError_t read_and_clear_kv_fp4_status(unsigned* out);
+cudaError_t launch_attn_fp4(const qmm_attn_fp4_args& a, void* workspace, cudaStream_t stream);
+size_t attn_fp4_workspace_bytes(const qmm_attn_fp4_args& a);
+cudaError_t read_and_clear_attn_fp4_status(unsigned* out);
 cudaError_t launch_lora(const qmm_lora_entry* entries, int count, const int32_t* ids, int M, int rank_max,
                         void* workspace, cudaStream_t stream);
 size_t lora_workspace_bytes(const qmm_lora_entry* entries, int count, int M, int rank_max);
 cudaError_t read_and_clear_lora_status(unsigned* out);
+
+// Tokens from logits (argument struct of the C ABI, checked by the caller).
+cudaError_t launch_sample(const qmm_sample_args& a, cudaStream_t stream);
+cudaError_t read_and_clear_sample_status(unsigned* out);
 
 // Host packers (qmm_pack.cpp).  Return 0, or 6 on non-finite input / fp16 overflow.
 int pack_q4k(const float* W, int64_t N, int64_t K, uint8_t* out, int threads);

@@ -51,6 +51,48 @@ qmm_status check_attn_shape(const qmm_attn_args& a) {
   return half_type(a.type) ? QMM_OK : QMM_ERR_TYPE;
 }
 
+bool valid_page(int n) { return n >= 16 && n <= 4096 && (n & (n - 1)) == 0; }
+// A tensor scale of a 4-bit cache: its products with every E4M3 value, and their reciprocals, are ordinary fp32 numbers.
+bool valid_scale(float s) { return s >= 0x1p-60f && s <= 0x1p60f; }
+
+// What a qmm_norm_rope call may not be, for either cache; QMM_OK for a call without rows as well.
+qmm_status check_norm_rope(const qmm_norm_rope_args& a) {
+  if (a.T < 0 || a.Hq < 1 || a.Hk < 0 || a.Hq > 65535 || a.Hk > 32767 || a.Hq + 2 * a.Hk > 65535) return QMM_ERR_SHAPE;
+  if (a.D != 64 && a.D != 128 && a.D != 256) return QMM_ERR_SHAPE;
+  if (a.rot < 0 || a.rot > a.D || a.rot % 16 != 0) return QMM_ERR_SHAPE;
+  if (!valid_dtype(a.in_type) || !half_type(a.out_type)) return QMM_ERR_TYPE;
+  if (a.T == 0) return QMM_OK;
+  const bool keys = a.Hk > 0, values = keys && a.V;
+  if (!a.Q || !a.Q_out || (keys && (!a.K || !a.K_cache || !a.slots)) || (values && !a.V_cache)) return QMM_ERR_NULL;
+  if (a.rot > 0 && (!a.cos_sin || !a.positions)) return QMM_ERR_NULL;
+  if (a.rot > 0 && a.max_pos < 1) return QMM_ERR_SHAPE;
+  const int64_t wq = (int64_t)a.Hq * a.D, wk = (int64_t)a.Hk * a.D;
+  if (a.ldq < wq || a.ldqo < wq || (keys && (a.ldk < wk || a.n_slots < 1)) || (values && a.ldv < wk)) return QMM_ERR_SHAPE;
+  const int64_t in_step = a.in_type == QMM_F32 ? 4 : 8;   // elements in 16 bytes
+  if (!aligned(a.Q, 16) || !aligned(a.Q_out, 16) || !aligned(a.q_weight, 16) || a.ldq % in_step || a.ldqo % 8)
+    return QMM_ERR_ALIGN;
+  if (keys && (!aligned(a.K, 16) || !aligned(a.K_cache, 16) || !aligned(a.k_weight, 16) || !aligned(a.slots, 8) ||
+               a.ldk % in_step))
+    return QMM_ERR_ALIGN;
+  if (values && (!aligned(a.V, 16) || !aligned(a.V_cache, 16) || a.ldv % in_step)) return QMM_ERR_ALIGN;
+  if (a.rot > 0 && (!aligned(a.cos_sin, 16) || !aligned(a.positions, 4))) return QMM_ERR_ALIGN;
+  return QMM_OK;
+}
+
+// The pointers of an attention call with rows, for either cache.
+qmm_status check_attn_pointers(const qmm_attn_args& a, const void* workspace_dev) {
+  if (!a.Q || !a.O || !a.K_cache || !a.V_cache || !a.row_starts || !workspace_dev) return QMM_ERR_NULL;
+  if ((a.prefix_len > 0 && !a.prefix_pages) || (a.B > 0 && (!a.kv_lens || (a.pages_per_stream > 0 && !a.pages))))
+    return QMM_ERR_NULL;
+  if (!aligned(a.Q, 16) || !aligned(a.O, 16) || !aligned(a.K_cache, 16) || !aligned(a.V_cache, 16) || a.ldq % 8 ||
+      a.ldo % 8 || !aligned(workspace_dev, 16))
+    return QMM_ERR_ALIGN;
+  if (!aligned(a.prefix_pages, 4) || !aligned(a.pages, 4) || !aligned(a.kv_lens, 4) || !aligned(a.row_starts, 4) ||
+      !aligned(a.lse, 4))
+    return QMM_ERR_ALIGN;
+  return QMM_OK;
+}
+
 bool valid_format(int fmt) { return fmt >= QMM_FMT_Q4K && fmt <= QMM_FMT_Q6K; }
 
 qmm_status check_job(const void* W, int64_t N, int64_t K, const uint16_t* X, const float* Y) {
@@ -408,27 +450,42 @@ int qmm_select_variant_batched(const qmm_entry* entries_host, int count, int M) 
 
 qmm_status qmm_norm_rope(const qmm_norm_rope_args* args_host, cudaStream_t stream) {
   if (!args_host) return QMM_ERR_NULL;
-  const qmm_norm_rope_args& a = *args_host;
-  if (a.T < 0 || a.Hq < 1 || a.Hk < 0 || a.Hq > 65535 || a.Hk > 32767 || a.Hq + 2 * a.Hk > 65535) return QMM_ERR_SHAPE;
-  if (a.D != 64 && a.D != 128 && a.D != 256) return QMM_ERR_SHAPE;
-  if (a.rot < 0 || a.rot > a.D || a.rot % 16 != 0) return QMM_ERR_SHAPE;
-  if (!valid_dtype(a.in_type) || !half_type(a.out_type)) return QMM_ERR_TYPE;
-  if (a.T == 0) return QMM_OK;
-  const bool keys = a.Hk > 0, values = keys && a.V;
-  if (!a.Q || !a.Q_out || (keys && (!a.K || !a.K_cache || !a.slots)) || (values && !a.V_cache)) return QMM_ERR_NULL;
-  if (a.rot > 0 && (!a.cos_sin || !a.positions)) return QMM_ERR_NULL;
-  if (a.rot > 0 && a.max_pos < 1) return QMM_ERR_SHAPE;
-  const int64_t wq = (int64_t)a.Hq * a.D, wk = (int64_t)a.Hk * a.D;
-  if (a.ldq < wq || a.ldqo < wq || (keys && (a.ldk < wk || a.n_slots < 1)) || (values && a.ldv < wk)) return QMM_ERR_SHAPE;
-  const int64_t in_step = a.in_type == QMM_F32 ? 4 : 8;   // elements in 16 bytes
-  if (!aligned(a.Q, 16) || !aligned(a.Q_out, 16) || !aligned(a.q_weight, 16) || a.ldq % in_step || a.ldqo % 8)
+  const qmm_status s = check_norm_rope(*args_host);
+  if (s != QMM_OK || args_host->T == 0) return s;
+  const cudaError_t e = q4k::launch_norm_rope(*args_host, stream);
+  return e == cudaSuccess ? QMM_OK : cuda_fail(e);
+}
+
+size_t qmm_kv_fp4_bytes(int64_t n_slots, int Hk, int D) {
+  if (n_slots < 1 || n_slots >= (int64_t(1) << 40) || Hk < 1 || Hk > 32767 || (D != 64 && D != 128 && D != 256)) return 0;
+  return (size_t)n_slots * Hk * (D / 2 + D / 16);
+}
+
+qmm_status qmm_norm_rope_fp4(const qmm_norm_rope_fp4_args* args_host, cudaStream_t stream) {
+  if (!args_host) return QMM_ERR_NULL;
+  const qmm_norm_rope_fp4_args& a = *args_host;
+  if (!valid_page(a.page_size) || !valid_scale(a.k_scale) || !valid_scale(a.v_scale)) return QMM_ERR_SHAPE;
+  const qmm_status s = check_norm_rope(a.base);
+  if (s != QMM_OK || a.base.T == 0) return s;
+  if (a.base.Hk > 0 && (a.base.n_slots % a.page_size || a.base.n_slots >= (int64_t(1) << 40))) return QMM_ERR_SHAPE;
+  const cudaError_t e = q4k::launch_norm_rope_fp4(a, stream);
+  return e == cudaSuccess ? QMM_OK : cuda_fail(e);
+}
+
+qmm_status qmm_kv_fp4_read(const qmm_kv_fp4_read_args* args_host, cudaStream_t stream) {
+  if (!args_host) return QMM_ERR_NULL;
+  const qmm_kv_fp4_read_args& a = *args_host;
+  if (!valid_page(a.page_size) || !valid_scale(a.k_scale) || !valid_scale(a.v_scale)) return QMM_ERR_SHAPE;
+  if (qmm_kv_fp4_bytes(a.n_slots, a.Hk, a.D) == 0 || a.n_slots % a.page_size || a.n < 0) return QMM_ERR_SHAPE;
+  if (!a.slots && a.n > a.n_slots) return QMM_ERR_SHAPE;
+  if (a.n >= (int64_t(1) << 40) || a.n * a.Hk >= (int64_t(1) << 43) / a.D) return QMM_ERR_SHAPE;
+  if (!valid_dtype(a.out_type)) return QMM_ERR_TYPE;
+  if (a.n == 0) return QMM_OK;
+  if (!a.K_cache || !a.K_out || !a.V_cache != !a.V_out) return QMM_ERR_NULL;
+  if (!aligned(a.K_cache, 16) || !aligned(a.V_cache, 16) || !aligned(a.K_out, 16) || !aligned(a.V_out, 16) ||
+      !aligned(a.slots, 8))
     return QMM_ERR_ALIGN;
-  if (keys && (!aligned(a.K, 16) || !aligned(a.K_cache, 16) || !aligned(a.k_weight, 16) || !aligned(a.slots, 8) ||
-               a.ldk % in_step))
-    return QMM_ERR_ALIGN;
-  if (values && (!aligned(a.V, 16) || !aligned(a.V_cache, 16) || a.ldv % in_step)) return QMM_ERR_ALIGN;
-  if (a.rot > 0 && (!aligned(a.cos_sin, 16) || !aligned(a.positions, 4))) return QMM_ERR_ALIGN;
-  const cudaError_t e = q4k::launch_norm_rope(a, stream);
+  const cudaError_t e = q4k::launch_kv_fp4_read(a, stream);
   return e == cudaSuccess ? QMM_OK : cuda_fail(e);
 }
 
@@ -441,20 +498,33 @@ qmm_status qmm_attn_shared(const qmm_attn_args* args_host, void* workspace_dev, 
                            cudaStream_t stream) {
   if (!args_host) return QMM_ERR_NULL;
   const qmm_attn_args& a = *args_host;
-  const qmm_status s = check_attn_shape(a);
+  qmm_status s = check_attn_shape(a);
+  if (s != QMM_OK || a.T == 0) return s;
+  s = check_attn_pointers(a, workspace_dev);
   if (s != QMM_OK) return s;
-  if (a.T == 0) return QMM_OK;
-  if (!a.Q || !a.O || !a.K_cache || !a.V_cache || !a.row_starts || !workspace_dev) return QMM_ERR_NULL;
-  if ((a.prefix_len > 0 && !a.prefix_pages) || (a.B > 0 && (!a.kv_lens || (a.pages_per_stream > 0 && !a.pages))))
-    return QMM_ERR_NULL;
-  if (!aligned(a.Q, 16) || !aligned(a.O, 16) || !aligned(a.K_cache, 16) || !aligned(a.V_cache, 16) || a.ldq % 8 ||
-      a.ldo % 8 || !aligned(workspace_dev, 16))
-    return QMM_ERR_ALIGN;
-  if (!aligned(a.prefix_pages, 4) || !aligned(a.pages, 4) || !aligned(a.kv_lens, 4) || !aligned(a.row_starts, 4) ||
-      !aligned(a.lse, 4))
-    return QMM_ERR_ALIGN;
   if (workspace_bytes < q4k::attn_workspace_bytes(a)) return QMM_ERR_BUFSIZE;
   const cudaError_t e = q4k::launch_attn(a, workspace_dev, stream);
+  return e == cudaSuccess ? QMM_OK : cuda_fail(e);
+}
+
+size_t qmm_attn_fp4_workspace_bytes(const qmm_attn_fp4_args* args_host) {
+  if (!args_host || check_attn_shape(args_host->base) != QMM_OK) return 0;
+  if (!valid_scale(args_host->k_scale) || !valid_scale(args_host->v_scale)) return 0;
+  return q4k::attn_fp4_workspace_bytes(*args_host);
+}
+
+qmm_status qmm_attn_shared_fp4(const qmm_attn_fp4_args* args_host, void* workspace_dev, size_t workspace_bytes,
+                               cudaStream_t stream) {
+  if (!args_host) return QMM_ERR_NULL;
+  const qmm_attn_fp4_args& a = *args_host;
+  qmm_status s = check_attn_shape(a.base);
+  if (s != QMM_OK) return s;
+  if (!valid_scale(a.k_scale) || !valid_scale(a.v_scale)) return QMM_ERR_SHAPE;
+  if (a.base.T == 0) return QMM_OK;
+  s = check_attn_pointers(a.base, workspace_dev);
+  if (s != QMM_OK) return s;
+  if (workspace_bytes < q4k::attn_fp4_workspace_bytes(a)) return QMM_ERR_BUFSIZE;
+  const cudaError_t e = q4k::launch_attn_fp4(a, workspace_dev, stream);
   return e == cudaSuccess ? QMM_OK : cuda_fail(e);
 }
 
@@ -487,6 +557,26 @@ qmm_status qmm_run_lora(const qmm_lora_entry* entries_host, int count, const int
   return e == cudaSuccess ? QMM_OK : cuda_fail(e);
 }
 
+qmm_status qmm_sample(const qmm_sample_args* args_host, cudaStream_t stream) {
+  if (!args_host) return QMM_ERR_NULL;
+  const qmm_sample_args& a = *args_host;
+  if (a.T < 0 || a.T > QMM_SAMPLE_MAX_ROWS || a.V < 1 || a.V > QMM_SAMPLE_MAX_V || a.B < 0 || a.B > QMM_ATTN_MAX_STREAMS)
+    return QMM_ERR_SHAPE;
+  if (a.T > 0 && (a.ld < a.V || a.ld >= (int64_t(1) << 40))) return QMM_ERR_SHAPE;
+  if (!valid_dtype(a.type)) return QMM_ERR_TYPE;
+  if (a.T > 0 && (!a.logits || !a.uniform || !a.tokens)) return QMM_ERR_NULL;
+  if (a.B > 0 && (!a.row_starts || !a.accepted || !a.next || (a.T > 0 && !a.fed))) return QMM_ERR_NULL;
+  if (!aligned(a.logits, a.type == QMM_F32 ? 4 : 2)) return QMM_ERR_ALIGN;
+  if (!aligned(a.temperature, 4) || !aligned(a.top_k, 4) || !aligned(a.top_p, 4) || !aligned(a.min_p, 4) ||
+      !aligned(a.uniform, 4) || !aligned(a.tokens, 4) || !aligned(a.logprobs, 4))
+    return QMM_ERR_ALIGN;
+  if (a.B > 0 && (!aligned(a.row_starts, 4) || !aligned(a.fed, 4) || !aligned(a.accepted, 4) || !aligned(a.next, 4)))
+    return QMM_ERR_ALIGN;
+  if (a.T == 0 && a.B == 0) return QMM_OK;
+  const cudaError_t e = q4k::launch_sample(a, stream);
+  return e == cudaSuccess ? QMM_OK : cuda_fail(e);
+}
+
 size_t qmm_stream_read_sink_words(void) {
   const int g = q4k::stream_read_grid();
   return g > 0 ? (size_t)g : 0;
@@ -511,14 +601,17 @@ size_t qmm_workspace_bytes_held(void) { return q4k::workspace_bytes_held(); }
 
 qmm_status qmm_device_status(unsigned* status_out) {
   if (!status_out) return QMM_ERR_NULL;
-  unsigned a = 0, b = 0, c = 0, d = 0, f = 0, g = 0;
+  unsigned a = 0, b = 0, c = 0, d = 0, f = 0, g = 0, h = 0, i = 0, j = 0;
   cudaError_t e = q4k::read_and_clear_fma_status(&a);
   if (e == cudaSuccess) e = q4k::read_and_clear_tc_status(&b);
   if (e == cudaSuccess) e = q4k::read_and_clear_pack_status(&c);
   if (e == cudaSuccess) e = q4k::read_and_clear_norm_rope_status(&d);
   if (e == cudaSuccess) e = q4k::read_and_clear_attn_status(&f);
   if (e == cudaSuccess) e = q4k::read_and_clear_lora_status(&g);
-  *status_out = a | b | c | d | f | g;
+  if (e == cudaSuccess) e = q4k::read_and_clear_kv_fp4_status(&h);
+  if (e == cudaSuccess) e = q4k::read_and_clear_attn_fp4_status(&i);
+  if (e == cudaSuccess) e = q4k::read_and_clear_sample_status(&j);
+  *status_out = a | b | c | d | f | g | h | i | j;
   return e == cudaSuccess ? QMM_OK : cuda_fail(e);
 }
 

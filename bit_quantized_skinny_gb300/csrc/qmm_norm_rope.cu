@@ -9,12 +9,19 @@
 // ones in flight while it works on these, the first ones while the row's position and slot arrive: the
 // kernel is bound by the bytes it reads and writes (16384 rows of 40 + 16 heads of 128, fp32 to bf16:
 // 104 us, 6.9 TB/s; without the loads ahead 144 us).
+//
+// Into a 4-bit cache (qmm_norm_rope_fp4) a block of 16 values is two neighbouring lanes, and the codes are
+// those of the formulas in real numbers, rounded to fp32 where the definition says so: a code is a step of
+// a third of the value, and it must not hang on the order of a sum.  The fp32 arithmetic knows its error;
+// where a border of a code or of a scale lies within it (one head of some thousand), the head is computed
+// again in 64 bits.
 #include <cstdint>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
 #include "q4k_internal.h"
+#include "q4k_kv_fp4.cuh"
 
 namespace q4k {
 namespace {
@@ -26,6 +33,8 @@ constexpr int kThreads = 64;
 struct Params {
   qmm_norm_rope_args a;
   int parts;   // CTAs of one row
+  int page_size, page_shift;   // of a 4-bit cache, and its tensors' scales
+  float k_scale, v_scale;
 };
 
 // 8 values of in_type at p as fp32.  Plain loads throughout this kernel: it starts while the kernel ahead
@@ -71,10 +80,101 @@ __device__ __forceinline__ void store8(void* base, int64_t at, const float (&y)[
   *reinterpret_cast<uint4*>(static_cast<uint16_t*>(base) + at) = make_uint4(w[0], w[1], w[2], w[3]);
 }
 
+// The largest bits of |y| over a block: of two lanes' eight values each.  An infinity or NaN has more than
+// any finite value.
+__device__ __forceinline__ uint32_t block_top(const float (&y)[8]) {
+  uint32_t top = 0;
+#pragma unroll
+  for (int k = 0; k < 8; ++k) top = max(top, __float_as_uint(y[k]) & 0x7FFFFFFFu);
+  return max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+}
+
+// Bit 0 of every nibble whose magnitude is 0.
+__device__ __forceinline__ uint32_t zeros_of(uint32_t codes) { return ~(codes | codes >> 1 | codes >> 2) & 0x11111111u; }
+
+// The codes and the scale of the lane's half of a block, by the definition: every quotient one fp32 rounding.
+__device__ __forceinline__ void encode(const float (&y)[8], float tensor_scale, uint32_t& codes, uint32_t& scale) {
+  const uint32_t top = block_top(y);
+  scale = kv4::kScaleNaN;
+  codes = 0;
+  if (top >= 0x7F800000u) return;
+  scale = kv4::e4m3_code(__fdiv_rn(__fdiv_rn(__uint_as_float(top), 6.0f), tensor_scale));
+  const float S = kv4::e4m3_value(scale) * tensor_scale;
+  if (!(S > 0.0f)) return;
+  float t[8];
+#pragma unroll
+  for (int k = 0; k < 8; ++k) t[k] = __fdiv_rn(y[k], S);
+  codes = kv4::e2m1_codes(t);
+  codes &= ~(zeros_of(codes) << 3);
+}
+
+// The same by one reciprocal, from values that are off by at most err; false: another code or scale is
+// within reach, and encode() has to decide.  kSlack: relative, for the quotients' own roundings (three fp32 ones and
+// the reciprocal's, below 2^-21 together).
+__device__ __forceinline__ bool encode_fast(const float (&y)[8], const float (&err)[8], float tensor_scale,
+                                            uint32_t& codes, uint32_t& scale) {
+  constexpr float kSlack = 0x1p-20f;
+  const uint32_t top = block_top(y);
+  float worst = 0.0f;
+#pragma unroll
+  for (int k = 0; k < 8; ++k) worst = fmaxf(worst, err[k]);
+  worst = fmaxf(worst, __shfl_xor_sync(0xffffffffu, worst, 1));
+  scale = kv4::kScaleNaN;
+  codes = 0;
+  if (top >= 0x7F800000u) return true;
+  const float a = __uint_as_float(top), to = __frcp_rn(6.0f) * __frcp_rn(tensor_scale);
+  scale = kv4::e4m3_code((a + worst) * to * (1.0f + kSlack));
+  bool sure = scale == kv4::e4m3_code(fmaxf(a - worst, 0.0f) * to * (1.0f - kSlack));
+  const float S = kv4::e4m3_value(scale) * tensor_scale, inv = __frcp_rn(S);
+  if (!(S > 0.0f)) return sure;
+  float lo[8], hi[8];
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    const float t = y[k] * inv, off = __fmaf_rn(fabsf(t), kSlack, err[k] * inv);
+    lo[k] = t - off;
+    hi[k] = t + off;
+  }
+  codes = kv4::e2m1_codes(hi);
+  codes &= ~(zeros_of(codes) << 3);   // 0 has no sign, so that the sign of a value that may be either is no border
+  uint32_t other = kv4::e2m1_codes(lo);
+  other &= ~(zeros_of(other) << 3);
+  return sure && codes == other;
+}
+
+// A key's head again, in 64 bits from the operands, rounded to fp32 once; a value's head is the operands.  Every
+// lane of the warp takes part; c and s: the lane's cosines and signed sines (see the kernel).
+template <int D, int IN>
+__device__ __noinline__ void exact_head(const qmm_norm_rope_args& a, int64_t t, int h, int l, bool is_k, const float (&c)[8],
+                                        const float (&s)[8], bool turns, float (&x)[8]) {
+  constexpr int kLanes = D / 8;
+  float in[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
+  const int heads = a.Hq + (a.V ? 2 : 1) * a.Hk;
+  if (is_k) load8<IN>(a.K, t * a.ldk + (int64_t)(h - a.Hq) * D + 8 * l, in);
+  else if (h >= a.Hq && h < heads) load8<IN>(a.V, t * a.ldv + (int64_t)(h - a.Hq - a.Hk) * D + 8 * l, in);
+  double sum = 0.0;
+#pragma unroll
+  for (int k = 0; k < 8; ++k) sum = __fma_rn((double)in[k], (double)in[k], sum);
+#pragma unroll
+  for (int off = kLanes / 2; off >= 1; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+  const double root = sqrt(sum / D + (double)a.eps);
+  double y[8];
+#pragma unroll
+  for (int k = 0; k < 8; ++k) y[k] = (double)in[k] / root * (a.k_weight ? (double)a.k_weight[8 * l + k] : 1.0);
+  const int half = a.rot / 2, step = half / 8;
+  const int from = (threadIdx.x & 31) + (8 * l < half ? step : (turns ? -step : 0));
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    double other = __shfl_sync(0xffffffffu, y[k], from);
+    if (a.interleaved) other = y[k ^ 1];
+    const double z = turns ? y[k] * (double)c[k] + other * (double)s[k] : y[k];
+    x[k] = is_k ? (float)z : in[k];
+  }
+}
+
 // CTA (t, part): the heads part, part + groups * parts, ... of row t (queries, then keys, then
 // values).
-template <int D, int IN, int OUT, int AHEAD>
-__global__ void __launch_bounds__(kThreads, AHEAD == 2 ? 16 : 0) norm_rope_kernel(const __grid_constant__ Params P) {
+template <int D, int IN, int OUT, int AHEAD, bool FP4>
+__global__ void __launch_bounds__(kThreads, AHEAD == 2 && !FP4 ? 16 : 0) norm_rope_kernel(const __grid_constant__ Params P) {
   constexpr int kLanes = D / 8;
   constexpr int kGroups = kThreads / kLanes;
   // launched early behind a launch that allows it: memory is read from here on
@@ -171,24 +271,62 @@ __global__ void __launch_bounds__(kThreads, AHEAD == 2 ? 16 : 0) norm_rope_kerne
 #pragma unroll
         for (int k = 0; k < 8; ++k) y[k] = __shfl_sync(0xffffffffu, x[u][k], from);
       }
+      float err[8];   // of x, as the 4-bit codes have to know it
+      if constexpr (FP4) {
+        // the norm: D/8 + log2(D/8) + 2 roundings of the mean's sum (half of that on its root), the root's 2, the
+        // two products', the rotation's 2: below 24 of 2^-24 for D = 256, on the terms that are added
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+          err[k] = is_k ? 0x1p-19f * (turns ? __fmaf_rn(fabsf(x[u][k]), fabsf(c[k]), fabsf(y[k] * s[k])) : fabsf(x[u][k])) : 0.0f;
+      }
       if (turns && (is_q || is_k))
 #pragma unroll
         for (int k = 0; k < 8; ++k) x[u][k] = __fmaf_rn(x[u][k], c[k], y[k] * s[k]);
-      if (is_q) store8<OUT>(a.Q_out, t * a.ldqo + (int64_t)h * D + 8 * l, x[u]);
+      if constexpr (FP4) {
+        if (is_q) store8<OUT>(a.Q_out, t * a.ldqo + (int64_t)h * D + 8 * l, x[u]);
+        if (h0 + u * stride + kGroups > a.Hq) {   // some lane of the CTA holds a key or a value
+          const float tensor_scale = is_k ? P.k_scale : P.v_scale;
+          uint32_t codes, scale;
+          const bool sure = encode_fast(x[u], err, tensor_scale, codes, scale);
+          const bool mine_too = !is_q && h < heads;
+          const bool in_range = !is_k || (sum < 1e38f && sum * (1.0f / D) + a.eps > 1e-30f);   // of the fp32 arithmetic
+          if (__any_sync(0xffffffffu, mine_too && !(sure && in_range))) {
+            exact_head<D, IN>(a, t, h, l, is_k, c, s, turns, x[u]);
+            uint32_t codes2, scale2;
+            encode(x[u], tensor_scale, codes2, scale2);
+            codes = codes2;
+            scale = scale2;
+          }
+          if (mine_too && slot >= 0) {
+            const bool key = is_k;
+            const int hh = key ? h - a.Hq : h - a.Hq - a.Hk, i = (int)(slot & (P.page_size - 1));
+            uint8_t* run = static_cast<uint8_t*>(key ? a.K_cache : a.V_cache) +
+                           kv4::run_at(slot >> P.page_shift, hh, a.Hk, P.page_size, D);
+            *reinterpret_cast<uint32_t*>(run + i * (D / 2) + 4 * l) = codes;
+            if ((l & 1) == 0) run[P.page_size * (D / 2) + i * (D / 16) + (l >> 1)] = (uint8_t)scale;
+          }
+        }
+      } else if (is_q) store8<OUT>(a.Q_out, t * a.ldqo + (int64_t)h * D + 8 * l, x[u]);
       else if (slot >= 0 && is_k) store8<OUT>(a.K_cache, (slot * a.Hk + h - a.Hq) * D + 8 * l, x[u]);
       else if (slot >= 0 && h < heads) store8<OUT>(a.V_cache, (slot * a.Hk + h - a.Hq - a.Hk) * D + 8 * l, x[u]);
     }
   }
 }
 
-template <int D, int IN, int OUT, int AHEAD>
-cudaError_t launch_ahead(const qmm_norm_rope_args& a, cudaStream_t stream) {
+// A 4-bit cache's page and scales; page_size 0: a cache of 16-bit values.
+struct Fp4 {
+  int page_size = 0;
+  float k_scale = 1.0f, v_scale = 1.0f;
+};
+
+template <int D, int IN, int OUT, int AHEAD, bool FP4>
+cudaError_t launch_ahead(const qmm_norm_rope_args& a, const Fp4& f, cudaStream_t stream) {
   constexpr int kGroups = kThreads / (D / 8);
   const int heads = a.Hq + (a.V ? 2 : 1) * a.Hk;
   const int most = (heads + kGroups - 1) / kGroups;
   int parts = 1;
   while (parts < most && (int64_t)a.T * parts < 2048) ++parts;   // few rows: a CTA per few heads
-  Params P{a, parts};
+  Params P{a, parts, f.page_size, f.page_size ? 31 - __builtin_clz((unsigned)f.page_size) : 0, f.k_scale, f.v_scale};
   if ((int64_t)a.T * parts > 0x7fffffff) return cudaErrorInvalidValue;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3((unsigned)(a.T * parts));
@@ -199,7 +337,7 @@ cudaError_t launch_ahead(const qmm_norm_rope_args& a, cudaStream_t stream) {
   at[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, norm_rope_kernel<D, IN, OUT, AHEAD>, P);
+  return cudaLaunchKernelEx(&cfg, norm_rope_kernel<D, IN, OUT, AHEAD, FP4>, P);
 }
 
 // Two heads at a time for many fp32 rows, unless a group's last pair would stand half empty after few pairs:
@@ -210,33 +348,40 @@ cudaError_t launch_ahead(const qmm_norm_rope_args& a, cudaStream_t stream) {
 // 124; 2311 rows of 30 heads of 64 5.8, 6.3): twice the instructions a byte, which fill half the issue slots,
 // and the waits for loads between them (two would gain 5 to 7 % with 8 heads a row).
 template <int D, int IN, int OUT>
-cudaError_t launch(const qmm_norm_rope_args& a, cudaStream_t stream) {
+cudaError_t launch(const qmm_norm_rope_args& a, const Fp4& f, cudaStream_t stream) {
+  if (f.page_size) return launch_ahead<D, IN, OUT, 1, true>(a, f, stream);
   if constexpr (IN == QMM_F32) {
     constexpr int kGroups = kThreads / (D / 8);
     const int steps = (a.Hq + (a.V ? 2 : 1) * a.Hk + kGroups - 1) / kGroups;
-    if (a.T > 2048 && (steps % 2 == 0 || steps >= 7)) return launch_ahead<D, IN, OUT, 2>(a, stream);
+    if (a.T > 2048 && (steps % 2 == 0 || steps >= 7)) return launch_ahead<D, IN, OUT, 2, false>(a, f, stream);
   }
-  return launch_ahead<D, IN, OUT, 1>(a, stream);
+  return launch_ahead<D, IN, OUT, 1, false>(a, f, stream);
 }
 
 template <int D, int IN>
-cudaError_t launch_out(const qmm_norm_rope_args& a, cudaStream_t stream) {
-  return a.out_type == QMM_BF16 ? launch<D, IN, QMM_BF16>(a, stream) : launch<D, IN, QMM_F16>(a, stream);
+cudaError_t launch_out(const qmm_norm_rope_args& a, const Fp4& f, cudaStream_t stream) {
+  return a.out_type == QMM_BF16 ? launch<D, IN, QMM_BF16>(a, f, stream) : launch<D, IN, QMM_F16>(a, f, stream);
 }
 
 template <int D>
-cudaError_t launch_in(const qmm_norm_rope_args& a, cudaStream_t stream) {
-  if (a.in_type == QMM_F32) return launch_out<D, QMM_F32>(a, stream);
-  if (a.in_type == QMM_BF16) return launch_out<D, QMM_BF16>(a, stream);
-  return launch_out<D, QMM_F16>(a, stream);
+cudaError_t launch_in(const qmm_norm_rope_args& a, const Fp4& f, cudaStream_t stream) {
+  if (a.in_type == QMM_F32) return launch_out<D, QMM_F32>(a, f, stream);
+  if (a.in_type == QMM_BF16) return launch_out<D, QMM_BF16>(a, f, stream);
+  return launch_out<D, QMM_F16>(a, f, stream);
+}
+
+cudaError_t launch_any(const qmm_norm_rope_args& a, const Fp4& f, cudaStream_t stream) {
+  if (a.D == 64) return launch_in<64>(a, f, stream);
+  if (a.D == 128) return launch_in<128>(a, f, stream);
+  return launch_in<256>(a, f, stream);
 }
 
 }  // namespace
 
-cudaError_t launch_norm_rope(const qmm_norm_rope_args& a, cudaStream_t stream) {
-  if (a.D == 64) return launch_in<64>(a, stream);
-  if (a.D == 128) return launch_in<128>(a, stream);
-  return launch_in<256>(a, stream);
+cudaError_t launch_norm_rope(const qmm_norm_rope_args& a, cudaStream_t stream) { return launch_any(a, Fp4{}, stream); }
+
+cudaError_t launch_norm_rope_fp4(const qmm_norm_rope_fp4_args& a, cudaStream_t stream) {
+  return launch_any(a.base, Fp4{a.page_size, a.k_scale, a.v_scale}, stream);
 }
 
 cudaError_t read_and_clear_norm_rope_status(unsigned* out) {

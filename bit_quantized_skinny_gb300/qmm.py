@@ -40,7 +40,8 @@ EXPORTS = ["qmm_packed_bytes", "qmm_pack", "qmm_run", "qmm_run_batched", "qmm_de
            "qmm_ffn_fused_workspace_bytes", "qmm_run_ffn_fused", "qmm_release", "qmm_workspace_bytes_held",
            "qmm_stream_read", "qmm_stream_read_sink_words", "qmm_set_wait_limit", "qmm_pack_dev",
            "qmm_norm_rope", "qmm_attn_workspace_bytes", "qmm_attn_shared", "qmm_lora_workspace_bytes",
-           "qmm_run_lora"]
+           "qmm_run_lora", "qmm_kv_fp4_bytes", "qmm_norm_rope_fp4", "qmm_kv_fp4_read", "qmm_attn_fp4_workspace_bytes",
+           "qmm_attn_shared_fp4", "qmm_sample"]
 NOALLOC_SCRATCH_BYTES = 4 << 20
 
 
@@ -81,6 +82,27 @@ class _AttnArgs(ctypes.Structure):
         ("prefix_len", ctypes.c_int64), ("pages", ctypes.c_void_p), ("pages_per_stream", ctypes.c_int64),
         ("kv_lens", ctypes.c_void_p), ("row_starts", ctypes.c_void_p), ("O", ctypes.c_void_p),
         ("ldo", ctypes.c_int64), ("lse", ctypes.c_void_p)]
+
+
+class _NormRopeFp4Args(ctypes.Structure):
+    _fields_ = [("base", _NormRopeArgs), ("page_size", ctypes.c_int), ("k_scale", ctypes.c_float), ("v_scale", ctypes.c_float)]
+
+
+class _KvFp4ReadArgs(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int) for n in ("Hk", "D", "page_size", "out_type")] + [
+        ("k_scale", ctypes.c_float), ("v_scale", ctypes.c_float), ("n_slots", ctypes.c_int64),
+        ("K_cache", ctypes.c_void_p), ("V_cache", ctypes.c_void_p), ("slots", ctypes.c_void_p), ("n", ctypes.c_int64),
+        ("K_out", ctypes.c_void_p), ("V_out", ctypes.c_void_p)]
+
+
+class _AttnFp4Args(ctypes.Structure):
+    _fields_ = [("base", _AttnArgs), ("k_scale", ctypes.c_float), ("v_scale", ctypes.c_float)]
+
+
+class _SampleArgs(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int) for n in ("T", "V", "type")] + [("logits", ctypes.c_void_p), ("ld", ctypes.c_int64)] + [
+        (n, ctypes.c_void_p) for n in ("temperature", "top_k", "top_p", "min_p", "uniform", "tokens", "logprobs")] + [
+        ("B", ctypes.c_int)] + [(n, ctypes.c_void_p) for n in ("row_starts", "fed", "accepted", "next")]
 
 
 class _LoraAdapter(ctypes.Structure):
@@ -164,6 +186,18 @@ def load(path: str | None = None):
     lib.qmm_attn_workspace_bytes.restype = ctypes.c_size_t
     lib.qmm_attn_shared.argtypes = [ctypes.POINTER(_AttnArgs), vp, ctypes.c_size_t, vp]
     lib.qmm_attn_shared.restype = i32
+    lib.qmm_kv_fp4_bytes.argtypes = [i64, i32, i32]
+    lib.qmm_kv_fp4_bytes.restype = ctypes.c_size_t
+    lib.qmm_norm_rope_fp4.argtypes = [ctypes.POINTER(_NormRopeFp4Args), vp]
+    lib.qmm_norm_rope_fp4.restype = i32
+    lib.qmm_kv_fp4_read.argtypes = [ctypes.POINTER(_KvFp4ReadArgs), vp]
+    lib.qmm_kv_fp4_read.restype = i32
+    lib.qmm_attn_fp4_workspace_bytes.argtypes = [ctypes.POINTER(_AttnFp4Args)]
+    lib.qmm_attn_fp4_workspace_bytes.restype = ctypes.c_size_t
+    lib.qmm_attn_shared_fp4.argtypes = [ctypes.POINTER(_AttnFp4Args), vp, ctypes.c_size_t, vp]
+    lib.qmm_attn_shared_fp4.restype = i32
+    lib.qmm_sample.argtypes = [ctypes.POINTER(_SampleArgs), vp]
+    lib.qmm_sample.restype = i32
     lib.qmm_lora_workspace_bytes.argtypes = [ctypes.POINTER(_LoraEntry), i32, i32, i32]
     lib.qmm_lora_workspace_bytes.restype = ctypes.c_size_t
     lib.qmm_run_lora.argtypes = [ctypes.POINTER(_LoraEntry), i32, vp, i32, i32, vp, ctypes.c_size_t, vp]
@@ -403,13 +437,9 @@ def _dense(t, dtype, what: str) -> int:
     return t.data_ptr()
 
 
-def make_norm_rope(Q, K, V, q_weight, k_weight, cos_sin, positions, slots, Q_out, K_cache, V_cache,
-                   eps: float = 1e-6, interleaved: bool = False):
-    """Arguments of norm_rope().  Q: T x Hq x D, K and V: T x Hk x D (rows may be strided), one of
-    fp32, bf16 and fp16; Q_out: T x Hq x D and the caches n_slots x Hk x D, bf16 or fp16; weights
-    fp32 D or None; cos_sin fp32 max_pos x rot or None (no rotation); positions int32 T, slots int64
-    T.  K, V, slots and the caches may be None together, and V with V_cache.  The tensors are kept
-    alive by what is returned."""
+def _norm_rope_args(Q, K, V, q_weight, k_weight, cos_sin, positions, slots, Q_out, K_cache, V_cache, eps, interleaved,
+                    cache):
+    """_NormRopeArgs without n_slots; cache(tensor, a, name): the checked data pointer of a cache."""
     import torch
     T, Hq, D = Q.shape
     a = _NormRopeArgs(T=T, Hq=Hq, Hk=0 if K is None else K.shape[1], D=D, rot=0 if cos_sin is None else cos_sin.shape[1],
@@ -417,22 +447,20 @@ def make_norm_rope(Q, K, V, q_weight, k_weight, cos_sin, positions, slots, Q_out
     a.Q, a.ldq, a.Q_out, a.ldqo = Q.data_ptr(), _rows(Q, "Q"), Q_out.data_ptr(), _rows(Q_out, "Q_out")
     if tuple(Q_out.shape) != (T, Hq, D):
         raise QmmError(2, "Q_out")
-    for t, cache, name in ((K, K_cache, "K"), (V, V_cache, "V")):
+    for t, held, name in ((K, K_cache, "K"), (V, V_cache, "V")):
         if t is None:
             continue
-        if cache is None:
+        if held is None:
             raise QmmError(1, name + "_cache")
-        if tuple(t.shape) != (T, a.Hk, D) or cache.shape[1:] != (a.Hk, D):
+        if tuple(t.shape) != (T, a.Hk, D):
             raise QmmError(2, name)
+        at = cache(held, a, name)
         if t.dtype != Q.dtype:
             raise QmmError(12, name)
         setattr(a, name, t.data_ptr())
         setattr(a, "ldk" if name == "K" else "ldv", _rows(t, name))
-        setattr(a, name + "_cache", _dense(cache, Q_out.dtype, name + "_cache"))
+        setattr(a, name + "_cache", at)
     if K is not None:
-        a.n_slots = K_cache.shape[0]
-        if V is not None and V_cache.shape[0] != a.n_slots:
-            raise QmmError(2, "V_cache")
         a.slots = _dense(slots, torch.int64, "slots")
     for w, name in ((q_weight, "q_weight"), (k_weight, "k_weight")):
         if w is not None and w.numel() != D:
@@ -444,6 +472,27 @@ def make_norm_rope(Q, K, V, q_weight, k_weight, cos_sin, positions, slots, Q_out
     for t, name in ((positions if cos_sin is not None else None, "positions"), (slots if K is not None else None, "slots")):
         if t is not None and t.numel() != T:
             raise QmmError(2, name)
+    return a
+
+
+def make_norm_rope(Q, K, V, q_weight, k_weight, cos_sin, positions, slots, Q_out, K_cache, V_cache,
+                   eps: float = 1e-6, interleaved: bool = False):
+    """Arguments of norm_rope().  Q: T x Hq x D, K and V: T x Hk x D (rows may be strided), one of
+    fp32, bf16 and fp16; Q_out: T x Hq x D and the caches n_slots x Hk x D, bf16 or fp16; weights
+    fp32 D or None; cos_sin fp32 max_pos x rot or None (no rotation); positions int32 T, slots int64
+    T.  K, V, slots and the caches may be None together, and V with V_cache.  The tensors are kept
+    alive by what is returned."""
+    def cache(held, a, name):
+        if held.shape[1:] != (a.Hk, a.D):
+            raise QmmError(2, name)
+        return _dense(held, Q_out.dtype, name + "_cache")
+
+    a = _norm_rope_args(Q, K, V, q_weight, k_weight, cos_sin, positions, slots, Q_out, K_cache, V_cache, eps, interleaved,
+                        cache)
+    if K is not None:
+        a.n_slots = K_cache.shape[0]
+        if V is not None and V_cache.shape[0] != a.n_slots:
+            raise QmmError(2, "V_cache")
     a._keep = (Q, K, V, q_weight, k_weight, cos_sin, positions, slots, Q_out, K_cache, V_cache)
     return a
 
@@ -454,19 +503,88 @@ def norm_rope(args, stream=None) -> None:
     _check(load().qmm_norm_rope(args, _stream_handle(stream)), "qmm_norm_rope")
 
 
-def make_attn(Q, K_cache, V_cache, page_size: int, prefix_pages, prefix_len: int, pages, kv_lens, row_starts, O,
-              scale: float, lse=None):
-    """Arguments of attn_shared().  Q, O: T x Hq x D (rows may be strided), caches n_slots x Hk x D, all
-    bf16 or all fp16; prefix_pages int32 (None without a prefix), pages int32 B x pages_per_stream,
-    kv_lens int32 B, row_starts int32 B + 1; lse fp32 T x Hq or None.  The tensors are kept alive by
-    what is returned."""
+def kv_fp4_bytes(n_slots: int, Hk: int, D: int) -> int:
+    """Bytes of one packed 4-bit cache (of the keys, or of the values); 0 for an invalid shape."""
+    return load().qmm_kv_fp4_bytes(n_slots, Hk, D)
+
+
+def _packed_cache(t, n_slots: int, Hk: int, D: int, what: str) -> int:
+    """Data pointer of a uint8 tensor that holds a packed cache."""
     import torch
-    if any(t is None for t in (K_cache, V_cache, pages, kv_lens, row_starts, O)):
-        raise QmmError(1, "make_attn")
+    if t is None:
+        raise QmmError(1, what)
+    if t.numel() < kv_fp4_bytes(n_slots, Hk, D):
+        raise QmmError(5, what)
+    return _dense(t, torch.uint8, what)
+
+
+def _device_of(tensors, what: str) -> int:
+    """Index of the one CUDA device that holds every tensor of `tensors` (None is skipped)."""
+    held = [t for t in tensors if t is not None]
+    if not all(t.is_cuda and t.device == held[0].device for t in held):
+        raise QmmError(2, what + ": tensors on one CUDA device")
+    return held[0].device.index
+
+
+def _handle_on(device: int, stream):
+    """_stream_handle(), for a call whose tensors are on `device`: the current one, by the library's rule."""
+    import torch
+    if torch.cuda.current_device() != device:
+        raise QmmError(2, f"tensors on device {device}, which is not the current one")
+    return _stream_handle(stream)
+
+
+def make_norm_rope_fp4(Q, K, V, q_weight, k_weight, cos_sin, positions, slots, Q_out, K_cache, V_cache, n_slots: int,
+                       page_size: int, k_scale: float = 1.0, v_scale: float = 1.0, eps: float = 1e-6,
+                       interleaved: bool = False):
+    """Arguments of norm_rope_fp4(): as make_norm_rope(), with packed caches (uint8 tensors of kv_fp4_bytes(n_slots,
+    Hk, D) bytes) and their page size and tensor scales."""
+    tensors = (Q, K, V, q_weight, k_weight, cos_sin, positions, slots, Q_out, K_cache, V_cache)
+    a = _NormRopeFp4Args(page_size=page_size, k_scale=k_scale, v_scale=v_scale)
+    a.base = _norm_rope_args(*tensors, eps, interleaved,
+                             lambda held, base, name: _packed_cache(held, n_slots, base.Hk, base.D, name + "_cache"))
+    a.base.n_slots = n_slots
+    a._device, a._keep = _device_of(tensors, "make_norm_rope_fp4"), tensors
+    return a
+
+
+def norm_rope_fp4(args, stream=None) -> None:
+    """qmm_norm_rope_fp4: norm and rotation of every query and key head, keys and values in 4 bits to their
+    cache slots.  `args` from make_norm_rope_fp4()."""
+    _check(load().qmm_norm_rope_fp4(args, _handle_on(args._device, stream)), "qmm_norm_rope_fp4")
+
+
+def make_kv_fp4_read(K_cache, V_cache, K_out, V_out, n_slots: int, page_size: int, k_scale: float = 1.0,
+                     v_scale: float = 1.0, slots=None):
+    """Arguments of kv_fp4_read().  Packed caches of n_slots slots; K_out, V_out: n x Hk x D, fp32, bf16 or fp16,
+    contiguous; slots: int64 n, or None for slots 0 .. n - 1.  V_cache and V_out may be None together."""
+    import torch
+    if K_out is None or (V_cache is None) != (V_out is None):
+        raise QmmError(1, "make_kv_fp4_read")
+    n, Hk, D = K_out.shape
+    if (V_out is not None and V_out.shape != K_out.shape) or (slots is not None and slots.numel() != n):
+        raise QmmError(2, "make_kv_fp4_read")
+    a = _KvFp4ReadArgs(Hk=Hk, D=D, page_size=page_size, out_type=_dtype_code(K_out), k_scale=k_scale, v_scale=v_scale,
+                       n_slots=n_slots, n=n, slots=_dense(slots, torch.int64, "slots"))
+    a.K_cache, a.K_out = _packed_cache(K_cache, n_slots, Hk, D, "K_cache"), _dense(K_out, K_out.dtype, "K_out")
+    if V_out is not None:
+        a.V_cache, a.V_out = _packed_cache(V_cache, n_slots, Hk, D, "V_cache"), _dense(V_out, K_out.dtype, "V_out")
+    tensors = (K_cache, V_cache, K_out, V_out, slots)
+    a._device, a._keep = _device_of(tensors, "make_kv_fp4_read"), tensors
+    return a
+
+
+def kv_fp4_read(args, stream=None) -> None:
+    """qmm_kv_fp4_read: slots of a 4-bit cache as values.  `args` from make_kv_fp4_read()."""
+    _check(load().qmm_kv_fp4_read(args, _handle_on(args._device, stream)), "qmm_kv_fp4_read")
+
+
+def _attn_args(Q, Hk: int, page_size: int, prefix_pages, prefix_len: int, pages, kv_lens, row_starts, O, scale: float, lse):
+    """_AttnArgs without the caches and n_slots."""
+    import torch
     T, Hq, D = Q.shape
-    n_slots, Hk, Dk = K_cache.shape
     B, per_stream = pages.shape
-    if Dk != D or V_cache.shape != K_cache.shape or O.shape != Q.shape:
+    if O.shape != Q.shape:
         raise QmmError(2, "make_attn")
     if kv_lens.numel() != B or row_starts.numel() != B + 1 or (lse is not None and tuple(lse.shape) != (T, Hq)):
         raise QmmError(2, "make_attn")
@@ -475,12 +593,28 @@ def make_attn(Q, K_cache, V_cache, page_size: int, prefix_pages, prefix_len: int
     if O.dtype != Q.dtype:
         raise QmmError(12, "O")
     a = _AttnArgs(T=T, B=B, Hq=Hq, Hk=Hk, D=D, page_size=page_size, type=_dtype_code(Q), scale=scale,
-                  n_slots=n_slots, prefix_len=prefix_len, pages_per_stream=per_stream)
+                  prefix_len=prefix_len, pages_per_stream=per_stream)
     a.Q, a.ldq, a.O, a.ldo = Q.data_ptr(), _rows(Q, "Q"), O.data_ptr(), _rows(O, "O")
-    a.K_cache, a.V_cache = _dense(K_cache, Q.dtype, "K_cache"), _dense(V_cache, Q.dtype, "V_cache")
     a.prefix_pages = _dense(prefix_pages, torch.int32, "prefix_pages")
     a.pages, a.kv_lens = _dense(pages, torch.int32, "pages"), _dense(kv_lens, torch.int32, "kv_lens")
     a.row_starts, a.lse = _dense(row_starts, torch.int32, "row_starts"), _dense(lse, torch.float32, "lse")
+    return a
+
+
+def make_attn(Q, K_cache, V_cache, page_size: int, prefix_pages, prefix_len: int, pages, kv_lens, row_starts, O,
+              scale: float, lse=None):
+    """Arguments of attn_shared().  Q, O: T x Hq x D (rows may be strided), caches n_slots x Hk x D, all
+    bf16 or all fp16; prefix_pages int32 (None without a prefix), pages int32 B x pages_per_stream,
+    kv_lens int32 B, row_starts int32 B + 1; lse fp32 T x Hq or None.  The tensors are kept alive by
+    what is returned."""
+    if any(t is None for t in (K_cache, V_cache, pages, kv_lens, row_starts, O)):
+        raise QmmError(1, "make_attn")
+    n_slots, Hk, Dk = K_cache.shape
+    if Dk != Q.shape[2] or V_cache.shape != K_cache.shape:
+        raise QmmError(2, "make_attn")
+    a = _attn_args(Q, Hk, page_size, prefix_pages, prefix_len, pages, kv_lens, row_starts, O, scale, lse)
+    a.n_slots = n_slots
+    a.K_cache, a.V_cache = _dense(K_cache, Q.dtype, "K_cache"), _dense(V_cache, Q.dtype, "V_cache")
     a._keep = (Q, K_cache, V_cache, prefix_pages, pages, kv_lens, row_starts, O, lse)
     return a
 
@@ -495,6 +629,77 @@ def attn_shared(args, workspace, stream=None) -> None:
     bytes."""
     _check(load().qmm_attn_shared(args, workspace.data_ptr(), workspace.numel() * workspace.element_size(),
                                   _stream_handle(stream)), "qmm_attn_shared")
+
+
+def make_attn_fp4(Q, K_cache, V_cache, Hk: int, page_size: int, prefix_pages, prefix_len: int, pages, kv_lens, row_starts,
+                  O, scale: float, k_scale: float = 1.0, v_scale: float = 1.0, lse=None):
+    """Arguments of attn_shared_fp4(): as make_attn(), with packed caches of Hk heads (uint8 tensors; their size gives
+    the number of slots) and their tensor scales."""
+    tensors = (Q, K_cache, V_cache, prefix_pages, pages, kv_lens, row_starts, O, lse)
+    if any(t is None for t in (K_cache, V_cache, pages, kv_lens, row_starts, O)):
+        raise QmmError(1, "make_attn_fp4")
+    a = _AttnFp4Args(k_scale=k_scale, v_scale=v_scale)
+    a.base = _attn_args(Q, Hk, page_size, prefix_pages, prefix_len, pages, kv_lens, row_starts, O, scale, lse)
+    page = kv_fp4_bytes(page_size, Hk, Q.shape[2]) if page_size > 0 else 0
+    if page == 0 or V_cache.numel() != K_cache.numel():
+        raise QmmError(2, "make_attn_fp4")
+    a.base.n_slots = n = K_cache.numel() // page * page_size
+    if n == 0:
+        raise QmmError(5, "K_cache")
+    a.base.K_cache, a.base.V_cache = (_packed_cache(t, n, Hk, Q.shape[2], name) for t, name in
+                                      ((K_cache, "K_cache"), (V_cache, "V_cache")))
+    a._device, a._keep = _device_of(tensors, "make_attn_fp4"), tensors
+    return a
+
+
+def attn_fp4_workspace_bytes(args) -> int:
+    return load().qmm_attn_fp4_workspace_bytes(args)
+
+
+def attn_shared_fp4(args, workspace, stream=None) -> None:
+    """qmm_attn_shared_fp4: attn_shared() over a 4-bit cache.  `args` from make_attn_fp4(); `workspace`: a device
+    tensor of >= attn_fp4_workspace_bytes(args) bytes."""
+    _check(load().qmm_attn_shared_fp4(args, workspace.data_ptr(), workspace.numel() * workspace.element_size(),
+                                      _handle_on(args._device, stream)), "qmm_attn_shared_fp4")
+
+
+def make_sample(logits, uniform, tokens, temperature=None, top_k=None, top_p=None, min_p=None, logprobs=None, fed=None,
+                row_starts=None, accepted=None, next=None):
+    """Arguments of sample().  logits: T x V, fp32, bf16 or fp16 (rows may be strided); uniform, temperature, top_p,
+    min_p: fp32 T, top_k: int32 T (None: off); tokens: int32 T; logprobs: fp32 T or None.  With drafts: fed int32
+    T (the token each row was fed), row_starts int32 B + 1, accepted and next int32 B.  The tensors are kept alive
+    by what is returned."""
+    import torch
+    drafts = (fed, row_starts, accepted, next)
+    if logits is None or uniform is None or tokens is None or any((t is None) != (fed is None) for t in drafts):
+        raise QmmError(1, "make_sample")
+    if logits.dim() != 2 or (logits.shape[1] > 1 and logits.stride(1) != 1):
+        raise QmmError(2, "logits")
+    T, V = logits.shape
+    a = _SampleArgs(T=T, V=V, type=_dtype_code(logits), logits=logits.data_ptr(),
+                    ld=logits.stride(0) if T > 1 else max(logits.stride(0), V))
+    f32, i32 = torch.float32, torch.int32
+    per_row = (("temperature", temperature, f32), ("top_k", top_k, i32), ("top_p", top_p, f32), ("min_p", min_p, f32),
+               ("uniform", uniform, f32), ("tokens", tokens, i32), ("logprobs", logprobs, f32), ("fed", fed, i32))
+    for name, t, dtype in per_row:
+        if t is not None and t.numel() != T:
+            raise QmmError(2, name)
+        setattr(a, name, _dense(t, dtype, name))
+    if fed is not None:
+        a.B = accepted.numel()
+        if next.numel() != a.B or row_starts.numel() != a.B + 1:
+            raise QmmError(2, "make_sample")
+        for name, t in (("row_starts", row_starts), ("accepted", accepted), ("next", next)):
+            setattr(a, name, _dense(t, i32, name))
+    tensors = (logits, uniform, tokens, temperature, top_k, top_p, min_p, logprobs, *drafts)
+    a._device, a._keep = _device_of(tensors, "make_sample"), tensors
+    return a
+
+
+def sample(args, stream=None) -> None:
+    """qmm_sample: the token of every row from its logits, and how many of each stream's drafted tokens stand.
+    `args` from make_sample()."""
+    _check(load().qmm_sample(args, _handle_on(args._device, stream)), "qmm_sample")
 
 
 def make_lora_adapters(items):

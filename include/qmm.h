@@ -467,6 +467,70 @@ size_t qmm_attn_workspace_bytes(const qmm_attn_args* args_host);   /* 0: invalid
 qmm_status qmm_attn_shared(const qmm_attn_args* args_host, void* workspace_dev, size_t workspace_bytes,
                            cudaStream_t stream);
 
+/* The same cache in 4 bits: 4.5 bits a value instead of 16, for contexts that do not fit, or whose reading bounds a
+ * decoding step.  A value is code * scale * tensor scale: an E2M1 code (0, 0.5, 1, 1.5, 2, 3, 4, 6 and
+ * negative), an E4M3 scale for each 16 neighbouring values of a head, and one fp32 scale for all keys
+ * (k_scale) and one for all values (v_scale), which the caller picks so that 2688 of it is above the largest value.
+ *
+ * A packed cache is n_slots / page_size pages one after another.  A page holds its Hk heads one after another, each
+ * page_size * (D/2 + D/16) bytes: first the codes of the page's slots (D/2 bytes a slot, value 2i in the low
+ * half of byte i, value 2i + 1 in the high half), then their scales (D/16 bytes a slot).  Pages, slots and
+ * page lists are those of the 16-bit cache.
+ *
+ * Rounding: the block's scale is E4M3((max|y| / 6) / tensor scale), to nearest even, at most 448; with
+ * S = scale * tensor scale a code is E2M1(y / S), to nearest even, at most 6, a 0 without sign; all
+ * codes are 0 where S is 0.  Each of these operations is rounded to binary32.  A block with an
+ * infinity or NaN gets the scale NaN and reads as 16 NaN.
+ *
+ * qmm_kv_fp4_bytes: bytes of one packed cache (of the keys, or of the values); 0 for an invalid shape.
+ *   1 <= n_slots, 1 <= Hk <= 32767, D 64, 128 or 256. */
+size_t qmm_kv_fp4_bytes(int64_t n_slots, int Hk, int D);
+
+/* qmm_norm_rope into a 4-bit cache: base.K_cache and base.V_cache are packed caches of base.n_slots slots in
+ * pages of page_size, base.out_type is the type of Q_out.  A key is normed and rotated in real arithmetic
+ * (to the last code: what fp32 leaves open is computed in 64 bits), rounded to binary32 and then as above; a value
+ * is rounded as above.  The same operands give the same bits in every call.
+ *   As qmm_norm_rope, and: page_size a power of two in [16, 4096], base.n_slots a multiple of it, k_scale and
+ *   v_scale in [2^-60, 2^60].
+ * Errors: as qmm_norm_rope. */
+typedef struct {
+  qmm_norm_rope_args base;
+  int page_size;
+  float k_scale, v_scale;
+} qmm_norm_rope_fp4_args;
+qmm_status qmm_norm_rope_fp4(const qmm_norm_rope_fp4_args* args_host, cudaStream_t stream);
+
+/* The values of n slots of a 4-bit cache: K_out and V_out are n x Hk x D of out_type (QMM_F32, QMM_BF16 or
+ * QMM_F16), row i from slot slots[i] (device), or from slot i where slots is NULL.  The value is rounded to binary32
+ * and then to out_type.  A negative slot leaves its row as it was.  V_cache and V_out may be NULL.
+ *   n >= 0 (at most n_slots without slots); n * Hk * D < 2^43; caches and outputs are 16-byte aligned, slots 8.
+ * Errors: QMM_ERR_NULL, QMM_ERR_SHAPE, QMM_ERR_TYPE, QMM_ERR_ALIGN, QMM_ERR_CUDA. */
+typedef struct {
+  int Hk, D, page_size, out_type;
+  float k_scale, v_scale;
+  int64_t n_slots;
+  const void *K_cache, *V_cache;
+  const int64_t* slots;
+  int64_t n;
+  void *K_out, *V_out;
+} qmm_kv_fp4_read_args;
+qmm_status qmm_kv_fp4_read(const qmm_kv_fp4_read_args* args_host, cudaStream_t stream);
+
+/* qmm_attn_shared over a 4-bit cache: base.K_cache and base.V_cache are packed caches of base.n_slots slots in pages of
+ * base.page_size, base.type is the type of Q and O.  Keys and values enter the products as they
+ * are stored (a code times its scale is exact in 16 bits), the weights of the values are rounded to fp16.
+ * bf16 queries are taken to fp16 with a power of two of their row that makes this exact down to 2^-24
+ * of the row's largest value.  A NaN that a row sees makes the 16 values of its block of O NaN (in a key: the whole row).
+ * Shapes, errors and everything else as qmm_attn_shared; k_scale and v_scale in [2^-60, 2^60].
+ *   workspace_dev: at least qmm_attn_fp4_workspace_bytes(args) bytes, as there. */
+typedef struct {
+  qmm_attn_args base;
+  float k_scale, v_scale;
+} qmm_attn_fp4_args;
+size_t qmm_attn_fp4_workspace_bytes(const qmm_attn_fp4_args* args_host);   /* 0: invalid arguments */
+qmm_status qmm_attn_shared_fp4(const qmm_attn_fp4_args* args_host, void* workspace_dev, size_t workspace_bytes,
+                               cudaStream_t stream);
+
 /* Low-rank adapters of the rows' requests beside shared projections:
  *     Y[i] = Y0[i] + scale_a * B_a (A_a x_i),   a = ids_dev[i]   (Y[i] = Y0[i] for ids[i] = -1)
  * for the M rows of X and each of `count` projections that share the rows' ids (q, k and v of a
@@ -501,6 +565,53 @@ typedef struct {
 size_t qmm_lora_workspace_bytes(const qmm_lora_entry* entries_host, int count, int M, int rank_max);
 qmm_status qmm_run_lora(const qmm_lora_entry* entries_host, int count, const int32_t* ids_dev, int M, int rank_max,
                         void* workspace_dev, size_t workspace_bytes, cudaStream_t stream);
+
+/* ------------------------------------------------------------------------------------------
+ * The token of every row, from the lm_head's logits and given random numbers, and how many of each
+ * stream's drafted tokens stand: the end of a verify pass.  For a row x of V logits with temperature T, top_k,
+ * top_p, min_p and the random number u:
+ *     w_i = exp((x_i - max x) / T); tokens in the order of falling x, equal ones by rising index;
+ *     top_k: the first top_k tokens stay;
+ *     top_p: of these, a token stays if the weights before it sum to less than top_p times the sum of all of them;
+ *     min_p: of these, a token stays if w_i >= min_p (w of the first token is 1);
+ *     the first token always stays;
+ *     token = the lowest i with  sum_{j <= i, j stays} w_j  >  u * sum_{j stays} w_j,
+ *     logprob = log(w_token / sum_{j stays} w_j).
+ * Weights are rounded to multiples of 2^-43 and summed as integers: no sum depends on an order, and a token on
+ * nothing but its row.  NaN and -inf logits are never taken; with +inf logits, these share the weight.  A row
+ * without any logit above -inf gives token -1 and logprob -inf.
+ *   temperature, top_p, min_p, uniform (fp32) and top_k (int32): device, one for each row.  temperature, top_k, top_p and
+ *   min_p may be NULL (1, off, off, off).  A temperature that is not above 0 picks the first token (logprob 0);
+ *   top_k < 1, top_p >= 1 and min_p <= 0 are off, and so is a NaN; u is taken into [0, 1).
+ *   T >= 0 rows, 1 <= V <= QMM_SAMPLE_MAX_V; type: QMM_F32, QMM_BF16 or QMM_F16; ld >= V elements between rows, any
+ *   alignment that the type needs.  tokens: T int32.  logprobs: T fp32, or NULL.
+ * Drafts (B > 0): stream b owns rows row_starts[b] .. row_starts[b+1]-1 (as in qmm_attn_shared), and fed[r] is the token
+ * that row r was fed: the stream's last token, then the drafted ones.  accepted[b] is the number of drafted tokens that
+ * stand: the leading rows r of the stream, but for its last, with tokens[r] == fed[r+1]; next[b] is the token
+ * behind them, tokens[row_starts[b] + accepted[b]].  A draft that was picked without chance is accepted with
+ * the probability that its row gives it, and next follows the row's distribution either way (the pages' lossless
+ * verification, "sixi-asi 0.8").  A stream without rows gets 0 and -1; with starts out of range, bit 2 of the
+ * status word is set as well.
+ *   0 <= B <= QMM_ATTN_MAX_STREAMS; row_starts: B + 1, fed: T, accepted, next: B, int32 on the device; not used for B = 0.
+ * Outputs must not overlap an input or each other.
+ * Errors: QMM_ERR_NULL, QMM_ERR_SHAPE, QMM_ERR_TYPE, QMM_ERR_ALIGN, QMM_ERR_CUDA. */
+#define QMM_SAMPLE_MAX_V 393216
+#define QMM_SAMPLE_MAX_ROWS 65535
+typedef struct {
+  int T, V, type;
+  const void* logits;
+  int64_t ld;
+  const float* temperature;
+  const int32_t* top_k;
+  const float *top_p, *min_p;
+  const float* uniform;
+  int32_t* tokens;
+  float* logprobs;
+  int B;
+  const int32_t *row_starts, *fed;
+  int32_t *accepted, *next;
+} qmm_sample_args;
+qmm_status qmm_sample(const qmm_sample_args* args_host, cudaStream_t stream);
 
 /* Measurement probe: read bytes (a multiple of 16) of device memory at buf_dev exactly once,
  * with 16-byte loads that bypass L1 and are marked evict-first in L2, and write one word per CTA
@@ -541,7 +652,8 @@ void qmm_set_wait_limit(uint32_t polls, uint32_t suspend_ns);
  * last read.  Bit 0: a kernel stopped waiting for its own weight copies after a bounded number
  * of polls; the outputs of the calls since the last read are then invalid.  Bit 1: qmm_pack_dev
  * met a non-finite weight or an fp16 scale overflow and wrote zeros for that super-block.  Bit 2:
- * qmm_norm_rope, qmm_attn_shared or qmm_run_lora met a device-side index out of range. */
+ * qmm_norm_rope, qmm_attn_shared (and their 4-bit forms), qmm_kv_fp4_read, qmm_run_lora or qmm_sample met a
+ * device-side index out of range. */
 qmm_status qmm_device_status(unsigned* status_out);
 
 /* Human-readable text of a status code (static storage). */
