@@ -47,7 +47,9 @@
 
 #include "q4k_device.cuh"
 #include "q4k_device_once.h"
+#include "q4k_formats.cuh"
 #include "q4k_internal.h"
+#include "q4k_kv_fp4.cuh"
 #include "q4k_tcgen05.cuh"
 
 namespace q4k {
@@ -61,9 +63,11 @@ constexpr int kLead = 4;             // units of a group besides its key tiles (
 constexpr int kMaxCtas = 152;
 constexpr int kLaneWarps = 4;
 constexpr int kLoadWarp = 8, kMmaWarp = 9 /* and 10 */, kQWarp = 11;
-constexpr int kThreads = 12 * 32;
+constexpr int kFirstDequantWarp = 12, kDequantWarps = 4;   // of a 4-bit cache
 constexpr uint32_t kTmemCols = 512;   // lane L: S at 64 L, p at 128 + 64 L and 160 + 64 L, O at 256 + 128 L
 constexpr float kGrow = 8.0f;
+constexpr float kLift = 7.0f;        // fp16 weights lie at 2^kLift: at most 2^(kLift + kGrow), and normal down to 2^(-14 - kLift)
+constexpr int kFactorTiles = 8;      // (the roles are a few tiles apart)
 constexpr uint32_t kWaitLimit = 1u << 17;
 constexpr float kLog2e = 1.44269504088896340736f, kLn2 = 0.69314718055994530942f;
 
@@ -85,23 +89,29 @@ struct Params {
   int tokens;         // of a row tile
   int n_pages, page_shift;
   uint32_t wait_polls, wait_ns;
+  float k_scale, v_scale;   // of a 4-bit cache's tensors
 };
 
-template <int D>
+template <int D, bool FP4>
 struct Smem {
   static constexpr int kHalf = kTile * 128;              // 64 keys of 64 values
   static constexpr int kTileBytes = kTile * D * 2;
   static constexpr int kQHalf = kRows * 128;
   static constexpr int kQBytes = kRows * D * 2;
-  static constexpr int kStages = 5;                      // of keys, and of values
+  static constexpr int kStages = FP4 && D == 128 ? 3 : 5;   // of keys, and of values
+  static constexpr int kPackBytes = kTile * kv4::slot_bytes(D);   // a tile as the 4-bit cache holds it
+  static constexpr int kPacks = 12;
   static constexpr int kQ = 0;
   static constexpr int kK = 2 * kQBytes;
   static constexpr int kV = kK + kStages * kTileBytes;
-  static constexpr int kStats = kV + kStages * kTileBytes;   // (top, sum) of the two lanes' rows
-  static constexpr int kMisc = kStats + 2 * kRows * 8;
+  static constexpr int kPack = kV + kStages * kTileBytes;
+  static constexpr int kStats = kPack + (FP4 ? kPacks * kPackBytes : 0);   // (top, sum) of the two lanes' rows
+  static constexpr int kFactors = kStats + 2 * kRows * 8;      // of the rows of the last kFactorTiles query tiles
+  static constexpr int kMisc = kFactors + (FP4 ? kFactorTiles * kRows * 4 : 0);
   static constexpr int kTotal = kMisc + 1024;
 };
-static_assert(Smem<128>::kTotal <= 227 * 1024 && Smem<64>::kTotal <= 227 * 1024, "shared memory");
+static_assert(Smem<128, false>::kTotal <= 227 * 1024 && Smem<128, true>::kTotal <= 227 * 1024 &&
+              Smem<64, false>::kTotal <= 227 * 1024 && Smem<64, true>::kTotal <= 227 * 1024, "shared memory");
 
 // Barriers.  A wait tells a phase from the one after it only, so a barrier is waited on by threads that
 // see all of its phases, or that know the phase before to be over and the one after not begun: a stage of keys or values has a full barrier for each set of users (lane
@@ -109,7 +119,8 @@ static_assert(Smem<128>::kTotal <= 227 * 1024 && Smem<64>::kTotal <= 227 * 1024,
 enum : int {
   kBarFullK = 0 /* 5 users + stage */, kBarFullV = 15, kBarEmptyK = 30, kBarEmptyV = 35, kBarQFull = 40, kBarQEmpty = 42,
   kBarS = 44, kBarFree = 46, kBarP = 48 /* 2 lane + item % 2 */, kBarO = 52, kBarEnd = 56, kBarJoin = 58, kBarDrain = 59,
-  kBars = 61
+  kBars16 = 61,                                    // of a cache of 16-bit values
+  kBarPackFull = 61, kBarPackEmpty = 73, kBars = 85   // and of a 4-bit cache's tiles
 };
 
 // Rows and own keys of a stream.
@@ -120,7 +131,7 @@ struct Stream {
 struct Misc {
   uint64_t bars[kBars];
   int64_t w0, w1, per;   // this CTA's units, units of a CTA
-  int64_t scan[kThreads / 32];
+  int64_t scan[16];
   int b, rb, h, rows;
   Stream s;           // stream b, if b >= 0
   int64_t unit;       // end of the CTA's units within that group
@@ -275,10 +286,27 @@ __device__ __noinline__ bool wait_slowly(uint32_t bar, uint32_t parity, uint32_t
   return false;
 }
 
-template <int D, int TYPE>
-__global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant__ Params P) {
+template <bool FP4>
+constexpr int kThreads = (FP4 ? kFirstDequantWarp + kDequantWarps : kFirstDequantWarp) * 32;
+
+// Bulk copy global -> shared with the default L2 policy (a prefix's tiles are read by several CTAs).
+__device__ __forceinline__ void bulk_copy(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
+               :: "r"(dst), "l"(src), "r"(bytes), "r"(bar) : "memory");
+}
+
+// One product of two fp16 pairs.
+__device__ __forceinline__ uint32_t mul2(uint32_t a, uint32_t b) {
+  const __half2 r = __hmul2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b));
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+
+template <int D, int TYPE, bool FP4>
+__global__ void __launch_bounds__(kThreads<FP4>, 1) attn_kernel(const __grid_constant__ Params P) {
   extern __shared__ __align__(1024) uint8_t smem[];
-  using L = Smem<D>;
+  using L = Smem<D, FP4>;
+  constexpr int kThreads = q4k::kThreads<FP4>;
+  constexpr int kProduct = FP4 ? QMM_F16 : TYPE;   // the type of the products' operands
   constexpr uint32_t kS = L::kStages;
   const qmm_attn_args& a = P.a;
   Misc& M = *reinterpret_cast<Misc*>(smem + L::kMisc);
@@ -289,12 +317,15 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
   const int G = a.Hq / a.Hk, block = 2 * P.tokens;
 
   // ---- barriers, tensor memory, and this CTA's piece of the list of key tiles
-  if (threadIdx.x < kBars) {
+  constexpr int kMyBars = FP4 ? kBars : kBars16;
+  if (threadIdx.x < kMyBars) {
     const int k = threadIdx.x;
     const bool two = (k >= kBarEmptyK && k < kBarQFull) || (k >= kBarQEmpty && k < kBarS);
-    mbar_init(bar(k), two ? 2 : (k >= kBarFree && k < kBarO) ? kLaneWarps : k == kBarJoin ? 2 * kLaneWarps : 1);
+    const bool by_warps = FP4 && (k < kBarEmptyK || k >= kBarPackEmpty);   // dequantised, and read by that
+    mbar_init(bar(k), by_warps ? kDequantWarps : two ? 2 : (k >= kBarFree && k < kBarO) ? kLaneWarps
+                      : k == kBarJoin ? 2 * kLaneWarps : 1);
     fence_barrier_init();
-  } else if (threadIdx.x == kBars) {
+  } else if (threadIdx.x == kMyBars) {
     M.abort = 0;
     for (int k = 0; k < 8; ++k) M.odd[k] = 0;
   }
@@ -302,7 +333,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
     tc::tmem_alloc(smem_addr(&M.tmem), kTmemCols);
     tc::tmem_relinquish();
   }
-  if (threadIdx.x < 3)
+  if (!FP4 && threadIdx.x < 3)
     asm volatile("prefetch.tensormap [%0];" :: "l"(threadIdx.x == 0 ? &P.mapK : threadIdx.x == 1 ? &P.mapV : &P.mapQ)
                  : "memory");
   // Launched early (behind a launch that allows it), this grid reads what was written before it from
@@ -404,8 +435,197 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
   Walker walk;
   walk.start(P, M);
   Seg g;
+  // Segment by segment, the order in which keys and values are copied and dequantised: K0, K1, V0, K2, V1, ...
+  // tile(values, t) of each; false ends it.
+  [[maybe_unused]] auto in_order = [&](int n, auto&& tile) -> bool {
+    for (int u = 0; u <= n; ++u) {
+      if (u < n && !tile(std::false_type{}, u)) return false;
+      if (u > 0 && !tile(std::true_type{}, u - 1)) return false;
+    }
+    return true;
+  };
 
-  if (warp == kLoadWarp) {
+  if (FP4 && warp == kLoadWarp) {
+    // ------------------------------------------------------------------ keys and values in 4 bits
+    // A tile is a run of codes and one of scales per page (or of 64 keys of a longer page): lane 2k copies the
+    // codes of run k, lane 2k + 1 its scales.  Pages behind the last key are not read.
+    const int per_run = min(a.page_size, kTile);
+    const int my_key = lane / 2 * per_run, my_bytes = lane % 2 ? D / 16 : D / 2;   // a slot
+    const uint32_t dst = lane % 2 ? kTile * (D / 2) + my_key * (D / 16) : my_key * (D / 2);
+    uint32_t filled = 0;
+    bool ok = true;
+    auto from = [&](const Seg& s, int tile) -> int64_t {   // offset of this lane's run in the caches, or -1
+      const int key = tile * kTile + my_key;
+      if (my_key >= kTile || key >= s.keys) return -1;
+      int page = s.pages[key >> P.page_shift];
+      if (page < 0 || page >= P.n_pages) {
+        atomicOr(&g_status, kErrIndex);
+        page = 0;   // (the rows that see it have unspecified values)
+      }
+      return kv4::run_at(page, s.h, a.Hk, a.page_size, D) + (lane % 2 ? a.page_size * (D / 2) : 0) +
+             (key & (a.page_size - 1)) * my_bytes;
+    };
+    auto copy = [&](const void* cache, int64_t at) -> bool {
+      const uint32_t st = filled % L::kPacks, use = filled / L::kPacks;
+      ok = ok && (use == 0 || wait_w(kBarPackEmpty + st, (use - 1) & 1));
+      if (!ok) return false;
+      const uint32_t runs = __popc(__ballot_sync(0xffffffffu, at >= 0)) / 2;
+      if (lane == 0) mbar_arrive_expect_tx(bar(kBarPackFull + st), runs * per_run * kv4::slot_bytes(D));
+      __syncwarp();
+      ++filled;
+      if (at >= 0)
+        bulk_copy(smem_addr(smem) + L::kPack + st * L::kPackBytes + dst, static_cast<const uint8_t*>(cache) + at,
+                  per_run * my_bytes, bar(kBarPackFull + st));
+      return true;
+    };
+    while (ok && walk.next(P, g)) {
+      const int n = g.j1 - g.j0;
+      // of the tile whose values come next, of the one whose keys come last, of the two behind it
+      int64_t v_at = -1, k_last = -1, k_at = from(g, g.j0), k_next = n > 1 ? from(g, g.j0 + 1) : -1;
+      in_order(n, [&](auto values, int t) {
+        if constexpr (decltype(values)::value) return copy(a.V_cache, t + 1 < n ? v_at : k_last);
+        v_at = k_last;   // (the values of a tile come behind the keys of the next, but for the last tile's)
+        k_last = k_at;
+        k_at = k_next;
+        k_next = t + 2 < n ? from(g, g.j0 + t + 2) : -1;
+        return copy(a.K_cache, k_last);
+      });
+    }
+    // no copy of this CTA is in flight when it ends
+    for (uint32_t k = filled > L::kPacks ? filled - L::kPacks : 0; k < filled; ++k)
+      mbar_wait(bar(kBarPackFull + k % L::kPacks), (k / L::kPacks) & 1, kWaitLimit);
+  } else if (FP4 && warp == kQWarp) {
+    // ------------------------------------------------------------------ query tiles in fp16
+    // A row of D/8 lanes.  A bf16 row is multiplied by the power of two that takes its largest value to
+    // [2^14, 2^15): exact for what is not 2^-31 of that; the softmax multiplies its scores by the inverse.
+    constexpr int kLanes = D / 8, kAtOnce = 32 / kLanes, kAhead = 4;
+    const float c = a.scale * P.k_scale * kLog2e;
+    float* factors = reinterpret_cast<float*>(smem + L::kFactors);
+    uint32_t pos = 0;
+    bool ok = true;
+    while (ok && walk.next(P, g)) {
+      const int n = g.rows > P.tokens ? 2 : 1;
+      for (int k = 0; ok && k < n; ++k, ++pos) {
+        const uint32_t st = pos & 1, use = pos >> 1;
+        ok = use == 0 || wait_w(kBarQEmpty + st, (use - 1) & 1);
+        if (!ok) break;
+        const int live = min(P.tokens, g.rows - k * P.tokens) * G;
+        uint8_t* tile = smem + L::kQ + st * L::kQBytes;
+        for (int r0 = 0; r0 < live; r0 += kAtOnce * kAhead) {
+          uint4 q[kAhead];
+#pragma unroll
+          for (int u = 0; u < kAhead; ++u) {
+            const int r = r0 + u * kAtOnce + lane / kLanes;
+            q[u] = make_uint4(0u, 0u, 0u, 0u);
+            if (r < live) {
+              const int tok = (int)((uint32_t)r / (uint32_t)G);
+              q[u] = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.Q) +
+                                                     (g.t0 + k * P.tokens + tok) * a.ldq +
+                                                     (int64_t)(g.h * G + r - tok * G) * D + 8 * (lane % kLanes));
+            }
+          }
+#pragma unroll
+          for (int u = 0; u < kAhead; ++u) {
+            const int r = r0 + u * kAtOnce + lane / kLanes;
+            uint32_t w[4] = {q[u].x, q[u].y, q[u].z, q[u].w};
+            int up = 127;   // exponent field of the row's power of two
+            if constexpr (TYPE == QMM_BF16) {
+              uint32_t top = 0;
+#pragma unroll
+              for (int e = 0; e < 4; ++e) top = max(top, max(w[e] & 0x7FFFu, w[e] >> 16 & 0x7FFFu));
+#pragma unroll
+              for (int off = kLanes / 2; off >= 1; off >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, off));
+              up = top == 0 || top >= 0x7F80u ? 127 : min(254, 268 - (int)(top >> 7));
+              const float f = __uint_as_float((uint32_t)up << 23);
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                w[e] = pack2<QMM_F16>(__uint_as_float(w[e] << 16) * f, __uint_as_float(w[e] & 0xFFFF0000u) * f);
+            }
+            if (r < live) {
+              const int d = lane % kLanes;   // 16 bytes of the row
+              *reinterpret_cast<uint4*>(tile + (d / 8) * L::kQHalf + r * 128 + ((d % 8) ^ (r & 7)) * 16) =
+                  make_uint4(w[0], w[1], w[2], w[3]);
+              if (d == 0) factors[(pos % kFactorTiles) * kRows + r] = scalbnf(c, 127 - up);
+            }
+          }
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(kBarQFull + st));
+      }
+    }
+  } else if (FP4 && warp >= kFirstDequantWarp) {
+    // ------------------------------------------------------------------ 4 bits to fp16
+    // A thread takes a block of 16 values: a code times its scale is exact in fp16 (two and four
+    // significant bits).  Rows of values behind the last key are zeroed, and so are NaN blocks among the keys that
+    // only some rows of the block see (a draft's last keys); attn_combine_kernel adds those back.
+    constexpr int kBlocks = D / kv4::kBlock, kUnits = kTile * kBlocks / (32 * kDequantWarps);
+    const int me = (warp - kFirstDequantWarp) * 32 + lane;
+    uint32_t taken = 0, filled[2] = {0, 0}, items = 0, segs = 0;
+    bool ok = true;
+    while (ok && walk.next(P, g)) {
+      const int n = g.j1 - g.j0;
+      const bool pair = g.rows > P.tokens;
+      const int clean_from = g.own ? clampi(g.first_keys, 0, g.keys) : g.keys;
+      ++segs;
+      ok = in_order(n, [&](auto values, int t) {
+        constexpr bool kValues = decltype(values)::value;
+        const uint32_t users = pair ? 2 : (items + t) & 1;
+        const uint32_t from = taken % L::kPacks, st = filled[kValues] % kS, use = filled[kValues] / kS;
+        if (!wait_w(kBarPackFull + from, (taken / L::kPacks) & 1)) return false;
+        if (use > 0 && !wait_w((kValues ? kBarEmptyV : kBarEmptyK) + st, (use - 1) & 1)) return false;
+        const uint8_t* src = smem + L::kPack + from * L::kPackBytes;
+        uint8_t* dst = smem + (kValues ? L::kV : L::kK) + st * L::kTileBytes;
+        const int base = (g.j0 + t) * kTile;
+        uint2 code[kUnits];
+        uint32_t scale[kUnits];
+#pragma unroll
+        for (int u = 0; u < kUnits; ++u) {
+          const int unit = u * 32 * kDequantWarps + me;
+          code[u] = *reinterpret_cast<const uint2*>(src + unit * 8);
+          scale[u] = src[kTile * (D / 2) + unit];
+        }
+#pragma unroll
+        for (int u = 0; u < kUnits; ++u) {
+          const int unit = u * 32 * kDequantWarps + me, key = unit / kBlocks, b = unit % kBlocks;
+          const uint32_t s = e4m3x2_pair(scale[u] * 0x101u);
+          uint32_t lo[4], hi[4];
+          e2m1x8_pairs(code[u].x, lo);
+          e2m1x8_pairs(code[u].y, hi);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            lo[e] = mul2(lo[e], s);
+            hi[e] = mul2(hi[e], s);
+          }
+          if constexpr (kValues) {
+            const bool odd = (scale[u] & 0x7Fu) == kv4::kScaleNaN && base + key >= clean_from;
+            if (base + key >= g.keys || odd) {
+              if (base + key < g.keys) *reinterpret_cast<volatile uint32_t*>(&M.odd[segs & 7]) = segs;
+#pragma unroll
+              for (int e = 0; e < 4; ++e) lo[e] = hi[e] = 0u;
+            }
+          }
+          uint8_t* row = dst + (b / 4) * L::kHalf + key * 128;
+          // (the halves of a key in turn: eight neighbouring threads write to eight different 16-byte columns)
+          const int c0 = 2 * (b % 4), turn = b / 4 & 1;
+          const uint4 first = turn ? make_uint4(hi[0], hi[1], hi[2], hi[3]) : make_uint4(lo[0], lo[1], lo[2], lo[3]);
+          const uint4 other = turn ? make_uint4(lo[0], lo[1], lo[2], lo[3]) : make_uint4(hi[0], hi[1], hi[2], hi[3]);
+          *reinterpret_cast<uint4*>(row + ((c0 + turn) ^ (key & 7)) * 16) = first;
+          *reinterpret_cast<uint4*>(row + ((c0 + 1 - turn) ^ (key & 7)) * 16) = other;
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(bar((kValues ? kBarFullV : kBarFullK) + kS * users + st));
+          mbar_arrive(bar(kBarPackEmpty + from));
+        }
+        ++taken;
+        ++filled[kValues];
+        return true;
+      });
+      items += pair ? 2 * n : n;
+    }
+  } else if (warp == kLoadWarp) {
     // ------------------------------------------------------------------ keys and values
     // A tile is one box per page (or 64 keys of a longer page) and half of 64 values; lane k copies
     // box k / halves of half k % halves.  Pages behind the last key are not read.
@@ -501,7 +721,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
     // products.  The scores of item j + 1 are issued ahead of the values of item j.  The empty barriers of keys and values count two arrivals, and the only user of a
     // tile makes both; those of query tiles count one of each lane.
     if (elect_one()) {
-      constexpr bool kBf16 = TYPE == QMM_BF16;
+      constexpr bool kBf16 = kProduct == QMM_BF16;
       constexpr uint32_t kIdS = tc::idesc_16_f32(128, kTile, kBf16, false);
       constexpr uint32_t kIdO = tc::idesc_16_f32(128, D, kBf16, true);
       const uint64_t dq = tc::smem_desc_sw128(smem_addr(smem + L::kQ), 16, 1024);
@@ -614,10 +834,11 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
     const uint32_t lanes = (uint32_t)(warp % kLaneWarps) << 21;   // first TMEM lane << 16
     const uint32_t tS = tmem + lanes + kTile * l, tP = tmem + lanes + 2 * kTile + kTile * l;
     const uint32_t tO = tmem + lanes + 4 * kTile;
-    const float c = a.scale * kLog2e;
+    float c = a.scale * kLog2e;
     float2* stats = reinterpret_cast<float2*>(smem + L::kStats);
     uint32_t parity = 0;   // of the next phases of the value stages' full barriers (single, both)
     uint32_t pos = 0, seen = 0, joins = 0, segs = 0, items = 0, ends = 0;
+    [[maybe_unused]] uint32_t tiles_q = 0;   // query tiles before the segment's
     bool ok = true;
     while (ok && walk.next(P, g)) {
       const int n = g.j1 - g.j0;
@@ -643,9 +864,14 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
         const uint32_t at = pair ? kS + st : st;
         parity ^= 1u << at;
         ok = wait_w(kBarS + l, buf);   // (and with S the products of two items before, the last readers of this p)
+        if constexpr (FP4) {   // (the product that made S waited for the query tile, and its rows' factors with it)
+          if (ok && i == first)
+            c = row < live ? reinterpret_cast<const float*>(smem + L::kFactors)[((tiles_q + (pair ? l : 0)) % kFactorTiles) * kRows + row]
+                           : 0.0f;
+        }
         // value rows that a weight of 0 must not meet
         const int upto = min(g.keys, base + kTile) - base;
-        if (ok && clean_from < base + kTile && (upto < kTile || g.own)) {
+        if (!FP4 && ok && clean_from < base + kTile && (upto < kTile || g.own)) {
           ok = wait_w(kBarFullV + kS * (pair ? 2 : l) + st, !(parity >> at & 1));
           if (!ok) break;
           uint8_t* V = smem + L::kV + st * L::kTileBytes;
@@ -709,7 +935,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
             }
           }
           if (grew) top = now;
-          const float off = top == -INFINITY ? 0.0f : -top;
+          const float off = top == -INFINITY ? 0.0f : FP4 ? kLift - top : -top;
           const uint64_t cc = f2pack(c, c), oo = f2pack(off, off);
           uint64_t part0 = 0, part1 = 0;   // sums of weights, two fp32 each
 #pragma unroll
@@ -719,8 +945,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
             const float p0 = exp2_fast(x.x), p1 = exp2_fast(x.y), p2 = exp2_fast(y.x), p3 = exp2_fast(y.y);
             part0 = add2(part0, f2pack(p0, p1));
             part1 = add2(part1, f2pack(p2, p3));
-            s[k / 2] = pack2<TYPE>(p0, p1);
-            s[k / 2 + 1] = pack2<TYPE>(p2, p3);
+            s[k / 2] = pack2<kProduct>(p0, p1);
+            s[k / 2 + 1] = pack2<kProduct>(p2, p3);
           }
           tc::st_x32(tP + kTile / 2 * buf, s);
           const float2 u = f2unpack(part0), v = f2unpack(part1);
@@ -737,6 +963,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
         if (st >= kS) st -= kS;
       }
       pos += n;   // value tiles before the next segment's
+      tiles_q += pair ? 2 : 1;
       if (!ok) break;
 
       // ---- the segment's sums to the workspace
@@ -767,6 +994,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
           st.sum = (!(s0.x == -INFINITY && s0.y == 0.0f) ? s0.y * exp2_fast(s0.x - st.top) : 0.0f) +
                    (!(s1.x == -INFINITY && s1.y == 0.0f) ? s1.y * exp2_fast(s1.x - st.top) : 0.0f);
         }
+        if constexpr (FP4) st.top -= kLift;
         (inside ? P.s_cta : P.s_rows)[record(row)] = st;
       }
       // O: 16 rows x 32 columns at a time; the four threads of a row write 128 bytes of it.  A row's
@@ -850,7 +1078,7 @@ __device__ __forceinline__ int column_of(int p) {
   return (p & ~31) + 8 * ((p & 7) >> 1) + 2 * ((p & 31) >> 3) + (p & 1);
 }
 
-template <int D, int TYPE, int SHARE>
+template <int D, int TYPE, int SHARE, bool FP4>
 __global__ void __launch_bounds__(32 * kCombineWarps) attn_combine_kernel(const __grid_constant__ Params P) {
   constexpr int kV = D / 32;   // values of a lane: positions kV * lane and on
   constexpr int kAhead = 8;    // records whose O a warp has in flight
@@ -1018,7 +1246,7 @@ __global__ void __launch_bounds__(32 * kCombineWarps) attn_combine_kernel(const 
     }
     top = best;
   }
-  const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+  const float inv = sum == 0.0f ? 0.0f : (FP4 ? P.v_scale : 1.0f) / sum;
 #pragma unroll
   for (int k = 0; k < kV; ++k) o[k] = sum == 0.0f ? 0.0f : o[k] * inv;
   if (odd) {
@@ -1028,6 +1256,14 @@ __global__ void __launch_bounds__(32 * kCombineWarps) attn_combine_kernel(const 
     for (int j = max(0, s.len - s.m); j < sees; ++j) {
       const int page = a.pages[b * a.pages_per_stream + j / a.page_size];
       if (page < 0 || page >= a.n_slots / a.page_size) continue;
+      if constexpr (FP4) {
+        const uint8_t* scales = static_cast<const uint8_t*>(a.V_cache) + kv4::run_at(page, head / G, a.Hk, a.page_size, D) +
+                                a.page_size * (D / 2) + (j % a.page_size) * (D / 16);
+#pragma unroll
+        for (int k = 0; k < kV; ++k)
+          if ((scales[column_of(kV * lane + k) / kv4::kBlock] & 0x7Fu) == kv4::kScaleNaN) extra[k] = NAN;
+        continue;
+      }
       const int64_t at = (((int64_t)page * a.page_size + j % a.page_size) * a.Hk + head / G) * D;
 #pragma unroll
       for (int k = 0; k < kV; ++k) {
@@ -1076,22 +1312,25 @@ bool tensor_map(CUtensorMap* m, const void* p, int D, int H, int64_t n, int64_t 
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int D, int TYPE>
+template <int D, int TYPE, bool FP4>
 cudaError_t set_smem_attr() {
   static DeviceOnce once;
   int dev = 0;
   const cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   return once.run(dev, cudaSuccess, [] {
-    return cudaFuncSetAttribute(attn_kernel<D, TYPE>, cudaFuncAttributeMaxDynamicSharedMemorySize, Smem<D>::kTotal);
+    return cudaFuncSetAttribute(attn_kernel<D, TYPE, FP4>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                Smem<D, FP4>::kTotal);
   });
 }
 
-template <int D, int TYPE>
-cudaError_t launch(const qmm_attn_args& a, void* workspace, cudaStream_t stream) {
+template <int D, int TYPE, bool FP4>
+cudaError_t launch(const qmm_attn_args& a, float k_scale, float v_scale, void* workspace, cudaStream_t stream) {
   const int G = a.Hq / a.Hk;
   Params P;
   P.a = a;
+  P.k_scale = k_scale;
+  P.v_scale = v_scale;
   P.tokens = kRows / G;
   P.n_pages = (int)(a.n_slots / a.page_size);
   P.page_shift = 31 - __builtin_clz((unsigned)a.page_size);
@@ -1103,11 +1342,11 @@ cudaError_t launch(const qmm_attn_args& a, void* workspace, cudaStream_t stream)
   P.s_cta = reinterpret_cast<RowStat*>(ws + sp.s_cta);
   get_wait_limit(&P.wait_polls, &P.wait_ns);
   const int per_box = a.page_size < kTile ? a.page_size : kTile;
-  if (!tensor_map(&P.mapQ, a.Q, D, a.Hq, a.T, a.ldq, G, P.tokens, TYPE) ||
+  if (!FP4 && (!tensor_map(&P.mapQ, a.Q, D, a.Hq, a.T, a.ldq, G, P.tokens, TYPE) ||
       !tensor_map(&P.mapK, a.K_cache, D, a.Hk, a.n_slots, (int64_t)a.Hk * D, 1, per_box, TYPE) ||
-      !tensor_map(&P.mapV, a.V_cache, D, a.Hk, a.n_slots, (int64_t)a.Hk * D, 1, per_box, TYPE))
+      !tensor_map(&P.mapV, a.V_cache, D, a.Hk, a.n_slots, (int64_t)a.Hk * D, 1, per_box, TYPE)))
     return cudaErrorInvalidValue;
-  cudaError_t e = set_smem_attr<D, TYPE>();
+  cudaError_t e = set_smem_attr<D, TYPE, FP4>();
   if (e != cudaSuccess) return e;
   const int sms = sm_count();
   if (sms < 1) return cudaErrorNoDevice;
@@ -1115,15 +1354,15 @@ cudaError_t launch(const qmm_attn_args& a, void* workspace, cudaStream_t stream)
   // each waits for it before it reads or writes memory.
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(sms < kMaxCtas ? sms : kMaxCtas);
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = Smem<D>::kTotal;
+  cfg.blockDim = dim3(kThreads<FP4>);
+  cfg.dynamicSmemBytes = Smem<D, FP4>::kTotal;
   cfg.stream = stream;
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, attn_kernel<D, TYPE>, P);
+  e = cudaLaunchKernelEx(&cfg, attn_kernel<D, TYPE, FP4>, P);
   if (e != cudaSuccess) return e;
   cfg.gridDim = dim3(a.T, (a.Hq + kCombineWarps - 1) / kCombineWarps);
   cfg.blockDim = dim3(32 * kCombineWarps);
@@ -1134,9 +1373,18 @@ cudaError_t launch(const qmm_attn_args& a, void* workspace, cudaStream_t stream)
   // 26.8 (27.0), 960 rows 31.4 (29.0).  640 rows of 8 streams' own 3000 to 6000 keys 15.0 (17.4).
   if ((int64_t)a.T * a.Hq * 4 <= 3 * kCombineWarps * (int64_t)sms) {
     cfg.gridDim.y = (a.Hq * 4 + kCombineWarps - 1) / kCombineWarps;
-    return cudaLaunchKernelEx(&cfg, attn_combine_kernel<D, TYPE, 4>, P);
+    return cudaLaunchKernelEx(&cfg, attn_combine_kernel<D, TYPE, 4, FP4>, P);
   }
-  return cudaLaunchKernelEx(&cfg, attn_combine_kernel<D, TYPE, 1>, P);
+  return cudaLaunchKernelEx(&cfg, attn_combine_kernel<D, TYPE, 1, FP4>, P);
+}
+
+template <bool FP4>
+cudaError_t launch_any(const qmm_attn_args& a, float k_scale, float v_scale, void* workspace, cudaStream_t stream) {
+  if (a.D == 64)
+    return a.type == QMM_BF16 ? launch<64, QMM_BF16, FP4>(a, k_scale, v_scale, workspace, stream)
+                              : launch<64, QMM_F16, FP4>(a, k_scale, v_scale, workspace, stream);
+  return a.type == QMM_BF16 ? launch<128, QMM_BF16, FP4>(a, k_scale, v_scale, workspace, stream)
+                            : launch<128, QMM_F16, FP4>(a, k_scale, v_scale, workspace, stream);
 }
 
 }  // namespace
@@ -1144,9 +1392,13 @@ cudaError_t launch(const qmm_attn_args& a, void* workspace, cudaStream_t stream)
 size_t attn_workspace_bytes(const qmm_attn_args& a) { return Space(a).total; }
 
 cudaError_t launch_attn(const qmm_attn_args& a, void* workspace, cudaStream_t stream) {
-  if (a.D == 64)
-    return a.type == QMM_BF16 ? launch<64, QMM_BF16>(a, workspace, stream) : launch<64, QMM_F16>(a, workspace, stream);
-  return a.type == QMM_BF16 ? launch<128, QMM_BF16>(a, workspace, stream) : launch<128, QMM_F16>(a, workspace, stream);
+  return launch_any<false>(a, 1.0f, 1.0f, workspace, stream);
+}
+
+size_t attn_fp4_workspace_bytes(const qmm_attn_fp4_args& a) { return Space(a.base).total; }
+
+cudaError_t launch_attn_fp4(const qmm_attn_fp4_args& a, void* workspace, cudaStream_t stream) {
+  return launch_any<true>(a.base, a.k_scale, a.v_scale, workspace, stream);
 }
 
 cudaError_t read_and_clear_attn_status(unsigned* out) {
