@@ -1,16 +1,18 @@
 // qmm_sample.cu — the token of every row from its logits, and how many drafted tokens stand (qmm_sample).
 //
-// Weights.  w = exp((x - max) / T) as an integer W = w 2^43, to a unit or two: two neighbouring tokens lie 2^-18 of the
+// Weights.  w = exp((x - max) / T) as an integer W = w 2^42, to a unit or two: two neighbouring tokens lie 2^-18 of the
 // sum apart where 250000 share it, so fp32 weights would pick the wrong one in every hundredth row; integers
 // also make every sum independent of its order.  t = (x - max) log2(e) / T is formed in two fp32 words
-// (the difference and the product are exact but for 2^-45), split into -(n + j/2048) and a rest g of at most 2^-12, and
-//     W = (2^43 2^(-j/2048) 2^g) >> n,     2^g - 1 = g ln2 + (g ln2)^2/2 + (g ln2)^3/6
-// with 2^(43 - j/2048) from a table and the correction as a 32-bit integer.
+// (the difference and the product are exact but for 2^-45), split into -(n + j/1024) and a rest g of at most 2^-11, and
+//     W = (2^42 2^(-j/1024) 2^g) >> n,     2^g - 1 = g ln2 + (g ln2)^2/2 + (g ln2)^3/6
+// with 2^(42 - j/1024) from a table and the correction as a 32-bit integer.
 #include <cstdint>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
+#include <cooperative_groups.h>
 
+#include "q4k_device_once.h"
 #include "q4k_internal.h"
 
 namespace q4k {
@@ -18,15 +20,19 @@ namespace {
 
 __device__ unsigned g_status;   // this file's kernels' status word
 
-constexpr int kThreads = 1024;
-constexpr int kUnit = 43;              // a weight of 1 is 2^kUnit; kMaxV of them stay below 2^62
-constexpr int kSteps = 2048;           // of the table, for one octave
+namespace cg = cooperative_groups;
+
+constexpr int kThreads = 512;
+constexpr int kUnit = 42;              // a weight of 1 is 2^kUnit; QMM_SAMPLE_MAX_V of them stay below 2^62
+constexpr int kSteps = 1024;           // of the table, for one octave
+constexpr int kBinBits = 11, kBins = 1 << kBinBits;
+constexpr int kMaxCluster = 16, kMaxRun = ((QMM_SAMPLE_MAX_V / kMaxCluster + kThreads - 1) / kThreads) | 1;
 static_assert(QMM_SAMPLE_MAX_V <= (1 << 19), "sums of weights");
 
 using u64 = unsigned long long;
 
-// 2^(43 - j/2048), j = 0 .. 2047: 2^(-1/2048) by eleven integer square roots of 1/2, then its powers, with 62 bits
-// behind the point (an error of 2^-51 at the end).
+// 2^(42 - j/1024), j = 0 .. 1023: 2^(-1/1024) by ten integer square roots of 1/2, then its powers, with 62 bits
+// behind the point (an error of 2^-52 at the end).
 struct Table {
   u64 v[kSteps];
 };
@@ -41,7 +47,7 @@ constexpr u64 isqrt(unsigned __int128 x) {
 constexpr Table make_table() {
   constexpr int kQ = 62;
   u64 r = u64(1) << (kQ - 1);
-  for (int k = 0; k < 11; ++k) r = isqrt((unsigned __int128)r << kQ);
+  for (int k = 0; k < 10; ++k) r = isqrt((unsigned __int128)r << kQ);
   Table t{};
   u64 at = u64(1) << kQ;
   for (int j = 0; j < kSteps; ++j) {
@@ -74,18 +80,18 @@ __device__ __forceinline__ u64 weight(float x, float top, Slope c, const u64* ta
   const float u = __fmaf_rn(th, -(float)kSteps, kMagic);
   const uint32_t k = __float_as_uint(u) - __float_as_uint(kMagic);
   const float gh = __fmaf_rn(u - kMagic, 1.0f / kSteps, th);
-  // 2^g - 1 in units of 2^-43: the leading product exact in two words
+  // 2^g - 1 in units of 2^-42: the leading product exact in two words
   constexpr float kLn2Hi = 0.693147182464599609375f, kLn2Lo = -1.904654323148236017e-09f;
   const float p = gh * kLn2Hi;
   const float low = __fmaf_rn(gh, kLn2Hi, -p) + __fmaf_rn(gh, kLn2Lo, tl * kLn2Hi) +
                     gh * gh * __fmaf_rn(gh, 0.0555041087f, 0.2402265070f);
-  const float big = p * 0x1p43f, v = __fmaf_rn(big, 0x1p-9f, kMagic), vi = v - kMagic;
-  const float rest = __fmaf_rn(vi, -0x1p9f, big) + low * 0x1p43f;
+  const float big = p * 0x1p42f, v = __fmaf_rn(big, 0x1p-9f, kMagic), vi = v - kMagic;
+  const float rest = __fmaf_rn(vi, -0x1p9f, big) + low * 0x1p42f;
   const int grow = ((int)(__float_as_uint(v) - __float_as_uint(kMagic)) << 9) +
                    (int)(__float_as_uint(rest + kMagic) - __float_as_uint(kMagic));
   const u64 base = table[k & (kSteps - 1)];
   const int n = (int)(k / kSteps);
-  const long long more = ((long long)(int)(base >> 13) * grow + (1 << 29)) >> 30;   // base * grow / 2^43
+  const long long more = ((long long)(int)(base >> 12) * grow + (1 << 29)) >> 30;   // base * grow / 2^42
   return (base + more + ((u64(1) << n) >> 1)) >> n;   // (without rounding 250000 small weights would lose half a unit each)
 }
 
@@ -124,168 +130,461 @@ __device__ __forceinline__ uint32_t key_of(float x) {
   return b & 0x80000000u ? ~b : b | 0x80000000u;
 }
 
-__device__ __forceinline__ u64 block_sum(u64 v, u64* space) {
-#pragma unroll
-  for (int off = 16; off >= 1; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
-  __syncthreads();
-  if ((threadIdx.x & 31) == 0) space[threadIdx.x >> 5] = v;
-  __syncthreads();
-  v = space[threadIdx.x & 31];
-#pragma unroll
-  for (int off = 16; off >= 1; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
-  return v;
-}
-// Sum over the threads before this one.
-__device__ __forceinline__ u64 block_before(u64 v, u64* space) {
-  u64 upto = v;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-#pragma unroll
-  for (int off = 1; off < 32; off <<= 1) {
-    const u64 x = __shfl_up_sync(0xffffffffu, upto, off);
-    if (lane >= off) upto += x;
-  }
-  __syncthreads();
-  if (lane == 31) space[warp] = upto;
-  __syncthreads();
-  u64 before = upto - v;
-  for (int w = 0; w < warp; ++w) before += space[w];
-  return before;
-}
+// A row lies in the shared memory of a cluster's CTAs, in order of the tokens: a CTA has a slice, a thread a run of it (an odd
+// number of floats, so that a warp's runs lie in different banks).
+struct Cta {
+  u64 part[4];            // this CTA's part of a sum, a maximum or a scan over the cluster; used in turn
+  u64 scan[kThreads / 32];
+  float scan_f[2][kThreads / 32];
+  union {                 // of this CTA
+    uint32_t count[kBins];
+    u64 mass[kBins / 2];
+  };
+  union {                 // of the cluster
+    uint32_t total[kBins];
+    u64 mass_total[kBins / 2];
+  };
+  u64 found[2];           // what the thread that found it tells the others
+  u64 table[kSteps];
+};
 
-// A CTA per row; each step of the two searches (for the top-k and the top-p border among the keys) is a pass.
+struct Keys {             // lo <= key <= hi
+  uint32_t lo, hi;
+};
+
 template <int TYPE>
-__global__ void __launch_bounds__(kThreads) sample_kernel(const __grid_constant__ qmm_sample_args a) {
-  __shared__ u64 space[32];
-  __shared__ int found;
-  const int t = blockIdx.x, V = a.V;
-  const void* row = static_cast<const uint8_t*>(a.logits) + t * a.ld * (TYPE == QMM_F32 ? 4 : 2);
-  const int per = (V + kThreads - 1) / kThreads, i0 = min(V, (int)threadIdx.x * per), i1 = min(V, i0 + per);
-  // the largest logit and its lowest index
-  u64 best = 0;
-  for (int i = i0; i < i1; ++i) {
-    const u64 v = (u64)key_of(logit<TYPE>(row, i)) << 32 | (0xFFFFFFFFu - (uint32_t)i);
-    best = v > best ? v : best;
-  }
+struct Sampler {
+  Cta& S;
+  float* x;               // the slice
+  const cg::cluster_group cluster = cg::this_cluster();
+  int turn = 0;           // of part
+  int run, first;         // floats of a thread; index of its first one in the row
+  const float* mine;
+  float top;
+  Slope c;
+
+  __device__ __forceinline__ u64 weight_of(float v) const { return v == -INFINITY ? u64(0) : weight(v, top, c, S.table); }
+
+  __device__ __forceinline__ u64 warp_sum(u64 v) {
 #pragma unroll
-  for (int off = 16; off >= 1; off >>= 1) {
-    const u64 v = __shfl_xor_sync(0xffffffffu, best, off);
-    best = v > best ? v : best;
+    for (int off = 16; off >= 1; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
+    return v;
   }
-  if ((threadIdx.x & 31) == 0) space[threadIdx.x >> 5] = best;
-  if (threadIdx.x == 0) found = -1;
-  __syncthreads();
-  for (int w = 0; w < 32; ++w) best = space[w] > best ? space[w] : best;
-  const int first = (int)(0xFFFFFFFFu - (uint32_t)best);
-  const float top = logit<TYPE>(row, first), temperature = a.temperature ? a.temperature[t] : 1.0f;
+  // The parts of the cluster's CTAs, one a lane; they may be written again four calls later.
+  __device__ __forceinline__ u64 exchange(u64 v) {
+    if (threadIdx.x == 0) S.part[turn] = v;
+    cluster.sync();
+    const int lane = threadIdx.x & 31;
+    u64 got = 0;
+    if (lane < (int)cluster.num_blocks()) got = *cluster.map_shared_rank(&S.part[turn], lane);
+    turn = (turn + 1) & 3;
+    return got;
+  }
+  __device__ __forceinline__ u64 cluster_sum(u64 v) {
+    v = warp_sum(v);
+    if ((threadIdx.x & 31) == 0) S.scan[threadIdx.x >> 5] = v;
+    __syncthreads();
+    v = (threadIdx.x & 31) < kThreads / 32 ? S.scan[threadIdx.x & 31] : 0;
+    return warp_sum(exchange(warp_sum(v)));
+  }
+  __device__ __forceinline__ u64 cluster_max(u64 v) {
+    auto most = [](u64 m) {
+#pragma unroll
+      for (int off = 16; off >= 1; off >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, off));
+      return m;
+    };
+    v = most(v);
+    if ((threadIdx.x & 31) == 0) S.scan[threadIdx.x >> 5] = v;
+    __syncthreads();
+    v = (threadIdx.x & 31) < kThreads / 32 ? S.scan[threadIdx.x & 31] : 0;
+    return most(exchange(most(v)));
+  }
+  // Sum over the threads of the CTA before this one; all: over the CTA.
+  template <class N>
+  __device__ __forceinline__ N block_before(N v, N* space, N* all) {
+    N upto = v;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const N u = __shfl_up_sync(0xffffffffu, upto, off);
+      if (lane >= off) upto += u;
+    }
+    __syncthreads();
+    if (lane == 31) space[warp] = upto;
+    __syncthreads();
+    N before = upto - v, sum = 0;
+#pragma unroll
+    for (int w = 0; w < kThreads / 32; ++w) {
+      if (w < warp) before += space[w];
+      sum += space[w];
+    }
+    *all = sum;
+    return before;
+  }
+  // Sum over the threads of the cluster before this one; all: over the cluster.
+  __device__ __forceinline__ u64 cluster_before(u64 v, u64* all) {
+    u64 sum;
+    const u64 before = block_before<u64>(v, S.scan, &sum);
+    const u64 parts = exchange(sum);
+    *all = warp_sum(parts);
+    return before + warp_sum((threadIdx.x & 31) < cluster.block_rank() ? parts : 0);
+  }
+
+  // Sums over the cluster's values that `in` takes, by bin(x), in `total` of every CTA: counts (N uint32_t, kBins of them) or
+  // weights (N u64, kBins / 2).
+  template <class N, class In, class Bin>
+  __device__ __forceinline__ void histogram(In&& in, Bin&& bin) {
+    constexpr int kN = kBins * 4 / (int)sizeof(N), kPer = 16 / (int)sizeof(N);
+    N* count = reinterpret_cast<N*>(S.count);
+    N* total = reinterpret_cast<N*>(S.total);
+    for (int b = threadIdx.x; b < kBins; b += kThreads) S.count[b] = S.total[b] = 0;
+    __syncthreads();
+    for (int j = 0; j < run; ++j) {
+      const float v = mine[j];
+      if (!in(v, first + j)) continue;
+      if constexpr (sizeof(N) == 4) atomicAdd(&count[bin(v)], 1u);
+      else atomicAdd(&count[bin(v)], weight_of(v));
+    }
+    cluster.sync();
+    // each CTA adds up its share of the bins from all CTAs, 16 bytes of one CTA a thread, and gives it to all
+    const int C = (int)cluster.num_blocks(), vecs = kThreads / C, rank = (int)cluster.block_rank();
+    const int peer = threadIdx.x / vecs, at = rank * (kN / C) + kPer * (threadIdx.x % vecs);
+    static_assert(kThreads * kPer == kN, "16 bytes a thread");
+    if (C > 1) {
+      const uint4 v = *cluster.map_shared_rank(reinterpret_cast<uint4*>(&count[at]), peer);
+      N part[kPer];
+      *reinterpret_cast<uint4*>(part) = v;
+#pragma unroll
+      for (int q = 0; q < kPer; ++q)
+        if (part[q]) atomicAdd(&total[at + q], part[q]);
+      __syncthreads();
+      if (peer != rank)
+        *cluster.map_shared_rank(reinterpret_cast<uint4*>(&total[at]), peer) = *reinterpret_cast<uint4*>(&total[at]);
+      cluster.sync();
+    } else {
+      *reinterpret_cast<uint4*>(&total[at]) = *reinterpret_cast<const uint4*>(&count[at]);
+      __syncthreads();
+    }
+  }
+  static constexpr int kMine = kBins / kThreads;   // bins of a thread
+
+  // The first bin whose sums reach n >= 1, with those before it.
+  template <class N>
+  __device__ __forceinline__ void find(u64 n, int* bin, u64* before) {
+    constexpr int kMine = kBins * 4 / (int)sizeof(N) / kThreads;
+    const N* total = reinterpret_cast<const N*>(S.total);
+    u64 sum = 0, all;
+#pragma unroll
+    for (int q = 0; q < kMine; ++q) sum += total[kMine * threadIdx.x + q];
+    u64 at = block_before<u64>(sum, S.scan, &all);
+    if (at < n && at + sum >= n) {
+#pragma unroll
+      for (int q = 0; q < kMine; ++q) {
+        const u64 m = total[kMine * threadIdx.x + q];
+        if (at < n && at + m >= n) {
+          S.found[0] = kMine * threadIdx.x + q;
+          S.found[1] = at;
+        }
+        at += m;
+      }
+    }
+    __syncthreads();
+    *bin = (int)S.found[0];
+    *before = S.found[1];
+    __syncthreads();
+  }
+
+  // Bins b1 .. b2 in which the weights' sum reaches `share` of itself, by bounds low(b) <= w <= high(b) of the weights of
+  // a bin.
+  template <class Low, class High>
+  __device__ __forceinline__ void find_weight(float share, Low&& low, High&& high, int* b1, int* b2) {
+    constexpr float kSlack = 1e-4f;   // beyond the roundings of these fp32 sums
+    float l[kMine], h[kMine], sum_l = 0.0f, sum_h = 0.0f, all_l, all_h;
+#pragma unroll
+    for (int q = 0; q < kMine; ++q) {
+      const int b = kMine * threadIdx.x + q;
+      const float n = (float)S.total[b];
+      l[q] = n > 0.0f ? n * low(b) * (1.0f - kSlack) : 0.0f;
+      h[q] = n > 0.0f ? n * high(b) * (1.0f + kSlack) : 0.0f;
+      sum_l += l[q];
+      sum_h += h[q];
+    }
+    float at_l = block_before<float>(sum_l, S.scan_f[0], &all_l), at_h = block_before<float>(sum_h, S.scan_f[1], &all_h);
+    const float lo = share * all_l * (1.0f - kSlack), hi = share * all_h * (1.0f + kSlack);
+    if (threadIdx.x == 0) S.found[0] = S.found[1] = kBins - 1;
+    __syncthreads();
+    int first_h = kBins, first_l = kBins;
+#pragma unroll
+    for (int q = kMine - 1; q >= 0; --q) {
+      float up_h = at_h, up_l = at_l;
+#pragma unroll
+      for (int r = 0; r <= q; ++r) {
+        up_h += h[r];
+        up_l += l[r];
+      }
+      if (up_h >= lo) first_h = kMine * threadIdx.x + q;
+      if (up_l >= hi) first_l = kMine * threadIdx.x + q;
+    }
+    if (first_h < kBins) atomicMin(&S.found[0], (u64)first_h);
+    if (first_l < kBins) atomicMin(&S.found[1], (u64)first_l);
+    __syncthreads();
+    *b1 = (int)S.found[0];
+    *b2 = max(*b1, (int)S.found[1]);
+    __syncthreads();
+  }
+
+  // Narrows a range of keys to the one on which the sums from its highest key down reach n, by bins of 2^shift keys; the sums
+  // before that key.
+  template <class N, class In>
+  __device__ __forceinline__ u64 narrow(Keys& r, u64 n, In&& in) {
+    constexpr int kBits = sizeof(N) == 4 ? kBinBits : kBinBits - 1;
+    u64 sum = 0;
+    while (r.lo < r.hi) {
+      const int shift = max(0, 32 - __clz(r.hi - r.lo) - kBits);
+      int b;
+      u64 before;
+      histogram<N>([&](float v, int i) { const uint32_t key = key_of(v); return key >= r.lo && key <= r.hi && in(v, i); },
+                   [&](float v) { return (int)((r.hi - key_of(v)) >> shift); });
+      find<N>(n - sum, &b, &before);
+      sum += before;
+      r.hi -= (uint32_t)b << shift;
+      r.lo = max(r.lo, r.hi - ((1u << shift) - 1));
+    }
+    return sum;
+  }
+
+  // Of `r` distinct ties on a key, the index of the last one that stays; INT_MAX if all do.
+  template <class In>
+  __device__ __forceinline__ int tie_index(uint32_t key, u64 r, In&& in) {
+    u64 n = 0, all;
+    for (int j = 0; j < run; ++j) n += in(mine[j], first + j) && key_of(mine[j]) == key;
+    const u64 before = cluster_before(n, &all);
+    if (all <= r) return 0x7fffffff;
+    u64 index = 0;
+    if (before < r && before + n >= r) {
+      u64 at = before;
+      for (int j = 0; j < run; ++j)
+        if (in(mine[j], first + j) && key_of(mine[j]) == key && ++at == r) index = (u64)(first + j) + 1;
+    }
+    return (int)cluster_sum(index) - 1;
+  }
+};
+
+// The float of a key.
+__device__ __forceinline__ float float_of(uint32_t key) { return __uint_as_float(key & 0x80000000u ? key & 0x7FFFFFFFu : ~key); }
+
+// A cluster per row.  The border of top_k is found by counting: 2048 bins, first over the distance from the largest logit,
+// then over the keys of the bin in which the border lies, until a bin is one key; ties on it go by index.  For
+// top_p the counts bound the weights' sums (a bin's weights are within 2 % of each other), which leaves a few
+// bins; what lies above them is added up exactly, and from there bins of keys hold exact sums.
+template <int TYPE>
+__global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_constant__ qmm_sample_args a, int run, int vec) {
+  extern __shared__ __align__(16) uint8_t smem[];
+  Sampler<TYPE> R{*reinterpret_cast<Cta*>(smem), reinterpret_cast<float*>(smem + sizeof(Cta))};
+  Cta& S = R.S;
+  // launched early behind a launch that allows it: memory is read from here on
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const int rank = (int)R.cluster.block_rank();
+  const int t = blockIdx.x / (int)R.cluster.num_blocks(), V = a.V, slice = run * kThreads, begin = rank * slice;
+  const int n = max(0, min(V - begin, slice));
+  const uint8_t* row = static_cast<const uint8_t*>(a.logits) + t * a.ld * (TYPE == QMM_F32 ? 4 : 2);
+  R.run = run;
+  R.first = begin + (int)threadIdx.x * run;
+  R.mine = R.x + (int)threadIdx.x * run;
+
+  // the slice, its largest logit (the lowest index of equal ones) and its lowest finite one
+  u64 best = 0;
+  float least_x = INFINITY;
+  auto take = [&](int i, float v) {
+    v = v == v ? v + 0.0f : -INFINITY;   // (-0 and 0 are equal)
+    R.x[i] = v;
+    best = max(best, (u64)key_of(v) << 32 | (0xFFFFFFFFu - (uint32_t)(begin + i)));
+    if (v > -INFINITY) least_x = fminf(least_x, v);
+  };
+  constexpr int kPerVec = TYPE == QMM_F32 ? 4 : 8;
+  const int whole = vec ? n / kPerVec * kPerVec : 0;
+  for (int i = kPerVec * threadIdx.x; i < whole; i += kPerVec * kThreads) {
+    const uint4 w = *reinterpret_cast<const uint4*>(row + (int64_t)(begin + i) * (TYPE == QMM_F32 ? 4 : 2));
+    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int q = 0; q < kPerVec; ++q) {
+      if constexpr (TYPE == QMM_F32) take(i + q, __uint_as_float(u[q]));
+      else if constexpr (TYPE == QMM_BF16) take(i + q, __uint_as_float(q & 1 ? u[q / 2] & 0xFFFF0000u : u[q / 2] << 16));
+      else take(i + q, __half2float(__ushort_as_half((uint16_t)(u[q / 2] >> (16 * (q & 1))))));
+    }
+  }
+  for (int i = whole + threadIdx.x; i < n; i += kThreads) take(i, logit<TYPE>(row, begin + i));
+  for (int i = n + threadIdx.x; i < slice; i += kThreads) R.x[i] = -INFINITY;
+  for (int j = threadIdx.x; j < kSteps; j += kThreads) S.table[j] = kTable.v[j];
+  best = R.cluster_max(best);
+  const int argmax = (int)(0xFFFFFFFFu - (uint32_t)best);
+  const uint32_t top_key = (uint32_t)(best >> 32);
+  const float top = float_of(top_key), temperature = a.temperature ? a.temperature[t] : 1.0f;
+  R.top = top;
   if (top == -INFINITY || !(temperature > 0.0f)) {
-    if (threadIdx.x == 0) {
-      a.tokens[t] = top == -INFINITY ? -1 : first;
+    if (rank == 0 && threadIdx.x == 0) {
+      a.tokens[t] = top == -INFINITY ? -1 : argmax;
       if (a.logprobs) a.logprobs[t] = top == -INFINITY ? -INFINITY : 0.0f;
     }
+    R.cluster.sync();   // no CTA ends while another one reads its shared memory
     return;
   }
-  const Slope c = slope_of(temperature);
-  auto W = [&](float x) { return x == -INFINITY ? u64(0) : weight(x, top, c, kTable.v); };
-
-  // top_k: tokens above the key kk, and the first rk of those on it
+  R.c = slope_of(temperature);
   const int k = a.top_k ? a.top_k[t] : 0;
-  uint32_t kk = 0;
-  u64 rk = ~u64(0);
-  if (k > 0 && k < V) {
-    for (int bit = 31; bit >= 0; --bit) {
-      u64 n = 0;
-      for (int i = i0; i < i1; ++i) n += key_of(logit<TYPE>(row, i)) >= (kk | 1u << bit);
-      if (block_sum(n, space) >= (u64)k) kk |= 1u << bit;
-    }
-    u64 n = 0;
-    for (int i = i0; i < i1; ++i) n += key_of(logit<TYPE>(row, i)) > kk;
-    rk = k - block_sum(n, space);
+  const float p = a.top_p ? a.top_p[t] : 1.0f, mp = a.min_p ? a.min_p[t] : 0.0f;
+  const bool by_k = k > 0 && k < V, by_p = p < 1.0f;
+
+  // bins over the distance from the top, as far as the row goes, or as weights are above 0
+  float per = 0.0f, width = INFINITY;
+  auto bins_over = [&](float span) {
+    per = kBins / span;
+    if (!(span > 0.0f && per < INFINITY)) per = 0.0f;   // one bin
+    width = per > 0.0f ? span / kBins : INFINITY;
+  };
+  float whole_span = 0.0f;
+  if (by_k || by_p) {
+    const u64 low = ~R.cluster_max(~(u64)key_of(least_x) & 0xFFFFFFFFu) & 0xFFFFFFFFu;
+    whole_span = top - float_of((uint32_t)low);
   }
-  const float p = a.top_p ? a.top_p[t] : 1.0f;
-  if (p < 1.0f) {
-    // the sum of what top_k left, and what has to lie before the first token that goes
-    u64 sum = 0, ties = 0;
-    for (int i = i0; i < i1; ++i) {
-      const float x = logit<TYPE>(row, i);
-      if (key_of(x) > kk) sum += W(x);
-      ties += key_of(x) == kk;
-    }
-    sum = block_sum(sum, space);
-    ties = block_sum(ties, space);
-    if (kk) sum += min(rk, ties) * W(__uint_as_float(kk & 0x80000000u ? kk & 0x7FFFFFFFu : ~kk));
-    bool exact;
-    u64 target = fraction_of(fmaxf(p, 0.0f), sum, &exact);
-    target = max(u64(1), target + !exact);
-    // the lowest key with less than that above it
-    uint32_t kp = 0xFFFFFFFFu;
-    for (int bit = 31; bit >= 0; --bit) {
-      const uint32_t lower = kp & ~(1u << bit);
-      u64 above = 0;
-      for (int i = i0; i < i1; ++i) {
-        const float x = logit<TYPE>(row, i);
-        if (key_of(x) > lower) above += W(x);
+  auto distance_bin = [&](float v) -> int {
+    const float d = (top - v) * per;
+    return d >= kBins - 1 ? kBins - 1 : (int)d;   // (NaN: an infinite top itself, bin 0)
+  };
+  // the keys of bins b1 .. b2
+  auto keys_of = [&](int b1, int b2) -> Keys {
+    if (threadIdx.x < 2) {
+      // the lowest key whose bin is at most b2; the lowest one whose bin is at most b1 - 1, less one
+      const int b = threadIdx.x ? b1 - 1 : b2;
+      uint32_t lo = 0x007FFFFFu, hi = 0xFF800001u;   // of -infinity, behind infinity
+      while (lo < hi) {
+        const uint32_t mid = lo + (hi - lo) / 2;
+        if (mid <= 0xFF800000u && distance_bin(float_of(mid)) > b) lo = mid + 1;
+        else hi = mid;
       }
-      if (block_sum(above, space) < target) kp = lower;
+      S.found[threadIdx.x] = threadIdx.x ? (b < 0 ? 0xFF800000u : lo - 1) : lo;
     }
-    if (kp >= kk) {
-      u64 above = 0;
-      for (int i = i0; i < i1; ++i) {
-        const float x = logit<TYPE>(row, i);
-        if (key_of(x) > kp) above += W(x);
-      }
-      above = block_sum(above, space);
-      const u64 one = W(__uint_as_float(kp & 0x80000000u ? kp & 0x7FFFFFFFu : ~kp));
-      const u64 rp = one ? (target - above + one - 1) / one : ~u64(0);
-      rk = kp == kk ? min(rk, rp) : rp;
-      kk = kp;
-    }
+    __syncthreads();
+    const Keys r{(uint32_t)S.found[0], (uint32_t)S.found[1]};
+    __syncthreads();
+    return r;
+  };
+
+  // what stays: keys above cut, and those on it up to the index last
+  uint32_t cut = 0;
+  int last = 0x7fffffff;
+  auto in = [&](float v, int i) {
+    const uint32_t key = key_of(v);
+    return key > cut || (key == cut && i <= last);
+  };
+  auto everything = [](float, int) { return true; };
+
+  if (by_k) {
+    int b;
+    u64 above;
+    bins_over(whole_span);
+    R.template histogram<uint32_t>(everything, distance_bin);
+    R.template find<uint32_t>((u64)k, &b, &above);
+    Keys r = keys_of(b, b);
+    above += R.template narrow<uint32_t>(r, (u64)k - above, everything);
+    last = R.tie_index(r.lo, (u64)k - above, everything);
+    cut = r.lo;
   }
-  u64 least = 0;
-  const float mp = a.min_p ? a.min_p[t] : 0.0f;
+  u64 least = 0;   // the least weight that min_p lets stay
   if (mp > 0.0f) {
     bool exact = true;
     least = mp < 1.0f ? fraction_of(mp, u64(1) << kUnit, &exact) + !exact : u64(1) << kUnit;
-    if (mp > 1.0f) {
-      kk = key_of(top);
-      rk = 1;
+  }
+  u64 sure = 0;            // this thread's weights above `open` that stay
+  Keys open{cut, top_key}; // what has not been added up
+  if (by_p) {
+    int b1, b2;
+    const float c = R.c.hi;
+    bins_over(fminf(whole_span, 47.0f / c));
+    R.template histogram<uint32_t>(in, distance_bin);
+    // (a bin's edges are off by a few roundings of the distance; the last one has everything further on)
+    auto high = [&](int b) { return b == 0 ? 1.0f : exp2f(-((float)b - 0.01f) * width * c) * (1.0f + 1e-4f); };
+    auto low = [&](int b) { return b == kBins - 1 || per == 0.0f ? 0.0f : exp2f(-((float)b + 1.01f) * width * c) * (1.0f - 1e-4f); };
+    R.find_weight(fmaxf(p, 1e-30f), low, high, &b1, &b2);
+    Keys r = keys_of(b1, b2);
+    u64 above = 0, all = 0;
+    for (int j = 0; j < run; ++j) {
+      const float v = R.mine[j];
+      if (!in(v, R.first + j)) continue;
+      const u64 w = R.weight_of(v);
+      all += w;
+      if (key_of(v) > r.hi) {
+        above += w;
+        if (w >= least) sure += w;
+      }
     }
+    all = R.cluster_sum(all);
+    above = R.cluster_sum(above);
+    open.hi = r.hi;
+    bool exact;
+    u64 target = fraction_of(fmaxf(p, 0.0f), all, &exact);
+    target = max(u64(1), target + !exact);
+    above += R.template narrow<u64>(r, target - above, in);
+    const u64 one = max(R.weight_of(float_of(r.lo)), u64(1));
+    const int index = R.tie_index(r.lo, (target - above + one - 1) / one, in);
+    if (r.lo > cut || index < last) last = index;   // (of those that top_k left on it)
+    open.lo = cut = r.lo;
+  }
+  if (mp > 1.0f) {
+    cut = top_key;
+    last = argmax;
+    sure = 0;
+    open = Keys{cut, top_key};
   }
 
   // what stays, and the token
-  u64 ties = 0;
-  for (int i = i0; i < i1; ++i) ties += key_of(logit<TYPE>(row, i)) == kk;
-  const u64 ties_before = block_before(ties, space);
-  auto stays = [&](float x, u64& tie) -> u64 {
-    const uint32_t key = key_of(x);
-    if (key < kk || (key == kk && tie++ >= rk)) return 0;
-    const u64 w = W(x);
-    return w >= least ? w : 0;
-  };
-  u64 sum = 0, tie = ties_before;
-  for (int i = i0; i < i1; ++i) sum += stays(logit<TYPE>(row, i), tie);
-  const u64 total = block_sum(sum, space), before = block_before(sum, space);
+  for (int j = 0; j < run; ++j) {
+    const float v = R.mine[j];
+    if (key_of(v) > open.hi || !in(v, R.first + j)) continue;
+    const u64 w = R.weight_of(v);
+    if (w >= least) sure += w;
+  }
+  u64 total;
+  const u64 before = R.cluster_before(sure, &total);
   bool exact;
   const float u = fminf(fmaxf(a.uniform[t], 0.0f), 0x1.fffffep-1f);
   const u64 target = fraction_of(u, total, &exact);
-  if (before <= target && before + sum > target) {
-    u64 at = before;
-    tie = ties_before;
-    for (int i = i0; i < i1; ++i) {
-      const float x = logit<TYPE>(row, i);
-      at += stays(x, tie);
-      if (at > target) {
-        a.tokens[t] = i;
-        if (a.logprobs)
-          a.logprobs[t] = (float)((x == top ? 0.0 : ((double)x - (double)top) / (double)temperature) -
-                                  log((double)total * 0x1p-43));
+  const uint32_t who = __ballot_sync(0xffffffffu, before <= target && before + sure > target);
+  if (who) {   // the warp goes through the run of its thread that has it
+    const int lane = threadIdx.x & 31, from = __ffs(who) - 1;
+    u64 at = __shfl_sync(0xffffffffu, before, from);
+    const int start = __shfl_sync(0xffffffffu, R.first, from);
+    for (int j0 = 0; j0 < run; j0 += 32) {
+      const int i = start + j0 + lane;
+      const float v = j0 + lane < run ? R.x[i - begin] : -INFINITY;
+      u64 w = j0 + lane < run && in(v, i) ? R.weight_of(v) : 0;
+      if (w < least) w = 0;
+      u64 upto = w;
+#pragma unroll
+      for (int off = 1; off < 32; off <<= 1) {
+        const u64 o = __shfl_up_sync(0xffffffffu, upto, off);
+        if (lane >= off) upto += o;
+      }
+      const uint32_t hit = __ballot_sync(0xffffffffu, at + upto > target);
+      if (hit) {
+        if (lane == __ffs(hit) - 1) {
+          a.tokens[t] = i;
+          if (a.logprobs)
+            a.logprobs[t] = (float)((v == top ? 0.0 : ((double)v - (double)top) / (double)temperature) -
+                                    log((double)total * (1.0 / (double)(u64(1) << kUnit))));
+        }
         break;
       }
+      at += __shfl_sync(0xffffffffu, upto, 31);
     }
   }
+  R.cluster.sync();   // no CTA ends while another one reads its shared memory
 }
 
 // A thread per stream.
 __global__ void __launch_bounds__(128) accept_kernel(const __grid_constant__ qmm_sample_args a) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int b = blockIdx.x * blockDim.x + threadIdx.x;
   if (b >= a.B) return;
   const int r0 = a.row_starts[b], r1 = a.row_starts[b + 1];
@@ -300,18 +599,70 @@ __global__ void __launch_bounds__(128) accept_kernel(const __grid_constant__ qmm
   a.next[b] = next;
 }
 
+// CTAs of a row.  A slice of at most 16384 floats leaves room for a second CTA on the SM, whose work covers this one's
+// barriers; with few rows, as many CTAs as find an SM, down to slices of 1024.
+int cluster_of(int T, int V, int sms) {
+  int C = 1;
+  while (C < kMaxCluster && (V + C - 1) / C > 16384) C *= 2;
+  while (C < kMaxCluster && (int64_t)T * C * 2 <= sms && V / C >= 2048) C *= 2;
+  return C;
+}
+
+template <int TYPE>
+cudaError_t launch(const qmm_sample_args& a, cudaStream_t stream) {
+  static DeviceOnce once;
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  e = once.run(dev, cudaSuccess, [] {
+    const cudaError_t f = cudaFuncSetAttribute(sample_kernel<TYPE>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    return f != cudaSuccess ? f : cudaFuncSetAttribute(sample_kernel<TYPE>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                       (int)(sizeof(Cta) + kMaxRun * kThreads * sizeof(float)));
+  });
+  if (e != cudaSuccess) return e;
+  const int sms = sm_count();
+  if (sms < 1) return cudaErrorNoDevice;
+  const int C = cluster_of(a.T, a.V, sms);
+  const int run = ((a.V + C - 1) / C + kThreads - 1) / kThreads | 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)a.T * C);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = sizeof(Cta) + (size_t)run * kThreads * sizeof(float);
+  cfg.stream = stream;
+  cudaLaunchAttribute at[2];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = C;
+  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+  at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 2;
+  // 16 bytes at a time where every row's slices begin on such a boundary (a slice is a multiple of 512 logits)
+  const int64_t size = a.type == QMM_F32 ? 4 : 2;
+  const int vec = reinterpret_cast<uintptr_t>(a.logits) % 16 == 0 && (a.T == 1 || a.ld * size % 16 == 0);
+  return cudaLaunchKernelEx(&cfg, sample_kernel<TYPE>, a, run, vec);
+}
+
 }  // namespace
 
 cudaError_t launch_sample(const qmm_sample_args& a, cudaStream_t stream) {
   if (a.T > 0) {
-    if (a.type == QMM_F32) sample_kernel<QMM_F32><<<a.T, kThreads, 0, stream>>>(a);
-    else if (a.type == QMM_BF16) sample_kernel<QMM_BF16><<<a.T, kThreads, 0, stream>>>(a);
-    else sample_kernel<QMM_F16><<<a.T, kThreads, 0, stream>>>(a);
-    const cudaError_t e = cudaGetLastError();
+    const cudaError_t e = a.type == QMM_F32    ? launch<QMM_F32>(a, stream)
+                          : a.type == QMM_BF16 ? launch<QMM_BF16>(a, stream)
+                                               : launch<QMM_F16>(a, stream);
     if (e != cudaSuccess) return e;
   }
-  if (a.B > 0) accept_kernel<<<(a.B + 127) / 128, 128, 0, stream>>>(a);
-  return cudaGetLastError();
+  if (a.B == 0) return cudaSuccess;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((a.B + 127) / 128);
+  cfg.blockDim = dim3(128);
+  cfg.stream = stream;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, accept_kernel, a);
 }
 
 cudaError_t read_and_clear_sample_status(unsigned* out) {

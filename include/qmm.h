@@ -577,7 +577,7 @@ qmm_status qmm_run_lora(const qmm_lora_entry* entries_host, int count, const int
  *     the first token always stays;
  *     token = the lowest i with  sum_{j <= i, j stays} w_j  >  u * sum_{j stays} w_j,
  *     logprob = log(w_token / sum_{j stays} w_j).
- * Weights are rounded to multiples of 2^-43 and summed as integers: no sum depends on an order, and a token on
+ * Weights are rounded to multiples of 2^-42 and summed as integers: no sum depends on an order, and a token on
  * nothing but its row.  NaN and -inf logits are never taken; with +inf logits, these share the weight.  A row
  * without any logit above -inf gives token -1 and logprob -inf.
  *   temperature, top_p, min_p, uniform (fp32) and top_k (int32): device, one for each row.  temperature, top_k, top_p and
