@@ -26,6 +26,7 @@ constexpr int kThreads = 512;
 constexpr int kUnit = 42;              // a weight of 1 is 2^kUnit; QMM_SAMPLE_MAX_V of them stay below 2^62
 constexpr int kSteps = 1024;           // of the table, for one octave
 constexpr int kBinBits = 11, kBins = 1 << kBinBits;
+constexpr int kList = 1024;            // tokens of a CTA's list, and of the cluster's
 constexpr int kMaxCluster = 16, kMaxRun = ((QMM_SAMPLE_MAX_V / kMaxCluster + kThreads - 1) / kThreads) | 1;
 static_assert(QMM_SAMPLE_MAX_V <= (1 << 19), "sums of weights");
 
@@ -131,11 +132,11 @@ __device__ __forceinline__ uint32_t key_of(float x) {
 }
 
 // A row lies in the shared memory of a cluster's CTAs, in order of the tokens: a CTA has a slice, a thread a run of it (an odd
-// number of floats, so that a warp's runs lie in different banks).
+// number of floats, so that a warp's runs lie in different banks).  Once a floor is known below which no token can
+// stay, a CTA lists its tokens above it; where all lists are short, the first CTA takes them and goes on alone.
 struct Cta {
-  u64 part[4];            // this CTA's part of a sum, a maximum or a scan over the cluster; used in turn
+  u64 part[4][2];         // this CTA's part of a sum, a maximum or a scan over the cluster; used in turn
   u64 scan[kThreads / 32];
-  float scan_f[2][kThreads / 32];
   union {                 // of this CTA
     uint32_t count[kBins];
     u64 mass[kBins / 2];
@@ -146,6 +147,8 @@ struct Cta {
   };
   u64 found[2];           // what the thread that found it tells the others
   u64 table[kSteps];
+  float list_x[2][kList];   // tokens above the floor, in order of their index
+  int list_i[2][kList];
 };
 
 struct Keys {             // lo <= key <= hi
@@ -157,12 +160,26 @@ struct Sampler {
   Cta& S;
   float* x;               // the slice
   const cg::cluster_group cluster = cg::this_cluster();
+  bool alone;             // the cluster's tokens are this CTA's
   int turn = 0;           // of part
-  int run, first;         // floats of a thread; index of its first one in the row
+  int run, first;         // tokens of a thread; index of its first one in the row, if they are a run of it
   const float* mine;
+  const int* index = nullptr;   // of its tokens, if they are not
+  uint32_t floor = 0;     // keys below it do not stay
+  int lists = 0;          // made so far: the next one goes to the other place
   float top;
   Slope c;
 
+  __device__ __forceinline__ int index_of(int j) const { return index ? index[j] : first + j; }
+  // Every token of this thread above the floor: f(value, index).
+  template <class F>
+  __device__ __forceinline__ void each(F&& f) {
+#pragma unroll 2
+    for (int j = 0; j < run; ++j) {
+      const float v = mine[j];
+      if (key_of(v) >= floor) f(v, index_of(j));
+    }
+  }
   __device__ __forceinline__ u64 weight_of(float v) const { return v == -INFINITY ? u64(0) : weight(v, top, c, S.table); }
 
   __device__ __forceinline__ u64 warp_sum(u64 v) {
@@ -171,33 +188,48 @@ struct Sampler {
     return v;
   }
   // The parts of the cluster's CTAs, one a lane; they may be written again four calls later.
-  __device__ __forceinline__ u64 exchange(u64 v) {
-    if (threadIdx.x == 0) S.part[turn] = v;
-    cluster.sync();
+  __device__ __forceinline__ u64 exchange(u64 v, u64 w = 0, u64* other = nullptr) {
     const int lane = threadIdx.x & 31;
-    u64 got = 0;
-    if (lane < (int)cluster.num_blocks()) got = *cluster.map_shared_rank(&S.part[turn], lane);
+    if (alone) {
+      if (other) *other = lane == 0 ? w : 0;
+      return lane == 0 ? v : 0;
+    }
+    if (threadIdx.x == 0) {
+      S.part[turn][0] = v;
+      S.part[turn][1] = w;
+    }
+    cluster.sync();
+    u64 got = 0, more = 0;
+    if (lane < (int)cluster.num_blocks()) {
+      const u64* from = cluster.map_shared_rank(S.part[turn], lane);
+      got = from[0];
+      if (other) more = from[1];
+    }
     turn = (turn + 1) & 3;
+    if (other) *other = more;
     return got;
   }
-  __device__ __forceinline__ u64 cluster_sum(u64 v) {
-    v = warp_sum(v);
+  // v over the warps of the CTA, in every lane of every warp: the parts of the warps, one a lane.
+  __device__ __forceinline__ u64 warps(u64 v) {
+    __syncthreads();
     if ((threadIdx.x & 31) == 0) S.scan[threadIdx.x >> 5] = v;
     __syncthreads();
-    v = (threadIdx.x & 31) < kThreads / 32 ? S.scan[threadIdx.x & 31] : 0;
-    return warp_sum(exchange(warp_sum(v)));
+    return (threadIdx.x & 31) < kThreads / 32 ? S.scan[threadIdx.x & 31] : 0;
   }
-  __device__ __forceinline__ u64 cluster_max(u64 v) {
-    auto most = [](u64 m) {
+  __device__ __forceinline__ static u64 warp_max(u64 m) {
 #pragma unroll
-      for (int off = 16; off >= 1; off >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, off));
-      return m;
-    };
-    v = most(v);
-    if ((threadIdx.x & 31) == 0) S.scan[threadIdx.x >> 5] = v;
-    __syncthreads();
-    v = (threadIdx.x & 31) < kThreads / 32 ? S.scan[threadIdx.x & 31] : 0;
-    return most(exchange(most(v)));
+    for (int off = 16; off >= 1; off >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, off));
+    return m;
+  }
+  __device__ __forceinline__ u64 cluster_sum(u64 v) { return warp_sum(exchange(warp_sum(warps(warp_sum(v))))); }
+  // The largest v and the largest w.
+  __device__ __forceinline__ u64 cluster_max(u64 v, u64 w, u64* most_w) {
+    v = warp_max(warps(warp_max(v)));
+    w = warp_max(warps(warp_max(w)));
+    u64 ws;
+    v = warp_max(exchange(v, w, &ws));
+    *most_w = warp_max(ws);
+    return v;
   }
   // Sum over the threads of the CTA before this one; all: over the CTA.
   template <class N>
@@ -227,27 +259,41 @@ struct Sampler {
     const u64 before = block_before<u64>(v, S.scan, &sum);
     const u64 parts = exchange(sum);
     *all = warp_sum(parts);
-    return before + warp_sum((threadIdx.x & 31) < cluster.block_rank() ? parts : 0);
+    return alone ? before : before + warp_sum((threadIdx.x & 31) < cluster.block_rank() ? parts : 0);
   }
 
   // Sums over the cluster's values that `in` takes, by bin(x), in `total` of every CTA: counts (N uint32_t, kBins of them) or
   // weights (N u64, kBins / 2).
   template <class N, class In, class Bin>
   __device__ __forceinline__ void histogram(In&& in, Bin&& bin) {
+    N* count = reinterpret_cast<N*>(S.count);
+    for (int b = threadIdx.x; b < kBins; b += kThreads) S.count[b] = S.total[b] = 0;
+    __syncthreads();
+    each([&](float v, int i) {
+      if (!in(v, i)) return;
+      if constexpr (sizeof(N) == 4) atomicAdd(&count[bin(v)], 1u);
+      else atomicAdd(&count[bin(v)], weight_of(v));
+    });
+    join<N>();
+  }
+  // Counts of bin(v) of one value of each thread, in the same way.
+  template <class Bin>
+  __device__ __forceinline__ void histogram_of(float v, Bin&& bin) {
+    for (int b = threadIdx.x; b < kBins; b += kThreads) S.count[b] = S.total[b] = 0;
+    __syncthreads();
+    atomicAdd(&S.count[bin(v)], 1u);
+    join<uint32_t>();
+  }
+  // `total` of all CTAs from their `count`.
+  template <class N>
+  __device__ __forceinline__ void join() {
     constexpr int kN = kBins * 4 / (int)sizeof(N), kPer = 16 / (int)sizeof(N);
     N* count = reinterpret_cast<N*>(S.count);
     N* total = reinterpret_cast<N*>(S.total);
-    for (int b = threadIdx.x; b < kBins; b += kThreads) S.count[b] = S.total[b] = 0;
-    __syncthreads();
-    for (int j = 0; j < run; ++j) {
-      const float v = mine[j];
-      if (!in(v, first + j)) continue;
-      if constexpr (sizeof(N) == 4) atomicAdd(&count[bin(v)], 1u);
-      else atomicAdd(&count[bin(v)], weight_of(v));
-    }
-    cluster.sync();
+    if (alone) __syncthreads();
+    else cluster.sync();
     // each CTA adds up its share of the bins from all CTAs, 16 bytes of one CTA a thread, and gives it to all
-    const int C = (int)cluster.num_blocks(), vecs = kThreads / C, rank = (int)cluster.block_rank();
+    const int C = alone ? 1 : (int)cluster.num_blocks(), vecs = kThreads / C, rank = alone ? 0 : (int)cluster.block_rank();
     const int peer = threadIdx.x / vecs, at = rank * (kN / C) + kPer * (threadIdx.x % vecs);
     static_assert(kThreads * kPer == kN, "16 bytes a thread");
     if (C > 1) {
@@ -266,8 +312,6 @@ struct Sampler {
       __syncthreads();
     }
   }
-  static constexpr int kMine = kBins / kThreads;   // bins of a thread
-
   // The first bin whose sums reach n >= 1, with those before it.
   template <class N>
   __device__ __forceinline__ void find(u64 n, int* bin, u64* before) {
@@ -294,45 +338,6 @@ struct Sampler {
     __syncthreads();
   }
 
-  // Bins b1 .. b2 in which the weights' sum reaches `share` of itself, by bounds low(b) <= w <= high(b) of the weights of
-  // a bin.
-  template <class Low, class High>
-  __device__ __forceinline__ void find_weight(float share, Low&& low, High&& high, int* b1, int* b2) {
-    constexpr float kSlack = 1e-4f;   // beyond the roundings of these fp32 sums
-    float l[kMine], h[kMine], sum_l = 0.0f, sum_h = 0.0f, all_l, all_h;
-#pragma unroll
-    for (int q = 0; q < kMine; ++q) {
-      const int b = kMine * threadIdx.x + q;
-      const float n = (float)S.total[b];
-      l[q] = n > 0.0f ? n * low(b) * (1.0f - kSlack) : 0.0f;
-      h[q] = n > 0.0f ? n * high(b) * (1.0f + kSlack) : 0.0f;
-      sum_l += l[q];
-      sum_h += h[q];
-    }
-    float at_l = block_before<float>(sum_l, S.scan_f[0], &all_l), at_h = block_before<float>(sum_h, S.scan_f[1], &all_h);
-    const float lo = share * all_l * (1.0f - kSlack), hi = share * all_h * (1.0f + kSlack);
-    if (threadIdx.x == 0) S.found[0] = S.found[1] = kBins - 1;
-    __syncthreads();
-    int first_h = kBins, first_l = kBins;
-#pragma unroll
-    for (int q = kMine - 1; q >= 0; --q) {
-      float up_h = at_h, up_l = at_l;
-#pragma unroll
-      for (int r = 0; r <= q; ++r) {
-        up_h += h[r];
-        up_l += l[r];
-      }
-      if (up_h >= lo) first_h = kMine * threadIdx.x + q;
-      if (up_l >= hi) first_l = kMine * threadIdx.x + q;
-    }
-    if (first_h < kBins) atomicMin(&S.found[0], (u64)first_h);
-    if (first_l < kBins) atomicMin(&S.found[1], (u64)first_l);
-    __syncthreads();
-    *b1 = (int)S.found[0];
-    *b2 = max(*b1, (int)S.found[1]);
-    __syncthreads();
-  }
-
   // Narrows a range of keys to the one on which the sums from its highest key down reach n, by bins of 2^shift keys; the sums
   // before that key.
   template <class N, class In>
@@ -353,30 +358,84 @@ struct Sampler {
     return sum;
   }
 
-  // Of `r` distinct ties on a key, the index of the last one that stays; INT_MAX if all do.
+  // Of `r` ties on a key, the index of the last one that stays; INT_MAX if all do.
   template <class In>
   __device__ __forceinline__ int tie_index(uint32_t key, u64 r, In&& in) {
     u64 n = 0, all;
-    for (int j = 0; j < run; ++j) n += in(mine[j], first + j) && key_of(mine[j]) == key;
+    each([&](float v, int i) { n += key_of(v) == key && in(v, i); });
     const u64 before = cluster_before(n, &all);
     if (all <= r) return 0x7fffffff;
-    u64 index = 0;
-    if (before < r && before + n >= r) {
-      u64 at = before;
-      for (int j = 0; j < run; ++j)
-        if (in(mine[j], first + j) && key_of(mine[j]) == key && ++at == r) index = (u64)(first + j) + 1;
+    u64 at = before, found = 0;
+    if (before < r && before + n >= r)
+      each([&](float v, int i) {
+        if (key_of(v) == key && in(v, i) && ++at == r) found = (u64)i + 1;
+      });
+    return (int)cluster_sum(found) - 1;
+  }
+
+  // Nothing below `lowest` stays: the CTA's other tokens into its list, and all lists to the first CTA if they are
+  // short.  false: this CTA is done.
+  __device__ __forceinline__ bool raise_floor(uint32_t lowest) {
+    floor = max(floor, lowest);
+    u64 n = 0, all, others;
+    each([&](float, int) { ++n; });
+    const u64 at = block_before<u64>(n, S.scan, &all);
+    const bool fits = all <= (u64)kList;
+    const int place = lists++ & 1;
+    if (fits) {
+      int to = (int)at;
+      each([&](float v, int i) {
+        S.list_x[place][to] = v;
+        S.list_i[place][to++] = i;
+      });
+      __syncthreads();
+      run = ((int)all + kThreads - 1) / kThreads;
+      const int from = min((int)all, (int)threadIdx.x * run);
+      run = min(run, (int)all - from);
+      mine = S.list_x[place] + from;
+      index = S.list_i[place] + from;
     }
-    return (int)cluster_sum(index) - 1;
+    if (alone) return true;
+    const u64 parts = exchange(fits ? all : (u64)kList + 1, 0, &others);   // (the lists are written before it)
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, C = (int)cluster.num_blocks();
+    u64 upto = parts;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const u64 o = __shfl_up_sync(0xffffffffu, upto, off);
+      if (lane >= off) upto += o;
+    }
+    const int sum = (int)__shfl_sync(0xffffffffu, upto, 31);
+    if (sum > kList) return true;
+    if (cluster.block_rank() == 0) {   // a warp for each CTA's list
+      for (int r = warp; r < C; r += kThreads / 32) {
+        const int to = (int)__shfl_sync(0xffffffffu, upto - parts, r), len = (int)__shfl_sync(0xffffffffu, parts, r);
+        const float* from_x = cluster.map_shared_rank(S.list_x[place], r);
+        const int* from_i = cluster.map_shared_rank(S.list_i[place], r);
+        for (int j = lane; j < len; j += 32) {
+          S.list_x[place ^ 1][to + j] = from_x[j];
+          S.list_i[place ^ 1][to + j] = from_i[j];
+        }
+      }
+    }
+    cluster.sync();   // no CTA ends while another one reads its shared memory
+    if (cluster.block_rank() != 0) return false;
+    alone = true;
+    run = (sum + kThreads - 1) / kThreads;
+    const int from = min(sum, (int)threadIdx.x * run);
+    run = min(run, sum - from);
+    mine = S.list_x[place ^ 1] + from;
+    index = S.list_i[place ^ 1] + from;
+    ++lists;
+    return true;
   }
 };
 
 // The float of a key.
 __device__ __forceinline__ float float_of(uint32_t key) { return __uint_as_float(key & 0x80000000u ? key & 0x7FFFFFFFu : ~key); }
 
-// A cluster per row.  The border of top_k is found by counting: 2048 bins, first over the distance from the largest logit,
-// then over the keys of the bin in which the border lies, until a bin is one key; ties on it go by index.  For
-// top_p the counts bound the weights' sums (a bin's weights are within 2 % of each other), which leaves a few
-// bins; what lies above them is added up exactly, and from there bins of keys hold exact sums.
+// A cluster per row.  The borders are found by sums over bins (of counts for top_k, of weights for top_p), first over the
+// distance from the largest logit, then over the keys of the bin in which the border lies, until a bin is one key; ties
+// on it go by index.  Before that, a floor leaves most of a vocabulary behind.
 template <int TYPE>
 __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_constant__ qmm_sample_args a, int run, int vec) {
   extern __shared__ __align__(16) uint8_t smem[];
@@ -389,35 +448,45 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
   const int t = blockIdx.x / (int)R.cluster.num_blocks(), V = a.V, slice = run * kThreads, begin = rank * slice;
   const int n = max(0, min(V - begin, slice));
   const uint8_t* row = static_cast<const uint8_t*>(a.logits) + t * a.ld * (TYPE == QMM_F32 ? 4 : 2);
+  R.alone = R.cluster.num_blocks() == 1;
   R.run = run;
   R.first = begin + (int)threadIdx.x * run;
   R.mine = R.x + (int)threadIdx.x * run;
 
-  // the slice, its largest logit (the lowest index of equal ones) and its lowest finite one
-  u64 best = 0;
-  float least_x = INFINITY;
-  auto take = [&](int i, float v) {
-    v = v == v ? v + 0.0f : -INFINITY;   // (-0 and 0 are equal)
-    R.x[i] = v;
-    best = max(best, (u64)key_of(v) << 32 | (0xFFFFFFFFu - (uint32_t)(begin + i)));
-    if (v > -INFINITY) least_x = fminf(least_x, v);
-  };
+  // the slice, its largest logit (the lowest index of equal ones)
+  auto take = [&](float v) { return v == v ? v + 0.0f : -INFINITY; };   // (-0 and 0 are equal)
   constexpr int kPerVec = TYPE == QMM_F32 ? 4 : 8;
   const int whole = vec ? n / kPerVec * kPerVec : 0;
   for (int i = kPerVec * threadIdx.x; i < whole; i += kPerVec * kThreads) {
     const uint4 w = *reinterpret_cast<const uint4*>(row + (int64_t)(begin + i) * (TYPE == QMM_F32 ? 4 : 2));
     const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+    float v[kPerVec];
 #pragma unroll
     for (int q = 0; q < kPerVec; ++q) {
-      if constexpr (TYPE == QMM_F32) take(i + q, __uint_as_float(u[q]));
-      else if constexpr (TYPE == QMM_BF16) take(i + q, __uint_as_float(q & 1 ? u[q / 2] & 0xFFFF0000u : u[q / 2] << 16));
-      else take(i + q, __half2float(__ushort_as_half((uint16_t)(u[q / 2] >> (16 * (q & 1))))));
+      if constexpr (TYPE == QMM_F32) v[q] = take(__uint_as_float(u[q]));
+      else if constexpr (TYPE == QMM_BF16) v[q] = take(__uint_as_float(q & 1 ? u[q / 2] & 0xFFFF0000u : u[q / 2] << 16));
+      else v[q] = take(__half2float(__ushort_as_half((uint16_t)(u[q / 2] >> (16 * (q & 1))))));
     }
+#pragma unroll
+    for (int q = 0; q < kPerVec; q += 4)
+      *reinterpret_cast<float4*>(&R.x[i + q]) = make_float4(v[q], v[q + 1], v[q + 2], v[q + 3]);
   }
-  for (int i = whole + threadIdx.x; i < n; i += kThreads) take(i, logit<TYPE>(row, begin + i));
+  for (int i = whole + threadIdx.x; i < n; i += kThreads) R.x[i] = take(logit<TYPE>(row, begin + i));
   for (int i = n + threadIdx.x; i < slice; i += kThreads) R.x[i] = -INFINITY;
   for (int j = threadIdx.x; j < kSteps; j += kThreads) S.table[j] = kTable.v[j];
-  best = R.cluster_max(best);
+  __syncthreads();
+  float own = -INFINITY;   // this thread's largest, and where
+  int where = 0;
+  for (int j = 0; j < run; ++j) {
+    const float v = R.mine[j];
+    if (v > own) {
+      own = v;
+      where = j;
+    }
+  }
+  u64 lows;   // of the threads' largest finite ones
+  const u64 best = R.cluster_max((u64)key_of(own) << 32 | (0xFFFFFFFFu - (uint32_t)(R.first + where)),
+                                 own > -INFINITY ? 0xFFFFFFFFu - key_of(own) : 0, &lows);
   const int argmax = (int)(0xFFFFFFFFu - (uint32_t)best);
   const uint32_t top_key = (uint32_t)(best >> 32);
   const float top = float_of(top_key), temperature = a.temperature ? a.temperature[t] : 1.0f;
@@ -427,7 +496,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
       a.tokens[t] = top == -INFINITY ? -1 : argmax;
       if (a.logprobs) a.logprobs[t] = top == -INFINITY ? -INFINITY : 0.0f;
     }
-    R.cluster.sync();   // no CTA ends while another one reads its shared memory
+    if (!R.alone) R.cluster.sync();   // no CTA ends while another one reads its shared memory
     return;
   }
   R.c = slope_of(temperature);
@@ -435,22 +504,17 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
   const float p = a.top_p ? a.top_p[t] : 1.0f, mp = a.min_p ? a.min_p[t] : 0.0f;
   const bool by_k = k > 0 && k < V, by_p = p < 1.0f;
 
-  // bins over the distance from the top, as far as the row goes, or as weights are above 0
-  float per = 0.0f, width = INFINITY;
+  // bins over the distance from the top
+  float per = 0.0f;
   auto bins_over = [&](float span) {
     per = kBins / span;
     if (!(span > 0.0f && per < INFINITY)) per = 0.0f;   // one bin
-    width = per > 0.0f ? span / kBins : INFINITY;
   };
-  float whole_span = 0.0f;
-  if (by_k || by_p) {
-    const u64 low = ~R.cluster_max(~(u64)key_of(least_x) & 0xFFFFFFFFu) & 0xFFFFFFFFu;
-    whole_span = top - float_of((uint32_t)low);
-  }
   auto distance_bin = [&](float v) -> int {
     const float d = (top - v) * per;
     return d >= kBins - 1 ? kBins - 1 : (int)d;   // (NaN: an infinite top itself, bin 0)
   };
+  auto half_bin = [&](float v) { return distance_bin(v) >> 1; };   // of weights
   // the keys of bins b1 .. b2
   auto keys_of = [&](int b1, int b2) -> Keys {
     if (threadIdx.x < 2) {
@@ -477,12 +541,21 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
     const uint32_t key = key_of(v);
     return key > cut || (key == cut && i <= last);
   };
+  // the lowest key that a token within d of the top can have
+  auto key_within = [&](float d) { return top < INFINITY ? key_of(top - d * (1.0f + 1e-5f) - fabsf(top) * 1e-6f) : top_key; };
   auto everything = [](float, int) { return true; };
 
   if (by_k) {
     int b;
     u64 above;
-    bins_over(whole_span);
+    // k threads have a token at or above the k-th largest of the threads' largest: nothing below it stays
+    bins_over(top - float_of(0xFFFFFFFFu - (uint32_t)lows));
+    if (k <= kThreads * (int)R.cluster.num_blocks()) {
+      R.histogram_of(own, distance_bin);
+      R.template find<uint32_t>((u64)k, &b, &above);
+      if (!R.raise_floor(keys_of(b, b).lo)) return;
+      bins_over(top - float_of(max(R.floor, 0x00800000u)));
+    }
     R.template histogram<uint32_t>(everything, distance_bin);
     R.template find<uint32_t>((u64)k, &b, &above);
     Keys r = keys_of(b, b);
@@ -495,55 +568,47 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
     bool exact = true;
     least = mp < 1.0f ? fraction_of(mp, u64(1) << kUnit, &exact) + !exact : u64(1) << kUnit;
   }
-  u64 sure = 0;            // this thread's weights above `open` that stay
-  Keys open{cut, top_key}; // what has not been added up
   if (by_p) {
-    int b1, b2;
-    const float c = R.c.hi;
-    bins_over(fminf(whole_span, 47.0f / c));
-    R.template histogram<uint32_t>(in, distance_bin);
-    // (a bin's edges are off by a few roundings of the distance; the last one has everything further on)
-    auto high = [&](int b) { return b == 0 ? 1.0f : exp2f(-((float)b - 0.01f) * width * c) * (1.0f + 1e-4f); };
-    auto low = [&](int b) { return b == kBins - 1 || per == 0.0f ? 0.0f : exp2f(-((float)b + 1.01f) * width * c) * (1.0f - 1e-4f); };
-    R.find_weight(fmaxf(p, 1e-30f), low, high, &b1, &b2);
-    Keys r = keys_of(b1, b2);
-    u64 above = 0, all = 0;
-    for (int j = 0; j < run; ++j) {
-      const float v = R.mine[j];
-      if (!in(v, R.first + j)) continue;
-      const u64 w = R.weight_of(v);
-      all += w;
-      if (key_of(v) > r.hi) {
-        above += w;
-        if (w >= least) sure += w;
-      }
-    }
+    u64 all = 0;
+    R.each([&](float v, int i) { if (in(v, i)) all += R.weight_of(v); });
     all = R.cluster_sum(all);
-    above = R.cluster_sum(above);
-    open.hi = r.hi;
     bool exact;
     u64 target = fraction_of(fmaxf(p, 0.0f), all, &exact);
     target = max(u64(1), target + !exact);
+    // tokens of less than (1 - top_p) of the sum, divided by their number, cannot make up what may go: the border is above
+    const float spare = fmaxf((float)(all - target), 1.0f) * 0.999f / (float)V, reach = log2f(0x1p42f / spare) / R.c.hi;
+    if (!(R.alone && R.index) && !R.raise_floor(max(cut, key_within(reach)))) return;
+    Keys r{max(R.floor, cut), top_key};
+    u64 above = 0;
+    bins_over(fminf(reach, top - float_of(max(r.lo, 0x00800000u))));
+    if (per > 0.0f) {
+      int b;
+      R.template histogram<u64>(in, half_bin);
+      R.template find<u64>(target, &b, &above);
+      r = keys_of(2 * b, 2 * b + 1);
+      r.hi = min(r.hi, top_key);
+    }
     above += R.template narrow<u64>(r, target - above, in);
     const u64 one = max(R.weight_of(float_of(r.lo)), u64(1));
     const int index = R.tie_index(r.lo, (target - above + one - 1) / one, in);
     if (r.lo > cut || index < last) last = index;   // (of those that top_k left on it)
-    open.lo = cut = r.lo;
+    cut = r.lo;
   }
-  if (mp > 1.0f) {
-    cut = top_key;
-    last = argmax;
-    sure = 0;
-    open = Keys{cut, top_key};
+  if (mp > 0.0f) {
+    if (!by_p && !(R.alone && R.index) && !R.raise_floor(max(cut, key_within(log2f(1.0f / fminf(mp, 1.0f)) / R.c.hi)))) return;
+    if (mp > 1.0f) {
+      cut = top_key;
+      last = argmax;
+    }
   }
 
   // what stays, and the token
-  for (int j = 0; j < run; ++j) {
-    const float v = R.mine[j];
-    if (key_of(v) > open.hi || !in(v, R.first + j)) continue;
+  u64 sure = 0;
+  R.each([&](float v, int i) {
+    if (!in(v, i)) return;
     const u64 w = R.weight_of(v);
     if (w >= least) sure += w;
-  }
+  });
   u64 total;
   const u64 before = R.cluster_before(sure, &total);
   bool exact;
@@ -553,11 +618,14 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
   if (who) {   // the warp goes through the run of its thread that has it
     const int lane = threadIdx.x & 31, from = __ffs(who) - 1;
     u64 at = __shfl_sync(0xffffffffu, before, from);
-    const int start = __shfl_sync(0xffffffffu, R.first, from);
-    for (int j0 = 0; j0 < run; j0 += 32) {
-      const int i = start + j0 + lane;
-      const float v = j0 + lane < run ? R.x[i - begin] : -INFINITY;
-      u64 w = j0 + lane < run && in(v, i) ? R.weight_of(v) : 0;
+    const int begin_of = __shfl_sync(0xffffffffu, (int)(R.mine - R.x), from), len = __shfl_sync(0xffffffffu, R.run, from);
+    const int first = __shfl_sync(0xffffffffu, R.first, from);
+    const int* index = R.index ? R.index + (__shfl_sync(0xffffffffu, (int)(R.mine - R.x), from) - (int)(R.mine - R.x)) : nullptr;
+    for (int j0 = 0; j0 < len; j0 += 32) {
+      const bool here = j0 + lane < len;
+      const float v = here ? R.x[begin_of + j0 + lane] : -INFINITY;
+      const int i = !here ? 0 : index ? index[j0 + lane] : first + j0 + lane;
+      u64 w = here && key_of(v) >= R.floor && in(v, i) ? R.weight_of(v) : 0;
       if (w < least) w = 0;
       u64 upto = w;
 #pragma unroll
@@ -578,7 +646,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
       at += __shfl_sync(0xffffffffu, upto, 31);
     }
   }
-  R.cluster.sync();   // no CTA ends while another one reads its shared memory
+  if (!R.alone) R.cluster.sync();   // no CTA ends while another one reads its shared memory
 }
 
 // A thread per stream.
