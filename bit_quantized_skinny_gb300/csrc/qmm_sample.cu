@@ -27,6 +27,7 @@ constexpr int kUnit = 42;              // a weight of 1 is 2^kUnit; QMM_SAMPLE_M
 constexpr int kSteps = 1024;           // of the table, for one octave
 constexpr int kBinBits = 11, kBins = 1 << kBinBits;
 constexpr int kList = 1024;            // tokens of a CTA's list, and of the cluster's
+static_assert(kList <= kBins / 2 && kList <= 2 * kThreads, "a list is sorted in the bins' place, two tokens a thread");
 constexpr int kMaxCluster = 16, kMaxRun = ((QMM_SAMPLE_MAX_V / kMaxCluster + kThreads - 1) / kThreads) | 1;
 static_assert(QMM_SAMPLE_MAX_V <= (1 << 19), "sums of weights");
 
@@ -131,12 +132,37 @@ __device__ __forceinline__ uint32_t key_of(float x) {
   return b & 0x80000000u ? ~b : b | 0x80000000u;
 }
 
+// The float of a key.
+__device__ __forceinline__ float float_of(uint32_t key) { return __uint_as_float(key & 0x80000000u ? key & 0x7FFFFFFFu : ~key); }
+
+// Sum over the warp, in every lane (32 lanes of 16 bits fit into 32).
+__device__ __forceinline__ u64 warp_sum(u64 v) {
+  u64 sum = 0;
+#pragma unroll
+  for (int q = 0; q < 4; ++q) sum += (u64)__reduce_add_sync(0xffffffffu, (uint32_t)(v >> (16 * q)) & 0xFFFFu) << (16 * q);
+  return sum;
+}
+// Sum over the lanes up to this one.
+__device__ __forceinline__ u64 warp_upto(u64 v) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int off = 1; off < 32; off <<= 1) {
+    const u64 u = __shfl_up_sync(0xffffffffu, v, off);
+    if (lane >= off) v += u;
+  }
+  return v;
+}
+
+constexpr int kWarps = kThreads / 32;
+
 // A row lies in the shared memory of a cluster's CTAs, in order of the tokens: a CTA has a slice, a thread a run of it (an odd
 // number of floats, so that a warp's runs lie in different banks).  Once a floor is known below which no token can
-// stay, a CTA lists its tokens above it; where all lists are short, the first CTA takes them and goes on alone.
+// stay, a CTA lists its tokens above it; where all lists are short, the first CTA takes them and ends the row alone.
 struct Cta {
-  u64 part[4][2];         // this CTA's part of a sum, a maximum or a scan over the cluster; used in turn
-  u64 scan[kThreads / 32];
+  u64 part[4];            // this CTA's part of a sum, a maximum or a scan over the cluster; used in turn
+  uint32_t low[4];
+  u64 scan[kWarps];
+  uint32_t scan_low[kWarps];
   union {                 // of this CTA
     uint32_t count[kBins];
     u64 mass[kBins / 2];
@@ -155,25 +181,31 @@ struct Keys {             // lo <= key <= hi
   uint32_t lo, hi;
 };
 
-template <int TYPE>
+enum Raised { kDone, kSpread, kAlone };   // this CTA has nothing left to do; goes on with the others; has all tokens
+
 struct Sampler {
   Cta& S;
   float* x;               // the slice
   const cg::cluster_group cluster = cg::this_cluster();
-  bool alone;             // the cluster's tokens are this CTA's
+  const int C = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
   int turn = 0;           // of part
   int run, first;         // tokens of a thread; index of its first one in the row, if they are a run of it
   const float* mine;
   const int* index = nullptr;   // of its tokens, if they are not
   uint32_t floor = 0;     // keys below it do not stay
+  uint32_t own = 0;       // the key of this thread's largest token
   int lists = 0;          // made so far: the next one goes to the other place
+  int listed = 0;         // alone: the tokens, their values and indices in list_x, list_i
+  const float* all_x;
+  const int* all_i;
   float top;
   Slope c;
 
   __device__ __forceinline__ int index_of(int j) const { return index ? index[j] : first + j; }
   // Every token of this thread above the floor: f(value, index).
   template <class F>
-  __device__ __forceinline__ void each(F&& f) {
+  __device__ __forceinline__ void each(F&& f) const {
+    if (own < floor) return;
 #pragma unroll 2
     for (int j = 0; j < run; ++j) {
       const float v = mine[j];
@@ -182,84 +214,78 @@ struct Sampler {
   }
   __device__ __forceinline__ u64 weight_of(float v) const { return v == -INFINITY ? u64(0) : weight(v, top, c, S.table); }
 
-  __device__ __forceinline__ u64 warp_sum(u64 v) {
-#pragma unroll
-    for (int off = 16; off >= 1; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
-    return v;
+  __device__ __forceinline__ void sync() const {
+    if (C > 1) cluster.sync();
+    else __syncthreads();
   }
   // The parts of the cluster's CTAs, one a lane; they may be written again four calls later.
-  __device__ __forceinline__ u64 exchange(u64 v, u64 w = 0, u64* other = nullptr) {
+  __device__ __forceinline__ u64 exchange(u64 v) {
     const int lane = threadIdx.x & 31;
-    if (alone) {
-      if (other) *other = lane == 0 ? w : 0;
-      return lane == 0 ? v : 0;
-    }
-    if (threadIdx.x == 0) {
-      S.part[turn][0] = v;
-      S.part[turn][1] = w;
-    }
+    if (C == 1) return lane == 0 ? v : 0;
+    if (threadIdx.x == 0) S.part[turn] = v;
     cluster.sync();
-    u64 got = 0, more = 0;
-    if (lane < (int)cluster.num_blocks()) {
-      const u64* from = cluster.map_shared_rank(S.part[turn], lane);
-      got = from[0];
-      if (other) more = from[1];
-    }
+    u64 got = 0;
+    if (lane < C) got = *cluster.map_shared_rank(&S.part[turn], lane);
     turn = (turn + 1) & 3;
-    if (other) *other = more;
     return got;
   }
-  // v over the warps of the CTA, in every lane of every warp: the parts of the warps, one a lane.
-  __device__ __forceinline__ u64 warps(u64 v) {
+  __device__ __forceinline__ u64 cluster_sum(u64 v) {
+    v = warp_sum(v);
     __syncthreads();
     if ((threadIdx.x & 31) == 0) S.scan[threadIdx.x >> 5] = v;
     __syncthreads();
-    return (threadIdx.x & 31) < kThreads / 32 ? S.scan[threadIdx.x & 31] : 0;
+    v = (threadIdx.x & 31) < kWarps ? S.scan[threadIdx.x & 31] : 0;
+    return warp_sum(exchange(warp_sum(v)));
   }
-  __device__ __forceinline__ static u64 warp_max(u64 m) {
-#pragma unroll
-    for (int off = 16; off >= 1; off >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, off));
-    return m;
-  }
-  __device__ __forceinline__ u64 cluster_sum(u64 v) { return warp_sum(exchange(warp_sum(warps(warp_sum(v))))); }
-  // The largest v and the largest w.
-  __device__ __forceinline__ u64 cluster_max(u64 v, u64 w, u64* most_w) {
-    v = warp_max(warps(warp_max(v)));
-    w = warp_max(warps(warp_max(w)));
-    u64 ws;
-    v = warp_max(exchange(v, w, &ws));
-    *most_w = warp_max(ws);
-    return v;
+  // The largest key and the lowest index that has it, and the lowest of `low`.
+  __device__ __forceinline__ void best_of(uint32_t& key, uint32_t& at, uint32_t& low) {
+    auto within = [&]() {
+      const uint32_t most = __reduce_max_sync(0xffffffffu, key);
+      at = __reduce_min_sync(0xffffffffu, key == most ? at : 0xFFFFFFFFu);
+      key = most;
+      low = __reduce_min_sync(0xffffffffu, low);
+    };
+    const int lane = threadIdx.x & 31;
+    auto have = [&](bool some, const u64* p, const uint32_t* l) {
+      const u64 v = some ? *p : 0;
+      key = (uint32_t)(v >> 32);
+      at = some ? (uint32_t)v : 0xFFFFFFFFu;
+      low = some ? *l : 0xFFFFFFFFu;
+      within();
+    };
+    within();
+    if (lane == 0) {
+      S.scan[threadIdx.x >> 5] = (u64)key << 32 | at;
+      S.scan_low[threadIdx.x >> 5] = low;
+    }
+    __syncthreads();
+    have(lane < kWarps, &S.scan[lane % kWarps], &S.scan_low[lane % kWarps]);
+    if (C == 1) return;
+    if (threadIdx.x == 0) {
+      S.part[turn] = (u64)key << 32 | at;
+      S.low[turn] = low;
+    }
+    cluster.sync();
+    have(lane < C, cluster.map_shared_rank(&S.part[turn], lane % C), cluster.map_shared_rank(&S.low[turn], lane % C));
+    turn = (turn + 1) & 3;
   }
   // Sum over the threads of the CTA before this one; all: over the CTA.
-  template <class N>
-  __device__ __forceinline__ N block_before(N v, N* space, N* all) {
-    N upto = v;
+  __device__ __forceinline__ u64 block_before(u64 v, u64* all) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-#pragma unroll
-    for (int off = 1; off < 32; off <<= 1) {
-      const N u = __shfl_up_sync(0xffffffffu, upto, off);
-      if (lane >= off) upto += u;
-    }
+    const u64 upto = warp_upto(v);
     __syncthreads();
-    if (lane == 31) space[warp] = upto;
+    if (lane == 31) S.scan[warp] = upto;
     __syncthreads();
-    N before = upto - v, sum = 0;
-#pragma unroll
-    for (int w = 0; w < kThreads / 32; ++w) {
-      if (w < warp) before += space[w];
-      sum += space[w];
-    }
-    *all = sum;
-    return before;
+    const u64 of = lane < kWarps ? S.scan[lane] : 0;
+    *all = warp_sum(of);
+    return upto - v + warp_sum(lane < warp ? of : 0);
   }
   // Sum over the threads of the cluster before this one; all: over the cluster.
   __device__ __forceinline__ u64 cluster_before(u64 v, u64* all) {
     u64 sum;
-    const u64 before = block_before<u64>(v, S.scan, &sum);
-    const u64 parts = exchange(sum);
+    const u64 before = block_before(v, &sum), parts = exchange(sum);
     *all = warp_sum(parts);
-    return alone ? before : before + warp_sum((threadIdx.x & 31) < cluster.block_rank() ? parts : 0);
+    return C == 1 ? before : before + warp_sum((threadIdx.x & 31) < rank ? parts : 0);
   }
 
   // Sums over the cluster's values that `in` takes, by bin(x), in `total` of every CTA: counts (N uint32_t, kBins of them) or
@@ -267,7 +293,7 @@ struct Sampler {
   template <class N, class In, class Bin>
   __device__ __forceinline__ void histogram(In&& in, Bin&& bin) {
     N* count = reinterpret_cast<N*>(S.count);
-    for (int b = threadIdx.x; b < kBins; b += kThreads) S.count[b] = S.total[b] = 0;
+    for (int b = threadIdx.x; b < kBins; b += kThreads) S.count[b] = 0;
     __syncthreads();
     each([&](float v, int i) {
       if (!in(v, i)) return;
@@ -279,52 +305,45 @@ struct Sampler {
   // Counts of bin(v) of one value of each thread, in the same way.
   template <class Bin>
   __device__ __forceinline__ void histogram_of(float v, Bin&& bin) {
-    for (int b = threadIdx.x; b < kBins; b += kThreads) S.count[b] = S.total[b] = 0;
+    for (int b = threadIdx.x; b < kBins; b += kThreads) S.count[b] = 0;
     __syncthreads();
     atomicAdd(&S.count[bin(v)], 1u);
     join<uint32_t>();
   }
-  // `total` of all CTAs from their `count`.
+  // `total` of all CTAs from their `count`: each adds up its share of the bins and gives it to all.
   template <class N>
   __device__ __forceinline__ void join() {
-    constexpr int kN = kBins * 4 / (int)sizeof(N), kPer = 16 / (int)sizeof(N);
+    constexpr int kN = kBins * 4 / (int)sizeof(N);
     N* count = reinterpret_cast<N*>(S.count);
     N* total = reinterpret_cast<N*>(S.total);
-    if (alone) __syncthreads();
-    else cluster.sync();
-    // each CTA adds up its share of the bins from all CTAs, 16 bytes of one CTA a thread, and gives it to all
-    const int C = alone ? 1 : (int)cluster.num_blocks(), vecs = kThreads / C, rank = alone ? 0 : (int)cluster.block_rank();
-    const int peer = threadIdx.x / vecs, at = rank * (kN / C) + kPer * (threadIdx.x % vecs);
-    static_assert(kThreads * kPer == kN, "16 bytes a thread");
-    if (C > 1) {
-      const uint4 v = *cluster.map_shared_rank(reinterpret_cast<uint4*>(&count[at]), peer);
-      N part[kPer];
-      *reinterpret_cast<uint4*>(part) = v;
-#pragma unroll
-      for (int q = 0; q < kPer; ++q)
-        if (part[q]) atomicAdd(&total[at + q], part[q]);
-      __syncthreads();
-      if (peer != rank)
-        *cluster.map_shared_rank(reinterpret_cast<uint4*>(&total[at]), peer) = *reinterpret_cast<uint4*>(&total[at]);
-      cluster.sync();
-    } else {
-      *reinterpret_cast<uint4*>(&total[at]) = *reinterpret_cast<const uint4*>(&count[at]);
-      __syncthreads();
+    sync();
+    const int bins = kN / C;
+    for (int b = rank * bins + threadIdx.x; b < (rank + 1) * bins; b += kThreads) {
+      N sum = 0;
+      if (C == 1) {
+        sum = count[b];
+      } else {
+#pragma unroll 8
+        for (int r = 0; r < C; ++r) sum += *cluster.map_shared_rank(&count[b], r);
+        for (int r = 0; r < C; ++r) *cluster.map_shared_rank(&total[b], r) = sum;
+      }
+      if (C == 1) total[b] = sum;
     }
+    sync();
   }
   // The first bin whose sums reach n >= 1, with those before it.
   template <class N>
   __device__ __forceinline__ void find(u64 n, int* bin, u64* before) {
     constexpr int kMine = kBins * 4 / (int)sizeof(N) / kThreads;
-    const N* total = reinterpret_cast<const N*>(S.total);
+    const N* total = reinterpret_cast<const N*>(S.total) + kMine * threadIdx.x;
     u64 sum = 0, all;
 #pragma unroll
-    for (int q = 0; q < kMine; ++q) sum += total[kMine * threadIdx.x + q];
-    u64 at = block_before<u64>(sum, S.scan, &all);
+    for (int q = 0; q < kMine; ++q) sum += total[q];
+    u64 at = block_before(sum, &all);
     if (at < n && at + sum >= n) {
 #pragma unroll
       for (int q = 0; q < kMine; ++q) {
-        const u64 m = total[kMine * threadIdx.x + q];
+        const u64 m = total[q];
         if (at < n && at + m >= n) {
           S.found[0] = kMine * threadIdx.x + q;
           S.found[1] = at;
@@ -358,6 +377,31 @@ struct Sampler {
     return sum;
   }
 
+  // The keys whose value `bin` (which does not rise with the key) puts into b1 .. b2: a warp for each end, 32 keys a step.
+  template <class Bin>
+  __device__ __forceinline__ Keys keys_of(int b1, int b2, Bin&& bin) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (warp < 2) {
+      // the lowest key whose bin is at most b: the range's low end, and one above its high end
+      const int b = warp ? b1 - 1 : b2;
+      uint32_t lo = 0x007FFFFFu, hi = 0xFF800001u;   // of -infinity, behind infinity: hi has a bin that low
+      while (lo < hi) {
+        const uint32_t step = (hi - lo + 31) / 32, key = lo + lane * step;   // lo, ..., lo + 31 steps
+        const bool low = key >= hi || bin(float_of(min(key, 0xFF800000u))) <= b;
+        const uint32_t some = __ballot_sync(0xffffffffu, low);
+        const int at = some ? __ffs(some) - 1 : 32;   // the first of the 32 that is low enough
+        hi = at < 32 ? min(hi, lo + at * step) : hi;
+        if (at == 0) break;
+        lo = lo + (at - 1) * step + 1;
+      }
+      if (lane == 0) S.found[warp] = warp ? (b < 0 ? 0xFF800000u : hi - 1) : hi;
+    }
+    __syncthreads();
+    const Keys r{(uint32_t)S.found[0], (uint32_t)S.found[1]};
+    __syncthreads();
+    return r;
+  }
+
   // Of `r` ties on a key, the index of the last one that stays; INT_MAX if all do.
   template <class In>
   __device__ __forceinline__ int tie_index(uint32_t key, u64 r, In&& in) {
@@ -373,82 +417,170 @@ struct Sampler {
     return (int)cluster_sum(found) - 1;
   }
 
-  // Nothing below `lowest` stays: the CTA's other tokens into its list, and all lists to the first CTA if they are
-  // short.  false: this CTA is done.
-  __device__ __forceinline__ bool raise_floor(uint32_t lowest) {
+  // Nothing below `lowest` stays, nor what `in` does not take: the CTA's other tokens into its list, and all lists to the
+  // first CTA if they are short.
+  template <class In>
+  __device__ __forceinline__ Raised raise_floor(uint32_t lowest, In&& in) {
     floor = max(floor, lowest);
-    u64 n = 0, all, others;
-    each([&](float, int) { ++n; });
-    const u64 at = block_before<u64>(n, S.scan, &all);
+    u64 n = 0, all;
+    each([&](float v, int i) { n += in(v, i); });
+    const u64 at = block_before(n, &all);
     const bool fits = all <= (u64)kList;
     const int place = lists++ & 1;
     if (fits) {
       int to = (int)at;
-      each([&](float v, int i) {
-        S.list_x[place][to] = v;
-        S.list_i[place][to++] = i;
-      });
-      __syncthreads();
+      if (n > 0)
+        each([&](float v, int i) {
+          if (in(v, i)) {
+            S.list_x[place][to] = v;
+            S.list_i[place][to++] = i;
+          }
+        });
       run = ((int)all + kThreads - 1) / kThreads;
       const int from = min((int)all, (int)threadIdx.x * run);
       run = min(run, (int)all - from);
       mine = S.list_x[place] + from;
       index = S.list_i[place] + from;
+      own = 0xFFFFFFFFu;
     }
-    if (alone) return true;
-    const u64 parts = exchange(fits ? all : (u64)kList + 1, 0, &others);   // (the lists are written before it)
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, C = (int)cluster.num_blocks();
-    u64 upto = parts;
-#pragma unroll
-    for (int off = 1; off < 32; off <<= 1) {
-      const u64 o = __shfl_up_sync(0xffffffffu, upto, off);
-      if (lane >= off) upto += o;
-    }
+    const u64 parts = exchange(fits ? all : u64(1) << 20), upto = warp_upto(parts);   // (the lists are written before it)
     const int sum = (int)__shfl_sync(0xffffffffu, upto, 31);
-    if (sum > kList) return true;
-    if (cluster.block_rank() == 0) {   // a warp for each CTA's list
-      for (int r = warp; r < C; r += kThreads / 32) {
+    if (sum > kList) {
+      __syncthreads();
+      return kSpread;
+    }
+    listed = sum;
+    all_x = S.list_x[place];
+    all_i = S.list_i[place];
+    if (C == 1) {
+      __syncthreads();
+      return kAlone;
+    }
+    if (rank == 0) {   // a warp for each CTA's list
+      float* xs = S.list_x[place ^ 1];
+      int* is = S.list_i[place ^ 1];
+      for (int r = threadIdx.x >> 5; r < C; r += kWarps) {
         const int to = (int)__shfl_sync(0xffffffffu, upto - parts, r), len = (int)__shfl_sync(0xffffffffu, parts, r);
         const float* from_x = cluster.map_shared_rank(S.list_x[place], r);
         const int* from_i = cluster.map_shared_rank(S.list_i[place], r);
-        for (int j = lane; j < len; j += 32) {
-          S.list_x[place ^ 1][to + j] = from_x[j];
-          S.list_i[place ^ 1][to + j] = from_i[j];
+        for (int j = threadIdx.x & 31; j < len; j += 32) {
+          xs[to + j] = from_x[j];
+          is[to + j] = from_i[j];
         }
       }
+      all_x = xs;
+      all_i = is;
     }
     cluster.sync();   // no CTA ends while another one reads its shared memory
-    if (cluster.block_rank() != 0) return false;
-    alone = true;
-    run = (sum + kThreads - 1) / kThreads;
-    const int from = min(sum, (int)threadIdx.x * run);
-    run = min(run, sum - from);
-    mine = S.list_x[place ^ 1] + from;
-    index = S.list_i[place ^ 1] + from;
-    ++lists;
-    return true;
+    return rank == 0 ? kAlone : kDone;
   }
 };
 
-// The float of a key.
-__device__ __forceinline__ float float_of(uint32_t key) { return __uint_as_float(key & 0x80000000u ? key & 0x7FFFFFFFu : ~key); }
+// log of total / 2^kUnit weights of 1, less w's: the logprob's terms in units of log2(e)^-1 are exact but for some 2^-34.
+__device__ __forceinline__ float logprob_of(float v, float top, Slope c, u64 total, const u64* table) {
+  // log2(total) = e + j / kSteps + log2(1 + r): the table's entry kSteps - j is 2^(j / kSteps) below one octave
+  const int e = 63 - __clzll(total);
+  const u64 m = e >= kUnit ? total >> (e - kUnit) : total << (kUnit - e);   // in [2^kUnit, 2^(kUnit + 1))
+  const float log2m = log2f((float)m * 0x1p-42f);
+  int j = min(kSteps - 1, max(0, (int)(log2m * kSteps)));
+  const u64 base = j ? 2 * table[kSteps - j] : u64(1) << kUnit;
+  const float r = (float)(long long)(m - base) / (float)base;
+  const float rest = r * 1.44269504f * (1.0f - r * (0.5f - r * 0.333333333f));
+  const float whole = (float)(e - kUnit) + (float)j * (1.0f / kSteps);        // exact
+  float th = 0.0f, tl = 0.0f;
+  if (v != top) {
+    const float d = v - top, b = d - v, lost = (v - (d - b)) + (-top - b);
+    th = d * c.hi;
+    tl = __fmaf_rn(d, c.hi, -th) + __fmaf_rn(d, c.lo, lost * c.hi);
+  }
+  const float s = th - whole, b = s - th, err = (th - (s - b)) + (-whole - b);   // s + err = th - whole
+  const float low = (tl - rest) + err, hi = s + low, lo = low - (hi - s);
+  return __fmaf_rn(hi, 0.693147182464599609375f, __fmaf_rn(hi, -1.904654323148236017e-09f, lo * 0.693147182f));
+}
+
+// The rest of a row whose tokens are R's list: they are sorted, and everything else is two sums along them.  k: how many of
+// them top_k leaves; all: the sum that top_p is a share of (0: of those k).
+__device__ __forceinline__ void end_alone(const qmm_sample_args& a, Sampler& R, int t, int k, float p, float mp, u64 least, u64 all) {
+  Cta& S = R.S;
+  const int tid = threadIdx.x, n = R.listed;
+  int n2 = 2;
+  while (n2 < n) n2 *= 2;
+  u64* sorted = S.mass;        // key, place from the end: the highest key first, of equal ones the lowest place
+  u64* kept = S.mass_total;    // weights that stay, by place
+  for (int e = tid; e < n2; e += kThreads)
+    sorted[e] = e < n ? (u64)key_of(R.all_x[e]) << 32 | (0xFFFFFFFFu - (uint32_t)e) : 0;
+  __syncthreads();
+  for (int size = 2; size <= n2; size *= 2) {
+    for (int stride = size / 2; stride > 0; stride /= 2) {
+      if (tid < n2 / 2) {
+        const int i = 2 * stride * (tid / stride) + tid % stride;
+        const u64 u = sorted[i], v = sorted[i + stride];
+        if ((u < v) == ((i & size) == 0)) {
+          sorted[i] = v;
+          sorted[i + stride] = u;
+        }
+      }
+      // (a warp keeps to its own 64 entries while the strides are at most 32)
+      const int next = stride > 1 ? stride / 2 : size;
+      if (stride > 32 || next > 32) __syncthreads();
+      else __syncwarp();
+    }
+  }
+  __syncthreads();
+  u64 w[2] = {0, 0}, sum;
+  int place[2];
+#pragma unroll
+  for (int q = 0; q < 2; ++q) {
+    const int e = 2 * tid + q;
+    place[q] = -1;
+    if (e < n) {
+      const u64 v = sorted[e];
+      place[q] = (int)(0xFFFFFFFFu - (uint32_t)v);
+      if (e < k) w[q] = R.weight_of(float_of((uint32_t)(v >> 32)));
+    }
+  }
+  u64 at = R.block_before(w[0] + w[1], &sum);
+  u64 target = ~u64(0);
+  if (p < 1.0f) {
+    bool exact;
+    target = fraction_of(fmaxf(p, 0.0f), all ? all : sum, &exact);
+    target = max(u64(1), target + !exact);
+  }
+#pragma unroll
+  for (int q = 0; q < 2; ++q) {
+    const bool stays = mp > 1.0f ? tid + q == 0 : at < target && w[q] >= least;
+    if (place[q] >= 0) kept[place[q]] = stays ? w[q] : 0;
+    at += w[q];
+  }
+  __syncthreads();
+  const u64 k0 = 2 * tid < n ? kept[2 * tid] : 0, k1 = 2 * tid + 1 < n ? kept[2 * tid + 1] : 0;
+  u64 total;
+  const u64 before = R.block_before(k0 + k1, &total);
+  bool exact;
+  const u64 goal = fraction_of(fminf(fmaxf(a.uniform[t], 0.0f), 0x1.fffffep-1f), total, &exact);
+  if (before <= goal && before + k0 + k1 > goal) {
+    const int e = 2 * tid + (before + k0 <= goal);
+    a.tokens[t] = R.all_i[e];
+    if (a.logprobs) a.logprobs[t] = logprob_of(R.all_x[e], R.top, R.c, total, S.table);
+  }
+}
 
 // A cluster per row.  The borders are found by sums over bins (of counts for top_k, of weights for top_p), first over the
 // distance from the largest logit, then over the keys of the bin in which the border lies, until a bin is one key; ties
-// on it go by index.  Before that, a floor leaves most of a vocabulary behind.
+// on it go by index.  Before that, a floor leaves most of a vocabulary behind, and what is above it is as a rule
+// few enough for one CTA to sort.
 template <int TYPE>
 __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_constant__ qmm_sample_args a, int run, int vec) {
   extern __shared__ __align__(16) uint8_t smem[];
-  Sampler<TYPE> R{*reinterpret_cast<Cta*>(smem), reinterpret_cast<float*>(smem + sizeof(Cta))};
+  Sampler R{*reinterpret_cast<Cta*>(smem), reinterpret_cast<float*>(smem + sizeof(Cta))};
   Cta& S = R.S;
-  // launched early behind a launch that allows it: memory is read from here on
+  for (int j = threadIdx.x; j < kSteps; j += kThreads) S.table[j] = kTable.v[j];
+  // launched early behind a launch that allows it: memory that it may be writing is read from here on
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  const int rank = (int)R.cluster.block_rank();
-  const int t = blockIdx.x / (int)R.cluster.num_blocks(), V = a.V, slice = run * kThreads, begin = rank * slice;
+  const int t = blockIdx.x / R.C, V = a.V, slice = run * kThreads, begin = R.rank * slice;
   const int n = max(0, min(V - begin, slice));
   const uint8_t* row = static_cast<const uint8_t*>(a.logits) + t * a.ld * (TYPE == QMM_F32 ? 4 : 2);
-  R.alone = R.cluster.num_blocks() == 1;
   R.run = run;
   R.first = begin + (int)threadIdx.x * run;
   R.mine = R.x + (int)threadIdx.x * run;
@@ -457,6 +589,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
   auto take = [&](float v) { return v == v ? v + 0.0f : -INFINITY; };   // (-0 and 0 are equal)
   constexpr int kPerVec = TYPE == QMM_F32 ? 4 : 8;
   const int whole = vec ? n / kPerVec * kPerVec : 0;
+#pragma unroll 4
   for (int i = kPerVec * threadIdx.x; i < whole; i += kPerVec * kThreads) {
     const uint4 w = *reinterpret_cast<const uint4*>(row + (int64_t)(begin + i) * (TYPE == QMM_F32 ? 4 : 2));
     const uint32_t u[4] = {w.x, w.y, w.z, w.w};
@@ -473,10 +606,10 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
   }
   for (int i = whole + threadIdx.x; i < n; i += kThreads) R.x[i] = take(logit<TYPE>(row, begin + i));
   for (int i = n + threadIdx.x; i < slice; i += kThreads) R.x[i] = -INFINITY;
-  for (int j = threadIdx.x; j < kSteps; j += kThreads) S.table[j] = kTable.v[j];
   __syncthreads();
   float own = -INFINITY;   // this thread's largest, and where
   int where = 0;
+#pragma unroll 4
   for (int j = 0; j < run; ++j) {
     const float v = R.mine[j];
     if (v > own) {
@@ -484,25 +617,28 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
       where = j;
     }
   }
-  u64 lows;   // of the threads' largest finite ones
-  const u64 best = R.cluster_max((u64)key_of(own) << 32 | (0xFFFFFFFFu - (uint32_t)(R.first + where)),
-                                 own > -INFINITY ? 0xFFFFFFFFu - key_of(own) : 0, &lows);
-  const int argmax = (int)(0xFFFFFFFFu - (uint32_t)best);
-  const uint32_t top_key = (uint32_t)(best >> 32);
+  R.own = key_of(own);
+  uint32_t top_key = R.own, argmax = (uint32_t)(R.first + where), lowest = own > -INFINITY ? R.own : 0xFFFFFFFFu;
+  R.best_of(top_key, argmax, lowest);
   const float top = float_of(top_key), temperature = a.temperature ? a.temperature[t] : 1.0f;
   R.top = top;
   if (top == -INFINITY || !(temperature > 0.0f)) {
-    if (rank == 0 && threadIdx.x == 0) {
-      a.tokens[t] = top == -INFINITY ? -1 : argmax;
+    if (R.rank == 0 && threadIdx.x == 0) {
+      a.tokens[t] = top == -INFINITY ? -1 : (int)argmax;
       if (a.logprobs) a.logprobs[t] = top == -INFINITY ? -INFINITY : 0.0f;
     }
-    if (!R.alone) R.cluster.sync();   // no CTA ends while another one reads its shared memory
+    R.sync();   // no CTA ends while another one reads its shared memory
     return;
   }
   R.c = slope_of(temperature);
   const int k = a.top_k ? a.top_k[t] : 0;
   const float p = a.top_p ? a.top_p[t] : 1.0f, mp = a.min_p ? a.min_p[t] : 0.0f;
   const bool by_k = k > 0 && k < V, by_p = p < 1.0f;
+  u64 least = 0;   // the least weight that min_p lets stay
+  if (mp > 0.0f) {
+    bool exact = true;
+    least = mp < 1.0f ? fraction_of(mp, u64(1) << kUnit, &exact) + !exact : u64(1) << kUnit;
+  }
 
   // bins over the distance from the top
   float per = 0.0f;
@@ -515,24 +651,9 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
     return d >= kBins - 1 ? kBins - 1 : (int)d;   // (NaN: an infinite top itself, bin 0)
   };
   auto half_bin = [&](float v) { return distance_bin(v) >> 1; };   // of weights
-  // the keys of bins b1 .. b2
-  auto keys_of = [&](int b1, int b2) -> Keys {
-    if (threadIdx.x < 2) {
-      // the lowest key whose bin is at most b2; the lowest one whose bin is at most b1 - 1, less one
-      const int b = threadIdx.x ? b1 - 1 : b2;
-      uint32_t lo = 0x007FFFFFu, hi = 0xFF800001u;   // of -infinity, behind infinity
-      while (lo < hi) {
-        const uint32_t mid = lo + (hi - lo) / 2;
-        if (mid <= 0xFF800000u && distance_bin(float_of(mid)) > b) lo = mid + 1;
-        else hi = mid;
-      }
-      S.found[threadIdx.x] = threadIdx.x ? (b < 0 ? 0xFF800000u : lo - 1) : lo;
-    }
-    __syncthreads();
-    const Keys r{(uint32_t)S.found[0], (uint32_t)S.found[1]};
-    __syncthreads();
-    return r;
-  };
+  // the lowest key that a token within d of the top can have
+  auto key_within = [&](float d) { return top < INFINITY ? key_of(top - d * (1.0f + 1e-5f) - fabsf(top) * 1e-6f) : top_key; };
+  auto distance_to = [&](uint32_t key) { return top - float_of(max(key, 0x00800000u)); };   // of a finite key
 
   // what stays: keys above cut, and those on it up to the index last
   uint32_t cut = 0;
@@ -541,32 +662,27 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
     const uint32_t key = key_of(v);
     return key > cut || (key == cut && i <= last);
   };
-  // the lowest key that a token within d of the top can have
-  auto key_within = [&](float d) { return top < INFINITY ? key_of(top - d * (1.0f + 1e-5f) - fabsf(top) * 1e-6f) : top_key; };
   auto everything = [](float, int) { return true; };
 
   if (by_k) {
     int b;
     u64 above;
-    // k threads have a token at or above the k-th largest of the threads' largest: nothing below it stays
-    bins_over(top - float_of(0xFFFFFFFFu - (uint32_t)lows));
-    if (k <= kThreads * (int)R.cluster.num_blocks()) {
+    bins_over(distance_to(lowest));
+    if (k <= kThreads * R.C) {
+      // k threads have a token at or above the k-th largest of the threads' largest: nothing below it stays
       R.histogram_of(own, distance_bin);
-      R.template find<uint32_t>((u64)k, &b, &above);
-      if (!R.raise_floor(keys_of(b, b).lo)) return;
-      bins_over(top - float_of(max(R.floor, 0x00800000u)));
+      R.find<uint32_t>((u64)k, &b, &above);
+      const Raised now = R.raise_floor(R.keys_of(b, b, distance_bin).lo, everything);
+      if (now == kAlone) end_alone(a, R, t, k, p, mp, least, 0);
+      if (now != kSpread) return;
+      bins_over(distance_to(R.floor));
     }
-    R.template histogram<uint32_t>(everything, distance_bin);
-    R.template find<uint32_t>((u64)k, &b, &above);
-    Keys r = keys_of(b, b);
-    above += R.template narrow<uint32_t>(r, (u64)k - above, everything);
+    R.histogram<uint32_t>(everything, distance_bin);
+    R.find<uint32_t>((u64)k, &b, &above);
+    Keys r = R.keys_of(b, b, distance_bin);
+    above += R.narrow<uint32_t>(r, (u64)k - above, everything);
     last = R.tie_index(r.lo, (u64)k - above, everything);
     cut = r.lo;
-  }
-  u64 least = 0;   // the least weight that min_p lets stay
-  if (mp > 0.0f) {
-    bool exact = true;
-    least = mp < 1.0f ? fraction_of(mp, u64(1) << kUnit, &exact) + !exact : u64(1) << kUnit;
   }
   if (by_p) {
     u64 all = 0;
@@ -577,29 +693,32 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
     target = max(u64(1), target + !exact);
     // tokens of less than (1 - top_p) of the sum, divided by their number, cannot make up what may go: the border is above
     const float spare = fmaxf((float)(all - target), 1.0f) * 0.999f / (float)V, reach = log2f(0x1p42f / spare) / R.c.hi;
-    if (!(R.alone && R.index) && !R.raise_floor(max(cut, key_within(reach)))) return;
-    Keys r{max(R.floor, cut), top_key};
+    const Raised now = R.raise_floor(max(cut, key_within(reach)), in);
+    if (now == kAlone) end_alone(a, R, t, R.listed, p, mp, least, all);
+    if (now != kSpread) return;
+    Keys r{R.floor, top_key};
     u64 above = 0;
-    bins_over(fminf(reach, top - float_of(max(r.lo, 0x00800000u))));
+    bins_over(fminf(reach, distance_to(R.floor)));
     if (per > 0.0f) {
       int b;
-      R.template histogram<u64>(in, half_bin);
-      R.template find<u64>(target, &b, &above);
-      r = keys_of(2 * b, 2 * b + 1);
+      R.histogram<u64>(in, half_bin);
+      R.find<u64>(target, &b, &above);
+      r = R.keys_of(2 * b, 2 * b + 1, distance_bin);
       r.hi = min(r.hi, top_key);
     }
-    above += R.template narrow<u64>(r, target - above, in);
+    above += R.narrow<u64>(r, target - above, in);
     const u64 one = max(R.weight_of(float_of(r.lo)), u64(1));
     const int index = R.tie_index(r.lo, (target - above + one - 1) / one, in);
     if (r.lo > cut || index < last) last = index;   // (of those that top_k left on it)
     cut = r.lo;
+  } else if (mp > 0.0f) {
+    const Raised now = R.raise_floor(max(cut, key_within(log2f(1.0f / fminf(mp, 1.0f)) / R.c.hi)), in);
+    if (now == kAlone) end_alone(a, R, t, R.listed, p, mp, least, 0);
+    if (now != kSpread) return;
   }
-  if (mp > 0.0f) {
-    if (!by_p && !(R.alone && R.index) && !R.raise_floor(max(cut, key_within(log2f(1.0f / fminf(mp, 1.0f)) / R.c.hi)))) return;
-    if (mp > 1.0f) {
-      cut = top_key;
-      last = argmax;
-    }
+  if (mp > 1.0f) {
+    cut = top_key;
+    last = (int)argmax;
   }
 
   // what stays, and the token
@@ -612,41 +731,32 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
   u64 total;
   const u64 before = R.cluster_before(sure, &total);
   bool exact;
-  const float u = fminf(fmaxf(a.uniform[t], 0.0f), 0x1.fffffep-1f);
-  const u64 target = fraction_of(u, total, &exact);
-  const uint32_t who = __ballot_sync(0xffffffffu, before <= target && before + sure > target);
-  if (who) {   // the warp goes through the run of its thread that has it
+  const u64 goal = fraction_of(fminf(fmaxf(a.uniform[t], 0.0f), 0x1.fffffep-1f), total, &exact);
+  const uint32_t who = __ballot_sync(0xffffffffu, before <= goal && before + sure > goal);
+  if (who) {   // the warp goes through the tokens of its thread that has it
     const int lane = threadIdx.x & 31, from = __ffs(who) - 1;
     u64 at = __shfl_sync(0xffffffffu, before, from);
-    const int begin_of = __shfl_sync(0xffffffffu, (int)(R.mine - R.x), from), len = __shfl_sync(0xffffffffu, R.run, from);
-    const int first = __shfl_sync(0xffffffffu, R.first, from);
-    const int* index = R.index ? R.index + (__shfl_sync(0xffffffffu, (int)(R.mine - R.x), from) - (int)(R.mine - R.x)) : nullptr;
+    const int off = __shfl_sync(0xffffffffu, (int)(R.mine - R.x), from) - (int)(R.mine - R.x);   // of its tokens from this thread's
+    const int len = __shfl_sync(0xffffffffu, R.run, from), first = __shfl_sync(0xffffffffu, R.first, from);
     for (int j0 = 0; j0 < len; j0 += 32) {
       const bool here = j0 + lane < len;
-      const float v = here ? R.x[begin_of + j0 + lane] : -INFINITY;
-      const int i = !here ? 0 : index ? index[j0 + lane] : first + j0 + lane;
+      const float v = here ? R.mine[off + j0 + lane] : -INFINITY;
+      const int i = !here ? 0 : R.index ? R.index[off + j0 + lane] : first + j0 + lane;
       u64 w = here && key_of(v) >= R.floor && in(v, i) ? R.weight_of(v) : 0;
       if (w < least) w = 0;
-      u64 upto = w;
-#pragma unroll
-      for (int off = 1; off < 32; off <<= 1) {
-        const u64 o = __shfl_up_sync(0xffffffffu, upto, off);
-        if (lane >= off) upto += o;
-      }
-      const uint32_t hit = __ballot_sync(0xffffffffu, at + upto > target);
+      const u64 upto = at + warp_upto(w);
+      const uint32_t hit = __ballot_sync(0xffffffffu, upto > goal);
       if (hit) {
         if (lane == __ffs(hit) - 1) {
           a.tokens[t] = i;
-          if (a.logprobs)
-            a.logprobs[t] = (float)((v == top ? 0.0 : ((double)v - (double)top) / (double)temperature) -
-                                    log((double)total * (1.0 / (double)(u64(1) << kUnit))));
+          if (a.logprobs) a.logprobs[t] = logprob_of(v, top, R.c, total, S.table);
         }
         break;
       }
-      at += __shfl_sync(0xffffffffu, upto, 31);
+      at = __shfl_sync(0xffffffffu, upto, 31);
     }
   }
-  if (!R.alone) R.cluster.sync();   // no CTA ends while another one reads its shared memory
+  R.sync();   // no CTA ends while another one reads its shared memory
 }
 
 // A thread per stream.
