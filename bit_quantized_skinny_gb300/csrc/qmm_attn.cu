@@ -558,71 +558,104 @@ __global__ void __launch_bounds__(kThreads<FP4>, 1) attn_kernel(const __grid_con
     // ------------------------------------------------------------------ 4 bits to fp16
     // A thread takes a block of 16 values: a code times its scale is exact in fp16 (two and four
     // significant bits).  Rows of values behind the last key are zeroed, and so are NaN blocks among the keys that
-    // only some rows of the block see (a draft's last keys); attn_combine_kernel adds those back.
+    // only some rows of the block see (a draft's last keys); attn_combine_kernel adds those back.  A step is the
+    // keys of a tile and the values of the one before: one round of waits, loads, fence and arrivals for both (by
+    // themselves each took as long, and the four warps, one a scheduler, have nobody to cover for them).
     constexpr int kBlocks = D / kv4::kBlock, kUnits = kTile * kBlocks / (32 * kDequantWarps);
     const int me = (warp - kFirstDequantWarp) * 32 + lane;
-    uint32_t taken = 0, filled[2] = {0, 0}, items = 0, segs = 0;
+    uint32_t taken = 0, filled_k = 0, filled_v = 0, items = 0, segs = 0;
     bool ok = true;
+    // (a phase that is over is the rule: the suspended wait costs 200 clocks even then)
+    auto soon = [&](int k, uint32_t parity) { if (!mbar_try(bar(k), parity)) ok = wait(k, parity) && ok; };
+    struct Units {
+      uint2 code[kUnits];
+      uint32_t scale[kUnits];
+    };
+    auto load = [&](uint32_t pack, Units& x) {
+      const uint8_t* src = smem + L::kPack + pack * L::kPackBytes;
+#pragma unroll
+      for (int u = 0; u < kUnits; ++u) {
+        const int unit = u * 32 * kDequantWarps + me;
+        x.code[u] = *reinterpret_cast<const uint2*>(src + unit * 8);
+        x.scale[u] = src[kTile * (D / 2) + unit];
+      }
+    };
+    auto store = [&](uint8_t* dst, const Units& x, auto&& drop) {   // drop(key of the tile, scale): zeros instead
+#pragma unroll
+      for (int u = 0; u < kUnits; ++u) {
+        const int unit = u * 32 * kDequantWarps + me, key = unit / kBlocks, b = unit % kBlocks;
+        const bool zero = drop(key, x.scale[u]);
+        const uint32_t s = zero ? 0u : e4m3x2_pair(x.scale[u] * 0x101u);
+        uint32_t lo[4], hi[4];
+        e2m1x8_pairs(x.code[u].x, lo);
+        e2m1x8_pairs(x.code[u].y, hi);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          lo[e] = mul2(lo[e], s);
+          hi[e] = mul2(hi[e], s);
+        }
+        uint8_t* row = dst + (b / 4) * L::kHalf + key * 128;
+        // (the halves of a key in turn: eight neighbouring threads write to eight different 16-byte columns)
+        const int c0 = 2 * (b % 4), turn = b / 4 & 1;
+        const uint4 first = turn ? make_uint4(hi[0], hi[1], hi[2], hi[3]) : make_uint4(lo[0], lo[1], lo[2], lo[3]);
+        const uint4 other = turn ? make_uint4(lo[0], lo[1], lo[2], lo[3]) : make_uint4(hi[0], hi[1], hi[2], hi[3]);
+        *reinterpret_cast<uint4*>(row + ((c0 + turn) ^ (key & 7)) * 16) = first;
+        *reinterpret_cast<uint4*>(row + ((c0 + 1 - turn) ^ (key & 7)) * 16) = other;
+      }
+    };
     while (ok && walk.next(P, g)) {
       const int n = g.j1 - g.j0;
       const bool pair = g.rows > P.tokens;
       const int clean_from = g.own ? clampi(g.first_keys, 0, g.keys) : g.keys;
       ++segs;
-      ok = in_order(n, [&](auto values, int t) {
-        constexpr bool kValues = decltype(values)::value;
-        const uint32_t users = pair ? 2 : (items + t) & 1;
-        const uint32_t from = taken % L::kPacks, st = filled[kValues] % kS, use = filled[kValues] / kS;
-        if (!wait_w(kBarPackFull + from, (taken / L::kPacks) & 1)) return false;
-        if (use > 0 && !wait_w((kValues ? kBarEmptyV : kBarEmptyK) + st, (use - 1) & 1)) return false;
-        const uint8_t* src = smem + L::kPack + from * L::kPackBytes;
-        uint8_t* dst = smem + (kValues ? L::kV : L::kK) + st * L::kTileBytes;
-        const int base = (g.j0 + t) * kTile;
-        uint2 code[kUnits];
-        uint32_t scale[kUnits];
-#pragma unroll
-        for (int u = 0; u < kUnits; ++u) {
-          const int unit = u * 32 * kDequantWarps + me;
-          code[u] = *reinterpret_cast<const uint2*>(src + unit * 8);
-          scale[u] = src[kTile * (D / 2) + unit];
+      for (int t = 0; ok && t <= n; ++t) {   // the keys of tile t, the values of tile t - 1
+        const bool keys = t < n, values = t > 0;
+        const uint32_t pk = taken % L::kPacks, pv = (taken + keys) % L::kPacks;
+        const uint32_t sk = filled_k % kS, sv = filled_v % kS;
+        if (keys) {
+          soon(kBarPackFull + pk, (taken / L::kPacks) & 1);
+          if (filled_k >= kS) soon(kBarEmptyK + sk, (filled_k / kS - 1) & 1);
         }
-#pragma unroll
-        for (int u = 0; u < kUnits; ++u) {
-          const int unit = u * 32 * kDequantWarps + me, key = unit / kBlocks, b = unit % kBlocks;
-          const uint32_t s = e4m3x2_pair(scale[u] * 0x101u);
-          uint32_t lo[4], hi[4];
-          e2m1x8_pairs(code[u].x, lo);
-          e2m1x8_pairs(code[u].y, hi);
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            lo[e] = mul2(lo[e], s);
-            hi[e] = mul2(hi[e], s);
+        if (values) {
+          soon(kBarPackFull + pv, ((taken + keys) / L::kPacks) & 1);
+          if (filled_v >= kS) soon(kBarEmptyV + sv, (filled_v / kS - 1) & 1);
+        }
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        Units k, v;
+        if (keys) load(pk, k);
+        if (values) load(pv, v);
+        if (keys) store(smem + L::kK + sk * L::kTileBytes, k, [](int, uint32_t) { return false; });
+        if (values) {
+          const int base = (g.j0 + t - 1) * kTile;
+          bool odd = false;
+          if (base + kTile <= clean_from) {
+            store(smem + L::kV + sv * L::kTileBytes, v, [](int, uint32_t) { return false; });
+          } else {
+            store(smem + L::kV + sv * L::kTileBytes, v, [&](int key, uint32_t scale) {
+              const bool behind = base + key >= g.keys, nan = (scale & 0x7Fu) == kv4::kScaleNaN && base + key >= clean_from;
+              odd |= nan && !behind;
+              return behind || nan;
+            });
+            if (odd) *reinterpret_cast<volatile uint32_t*>(&M.odd[segs & 7]) = segs;
           }
-          if constexpr (kValues) {
-            const bool odd = (scale[u] & 0x7Fu) == kv4::kScaleNaN && base + key >= clean_from;
-            if (base + key >= g.keys || odd) {
-              if (base + key < g.keys) *reinterpret_cast<volatile uint32_t*>(&M.odd[segs & 7]) = segs;
-#pragma unroll
-              for (int e = 0; e < 4; ++e) lo[e] = hi[e] = 0u;
-            }
-          }
-          uint8_t* row = dst + (b / 4) * L::kHalf + key * 128;
-          // (the halves of a key in turn: eight neighbouring threads write to eight different 16-byte columns)
-          const int c0 = 2 * (b % 4), turn = b / 4 & 1;
-          const uint4 first = turn ? make_uint4(hi[0], hi[1], hi[2], hi[3]) : make_uint4(lo[0], lo[1], lo[2], lo[3]);
-          const uint4 other = turn ? make_uint4(lo[0], lo[1], lo[2], lo[3]) : make_uint4(hi[0], hi[1], hi[2], hi[3]);
-          *reinterpret_cast<uint4*>(row + ((c0 + turn) ^ (key & 7)) * 16) = first;
-          *reinterpret_cast<uint4*>(row + ((c0 + 1 - turn) ^ (key & 7)) * 16) = other;
         }
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) {
-          mbar_arrive(bar((kValues ? kBarFullV : kBarFullK) + kS * users + st));
-          mbar_arrive(bar(kBarPackEmpty + from));
+          if (keys) {
+            mbar_arrive(bar(kBarFullK + kS * (pair ? 2 : (items + t) & 1) + sk));
+            mbar_arrive(bar(kBarPackEmpty + pk));
+          }
+          if (values) {
+            mbar_arrive(bar(kBarFullV + kS * (pair ? 2 : (items + t - 1) & 1) + sv));
+            mbar_arrive(bar(kBarPackEmpty + pv));
+          }
         }
-        ++taken;
-        ++filled[kValues];
-        return true;
-      });
+        taken += (keys ? 1 : 0) + (values ? 1 : 0);
+        filled_k += keys;
+        filled_v += values;
+      }
       items += pair ? 2 * n : n;
     }
   } else if (warp == kLoadWarp) {
