@@ -1,15 +1,8 @@
 // qmm_attn.cu — attention of several streams' rows over a prefix that they share and over each
 // stream's own keys, both in pages of one cache (qmm_attn_shared).
 //
-// Work.  A group is a block of rows that see the same keys, with one key/value head: for the prefix
-// the rows of all streams, for own keys the rows of one stream; the G query heads of a key/value
-// head are rows of the same block, so a key is read once for all of them.  A row tile is 128 rows
-// (128 / G tokens) and a block up to two tiles; a key tile is 64 keys.  The key tiles of all groups
-// form one list, each group led by kLead units for what a segment costs besides its tiles, cut into
-// equal pieces, one per CTA (one CTA an SM): every SM has the same work whatever the lengths, and the
-// lengths stay on the device.  A piece holds one or several segments (runs of one group's key tiles).
-// Each segment leaves its sums unnormalised in the workspace, with the running maximum and weight sum
-// of each row, and attn_combine_kernel joins a row's segments in their order.
+// Work: equal pieces of the list of all key tiles, joined by a second launch (q4k_attn_parts.cuh).  A row tile is 128
+// rows (128 / G tokens) and a block up to two tiles; a key tile is 64 keys.
 //
 // One segment.  Two lanes of flash attention take turns on the tensor cores: with more than one row
 // tile each lane has a row tile and both read every key tile; with one, the lanes take the key tiles
@@ -45,11 +38,10 @@
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
+#include "q4k_attn_parts.cuh"
 #include "q4k_device.cuh"
 #include "q4k_device_once.h"
-#include "q4k_formats.cuh"
 #include "q4k_internal.h"
-#include "q4k_kv_fp4.cuh"
 #include "q4k_tcgen05.cuh"
 
 namespace q4k {
@@ -57,61 +49,35 @@ namespace {
 
 __device__ unsigned g_status;   // this file's kernels' status word
 
-constexpr int kRows = 128;           // rows of a row tile
 constexpr int kTile = 64;            // keys of a key tile
 constexpr int kLead = 4;             // units of a group besides its key tiles (2, 3, 6: 10, 6, 2 % slower for 16 streams)
-constexpr int kMaxCtas = 152;
 constexpr int kLaneWarps = 4;
 constexpr int kLoadWarp = 8, kMmaWarp = 9 /* and 10 */, kQWarp = 11;
-constexpr int kFirstDequantWarp = 12, kDequantWarps = 4;   // of a 4-bit cache
+constexpr int kThreads = 12 * 32;
 constexpr uint32_t kTmemCols = 512;   // lane L: S at 64 L, p at 128 + 64 L and 160 + 64 L, O at 256 + 128 L
 constexpr float kGrow = 8.0f;
-constexpr float kLift = 7.0f;        // fp16 weights lie at 2^kLift: at most 2^(kLift + kGrow), and normal down to 2^(-14 - kLift)
-constexpr int kFactorTiles = 8;      // (the roles are a few tiles apart)
 constexpr uint32_t kWaitLimit = 1u << 17;
-constexpr float kLog2e = 1.44269504088896340736f, kLn2 = 0.69314718055994530942f;
+constexpr float kLog2e = 1.44269504088896340736f;
 
-// One row's state beside its O: the maximum in units of log2, the weight sum, whether values were
-// taken out of the block (nonzero), and, in the record of a group's first segment, the CTAs that hold
-// the others: their number << 16 | the first of them.
-struct RowStat {
-  float top, sum;
-  uint32_t odd, rest;
-};
-
-struct Params {
-  qmm_attn_args a;
+struct Params : Common {
   CUtensorMap mapQ, mapK, mapV;
-  float* o_rows;      // [2][T * Hq][D]: first segments, of the prefix and of own keys
-  RowStat* s_rows;
-  float* o_cta;       // [kMaxCtas][2 * kRows][D]: a CTA's first segment that begins inside a group
-  RowStat* s_cta;
-  int tokens;         // of a row tile
-  int n_pages, page_shift;
-  uint32_t wait_polls, wait_ns;
-  float k_scale, v_scale;   // of a 4-bit cache's tensors
 };
 
-template <int D, bool FP4>
+template <int D>
 struct Smem {
   static constexpr int kHalf = kTile * 128;              // 64 keys of 64 values
   static constexpr int kTileBytes = kTile * D * 2;
   static constexpr int kQHalf = kRows * 128;
   static constexpr int kQBytes = kRows * D * 2;
-  static constexpr int kStages = FP4 && D == 128 ? 3 : 5;   // of keys, and of values
-  static constexpr int kPackBytes = kTile * kv4::slot_bytes(D);   // a tile as the 4-bit cache holds it
-  static constexpr int kPacks = 12;
+  static constexpr int kStages = 5;                      // of keys, and of values
   static constexpr int kQ = 0;
   static constexpr int kK = 2 * kQBytes;
   static constexpr int kV = kK + kStages * kTileBytes;
-  static constexpr int kPack = kV + kStages * kTileBytes;
-  static constexpr int kStats = kPack + (FP4 ? kPacks * kPackBytes : 0);   // (top, sum) of the two lanes' rows
-  static constexpr int kFactors = kStats + 2 * kRows * 8;      // of the rows of the last kFactorTiles query tiles
-  static constexpr int kMisc = kFactors + (FP4 ? kFactorTiles * kRows * 4 : 0);
+  static constexpr int kStats = kV + kStages * kTileBytes;   // (top, sum) of the two lanes' rows
+  static constexpr int kMisc = kStats + 2 * kRows * 8;
   static constexpr int kTotal = kMisc + 1024;
 };
-static_assert(Smem<128, false>::kTotal <= 227 * 1024 && Smem<128, true>::kTotal <= 227 * 1024 &&
-              Smem<64, false>::kTotal <= 227 * 1024 && Smem<64, true>::kTotal <= 227 * 1024, "shared memory");
+static_assert(Smem<128>::kTotal <= 227 * 1024 && Smem<64>::kTotal <= 227 * 1024, "shared memory");
 
 // Barriers.  A wait tells a phase from the one after it only, so a barrier is waited on by threads that
 // see all of its phases, or that know the phase before to be over and the one after not begun: a stage of keys or values has a full barrier for each set of users (lane
@@ -119,140 +85,22 @@ static_assert(Smem<128, false>::kTotal <= 227 * 1024 && Smem<128, true>::kTotal 
 enum : int {
   kBarFullK = 0 /* 5 users + stage */, kBarFullV = 15, kBarEmptyK = 30, kBarEmptyV = 35, kBarQFull = 40, kBarQEmpty = 42,
   kBarS = 44, kBarFree = 46, kBarP = 48 /* 2 lane + item % 2 */, kBarO = 52, kBarEnd = 56, kBarJoin = 58, kBarDrain = 59,
-  kBars16 = 61,                                    // of a cache of 16-bit values
-  kBarPackFull = 61, kBarPackEmpty = 73, kBars = 85   // and of a 4-bit cache's tiles
-};
-
-// Rows and own keys of a stream.
-struct Stream {
-  int t0, m, len;
+  kBars = 61
 };
 
 struct Misc {
   uint64_t bars[kBars];
-  int64_t w0, w1, per;   // this CTA's units, units of a CTA
-  int64_t scan[16];
-  int b, rb, h, rows;
-  Stream s;           // stream b, if b >= 0
-  int64_t unit;       // end of the CTA's units within that group
+  Piece piece;
   uint32_t tmem;
   int abort;
   uint32_t odd[8];    // [s % 8]: s, if values were taken out in segment s (the lanes drift a few apart)
 };
 static_assert(sizeof(Misc) <= 1024, "misc");
 
-__device__ __forceinline__ int clampi(int v, int lo, int hi) { return v < lo ? lo : (v > hi ? hi : v); }
-
-// Stream b, whatever the arrays hold.
-__device__ __forceinline__ Stream stream_of(const qmm_attn_args& a, int b, bool* bad = nullptr) {
-  const int r0 = a.row_starts[b], r1 = a.row_starts[b + 1], n = a.kv_lens[b];
-  const int cap = (int)(a.pages_per_stream * a.page_size);
-  Stream s;
-  s.t0 = clampi(r0, 0, a.T);
-  s.m = clampi(r1, s.t0, a.T) - s.t0;
-  s.len = n < 0 || n > cap ? 0 : n;
-  if (bad) *bad = r0 < 0 || r1 < r0 || r1 > a.T || (b == 0 && r0 != 0) || s.len != n;
-  return s;
-}
-// Own keys that the rows of row block rb may see (by its last row), and the tiles they fill.
-__device__ __forceinline__ int keys_of(const Stream& s, int rb, int block) {
-  return clampi(s.len - s.m + min(s.m, (rb + 1) * block), 0, s.len);
-}
-__device__ __forceinline__ int tiles_of(int keys) { return (keys + kTile - 1) / kTile; }
-__device__ __forceinline__ int units_of(int tiles) { return tiles > 0 ? tiles + kLead : 0; }
-
-// A run of key tiles of one group.
-struct Seg {
-  bool own;
-  int h;            // key/value head
-  int t0, rows;     // first row of the block, its rows (tokens)
-  int keys;         // keys that its last row sees
-  int first_keys;   // keys that its first row sees (below 0: rows further on see none either)
-  int j0, j1;       // key tiles
-  int rest;         // units of the group in the CTAs behind this one
-  const int32_t* pages;
-};
-
-// Steps through a CTA's segments, the last one first; every role has its own.  (A piece usually ends with
-// the beginning of a group and begins with the end of another: from the last one, the CTAs of the row
-// blocks of a long prefix read its keys from the front at about the same time, and find them in L2.
-// From the first one, each began elsewhere: 64 x 16 rows over 32768 keys read 1.9 GB from memory, not
-// 0.48 GB.)
-struct Walker {
-  int64_t left;
-  int b, rb, h, j;   // group, end of what is left of it in units (-1: all)
-  Stream s;
-  int block, rows;   // rows of a block, rows in streams
-
-  __device__ __forceinline__ void start(const Params& P, const Misc& m) {
-    left = m.w1 - m.w0;
-    b = m.b; rb = m.rb; h = m.h; j = (int)m.unit;
-    block = 2 * P.tokens;
-    rows = m.rows;
-    s = m.s;
-  }
-  __device__ __forceinline__ bool next(const Params& P, Seg& g) {
-    const qmm_attn_args& a = P.a;
-    while (left > 0 && b >= -1) {
-      if (rb < 0) {   // no group left of this stream
-        if (--b < -1) return false;
-        if (b >= 0) s = stream_of(a, b);
-        rb = ((b >= 0 ? s.m : rows) + block - 1) / block - 1;
-        h = a.Hk - 1;
-        j = -1;
-        continue;
-      }
-      g.own = b >= 0;
-      g.t0 = rb * block;
-      g.rows = min(block, (g.own ? s.m : rows) - g.t0);
-      if (g.own) {
-        g.keys = keys_of(s, rb, block);
-        g.first_keys = s.len - s.m + g.t0 + 1;
-        g.pages = a.pages + b * a.pages_per_stream;
-        g.t0 += s.t0;
-      } else {
-        g.keys = g.first_keys = (int)a.prefix_len;
-        g.pages = a.prefix_pages;
-      }
-      g.h = h;
-      const int units = units_of(tiles_of(g.keys)), end = j < 0 ? units : j;
-      const int take = (int)min((int64_t)end, left);
-      left -= take;
-      g.j0 = max(0, end - take - kLead);
-      g.j1 = end - kLead;
-      g.rest = units - end;
-      j = -1;
-      if (--h < 0) {
-        h = a.Hk - 1;
-        --rb;
-      }
-      if (g.j1 > g.j0) return true;   // (else the piece holds only some of the group's lead)
-    }
-    return false;
-  }
-};
-
 __device__ __forceinline__ void tma_3d(uint32_t dst, const CUtensorMap* map, int x, int y, int z, uint32_t bar) {
   asm volatile(
       "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];"
       :: "r"(dst), "l"(map), "r"(x), "r"(y), "r"(z), "r"(bar) : "memory");
-}
-
-__device__ __forceinline__ float exp2_fast(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
-template <int TYPE>
-__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
-  if constexpr (TYPE == QMM_BF16) {
-    const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
-    return *reinterpret_cast<const uint32_t*>(&v);
-  } else {
-    const __half2 v = __floats2half2_rn(lo, hi);
-    return *reinterpret_cast<const uint32_t*>(&v);
-  }
 }
 
 // Whether one of the two 16-bit values of w is an infinity or NaN (all exponent bits set).
@@ -286,27 +134,10 @@ __device__ __noinline__ bool wait_slowly(uint32_t bar, uint32_t parity, uint32_t
   return false;
 }
 
-template <bool FP4>
-constexpr int kThreads = (FP4 ? kFirstDequantWarp + kDequantWarps : kFirstDequantWarp) * 32;
-
-// Bulk copy global -> shared with the default L2 policy (a prefix's tiles are read by several CTAs).
-__device__ __forceinline__ void bulk_copy(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
-  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
-               :: "r"(dst), "l"(src), "r"(bytes), "r"(bar) : "memory");
-}
-
-// One product of two fp16 pairs.
-__device__ __forceinline__ uint32_t mul2(uint32_t a, uint32_t b) {
-  const __half2 r = __hmul2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b));
-  return *reinterpret_cast<const uint32_t*>(&r);
-}
-
-template <int D, int TYPE, bool FP4>
-__global__ void __launch_bounds__(kThreads<FP4>, 1) attn_kernel(const __grid_constant__ Params P) {
+template <int D, int TYPE>
+__global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant__ Params P) {
   extern __shared__ __align__(1024) uint8_t smem[];
-  using L = Smem<D, FP4>;
-  constexpr int kThreads = q4k::kThreads<FP4>;
-  constexpr int kProduct = FP4 ? QMM_F16 : TYPE;   // the type of the products' operands
+  using L = Smem<D>;
   constexpr uint32_t kS = L::kStages;
   const qmm_attn_args& a = P.a;
   Misc& M = *reinterpret_cast<Misc*>(smem + L::kMisc);
@@ -314,18 +145,15 @@ __global__ void __launch_bounds__(kThreads<FP4>, 1) attn_kernel(const __grid_con
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t bars = smem_addr(M.bars);
   auto bar = [&](int k) { return bars + 8u * k; };
-  const int G = a.Hq / a.Hk, block = 2 * P.tokens;
+  const int G = a.Hq / a.Hk;
 
   // ---- barriers, tensor memory, and this CTA's piece of the list of key tiles
-  constexpr int kMyBars = FP4 ? kBars : kBars16;
-  if (threadIdx.x < kMyBars) {
+  if (threadIdx.x < kBars) {
     const int k = threadIdx.x;
     const bool two = (k >= kBarEmptyK && k < kBarQFull) || (k >= kBarQEmpty && k < kBarS);
-    const bool by_warps = FP4 && (k < kBarEmptyK || k >= kBarPackEmpty);   // dequantised, and read by that
-    mbar_init(bar(k), by_warps ? kDequantWarps : two ? 2 : (k >= kBarFree && k < kBarO) ? kLaneWarps
-                      : k == kBarJoin ? 2 * kLaneWarps : 1);
+    mbar_init(bar(k), two ? 2 : (k >= kBarFree && k < kBarO) ? kLaneWarps : k == kBarJoin ? 2 * kLaneWarps : 1);
     fence_barrier_init();
-  } else if (threadIdx.x == kMyBars) {
+  } else if (threadIdx.x == kBars) {
     M.abort = 0;
     for (int k = 0; k < 8; ++k) M.odd[k] = 0;
   }
@@ -333,91 +161,14 @@ __global__ void __launch_bounds__(kThreads<FP4>, 1) attn_kernel(const __grid_con
     tc::tmem_alloc(smem_addr(&M.tmem), kTmemCols);
     tc::tmem_relinquish();
   }
-  if (!FP4 && threadIdx.x < 3)
+  if (threadIdx.x < 3)
     asm volatile("prefetch.tensormap [%0];" :: "l"(threadIdx.x == 0 ? &P.mapK : threadIdx.x == 1 ? &P.mapV : &P.mapQ)
                  : "memory");
   // Launched early (behind a launch that allows it), this grid reads what was written before it from
   // here on; the combine launch, which reads the lengths before its own wait, may start from here on.
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  {
-    // the page tables towards L2 while the pieces are worked out: one 128-byte line a thread
-    const int64_t line = ((int64_t)blockIdx.x * kThreads + threadIdx.x) * 32;
-    const int64_t n_pre = (a.prefix_len + a.page_size - 1) >> P.page_shift, n_own = a.B * a.pages_per_stream;
-    if (line < n_pre) asm volatile("prefetch.global.L2 [%0];" :: "l"(a.prefix_pages + line));
-    if (line < n_own) asm volatile("prefetch.global.L2 [%0];" :: "l"(a.pages + line));
-    constexpr int kPer = (QMM_ATTN_MAX_STREAMS + kThreads - 1) / kThreads;
-    Stream str[kPer];
-    int64_t mine[kPer], sum = 0;
-    bool wrong = false;
-    const int rows = a.B > 0 ? clampi(a.row_starts[a.B], 0, a.T) : 0;
-#pragma unroll
-    for (int q = 0; q < kPer; ++q) {
-      const int b = threadIdx.x * kPer + q;
-      mine[q] = 0;
-      if (b < a.B) {
-        bool bad;
-        str[q] = stream_of(a, b, &bad);
-        wrong |= bad;
-        for (int rb = 0; rb * block < str[q].m; ++rb)
-          mine[q] += (int64_t)a.Hk * units_of(tiles_of(keys_of(str[q], rb, block)));
-      }
-      sum += mine[q];
-    }
-    if (wrong && blockIdx.x == 0) atomicOr(&g_status, kErrIndex);
-    int64_t upto = sum;
-#pragma unroll
-    for (int off = 1; off < 32; off <<= 1) {
-      const int64_t v = __shfl_up_sync(0xffffffffu, upto, off);
-      if (lane >= off) upto += v;
-    }
-    if (lane == 31) M.scan[warp] = upto;
-    __syncthreads();
-    int64_t before = upto - sum, own = 0;
-#pragma unroll
-    for (int w = 0; w < kThreads / 32; ++w) {
-      if (w < warp) before += M.scan[w];
-      own += M.scan[w];
-    }
-    const int punits = units_of(tiles_of((int)a.prefix_len));
-    const int64_t prefix = (int64_t)((rows + block - 1) / block) * a.Hk * punits;
-    const int64_t W = prefix + own;
-    // equal pieces: no CTA has more than ceil(W / CTAs), whichever way the remainder falls
-    const int64_t per = W < (int64_t(1) << 31) ? (int64_t)(((uint32_t)W + gridDim.x - 1) / gridDim.x)
-                                               : (W + gridDim.x - 1) / gridDim.x;
-    const int64_t w0 = min(W, blockIdx.x * per), w1 = min(W, w0 + per);
-    const int64_t last = w1 - 1;   // its group is the first one the CTA works on
-    if (threadIdx.x == 0) {
-      M.w0 = w0;
-      M.w1 = w1;
-      M.per = per;
-      M.rows = rows;
-      if (w0 < w1 && last < prefix) {
-        const int64_t g = prefix < (int64_t(1) << 31) ? (int64_t)((uint32_t)last / (uint32_t)punits) : last / punits;
-        M.b = -1;
-        M.rb = (int)((uint32_t)g / (uint32_t)a.Hk);
-        M.h = (int)((uint32_t)g - (uint32_t)M.rb * (uint32_t)a.Hk);
-        M.unit = last - g * punits + 1;
-      }
-    }
-    before += prefix;
-#pragma unroll
-    for (int q = 0; q < kPer; ++q) {
-      const int b = threadIdx.x * kPer + q;
-      if (b < a.B && w0 < w1 && last >= before && last < before + mine[q]) {
-        int64_t at = last - before;
-        int rb = 0, h = 0, n = units_of(tiles_of(keys_of(str[q], 0, block)));
-        while (at >= (int64_t)a.Hk * n) { at -= (int64_t)a.Hk * n; n = units_of(tiles_of(keys_of(str[q], ++rb, block))); }
-        while (at >= n) { at -= n; ++h; }
-        M.s = str[q];
-        M.b = b;
-        M.rb = rb;
-        M.h = h;
-        M.unit = at + 1;
-      }
-      before += mine[q];
-    }
-  }
+  deal<kThreads, kTile, kLead>(P, M.piece, &g_status);
   tc::fence_before_sync();
   __syncthreads();
   tc::fence_after_sync();
@@ -432,233 +183,11 @@ __global__ void __launch_bounds__(kThreads<FP4>, 1) attn_kernel(const __grid_con
   };
   auto wait_w = [&](int k, uint32_t parity) -> bool { return __all_sync(0xffffffffu, wait(k, parity)); };
 
-  Walker walk;
-  walk.start(P, M);
+  Walker<kTile, kLead> walk;
+  walk.start(P, M.piece);
   Seg g;
-  // Segment by segment, the order in which keys and values are copied and dequantised: K0, K1, V0, K2, V1, ...
-  // tile(values, t) of each; false ends it.
-  [[maybe_unused]] auto in_order = [&](int n, auto&& tile) -> bool {
-    for (int u = 0; u <= n; ++u) {
-      if (u < n && !tile(std::false_type{}, u)) return false;
-      if (u > 0 && !tile(std::true_type{}, u - 1)) return false;
-    }
-    return true;
-  };
 
-  if (FP4 && warp == kLoadWarp) {
-    // ------------------------------------------------------------------ keys and values in 4 bits
-    // A tile is a run of codes and one of scales per page (or of 64 keys of a longer page): lane 2k copies the
-    // codes of run k, lane 2k + 1 its scales.  Pages behind the last key are not read.
-    const int per_run = min(a.page_size, kTile);
-    const int my_key = lane / 2 * per_run, my_bytes = lane % 2 ? D / 16 : D / 2;   // a slot
-    const uint32_t dst = lane % 2 ? kTile * (D / 2) + my_key * (D / 16) : my_key * (D / 2);
-    uint32_t filled = 0;
-    bool ok = true;
-    auto from = [&](const Seg& s, int tile) -> int64_t {   // offset of this lane's run in the caches, or -1
-      const int key = tile * kTile + my_key;
-      if (my_key >= kTile || key >= s.keys) return -1;
-      int page = s.pages[key >> P.page_shift];
-      if (page < 0 || page >= P.n_pages) {
-        atomicOr(&g_status, kErrIndex);
-        page = 0;   // (the rows that see it have unspecified values)
-      }
-      return kv4::run_at(page, s.h, a.Hk, a.page_size, D) + (lane % 2 ? a.page_size * (D / 2) : 0) +
-             (key & (a.page_size - 1)) * my_bytes;
-    };
-    auto copy = [&](const void* cache, int64_t at) -> bool {
-      const uint32_t st = filled % L::kPacks, use = filled / L::kPacks;
-      ok = ok && (use == 0 || wait_w(kBarPackEmpty + st, (use - 1) & 1));
-      if (!ok) return false;
-      const uint32_t runs = __popc(__ballot_sync(0xffffffffu, at >= 0)) / 2;
-      if (lane == 0) mbar_arrive_expect_tx(bar(kBarPackFull + st), runs * per_run * kv4::slot_bytes(D));
-      __syncwarp();
-      ++filled;
-      if (at >= 0)
-        bulk_copy(smem_addr(smem) + L::kPack + st * L::kPackBytes + dst, static_cast<const uint8_t*>(cache) + at,
-                  per_run * my_bytes, bar(kBarPackFull + st));
-      return true;
-    };
-    while (ok && walk.next(P, g)) {
-      const int n = g.j1 - g.j0;
-      // of the tile whose values come next, of the one whose keys come last, of the two behind it
-      int64_t v_at = -1, k_last = -1, k_at = from(g, g.j0), k_next = n > 1 ? from(g, g.j0 + 1) : -1;
-      in_order(n, [&](auto values, int t) {
-        if constexpr (decltype(values)::value) return copy(a.V_cache, t + 1 < n ? v_at : k_last);
-        v_at = k_last;   // (the values of a tile come behind the keys of the next, but for the last tile's)
-        k_last = k_at;
-        k_at = k_next;
-        k_next = t + 2 < n ? from(g, g.j0 + t + 2) : -1;
-        return copy(a.K_cache, k_last);
-      });
-    }
-    // no copy of this CTA is in flight when it ends
-    for (uint32_t k = filled > L::kPacks ? filled - L::kPacks : 0; k < filled; ++k)
-      mbar_wait(bar(kBarPackFull + k % L::kPacks), (k / L::kPacks) & 1, kWaitLimit);
-  } else if (FP4 && warp == kQWarp) {
-    // ------------------------------------------------------------------ query tiles in fp16
-    // A row of D/8 lanes.  A bf16 row is multiplied by the power of two that takes its largest value to
-    // [2^14, 2^15): exact for what is not 2^-31 of that; the softmax multiplies its scores by the inverse.
-    constexpr int kLanes = D / 8, kAtOnce = 32 / kLanes, kAhead = 4;
-    const float c = a.scale * P.k_scale * kLog2e;
-    float* factors = reinterpret_cast<float*>(smem + L::kFactors);
-    uint32_t pos = 0;
-    bool ok = true;
-    while (ok && walk.next(P, g)) {
-      const int n = g.rows > P.tokens ? 2 : 1;
-      for (int k = 0; ok && k < n; ++k, ++pos) {
-        const uint32_t st = pos & 1, use = pos >> 1;
-        ok = use == 0 || wait_w(kBarQEmpty + st, (use - 1) & 1);
-        if (!ok) break;
-        const int live = min(P.tokens, g.rows - k * P.tokens) * G;
-        uint8_t* tile = smem + L::kQ + st * L::kQBytes;
-        for (int r0 = 0; r0 < live; r0 += kAtOnce * kAhead) {
-          uint4 q[kAhead];
-#pragma unroll
-          for (int u = 0; u < kAhead; ++u) {
-            const int r = r0 + u * kAtOnce + lane / kLanes;
-            q[u] = make_uint4(0u, 0u, 0u, 0u);
-            if (r < live) {
-              const int tok = (int)((uint32_t)r / (uint32_t)G);
-              q[u] = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.Q) +
-                                                     (g.t0 + k * P.tokens + tok) * a.ldq +
-                                                     (int64_t)(g.h * G + r - tok * G) * D + 8 * (lane % kLanes));
-            }
-          }
-#pragma unroll
-          for (int u = 0; u < kAhead; ++u) {
-            const int r = r0 + u * kAtOnce + lane / kLanes;
-            uint32_t w[4] = {q[u].x, q[u].y, q[u].z, q[u].w};
-            int up = 127;   // exponent field of the row's power of two
-            if constexpr (TYPE == QMM_BF16) {
-              uint32_t top = 0;
-#pragma unroll
-              for (int e = 0; e < 4; ++e) top = max(top, max(w[e] & 0x7FFFu, w[e] >> 16 & 0x7FFFu));
-#pragma unroll
-              for (int off = kLanes / 2; off >= 1; off >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, off));
-              up = top == 0 || top >= 0x7F80u ? 127 : min(254, 268 - (int)(top >> 7));
-              const float f = __uint_as_float((uint32_t)up << 23);
-#pragma unroll
-              for (int e = 0; e < 4; ++e)
-                w[e] = pack2<QMM_F16>(__uint_as_float(w[e] << 16) * f, __uint_as_float(w[e] & 0xFFFF0000u) * f);
-            }
-            if (r < live) {
-              const int d = lane % kLanes;   // 16 bytes of the row
-              *reinterpret_cast<uint4*>(tile + (d / 8) * L::kQHalf + r * 128 + ((d % 8) ^ (r & 7)) * 16) =
-                  make_uint4(w[0], w[1], w[2], w[3]);
-              if (d == 0) factors[(pos % kFactorTiles) * kRows + r] = scalbnf(c, 127 - up);
-            }
-          }
-        }
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bar(kBarQFull + st));
-      }
-    }
-  } else if (FP4 && warp >= kFirstDequantWarp) {
-    // ------------------------------------------------------------------ 4 bits to fp16
-    // A thread takes a block of 16 values: a code times its scale is exact in fp16 (two and four
-    // significant bits).  Rows of values behind the last key are zeroed, and so are NaN blocks among the keys that
-    // only some rows of the block see (a draft's last keys); attn_combine_kernel adds those back.  A step is the
-    // keys of a tile and the values of the one before: one round of waits, loads, fence and arrivals for both (by
-    // themselves each took as long, and the four warps, one a scheduler, have nobody to cover for them).
-    constexpr int kBlocks = D / kv4::kBlock, kUnits = kTile * kBlocks / (32 * kDequantWarps);
-    const int me = (warp - kFirstDequantWarp) * 32 + lane;
-    uint32_t taken = 0, filled_k = 0, filled_v = 0, items = 0, segs = 0;
-    bool ok = true;
-    // (a phase that is over is the rule: the suspended wait costs 200 clocks even then)
-    auto soon = [&](int k, uint32_t parity) { if (!mbar_try(bar(k), parity)) ok = wait(k, parity) && ok; };
-    struct Units {
-      uint2 code[kUnits];
-      uint32_t scale[kUnits];
-    };
-    auto load = [&](uint32_t pack, Units& x) {
-      const uint8_t* src = smem + L::kPack + pack * L::kPackBytes;
-#pragma unroll
-      for (int u = 0; u < kUnits; ++u) {
-        const int unit = u * 32 * kDequantWarps + me;
-        x.code[u] = *reinterpret_cast<const uint2*>(src + unit * 8);
-        x.scale[u] = src[kTile * (D / 2) + unit];
-      }
-    };
-    auto store = [&](uint8_t* dst, const Units& x, auto&& drop) {   // drop(key of the tile, scale): zeros instead
-#pragma unroll
-      for (int u = 0; u < kUnits; ++u) {
-        const int unit = u * 32 * kDequantWarps + me, key = unit / kBlocks, b = unit % kBlocks;
-        const bool zero = drop(key, x.scale[u]);
-        const uint32_t s = zero ? 0u : e4m3x2_pair(x.scale[u] * 0x101u);
-        uint32_t lo[4], hi[4];
-        e2m1x8_pairs(x.code[u].x, lo);
-        e2m1x8_pairs(x.code[u].y, hi);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          lo[e] = mul2(lo[e], s);
-          hi[e] = mul2(hi[e], s);
-        }
-        uint8_t* row = dst + (b / 4) * L::kHalf + key * 128;
-        // (the halves of a key in turn: eight neighbouring threads write to eight different 16-byte columns)
-        const int c0 = 2 * (b % 4), turn = b / 4 & 1;
-        const uint4 first = turn ? make_uint4(hi[0], hi[1], hi[2], hi[3]) : make_uint4(lo[0], lo[1], lo[2], lo[3]);
-        const uint4 other = turn ? make_uint4(lo[0], lo[1], lo[2], lo[3]) : make_uint4(hi[0], hi[1], hi[2], hi[3]);
-        *reinterpret_cast<uint4*>(row + ((c0 + turn) ^ (key & 7)) * 16) = first;
-        *reinterpret_cast<uint4*>(row + ((c0 + 1 - turn) ^ (key & 7)) * 16) = other;
-      }
-    };
-    while (ok && walk.next(P, g)) {
-      const int n = g.j1 - g.j0;
-      const bool pair = g.rows > P.tokens;
-      const int clean_from = g.own ? clampi(g.first_keys, 0, g.keys) : g.keys;
-      ++segs;
-      for (int t = 0; ok && t <= n; ++t) {   // the keys of tile t, the values of tile t - 1
-        const bool keys = t < n, values = t > 0;
-        const uint32_t pk = taken % L::kPacks, pv = (taken + keys) % L::kPacks;
-        const uint32_t sk = filled_k % kS, sv = filled_v % kS;
-        if (keys) {
-          soon(kBarPackFull + pk, (taken / L::kPacks) & 1);
-          if (filled_k >= kS) soon(kBarEmptyK + sk, (filled_k / kS - 1) & 1);
-        }
-        if (values) {
-          soon(kBarPackFull + pv, ((taken + keys) / L::kPacks) & 1);
-          if (filled_v >= kS) soon(kBarEmptyV + sv, (filled_v / kS - 1) & 1);
-        }
-        ok = __all_sync(0xffffffffu, ok);
-        if (!ok) break;
-        Units k, v;
-        if (keys) load(pk, k);
-        if (values) load(pv, v);
-        if (keys) store(smem + L::kK + sk * L::kTileBytes, k, [](int, uint32_t) { return false; });
-        if (values) {
-          const int base = (g.j0 + t - 1) * kTile;
-          bool odd = false;
-          if (base + kTile <= clean_from) {
-            store(smem + L::kV + sv * L::kTileBytes, v, [](int, uint32_t) { return false; });
-          } else {
-            store(smem + L::kV + sv * L::kTileBytes, v, [&](int key, uint32_t scale) {
-              const bool behind = base + key >= g.keys, nan = (scale & 0x7Fu) == kv4::kScaleNaN && base + key >= clean_from;
-              odd |= nan && !behind;
-              return behind || nan;
-            });
-            if (odd) *reinterpret_cast<volatile uint32_t*>(&M.odd[segs & 7]) = segs;
-          }
-        }
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) {
-          if (keys) {
-            mbar_arrive(bar(kBarFullK + kS * (pair ? 2 : (items + t) & 1) + sk));
-            mbar_arrive(bar(kBarPackEmpty + pk));
-          }
-          if (values) {
-            mbar_arrive(bar(kBarFullV + kS * (pair ? 2 : (items + t - 1) & 1) + sv));
-            mbar_arrive(bar(kBarPackEmpty + pv));
-          }
-        }
-        taken += (keys ? 1 : 0) + (values ? 1 : 0);
-        filled_k += keys;
-        filled_v += values;
-      }
-      items += pair ? 2 * n : n;
-    }
-  } else if (warp == kLoadWarp) {
+  if (warp == kLoadWarp) {
     // ------------------------------------------------------------------ keys and values
     // A tile is one box per page (or 64 keys of a longer page) and half of 64 values; lane k copies
     // box k / halves of half k % halves.  Pages behind the last key are not read.
@@ -754,7 +283,7 @@ __global__ void __launch_bounds__(kThreads<FP4>, 1) attn_kernel(const __grid_con
     // products.  The scores of item j + 1 are issued ahead of the values of item j.  The empty barriers of keys and values count two arrivals, and the only user of a
     // tile makes both; those of query tiles count one of each lane.
     if (elect_one()) {
-      constexpr bool kBf16 = kProduct == QMM_BF16;
+      constexpr bool kBf16 = TYPE == QMM_BF16;
       constexpr uint32_t kIdS = tc::idesc_16_f32(128, kTile, kBf16, false);
       constexpr uint32_t kIdO = tc::idesc_16_f32(128, D, kBf16, true);
       const uint64_t dq = tc::smem_desc_sw128(smem_addr(smem + L::kQ), 16, 1024);
@@ -764,7 +293,7 @@ __global__ void __launch_bounds__(kThreads<FP4>, 1) attn_kernel(const __grid_con
       const uint32_t tS = tmem + kTile * l, tP = tmem + 2 * kTile + kTile * l, tO = tmem + 4 * kTile + kRows * l;
       const int barP = kBarP + 2 * l, barO = kBarO + 2 * l;
       struct Pass {
-        Walker w;
+        Walker<kTile, kLead> w;
         int left = 0;                  // the lane's items left of the segment
         bool pair = false, fresh = false;   // two row tiles; no item of the segment yet
         uint32_t users = 0;            // kS * users of the segment's tiles
@@ -867,11 +396,10 @@ __global__ void __launch_bounds__(kThreads<FP4>, 1) attn_kernel(const __grid_con
     const uint32_t lanes = (uint32_t)(warp % kLaneWarps) << 21;   // first TMEM lane << 16
     const uint32_t tS = tmem + lanes + kTile * l, tP = tmem + lanes + 2 * kTile + kTile * l;
     const uint32_t tO = tmem + lanes + 4 * kTile;
-    float c = a.scale * kLog2e;
+    const float c = a.scale * kLog2e;
     float2* stats = reinterpret_cast<float2*>(smem + L::kStats);
     uint32_t parity = 0;   // of the next phases of the value stages' full barriers (single, both)
     uint32_t pos = 0, seen = 0, joins = 0, segs = 0, items = 0, ends = 0;
-    [[maybe_unused]] uint32_t tiles_q = 0;   // query tiles before the segment's
     bool ok = true;
     while (ok && walk.next(P, g)) {
       const int n = g.j1 - g.j0;
@@ -897,14 +425,9 @@ __global__ void __launch_bounds__(kThreads<FP4>, 1) attn_kernel(const __grid_con
         const uint32_t at = pair ? kS + st : st;
         parity ^= 1u << at;
         ok = wait_w(kBarS + l, buf);   // (and with S the products of two items before, the last readers of this p)
-        if constexpr (FP4) {   // (the product that made S waited for the query tile, and its rows' factors with it)
-          if (ok && i == first)
-            c = row < live ? reinterpret_cast<const float*>(smem + L::kFactors)[((tiles_q + (pair ? l : 0)) % kFactorTiles) * kRows + row]
-                           : 0.0f;
-        }
         // value rows that a weight of 0 must not meet
         const int upto = min(g.keys, base + kTile) - base;
-        if (!FP4 && ok && clean_from < base + kTile && (upto < kTile || g.own)) {
+        if (ok && clean_from < base + kTile && (upto < kTile || g.own)) {
           ok = wait_w(kBarFullV + kS * (pair ? 2 : l) + st, !(parity >> at & 1));
           if (!ok) break;
           uint8_t* V = smem + L::kV + st * L::kTileBytes;
@@ -968,7 +491,7 @@ __global__ void __launch_bounds__(kThreads<FP4>, 1) attn_kernel(const __grid_con
             }
           }
           if (grew) top = now;
-          const float off = top == -INFINITY ? 0.0f : FP4 ? kLift - top : -top;
+          const float off = top == -INFINITY ? 0.0f : -top;
           const uint64_t cc = f2pack(c, c), oo = f2pack(off, off);
           uint64_t part0 = 0, part1 = 0;   // sums of weights, two fp32 each
 #pragma unroll
@@ -978,8 +501,8 @@ __global__ void __launch_bounds__(kThreads<FP4>, 1) attn_kernel(const __grid_con
             const float p0 = exp2_fast(x.x), p1 = exp2_fast(x.y), p2 = exp2_fast(y.x), p3 = exp2_fast(y.y);
             part0 = add2(part0, f2pack(p0, p1));
             part1 = add2(part1, f2pack(p2, p3));
-            s[k / 2] = pack2<kProduct>(p0, p1);
-            s[k / 2 + 1] = pack2<kProduct>(p2, p3);
+            s[k / 2] = pack2<TYPE>(p0, p1);
+            s[k / 2 + 1] = pack2<TYPE>(p2, p3);
           }
           tc::st_x32(tP + kTile / 2 * buf, s);
           const float2 u = f2unpack(part0), v = f2unpack(part1);
@@ -996,7 +519,6 @@ __global__ void __launch_bounds__(kThreads<FP4>, 1) attn_kernel(const __grid_con
         if (st >= kS) st -= kS;
       }
       pos += n;   // value tiles before the next segment's
-      tiles_q += pair ? 2 : 1;
       if (!ok) break;
 
       // ---- the segment's sums to the workspace
@@ -1018,7 +540,7 @@ __global__ void __launch_bounds__(kThreads<FP4>, 1) attn_kernel(const __grid_con
       };
       float* out = inside ? P.o_cta : P.o_rows;
       if (row < live && (pair || l == 0)) {
-        const uint32_t per = (uint32_t)min(M.per, (int64_t)0x7fffffff);
+        const uint32_t per = (uint32_t)min(M.piece.per, (int64_t)0x7fffffff);
         const uint32_t others = g.rest > 0 ? ((uint32_t)g.rest + per - 1) / per : 0;
         RowStat st{top, sum, odd, others << 16 | (blockIdx.x + 1)};
         if (!pair) {
@@ -1027,7 +549,6 @@ __global__ void __launch_bounds__(kThreads<FP4>, 1) attn_kernel(const __grid_con
           st.sum = (!(s0.x == -INFINITY && s0.y == 0.0f) ? s0.y * exp2_fast(s0.x - st.top) : 0.0f) +
                    (!(s1.x == -INFINITY && s1.y == 0.0f) ? s1.y * exp2_fast(s1.x - st.top) : 0.0f);
         }
-        if constexpr (FP4) st.top -= kLift;
         (inside ? P.s_cta : P.s_rows)[record(row)] = st;
       }
       // O: 16 rows x 32 columns at a time; the four threads of a row write 128 bytes of it.  A row's
@@ -1101,235 +622,6 @@ __global__ void __launch_bounds__(kThreads<FP4>, 1) attn_kernel(const __grid_con
 }
 
 // ------------------------------------------------------------------------------------------
-// Joins a row's segments: SHARE warps per (row, head).  The segments of a group are the one that begins
-// it (in the row's own record) and those of the CTAs whose piece begins inside it.
-constexpr int kCombineWarps = 8;
-
-// Column of the value at position p of a row's record: the epilogue keeps columns 8k + 2q, 8k + 2q + 1
-// (k = 0..3) of each 32 together, as the 8 values of thread q of four.
-__device__ __forceinline__ int column_of(int p) {
-  return (p & ~31) + 8 * ((p & 7) >> 1) + 2 * ((p & 31) >> 3) + (p & 1);
-}
-
-template <int D, int TYPE, int SHARE, bool FP4>
-__global__ void __launch_bounds__(32 * kCombineWarps) attn_combine_kernel(const __grid_constant__ Params P) {
-  constexpr int kV = D / 32;   // values of a lane: positions kV * lane and on
-  constexpr int kAhead = 8;    // records whose O a warp has in flight
-  const qmm_attn_args& a = P.a;
-  __shared__ int stream;
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  const int t = blockIdx.x, lane = threadIdx.x & 31;
-  const int head = (blockIdx.y * kCombineWarps + (threadIdx.x >> 5)) / SHARE, share = (threadIdx.x >> 5) % SHARE;
-  if (threadIdx.x == 0) stream = -1;
-  __syncthreads();
-  for (int b = threadIdx.x; b < a.B; b += blockDim.x) {
-    const Stream s = stream_of(a, b);
-    if (t >= s.t0 && t < s.t0 + s.m) stream = b;   // one stream, if the starts do not decrease
-  }
-  __syncthreads();
-  if (SHARE == 1 && head >= a.Hq) return;
-  const int b = head < a.Hq ? stream : -1, G = a.Hq / a.Hk, block = 2 * P.tokens;
-  Stream s{};
-  bool has[2] = {b >= 0 && a.prefix_len > 0 && t < a.row_starts[a.B], false};   // key tiles of the prefix, of own keys
-  if (b >= 0) {
-    s = stream_of(a, b);
-    has[1] = keys_of(s, (t - s.t0) / block, block) > 0;
-  }
-  const int64_t rec = (int64_t)t * a.Hq + head;
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-
-  auto load = [&](const float* p, float (&x)[kV]) {
-    if constexpr (kV == 4) {
-      const float4 v = *reinterpret_cast<const float4*>(p + 4 * lane);
-      x[0] = v.x; x[1] = v.y; x[2] = v.z; x[3] = v.w;
-    } else {
-      const float2 v = *reinterpret_cast<const float2*>(p + 2 * lane);
-      x[0] = v.x; x[1] = v.y;
-    }
-  };
-  // a row that saw none of a segment's keys has no part in it
-  auto saw = [](const RowStat& r) { return !(r.top == -INFINITY && r.sum == 0.0f); };
-  RowStat st[2] = {{-INFINITY, 0.0f, 0u, 0u}, {-INFINITY, 0.0f, 0u, 0u}};
-  float x[2][kV] = {};
-#pragma unroll
-  for (int k = 0; k < 2; ++k)
-    if (has[k]) {
-      const int64_t at = k ? (int64_t)a.T * a.Hq + rec : rec;
-      st[k] = P.s_rows[at];
-      if (share == 0) load(P.o_rows + at * D, x[k]);
-    }
-  float top = share == 0 ? fmaxf(st[0].top, st[1].top) : -INFINITY, sum = 0.0f, o[kV] = {};
-  uint32_t odd = st[0].odd | st[1].odd;
-#pragma unroll
-  for (int k = 0; k < 2; ++k)
-    if (share == 0 && saw(st[k])) {
-      const float w = exp2_fast(st[k].top - top);
-      sum = __fmaf_rn(st[k].sum, w, sum);
-#pragma unroll
-      for (int q = 0; q < kV; ++q) o[q] = __fmaf_rn(x[k][q], w, o[q]);
-    }
-  // the other segments of the two groups, one a lane
-  const int n0 = min((int)(st[0].rest >> 16), kMaxCtas), all = n0 + min((int)(st[1].rest >> 16), kMaxCtas);
-  const int part = (all + SHARE - 1) / SHARE, end = min(all, (share + 1) * part);   // this warp's of them
-  int row[2] = {0, 0};   // of the tiles of each group's block
-  if (all > 0) {
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      const int in = (k ? t - s.t0 : t) % block;
-      row[k] = (in < P.tokens ? in * G : kRows + (in - P.tokens) * G) + head % G;
-    }
-  }
-  constexpr int kFew = 3;
-  if (SHARE == 1 && all > 0 && all <= kFew) {   // few of them, as a rule where rows are many: one after the other
-    RowStat q[kFew];
-    float y[kFew][kV];
-#pragma unroll
-    for (int r = 0; r < kFew; ++r) {
-      q[r] = RowStat{-INFINITY, 0.0f, 0u, 0u};
-      if (r < all) {
-        const bool own = r >= n0;
-        const int cta = min((int)((own ? st[1].rest : st[0].rest) & 0xFFFFu) + (own ? r - n0 : r), kMaxCtas - 1);
-        const int at = cta * 2 * kRows + (own ? row[1] : row[0]);
-        q[r] = P.s_cta[at];
-        load(P.o_cta + (int64_t)at * D, y[r]);
-      }
-    }
-#pragma unroll
-    for (int r = 0; r < kFew; ++r) {
-      if (!saw(q[r])) continue;
-      const float best = fmaxf(top, q[r].top), f = exp2_fast(q[r].top - best);
-      const float keep = top == -INFINITY && sum == 0.0f ? 0.0f : exp2_fast(top - best);
-      sum = __fmaf_rn(sum, keep, q[r].sum * f);
-      top = best;
-      odd |= q[r].odd;
-#pragma unroll
-      for (int k = 0; k < kV; ++k) o[k] = __fmaf_rn(y[r][k], f, o[k] * keep);
-    }
-  } else if (share * part < end) {
-    for (int r0 = share * part; r0 < end; r0 += 32) {
-      const int r = r0 + lane;
-      const bool own = r >= n0, live = r < end;
-      const int cta = min((int)((own ? st[1].rest : st[0].rest) & 0xFFFFu) + (own ? r - n0 : r), kMaxCtas - 1);
-      const int at = cta * 2 * kRows + (own ? row[1] : row[0]);
-      RowStat q{-INFINITY, 0.0f, 0u, 0u};
-      if (live) q = P.s_cta[at];
-      // their O, some at a time, asked for before the statistics are there
-      float best = top, keep = 1.0f, w = 0.0f;
-#pragma unroll 1
-      for (int j0 = 0; j0 < 32 && r0 + j0 < end; j0 += kAhead) {
-        float y[kAhead][kV];
-#pragma unroll
-        for (int j = 0; j < kAhead; ++j) {
-          const int from = __shfl_sync(0xffffffffu, at, j0 + j);
-#pragma unroll
-          for (int k = 0; k < kV; ++k) y[j][k] = 0.0f;
-          if (r0 + j0 + j < end) load(P.o_cta + (int64_t)from * D, y[j]);
-        }
-        if (j0 == 0) {
-          best = q.top;
-#pragma unroll
-          for (int off = 16; off >= 1; off >>= 1) best = fmaxf(best, __shfl_xor_sync(0xffffffffu, best, off));
-          best = fmaxf(best, top);
-          w = saw(q) ? exp2_fast(q.top - best) : 0.0f;
-          float part = saw(q) ? q.sum * w : 0.0f;
-#pragma unroll
-          for (int off = 16; off >= 1; off >>= 1) part += __shfl_xor_sync(0xffffffffu, part, off);
-          keep = top == -INFINITY && sum == 0.0f ? 0.0f : exp2_fast(top - best);
-          sum = __fmaf_rn(sum, keep, part);
-          top = best;
-          odd |= __any_sync(0xffffffffu, q.odd != 0);
-#pragma unroll
-          for (int k = 0; k < kV; ++k) o[k] *= keep;
-        }
-#pragma unroll
-        for (int j = 0; j < kAhead; ++j) {
-          const float f = __shfl_sync(0xffffffffu, w, j0 + j);
-          if (f != 0.0f)   // (of a segment none of whose keys the row saw, O means nothing)
-#pragma unroll
-            for (int k = 0; k < kV; ++k) o[k] = __fmaf_rn(y[j][k], f, o[k]);
-        }
-      }
-    }
-  }
-  if constexpr (SHARE > 1) {   // the warps of a row, joined by the first
-    __shared__ float o_s[kCombineWarps][D];
-    __shared__ float4 stat_s[kCombineWarps];
-    const int w0 = threadIdx.x >> 5;
-#pragma unroll
-    for (int k = 0; k < kV; ++k) o_s[w0][kV * lane + k] = o[k];
-    if (lane == 0) stat_s[w0] = make_float4(top, sum, __uint_as_float(odd), 0.0f);
-    __syncthreads();
-    if (share != 0 || head >= a.Hq) return;
-    float best = top;
-#pragma unroll
-    for (int w = 1; w < SHARE; ++w) best = fmaxf(best, stat_s[w0 + w].x);
-    const float keep = top == -INFINITY && sum == 0.0f ? 0.0f : exp2_fast(top - best);
-    sum *= keep;
-#pragma unroll
-    for (int k = 0; k < kV; ++k) o[k] *= keep;
-#pragma unroll
-    for (int w = 1; w < SHARE; ++w) {
-      const float4 q = stat_s[w0 + w];
-      odd |= __float_as_uint(q.z);
-      if (q.x == -INFINITY && q.y == 0.0f) continue;
-      const float f = exp2_fast(q.x - best);
-      sum = __fmaf_rn(q.y, f, sum);
-#pragma unroll
-      for (int k = 0; k < kV; ++k) o[k] = __fmaf_rn(o_s[w0 + w][kV * lane + k], f, o[k]);
-    }
-    top = best;
-  }
-  const float inv = sum == 0.0f ? 0.0f : (FP4 ? P.v_scale : 1.0f) / sum;
-#pragma unroll
-  for (int k = 0; k < kV; ++k) o[k] = sum == 0.0f ? 0.0f : o[k] * inv;
-  if (odd) {
-    // infinities and NaN among the keys that only some rows of the block see: their sum
-    float extra[kV] = {};
-    const int sees = clampi(s.len - s.m + t - s.t0 + 1, 0, s.len);
-    for (int j = max(0, s.len - s.m); j < sees; ++j) {
-      const int page = a.pages[b * a.pages_per_stream + j / a.page_size];
-      if (page < 0 || page >= a.n_slots / a.page_size) continue;
-      if constexpr (FP4) {
-        const uint8_t* scales = static_cast<const uint8_t*>(a.V_cache) + kv4::run_at(page, head / G, a.Hk, a.page_size, D) +
-                                a.page_size * (D / 2) + (j % a.page_size) * (D / 16);
-#pragma unroll
-        for (int k = 0; k < kV; ++k)
-          if ((scales[column_of(kV * lane + k) / kv4::kBlock] & 0x7Fu) == kv4::kScaleNaN) extra[k] = NAN;
-        continue;
-      }
-      const int64_t at = (((int64_t)page * a.page_size + j % a.page_size) * a.Hk + head / G) * D;
-#pragma unroll
-      for (int k = 0; k < kV; ++k) {
-        const uint16_t raw = static_cast<const uint16_t*>(a.V_cache)[at + column_of(kV * lane + k)];
-        const float v = TYPE == QMM_BF16 ? __uint_as_float((uint32_t)raw << 16) : __half2float(__ushort_as_half(raw));
-        if (!(fabsf(v) < INFINITY)) extra[k] += v;
-      }
-    }
-#pragma unroll
-    for (int k = 0; k < kV; ++k) o[k] += extra[k];
-  }
-  uint16_t* out = static_cast<uint16_t*>(a.O) + (int64_t)t * a.ldo + (int64_t)head * D;
-#pragma unroll
-  for (int k = 0; k < kV; k += 2)
-    *reinterpret_cast<uint32_t*>(out + column_of(kV * lane + k)) = pack2<TYPE>(o[k], o[k + 1]);
-  if (a.lse && lane == 0) a.lse[(int64_t)t * a.Hq + head] = sum == 0.0f ? -INFINITY : __fmaf_rn(top, kLn2, logf(sum));
-}
-
-// ------------------------------------------------------------------------------------------
-
-size_t up(size_t n) { return (n + 255) & ~(size_t)255; }
-
-struct Space {
-  size_t o_rows, s_rows, o_cta, s_cta, total;
-  explicit Space(const qmm_attn_args& a) {
-    const size_t rows = 2 * (size_t)a.T * a.Hq, cta = (size_t)kMaxCtas * 2 * kRows;
-    o_rows = 0;
-    o_cta = o_rows + up(rows * a.D * sizeof(float));
-    s_rows = o_cta + up(cta * a.D * sizeof(float));
-    s_cta = s_rows + up(rows * sizeof(RowStat));
-    total = s_cta + up(cta * sizeof(RowStat)) + 256;   // the base may be 16-byte aligned only
-  }
-};
 
 // A T x H x D (or slots x H x D) tensor of 16-bit values with `ld` values between its outer rows; boxes
 // of 64 values, `heads` heads and `rows` rows, 128-byte swizzle.
@@ -1345,41 +637,28 @@ bool tensor_map(CUtensorMap* m, const void* p, int D, int H, int64_t n, int64_t 
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int D, int TYPE, bool FP4>
+template <int D, int TYPE>
 cudaError_t set_smem_attr() {
   static DeviceOnce once;
   int dev = 0;
   const cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   return once.run(dev, cudaSuccess, [] {
-    return cudaFuncSetAttribute(attn_kernel<D, TYPE, FP4>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                Smem<D, FP4>::kTotal);
+    return cudaFuncSetAttribute(attn_kernel<D, TYPE>, cudaFuncAttributeMaxDynamicSharedMemorySize, Smem<D>::kTotal);
   });
 }
 
-template <int D, int TYPE, bool FP4>
-cudaError_t launch(const qmm_attn_args& a, float k_scale, float v_scale, void* workspace, cudaStream_t stream) {
+template <int D, int TYPE>
+cudaError_t launch(const qmm_attn_args& a, void* workspace, cudaStream_t stream) {
   const int G = a.Hq / a.Hk;
   Params P;
-  P.a = a;
-  P.k_scale = k_scale;
-  P.v_scale = v_scale;
-  P.tokens = kRows / G;
-  P.n_pages = (int)(a.n_slots / a.page_size);
-  P.page_shift = 31 - __builtin_clz((unsigned)a.page_size);
-  const Space sp(a);
-  uint8_t* ws = reinterpret_cast<uint8_t*>(up(reinterpret_cast<uintptr_t>(workspace)));
-  P.o_rows = reinterpret_cast<float*>(ws + sp.o_rows);
-  P.o_cta = reinterpret_cast<float*>(ws + sp.o_cta);
-  P.s_rows = reinterpret_cast<RowStat*>(ws + sp.s_rows);
-  P.s_cta = reinterpret_cast<RowStat*>(ws + sp.s_cta);
-  get_wait_limit(&P.wait_polls, &P.wait_ns);
+  fill(P, a, kRows / G, 2 * (kRows / G), workspace);
   const int per_box = a.page_size < kTile ? a.page_size : kTile;
-  if (!FP4 && (!tensor_map(&P.mapQ, a.Q, D, a.Hq, a.T, a.ldq, G, P.tokens, TYPE) ||
+  if (!tensor_map(&P.mapQ, a.Q, D, a.Hq, a.T, a.ldq, G, P.tokens, TYPE) ||
       !tensor_map(&P.mapK, a.K_cache, D, a.Hk, a.n_slots, (int64_t)a.Hk * D, 1, per_box, TYPE) ||
-      !tensor_map(&P.mapV, a.V_cache, D, a.Hk, a.n_slots, (int64_t)a.Hk * D, 1, per_box, TYPE)))
+      !tensor_map(&P.mapV, a.V_cache, D, a.Hk, a.n_slots, (int64_t)a.Hk * D, 1, per_box, TYPE))
     return cudaErrorInvalidValue;
-  cudaError_t e = set_smem_attr<D, TYPE, FP4>();
+  cudaError_t e = set_smem_attr<D, TYPE>();
   if (e != cudaSuccess) return e;
   const int sms = sm_count();
   if (sms < 1) return cudaErrorNoDevice;
@@ -1387,37 +666,17 @@ cudaError_t launch(const qmm_attn_args& a, float k_scale, float v_scale, void* w
   // each waits for it before it reads or writes memory.
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(sms < kMaxCtas ? sms : kMaxCtas);
-  cfg.blockDim = dim3(kThreads<FP4>);
-  cfg.dynamicSmemBytes = Smem<D, FP4>::kTotal;
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = Smem<D>::kTotal;
   cfg.stream = stream;
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, attn_kernel<D, TYPE, FP4>, P);
+  e = cudaLaunchKernelEx(&cfg, attn_kernel<D, TYPE>, P);
   if (e != cudaSuccess) return e;
-  cfg.gridDim = dim3(a.T, (a.Hq + kCombineWarps - 1) / kCombineWarps);
-  cfg.blockDim = dim3(32 * kCombineWarps);
-  cfg.dynamicSmemBytes = 0;
-  // Four warps share a row's records where all of their CTAs, three an SM, run at once; with more rows, one
-  // warp a row.  The limit shows at any number of records.  Behind 32768 shared keys, some 19 records a row:
-  // 800 rows 35.7 us (one warp a row 37.5), 960 rows 38.4 (37.8), 1280 rows 44.5 (43.7).  Behind 8192: 800 rows
-  // 26.8 (27.0), 960 rows 31.4 (29.0).  640 rows of 8 streams' own 3000 to 6000 keys 15.0 (17.4).
-  if ((int64_t)a.T * a.Hq * 4 <= 3 * kCombineWarps * (int64_t)sms) {
-    cfg.gridDim.y = (a.Hq * 4 + kCombineWarps - 1) / kCombineWarps;
-    return cudaLaunchKernelEx(&cfg, attn_combine_kernel<D, TYPE, 4, FP4>, P);
-  }
-  return cudaLaunchKernelEx(&cfg, attn_combine_kernel<D, TYPE, 1, FP4>, P);
-}
-
-template <bool FP4>
-cudaError_t launch_any(const qmm_attn_args& a, float k_scale, float v_scale, void* workspace, cudaStream_t stream) {
-  if (a.D == 64)
-    return a.type == QMM_BF16 ? launch<64, QMM_BF16, FP4>(a, k_scale, v_scale, workspace, stream)
-                              : launch<64, QMM_F16, FP4>(a, k_scale, v_scale, workspace, stream);
-  return a.type == QMM_BF16 ? launch<128, QMM_BF16, FP4>(a, k_scale, v_scale, workspace, stream)
-                            : launch<128, QMM_F16, FP4>(a, k_scale, v_scale, workspace, stream);
+  return launch_combine<D, TYPE, false>(P, sms, stream);
 }
 
 }  // namespace
@@ -1425,13 +684,9 @@ cudaError_t launch_any(const qmm_attn_args& a, float k_scale, float v_scale, voi
 size_t attn_workspace_bytes(const qmm_attn_args& a) { return Space(a).total; }
 
 cudaError_t launch_attn(const qmm_attn_args& a, void* workspace, cudaStream_t stream) {
-  return launch_any<false>(a, 1.0f, 1.0f, workspace, stream);
-}
-
-size_t attn_fp4_workspace_bytes(const qmm_attn_fp4_args& a) { return Space(a.base).total; }
-
-cudaError_t launch_attn_fp4(const qmm_attn_fp4_args& a, void* workspace, cudaStream_t stream) {
-  return launch_any<true>(a.base, a.k_scale, a.v_scale, workspace, stream);
+  if (a.D == 64)
+    return a.type == QMM_BF16 ? launch<64, QMM_BF16>(a, workspace, stream) : launch<64, QMM_F16>(a, workspace, stream);
+  return a.type == QMM_BF16 ? launch<128, QMM_BF16>(a, workspace, stream) : launch<128, QMM_F16>(a, workspace, stream);
 }
 
 cudaError_t read_and_clear_attn_status(unsigned* out) {
