@@ -102,6 +102,7 @@ cudaError_t launch_kv_fp4_read(const qmm_kv_fp4_read_args& a, cudaStream_t strea
 cudaError_t read_and_clear_kv_fp4_status(unsigned* out);
 cudaError_t launch_attn_fp4(const qmm_attn_fp4_args& a, void* workspace, cudaStream_t stream);
 size_t attn_fp4_workspace_bytes(const qmm_attn_fp4_args& a);
+cudaError_t read_and_clear_attn_fp4_status(unsigned* out);
 cudaError_t launch_lora(const qmm_lora_entry* entries, int count, const int32_t* ids, int M, int rank_max,
                         void* workspace, cudaStream_t stream);
 size_t lora_workspace_bytes(const qmm_lora_entry* entries, int count, int M, int rank_max);

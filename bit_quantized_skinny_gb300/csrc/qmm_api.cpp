@@ -601,7 +601,7 @@ size_t qmm_workspace_bytes_held(void) { return q4k::workspace_bytes_held(); }
 
 qmm_status qmm_device_status(unsigned* status_out) {
   if (!status_out) return QMM_ERR_NULL;
-  unsigned a = 0, b = 0, c = 0, d = 0, f = 0, g = 0, h = 0, i = 0;
+  unsigned a = 0, b = 0, c = 0, d = 0, f = 0, g = 0, h = 0, i = 0, j = 0;
   cudaError_t e = q4k::read_and_clear_fma_status(&a);
   if (e == cudaSuccess) e = q4k::read_and_clear_tc_status(&b);
   if (e == cudaSuccess) e = q4k::read_and_clear_pack_status(&c);
@@ -609,8 +609,9 @@ qmm_status qmm_device_status(unsigned* status_out) {
   if (e == cudaSuccess) e = q4k::read_and_clear_attn_status(&f);
   if (e == cudaSuccess) e = q4k::read_and_clear_lora_status(&g);
   if (e == cudaSuccess) e = q4k::read_and_clear_kv_fp4_status(&h);
-  if (e == cudaSuccess) e = q4k::read_and_clear_sample_status(&i);
-  *status_out = a | b | c | d | f | g | h | i;
+  if (e == cudaSuccess) e = q4k::read_and_clear_attn_fp4_status(&i);
+  if (e == cudaSuccess) e = q4k::read_and_clear_sample_status(&j);
+  *status_out = a | b | c | d | f | g | h | i | j;
   return e == cudaSuccess ? QMM_OK : cuda_fail(e);
 }
 

@@ -1,0 +1,703 @@
+// qmm_attn_fp4.cu — attention of several streams' rows over a prefix that they share and over each
+// stream's own keys, in pages of a 4-bit cache (qmm_attn_shared_fp4).
+//
+// Work: equal pieces of the list of all key tiles, joined by a second launch (q4k_attn_parts.cuh).  A block is N / G
+// tokens (at most N rows), a key tile 128 keys.
+//
+// A key is 72 bytes, and what an SM does for it is mostly to turn these into fp16 (a code times its scale
+// is exact there).  So everything is laid out by the keys, with the rows as the narrow side of both products:
+//     S^T = K Q^T        tcgen05, K (128 keys x D) from tensor memory, where four warps put it, a thread a key
+//     p = 2^(c S + off)  a thread per key, S^T from tensor memory, c = scale k_scale log2 e over the row's power of two
+//     O^T += V^T p^T     tcgen05, V (MN-major) and p^T from shared memory; four more warps write V
+// so few rows cost little, the exponentials of a row are spread over 128 threads, and no 128-row tile of queries
+// is read again for every tile.
+// off moves, and O^T is rescaled, only when a row's maximum grew by more than 8; weights are then at most 2^15, and
+// fp16 holds those down to 2^-21 of the largest at full precision.
+//
+// Keys that a row may not see are set to -inf by position, so their K may hold anything.  Value rows behind the last key
+// are zeroed, and so are NaN blocks among the keys that only some rows of the block see (a draft's last keys);
+// attn_combine_kernel adds those back, from the cache, to the rows that see them.
+#include <cstdint>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include "q4k_attn_parts.cuh"
+#include "q4k_device.cuh"
+#include "q4k_device_once.h"
+#include "q4k_formats.cuh"
+#include "q4k_internal.h"
+#include "q4k_kv_fp4.cuh"
+#include "q4k_tcgen05.cuh"
+
+namespace q4k {
+namespace {
+
+__device__ unsigned g_status;   // this file's kernels' status word
+
+constexpr int kTile = 128;           // keys of a key tile
+constexpr int kLead = 3;             // units of a group besides its key tiles
+constexpr int kN = 64;               // rows of a block
+constexpr int kChunk = 32;           // rows that a softmax thread has in registers at a time
+// warps: 0-3 softmax, 4 copies, 5 tensor cores, 6 queries, 8-11 keys, 12-15 values to fp16
+constexpr int kLoadWarp = 4, kMmaWarp = 5, kQWarp = 6, kKeyWarp = 8, kValueWarp = 12;
+constexpr int kThreads = 16 * 32, kGroupWarps = 4;
+constexpr uint32_t kTmemCols = 512;
+constexpr int kKeyBufs = 4;          // tiles of keys in tensor memory
+constexpr int kPacks = 10;           // packed tiles in shared memory: of keys and of values in turn
+constexpr int kFactorTiles = 8;      // (the softmax is a few query tiles behind)
+constexpr float kGrow = 8.0f;
+constexpr float kLift = 7.0f;        // log2 of the largest weight when off is set
+constexpr uint32_t kWaitLimit = 1u << 17;
+constexpr float kLog2e = 1.44269504088896340736f;
+
+template <int D>
+struct Smem {
+  static constexpr int kPackBytes = kTile * kv4::slot_bytes(D);
+  static constexpr int kVHalf = kTile * 128;             // 128 keys of 64 values
+  static constexpr int kVBytes = kTile * D * 2;
+  static constexpr int kValueBufs = D == 128 ? 2 : 3;
+  static constexpr int kQHalf = kN * 128;                // 64 values of N rows
+  static constexpr int kQBytes = kN * D * 2;
+  static constexpr int kPHalf = kN * 128;                // 64 keys of N rows
+  static constexpr int kPBytes = kN * kTile * 2;
+  static constexpr int kV = 0;
+  static constexpr int kQ = kV + kValueBufs * kVBytes;
+  static constexpr int kP = kQ + 2 * kQBytes;
+  static constexpr int kPack = kP + 2 * kPBytes;
+  static constexpr int kFactors = kPack + kPacks * kPackBytes;   // of the rows of the last kFactorTiles query tiles
+  static constexpr int kOff = kFactors + kFactorTiles * kN * 4;  // each softmax warp's copy of the rows' off
+  static constexpr int kRed = kOff + kGroupWarps * kN * 4;       // the softmax warps' maxima or sums of the rows
+  static constexpr int kMisc = kRed + kGroupWarps * kN * 4;
+  static constexpr int kTotal = kMisc + 1024;
+};
+static_assert(Smem<128>::kTotal <= 227 * 1024 && Smem<64>::kTotal <= 227 * 1024, "shared memory");
+
+// Tensor memory: K at 0, S^T behind it (two of them), then O^T.
+template <int D>
+struct Tmem {
+  static constexpr uint32_t kS = kKeyBufs * D / 2, kO = kS + 2 * kN;
+  static_assert(kO + kN <= kTmemCols, "tensor memory");
+};
+
+// Barriers; a wait tells a phase from the one after it only, and every wait here is for the phase of a tile (or a segment)
+// of whose successor on the same barrier the waiting role itself is a condition.
+enum : int {
+  kBarPackFull = 0, kBarPackEmpty = 10, kBarKeyFull = 20, kBarKeyEmpty = 24, kBarValueFull = 28, kBarValueEmpty = 31,
+  kBarS = 34, kBarSFree = 36, kBarP = 38, kBarO = 40 /* products of a tile's values are done */, kBarQFull = 42,
+  kBarQEmpty = 44, kBarOFree = 46, kBarDrain = 47, kBars = 48
+};
+
+struct Misc {
+  uint64_t bars[kBars];
+  Piece piece;
+  uint32_t tmem;
+  int abort;
+  uint32_t odd[8];    // [s % 8]: s, if values were taken out in segment s
+};
+static_assert(sizeof(Misc) <= 1024, "misc");
+
+__device__ __forceinline__ void bulk_copy(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
+               :: "r"(dst), "l"(src), "r"(bytes), "r"(bar) : "memory");
+}
+
+// One product of two fp16 pairs.
+__device__ __forceinline__ uint32_t mul2(uint32_t a, uint32_t b) {
+  const __half2 r = __hmul2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b));
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+
+// Four chained MMAs with both operands in shared memory, their descriptors' steps apart (in 16-byte units).
+__device__ __forceinline__ void mma_ss_x4(uint32_t d_taddr, uint64_t a, uint64_t a_step, uint64_t b, uint64_t b_step,
+                                          uint32_t idesc, uint32_t accumulate_first) {
+  asm volatile(
+      "{\n .reg .pred p0, p1;\n setp.ne.b32 p0, %4, 0;\n setp.eq.b32 p1, %4, %4;\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p0;\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], %5, %6, %3, p1;\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], %7, %8, %3, p1;\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], %9, %10, %3, p1;\n}"
+      :: "r"(d_taddr), "l"(a), "l"(b), "r"(idesc), "r"(accumulate_first), "l"(a + a_step), "l"(b + b_step),
+         "l"(a + 2 * a_step), "l"(b + 2 * b_step), "l"(a + 3 * a_step), "l"(b + 3 * b_step)
+      : "memory");
+}
+
+// The softmax warps meet: whether any of their threads says so.
+__device__ __forceinline__ bool any_of_softmax(bool mine) {
+  uint32_t any;
+  asm volatile("{\n .reg .pred p, q;\n setp.ne.b32 p, %1, 0;\n barrier.cta.red.or.pred q, 1, 128, p;\n selp.u32 %0, 1, 0, q;\n}"
+               : "=r"(any) : "r"((uint32_t)mine) : "memory");
+  return any != 0;
+}
+
+// The wait for a phase that has not completed yet (out of line: the roles' loops stay short).
+__device__ __noinline__ bool wait_slowly(uint32_t bar, uint32_t parity, uint32_t polls, uint32_t ns,
+                                         volatile int* abort_flag) {
+  if (*abort_flag) return false;
+  if (mbar_wait(bar, parity, polls, ns)) return true;
+  atomicOr(&g_status, kErrWaitTimeout);
+  *abort_flag = 1;
+  return false;
+}
+
+// fp16 pairs of a block's eight bytes of codes and its scale (both halves).
+__device__ __forceinline__ void to_half(uint2 code, uint32_t s, uint32_t (&h)[8]) {
+  uint32_t lo[4], hi[4];
+  e2m1x8_pairs(code.x, lo);
+  e2m1x8_pairs(code.y, hi);
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    h[e] = mul2(lo[e], s);
+    h[4 + e] = mul2(hi[e], s);
+  }
+}
+
+template <int D, int TYPE>
+__global__ void __launch_bounds__(kThreads, 1) attn_fp4_kernel(const __grid_constant__ Common P) {
+  extern __shared__ __align__(1024) uint8_t smem[];
+  using L = Smem<D>;
+  using T = Tmem<D>;
+  constexpr uint32_t kVB = L::kValueBufs;
+  const qmm_attn_args& a = P.a;
+  Misc& M = *reinterpret_cast<Misc*>(smem + L::kMisc);
+  volatile int* abort_flag = &M.abort;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t bars = smem_addr(M.bars);
+  auto bar = [&](int k) { return bars + 8u * k; };
+  const int G = a.Hq / a.Hk;
+
+  // ---- barriers, tensor memory, and this CTA's piece of the list of key tiles
+  if (threadIdx.x < kBars) {
+    const int k = threadIdx.x;
+    const bool warps = (k >= kBarPackEmpty && k < kBarKeyEmpty) || (k >= kBarValueFull && k < kBarValueEmpty) ||
+                       (k >= kBarSFree && k < kBarO) || k == kBarOFree;
+    mbar_init(bar(k), warps ? kGroupWarps : 1);
+    fence_barrier_init();
+  } else if (threadIdx.x == kBars) {
+    M.abort = 0;
+    for (int k = 0; k < 8; ++k) M.odd[k] = 0;
+  }
+  if (warp == kMmaWarp) {
+    tc::tmem_alloc(smem_addr(&M.tmem), kTmemCols);
+    tc::tmem_relinquish();
+  }
+  // Launched early (behind a launch that allows it), this grid reads what was written before it from
+  // here on; the combine launch, which reads the lengths before its own wait, may start from here on.
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  deal<kThreads, kTile, kLead>(P, M.piece, &g_status);
+  tc::fence_before_sync();
+  __syncthreads();
+  tc::fence_after_sync();
+  const uint32_t tmem = M.tmem;
+
+  // A bounded wait for a phase of a barrier; false: this wait, or another one, gave up.  (A phase that is over is the
+  // rule, and a suspended wait takes 200 clocks to see it.)
+  auto wait = [&](int k, uint32_t parity) -> bool {
+    if (mbar_try(bar(k), parity)) return true;
+    if (mbar_wait(bar(k), parity, 1, P.wait_ns ? P.wait_ns : kSuspendNs)) return true;
+    return wait_slowly(bar(k), parity, P.wait_polls ? P.wait_polls : kWaitLimit, P.wait_ns ? P.wait_ns : kSuspendNs,
+                       abort_flag);
+  };
+  auto wait_w = [&](int k, uint32_t parity) -> bool { return __all_sync(0xffffffffu, wait(k, parity)); };
+
+  Walker<kTile, kLead> walk;
+  walk.start(P, M.piece);
+  Seg g;
+
+  if (warp == kLoadWarp) {
+    // ------------------------------------------------------------------ packed tiles
+    // A tile is a run of codes and one of scales per page (or of 128 keys of a longer page): lane 2k copies the
+    // codes of run k, lane 2k + 1 its scales.  Pages behind the last key are not read.
+    const int per_run = min(a.page_size, kTile);
+    const int my_key = lane / 2 * per_run, my_bytes = lane % 2 ? D / 16 : D / 2;   // a slot
+    const uint32_t dst = lane % 2 ? kTile * (D / 2) + my_key * (D / 16) : my_key * (D / 2);
+    uint32_t filled = 0;
+    bool ok = true;
+    auto from = [&](const Seg& s, int tile) -> int64_t {   // offset of this lane's run in the caches, or -1
+      const int key = tile * kTile + my_key;
+      if (my_key >= kTile || key >= s.keys) return -1;
+      int page = s.pages[key >> P.page_shift];
+      if (page < 0 || page >= P.n_pages) {
+        atomicOr(&g_status, kErrIndex);
+        page = 0;   // (the rows that see it have unspecified values)
+      }
+      return kv4::run_at(page, s.h, a.Hk, a.page_size, D) + (lane % 2 ? a.page_size * (D / 2) : 0) +
+             (key & (a.page_size - 1)) * my_bytes;
+    };
+    auto copy = [&](const void* cache, int64_t at) {
+      const uint32_t st = filled % kPacks, use = filled / kPacks;
+      ok = ok && (use == 0 || wait_w(kBarPackEmpty + st, (use - 1) & 1));
+      if (!ok) return;
+      const uint32_t runs = __popc(__ballot_sync(0xffffffffu, at >= 0)) / 2;
+      if (lane == 0) mbar_arrive_expect_tx(bar(kBarPackFull + st), runs * per_run * kv4::slot_bytes(D));
+      __syncwarp();
+      ++filled;
+      if (at >= 0)
+        bulk_copy(smem_addr(smem) + L::kPack + st * L::kPackBytes + dst, static_cast<const uint8_t*>(cache) + at,
+                  per_run * my_bytes, bar(kBarPackFull + st));
+    };
+    while (ok && walk.next(P, g)) {
+      int64_t at = from(g, g.j0), next = g.j0 + 1 < g.j1 ? from(g, g.j0 + 1) : -1;
+      for (int j = g.j0; ok && j < g.j1; ++j) {
+        const int64_t later = j + 2 < g.j1 ? from(g, j + 2) : -1;
+        copy(a.K_cache, at);
+        copy(a.V_cache, at);
+        at = next;
+        next = later;
+      }
+    }
+    // no copy of this CTA is in flight when it ends
+    for (uint32_t k = filled > kPacks ? filled - kPacks : 0; k < filled; ++k)
+      mbar_wait(bar(kBarPackFull + k % kPacks), (k / kPacks) & 1, kWaitLimit);
+  } else if (warp == kQWarp) {
+    // ------------------------------------------------------------------ query tiles in fp16
+    // A row of D/8 lanes.  A bf16 row is multiplied by the power of two that takes its largest value to
+    // [2^14, 2^15): exact for what is not 2^-31 of that; the softmax multiplies its scores by the inverse.
+    constexpr int kLanes = D / 8, kAtOnce = 32 / kLanes, kAhead = 4;
+    const float c = a.scale * P.k_scale * kLog2e;
+    float* factors = reinterpret_cast<float*>(smem + L::kFactors);
+    uint32_t pos = 0;
+    bool ok = true;
+    for (; ok && walk.next(P, g); ++pos) {
+      const uint32_t st = pos & 1, use = pos >> 1;
+      ok = use == 0 || wait_w(kBarQEmpty + st, (use - 1) & 1);
+      if (!ok) break;
+      const int live = g.rows * G;
+      uint8_t* tile = smem + L::kQ + st * L::kQBytes;
+      for (int r0 = 0; r0 < live; r0 += kAtOnce * kAhead) {
+        uint4 q[kAhead];
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u) {
+          const int r = r0 + u * kAtOnce + lane / kLanes;
+          q[u] = make_uint4(0u, 0u, 0u, 0u);
+          if (r < live) {
+            const int tok = (int)((uint32_t)r / (uint32_t)G);
+            q[u] = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.Q) + (g.t0 + tok) * a.ldq +
+                                                   (int64_t)(g.h * G + r - tok * G) * D + 8 * (lane % kLanes));
+          }
+        }
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u) {
+          const int r = r0 + u * kAtOnce + lane / kLanes;
+          uint32_t w[4] = {q[u].x, q[u].y, q[u].z, q[u].w};
+          int up = 127;   // exponent field of the row's power of two
+          if constexpr (TYPE == QMM_BF16) {
+            uint32_t top = 0;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) top = max(top, max(w[e] & 0x7FFFu, w[e] >> 16 & 0x7FFFu));
+#pragma unroll
+            for (int off = kLanes / 2; off >= 1; off >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, off));
+            up = top == 0 || top >= 0x7F80u ? 127 : min(254, 268 - (int)(top >> 7));
+            const float f = __uint_as_float((uint32_t)up << 23);
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              w[e] = pack2<QMM_F16>(__uint_as_float(w[e] << 16) * f, __uint_as_float(w[e] & 0xFFFF0000u) * f);
+          }
+          if (r < live) {
+            const int d = lane % kLanes;   // 16 bytes of the row
+            *reinterpret_cast<uint4*>(tile + (d / 8) * L::kQHalf + r * 128 + ((d % 8) ^ (r & 7)) * 16) =
+                make_uint4(w[0], w[1], w[2], w[3]);
+            if (d == 0) factors[(pos % kFactorTiles) * kN + r] = scalbnf(c, 127 - up);
+          }
+        }
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(kBarQFull + st));
+    }
+  } else if (warp == kMmaWarp) {
+    // ------------------------------------------------------------------ tensor cores
+    // The scores of a tile are issued ahead of the values of the one before it.
+    if (elect_one()) {
+      constexpr uint32_t kIdS = tc::idesc_16_f32(128, kN, false, false);
+      constexpr uint32_t kIdO = tc::idesc_16_f32(128, kN, false, false) | 1u << 15;   // V: MN-major
+      const uint64_t dq = tc::smem_desc_sw128(smem_addr(smem + L::kQ), 16, 1024);
+      const uint64_t dp = tc::smem_desc_sw128(smem_addr(smem + L::kP), 16, 1024);
+      // D = 64: O^T has 128 lanes all the same; the upper ones are products with other keys, and nobody reads them
+      const uint64_t dv = tc::smem_desc_sw128(smem_addr(smem + L::kV), D == 128 ? L::kVHalf : L::kVHalf / 2, 1024);
+      struct Pass {
+        Walker<kTile, kLead> w;
+        int left = 0;              // tiles left of the segment
+        uint32_t tile = 0, seg = 0;   // of the next one; segments begun
+      } qk, pv;
+      qk.w = pv.w = walk;
+      bool ok = true;
+      auto begin = [&](Pass& p) -> bool {   // whether there is another tile; first: whether it begins a segment
+        if (p.left == 0) {
+          if (!p.w.next(P, g)) return false;
+          p.left = g.j1 - g.j0;
+          ++p.seg;
+          return true;
+        }
+        return true;
+      };
+      auto scores = [&]() -> bool {
+        const bool fresh = qk.left == 0;
+        if (!begin(qk)) return false;
+        const uint32_t slot = (qk.seg - 1) & 1, kb = qk.tile % kKeyBufs, buf = qk.tile & 1;
+        if (fresh) ok = ok && wait(kBarQFull + slot, ((qk.seg - 1) >> 1) & 1);
+        ok = ok && wait(kBarKeyFull + kb, (qk.tile / kKeyBufs) & 1);
+        if (qk.tile >= 2) ok = ok && wait(kBarSFree + buf, ((qk.tile >> 1) - 1) & 1);
+        if (!ok) return false;
+        tc::fence_after_sync();
+#pragma unroll
+        for (int k = 0; k < D / 64; ++k)   // 64 values of the head: 4 MMAs, 8 columns and 32 bytes of each row further
+          tc::mma_f16_ts_x4(tmem + T::kS + kN * buf, tmem + kb * (D / 2) + 32 * k,
+                            dq + ((slot * L::kQBytes + k * L::kQHalf) >> 4), 2, kIdS, k > 0);
+        tc::commit(bar(kBarS + buf));
+        tc::commit(bar(kBarKeyEmpty + kb));
+        if (qk.left == 1) tc::commit(bar(kBarQEmpty + slot));
+        --qk.left;
+        ++qk.tile;
+        return true;
+      };
+      auto values = [&]() -> bool {
+        const bool fresh = pv.left == 0;
+        if (!begin(pv)) return false;
+        const uint32_t vb = pv.tile % kVB, buf = pv.tile & 1;
+        if (fresh && pv.seg > 1) ok = ok && wait(kBarOFree, pv.seg & 1);   // (segment s ends its phase s)
+        ok = ok && wait(kBarValueFull + vb, (pv.tile / kVB) & 1) && wait(kBarP + buf, (pv.tile >> 1) & 1);
+        if (!ok) return false;
+        tc::fence_after_sync();
+#pragma unroll
+        for (int k = 0; k < 2; ++k)   // 64 keys: 4 MMAs of 16 rows of V
+          mma_ss_x4(tmem + T::kO, dv + ((vb * L::kVBytes + k * 64 * 128) >> 4), 128,
+                    dp + ((buf * L::kPBytes + k * L::kPHalf) >> 4), 2, kIdO, !fresh || k > 0);
+        tc::commit(bar(kBarO + buf));
+        tc::commit(bar(kBarValueEmpty + vb));
+        --pv.left;
+        ++pv.tile;
+        return true;
+      };
+      scores();
+      while (ok) {
+        scores();
+        if (!ok || !values()) break;
+      }
+      // no tensor-core operation of this CTA is in flight when it ends
+      tc::commit(bar(kBarDrain));
+      mbar_wait(bar(kBarDrain), 0, kWaitLimit);
+    }
+    __syncwarp();
+  } else if (warp >= kKeyWarp && warp < kValueWarp) {
+    // ------------------------------------------------------------------ keys to fp16, in tensor memory
+    // A thread takes a key: D/2 bytes of codes, D/16 scales, D/2 columns of its lane.  (What lies behind the last key
+    // is masked by position.)
+    const int key = (warp - kKeyWarp) * 32 + lane;
+    const uint32_t lanes = (uint32_t)(warp - kKeyWarp) << 21;   // first TMEM lane << 16
+    uint32_t tile = 0;
+    bool ok = true;
+    while (ok && walk.next(P, g)) {
+      for (int j = g.j0; j < g.j1; ++j, ++tile) {
+        const uint32_t from = 2 * tile % kPacks, kb = tile % kKeyBufs;
+        ok = wait(kBarPackFull + from, (2 * tile / kPacks) & 1) &&
+             (tile < kKeyBufs || wait(kBarKeyEmpty + kb, (tile / kKeyBufs - 1) & 1));
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        tc::fence_after_sync();
+        const uint8_t* src = smem + L::kPack + from * L::kPackBytes;
+        uint4 code[D / 32];
+        uint32_t scale[D / 64];
+#pragma unroll
+        for (int q = 0; q < D / 32; ++q) code[q] = *reinterpret_cast<const uint4*>(src + key * (D / 2) + 16 * q);
+#pragma unroll
+        for (int q = 0; q < D / 64; ++q)
+          scale[q] = *reinterpret_cast<const uint32_t*>(src + kTile * (D / 2) + key * (D / 16) + 4 * q);
+#pragma unroll
+        for (int q = 0; q < D / 32; ++q) {   // two blocks
+          uint32_t h[16];
+          uint32_t (&h0)[8] = *reinterpret_cast<uint32_t (*)[8]>(&h[0]), (&h1)[8] = *reinterpret_cast<uint32_t (*)[8]>(&h[8]);
+          const uint32_t two = scale[q / 2] >> (16 * (q & 1));
+          to_half(make_uint2(code[q].x, code[q].y), e4m3x2_pair(__byte_perm(two, 0, 0x00)), h0);
+          to_half(make_uint2(code[q].z, code[q].w), e4m3x2_pair(__byte_perm(two, 0, 0x11)), h1);
+          tc::st_x16(tmem + lanes + kb * (D / 2) + 16 * q, h);
+        }
+        tc::wait_st();
+        tc::fence_before_sync();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(bar(kBarKeyFull + kb));
+          mbar_arrive(bar(kBarPackEmpty + from));
+        }
+      }
+    }
+  } else if (warp >= kValueWarp) {
+    // ------------------------------------------------------------------ values to fp16, in shared memory
+    // A thread takes a block of 16 values at a time: of neighbouring threads four have the blocks of 64 values of one
+    // key, so that eight write to eight different 16-byte columns.
+    constexpr int kBlocks = D / kv4::kBlock, kUnits = kTile * kBlocks / (32 * kGroupWarps), kHalves = D / 64;
+    const int me = (warp - kValueWarp) * 32 + lane;
+    uint32_t tile = 0, segs = 0;
+    bool ok = true;
+    while (ok && walk.next(P, g)) {
+      const int clean_from = g.own ? clampi(g.first_keys, 0, g.keys) : g.keys;
+      ++segs;
+      for (int j = g.j0; j < g.j1; ++j, ++tile) {
+        const uint32_t from = (2 * tile + 1) % kPacks, vb = tile % kVB;
+        ok = wait(kBarPackFull + from, ((2 * tile + 1) / kPacks) & 1) &&
+             (tile < kVB || wait(kBarValueEmpty + vb, (tile / kVB - 1) & 1));
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        const uint8_t* src = smem + L::kPack + from * L::kPackBytes;
+        uint8_t* dst = smem + L::kV + vb * L::kVBytes;
+        const int base = j * kTile;
+        uint2 code[kUnits];
+        uint32_t scale[kUnits];
+        auto key_of = [&](int u) { return u / kHalves * 32 + me / 4; };
+        auto block_of = [&](int u) { return u % kHalves * 4 + me % 4; };
+#pragma unroll
+        for (int u = 0; u < kUnits; ++u) {
+          code[u] = *reinterpret_cast<const uint2*>(src + key_of(u) * (D / 2) + block_of(u) * 8);
+          scale[u] = src[kTile * (D / 2) + key_of(u) * kBlocks + block_of(u)];
+        }
+        if (base + kTile > clean_from) {   // zeros behind the last key, and for the NaN blocks of keys that not every row sees
+          bool odd = false;
+#pragma unroll
+          for (int u = 0; u < kUnits; ++u) {
+            const int key = base + key_of(u);
+            const bool nan = (scale[u] & 0x7Fu) == kv4::kScaleNaN && key >= clean_from && key < g.keys;
+            odd |= nan;
+            if (nan || key >= g.keys) scale[u] = 0;
+          }
+          if (odd) *reinterpret_cast<volatile uint32_t*>(&M.odd[segs & 7]) = segs;
+        }
+#pragma unroll
+        for (int u = 0; u < kUnits; ++u) {
+          uint32_t h[8];
+          to_half(code[u], e4m3x2_pair(scale[u] * 0x101u), h);
+          const int key = key_of(u);
+          uint8_t* row = dst + (u % kHalves) * L::kVHalf + key * 128;
+          const int c0 = 2 * (me % 4);
+          *reinterpret_cast<uint4*>(row + (c0 ^ (key & 7)) * 16) = make_uint4(h[0], h[1], h[2], h[3]);
+          *reinterpret_cast<uint4*>(row + ((c0 + 1) ^ (key & 7)) * 16) = make_uint4(h[4], h[5], h[6], h[7]);
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(bar(kBarValueFull + vb));
+          mbar_arrive(bar(kBarPackEmpty + from));
+        }
+      }
+    }
+  } else if (warp < kGroupWarps) {
+    // ------------------------------------------------------------------ softmax, a thread per key
+    const int mine = warp * 32 + lane;                // key of the tile; value of O^T
+    const uint32_t lanes = (uint32_t)warp << 21;      // first TMEM lane << 16
+    float* off = reinterpret_cast<float*>(smem + L::kOff) + warp * kN;
+    float* red = reinterpret_cast<float*>(smem + L::kRed);
+    uint32_t tile = 0, segs = 0;
+    bool ok = true, left = false;
+    while (!left && walk.next(P, g)) {
+      const float* factors = reinterpret_cast<const float*>(smem + L::kFactors) + segs % kFactorTiles * kN;
+      const int live = g.rows * G;
+      ++segs;
+      float sum[kN];
+#pragma unroll
+      for (int r = 0; r < kN; ++r) sum[r] = 0.0f;
+      for (int r = lane; r < kN; r += 32) off[r] = 0.0f;
+      __syncwarp();
+      for (int j = g.j0; !left && j < g.j1; ++j, ++tile) {
+        const uint32_t buf = tile & 1, phase = (tile >> 1) & 1;
+        const int key = j * kTile + mine;
+        // the first row that sees this thread's key
+        const int from = key >= g.keys ? kN : g.own ? max(0, key - g.first_keys + 1) * G : 0;
+        const bool hidden = __any_sync(0xffffffffu, from > 0);
+        ok = wait_w(kBarS + buf, phase) && ok;
+        tc::fence_after_sync();
+#pragma unroll
+        for (int c0 = 0; c0 < kN; c0 += kChunk) {
+          if (c0 >= live) break;
+          uint32_t s[kChunk];
+          tc::ld_wait_x32(tmem + lanes + T::kS + kN * buf + c0, s);
+          if (c0 + kChunk >= live) {   // the last chunk: S^T is free
+            tc::fence_before_sync();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(kBarSFree + buf));
+          }
+          float x[kChunk];
+          bool grew = false;
+#pragma unroll
+          for (int r = 0; r < kChunk; r += 4) {
+            const float4 f = *reinterpret_cast<const float4*>(factors + c0 + r), o = *reinterpret_cast<const float4*>(off + c0 + r);
+            x[r] = __fmaf_rn(__uint_as_float(s[r]), f.x, o.x);
+            x[r + 1] = __fmaf_rn(__uint_as_float(s[r + 1]), f.y, o.y);
+            x[r + 2] = __fmaf_rn(__uint_as_float(s[r + 2]), f.z, o.z);
+            x[r + 3] = __fmaf_rn(__uint_as_float(s[r + 3]), f.w, o.w);
+          }
+          if (hidden)
+#pragma unroll
+            for (int r = 0; r < kChunk; ++r)
+              if (c0 + r < from) x[r] = -INFINITY;
+#pragma unroll
+          for (int r = 0; r < kChunk; ++r) grew |= c0 + r < live && x[r] > kLift + kGrow;
+          const bool first = j == g.j0;
+          if (any_of_softmax(grew || !ok || first)) {
+            if (any_of_softmax(!ok)) {
+              left = true;
+              break;
+            }
+            // the rows' maxima of this tile: lane r of each warp gets row c0 + r's
+            float most = -INFINITY;
+#pragma unroll
+            for (int r = 0; r < kChunk; ++r) {
+              const float v = x[r] == x[r] ? x[r] : -INFINITY;
+              const uint32_t b = __float_as_uint(v), up = __reduce_max_sync(0xffffffffu, b & 0x80000000u ? ~b : b | 0x80000000u);
+              if (lane == r) most = __uint_as_float(up & 0x80000000u ? up & 0x7FFFFFFFu : ~up);
+            }
+            red[warp * kN + c0 + lane] = most;
+            any_of_softmax(false);
+#pragma unroll
+            for (int w = 0; w < kGroupWarps; ++w) most = fmaxf(most, red[w * kN + c0 + lane]);
+            // a row that sees no key of the segment's first tile sees none of the segment
+            const float was = off[c0 + lane];
+            const float now = most > -INFINITY && (first || most > kLift + kGrow) ? was - (most - kLift) : was;
+            const float moved = now - was, keep = exp2_fast(moved);
+            __syncwarp();
+            off[c0 + lane] = now;
+            __syncwarp();
+#pragma unroll
+            for (int r = 0; r < kChunk; ++r) {
+              x[r] += __shfl_sync(0xffffffffu, moved, r);
+              if (!first) sum[c0 + r] *= __shfl_sync(0xffffffffu, keep, r);
+            }
+            if (!first) {
+              // O^T, once the products of the tile before are in it
+              ok = wait_w(kBarO + (buf ^ 1), ((tile - 1) >> 1) & 1) && ok;
+              tc::fence_after_sync();
+              uint32_t o[kChunk];
+              tc::ld_wait_x32(tmem + lanes + T::kO + c0, o);
+#pragma unroll
+              for (int r = 0; r < kChunk; ++r)
+                o[r] = __float_as_uint(__uint_as_float(o[r]) * __shfl_sync(0xffffffffu, keep, r));
+              tc::st_x32(tmem + lanes + T::kO + c0, o);
+              tc::wait_st();
+            }
+          }
+          if (c0 == 0 && tile >= 2) ok = wait_w(kBarO + buf, phase ^ 1) && ok;   // the last readers of this p
+          uint8_t* p = smem + L::kP + buf * L::kPBytes + (mine / 64) * L::kPHalf;
+          const int at = mine % 64 * 2;
+#pragma unroll
+          for (int r = 0; r < kChunk; r += 8) {
+            if (c0 + r >= live) break;
+#pragma unroll
+            for (int q = 0; q < 8; ++q) {
+              const float w = exp2_fast(x[r + q]);
+              sum[c0 + r + q] += w;
+              *reinterpret_cast<__half*>(p + (c0 + r + q) * 128 + (at ^ ((r + q) & 7) << 4)) = __float2half_rn(w);
+            }
+          }
+        }
+        fence_proxy_async_smem();
+        tc::fence_before_sync();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(kBarP + buf));
+      }
+      if (left) break;
+
+      // ---- the segment's sums to the workspace
+      ok = wait_w(kBarO + ((tile - 1) & 1), ((tile - 1) >> 1) & 1) && ok;
+      if (any_of_softmax(!ok)) break;
+      tc::fence_after_sync();
+      const bool inside = g.j0 > 0;   // not the first segment of its group: the CTA's own record
+      auto record = [&](int r) -> int64_t {
+        return inside ? (int64_t)blockIdx.x * 2 * kRows + r
+                      : ((int64_t)(g.own ? a.T : 0) + g.t0 + r / G) * a.Hq + (int64_t)g.h * G + r % G;
+      };
+      float* out = inside ? P.o_cta : P.o_rows;
+#pragma unroll
+      for (int c0 = 0; c0 < kN; c0 += 32) {
+        if (c0 >= live) break;
+        float part[32];
+#pragma unroll
+        for (int r = 0; r < 32; ++r) part[r] = sum[c0 + r];
+        butterfly_reduce<32>(part, lane);
+        red[warp * kN + c0 + lane] = part[0];
+      }
+      any_of_softmax(false);
+      if (mine < live) {
+        const float all = (red[mine] + red[kN + mine]) + (red[2 * kN + mine] + red[3 * kN + mine]);
+        const uint32_t per = (uint32_t)min(M.piece.per, (int64_t)0x7fffffff);
+        const uint32_t others = g.rest > 0 ? ((uint32_t)g.rest + per - 1) / per : 0;
+        const uint32_t odd = *reinterpret_cast<volatile uint32_t*>(&M.odd[segs & 7]) == segs;
+        (inside ? P.s_cta : P.s_rows)[record(mine)] =
+            RowStat{all == 0.0f ? -INFINITY : -off[mine], all, odd, others << 16 | (blockIdx.x + 1)};
+      }
+      // O^T: this thread's value of every row, at the place where the combine launch looks for it (column_of)
+      if (mine < D) {
+        const int place = (mine & ~31) + 8 * (mine >> 1 & 3) + 2 * (mine >> 3 & 3) + (mine & 1);
+#pragma unroll
+        for (int c0 = 0; c0 < kN; c0 += 32) {
+          if (c0 >= live) break;
+          uint32_t o[32];
+          tc::ld_wait_x32(tmem + lanes + T::kO + c0, o);
+#pragma unroll
+          for (int r = 0; r < 32; ++r)
+            if (c0 + r < live) out[record(c0 + r) * D + place] = __uint_as_float(o[r]);
+        }
+      }
+      tc::fence_before_sync();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(kBarOFree));
+      any_of_softmax(false);   // (red is written again behind this)
+    }
+  }
+
+  tc::fence_before_sync();
+  __syncthreads();
+  tc::fence_after_sync();
+  if (warp == kMmaWarp) tc::tmem_dealloc(tmem, kTmemCols);
+}
+
+template <int D, int TYPE>
+cudaError_t launch(const qmm_attn_fp4_args& f, void* workspace, cudaStream_t stream) {
+  static DeviceOnce once;
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  e = once.run(dev, cudaSuccess, [] {
+    return cudaFuncSetAttribute(attn_fp4_kernel<D, TYPE>, cudaFuncAttributeMaxDynamicSharedMemorySize, Smem<D>::kTotal);
+  });
+  if (e != cudaSuccess) return e;
+  const int sms = sm_count();
+  if (sms < 1) return cudaErrorNoDevice;
+  const int tokens = kN / (f.base.Hq / f.base.Hk);
+  Common P;
+  fill(P, f.base, tokens, tokens, workspace);
+  P.k_scale = f.k_scale;
+  P.v_scale = f.v_scale;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(sms < kMaxCtas ? sms : kMaxCtas);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = Smem<D>::kTotal;
+  cfg.stream = stream;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  e = cudaLaunchKernelEx(&cfg, attn_fp4_kernel<D, TYPE>, P);
+  if (e != cudaSuccess) return e;
+  return launch_combine<D, TYPE, true>(P, sms, stream);
+}
+
+}  // namespace
+
+size_t attn_fp4_workspace_bytes(const qmm_attn_fp4_args& f) { return Space(f.base).total; }
+
+cudaError_t launch_attn_fp4(const qmm_attn_fp4_args& f, void* workspace, cudaStream_t stream) {
+  if (f.base.D == 64)
+    return f.base.type == QMM_BF16 ? launch<64, QMM_BF16>(f, workspace, stream) : launch<64, QMM_F16>(f, workspace, stream);
+  return f.base.type == QMM_BF16 ? launch<128, QMM_BF16>(f, workspace, stream) : launch<128, QMM_F16>(f, workspace, stream);
+}
+
+cudaError_t read_and_clear_attn_fp4_status(unsigned* out) {
+  unsigned v = 0, zero = 0;
+  cudaError_t e = cudaMemcpyFromSymbol(&v, g_status, sizeof(v));
+  if (e != cudaSuccess) return e;
+  e = cudaMemcpyToSymbol(g_status, &zero, sizeof(zero));
+  *out = v;
+  return e;
+}
+
+}  // namespace q4k
