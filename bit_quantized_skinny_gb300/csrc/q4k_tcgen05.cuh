@@ -201,6 +201,15 @@ __device__ __forceinline__ void ld_x32(uint32_t taddr, float (&v)[32]) {
   for (int k = 0; k < 32; ++k) v[k] = __uint_as_float(r[k]);
 }
 
+// Eight columns of the warp's lanes into registers, and the wait for them (see ld_wait_x32).
+__device__ __forceinline__ void ld_wait_x8(uint32_t taddr, uint32_t (&r)[8]) {
+  asm volatile(
+      " tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];\n"
+      " tcgen05.wait::ld.sync.aligned;"
+      : "=&r"(r[0]), "=&r"(r[1]), "=&r"(r[2]), "=&r"(r[3]), "=&r"(r[4]), "=&r"(r[5]), "=&r"(r[6]), "=&r"(r[7])
+      : "r"(taddr) : "memory");
+}
+
 // 32 or 64 columns of the warp's lanes into registers, and the wait for them in the same statement: no
 // register is read before it has arrived, whatever the compiler moves.
 __device__ __forceinline__ void ld_wait_x32(uint32_t taddr, uint32_t (&r)[32]) {

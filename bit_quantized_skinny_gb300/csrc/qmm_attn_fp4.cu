@@ -8,9 +8,11 @@
 // is exact there).  So everything is laid out by the keys, with the rows as the narrow side of both products:
 //     S^T = K Q^T        tcgen05, K (128 keys x D) from tensor memory, where four warps put it, a thread a key
 //     p = 2^(c S + off)  a thread per key, S^T from tensor memory, c = scale k_scale log2 e over the row's power of two
-//     O^T += V^T p^T     tcgen05, V (MN-major) and p^T from shared memory; four more warps write V
+//     O^T += V^T p^T     tcgen05, V and p^T (both MN-major) from shared memory; four more warps write V
+//     l += 1 p^T         tcgen05, ones from tensor memory: the rows' sums of weights, of the rounded ones as in O^T
 // so few rows cost little, the exponentials of a row are spread over 128 threads, and no 128-row tile of queries
-// is read again for every tile.
+// is read again for every tile.  Two groups of softmax warps have half of a block's rows each, or, where a block has no
+// more than one of them takes, the key tiles in turn, with sums of their own that are joined at a segment's end.
 // off moves, and O^T is rescaled, only when a row's maximum grew by more than 8; weights are then at most 2^15, and
 // fp16 holds those down to 2^-21 of the largest at full precision.
 //
@@ -18,6 +20,7 @@
 // are zeroed, and so are NaN blocks among the keys that only some rows of the block see (a draft's last keys);
 // attn_combine_kernel adds those back, from the cache, to the rows that see them.
 #include <cstdint>
+#include <type_traits>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -38,12 +41,12 @@ __device__ unsigned g_status;   // this file's kernels' status word
 constexpr int kTile = 128;           // keys of a key tile
 constexpr int kLead = 3;             // units of a group besides its key tiles
 constexpr int kN = 64;               // rows of a block
-constexpr int kChunk = 32;           // rows that a softmax thread has in registers at a time
-// warps: 0-3 softmax, 4 copies, 5 tensor cores, 6 queries, 8-11 keys, 12-15 values to fp16
-constexpr int kLoadWarp = 4, kMmaWarp = 5, kQWarp = 6, kKeyWarp = 8, kValueWarp = 12;
-constexpr int kThreads = 16 * 32, kGroupWarps = 4;
+constexpr int kHalf = kN / 2;        // rows of a softmax group
+// warps: 0-3 and 4-7 softmax, 8 copies, 9 tensor cores, 10 queries, 12-15 keys and 16-19 values to fp16
+constexpr int kLoadWarp = 8, kMmaWarp = 9, kQWarp = 10, kKeyWarp = 12, kValueWarp = 16;
+constexpr int kThreads = 20 * 32, kGroupWarps = 4;
 constexpr uint32_t kTmemCols = 512;
-constexpr int kKeyBufs = 4;          // tiles of keys in tensor memory
+constexpr int kKeyBufs = 3;          // tiles of keys in tensor memory
 constexpr int kPacks = 10;           // packed tiles in shared memory: of keys and of values in turn
 constexpr int kFactorTiles = 8;      // (the softmax is a few query tiles behind)
 constexpr float kGrow = 8.0f;
@@ -59,31 +62,30 @@ struct Smem {
   static constexpr int kValueBufs = D == 128 ? 2 : 3;
   static constexpr int kQHalf = kN * 128;                // 64 values of N rows
   static constexpr int kQBytes = kN * D * 2;
-  static constexpr int kPHalf = kN * 128;                // 64 keys of N rows
-  static constexpr int kPBytes = kN * kTile * 2;
+  static constexpr int kPBytes = kTile * 128;            // 128 keys of 64 rows
   static constexpr int kV = 0;
   static constexpr int kQ = kV + kValueBufs * kVBytes;
   static constexpr int kP = kQ + 2 * kQBytes;
   static constexpr int kPack = kP + 2 * kPBytes;
   static constexpr int kFactors = kPack + kPacks * kPackBytes;   // of the rows of the last kFactorTiles query tiles
-  static constexpr int kOff = kFactors + kFactorTiles * kN * 4;  // each softmax warp's copy of the rows' off
-  static constexpr int kRed = kOff + kGroupWarps * kN * 4;       // the softmax warps' maxima or sums of the rows
-  static constexpr int kMisc = kRed + kGroupWarps * kN * 4;
+  static constexpr int kOff = kFactors + kFactorTiles * kN * 4;  // each softmax warp's copy of its group's rows' off
+  static constexpr int kRed = kOff + 2 * kGroupWarps * kHalf * 4;   // the softmax warps' maxima of the rows
+  static constexpr int kMisc = kRed + 2 * kGroupWarps * kHalf * 4;
   static constexpr int kTotal = kMisc + 1024;
 };
 static_assert(Smem<128>::kTotal <= 227 * 1024 && Smem<64>::kTotal <= 227 * 1024, "shared memory");
 
-// Tensor memory: K at 0, S^T behind it (two of them), then O^T.
+// Tensor memory: K at 0, S^T behind it (two of them), then O^T, l, and the ones.
 template <int D>
 struct Tmem {
-  static constexpr uint32_t kS = kKeyBufs * D / 2, kO = kS + 2 * kN;
-  static_assert(kO + kN <= kTmemCols, "tensor memory");
+  static constexpr uint32_t kS = kKeyBufs * D / 2, kO = kS + 2 * kN, kL = kO + kN, kOnes = kL + kN;
+  static_assert(kOnes + 32 <= kTmemCols, "tensor memory");
 };
 
 // Barriers; a wait tells a phase from the one after it only, and every wait here is for the phase of a tile (or a segment)
 // of whose successor on the same barrier the waiting role itself is a condition.
 enum : int {
-  kBarPackFull = 0, kBarPackEmpty = 10, kBarKeyFull = 20, kBarKeyEmpty = 24, kBarValueFull = 28, kBarValueEmpty = 31,
+  kBarPackFull = 0, kBarPackEmpty = 10, kBarKeyFull = 20, kBarKeyEmpty = 24 /* 20 + and 24 + buffer */, kBarValueFull = 28, kBarValueEmpty = 31,
   kBarS = 34, kBarSFree = 36, kBarP = 38, kBarO = 40 /* products of a tile's values are done */, kBarQFull = 42,
   kBarQEmpty = 44, kBarOFree = 46, kBarDrain = 47, kBars = 48
 };
@@ -122,11 +124,11 @@ __device__ __forceinline__ void mma_ss_x4(uint32_t d_taddr, uint64_t a, uint64_t
       : "memory");
 }
 
-// The softmax warps meet: whether any of their threads says so.
-__device__ __forceinline__ bool any_of_softmax(bool mine) {
+// `threads` threads (a softmax group, or both) meet at barrier `id`: whether any of them says so.
+__device__ __forceinline__ bool any_of(bool mine, int id, int threads) {
   uint32_t any;
-  asm volatile("{\n .reg .pred p, q;\n setp.ne.b32 p, %1, 0;\n barrier.cta.red.or.pred q, 1, 128, p;\n selp.u32 %0, 1, 0, q;\n}"
-               : "=r"(any) : "r"((uint32_t)mine) : "memory");
+  asm volatile("{\n .reg .pred p, q;\n setp.ne.b32 p, %1, 0;\n barrier.cta.red.or.pred q, %2, %3, p;\n selp.u32 %0, 1, 0, q;\n}"
+               : "=r"(any) : "r"((uint32_t)mine), "r"(id), "r"(threads) : "memory");
   return any != 0;
 }
 
@@ -140,15 +142,16 @@ __device__ __noinline__ bool wait_slowly(uint32_t bar, uint32_t parity, uint32_t
   return false;
 }
 
-// fp16 pairs of a block's eight bytes of codes and its scale (both halves).
-__device__ __forceinline__ void to_half(uint2 code, uint32_t s, uint32_t (&h)[8]) {
+// fp16 pairs of a block's eight bytes of codes and its scale (both halves), to h[AT] and on.
+template <int AT, int N>
+__device__ __forceinline__ void to_half(uint2 code, uint32_t s, uint32_t (&h)[N]) {
   uint32_t lo[4], hi[4];
   e2m1x8_pairs(code.x, lo);
   e2m1x8_pairs(code.y, hi);
 #pragma unroll
   for (int e = 0; e < 4; ++e) {
-    h[e] = mul2(lo[e], s);
-    h[4 + e] = mul2(hi[e], s);
+    h[AT + e] = mul2(lo[e], s);
+    h[AT + 4 + e] = mul2(hi[e], s);
   }
 }
 
@@ -169,9 +172,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fp4_kernel(const __grid_cons
   // ---- barriers, tensor memory, and this CTA's piece of the list of key tiles
   if (threadIdx.x < kBars) {
     const int k = threadIdx.x;
-    const bool warps = (k >= kBarPackEmpty && k < kBarKeyEmpty) || (k >= kBarValueFull && k < kBarValueEmpty) ||
-                       (k >= kBarSFree && k < kBarO) || k == kBarOFree;
-    mbar_init(bar(k), warps ? kGroupWarps : 1);
+    const bool warps = (k >= kBarPackEmpty && k < kBarKeyEmpty) || (k >= kBarValueFull && k < kBarValueEmpty);
+    const bool softmax = (k >= kBarSFree && k < kBarO) || k == kBarOFree;
+    mbar_init(bar(k), softmax ? 2 * kGroupWarps : warps ? kGroupWarps : 1);
     fence_barrier_init();
   } else if (threadIdx.x == kBars) {
     M.abort = 0;
@@ -190,6 +193,16 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fp4_kernel(const __grid_cons
   __syncthreads();
   tc::fence_after_sync();
   const uint32_t tmem = M.tmem;
+  if (warp < kGroupWarps) {   // (all lanes)
+    uint32_t ones[32];
+#pragma unroll
+    for (int k = 0; k < 32; ++k) ones[k] = 0x3C003C00u;
+    tc::st_x32(tmem + ((uint32_t)warp << 21) + T::kOnes, ones);
+    tc::wait_st();
+    tc::fence_before_sync();
+  }
+  __syncthreads();
+  tc::fence_after_sync();
 
   // A bounded wait for a phase of a barrier; false: this wait, or another one, gave up.  (A phase that is over is the
   // rule, and a suspended wait takes 200 clocks to see it.)
@@ -302,6 +315,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fp4_kernel(const __grid_cons
           }
         }
       }
+      // scores of rows behind the last one come to 0 (or NaN): they never grow
+      for (int r = live + lane; r < kN; r += 32) factors[(pos % kFactorTiles) * kN + r] = 0.0f;
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(kBarQFull + st));
@@ -310,31 +325,32 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fp4_kernel(const __grid_cons
     // ------------------------------------------------------------------ tensor cores
     // The scores of a tile are issued ahead of the values of the one before it.
     if (elect_one()) {
-      constexpr uint32_t kIdS = tc::idesc_16_f32(128, kN, false, false);
-      constexpr uint32_t kIdO = tc::idesc_16_f32(128, kN, false, false) | 1u << 15;   // V: MN-major
+      constexpr uint32_t kIdBoth = tc::idesc_16_f32(128, kN, false, false), kIdHalf = tc::idesc_16_f32(128, kHalf, false, false);
+      constexpr uint32_t kMnMajorA = 1u << 15, kMnMajorB = 1u << 16;   // V and p
       const uint64_t dq = tc::smem_desc_sw128(smem_addr(smem + L::kQ), 16, 1024);
       const uint64_t dp = tc::smem_desc_sw128(smem_addr(smem + L::kP), 16, 1024);
       // D = 64: O^T has 128 lanes all the same; the upper ones are products with other keys, and nobody reads them
       const uint64_t dv = tc::smem_desc_sw128(smem_addr(smem + L::kV), D == 128 ? L::kVHalf : L::kVHalf / 2, 1024);
       struct Pass {
         Walker<kTile, kLead> w;
-        int left = 0;              // tiles left of the segment
-        uint32_t tile = 0, seg = 0;   // of the next one; segments begun
+        int left = 0, done = 0;       // tiles of the segment left, and gone
+        bool both = false;            // more rows than one group has
+        uint32_t tile = 0, seg = 0;   // the next one; segments begun
       } qk, pv;
       qk.w = pv.w = walk;
       bool ok = true;
-      auto begin = [&](Pass& p) -> bool {   // whether there is another tile; first: whether it begins a segment
-        if (p.left == 0) {
-          if (!p.w.next(P, g)) return false;
-          p.left = g.j1 - g.j0;
-          ++p.seg;
-          return true;
-        }
+      auto begin = [&](Pass& p) -> bool {   // whether there is another tile
+        if (p.left > 0) return true;
+        if (!p.w.next(P, g)) return false;
+        p.left = g.j1 - g.j0;
+        p.done = 0;
+        p.both = g.rows * G > kHalf;
+        ++p.seg;
         return true;
       };
       auto scores = [&]() -> bool {
-        const bool fresh = qk.left == 0;
         if (!begin(qk)) return false;
+        const bool fresh = qk.done == 0;
         const uint32_t slot = (qk.seg - 1) & 1, kb = qk.tile % kKeyBufs, buf = qk.tile & 1;
         if (fresh) ok = ok && wait(kBarQFull + slot, ((qk.seg - 1) >> 1) & 1);
         ok = ok && wait(kBarKeyFull + kb, (qk.tile / kKeyBufs) & 1);
@@ -344,29 +360,34 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fp4_kernel(const __grid_cons
 #pragma unroll
         for (int k = 0; k < D / 64; ++k)   // 64 values of the head: 4 MMAs, 8 columns and 32 bytes of each row further
           tc::mma_f16_ts_x4(tmem + T::kS + kN * buf, tmem + kb * (D / 2) + 32 * k,
-                            dq + ((slot * L::kQBytes + k * L::kQHalf) >> 4), 2, kIdS, k > 0);
+                            dq + ((slot * L::kQBytes + k * L::kQHalf) >> 4), 2, qk.both ? kIdBoth : kIdHalf, k > 0);
         tc::commit(bar(kBarS + buf));
         tc::commit(bar(kBarKeyEmpty + kb));
         if (qk.left == 1) tc::commit(bar(kBarQEmpty + slot));
         --qk.left;
+        ++qk.done;
         ++qk.tile;
         return true;
       };
       auto values = [&]() -> bool {
-        const bool fresh = pv.left == 0;
         if (!begin(pv)) return false;
         const uint32_t vb = pv.tile % kVB, buf = pv.tile & 1;
-        if (fresh && pv.seg > 1) ok = ok && wait(kBarOFree, pv.seg & 1);   // (segment s ends its phase s)
+        const bool fresh = pv.done < (pv.both ? 1 : 2);   // the first of its sums
+        if (pv.done == 0 && pv.seg > 1) ok = ok && wait(kBarOFree, pv.seg & 1);   // (segment s ends its phase s)
         ok = ok && wait(kBarValueFull + vb, (pv.tile / kVB) & 1) && wait(kBarP + buf, (pv.tile >> 1) & 1);
         if (!ok) return false;
         tc::fence_after_sync();
+        const uint32_t at = pv.both ? 0 : kHalf * buf, id = (pv.both ? kIdBoth : kIdHalf) | kMnMajorB;
 #pragma unroll
-        for (int k = 0; k < 2; ++k)   // 64 keys: 4 MMAs of 16 rows of V
-          mma_ss_x4(tmem + T::kO, dv + ((vb * L::kVBytes + k * 64 * 128) >> 4), 128,
-                    dp + ((buf * L::kPBytes + k * L::kPHalf) >> 4), 2, kIdO, !fresh || k > 0);
+        for (int k = 0; k < 2; ++k) {   // 64 keys: 4 MMAs of 16 rows of V and of p
+          const uint64_t p = dp + ((buf * L::kPBytes + k * 64 * 128) >> 4);
+          mma_ss_x4(tmem + T::kO + at, dv + ((vb * L::kVBytes + k * 64 * 128) >> 4), 128, p, 128, id | kMnMajorA, !fresh || k > 0);
+          tc::mma_f16_ts_x4(tmem + T::kL + at, tmem + T::kOnes, p, 128, id, !fresh || k > 0);
+        }
         tc::commit(bar(kBarO + buf));
         tc::commit(bar(kBarValueEmpty + vb));
         --pv.left;
+        ++pv.done;
         ++pv.tile;
         return true;
       };
@@ -407,10 +428,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fp4_kernel(const __grid_cons
 #pragma unroll
         for (int q = 0; q < D / 32; ++q) {   // two blocks
           uint32_t h[16];
-          uint32_t (&h0)[8] = *reinterpret_cast<uint32_t (*)[8]>(&h[0]), (&h1)[8] = *reinterpret_cast<uint32_t (*)[8]>(&h[8]);
           const uint32_t two = scale[q / 2] >> (16 * (q & 1));
-          to_half(make_uint2(code[q].x, code[q].y), e4m3x2_pair(__byte_perm(two, 0, 0x00)), h0);
-          to_half(make_uint2(code[q].z, code[q].w), e4m3x2_pair(__byte_perm(two, 0, 0x11)), h1);
+          to_half<0>(make_uint2(code[q].x, code[q].y), e4m3x2_pair(__byte_perm(two, 0, 0x00)), h);
+          to_half<8>(make_uint2(code[q].z, code[q].w), e4m3x2_pair(__byte_perm(two, 0, 0x11)), h);
           tc::st_x16(tmem + lanes + kb * (D / 2) + 16 * q, h);
         }
         tc::wait_st();
@@ -465,7 +485,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fp4_kernel(const __grid_cons
 #pragma unroll
         for (int u = 0; u < kUnits; ++u) {
           uint32_t h[8];
-          to_half(code[u], e4m3x2_pair(scale[u] * 0x101u), h);
+          to_half<0>(code[u], e4m3x2_pair(scale[u] * 0x101u), h);
           const int key = key_of(u);
           uint8_t* row = dst + (u % kHalves) * L::kVHalf + key * 128;
           const int c0 = 2 * (me % 4);
@@ -480,124 +500,162 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fp4_kernel(const __grid_cons
         }
       }
     }
-  } else if (warp < kGroupWarps) {
+  } else if (warp < 2 * kGroupWarps) {
     // ------------------------------------------------------------------ softmax, a thread per key
-    const int mine = warp * 32 + lane;                // key of the tile; value of O^T
-    const uint32_t lanes = (uint32_t)warp << 21;      // first TMEM lane << 16
-    float* off = reinterpret_cast<float*>(smem + L::kOff) + warp * kN;
-    float* red = reinterpret_cast<float*>(smem + L::kRed);
+    const int grp = warp / kGroupWarps, wg = warp % kGroupWarps;
+    const int mine = wg * 32 + lane;                  // key of the tile; value of O^T
+    const uint32_t lanes = (uint32_t)wg << 21;        // first TMEM lane << 16
+    float* off = reinterpret_cast<float*>(smem + L::kOff) + warp * kHalf;
+    float* red = reinterpret_cast<float*>(smem + L::kRed) + grp * kGroupWarps * kHalf;
+    auto any_here = [&](bool x) { return any_of(x, 1 + grp, 32 * kGroupWarps); };
     uint32_t tile = 0, segs = 0;
-    bool ok = true, left = false;
-    while (!left && walk.next(P, g)) {
-      const float* factors = reinterpret_cast<const float*>(smem + L::kFactors) + segs % kFactorTiles * kN;
-      const int live = g.rows * G;
+    bool ok = true;
+    while (walk.next(P, g)) {
+      const int rows = g.rows * G;
+      const bool both = rows > kHalf;
+      const int c0 = both ? kHalf * grp : 0, live = both ? clampi(rows - c0, 0, kHalf) : rows;   // the group's rows
+      const float* factors = reinterpret_cast<const float*>(smem + L::kFactors) + segs % kFactorTiles * kN + c0;
       ++segs;
-      float sum[kN];
-#pragma unroll
-      for (int r = 0; r < kN; ++r) sum[r] = 0.0f;
-      for (int r = lane; r < kN; r += 32) off[r] = 0.0f;
+      off[lane] = 0.0f;
       __syncwarp();
-      for (int j = g.j0; !left && j < g.j1; ++j, ++tile) {
+      bool first = true;
+      for (int j = g.j0; j < g.j1; ++j, ++tile) {
         const uint32_t buf = tile & 1, phase = (tile >> 1) & 1;
+        if (!both && (int)buf != grp) continue;
         const int key = j * kTile + mine;
-        // the first row that sees this thread's key
-        const int from = key >= g.keys ? kN : g.own ? max(0, key - g.first_keys + 1) * G : 0;
+        // the first of the group's rows that sees this thread's key
+        const int from = (key >= g.keys ? kN : g.own ? max(0, key - g.first_keys + 1) * G : 0) - c0;
         const bool hidden = __any_sync(0xffffffffu, from > 0);
         ok = wait_w(kBarS + buf, phase) && ok;
         tc::fence_after_sync();
-#pragma unroll
-        for (int c0 = 0; c0 < kN; c0 += kChunk) {
-          if (c0 >= live) break;
-          uint32_t s[kChunk];
+        uint32_t s[kHalf];
+        if (live > 8) {
           tc::ld_wait_x32(tmem + lanes + T::kS + kN * buf + c0, s);
-          if (c0 + kChunk >= live) {   // the last chunk: S^T is free
-            tc::fence_before_sync();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(bar(kBarSFree + buf));
-          }
-          float x[kChunk];
-          bool grew = false;
+        } else {
+          uint32_t few[8];
+          tc::ld_wait_x8(tmem + lanes + T::kS + kN * buf + c0, few);
 #pragma unroll
-          for (int r = 0; r < kChunk; r += 4) {
-            const float4 f = *reinterpret_cast<const float4*>(factors + c0 + r), o = *reinterpret_cast<const float4*>(off + c0 + r);
-            x[r] = __fmaf_rn(__uint_as_float(s[r]), f.x, o.x);
-            x[r + 1] = __fmaf_rn(__uint_as_float(s[r + 1]), f.y, o.y);
-            x[r + 2] = __fmaf_rn(__uint_as_float(s[r + 2]), f.z, o.z);
-            x[r + 3] = __fmaf_rn(__uint_as_float(s[r + 3]), f.w, o.w);
+          for (int r = 0; r < 8; ++r) s[r] = few[r];
+        }
+        tc::fence_before_sync();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(bar(kBarSFree + buf));
+          if (!both) mbar_arrive(bar(kBarSFree + buf));   // (the other group has no part in it)
+        }
+        if (tile >= 2) ok = wait_w(kBarO + buf, phase ^ 1) && ok;   // the last readers of this p
+        // eight rows' scores in units of log2, plus off
+        auto scores = [&](auto r_, float (&x)[8]) {
+          constexpr int r = decltype(r_)::value;
+#pragma unroll
+          for (int q = 0; q < 8; q += 4) {
+            const float4 f = *reinterpret_cast<const float4*>(factors + r + q), o = *reinterpret_cast<const float4*>(off + r + q);
+            const float2 u = f2unpack(fma2(f2pack(__uint_as_float(s[r + q]), __uint_as_float(s[r + q + 1])), f2pack(f.x, f.y), f2pack(o.x, o.y)));
+            const float2 v = f2unpack(fma2(f2pack(__uint_as_float(s[r + q + 2]), __uint_as_float(s[r + q + 3])), f2pack(f.z, f.w), f2pack(o.z, o.w)));
+            x[q] = u.x;
+            x[q + 1] = u.y;
+            x[q + 2] = v.x;
+            x[q + 3] = v.y;
           }
           if (hidden)
 #pragma unroll
-            for (int r = 0; r < kChunk; ++r)
-              if (c0 + r < from) x[r] = -INFINITY;
+            for (int q = 0; q < 8; ++q)
+              if (r + q < from) x[q] = -INFINITY;
+        };
+        uint8_t* p = smem + L::kP + buf * L::kPBytes + mine * 128;
+        // the rows' weights to shared memory; the largest exponent
+        auto weights = [&]() -> float {
+          float most = -INFINITY;
+          auto eight = [&](auto r_) {
+            constexpr int r = decltype(r_)::value;
+            if (r >= live) return;
+            float x[8];
+            scores(r_, x);
+            uint32_t w[4];
 #pragma unroll
-          for (int r = 0; r < kChunk; ++r) grew |= c0 + r < live && x[r] > kLift + kGrow;
-          const bool first = j == g.j0;
-          if (any_of_softmax(grew || !ok || first)) {
-            if (any_of_softmax(!ok)) {
-              left = true;
-              break;
+            for (int q = 0; q < 8; q += 2) {
+              most = fmaxf(most, fmaxf(x[q], x[q + 1]));
+              w[q / 2] = pack2<QMM_F16>(exp2_fast(x[q]), exp2_fast(x[q + 1]));
             }
-            // the rows' maxima of this tile: lane r of each warp gets row c0 + r's
-            float most = -INFINITY;
-#pragma unroll
-            for (int r = 0; r < kChunk; ++r) {
-              const float v = x[r] == x[r] ? x[r] : -INFINITY;
-              const uint32_t b = __float_as_uint(v), up = __reduce_max_sync(0xffffffffu, b & 0x80000000u ? ~b : b | 0x80000000u);
-              if (lane == r) most = __uint_as_float(up & 0x80000000u ? up & 0x7FFFFFFFu : ~up);
-            }
-            red[warp * kN + c0 + lane] = most;
-            any_of_softmax(false);
-#pragma unroll
-            for (int w = 0; w < kGroupWarps; ++w) most = fmaxf(most, red[w * kN + c0 + lane]);
-            // a row that sees no key of the segment's first tile sees none of the segment
-            const float was = off[c0 + lane];
-            const float now = most > -INFINITY && (first || most > kLift + kGrow) ? was - (most - kLift) : was;
-            const float moved = now - was, keep = exp2_fast(moved);
-            __syncwarp();
-            off[c0 + lane] = now;
-            __syncwarp();
-#pragma unroll
-            for (int r = 0; r < kChunk; ++r) {
-              x[r] += __shfl_sync(0xffffffffu, moved, r);
-              if (!first) sum[c0 + r] *= __shfl_sync(0xffffffffu, keep, r);
-            }
-            if (!first) {
-              // O^T, once the products of the tile before are in it
-              ok = wait_w(kBarO + (buf ^ 1), ((tile - 1) >> 1) & 1) && ok;
-              tc::fence_after_sync();
-              uint32_t o[kChunk];
-              tc::ld_wait_x32(tmem + lanes + T::kO + c0, o);
-#pragma unroll
-              for (int r = 0; r < kChunk; ++r)
-                o[r] = __float_as_uint(__uint_as_float(o[r]) * __shfl_sync(0xffffffffu, keep, r));
-              tc::st_x32(tmem + lanes + T::kO + c0, o);
-              tc::wait_st();
-            }
+            *reinterpret_cast<uint4*>(p + (((c0 + r) / 8) ^ (mine & 7)) * 16) = make_uint4(w[0], w[1], w[2], w[3]);
+          };
+          eight(std::integral_constant<int, 0>{});
+          eight(std::integral_constant<int, 8>{});
+          eight(std::integral_constant<int, 16>{});
+          eight(std::integral_constant<int, 24>{});
+          return most;
+        };
+        const bool grew = !first && weights() > kLift + kGrow;
+        if (any_here(grew || !ok || first)) {
+          if (any_here(!ok)) {
+            ok = false;
+            tile += g.j1 - j;
+            break;
           }
-          if (c0 == 0 && tile >= 2) ok = wait_w(kBarO + buf, phase ^ 1) && ok;   // the last readers of this p
-          uint8_t* p = smem + L::kP + buf * L::kPBytes + (mine / 64) * L::kPHalf;
-          const int at = mine % 64 * 2;
-#pragma unroll
-          for (int r = 0; r < kChunk; r += 8) {
-            if (c0 + r >= live) break;
+          // the rows' maxima of this tile: lane r of each warp gets row r's
+          float top = -INFINITY;
+          auto maxima = [&](auto r_) {
+            constexpr int r = decltype(r_)::value;
+            if (r >= live) return;
+            float x[8];
+            scores(r_, x);
 #pragma unroll
             for (int q = 0; q < 8; ++q) {
-              const float w = exp2_fast(x[r + q]);
-              sum[c0 + r + q] += w;
-              *reinterpret_cast<__half*>(p + (c0 + r + q) * 128 + (at ^ ((r + q) & 7) << 4)) = __float2half_rn(w);
+              const float v = x[q] == x[q] ? x[q] : -INFINITY;
+              const uint32_t b = __float_as_uint(v), up = __reduce_max_sync(0xffffffffu, b & 0x80000000u ? ~b : b | 0x80000000u);
+              if (lane == r + q) top = __uint_as_float(up & 0x80000000u ? up & 0x7FFFFFFFu : ~up);
             }
+          };
+          maxima(std::integral_constant<int, 0>{});
+          maxima(std::integral_constant<int, 8>{});
+          maxima(std::integral_constant<int, 16>{});
+          maxima(std::integral_constant<int, 24>{});
+          red[wg * kHalf + lane] = top;
+          any_here(false);
+#pragma unroll
+          for (int w = 0; w < kGroupWarps; ++w) top = fmaxf(top, red[w * kHalf + lane]);
+          // a row that sees no key of the group's first tile sees none of its later ones
+          const float was = off[lane];
+          const float now = top > -INFINITY && (first || top > kLift + kGrow) ? was - (top - kLift) : was;
+          const float keep = exp2_fast(now - was);
+          __syncwarp();
+          off[lane] = now;
+          __syncwarp();
+          if (!first) {
+            // O^T and l, once the products of the group's tile before are in them
+            ok = wait_w(kBarO + (both ? buf ^ 1 : buf), both ? ((tile - 1) >> 1) & 1 : phase ^ 1) && ok;
+            tc::fence_after_sync();
+#pragma unroll 1
+            for (int r0 = 0; r0 < live; r0 += 8) {
+              uint32_t o[8], l[8];
+              tc::ld_wait_x8(tmem + lanes + T::kO + kHalf * grp + r0, o);
+              tc::ld_wait_x8(tmem + lanes + T::kL + kHalf * grp + r0, l);
+#pragma unroll
+              for (int r = 0; r < 8; ++r) {
+                const float k = __shfl_sync(0xffffffffu, keep, r0 + r);
+                o[r] = __float_as_uint(__uint_as_float(o[r]) * k);
+                l[r] = __float_as_uint(__uint_as_float(l[r]) * k);
+              }
+              tc::st_x8(tmem + lanes + T::kO + kHalf * grp + r0, o);
+              tc::st_x8(tmem + lanes + T::kL + kHalf * grp + r0, l);
+            }
+            tc::wait_st();
           }
+          weights();
         }
+        first = false;
         fence_proxy_async_smem();
         tc::fence_before_sync();
         __syncwarp();
-        if (lane == 0) mbar_arrive(bar(kBarP + buf));
+        if (lane == 0) {
+          mbar_arrive(bar(kBarP + buf));
+          if (!both) mbar_arrive(bar(kBarP + buf));
+        }
       }
-      if (left) break;
 
       // ---- the segment's sums to the workspace
-      ok = wait_w(kBarO + ((tile - 1) & 1), ((tile - 1) >> 1) & 1) && ok;
-      if (any_of_softmax(!ok)) break;
+      if (ok) ok = wait_w(kBarO + ((tile - 1) & 1), ((tile - 1) >> 1) & 1);   // (and with these products all before)
+      if (any_of(!ok, 3, 64 * kGroupWarps)) break;
       tc::fence_after_sync();
       const bool inside = g.j0 > 0;   // not the first segment of its group: the CTA's own record
       auto record = [&](int r) -> int64_t {
@@ -605,41 +663,50 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fp4_kernel(const __grid_cons
                       : ((int64_t)(g.own ? a.T : 0) + g.t0 + r / G) * a.Hq + (int64_t)g.h * G + r % G;
       };
       float* out = inside ? P.o_cta : P.o_rows;
-#pragma unroll
-      for (int c0 = 0; c0 < kN; c0 += 32) {
-        if (c0 >= live) break;
-        float part[32];
-#pragma unroll
-        for (int r = 0; r < 32; ++r) part[r] = sum[c0 + r];
-        butterfly_reduce<32>(part, lane);
-        red[warp * kN + c0 + lane] = part[0];
-      }
-      any_of_softmax(false);
-      if (mine < live) {
-        const float all = (red[mine] + red[kN + mine]) + (red[2 * kN + mine] + red[3 * kN + mine]);
-        const uint32_t per = (uint32_t)min(M.piece.per, (int64_t)0x7fffffff);
-        const uint32_t others = g.rest > 0 ? ((uint32_t)g.rest + per - 1) / per : 0;
-        const uint32_t odd = *reinterpret_cast<volatile uint32_t*>(&M.odd[segs & 7]) == segs;
-        (inside ? P.s_cta : P.s_rows)[record(mine)] =
-            RowStat{all == 0.0f ? -INFINITY : -off[mine], all, odd, others << 16 | (blockIdx.x + 1)};
-      }
       // O^T: this thread's value of every row, at the place where the combine launch looks for it (column_of)
-      if (mine < D) {
-        const int place = (mine & ~31) + 8 * (mine >> 1 & 3) + 2 * (mine >> 3 & 3) + (mine & 1);
+      const int place = (mine & ~31) + 8 * (mine >> 1 & 3) + 2 * (mine >> 3 & 3) + (mine & 1);
+      const float* offs = reinterpret_cast<const float*>(smem + L::kOff);
+      // a group without a tile has no sums of its own
+      const bool has0 = both || g.j1 - g.j0 > 1 || ((tile - 1) & 1) == 0, has1 = both || g.j1 - g.j0 > 1 || ((tile - 1) & 1) == 1;
+      // eight rows: of the group's; or, of both groups' sums, the group's half of them
+#pragma unroll 1
+      for (int r0 = both ? 0 : 16 * grp; r0 < min(live, both ? kHalf : 16 * grp + 16); r0 += 8) {
+        uint32_t o[8], l[8], o1[8], l1[8];
+        const uint32_t at = (both ? kHalf * grp : 0) + r0;
+        tc::ld_wait_x8(tmem + lanes + T::kL + at, l);
+        tc::ld_wait_x8(tmem + lanes + T::kO + at, o);
+        if (!both) {
+          tc::ld_wait_x8(tmem + lanes + T::kL + kHalf + r0, l1);
+          tc::ld_wait_x8(tmem + lanes + T::kO + kHalf + r0, o1);
+        }
+        RowStat mine_of{};
 #pragma unroll
-        for (int c0 = 0; c0 < kN; c0 += 32) {
-          if (c0 >= live) break;
-          uint32_t o[32];
-          tc::ld_wait_x32(tmem + lanes + T::kO + c0, o);
-#pragma unroll
-          for (int r = 0; r < 32; ++r)
-            if (c0 + r < live) out[record(c0 + r) * D + place] = __uint_as_float(o[r]);
+        for (int r = 0; r < 8; ++r) {
+          float v = __uint_as_float(o[r]), all = has0 ? __uint_as_float(l[r]) : 0.0f;
+          float top = -offs[(both ? grp : 0) * kGroupWarps * kHalf + r0 + r];
+          if (!both) {
+            const float all1 = has1 ? __uint_as_float(l1[r]) : 0.0f, top1 = -offs[kGroupWarps * kHalf + r0 + r];
+            const float best = all == 0.0f ? top1 : all1 == 0.0f ? top : fmaxf(top, top1);
+            const float f0 = all == 0.0f ? 0.0f : exp2_fast(top - best), f1 = all1 == 0.0f ? 0.0f : exp2_fast(top1 - best);
+            v = (f0 != 0.0f ? v * f0 : 0.0f) + (f1 != 0.0f ? __uint_as_float(o1[r]) * f1 : 0.0f);
+            all = all * f0 + all1 * f1;
+            top = best;
+          }
+          if (r0 + r < live && mine < D) out[record(c0 + r0 + r) * D + place] = v;
+          if (lane == r) mine_of = RowStat{all == 0.0f ? -INFINITY : top, all, 0u, 0u};
+        }
+        if (wg == 0 && lane < 8 && r0 + lane < live) {
+          const uint32_t per = (uint32_t)min(M.piece.per, (int64_t)0x7fffffff);
+          const uint32_t others = g.rest > 0 ? ((uint32_t)g.rest + per - 1) / per : 0;
+          mine_of.odd = *reinterpret_cast<volatile uint32_t*>(&M.odd[segs & 7]) == segs;
+          mine_of.rest = others << 16 | (blockIdx.x + 1);
+          (inside ? P.s_cta : P.s_rows)[record(c0 + r0 + lane)] = mine_of;
         }
       }
       tc::fence_before_sync();
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(kBarOFree));
-      any_of_softmax(false);   // (red is written again behind this)
+      any_of(false, 3, 64 * kGroupWarps);   // (off is written again behind this)
     }
   }
 
