@@ -9,7 +9,8 @@
 //     S^T = K Q^T        tcgen05, K (128 keys x D) from tensor memory, where four warps put it, a thread a key
 //     p = 2^(c S + off)  a thread per key, S^T from tensor memory, c = scale k_scale log2 e over the row's power of two
 //     O^T += V^T p^T     tcgen05, V and p^T (both MN-major) from shared memory; four more warps write V
-//     l += 1 p^T         tcgen05, ones from tensor memory: the rows' sums of weights, of the rounded ones as in O^T
+//     l += 1 p^T         tcgen05, ones from tensor memory: the rows' sums of weights (of up to eight rows the softmax adds
+//                        them up itself: these products take as long as half of those before)
 // so few rows cost little, the exponentials of a row are spread over 128 threads, and no 128-row tile of queries
 // is read again for every tile.  Two groups of softmax warps have half of a block's rows each, or, where a block has no
 // more than one of them takes, the key tiles in turn, with sums of their own that are joined at a segment's end.
@@ -42,8 +43,9 @@ constexpr int kTile = 128;           // keys of a key tile
 constexpr int kLead = 3;             // units of a group besides its key tiles
 constexpr int kN = 64;               // rows of a block
 constexpr int kHalf = kN / 2;        // rows of a softmax group
-// warps: 0-3 and 4-7 softmax, 8 copies, 9 tensor cores, 10 queries, 12-15 keys and 16-19 values to fp16
-constexpr int kLoadWarp = 8, kMmaWarp = 9, kQWarp = 10, kKeyWarp = 12, kValueWarp = 16;
+constexpr int kFew = 8;              // rows whose weights a softmax thread adds up itself
+// warps: 0-3 and 4-7 softmax, 8 copies, 9 and 11 tensor cores, 10 queries, 12-15 keys and 16-19 values to fp16
+constexpr int kLoadWarp = 8, kScoreWarp = 9, kQWarp = 10, kSumWarp = 11, kKeyWarp = 12, kValueWarp = 16;
 constexpr int kThreads = 20 * 32, kGroupWarps = 4;
 constexpr uint32_t kTmemCols = 512;
 constexpr int kKeyBufs = 3;          // tiles of keys in tensor memory
@@ -87,7 +89,7 @@ struct Tmem {
 enum : int {
   kBarPackFull = 0, kBarPackEmpty = 10, kBarKeyFull = 20, kBarKeyEmpty = 24 /* 20 + and 24 + buffer */, kBarValueFull = 28, kBarValueEmpty = 31,
   kBarS = 34, kBarSFree = 36, kBarP = 38, kBarO = 40 /* products of a tile's values are done */, kBarQFull = 42,
-  kBarQEmpty = 44, kBarOFree = 46, kBarDrain = 47, kBars = 48
+  kBarQEmpty = 44, kBarOFree = 46, kBarDrain = 47 /* and 48 */, kBars = 49
 };
 
 struct Misc {
@@ -135,12 +137,18 @@ __device__ __forceinline__ bool any_of(bool mine, int id, int threads) {
 // The wait for a phase that has not completed yet (out of line: the roles' loops stay short).
 __device__ __noinline__ bool wait_slowly(uint32_t bar, uint32_t parity, uint32_t polls, uint32_t ns,
                                          volatile int* abort_flag) {
+  if (mbar_wait(bar, parity, 1, ns)) return true;
   if (*abort_flag) return false;
   if (mbar_wait(bar, parity, polls, ns)) return true;
   atomicOr(&g_status, kErrWaitTimeout);
   *abort_flag = 1;
   return false;
 }
+
+// The walk's next segment (out of line, and its state in memory: the roles' loops fit the instruction cache and
+// their registers).
+using Walk = Walker<kTile, kLead>;
+__device__ __noinline__ bool next_of(Walk& walk, const Common& P, Seg& g) { return walk.next(P, g); }
 
 // fp16 pairs of a block's eight bytes of codes and its scale (both halves), to h[AT] and on.
 template <int AT, int N>
@@ -180,7 +188,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fp4_kernel(const __grid_cons
     M.abort = 0;
     for (int k = 0; k < 8; ++k) M.odd[k] = 0;
   }
-  if (warp == kMmaWarp) {
+  if (warp == kScoreWarp) {
     tc::tmem_alloc(smem_addr(&M.tmem), kTmemCols);
     tc::tmem_relinquish();
   }
@@ -208,13 +216,12 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fp4_kernel(const __grid_cons
   // rule, and a suspended wait takes 200 clocks to see it.)
   auto wait = [&](int k, uint32_t parity) -> bool {
     if (mbar_try(bar(k), parity)) return true;
-    if (mbar_wait(bar(k), parity, 1, P.wait_ns ? P.wait_ns : kSuspendNs)) return true;
     return wait_slowly(bar(k), parity, P.wait_polls ? P.wait_polls : kWaitLimit, P.wait_ns ? P.wait_ns : kSuspendNs,
                        abort_flag);
   };
   auto wait_w = [&](int k, uint32_t parity) -> bool { return __all_sync(0xffffffffu, wait(k, parity)); };
 
-  Walker<kTile, kLead> walk;
+  Walk walk;
   walk.start(P, M.piece);
   Seg g;
 
@@ -250,7 +257,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fp4_kernel(const __grid_cons
         bulk_copy(smem_addr(smem) + L::kPack + st * L::kPackBytes + dst, static_cast<const uint8_t*>(cache) + at,
                   per_run * my_bytes, bar(kBarPackFull + st));
     };
-    while (ok && walk.next(P, g)) {
+    while (ok && next_of(walk, P, g)) {
       int64_t at = from(g, g.j0), next = g.j0 + 1 < g.j1 ? from(g, g.j0 + 1) : -1;
       for (int j = g.j0; ok && j < g.j1; ++j) {
         const int64_t later = j + 2 < g.j1 ? from(g, j + 2) : -1;
@@ -272,7 +279,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fp4_kernel(const __grid_cons
     float* factors = reinterpret_cast<float*>(smem + L::kFactors);
     uint32_t pos = 0;
     bool ok = true;
-    for (; ok && walk.next(P, g); ++pos) {
+    for (; ok && next_of(walk, P, g); ++pos) {
       const uint32_t st = pos & 1, use = pos >> 1;
       ok = use == 0 || wait_w(kBarQEmpty + st, (use - 1) & 1);
       if (!ok) break;
@@ -321,84 +328,75 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fp4_kernel(const __grid_cons
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(kBarQFull + st));
     }
-  } else if (warp == kMmaWarp) {
-    // ------------------------------------------------------------------ tensor cores
-    // The scores of a tile are issued ahead of the values of the one before it.
+  } else if (warp == kScoreWarp) {
+    // ------------------------------------------------------------------ tensor cores, scores
+    // (A warp for each product: issue waits for the tensor cores, and one warp's waits for its operands cost the other's
+    // products nothing.)
     if (elect_one()) {
       constexpr uint32_t kIdBoth = tc::idesc_16_f32(128, kN, false, false), kIdHalf = tc::idesc_16_f32(128, kHalf, false, false);
-      constexpr uint32_t kMnMajorA = 1u << 15, kMnMajorB = 1u << 16;   // V and p
       const uint64_t dq = tc::smem_desc_sw128(smem_addr(smem + L::kQ), 16, 1024);
-      const uint64_t dp = tc::smem_desc_sw128(smem_addr(smem + L::kP), 16, 1024);
-      // D = 64: O^T has 128 lanes all the same; the upper ones are products with other keys, and nobody reads them
-      const uint64_t dv = tc::smem_desc_sw128(smem_addr(smem + L::kV), D == 128 ? L::kVHalf : L::kVHalf / 2, 1024);
-      struct Pass {
-        Walker<kTile, kLead> w;
-        int left = 0, done = 0;       // tiles of the segment left, and gone
-        bool both = false;            // more rows than one group has
-        uint32_t tile = 0, seg = 0;   // the next one; segments begun
-      } qk, pv;
-      qk.w = pv.w = walk;
+      uint32_t tile = 0, segs = 0;
       bool ok = true;
-      auto begin = [&](Pass& p) -> bool {   // whether there is another tile
-        if (p.left > 0) return true;
-        if (!p.w.next(P, g)) return false;
-        p.left = g.j1 - g.j0;
-        p.done = 0;
-        p.both = g.rows * G > kHalf;
-        ++p.seg;
-        return true;
-      };
-      auto scores = [&]() -> bool {
-        if (!begin(qk)) return false;
-        const bool fresh = qk.done == 0;
-        const uint32_t slot = (qk.seg - 1) & 1, kb = qk.tile % kKeyBufs, buf = qk.tile & 1;
-        if (fresh) ok = ok && wait(kBarQFull + slot, ((qk.seg - 1) >> 1) & 1);
-        ok = ok && wait(kBarKeyFull + kb, (qk.tile / kKeyBufs) & 1);
-        if (qk.tile >= 2) ok = ok && wait(kBarSFree + buf, ((qk.tile >> 1) - 1) & 1);
-        if (!ok) return false;
-        tc::fence_after_sync();
+      while (ok && next_of(walk, P, g)) {
+        const uint32_t slot = segs & 1, id = g.rows * G > kHalf ? kIdBoth : kIdHalf;
+        ok = wait(kBarQFull + slot, (segs >> 1) & 1);
+        ++segs;
+        for (int left = g.j1 - g.j0; ok && left > 0; --left, ++tile) {
+          const uint32_t kb = tile % kKeyBufs, buf = tile & 1;
+          ok = wait(kBarKeyFull + kb, (tile / kKeyBufs) & 1);
+          if (tile >= 2) ok = ok && wait(kBarSFree + buf, ((tile >> 1) - 1) & 1);
+          if (!ok) break;
+          tc::fence_after_sync();
 #pragma unroll
-        for (int k = 0; k < D / 64; ++k)   // 64 values of the head: 4 MMAs, 8 columns and 32 bytes of each row further
-          tc::mma_f16_ts_x4(tmem + T::kS + kN * buf, tmem + kb * (D / 2) + 32 * k,
-                            dq + ((slot * L::kQBytes + k * L::kQHalf) >> 4), 2, qk.both ? kIdBoth : kIdHalf, k > 0);
-        tc::commit(bar(kBarS + buf));
-        tc::commit(bar(kBarKeyEmpty + kb));
-        if (qk.left == 1) tc::commit(bar(kBarQEmpty + slot));
-        --qk.left;
-        ++qk.done;
-        ++qk.tile;
-        return true;
-      };
-      auto values = [&]() -> bool {
-        if (!begin(pv)) return false;
-        const uint32_t vb = pv.tile % kVB, buf = pv.tile & 1;
-        const bool fresh = pv.done < (pv.both ? 1 : 2);   // the first of its sums
-        if (pv.done == 0 && pv.seg > 1) ok = ok && wait(kBarOFree, pv.seg & 1);   // (segment s ends its phase s)
-        ok = ok && wait(kBarValueFull + vb, (pv.tile / kVB) & 1) && wait(kBarP + buf, (pv.tile >> 1) & 1);
-        if (!ok) return false;
-        tc::fence_after_sync();
-        const uint32_t at = pv.both ? 0 : kHalf * buf, id = (pv.both ? kIdBoth : kIdHalf) | kMnMajorB;
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {   // 64 keys: 4 MMAs of 16 rows of V and of p
-          const uint64_t p = dp + ((buf * L::kPBytes + k * 64 * 128) >> 4);
-          mma_ss_x4(tmem + T::kO + at, dv + ((vb * L::kVBytes + k * 64 * 128) >> 4), 128, p, 128, id | kMnMajorA, !fresh || k > 0);
-          tc::mma_f16_ts_x4(tmem + T::kL + at, tmem + T::kOnes, p, 128, id, !fresh || k > 0);
+          for (int k = 0; k < D / 64; ++k)   // 64 values of the head: 4 MMAs, 8 columns and 32 bytes of each row further
+            tc::mma_f16_ts_x4(tmem + T::kS + kN * buf, tmem + kb * (D / 2) + 32 * k,
+                              dq + ((slot * L::kQBytes + k * L::kQHalf) >> 4), 2, id, k > 0);
+          tc::commit(bar(kBarS + buf));
+          tc::commit(bar(kBarKeyEmpty + kb));
+          if (left == 1) tc::commit(bar(kBarQEmpty + slot));
         }
-        tc::commit(bar(kBarO + buf));
-        tc::commit(bar(kBarValueEmpty + vb));
-        --pv.left;
-        ++pv.done;
-        ++pv.tile;
-        return true;
-      };
-      scores();
-      while (ok) {
-        scores();
-        if (!ok || !values()) break;
       }
       // no tensor-core operation of this CTA is in flight when it ends
       tc::commit(bar(kBarDrain));
       mbar_wait(bar(kBarDrain), 0, kWaitLimit);
+    }
+    __syncwarp();
+  } else if (warp == kSumWarp) {
+    // ------------------------------------------------------------------ tensor cores, weighted sums
+    if (elect_one()) {
+      constexpr uint32_t kMnMajorA = 1u << 15, kMnMajorB = 1u << 16;   // V and p
+      constexpr uint32_t kIdBoth = tc::idesc_16_f32(128, kN, false, false) | kMnMajorB;
+      constexpr uint32_t kIdHalf = tc::idesc_16_f32(128, kHalf, false, false) | kMnMajorB;
+      const uint64_t dp = tc::smem_desc_sw128(smem_addr(smem + L::kP), 16, 1024);
+      // D = 64: O^T has 128 lanes all the same; the upper ones are products with other keys, and nobody reads them
+      const uint64_t dv = tc::smem_desc_sw128(smem_addr(smem + L::kV), D == 128 ? L::kVHalf : L::kVHalf / 2, 1024);
+      uint32_t tile = 0, segs = 0;
+      bool ok = true;
+      while (ok && next_of(walk, P, g)) {
+        const bool both = g.rows * G > kHalf, sums = g.rows * G > kFew;
+        const uint32_t id = both ? kIdBoth : kIdHalf;
+        if (segs > 0) ok = wait(kBarOFree, (segs - 1) & 1);
+        ++segs;
+        const int n = g.j1 - g.j0;
+        for (int i = 0; ok && i < n; ++i, ++tile) {
+          const uint32_t vb = tile % kVB, buf = tile & 1, at = both ? 0 : kHalf * buf;
+          const bool fresh = i < (both ? 1 : 2);   // the first of its sums
+          ok = wait(kBarValueFull + vb, (tile / kVB) & 1) && wait(kBarP + buf, (tile >> 1) & 1);
+          if (!ok) break;
+          tc::fence_after_sync();
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {   // 64 keys: 4 MMAs of 16 rows of V and of p
+            const uint64_t p = dp + ((buf * L::kPBytes + k * 64 * 128) >> 4);
+            mma_ss_x4(tmem + T::kO + at, dv + ((vb * L::kVBytes + k * 64 * 128) >> 4), 128, p, 128, id | kMnMajorA,
+                      !fresh || k > 0);
+            if (sums) tc::mma_f16_ts_x4(tmem + T::kL + at, tmem + T::kOnes, p, 128, id, !fresh || k > 0);
+          }
+          tc::commit(bar(kBarO + buf));
+          tc::commit(bar(kBarValueEmpty + vb));
+        }
+      }
+      tc::commit(bar(kBarDrain + 1));
+      mbar_wait(bar(kBarDrain + 1), 0, kWaitLimit);
     }
     __syncwarp();
   } else if (warp >= kKeyWarp && warp < kValueWarp) {
@@ -409,8 +407,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fp4_kernel(const __grid_cons
     const uint32_t lanes = (uint32_t)(warp - kKeyWarp) << 21;   // first TMEM lane << 16
     uint32_t tile = 0;
     bool ok = true;
-    while (ok && walk.next(P, g)) {
-      for (int j = g.j0; j < g.j1; ++j, ++tile) {
+    while (ok && next_of(walk, P, g)) {
+      const int j1 = g.j1;
+      for (int j = g.j0; j < j1; ++j, ++tile) {
         const uint32_t from = 2 * tile % kPacks, kb = tile % kKeyBufs;
         ok = wait(kBarPackFull + from, (2 * tile / kPacks) & 1) &&
              (tile < kKeyBufs || wait(kBarKeyEmpty + kb, (tile / kKeyBufs - 1) & 1));
@@ -450,10 +449,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fp4_kernel(const __grid_cons
     const int me = (warp - kValueWarp) * 32 + lane;
     uint32_t tile = 0, segs = 0;
     bool ok = true;
-    while (ok && walk.next(P, g)) {
-      const int clean_from = g.own ? clampi(g.first_keys, 0, g.keys) : g.keys;
+    while (ok && next_of(walk, P, g)) {
+      const int j1 = g.j1, keys = g.keys, clean_from = g.own ? clampi(g.first_keys, 0, keys) : keys;
       ++segs;
-      for (int j = g.j0; j < g.j1; ++j, ++tile) {
+      for (int j = g.j0; j < j1; ++j, ++tile) {
         const uint32_t from = (2 * tile + 1) % kPacks, vb = tile % kVB;
         ok = wait(kBarPackFull + from, ((2 * tile + 1) / kPacks) & 1) &&
              (tile < kVB || wait(kBarValueEmpty + vb, (tile / kVB - 1) & 1));
@@ -476,9 +475,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fp4_kernel(const __grid_cons
 #pragma unroll
           for (int u = 0; u < kUnits; ++u) {
             const int key = base + key_of(u);
-            const bool nan = (scale[u] & 0x7Fu) == kv4::kScaleNaN && key >= clean_from && key < g.keys;
+            const bool nan = (scale[u] & 0x7Fu) == kv4::kScaleNaN && key >= clean_from && key < keys;
             odd |= nan;
-            if (nan || key >= g.keys) scale[u] = 0;
+            if (nan || key >= keys) scale[u] = 0;
           }
           if (odd) *reinterpret_cast<volatile uint32_t*>(&M.odd[segs & 7]) = segs;
         }
@@ -510,21 +509,23 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fp4_kernel(const __grid_cons
     auto any_here = [&](bool x) { return any_of(x, 1 + grp, 32 * kGroupWarps); };
     uint32_t tile = 0, segs = 0;
     bool ok = true;
-    while (walk.next(P, g)) {
+    while (next_of(walk, P, g)) {
       const int rows = g.rows * G;
       const bool both = rows > kHalf;
       const int c0 = both ? kHalf * grp : 0, live = both ? clampi(rows - c0, 0, kHalf) : rows;   // the group's rows
       const float* factors = reinterpret_cast<const float*>(smem + L::kFactors) + segs % kFactorTiles * kN + c0;
+      const int j1 = g.j1, keys = g.keys, first_keys = g.first_keys;
       ++segs;
       off[lane] = 0.0f;
       __syncwarp();
-      bool first = true;
-      for (int j = g.j0; j < g.j1; ++j, ++tile) {
+      float sum[kFew] = {};   // of this thread's weights, where there are few rows
+      bool first = true, leave = false;   // leave: the whole group knows that a wait gave up
+      for (int j = g.j0; j < j1; ++j, ++tile) {
         const uint32_t buf = tile & 1, phase = (tile >> 1) & 1;
         if (!both && (int)buf != grp) continue;
         const int key = j * kTile + mine;
         // the first of the group's rows that sees this thread's key
-        const int from = (key >= g.keys ? kN : g.own ? max(0, key - g.first_keys + 1) * G : 0) - c0;
+        const int from = (key >= keys ? kN : max(0, key - first_keys + 1) * G) - c0;
         const bool hidden = __any_sync(0xffffffffu, from > 0);
         ok = wait_w(kBarS + buf, phase) && ok;
         tc::fence_after_sync();
@@ -563,87 +564,104 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fp4_kernel(const __grid_cons
               if (r + q < from) x[q] = -INFINITY;
         };
         uint8_t* p = smem + L::kP + buf * L::kPBytes + mine * 128;
-        // the rows' weights to shared memory; the largest exponent
-        auto weights = [&]() -> float {
-          float most = -INFINITY;
+        // N rows' weights to shared memory (those behind the last row do no harm); the largest exponent
+        float add[kFew];
+        auto weights_of = [&](auto n_) -> float {
+          constexpr int N = decltype(n_)::value;
+          float most[2] = {-INFINITY, -INFINITY};
           auto eight = [&](auto r_) {
             constexpr int r = decltype(r_)::value;
-            if (r >= live) return;
-            float x[8];
-            scores(r_, x);
-            uint32_t w[4];
+            if constexpr (r < N) {
+              float x[8];
+              scores(r_, x);
+              uint32_t w[4];
 #pragma unroll
-            for (int q = 0; q < 8; q += 2) {
-              most = fmaxf(most, fmaxf(x[q], x[q + 1]));
-              w[q / 2] = pack2<QMM_F16>(exp2_fast(x[q]), exp2_fast(x[q + 1]));
+              for (int q = 0; q < 8; q += 2) {
+                most[q / 2 % 2] = fmaxf(most[q / 2 % 2], fmaxf(x[q], x[q + 1]));
+                const float e0 = exp2_fast(x[q]), e1 = exp2_fast(x[q + 1]);
+                w[q / 2] = pack2<QMM_F16>(e0, e1);
+                if constexpr (N == kFew) {
+                  add[q] = e0;
+                  add[q + 1] = e1;
+                }
+              }
+              *reinterpret_cast<uint4*>(p + (((c0 + r) / 8) ^ (mine & 7)) * 16) = make_uint4(w[0], w[1], w[2], w[3]);
             }
-            *reinterpret_cast<uint4*>(p + (((c0 + r) / 8) ^ (mine & 7)) * 16) = make_uint4(w[0], w[1], w[2], w[3]);
           };
           eight(std::integral_constant<int, 0>{});
           eight(std::integral_constant<int, 8>{});
           eight(std::integral_constant<int, 16>{});
           eight(std::integral_constant<int, 24>{});
-          return most;
+          return fmaxf(most[0], most[1]);
         };
-        const bool grew = !first && weights() > kLift + kGrow;
-        if (any_here(grew || !ok || first)) {
-          if (any_here(!ok)) {
-            ok = false;
-            tile += g.j1 - j;
-            break;
-          }
-          // the rows' maxima of this tile: lane r of each warp gets row r's
-          float top = -INFINITY;
-          auto maxima = [&](auto r_) {
-            constexpr int r = decltype(r_)::value;
-            if (r >= live) return;
-            float x[8];
-            scores(r_, x);
+        auto weights = [&]() -> float {
+          if (live > kFew) return weights_of(std::integral_constant<int, 32>{});
+          return weights_of(std::integral_constant<int, kFew>{});
+        };
+        for (bool set = first;; set = true) {   // twice, where off has to move before the weights hold
+          if (set) {
+            leave = any_here(!ok);
+            if (leave) break;
+            // the rows' maxima of this tile: lane r of each warp gets row r's
+            float top = -INFINITY;
+            auto maxima = [&](auto r_) {
+              constexpr int r = decltype(r_)::value;
+              if (r >= live) return;
+              float x[8];
+              scores(r_, x);
 #pragma unroll
-            for (int q = 0; q < 8; ++q) {
-              const float v = x[q] == x[q] ? x[q] : -INFINITY;
-              const uint32_t b = __float_as_uint(v), up = __reduce_max_sync(0xffffffffu, b & 0x80000000u ? ~b : b | 0x80000000u);
-              if (lane == r + q) top = __uint_as_float(up & 0x80000000u ? up & 0x7FFFFFFFu : ~up);
-            }
-          };
-          maxima(std::integral_constant<int, 0>{});
-          maxima(std::integral_constant<int, 8>{});
-          maxima(std::integral_constant<int, 16>{});
-          maxima(std::integral_constant<int, 24>{});
-          red[wg * kHalf + lane] = top;
-          any_here(false);
-#pragma unroll
-          for (int w = 0; w < kGroupWarps; ++w) top = fmaxf(top, red[w * kHalf + lane]);
-          // a row that sees no key of the group's first tile sees none of its later ones
-          const float was = off[lane];
-          const float now = top > -INFINITY && (first || top > kLift + kGrow) ? was - (top - kLift) : was;
-          const float keep = exp2_fast(now - was);
-          __syncwarp();
-          off[lane] = now;
-          __syncwarp();
-          if (!first) {
-            // O^T and l, once the products of the group's tile before are in them
-            ok = wait_w(kBarO + (both ? buf ^ 1 : buf), both ? ((tile - 1) >> 1) & 1 : phase ^ 1) && ok;
-            tc::fence_after_sync();
-#pragma unroll 1
-            for (int r0 = 0; r0 < live; r0 += 8) {
-              uint32_t o[8], l[8];
-              tc::ld_wait_x8(tmem + lanes + T::kO + kHalf * grp + r0, o);
-              tc::ld_wait_x8(tmem + lanes + T::kL + kHalf * grp + r0, l);
-#pragma unroll
-              for (int r = 0; r < 8; ++r) {
-                const float k = __shfl_sync(0xffffffffu, keep, r0 + r);
-                o[r] = __float_as_uint(__uint_as_float(o[r]) * k);
-                l[r] = __float_as_uint(__uint_as_float(l[r]) * k);
+              for (int q = 0; q < 8; ++q) {
+                const float v = x[q] == x[q] ? x[q] : -INFINITY;
+                const uint32_t b = __float_as_uint(v), up = __reduce_max_sync(0xffffffffu, b & 0x80000000u ? ~b : b | 0x80000000u);
+                if (lane == r + q) top = __uint_as_float(up & 0x80000000u ? up & 0x7FFFFFFFu : ~up);
               }
-              tc::st_x8(tmem + lanes + T::kO + kHalf * grp + r0, o);
-              tc::st_x8(tmem + lanes + T::kL + kHalf * grp + r0, l);
+            };
+            maxima(std::integral_constant<int, 0>{});
+            maxima(std::integral_constant<int, 8>{});
+            maxima(std::integral_constant<int, 16>{});
+            maxima(std::integral_constant<int, 24>{});
+            red[wg * kHalf + lane] = top;
+            any_here(false);
+#pragma unroll
+            for (int w = 0; w < kGroupWarps; ++w) top = fmaxf(top, red[w * kHalf + lane]);
+            // a row that sees no key of the group's first tile sees none of its later ones
+            const float was = off[lane];
+            const float now = top > -INFINITY && (first || top > kLift + kGrow) ? was - (top - kLift) : was;
+            const float keep = exp2_fast(now - was);
+            __syncwarp();
+            off[lane] = now;
+            __syncwarp();
+            if (!first) {
+              // O^T and l, once the products of the group's tile before are in them
+              ok = wait_w(kBarO + (both ? buf ^ 1 : buf), both ? ((tile - 1) >> 1) & 1 : phase ^ 1) && ok;
+              tc::fence_after_sync();
+#pragma unroll 1
+              for (int r0 = 0; r0 < live; r0 += 8) {
+                uint32_t o[8], l[8];
+                tc::ld_wait_x8(tmem + lanes + T::kO + kHalf * grp + r0, o);
+                tc::ld_wait_x8(tmem + lanes + T::kL + kHalf * grp + r0, l);
+#pragma unroll
+                for (int r = 0; r < 8; ++r) {
+                  const float k = __shfl_sync(0xffffffffu, keep, r0 + r);
+                  o[r] = __float_as_uint(__uint_as_float(o[r]) * k);
+                  l[r] = __float_as_uint(__uint_as_float(l[r]) * k);
+                }
+                tc::st_x8(tmem + lanes + T::kO + kHalf * grp + r0, o);
+                tc::st_x8(tmem + lanes + T::kL + kHalf * grp + r0, l);
+              }
+              tc::wait_st();
+#pragma unroll
+              for (int r = 0; r < kFew; ++r) sum[r] *= __shfl_sync(0xffffffffu, keep, r);
             }
-            tc::wait_st();
           }
-          weights();
+          const float most = weights();
+          if (set || !any_here(most > kLift + kGrow || !ok)) break;
         }
+        if (leave) break;
         first = false;
+        if (rows <= kFew)
+#pragma unroll
+          for (int r = 0; r < kFew; ++r) sum[r] += add[r];
         fence_proxy_async_smem();
         tc::fence_before_sync();
         __syncwarp();
@@ -654,14 +672,25 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fp4_kernel(const __grid_cons
       }
 
       // ---- the segment's sums to the workspace
-      if (ok) ok = wait_w(kBarO + ((tile - 1) & 1), ((tile - 1) >> 1) & 1);   // (and with these products all before)
-      if (any_of(!ok, 3, 64 * kGroupWarps)) break;
+      if (!leave) ok = wait_w(kBarO + ((tile - 1) & 1), ((tile - 1) >> 1) & 1) && ok;   // (and with these products all before)
+      if (rows <= kFew) {
+        float own = 0.0f;   // lane r: row r's over the warp
+#pragma unroll
+        for (int r = 0; r < kFew; ++r) {
+          float v = sum[r];
+#pragma unroll
+          for (int o = 16; o >= 1; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+          if (lane == r) own = v;
+        }
+        red[wg * kHalf + lane] = own;
+      }
+      if (any_of(!ok || leave, 3, 64 * kGroupWarps)) break;
       tc::fence_after_sync();
       const bool inside = g.j0 > 0;   // not the first segment of its group: the CTA's own record
-      auto record = [&](int r) -> int64_t {
-        return inside ? (int64_t)blockIdx.x * 2 * kRows + r
-                      : ((int64_t)(g.own ? a.T : 0) + g.t0 + r / G) * a.Hq + (int64_t)g.h * G + r % G;
-      };
+      // lane r: where the record of row r of the group lies
+      const int row = c0 + lane, tok = (int)((uint32_t)row / (uint32_t)G);
+      const int64_t record = inside ? (int64_t)blockIdx.x * 2 * kRows + row
+                                    : ((int64_t)(g.own ? a.T : 0) + g.t0 + tok) * a.Hq + (int64_t)g.h * G + row - tok * G;
       float* out = inside ? P.o_cta : P.o_rows;
       // O^T: this thread's value of every row, at the place where the combine launch looks for it (column_of)
       const int place = (mine & ~31) + 8 * (mine >> 1 & 3) + 2 * (mine >> 3 & 3) + (mine & 1);
@@ -679,6 +708,17 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fp4_kernel(const __grid_cons
           tc::ld_wait_x8(tmem + lanes + T::kL + kHalf + r0, l1);
           tc::ld_wait_x8(tmem + lanes + T::kO + kHalf + r0, o1);
         }
+        if (rows <= kFew) {
+          const float* reds = reinterpret_cast<const float*>(smem + L::kRed);
+#pragma unroll
+          for (int r = 0; r < kFew; ++r) {
+            auto sum_of = [&](const float* x) {
+              return __float_as_uint((x[r] + x[kHalf + r]) + (x[2 * kHalf + r] + x[3 * kHalf + r]));
+            };
+            l[r] = sum_of(reds);
+            l1[r] = sum_of(reds + kGroupWarps * kHalf);
+          }
+        }
         RowStat mine_of{};
 #pragma unroll
         for (int r = 0; r < 8; ++r) {
@@ -692,28 +732,30 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fp4_kernel(const __grid_cons
             all = all * f0 + all1 * f1;
             top = best;
           }
-          if (r0 + r < live && mine < D) out[record(c0 + r0 + r) * D + place] = v;
+          const int64_t at_r = __shfl_sync(0xffffffffu, record, r0 + r);
+          if (r0 + r < live && mine < D) out[at_r * D + place] = v;
           if (lane == r) mine_of = RowStat{all == 0.0f ? -INFINITY : top, all, 0u, 0u};
         }
+        const int64_t at_mine = __shfl_sync(0xffffffffu, record, r0 + (lane & 7));
         if (wg == 0 && lane < 8 && r0 + lane < live) {
           const uint32_t per = (uint32_t)min(M.piece.per, (int64_t)0x7fffffff);
           const uint32_t others = g.rest > 0 ? ((uint32_t)g.rest + per - 1) / per : 0;
           mine_of.odd = *reinterpret_cast<volatile uint32_t*>(&M.odd[segs & 7]) == segs;
           mine_of.rest = others << 16 | (blockIdx.x + 1);
-          (inside ? P.s_cta : P.s_rows)[record(c0 + r0 + lane)] = mine_of;
+          (inside ? P.s_cta : P.s_rows)[at_mine] = mine_of;
         }
       }
       tc::fence_before_sync();
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(kBarOFree));
-      any_of(false, 3, 64 * kGroupWarps);   // (off is written again behind this)
+      any_of(false, 3, 64 * kGroupWarps);   // (off and red are written again behind this)
     }
   }
 
   tc::fence_before_sync();
   __syncthreads();
   tc::fence_after_sync();
-  if (warp == kMmaWarp) tc::tmem_dealloc(tmem, kTmemCols);
+  if (warp == kScoreWarp) tc::tmem_dealloc(tmem, kTmemCols);
 }
 
 template <int D, int TYPE>
