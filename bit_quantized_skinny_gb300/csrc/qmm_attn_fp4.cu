@@ -518,7 +518,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fp4_kernel(const __grid_cons
       ++segs;
       off[lane] = 0.0f;
       __syncwarp();
-      float sum[kFew] = {};   // of this thread's weights, where there are few rows
+      float sum[kFew] = {}, add[kFew] = {};   // of this thread's weights, and in the tile, where there are few rows
       bool first = true, leave = false;   // leave: the whole group knows that a wait gave up
       for (int j = g.j0; j < j1; ++j, ++tile) {
         const uint32_t buf = tile & 1, phase = (tile >> 1) & 1;
@@ -529,30 +529,17 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fp4_kernel(const __grid_cons
         const bool hidden = __any_sync(0xffffffffu, from > 0);
         ok = wait_w(kBarS + buf, phase) && ok;
         tc::fence_after_sync();
-        uint32_t s[kHalf];
-        if (live > 8) {
-          tc::ld_wait_x32(tmem + lanes + T::kS + kN * buf + c0, s);
-        } else {
-          uint32_t few[8];
-          tc::ld_wait_x8(tmem + lanes + T::kS + kN * buf + c0, few);
-#pragma unroll
-          for (int r = 0; r < 8; ++r) s[r] = few[r];
-        }
-        tc::fence_before_sync();
-        __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(bar(kBarSFree + buf));
-          if (!both) mbar_arrive(bar(kBarSFree + buf));   // (the other group has no part in it)
-        }
         if (tile >= 2) ok = wait_w(kBarO + buf, phase ^ 1) && ok;   // the last readers of this p
-        // eight rows' scores in units of log2, plus off
-        auto scores = [&](auto r_, float (&x)[8]) {
-          constexpr int r = decltype(r_)::value;
+        // sixteen rows' scores in units of log2, plus off.  (The loops over them are not unrolled: five warps a scheduler
+        // in as many loops are bound by the instructions' way to them before anything else.)
+        auto scores = [&](int r, float (&x)[16]) {
+          uint32_t s[16];
+          tc::ld_wait_x16(tmem + lanes + T::kS + kN * buf + c0 + r, s);
 #pragma unroll
-          for (int q = 0; q < 8; q += 4) {
+          for (int q = 0; q < 16; q += 4) {
             const float4 f = *reinterpret_cast<const float4*>(factors + r + q), o = *reinterpret_cast<const float4*>(off + r + q);
-            const float2 u = f2unpack(fma2(f2pack(__uint_as_float(s[r + q]), __uint_as_float(s[r + q + 1])), f2pack(f.x, f.y), f2pack(o.x, o.y)));
-            const float2 v = f2unpack(fma2(f2pack(__uint_as_float(s[r + q + 2]), __uint_as_float(s[r + q + 3])), f2pack(f.z, f.w), f2pack(o.z, o.w)));
+            const float2 u = f2unpack(fma2(f2pack(__uint_as_float(s[q]), __uint_as_float(s[q + 1])), f2pack(f.x, f.y), f2pack(o.x, o.y)));
+            const float2 v = f2unpack(fma2(f2pack(__uint_as_float(s[q + 2]), __uint_as_float(s[q + 3])), f2pack(f.z, f.w), f2pack(o.z, o.w)));
             x[q] = u.x;
             x[q + 1] = u.y;
             x[q + 2] = v.x;
@@ -560,43 +547,34 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fp4_kernel(const __grid_cons
           }
           if (hidden)
 #pragma unroll
-            for (int q = 0; q < 8; ++q)
+            for (int q = 0; q < 16; ++q)
               if (r + q < from) x[q] = -INFINITY;
         };
         uint8_t* p = smem + L::kP + buf * L::kPBytes + mine * 128;
-        // N rows' weights to shared memory (those behind the last row do no harm); the largest exponent
-        float add[kFew];
-        auto weights_of = [&](auto n_) -> float {
-          constexpr int N = decltype(n_)::value;
-          float most[2] = {-INFINITY, -INFINITY};
-          auto eight = [&](auto r_) {
-            constexpr int r = decltype(r_)::value;
-            if constexpr (r < N) {
-              float x[8];
-              scores(r_, x);
+        // the rows' weights to shared memory (those behind the last row do no harm); the largest exponent
+        auto weights = [&]() -> float {
+          float most = -INFINITY;
+#pragma unroll 1
+          for (int r = 0; r < live; r += 16) {
+            float x[16];
+            scores(r, x);
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
               uint32_t w[4];
 #pragma unroll
-              for (int q = 0; q < 8; q += 2) {
-                most[q / 2 % 2] = fmaxf(most[q / 2 % 2], fmaxf(x[q], x[q + 1]));
-                const float e0 = exp2_fast(x[q]), e1 = exp2_fast(x[q + 1]);
-                w[q / 2] = pack2<QMM_F16>(e0, e1);
-                if constexpr (N == kFew) {
-                  add[q] = e0;
-                  add[q + 1] = e1;
-                }
+              for (int q = 8 * h; q < 8 * h + 8; q += 2) {
+                most = fmaxf(most, fmaxf(x[q], x[q + 1]));
+                x[q] = exp2_fast(x[q]);
+                x[q + 1] = exp2_fast(x[q + 1]);
+                w[q / 2 - 4 * h] = pack2<QMM_F16>(x[q], x[q + 1]);
               }
-              *reinterpret_cast<uint4*>(p + (((c0 + r) / 8) ^ (mine & 7)) * 16) = make_uint4(w[0], w[1], w[2], w[3]);
+              *reinterpret_cast<uint4*>(p + (((c0 + r) / 8 + h) ^ (mine & 7)) * 16) = make_uint4(w[0], w[1], w[2], w[3]);
             }
-          };
-          eight(std::integral_constant<int, 0>{});
-          eight(std::integral_constant<int, 8>{});
-          eight(std::integral_constant<int, 16>{});
-          eight(std::integral_constant<int, 24>{});
-          return fmaxf(most[0], most[1]);
-        };
-        auto weights = [&]() -> float {
-          if (live > kFew) return weights_of(std::integral_constant<int, 32>{});
-          return weights_of(std::integral_constant<int, kFew>{});
+            if (rows <= kFew)
+#pragma unroll
+              for (int q = 0; q < kFew; ++q) add[q] = x[q];
+          }
+          return most;
         };
         for (bool set = first;; set = true) {   // twice, where off has to move before the weights hold
           if (set) {
@@ -604,22 +582,17 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fp4_kernel(const __grid_cons
             if (leave) break;
             // the rows' maxima of this tile: lane r of each warp gets row r's
             float top = -INFINITY;
-            auto maxima = [&](auto r_) {
-              constexpr int r = decltype(r_)::value;
-              if (r >= live) return;
-              float x[8];
-              scores(r_, x);
+#pragma unroll 1
+            for (int r = 0; r < live; r += 16) {
+              float x[16];
+              scores(r, x);
 #pragma unroll
-              for (int q = 0; q < 8; ++q) {
+              for (int q = 0; q < 16; ++q) {
                 const float v = x[q] == x[q] ? x[q] : -INFINITY;
                 const uint32_t b = __float_as_uint(v), up = __reduce_max_sync(0xffffffffu, b & 0x80000000u ? ~b : b | 0x80000000u);
                 if (lane == r + q) top = __uint_as_float(up & 0x80000000u ? up & 0x7FFFFFFFu : ~up);
               }
-            };
-            maxima(std::integral_constant<int, 0>{});
-            maxima(std::integral_constant<int, 8>{});
-            maxima(std::integral_constant<int, 16>{});
-            maxima(std::integral_constant<int, 24>{});
+            }
             red[wg * kHalf + lane] = top;
             any_here(false);
 #pragma unroll
@@ -667,7 +640,11 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fp4_kernel(const __grid_cons
         __syncwarp();
         if (lane == 0) {
           mbar_arrive(bar(kBarP + buf));
-          if (!both) mbar_arrive(bar(kBarP + buf));
+          mbar_arrive(bar(kBarSFree + buf));
+          if (!both) {   // (the other group has no part in it)
+            mbar_arrive(bar(kBarP + buf));
+            mbar_arrive(bar(kBarSFree + buf));
+          }
         }
       }
 
