@@ -40,7 +40,7 @@ namespace {
 __device__ unsigned g_status;   // this file's kernels' status word
 
 constexpr int kTile = 128;           // keys of a key tile
-constexpr int kLead = 3;             // units of a group besides its key tiles
+constexpr int kLead = 6;             // units of a group besides its key tiles
 constexpr int kN = 64;               // rows of a block
 constexpr int kHalf = kN / 2;        // rows of a softmax group
 constexpr int kFew = 8;              // rows whose weights a softmax thread adds up itself
@@ -272,11 +272,13 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fp4_kernel(const __grid_cons
       mbar_wait(bar(kBarPackFull + k % kPacks), (k / kPacks) & 1, kWaitLimit);
   } else if (warp == kQWarp) {
     // ------------------------------------------------------------------ query tiles in fp16
-    // A row of D/8 lanes.  A bf16 row is multiplied by the power of two that takes its largest value to
-    // [2^14, 2^15): exact for what is not 2^-31 of that; the softmax multiplies its scores by the inverse.
-    constexpr int kLanes = D / 8, kAtOnce = 32 / kLanes, kAhead = 4;
+    // The rows come as they are, 16 bytes a lane, and bf16 ones are turned in place: a row is multiplied by the power of
+    // two that takes its largest value to [2^14, 2^15), exact for what is not 2^-31 of that; the softmax
+    // multiplies its scores by the inverse.  (All copies of a tile are in flight at once, and the code is short: it runs
+    // once a segment, and instructions that come from afar cost more than they do.)
+    constexpr int kLanes = D / 8, kAtOnce = 32 / kLanes;
     const float c = a.scale * P.k_scale * kLog2e;
-    float* factors = reinterpret_cast<float*>(smem + L::kFactors);
+    const int d = lane % kLanes;   // 16 bytes of a row
     uint32_t pos = 0;
     bool ok = true;
     for (; ok && next_of(walk, P, g); ++pos) {
@@ -284,46 +286,44 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fp4_kernel(const __grid_cons
       ok = use == 0 || wait_w(kBarQEmpty + st, (use - 1) & 1);
       if (!ok) break;
       const int live = g.rows * G;
-      uint8_t* tile = smem + L::kQ + st * L::kQBytes;
-      for (int r0 = 0; r0 < live; r0 += kAtOnce * kAhead) {
-        uint4 q[kAhead];
-#pragma unroll
-        for (int u = 0; u < kAhead; ++u) {
-          const int r = r0 + u * kAtOnce + lane / kLanes;
-          q[u] = make_uint4(0u, 0u, 0u, 0u);
-          if (r < live) {
-            const int tok = (int)((uint32_t)r / (uint32_t)G);
-            q[u] = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.Q) + (g.t0 + tok) * a.ldq +
-                                                   (int64_t)(g.h * G + r - tok * G) * D + 8 * (lane % kLanes));
-          }
-        }
-#pragma unroll
-        for (int u = 0; u < kAhead; ++u) {
-          const int r = r0 + u * kAtOnce + lane / kLanes;
-          uint32_t w[4] = {q[u].x, q[u].y, q[u].z, q[u].w};
-          int up = 127;   // exponent field of the row's power of two
-          if constexpr (TYPE == QMM_BF16) {
-            uint32_t top = 0;
-#pragma unroll
-            for (int e = 0; e < 4; ++e) top = max(top, max(w[e] & 0x7FFFu, w[e] >> 16 & 0x7FFFu));
-#pragma unroll
-            for (int off = kLanes / 2; off >= 1; off >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, off));
-            up = top == 0 || top >= 0x7F80u ? 127 : min(254, 268 - (int)(top >> 7));
-            const float f = __uint_as_float((uint32_t)up << 23);
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-              w[e] = pack2<QMM_F16>(__uint_as_float(w[e] << 16) * f, __uint_as_float(w[e] & 0xFFFF0000u) * f);
-          }
-          if (r < live) {
-            const int d = lane % kLanes;   // 16 bytes of the row
-            *reinterpret_cast<uint4*>(tile + (d / 8) * L::kQHalf + r * 128 + ((d % 8) ^ (r & 7)) * 16) =
-                make_uint4(w[0], w[1], w[2], w[3]);
-            if (d == 0) factors[(pos % kFactorTiles) * kN + r] = scalbnf(c, 127 - up);
-          }
-        }
+      const uint16_t* from = static_cast<const uint16_t*>(a.Q) + g.t0 * a.ldq + (int64_t)g.h * G * D + 8 * d;
+      uint8_t* tile = smem + L::kQ + st * L::kQBytes + (d / 8) * L::kQHalf;
+      float* factors = reinterpret_cast<float*>(smem + L::kFactors) + (pos % kFactorTiles) * kN;
+      int tok = 0, head = lane / kLanes;   // of this lane's row
+      while (head >= G) {
+        head -= G;
+        ++tok;
       }
-      // scores of rows behind the last one come to 0 (or NaN): they never grow
-      for (int r = live + lane; r < kN; r += 32) factors[(pos % kFactorTiles) * kN + r] = 0.0f;
+#pragma unroll 1
+      for (int r = lane / kLanes; r < live; r += kAtOnce) {
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;"
+                     :: "r"(smem_addr(tile) + r * 128 + ((d % 8) ^ (r & 7)) * 16), "l"(from + tok * a.ldq + head * D) : "memory");
+        for (head += kAtOnce; head >= G; head -= G) ++tok;
+      }
+      asm volatile("cp.async.wait_all;" ::: "memory");
+      __syncwarp();
+#pragma unroll 1
+      for (int r0 = 0; r0 < kN; r0 += kAtOnce) {
+        const int r = r0 + lane / kLanes;
+        int up = 127;   // exponent field of the row's power of two
+        if (TYPE == QMM_BF16 && r0 < live) {
+          uint4* at = reinterpret_cast<uint4*>(tile + r * 128 + ((d % 8) ^ (r & 7)) * 16);
+          const uint4 q = *at;
+          uint32_t w[4] = {q.x, q.y, q.z, q.w}, top = 0;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) top = max(top, max(w[e] & 0x7FFFu, w[e] >> 16 & 0x7FFFu));
+#pragma unroll
+          for (int o = kLanes / 2; o >= 1; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+          up = top == 0 || top >= 0x7F80u ? 127 : min(254, 268 - (int)(top >> 7));
+          const float f = __uint_as_float((uint32_t)up << 23);
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            w[e] = pack2<QMM_F16>(__uint_as_float(w[e] << 16) * f, __uint_as_float(w[e] & 0xFFFF0000u) * f);
+          *at = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+        // (scores of rows behind the last one come to 0 or NaN: they never grow)
+        if (d == 0) factors[r] = r < live ? scalbnf(c, 127 - up) : 0.0f;
+      }
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(kBarQFull + st));
@@ -514,7 +514,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fp4_kernel(const __grid_cons
       const bool both = rows > kHalf;
       const int c0 = both ? kHalf * grp : 0, live = both ? clampi(rows - c0, 0, kHalf) : rows;   // the group's rows
       const float* factors = reinterpret_cast<const float*>(smem + L::kFactors) + segs % kFactorTiles * kN + c0;
-      const int j1 = g.j1, keys = g.keys, first_keys = g.first_keys;
+      const int j1 = g.j1, n = g.j1 - g.j0, keys = g.keys, first_keys = g.first_keys;
       ++segs;
       off[lane] = 0.0f;
       __syncwarp();
@@ -663,63 +663,67 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fp4_kernel(const __grid_cons
       }
       if (any_of(!ok || leave, 3, 64 * kGroupWarps)) break;
       tc::fence_after_sync();
+      // Lane r has row r of the group (of both groups' sums, where they had the tiles in turn): its sum, its
+      // exponent, what the groups' sums count, and where its record lies.
+      const uint32_t tO = tmem + lanes + T::kO, tL = tmem + lanes + T::kL;
+      auto sum_of = [&](int gr) -> float {
+        const float* x = reinterpret_cast<const float*>(smem + L::kRed) + gr * kGroupWarps * kHalf + lane;
+        if (rows <= kFew) return (x[0] + x[kHalf]) + (x[2 * kHalf] + x[3 * kHalf]);
+        float l = 0.0f;
+#pragma unroll 1
+        for (int r0 = 0; r0 < live; r0 += 8) {
+          uint32_t o[8];
+          tc::ld_wait_x8(tL + kHalf * gr + r0, o);
+#pragma unroll
+          for (int r = 0; r < 8; ++r)
+            if (lane == r0 + r) l = __uint_as_float(o[r]);
+        }
+        return l;
+      };
+      const float* offs = reinterpret_cast<const float*>(smem + L::kOff) + lane;
+      float f[2] = {1.0f, 0.0f}, all = 0.0f, top = -INFINITY;
+#pragma unroll 1
+      for (int k = both ? grp : 0; k < (both ? grp + 1 : 2); ++k) {
+        const bool has = both || n > 1 || (int)((tile - 1) & 1) == k;   // (a group without a tile has no sums)
+        const float l = has ? sum_of(k) : 0.0f, t = -offs[k * kGroupWarps * kHalf];
+        if (l != 0.0f) {   // (NaN counts)
+          const float best = fmaxf(top, t), w = exp2_fast(t - best), was = exp2_fast(top - best);
+          all = all * was + l * w;
+          f[0] = k == 0 || both ? w : f[0] * was;
+          f[1] = k == 0 || both ? 0.0f : w;
+          top = best;
+        } else if (k == 0 && !both) {
+          f[0] = 0.0f;
+        }
+      }
       const bool inside = g.j0 > 0;   // not the first segment of its group: the CTA's own record
-      // lane r: where the record of row r of the group lies
       const int row = c0 + lane, tok = (int)((uint32_t)row / (uint32_t)G);
       const int64_t record = inside ? (int64_t)blockIdx.x * 2 * kRows + row
                                     : ((int64_t)(g.own ? a.T : 0) + g.t0 + tok) * a.Hq + (int64_t)g.h * G + row - tok * G;
-      float* out = inside ? P.o_cta : P.o_rows;
-      // O^T: this thread's value of every row, at the place where the combine launch looks for it (column_of)
-      const int place = (mine & ~31) + 8 * (mine >> 1 & 3) + 2 * (mine >> 3 & 3) + (mine & 1);
-      const float* offs = reinterpret_cast<const float*>(smem + L::kOff);
-      // a group without a tile has no sums of its own
-      const bool has0 = both || g.j1 - g.j0 > 1 || ((tile - 1) & 1) == 0, has1 = both || g.j1 - g.j0 > 1 || ((tile - 1) & 1) == 1;
-      // eight rows: of the group's; or, of both groups' sums, the group's half of them
+      if (wg == 0 && (both || grp == 0) && lane < live) {
+        const uint32_t per = (uint32_t)min(M.piece.per, (int64_t)0x7fffffff);
+        const uint32_t others = g.rest > 0 ? ((uint32_t)g.rest + per - 1) / per : 0;
+        const uint32_t odd = *reinterpret_cast<volatile uint32_t*>(&M.odd[segs & 7]) == segs;
+        (inside ? P.s_cta : P.s_rows)[record] = RowStat{top, all, odd, others << 16 | (blockIdx.x + 1)};
+      }
+      // O^T: this thread's value of every row (of both groups' sums, half the rows a group), at the place where the
+      // combine launch looks for it (column_of)
+      float* out = (inside ? P.o_cta : P.o_rows) + (mine & ~31) + 8 * (mine >> 1 & 3) + 2 * (mine >> 3 & 3) + (mine & 1);
+      const int r1 = both ? live : min(live, 16 * grp + 16);
 #pragma unroll 1
-      for (int r0 = both ? 0 : 16 * grp; r0 < min(live, both ? kHalf : 16 * grp + 16); r0 += 8) {
-        uint32_t o[8], l[8], o1[8], l1[8];
-        const uint32_t at = (both ? kHalf * grp : 0) + r0;
-        tc::ld_wait_x8(tmem + lanes + T::kL + at, l);
-        tc::ld_wait_x8(tmem + lanes + T::kO + at, o);
-        if (!both) {
-          tc::ld_wait_x8(tmem + lanes + T::kL + kHalf + r0, l1);
-          tc::ld_wait_x8(tmem + lanes + T::kO + kHalf + r0, o1);
-        }
-        if (rows <= kFew) {
-          const float* reds = reinterpret_cast<const float*>(smem + L::kRed);
-#pragma unroll
-          for (int r = 0; r < kFew; ++r) {
-            auto sum_of = [&](const float* x) {
-              return __float_as_uint((x[r] + x[kHalf + r]) + (x[2 * kHalf + r] + x[3 * kHalf + r]));
-            };
-            l[r] = sum_of(reds);
-            l1[r] = sum_of(reds + kGroupWarps * kHalf);
-          }
-        }
-        RowStat mine_of{};
+      for (int r0 = both ? 0 : 16 * grp; r0 < r1; r0 += 8) {
+        uint32_t o[8], o1[8];
+        tc::ld_wait_x8(tO + (both ? kHalf * grp : 0) + r0, o);
+        if (!both) tc::ld_wait_x8(tO + kHalf + r0, o1);
 #pragma unroll
         for (int r = 0; r < 8; ++r) {
-          float v = __uint_as_float(o[r]), all = has0 ? __uint_as_float(l[r]) : 0.0f;
-          float top = -offs[(both ? grp : 0) * kGroupWarps * kHalf + r0 + r];
+          const int64_t at = __shfl_sync(0xffffffffu, record, r0 + r) * D;
+          float v = __uint_as_float(o[r]);
           if (!both) {
-            const float all1 = has1 ? __uint_as_float(l1[r]) : 0.0f, top1 = -offs[kGroupWarps * kHalf + r0 + r];
-            const float best = all == 0.0f ? top1 : all1 == 0.0f ? top : fmaxf(top, top1);
-            const float f0 = all == 0.0f ? 0.0f : exp2_fast(top - best), f1 = all1 == 0.0f ? 0.0f : exp2_fast(top1 - best);
-            v = (f0 != 0.0f ? v * f0 : 0.0f) + (f1 != 0.0f ? __uint_as_float(o1[r]) * f1 : 0.0f);
-            all = all * f0 + all1 * f1;
-            top = best;
+            const float u = __shfl_sync(0xffffffffu, f[0], r0 + r), w = __shfl_sync(0xffffffffu, f[1], r0 + r);
+            v = (u != 0.0f ? v * u : 0.0f) + (w != 0.0f ? __uint_as_float(o1[r]) * w : 0.0f);
           }
-          const int64_t at_r = __shfl_sync(0xffffffffu, record, r0 + r);
-          if (r0 + r < live && mine < D) out[at_r * D + place] = v;
-          if (lane == r) mine_of = RowStat{all == 0.0f ? -INFINITY : top, all, 0u, 0u};
-        }
-        const int64_t at_mine = __shfl_sync(0xffffffffu, record, r0 + (lane & 7));
-        if (wg == 0 && lane < 8 && r0 + lane < live) {
-          const uint32_t per = (uint32_t)min(M.piece.per, (int64_t)0x7fffffff);
-          const uint32_t others = g.rest > 0 ? ((uint32_t)g.rest + per - 1) / per : 0;
-          mine_of.odd = *reinterpret_cast<volatile uint32_t*>(&M.odd[segs & 7]) == segs;
-          mine_of.rest = others << 16 | (blockIdx.x + 1);
-          (inside ? P.s_cta : P.s_rows)[at_mine] = mine_of;
+          if (r0 + r < live && mine < D) out[at] = v;
         }
       }
       tc::fence_before_sync();
