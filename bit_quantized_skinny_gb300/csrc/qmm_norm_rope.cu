@@ -142,11 +142,15 @@ __device__ __forceinline__ bool encode_fast(const float (&y)[8], const float (&e
 }
 
 // A key's head again, in 64 bits from the operands, rounded to fp32 once; a value's head is the operands.  Every
-// lane of the warp takes part; c and s: the lane's cosines and signed sines (see the kernel).
+// lane of the warp takes part.  (Operands and result go by value: arrays that a call has the address of would live in
+// memory in the kernel's loop too.)
+struct Eight {
+  float x[8];
+};
 template <int D, int IN>
-__device__ __noinline__ void exact_head(const qmm_norm_rope_args& a, int64_t t, int h, int l, bool is_k, const float (&c)[8],
-                                        const float (&s)[8], bool turns, float (&x)[8]) {
+__device__ __noinline__ Eight exact_head(const qmm_norm_rope_args& a, int64_t t, int h, int l, bool is_k) {
   constexpr int kLanes = D / 8;
+  const bool turns = 8 * l < a.rot;
   float in[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
   const int heads = a.Hq + (a.V ? 2 : 1) * a.Hk;
   if (is_k) load8<IN>(a.K, t * a.ldk + (int64_t)(h - a.Hq) * D + 8 * l, in);
@@ -162,13 +166,23 @@ __device__ __noinline__ void exact_head(const qmm_norm_rope_args& a, int64_t t, 
   for (int k = 0; k < 8; ++k) y[k] = (double)in[k] / root * (a.k_weight ? (double)a.k_weight[8 * l + k] : 1.0);
   const int half = a.rot / 2, step = half / 8;
   const int from = (threadIdx.x & 31) + (8 * l < half ? step : (turns ? -step : 0));
+  int64_t pos = turns ? a.positions[t] : 0;
+  if (pos < 0 || pos >= a.max_pos) pos = 0;
+  Eight out;
 #pragma unroll
   for (int k = 0; k < 8; ++k) {
+    const int i = 8 * l + k, pair = a.interleaved ? i / 2 : i < half ? i : i - half;   // of the value
+    const bool second = a.interleaved ? i & 1 : i >= half;
     double other = __shfl_sync(0xffffffffu, y[k], from);
     if (a.interleaved) other = y[k ^ 1];
-    const double z = turns ? y[k] * (double)c[k] + other * (double)s[k] : y[k];
-    x[k] = is_k ? (float)z : in[k];
+    double z = y[k];
+    if (turns) {
+      const double c = a.cos_sin[pos * a.rot + pair], s = a.cos_sin[pos * a.rot + half + pair];
+      z = second ? z * c + other * s : z * c - other * s;
+    }
+    out.x[k] = is_k ? (float)z : in[k];
   }
+  return out;
 }
 
 // CTA (t, part): the heads part, part + groups * parts, ... of row t (queries, then keys, then
@@ -291,11 +305,8 @@ __global__ void __launch_bounds__(kThreads, AHEAD == 2 && !FP4 ? 16 : 0) norm_ro
           const bool mine_too = !is_q && h < heads;
           const bool in_range = !is_k || (sum < 1e38f && sum * (1.0f / D) + a.eps > 1e-30f);   // of the fp32 arithmetic
           if (__any_sync(0xffffffffu, mine_too && !(sure && in_range))) {
-            exact_head<D, IN>(a, t, h, l, is_k, c, s, turns, x[u]);
-            uint32_t codes2, scale2;
-            encode(x[u], tensor_scale, codes2, scale2);
-            codes = codes2;
-            scale = scale2;
+            const Eight y = exact_head<D, IN>(a, t, h, l, is_k);
+            encode(y.x, tensor_scale, codes, scale);
           }
           if (mine_too && slot >= 0) {
             const bool key = is_k;
