@@ -109,11 +109,11 @@ __device__ __forceinline__ void encode(const float (&y)[8], float tensor_scale, 
 }
 
 // The same by one reciprocal, from values that are off by at most err; false: another code or scale is
-// within reach, and encode() has to decide.  kSlack: relative, for the quotients' own roundings (three fp32 ones and
-// the reciprocal's, below 2^-21 together).
+// within reach, and encode() has to decide.  Relative, for the roundings of the quotients here and in encode(): a code's
+// three (2^-24 each), a scale's seven.
 __device__ __forceinline__ bool encode_fast(const float (&y)[8], const float (&err)[8], float tensor_scale,
                                             uint32_t& codes, uint32_t& scale) {
-  constexpr float kSlack = 0x1p-20f;
+  constexpr float kCodeSlack = 0x1p-22f, kScaleSlack = 0x1p-21f;
   const uint32_t top = block_top(y);
   float worst = 0.0f;
 #pragma unroll
@@ -123,14 +123,14 @@ __device__ __forceinline__ bool encode_fast(const float (&y)[8], const float (&e
   codes = 0;
   if (top >= 0x7F800000u) return true;
   const float a = __uint_as_float(top), to = __frcp_rn(6.0f) * __frcp_rn(tensor_scale);
-  scale = kv4::e4m3_code((a + worst) * to * (1.0f + kSlack));
-  bool sure = scale == kv4::e4m3_code(fmaxf(a - worst, 0.0f) * to * (1.0f - kSlack));
+  scale = kv4::e4m3_code((a + worst) * to * (1.0f + kScaleSlack));
+  bool sure = scale == kv4::e4m3_code(fmaxf(a - worst, 0.0f) * to * (1.0f - kScaleSlack));
   const float S = kv4::e4m3_value(scale) * tensor_scale, inv = __frcp_rn(S);
   if (!(S > 0.0f)) return sure;
   float lo[8], hi[8];
 #pragma unroll
   for (int k = 0; k < 8; ++k) {
-    const float t = y[k] * inv, off = __fmaf_rn(fabsf(t), kSlack, err[k] * inv);
+    const float t = y[k] * inv, off = __fmaf_rn(fabsf(t), kCodeSlack, err[k] * inv);
     lo[k] = t - off;
     hi[k] = t + off;
   }
@@ -160,10 +160,10 @@ __device__ __noinline__ Eight exact_head(const qmm_norm_rope_args& a, int64_t t,
   for (int k = 0; k < 8; ++k) sum = __fma_rn((double)in[k], (double)in[k], sum);
 #pragma unroll
   for (int off = kLanes / 2; off >= 1; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
-  const double root = sqrt(sum / D + (double)a.eps);
+  const double r = 1.0 / sqrt(sum / D + (double)a.eps);   // (its rounding and the products' are below 2^-51)
   double y[8];
 #pragma unroll
-  for (int k = 0; k < 8; ++k) y[k] = (double)in[k] / root * (a.k_weight ? (double)a.k_weight[8 * l + k] : 1.0);
+  for (int k = 0; k < 8; ++k) y[k] = (double)in[k] * (a.k_weight ? (double)a.k_weight[8 * l + k] : 1.0) * r;
   const int half = a.rot / 2, step = half / 8;
   const int from = (threadIdx.x & 31) + (8 * l < half ? step : (turns ? -step : 0));
   int64_t pos = turns ? a.positions[t] : 0;
@@ -188,7 +188,7 @@ __device__ __noinline__ Eight exact_head(const qmm_norm_rope_args& a, int64_t t,
 // CTA (t, part): the heads part, part + groups * parts, ... of row t (queries, then keys, then
 // values).
 template <int D, int IN, int OUT, int AHEAD, bool FP4>
-__global__ void __launch_bounds__(kThreads, AHEAD == 2 && !FP4 ? 16 : 0) norm_rope_kernel(const __grid_constant__ Params P) {
+__global__ void __launch_bounds__(kThreads, AHEAD == 2 || FP4 ? 16 : 0) norm_rope_kernel(const __grid_constant__ Params P) {
   constexpr int kLanes = D / 8;
   constexpr int kGroups = kThreads / kLanes;
   // launched early behind a launch that allows it: memory is read from here on
@@ -262,12 +262,19 @@ __global__ void __launch_bounds__(kThreads, AHEAD == 2 && !FP4 ? 16 : 0) norm_ro
       const int h = h0 + u * stride + mine;
       const bool is_q = h < a.Hq, is_k = !is_q && h < a.Hq + a.Hk;
       float sum = 0.0f;
+      if constexpr (FP4) {   // (three roundings, not eight: see err)
+        float pair[4];
 #pragma unroll
-      for (int k = 0; k < 8; ++k) sum = __fmaf_rn(x[u][k], x[u][k], sum);
+        for (int k = 0; k < 4; ++k) pair[k] = __fmaf_rn(x[u][2 * k], x[u][2 * k], x[u][2 * k + 1] * x[u][2 * k + 1]);
+        sum = (pair[0] + pair[1]) + (pair[2] + pair[3]);
+      } else {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) sum = __fmaf_rn(x[u][k], x[u][k], sum);
+      }
 #pragma unroll
       for (int off = kLanes / 2; off >= 1; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
       if (is_q || is_k) {
-        const float r = rsqrtf(sum * (1.0f / D) + a.eps);
+        const float r = FP4 ? __frsqrt_rn(sum * (1.0f / D) + a.eps) : rsqrtf(sum * (1.0f / D) + a.eps);
         float g[8] = {1.0f, 1.0f, 1.0f, 1.0f, 1.0f, 1.0f, 1.0f, 1.0f};
         const float* w = is_q ? a.q_weight : a.k_weight;
         if (w) load8<QMM_F32>(w, 8 * l, g);
@@ -287,11 +294,11 @@ __global__ void __launch_bounds__(kThreads, AHEAD == 2 && !FP4 ? 16 : 0) norm_ro
       }
       float err[8];   // of x, as the 4-bit codes have to know it
       if constexpr (FP4) {
-        // the norm: D/8 + log2(D/8) + 2 roundings of the mean's sum (half of that on its root), the root's 2, the
-        // two products', the rotation's 2: below 24 of 2^-24 for D = 256, on the terms that are added
+        // in units of 2^-24, on the terms that are added: half of the mean's roundings (a square's, three and log2(D/8) sums', eps':
+        // 10 at most), the root's, the two products', the rotation's two: 10; and the error's own roundings
 #pragma unroll
         for (int k = 0; k < 8; ++k)
-          err[k] = is_k ? 0x1p-19f * (turns ? __fmaf_rn(fabsf(x[u][k]), fabsf(c[k]), fabsf(y[k] * s[k])) : fabsf(x[u][k])) : 0.0f;
+          err[k] = is_k ? 0x1.5p-21f * (turns ? __fmaf_rn(fabsf(x[u][k]), fabsf(c[k]), fabsf(y[k] * s[k])) : fabsf(x[u][k])) : 0.0f;
       }
       if (turns && (is_q || is_k))
 #pragma unroll
