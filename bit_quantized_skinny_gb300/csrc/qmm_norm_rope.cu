@@ -141,48 +141,65 @@ __device__ __forceinline__ bool encode_fast(const float (&y)[8], const float (&e
   return sure && codes == other;
 }
 
-// A key's head again, in 64 bits from the operands, rounded to fp32 once; a value's head is the operands.  Every
-// lane of the warp takes part.  (Operands and result go by value: arrays that a call has the address of would live in
-// memory in the kernel's loop too.)
+// m^(-1/2) to 2^-50: the fp32 one of m brought into [1, 4), and two steps of Newton's iteration, r += r (1 - m r^2) / 2.
+__device__ __forceinline__ double inv_root(double m) {
+  if (!(m > 0.0) || m > 1e300) return rsqrtf((float)m);   // 0, infinity and NaN (finite operands stay below 1e80)
+  const int e = ((__double2hiint(m) >> 20) - 1023) & ~1;
+  const double f = m * __hiloint2double((1023 - e) << 20, 0);
+  double r = rsqrtf((float)f);
+#pragma unroll
+  for (int step = 0; step < 2; ++step) r = __fma_rn(r * 0.5, __fma_rn(-f * r, r, 1.0), r);
+  return r * __hiloint2double((1023 - e / 2) << 20, 0);
+}
+
+// A key's head in some thousands comes here, and values that lie exactly between two codes, as they do where the tensor's
+// scale is a short decimal.  (A 64-bit operation takes 16 cycles a warp: 2311 rows of 30 heads of 64 take 13.1 us,
+// 8.7 with no key's head here, 21.5 when values went the 64 bits' way too.)
+//
+// The codes (x) and the scale (y) of the lane's eight values by the definition, a key's from 64 bits where `keys`: again from
+// the operands, rounded to fp32 once.  Every lane of the warp takes part.  (Values go in and out by value: an array that a
+// call has the address of would live in memory in the kernel's loop too.)
 struct Eight {
   float x[8];
 };
 template <int D, int IN>
-__device__ __noinline__ Eight exact_head(const qmm_norm_rope_args& a, int64_t t, int h, int l, bool is_k) {
-  constexpr int kLanes = D / 8;
-  const bool turns = 8 * l < a.rot;
-  float in[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
-  const int heads = a.Hq + (a.V ? 2 : 1) * a.Hk;
-  if (is_k) load8<IN>(a.K, t * a.ldk + (int64_t)(h - a.Hq) * D + 8 * l, in);
-  else if (h >= a.Hq && h < heads) load8<IN>(a.V, t * a.ldv + (int64_t)(h - a.Hq - a.Hk) * D + 8 * l, in);
-  double sum = 0.0;
+__device__ __noinline__ uint2 decide(const qmm_norm_rope_args& a, int64_t t, int h, int l, Eight in, bool keys,
+                                     float tensor_scale) {
+  if (keys) {
+    constexpr int kLanes = D / 8;
+    const bool is_k = h >= a.Hq && h < a.Hq + a.Hk, turns = 8 * l < a.rot;
+    float x[8];
+    load8<IN>(a.K, t * a.ldk + (int64_t)(is_k ? h - a.Hq : 0) * D + 8 * l, x);
+    double sum = 0.0;
 #pragma unroll
-  for (int k = 0; k < 8; ++k) sum = __fma_rn((double)in[k], (double)in[k], sum);
+    for (int k = 0; k < 8; ++k) sum = __fma_rn((double)x[k], (double)x[k], sum);
 #pragma unroll
-  for (int off = kLanes / 2; off >= 1; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
-  const double r = 1.0 / sqrt(sum / D + (double)a.eps);   // (its rounding and the products' are below 2^-51)
-  double y[8];
+    for (int off = kLanes / 2; off >= 1; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+    const double r = inv_root(sum * (1.0 / D) + (double)a.eps);   // (off by less than 2^-50, as the products are)
+    double y[8];
 #pragma unroll
-  for (int k = 0; k < 8; ++k) y[k] = (double)in[k] * (a.k_weight ? (double)a.k_weight[8 * l + k] : 1.0) * r;
-  const int half = a.rot / 2, step = half / 8;
-  const int from = (threadIdx.x & 31) + (8 * l < half ? step : (turns ? -step : 0));
-  int64_t pos = turns ? a.positions[t] : 0;
-  if (pos < 0 || pos >= a.max_pos) pos = 0;
-  Eight out;
+    for (int k = 0; k < 8; ++k) y[k] = (double)x[k] * (a.k_weight ? (double)a.k_weight[8 * l + k] : 1.0) * r;
+    const int half = a.rot / 2, step = half / 8;
+    const int from = (threadIdx.x & 31) + (8 * l < half ? step : (turns ? -step : 0));
+    int64_t pos = turns ? a.positions[t] : 0;
+    if (pos < 0 || pos >= a.max_pos) pos = 0;
 #pragma unroll
-  for (int k = 0; k < 8; ++k) {
-    const int i = 8 * l + k, pair = a.interleaved ? i / 2 : i < half ? i : i - half;   // of the value
-    const bool second = a.interleaved ? i & 1 : i >= half;
-    double other = __shfl_sync(0xffffffffu, y[k], from);
-    if (a.interleaved) other = y[k ^ 1];
-    double z = y[k];
-    if (turns) {
-      const double c = a.cos_sin[pos * a.rot + pair], s = a.cos_sin[pos * a.rot + half + pair];
-      z = second ? z * c + other * s : z * c - other * s;
+    for (int k = 0; k < 8; ++k) {
+      const int i = 8 * l + k, pair = a.interleaved ? i / 2 : i < half ? i : i - half;   // of the value
+      const bool second = a.interleaved ? i & 1 : i >= half;
+      double other = __shfl_sync(0xffffffffu, y[k], from);
+      if (a.interleaved) other = y[k ^ 1];
+      double z = y[k];
+      if (turns) {
+        const double c = a.cos_sin[pos * a.rot + pair], s = a.cos_sin[pos * a.rot + half + pair];
+        z = second ? z * c + other * s : z * c - other * s;
+      }
+      if (is_k) in.x[k] = (float)z;
     }
-    out.x[k] = is_k ? (float)z : in[k];
   }
-  return out;
+  uint32_t codes, scale;
+  encode(in.x, tensor_scale, codes, scale);
+  return make_uint2(codes, scale);
 }
 
 // CTA (t, part): the heads part, part + groups * parts, ... of row t (queries, then keys, then
@@ -312,8 +329,12 @@ __global__ void __launch_bounds__(kThreads, AHEAD == 2 || FP4 ? 16 : 0) norm_rop
           const bool mine_too = !is_q && h < heads;
           const bool in_range = !is_k || (sum < 1e38f && sum * (1.0f / D) + a.eps > 1e-30f);   // of the fp32 arithmetic
           if (__any_sync(0xffffffffu, mine_too && !(sure && in_range))) {
-            const Eight y = exact_head<D, IN>(a, t, h, l, is_k);
-            encode(y.x, tensor_scale, codes, scale);
+            Eight now;
+#pragma unroll
+            for (int k = 0; k < 8; ++k) now.x[k] = x[u][k];
+            const uint2 by = decide<D, IN>(a, t, h, l, now, __any_sync(0xffffffffu, is_k && !(sure && in_range)), tensor_scale);
+            codes = by.x;
+            scale = by.y;
           }
           if (mine_too && slot >= 0) {
             const bool key = is_k;
