@@ -9,11 +9,11 @@
 //     S^T = K Q^T        tcgen05, K (128 keys x D) from tensor memory, where four warps put it, a thread a key
 //     p = 2^(c S + off)  a thread per key, S^T from tensor memory, c = scale k_scale log2 e over the row's power of two
 //     O^T += V^T p^T     tcgen05, V and p^T (both MN-major) from shared memory; four more warps write V
-//     l += 1 p^T         tcgen05, ones from tensor memory: the rows' sums of weights (of up to eight rows the softmax adds
+//     l += 1 p^T         tcgen05, ones from shared memory: the rows' sums of weights (of up to eight rows the softmax adds
 //                        them up itself: these products take as long as half of those before)
 // so few rows cost little, the exponentials of a row are spread over 128 threads, and no 128-row tile of queries
-// is read again for every tile.  Two groups of softmax warps have half of a block's rows each, or, where a block has no
-// more than one of them takes, the key tiles in turn, with sums of their own that are joined at a segment's end.
+// is read again for every tile.  Two groups of softmax warps have the key tiles in turn, with sums of their own that are
+// joined at a segment's end: what a tile costs a group besides its rows (waits, votes, fences) is then paid once for all of them.
 // off moves, and O^T is rescaled, only when a row's maximum grew by more than 8; weights are then at most 2^15, and
 // fp16 holds those down to 2^-21 of the largest at full precision.
 //
@@ -42,14 +42,14 @@ __device__ unsigned g_status;   // this file's kernels' status word
 constexpr int kTile = 128;           // keys of a key tile
 constexpr int kLead = 6;             // units of a group besides its key tiles
 constexpr int kN = 64;               // rows of a block
-constexpr int kHalf = kN / 2;        // rows of a softmax group
+constexpr int kHalf = kN / 2;        // rows up to which the products are half as wide
 constexpr int kFew = 8;              // rows whose weights a softmax thread adds up itself
 // warps: 0-3 and 4-7 softmax, 8 copies, 9 and 11 tensor cores, 10 queries, 12-15 keys and 16-19 values to fp16
 constexpr int kLoadWarp = 8, kScoreWarp = 9, kQWarp = 10, kSumWarp = 11, kKeyWarp = 12, kValueWarp = 16;
 constexpr int kThreads = 20 * 32, kGroupWarps = 4;
 constexpr uint32_t kTmemCols = 512;
-constexpr int kKeyBufs = 3;          // tiles of keys in tensor memory
-constexpr int kPacks = 10;           // packed tiles in shared memory: of keys and of values in turn
+constexpr int kKeyBufs = 2;          // tiles of keys in tensor memory
+constexpr int kPacks = 9;            // packed tiles in shared memory: of keys and of values in turn
 constexpr int kFactorTiles = 8;      // (the softmax is a few query tiles behind)
 constexpr float kGrow = 8.0f;
 constexpr float kLift = 7.0f;        // log2 of the largest weight when off is set
@@ -68,20 +68,22 @@ struct Smem {
   static constexpr int kV = 0;
   static constexpr int kQ = kV + kValueBufs * kVBytes;
   static constexpr int kP = kQ + 2 * kQBytes;
-  static constexpr int kPack = kP + 2 * kPBytes;
+  static constexpr int kOnes = kP + 2 * kPBytes;         // 16 keys of 128 ones
+  static constexpr int kOnesHalf = 16 * 128;
+  static constexpr int kPack = kOnes + 2 * kOnesHalf;
   static constexpr int kFactors = kPack + kPacks * kPackBytes;   // of the rows of the last kFactorTiles query tiles
   static constexpr int kOff = kFactors + kFactorTiles * kN * 4;  // each softmax warp's copy of its group's rows' off
-  static constexpr int kRed = kOff + 2 * kGroupWarps * kHalf * 4;   // the softmax warps' maxima of the rows
-  static constexpr int kMisc = kRed + 2 * kGroupWarps * kHalf * 4;
+  static constexpr int kRed = kOff + 2 * kGroupWarps * kN * 4;   // the softmax warps' maxima of the rows
+  static constexpr int kMisc = kRed + 2 * kGroupWarps * kN * 4;
   static constexpr int kTotal = kMisc + 1024;
 };
 static_assert(Smem<128>::kTotal <= 227 * 1024 && Smem<64>::kTotal <= 227 * 1024, "shared memory");
 
-// Tensor memory: K at 0, S^T behind it (two of them), then O^T, l, and the ones.
+// Tensor memory: K at 0, then S^T, O^T and l, one for each group.
 template <int D>
 struct Tmem {
-  static constexpr uint32_t kS = kKeyBufs * D / 2, kO = kS + 2 * kN, kL = kO + kN, kOnes = kL + kN;
-  static_assert(kOnes + 32 <= kTmemCols, "tensor memory");
+  static constexpr uint32_t kS = kKeyBufs * D / 2, kO = kS + 2 * kN, kL = kO + 2 * kN;
+  static_assert(kL + 2 * kN <= kTmemCols, "tensor memory");
 };
 
 // Barriers; a wait tells a phase from the one after it only, and every wait here is for the phase of a tile (or a segment)
@@ -180,9 +182,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fp4_kernel(const __grid_cons
   // ---- barriers, tensor memory, and this CTA's piece of the list of key tiles
   if (threadIdx.x < kBars) {
     const int k = threadIdx.x;
-    const bool warps = (k >= kBarPackEmpty && k < kBarKeyEmpty) || (k >= kBarValueFull && k < kBarValueEmpty);
-    const bool softmax = (k >= kBarSFree && k < kBarO) || k == kBarOFree;
-    mbar_init(bar(k), softmax ? 2 * kGroupWarps : warps ? kGroupWarps : 1);
+    const bool warps = (k >= kBarPackEmpty && k < kBarKeyEmpty) || (k >= kBarValueFull && k < kBarValueEmpty) ||
+                       (k >= kBarSFree && k < kBarO);
+    mbar_init(bar(k), k == kBarOFree ? 2 * kGroupWarps : warps ? kGroupWarps : 1);
     fence_barrier_init();
   } else if (threadIdx.x == kBars) {
     M.abort = 0;
@@ -194,6 +196,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fp4_kernel(const __grid_cons
   }
   // Launched early (behind a launch that allows it), this grid reads what was written before it from
   // here on; the combine launch, which reads the lengths before its own wait, may start from here on.
+  for (int k = threadIdx.x; k < L::kOnesHalf / 2; k += kThreads)
+    reinterpret_cast<uint32_t*>(smem + L::kOnes)[k] = 0x3C003C00u;
+  fence_proxy_async_smem();
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   deal<kThreads, kTile, kLead>(P, M.piece, &g_status);
@@ -201,17 +206,6 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fp4_kernel(const __grid_cons
   __syncthreads();
   tc::fence_after_sync();
   const uint32_t tmem = M.tmem;
-  if (warp < kGroupWarps) {   // (all lanes)
-    uint32_t ones[32];
-#pragma unroll
-    for (int k = 0; k < 32; ++k) ones[k] = 0x3C003C00u;
-    tc::st_x32(tmem + ((uint32_t)warp << 21) + T::kOnes, ones);
-    tc::wait_st();
-    tc::fence_before_sync();
-  }
-  __syncthreads();
-  tc::fence_after_sync();
-
   // A bounded wait for a phase of a barrier; false: this wait, or another one, gave up.  (A phase that is over is the
   // rule, and a suspended wait takes 200 clocks to see it.)
   auto wait = [&](int k, uint32_t parity) -> bool {
@@ -370,17 +364,18 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fp4_kernel(const __grid_cons
       const uint64_t dp = tc::smem_desc_sw128(smem_addr(smem + L::kP), 16, 1024);
       // D = 64: O^T has 128 lanes all the same; the upper ones are products with other keys, and nobody reads them
       const uint64_t dv = tc::smem_desc_sw128(smem_addr(smem + L::kV), D == 128 ? L::kVHalf : L::kVHalf / 2, 1024);
+      const uint64_t ones = tc::smem_desc_sw128(smem_addr(smem + L::kOnes), L::kOnesHalf, 1024);
       uint32_t tile = 0, segs = 0;
       bool ok = true;
       while (ok && next_of(walk, P, g)) {
-        const bool both = g.rows * G > kHalf, sums = g.rows * G > kFew;
-        const uint32_t id = both ? kIdBoth : kIdHalf;
+        const bool sums = g.rows * G > kFew;
+        const uint32_t id = g.rows * G > kHalf ? kIdBoth : kIdHalf;
         if (segs > 0) ok = wait(kBarOFree, (segs - 1) & 1);
         ++segs;
         const int n = g.j1 - g.j0;
         for (int i = 0; ok && i < n; ++i, ++tile) {
-          const uint32_t vb = tile % kVB, buf = tile & 1, at = both ? 0 : kHalf * buf;
-          const bool fresh = i < (both ? 1 : 2);   // the first of its sums
+          const uint32_t vb = tile % kVB, buf = tile & 1, at = kN * buf;
+          const bool fresh = i < 2;   // the first of its sums
           ok = wait(kBarValueFull + vb, (tile / kVB) & 1) && wait(kBarP + buf, (tile >> 1) & 1);
           if (!ok) break;
           tc::fence_after_sync();
@@ -389,7 +384,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fp4_kernel(const __grid_cons
             const uint64_t p = dp + ((buf * L::kPBytes + k * 64 * 128) >> 4);
             mma_ss_x4(tmem + T::kO + at, dv + ((vb * L::kVBytes + k * 64 * 128) >> 4), 128, p, 128, id | kMnMajorA,
                       !fresh || k > 0);
-            if (sums) tc::mma_f16_ts_x4(tmem + T::kL + at, tmem + T::kOnes, p, 128, id, !fresh || k > 0);
+            if (sums) mma_ss_x4(tmem + T::kL + at, ones, 0, p, 128, id | kMnMajorA, !fresh || k > 0);
           }
           tc::commit(bar(kBarO + buf));
           tc::commit(bar(kBarValueEmpty + vb));
@@ -504,28 +499,26 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fp4_kernel(const __grid_cons
     const int grp = warp / kGroupWarps, wg = warp % kGroupWarps;
     const int mine = wg * 32 + lane;                  // key of the tile; value of O^T
     const uint32_t lanes = (uint32_t)wg << 21;        // first TMEM lane << 16
-    float* off = reinterpret_cast<float*>(smem + L::kOff) + warp * kHalf;
-    float* red = reinterpret_cast<float*>(smem + L::kRed) + grp * kGroupWarps * kHalf;
+    float* off = reinterpret_cast<float*>(smem + L::kOff) + warp * kN;
+    float* red = reinterpret_cast<float*>(smem + L::kRed) + grp * kGroupWarps * kN;
     auto any_here = [&](bool x) { return any_of(x, 1 + grp, 32 * kGroupWarps); };
     uint32_t tile = 0, segs = 0;
     bool ok = true;
     while (next_of(walk, P, g)) {
       const int rows = g.rows * G;
-      const bool both = rows > kHalf;
-      const int c0 = both ? kHalf * grp : 0, live = both ? clampi(rows - c0, 0, kHalf) : rows;   // the group's rows
-      const float* factors = reinterpret_cast<const float*>(smem + L::kFactors) + segs % kFactorTiles * kN + c0;
+      const float* factors = reinterpret_cast<const float*>(smem + L::kFactors) + segs % kFactorTiles * kN;
       const int j1 = g.j1, n = g.j1 - g.j0, keys = g.keys, first_keys = g.first_keys;
       ++segs;
-      off[lane] = 0.0f;
+      off[lane] = off[kHalf + lane] = 0.0f;
       __syncwarp();
       float sum[kFew] = {}, add[kFew] = {};   // of this thread's weights, and in the tile, where there are few rows
       bool first = true, leave = false;   // leave: the whole group knows that a wait gave up
       for (int j = g.j0; j < j1; ++j, ++tile) {
         const uint32_t buf = tile & 1, phase = (tile >> 1) & 1;
-        if (!both && (int)buf != grp) continue;
+        if ((int)buf != grp) continue;
         const int key = j * kTile + mine;
-        // the first of the group's rows that sees this thread's key
-        const int from = (key >= keys ? kN : max(0, key - first_keys + 1) * G) - c0;
+        // the first row that sees this thread's key
+        const int from = key >= keys ? kN : max(0, key - first_keys + 1) * G;
         const bool hidden = __any_sync(0xffffffffu, from > 0);
         ok = wait_w(kBarS + buf, phase) && ok;
         tc::fence_after_sync();
@@ -534,7 +527,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fp4_kernel(const __grid_cons
         // in as many loops are bound by the instructions' way to them before anything else.)
         auto scores = [&](int r, float (&x)[16]) {
           uint32_t s[16];
-          tc::ld_wait_x16(tmem + lanes + T::kS + kN * buf + c0 + r, s);
+          tc::ld_wait_x16(tmem + lanes + T::kS + kN * buf + r, s);
 #pragma unroll
           for (int q = 0; q < 16; q += 4) {
             const float4 f = *reinterpret_cast<const float4*>(factors + r + q), o = *reinterpret_cast<const float4*>(off + r + q);
@@ -555,7 +548,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fp4_kernel(const __grid_cons
         auto weights = [&]() -> float {
           float most = -INFINITY;
 #pragma unroll 1
-          for (int r = 0; r < live; r += 16) {
+          for (int r = 0; r < rows; r += 16) {
             float x[16];
             scores(r, x);
 #pragma unroll
@@ -568,7 +561,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fp4_kernel(const __grid_cons
                 x[q + 1] = exp2_fast(x[q + 1]);
                 w[q / 2 - 4 * h] = pack2<QMM_F16>(x[q], x[q + 1]);
               }
-              *reinterpret_cast<uint4*>(p + (((c0 + r) / 8 + h) ^ (mine & 7)) * 16) = make_uint4(w[0], w[1], w[2], w[3]);
+              *reinterpret_cast<uint4*>(p + ((r / 8 + h) ^ (mine & 7)) * 16) = make_uint4(w[0], w[1], w[2], w[3]);
             }
             if (rows <= kFew)
 #pragma unroll
@@ -580,51 +573,53 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fp4_kernel(const __grid_cons
           if (set) {
             leave = any_here(!ok);
             if (leave) break;
-            // the rows' maxima of this tile: lane r of each warp gets row r's
-            float top = -INFINITY;
+            // the rows' maxima of this tile
 #pragma unroll 1
-            for (int r = 0; r < live; r += 16) {
-              float x[16];
+            for (int r = 0; r < rows; r += 16) {
+              float x[16], top = -INFINITY;
               scores(r, x);
 #pragma unroll
               for (int q = 0; q < 16; ++q) {
                 const float v = x[q] == x[q] ? x[q] : -INFINITY;
                 const uint32_t b = __float_as_uint(v), up = __reduce_max_sync(0xffffffffu, b & 0x80000000u ? ~b : b | 0x80000000u);
-                if (lane == r + q) top = __uint_as_float(up & 0x80000000u ? up & 0x7FFFFFFFu : ~up);
+                if (lane == q) top = __uint_as_float(up & 0x80000000u ? up & 0x7FFFFFFFu : ~up);
+              }
+              if (lane < 16) red[wg * kN + r + lane] = top;
+            }
+            any_here(false);
+            float keep[2] = {1.0f, 1.0f};   // of rows lane and kHalf + lane
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const int r = kHalf * h + lane;
+              if (r < rows) {
+                const float top = fmaxf(fmaxf(red[r], red[kN + r]), fmaxf(red[2 * kN + r], red[3 * kN + r]));
+                // a row that sees no key of the group's first tile sees none of its later ones
+                const float was = off[r];
+                const float now = top > -INFINITY && (first || top > kLift + kGrow) ? was - (top - kLift) : was;
+                keep[h] = exp2_fast(now - was);
+                off[r] = now;
               }
             }
-            red[wg * kHalf + lane] = top;
-            any_here(false);
-#pragma unroll
-            for (int w = 0; w < kGroupWarps; ++w) top = fmaxf(top, red[w * kHalf + lane]);
-            // a row that sees no key of the group's first tile sees none of its later ones
-            const float was = off[lane];
-            const float now = top > -INFINITY && (first || top > kLift + kGrow) ? was - (top - kLift) : was;
-            const float keep = exp2_fast(now - was);
             __syncwarp();
-            off[lane] = now;
-            __syncwarp();
-            if (!first) {
-              // O^T and l, once the products of the group's tile before are in them
-              ok = wait_w(kBarO + (both ? buf ^ 1 : buf), both ? ((tile - 1) >> 1) & 1 : phase ^ 1) && ok;
-              tc::fence_after_sync();
+            if (!first) {   // O^T and l: the products of the group's tile before are in them
 #pragma unroll 1
-              for (int r0 = 0; r0 < live; r0 += 8) {
+              for (int r0 = 0; r0 < rows; r0 += 8) {
                 uint32_t o[8], l[8];
-                tc::ld_wait_x8(tmem + lanes + T::kO + kHalf * grp + r0, o);
-                tc::ld_wait_x8(tmem + lanes + T::kL + kHalf * grp + r0, l);
+                tc::ld_wait_x8(tmem + lanes + T::kO + kN * grp + r0, o);
+                tc::ld_wait_x8(tmem + lanes + T::kL + kN * grp + r0, l);
+                const float of = r0 < kHalf ? keep[0] : keep[1];
 #pragma unroll
                 for (int r = 0; r < 8; ++r) {
-                  const float k = __shfl_sync(0xffffffffu, keep, r0 + r);
+                  const float k = __shfl_sync(0xffffffffu, of, (r0 & (kHalf - 1)) + r);
                   o[r] = __float_as_uint(__uint_as_float(o[r]) * k);
                   l[r] = __float_as_uint(__uint_as_float(l[r]) * k);
                 }
-                tc::st_x8(tmem + lanes + T::kO + kHalf * grp + r0, o);
-                tc::st_x8(tmem + lanes + T::kL + kHalf * grp + r0, l);
+                tc::st_x8(tmem + lanes + T::kO + kN * grp + r0, o);
+                tc::st_x8(tmem + lanes + T::kL + kN * grp + r0, l);
               }
               tc::wait_st();
 #pragma unroll
-              for (int r = 0; r < kFew; ++r) sum[r] *= __shfl_sync(0xffffffffu, keep, r);
+              for (int r = 0; r < kFew; ++r) sum[r] *= __shfl_sync(0xffffffffu, keep[0], r);
             }
           }
           const float most = weights();
@@ -641,10 +636,6 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fp4_kernel(const __grid_cons
         if (lane == 0) {
           mbar_arrive(bar(kBarP + buf));
           mbar_arrive(bar(kBarSFree + buf));
-          if (!both) {   // (the other group has no part in it)
-            mbar_arrive(bar(kBarP + buf));
-            mbar_arrive(bar(kBarSFree + buf));
-          }
         }
       }
 
@@ -659,70 +650,65 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fp4_kernel(const __grid_cons
           for (int o = 16; o >= 1; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
           if (lane == r) own = v;
         }
-        red[wg * kHalf + lane] = own;
+        red[wg * kN + lane] = own;
       }
       if (any_of(!ok || leave, 3, 64 * kGroupWarps)) break;
       tc::fence_after_sync();
-      // Lane r has row r of the group (of both groups' sums, where they had the tiles in turn): its sum, its
-      // exponent, what the groups' sums count, and where its record lies.
-      const uint32_t tO = tmem + lanes + T::kO, tL = tmem + lanes + T::kL;
+      // Each group joins both groups' sums of half of the rows, from c0 on; lane r has row c0 + r: its sum, its exponent, what
+      // the groups' sums count, and where its record lies.
+      const int half = (rows + 15) / 16 * 8, c0 = grp * half, live = grp ? max(0, rows - half) : min(half, rows);
+      const int row = min(c0 + lane, kN - 1);
+      const uint32_t tO = tmem + lanes + T::kO + c0, tL = tmem + lanes + T::kL + c0;
       auto sum_of = [&](int gr) -> float {
-        const float* x = reinterpret_cast<const float*>(smem + L::kRed) + gr * kGroupWarps * kHalf + lane;
-        if (rows <= kFew) return (x[0] + x[kHalf]) + (x[2 * kHalf] + x[3 * kHalf]);
+        const float* x = reinterpret_cast<const float*>(smem + L::kRed) + gr * kGroupWarps * kN + row;
+        if (rows <= kFew) return (x[0] + x[kN]) + (x[2 * kN] + x[3 * kN]);
         float l = 0.0f;
 #pragma unroll 1
         for (int r0 = 0; r0 < live; r0 += 8) {
           uint32_t o[8];
-          tc::ld_wait_x8(tL + kHalf * gr + r0, o);
+          tc::ld_wait_x8(tL + kN * gr + r0, o);
 #pragma unroll
           for (int r = 0; r < 8; ++r)
             if (lane == r0 + r) l = __uint_as_float(o[r]);
         }
         return l;
       };
-      const float* offs = reinterpret_cast<const float*>(smem + L::kOff) + lane;
-      float f[2] = {1.0f, 0.0f}, all = 0.0f, top = -INFINITY;
+      const float* offs = reinterpret_cast<const float*>(smem + L::kOff) + row;
+      float f[2] = {0.0f, 0.0f}, all = 0.0f, top = -INFINITY;
 #pragma unroll 1
-      for (int k = both ? grp : 0; k < (both ? grp + 1 : 2); ++k) {
-        const bool has = both || n > 1 || (int)((tile - 1) & 1) == k;   // (a group without a tile has no sums)
-        const float l = has ? sum_of(k) : 0.0f, t = -offs[k * kGroupWarps * kHalf];
+      for (int k = 0; k < 2; ++k) {
+        const bool has = n > 1 || (int)((tile - 1) & 1) == k;   // (a group without a tile has no sums)
+        const float l = has ? sum_of(k) : 0.0f, t = -offs[k * kGroupWarps * kN];
         if (l != 0.0f) {   // (NaN counts)
           const float best = fmaxf(top, t), w = exp2_fast(t - best), was = exp2_fast(top - best);
           all = all * was + l * w;
-          f[0] = k == 0 || both ? w : f[0] * was;
-          f[1] = k == 0 || both ? 0.0f : w;
+          f[0] = k == 0 ? w : f[0] * was;
+          f[1] = k == 0 ? 0.0f : w;
           top = best;
-        } else if (k == 0 && !both) {
-          f[0] = 0.0f;
         }
       }
       const bool inside = g.j0 > 0;   // not the first segment of its group: the CTA's own record
-      const int row = c0 + lane, tok = (int)((uint32_t)row / (uint32_t)G);
+      const int tok = (int)((uint32_t)row / (uint32_t)G);
       const int64_t record = inside ? (int64_t)blockIdx.x * 2 * kRows + row
                                     : ((int64_t)(g.own ? a.T : 0) + g.t0 + tok) * a.Hq + (int64_t)g.h * G + row - tok * G;
-      if (wg == 0 && (both || grp == 0) && lane < live) {
+      if (wg == 0 && lane < live) {
         const uint32_t per = (uint32_t)min(M.piece.per, (int64_t)0x7fffffff);
         const uint32_t others = g.rest > 0 ? ((uint32_t)g.rest + per - 1) / per : 0;
         const uint32_t odd = *reinterpret_cast<volatile uint32_t*>(&M.odd[segs & 7]) == segs;
         (inside ? P.s_cta : P.s_rows)[record] = RowStat{top, all, odd, others << 16 | (blockIdx.x + 1)};
       }
-      // O^T: this thread's value of every row (of both groups' sums, half the rows a group), at the place where the
-      // combine launch looks for it (column_of)
+      // O^T: this thread's value of every row, at the place where the combine launch looks for it (column_of)
       float* out = (inside ? P.o_cta : P.o_rows) + (mine & ~31) + 8 * (mine >> 1 & 3) + 2 * (mine >> 3 & 3) + (mine & 1);
-      const int r1 = both ? live : min(live, 16 * grp + 16);
 #pragma unroll 1
-      for (int r0 = both ? 0 : 16 * grp; r0 < r1; r0 += 8) {
+      for (int r0 = 0; r0 < live; r0 += 8) {
         uint32_t o[8], o1[8];
-        tc::ld_wait_x8(tO + (both ? kHalf * grp : 0) + r0, o);
-        if (!both) tc::ld_wait_x8(tO + kHalf + r0, o1);
+        tc::ld_wait_x8(tO + r0, o);
+        tc::ld_wait_x8(tO + kN + r0, o1);
 #pragma unroll
         for (int r = 0; r < 8; ++r) {
           const int64_t at = __shfl_sync(0xffffffffu, record, r0 + r) * D;
-          float v = __uint_as_float(o[r]);
-          if (!both) {
-            const float u = __shfl_sync(0xffffffffu, f[0], r0 + r), w = __shfl_sync(0xffffffffu, f[1], r0 + r);
-            v = (u != 0.0f ? v * u : 0.0f) + (w != 0.0f ? __uint_as_float(o1[r]) * w : 0.0f);
-          }
+          const float u = __shfl_sync(0xffffffffu, f[0], r0 + r), w = __shfl_sync(0xffffffffu, f[1], r0 + r);
+          const float v = (u != 0.0f ? __uint_as_float(o[r]) * u : 0.0f) + (w != 0.0f ? __uint_as_float(o1[r]) * w : 0.0f);
           if (r0 + r < live && mine < D) out[at] = v;
         }
       }
