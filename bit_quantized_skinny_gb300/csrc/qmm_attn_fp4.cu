@@ -48,7 +48,9 @@ constexpr int kFew = 8;              // rows whose weights a softmax thread adds
 constexpr int kLoadWarp = 8, kScoreWarp = 9, kQWarp = 10, kSumWarp = 11, kKeyWarp = 12, kValueWarp = 16;
 constexpr int kThreads = 20 * 32, kGroupWarps = 4;
 constexpr uint32_t kTmemCols = 512;
-constexpr int kKeyBufs = 2;          // tiles of keys in tensor memory
+constexpr int kKeyBufs = 3;          // of 64 values of a tile's keys, in tensor memory
+constexpr int kScoreBufs = 4;        // two for each group
+constexpr int kOnesN = 16;           // columns of l, all the same
 constexpr int kPacks = 9;            // packed tiles in shared memory: of keys and of values in turn
 constexpr int kFactorTiles = 8;      // (the softmax is a few query tiles behind)
 constexpr float kGrow = 8.0f;
@@ -68,9 +70,9 @@ struct Smem {
   static constexpr int kV = 0;
   static constexpr int kQ = kV + kValueBufs * kVBytes;
   static constexpr int kP = kQ + 2 * kQBytes;
-  static constexpr int kOnes = kP + 2 * kPBytes;         // 16 keys of 128 ones
-  static constexpr int kOnesHalf = 16 * 128;
-  static constexpr int kPack = kOnes + 2 * kOnesHalf;
+  static constexpr int kOnes = kP + 2 * kPBytes;         // 64 keys of kOnesN ones
+  static constexpr int kOnesBytes = kOnesN * 128;
+  static constexpr int kPack = kOnes + kOnesBytes;
   static constexpr int kFactors = kPack + kPacks * kPackBytes;   // of the rows of the last kFactorTiles query tiles
   static constexpr int kOff = kFactors + kFactorTiles * kN * 4;  // each softmax warp's copy of its group's rows' off
   static constexpr int kRed = kOff + 2 * kGroupWarps * kN * 4;   // the softmax warps' maxima of the rows
@@ -79,19 +81,18 @@ struct Smem {
 };
 static_assert(Smem<128>::kTotal <= 227 * 1024 && Smem<64>::kTotal <= 227 * 1024, "shared memory");
 
-// Tensor memory: K at 0, then S^T, O^T and l, one for each group.
-template <int D>
+// Tensor memory: K at 0, then S^T (tile t's in t % kScoreBufs), O^T and l of each group.  (l has the rows as its lanes.)
 struct Tmem {
-  static constexpr uint32_t kS = kKeyBufs * D / 2, kO = kS + 2 * kN, kL = kO + 2 * kN;
-  static_assert(kL + 2 * kN <= kTmemCols, "tensor memory");
+  static constexpr uint32_t kS = kKeyBufs * 32, kO = kS + kScoreBufs * kN, kL = kO + 2 * kN;
+  static_assert(kL + 2 * kOnesN <= kTmemCols, "tensor memory");
 };
 
 // Barriers; a wait tells a phase from the one after it only, and every wait here is for the phase of a tile (or a segment)
 // of whose successor on the same barrier the waiting role itself is a condition.
 enum : int {
   kBarPackFull = 0, kBarPackEmpty = 10, kBarKeyFull = 20, kBarKeyEmpty = 24 /* 20 + and 24 + buffer */, kBarValueFull = 28, kBarValueEmpty = 31,
-  kBarS = 34, kBarSFree = 36, kBarP = 38, kBarO = 40 /* products of a tile's values are done */, kBarQFull = 42,
-  kBarQEmpty = 44, kBarOFree = 46, kBarDrain = 47 /* and 48 */, kBars = 49
+  kBarS = 34, kBarSFree = 38, kBarP = 42, kBarO = 44 /* products of a tile's values are done */, kBarQFull = 46,
+  kBarQEmpty = 48, kBarOFree = 50, kBarDrain = 51 /* and 52 */, kBars = 53
 };
 
 struct Misc {
@@ -169,7 +170,7 @@ template <int D, int TYPE>
 __global__ void __launch_bounds__(kThreads, 1) attn_fp4_kernel(const __grid_constant__ Common P) {
   extern __shared__ __align__(1024) uint8_t smem[];
   using L = Smem<D>;
-  using T = Tmem<D>;
+  using T = Tmem;
   constexpr uint32_t kVB = L::kValueBufs;
   const qmm_attn_args& a = P.a;
   Misc& M = *reinterpret_cast<Misc*>(smem + L::kMisc);
@@ -196,7 +197,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fp4_kernel(const __grid_cons
   }
   // Launched early (behind a launch that allows it), this grid reads what was written before it from
   // here on; the combine launch, which reads the lengths before its own wait, may start from here on.
-  for (int k = threadIdx.x; k < L::kOnesHalf / 2; k += kThreads)
+  for (int k = threadIdx.x; k < L::kOnesBytes / 4; k += kThreads)
     reinterpret_cast<uint32_t*>(smem + L::kOnes)[k] = 0x3C003C00u;
   fence_proxy_async_smem();
   asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -329,24 +330,26 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fp4_kernel(const __grid_cons
     if (elect_one()) {
       constexpr uint32_t kIdBoth = tc::idesc_16_f32(128, kN, false, false), kIdHalf = tc::idesc_16_f32(128, kHalf, false, false);
       const uint64_t dq = tc::smem_desc_sw128(smem_addr(smem + L::kQ), 16, 1024);
-      uint32_t tile = 0, segs = 0;
+      uint32_t tile = 0, unit = 0, segs = 0;
       bool ok = true;
       while (ok && next_of(walk, P, g)) {
         const uint32_t slot = segs & 1, id = g.rows * G > kHalf ? kIdBoth : kIdHalf;
         ok = wait(kBarQFull + slot, (segs >> 1) & 1);
         ++segs;
         for (int left = g.j1 - g.j0; ok && left > 0; --left, ++tile) {
-          const uint32_t kb = tile % kKeyBufs, buf = tile & 1;
-          ok = wait(kBarKeyFull + kb, (tile / kKeyBufs) & 1);
-          if (tile >= 2) ok = ok && wait(kBarSFree + buf, ((tile >> 1) - 1) & 1);
+          const uint32_t buf = tile % kScoreBufs;
+          if (tile >= kScoreBufs) ok = wait(kBarSFree + buf, (tile / kScoreBufs - 1) & 1);
+#pragma unroll 1
+          for (uint32_t k = 0; ok && k < D / 64; ++k, ++unit) {   // 64 values of the head: 4 MMAs, 8 columns and 32 bytes of each row further
+            const uint32_t kb = unit % kKeyBufs;
+            ok = wait(kBarKeyFull + kb, (unit / kKeyBufs) & 1);
+            if (!ok) break;
+            tc::fence_after_sync();
+            tc::mma_f16_ts_x4(tmem + T::kS + kN * buf, tmem + 32 * kb, dq + ((slot * L::kQBytes + k * L::kQHalf) >> 4), 2, id, k > 0);
+            tc::commit(bar(kBarKeyEmpty + kb));
+          }
           if (!ok) break;
-          tc::fence_after_sync();
-#pragma unroll
-          for (int k = 0; k < D / 64; ++k)   // 64 values of the head: 4 MMAs, 8 columns and 32 bytes of each row further
-            tc::mma_f16_ts_x4(tmem + T::kS + kN * buf, tmem + kb * (D / 2) + 32 * k,
-                              dq + ((slot * L::kQBytes + k * L::kQHalf) >> 4), 2, id, k > 0);
           tc::commit(bar(kBarS + buf));
-          tc::commit(bar(kBarKeyEmpty + kb));
           if (left == 1) tc::commit(bar(kBarQEmpty + slot));
         }
       }
@@ -364,7 +367,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fp4_kernel(const __grid_cons
       const uint64_t dp = tc::smem_desc_sw128(smem_addr(smem + L::kP), 16, 1024);
       // D = 64: O^T has 128 lanes all the same; the upper ones are products with other keys, and nobody reads them
       const uint64_t dv = tc::smem_desc_sw128(smem_addr(smem + L::kV), D == 128 ? L::kVHalf : L::kVHalf / 2, 1024);
-      const uint64_t ones = tc::smem_desc_sw128(smem_addr(smem + L::kOnes), L::kOnesHalf, 1024);
+      // l = p 1^T: p as the 128-row operand, whose upper rows (the next eight keys, and 1 KB behind p) nobody reads
+      constexpr uint32_t kIdSum = tc::idesc_16_f32(128, kOnesN, false, false) | kMnMajorA;
+      const uint64_t dpa = tc::smem_desc_sw128(smem_addr(smem + L::kP), 1024, 1024);
+      const uint64_t ones = tc::smem_desc_sw128(smem_addr(smem + L::kOnes), 16, 1024);
       uint32_t tile = 0, segs = 0;
       bool ok = true;
       while (ok && next_of(walk, P, g)) {
@@ -374,17 +380,17 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fp4_kernel(const __grid_cons
         ++segs;
         const int n = g.j1 - g.j0;
         for (int i = 0; ok && i < n; ++i, ++tile) {
-          const uint32_t vb = tile % kVB, buf = tile & 1, at = kN * buf;
+          const uint32_t vb = tile % kVB, buf = tile & 1;
           const bool fresh = i < 2;   // the first of its sums
           ok = wait(kBarValueFull + vb, (tile / kVB) & 1) && wait(kBarP + buf, (tile >> 1) & 1);
           if (!ok) break;
           tc::fence_after_sync();
 #pragma unroll
           for (int k = 0; k < 2; ++k) {   // 64 keys: 4 MMAs of 16 rows of V and of p
-            const uint64_t p = dp + ((buf * L::kPBytes + k * 64 * 128) >> 4);
-            mma_ss_x4(tmem + T::kO + at, dv + ((vb * L::kVBytes + k * 64 * 128) >> 4), 128, p, 128, id | kMnMajorA,
+            const uint32_t p = (buf * L::kPBytes + k * 64 * 128) >> 4;
+            mma_ss_x4(tmem + T::kO + kN * buf, dv + ((vb * L::kVBytes + k * 64 * 128) >> 4), 128, dp + p, 128, id | kMnMajorA,
                       !fresh || k > 0);
-            if (sums) mma_ss_x4(tmem + T::kL + at, ones, 0, p, 128, id | kMnMajorA, !fresh || k > 0);
+            if (sums) mma_ss_x4(tmem + T::kL + kOnesN * buf, dpa + p, 128, ones, 0, kIdSum, !fresh || k > 0);
           }
           tc::commit(bar(kBarO + buf));
           tc::commit(bar(kBarValueEmpty + vb));
@@ -400,40 +406,36 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fp4_kernel(const __grid_cons
     // is masked by position.)
     const int key = (warp - kKeyWarp) * 32 + lane;
     const uint32_t lanes = (uint32_t)(warp - kKeyWarp) << 21;   // first TMEM lane << 16
-    uint32_t tile = 0;
+    uint32_t tile = 0, unit = 0;
     bool ok = true;
     while (ok && next_of(walk, P, g)) {
       const int j1 = g.j1;
       for (int j = g.j0; j < j1; ++j, ++tile) {
-        const uint32_t from = 2 * tile % kPacks, kb = tile % kKeyBufs;
-        ok = wait(kBarPackFull + from, (2 * tile / kPacks) & 1) &&
-             (tile < kKeyBufs || wait(kBarKeyEmpty + kb, (tile / kKeyBufs - 1) & 1));
-        ok = __all_sync(0xffffffffu, ok);
-        if (!ok) break;
-        tc::fence_after_sync();
+        const uint32_t from = 2 * tile % kPacks;
+        ok = wait_w(kBarPackFull + from, (2 * tile / kPacks) & 1);
         const uint8_t* src = smem + L::kPack + from * L::kPackBytes;
-        uint4 code[D / 32];
-        uint32_t scale[D / 64];
-#pragma unroll
-        for (int q = 0; q < D / 32; ++q) code[q] = *reinterpret_cast<const uint4*>(src + key * (D / 2) + 16 * q);
-#pragma unroll
-        for (int q = 0; q < D / 64; ++q)
-          scale[q] = *reinterpret_cast<const uint32_t*>(src + kTile * (D / 2) + key * (D / 16) + 4 * q);
-#pragma unroll
-        for (int q = 0; q < D / 32; ++q) {   // two blocks
-          uint32_t h[16];
-          const uint32_t two = scale[q / 2] >> (16 * (q & 1));
-          to_half<0>(make_uint2(code[q].x, code[q].y), e4m3x2_pair(__byte_perm(two, 0, 0x00)), h);
-          to_half<8>(make_uint2(code[q].z, code[q].w), e4m3x2_pair(__byte_perm(two, 0, 0x11)), h);
-          tc::st_x16(tmem + lanes + kb * (D / 2) + 16 * q, h);
+#pragma unroll 1
+        for (int half = 0; ok && half < D / 64; ++half, ++unit) {
+          const uint32_t kb = unit % kKeyBufs;
+          ok = unit < kKeyBufs || wait_w(kBarKeyEmpty + kb, (unit / kKeyBufs - 1) & 1);
+          if (!ok) break;
+          tc::fence_after_sync();
+#pragma unroll 1
+          for (int q = 0; q < 2; ++q) {   // two blocks
+            const uint4 code = *reinterpret_cast<const uint4*>(src + key * (D / 2) + 32 * half + 16 * q);
+            const uint32_t two = *reinterpret_cast<const uint16_t*>(src + kTile * (D / 2) + key * (D / 16) + 4 * half + 2 * q);
+            uint32_t h[16];
+            to_half<0>(make_uint2(code.x, code.y), e4m3x2_pair(__byte_perm(two, 0, 0x00)), h);
+            to_half<8>(make_uint2(code.z, code.w), e4m3x2_pair(__byte_perm(two, 0, 0x11)), h);
+            tc::st_x16(tmem + lanes + 32 * kb + 16 * q, h);
+          }
+          tc::wait_st();
+          tc::fence_before_sync();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(kBarKeyFull + kb));
         }
-        tc::wait_st();
-        tc::fence_before_sync();
-        __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(bar(kBarKeyFull + kb));
-          mbar_arrive(bar(kBarPackEmpty + from));
-        }
+        if (!ok) break;
+        if (lane == 0) mbar_arrive(bar(kBarPackEmpty + from));
       }
     }
   } else if (warp >= kValueWarp) {
@@ -456,36 +458,35 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fp4_kernel(const __grid_cons
         const uint8_t* src = smem + L::kPack + from * L::kPackBytes;
         uint8_t* dst = smem + L::kV + vb * L::kVBytes;
         const int base = j * kTile;
-        uint2 code[kUnits];
-        uint32_t scale[kUnits];
-        auto key_of = [&](int u) { return u / kHalves * 32 + me / 4; };
-        auto block_of = [&](int u) { return u % kHalves * 4 + me % 4; };
+        // zeros behind the last key, and for the NaN blocks of keys that not every row sees
+        const bool check = base + kTile > clean_from;
+        bool odd = false;
+#pragma unroll 1
+        for (int u0 = 0; u0 < kUnits; u0 += 2) {
+          uint2 code[2];
+          uint32_t scale[2];
 #pragma unroll
-        for (int u = 0; u < kUnits; ++u) {
-          code[u] = *reinterpret_cast<const uint2*>(src + key_of(u) * (D / 2) + block_of(u) * 8);
-          scale[u] = src[kTile * (D / 2) + key_of(u) * kBlocks + block_of(u)];
-        }
-        if (base + kTile > clean_from) {   // zeros behind the last key, and for the NaN blocks of keys that not every row sees
-          bool odd = false;
-#pragma unroll
-          for (int u = 0; u < kUnits; ++u) {
-            const int key = base + key_of(u);
-            const bool nan = (scale[u] & 0x7Fu) == kv4::kScaleNaN && key >= clean_from && key < keys;
-            odd |= nan;
-            if (nan || key >= keys) scale[u] = 0;
+          for (int e = 0; e < 2; ++e) {
+            const int u = u0 + e, key = u / kHalves * 32 + me / 4, block = u % kHalves * 4 + me % 4;
+            code[e] = *reinterpret_cast<const uint2*>(src + key * (D / 2) + block * 8);
+            scale[e] = src[kTile * (D / 2) + key * kBlocks + block];
+            if (check) {
+              const bool nan = (scale[e] & 0x7Fu) == kv4::kScaleNaN && base + key >= clean_from && base + key < keys;
+              odd |= nan;
+              if (nan || base + key >= keys) scale[e] = 0;
+            }
           }
-          if (odd) *reinterpret_cast<volatile uint32_t*>(&M.odd[segs & 7]) = segs;
-        }
 #pragma unroll
-        for (int u = 0; u < kUnits; ++u) {
-          uint32_t h[8];
-          to_half<0>(code[u], e4m3x2_pair(scale[u] * 0x101u), h);
-          const int key = key_of(u);
-          uint8_t* row = dst + (u % kHalves) * L::kVHalf + key * 128;
-          const int c0 = 2 * (me % 4);
-          *reinterpret_cast<uint4*>(row + (c0 ^ (key & 7)) * 16) = make_uint4(h[0], h[1], h[2], h[3]);
-          *reinterpret_cast<uint4*>(row + ((c0 + 1) ^ (key & 7)) * 16) = make_uint4(h[4], h[5], h[6], h[7]);
+          for (int e = 0; e < 2; ++e) {
+            const int u = u0 + e, key = u / kHalves * 32 + me / 4, c0 = 2 * (me % 4);
+            uint32_t h[8];
+            to_half<0>(code[e], e4m3x2_pair(scale[e] * 0x101u), h);
+            uint8_t* row = dst + (u % kHalves) * L::kVHalf + key * 128;
+            *reinterpret_cast<uint4*>(row + (c0 ^ (key & 7)) * 16) = make_uint4(h[0], h[1], h[2], h[3]);
+            *reinterpret_cast<uint4*>(row + ((c0 + 1) ^ (key & 7)) * 16) = make_uint4(h[4], h[5], h[6], h[7]);
+          }
         }
+        if (odd) *reinterpret_cast<volatile uint32_t*>(&M.odd[segs & 7]) = segs;
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) {
@@ -514,20 +515,20 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fp4_kernel(const __grid_cons
       float sum[kFew] = {}, add[kFew] = {};   // of this thread's weights, and in the tile, where there are few rows
       bool first = true, leave = false;   // leave: the whole group knows that a wait gave up
       for (int j = g.j0; j < j1; ++j, ++tile) {
-        const uint32_t buf = tile & 1, phase = (tile >> 1) & 1;
+        const uint32_t buf = tile & 1, phase = (tile >> 1) & 1, at = tile % kScoreBufs;
         if ((int)buf != grp) continue;
         const int key = j * kTile + mine;
         // the first row that sees this thread's key
         const int from = key >= keys ? kN : max(0, key - first_keys + 1) * G;
         const bool hidden = __any_sync(0xffffffffu, from > 0);
-        ok = wait_w(kBarS + buf, phase) && ok;
+        ok = wait_w(kBarS + at, (tile / kScoreBufs) & 1) && ok;
         tc::fence_after_sync();
         if (tile >= 2) ok = wait_w(kBarO + buf, phase ^ 1) && ok;   // the last readers of this p
         // sixteen rows' scores in units of log2, plus off.  (The loops over them are not unrolled: five warps a scheduler
         // in as many loops are bound by the instructions' way to them before anything else.)
         auto scores = [&](int r, float (&x)[16]) {
           uint32_t s[16];
-          tc::ld_wait_x16(tmem + lanes + T::kS + kN * buf + r, s);
+          tc::ld_wait_x16(tmem + lanes + T::kS + kN * at + r, s);
 #pragma unroll
           for (int q = 0; q < 16; q += 4) {
             const float4 f = *reinterpret_cast<const float4*>(factors + r + q), o = *reinterpret_cast<const float4*>(off + r + q);
@@ -604,18 +605,20 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fp4_kernel(const __grid_cons
             if (!first) {   // O^T and l: the products of the group's tile before are in them
 #pragma unroll 1
               for (int r0 = 0; r0 < rows; r0 += 8) {
-                uint32_t o[8], l[8];
+                uint32_t o[8];
                 tc::ld_wait_x8(tmem + lanes + T::kO + kN * grp + r0, o);
-                tc::ld_wait_x8(tmem + lanes + T::kL + kN * grp + r0, l);
                 const float of = r0 < kHalf ? keep[0] : keep[1];
 #pragma unroll
-                for (int r = 0; r < 8; ++r) {
-                  const float k = __shfl_sync(0xffffffffu, of, (r0 & (kHalf - 1)) + r);
-                  o[r] = __float_as_uint(__uint_as_float(o[r]) * k);
-                  l[r] = __float_as_uint(__uint_as_float(l[r]) * k);
-                }
+                for (int r = 0; r < 8; ++r)
+                  o[r] = __float_as_uint(__uint_as_float(o[r]) * __shfl_sync(0xffffffffu, of, (r0 & (kHalf - 1)) + r));
                 tc::st_x8(tmem + lanes + T::kO + kN * grp + r0, o);
-                tc::st_x8(tmem + lanes + T::kL + kN * grp + r0, l);
+              }
+              if (rows > kFew && wg < 2) {   // (its first column is read in the end)
+                uint32_t l[8];
+                tc::ld_wait_x8(tmem + lanes + T::kL + kOnesN * grp, l);
+#pragma unroll
+                for (int r = 0; r < 8; ++r) l[r] = __float_as_uint(__uint_as_float(l[r]) * (wg ? keep[1] : keep[0]));
+                tc::st_x8(tmem + lanes + T::kL + kOnesN * grp, l);
               }
               tc::wait_st();
 #pragma unroll
@@ -635,12 +638,15 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fp4_kernel(const __grid_cons
         __syncwarp();
         if (lane == 0) {
           mbar_arrive(bar(kBarP + buf));
-          mbar_arrive(bar(kBarSFree + buf));
+          mbar_arrive(bar(kBarSFree + at));
         }
       }
 
       // ---- the segment's sums to the workspace
-      if (!leave) ok = wait_w(kBarO + ((tile - 1) & 1), ((tile - 1) >> 1) & 1) && ok;   // (and with these products all before)
+      // (the products of the group's last tile, and with them all before; of the other group's barrier this one could take a
+      // phase for the one after it)
+      const uint32_t last = tile - 1 - ((tile - 1 - grp) & 1);
+      if (!leave && (n > 1 || last == tile - 1)) ok = wait_w(kBarO + grp, (last >> 1) & 1) && ok;
       if (rows <= kFew) {
         float own = 0.0f;   // lane r: row r's over the warp
 #pragma unroll
@@ -651,6 +657,11 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fp4_kernel(const __grid_cons
           if (lane == r) own = v;
         }
         red[wg * kN + lane] = own;
+      } else if (wg < 2) {   // lane r: row kHalf wg + r's
+        uint32_t l[8];
+        tc::fence_after_sync();
+        tc::ld_wait_x8(tmem + lanes + T::kL + kOnesN * grp, l);
+        red[kHalf * wg + lane] = __uint_as_float(l[0]);
       }
       if (any_of(!ok || leave, 3, 64 * kGroupWarps)) break;
       tc::fence_after_sync();
@@ -658,20 +669,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fp4_kernel(const __grid_cons
       // the groups' sums count, and where its record lies.
       const int half = (rows + 15) / 16 * 8, c0 = grp * half, live = grp ? max(0, rows - half) : min(half, rows);
       const int row = min(c0 + lane, kN - 1);
-      const uint32_t tO = tmem + lanes + T::kO + c0, tL = tmem + lanes + T::kL + c0;
+      const uint32_t tO = tmem + lanes + T::kO + c0;
       auto sum_of = [&](int gr) -> float {
         const float* x = reinterpret_cast<const float*>(smem + L::kRed) + gr * kGroupWarps * kN + row;
-        if (rows <= kFew) return (x[0] + x[kN]) + (x[2 * kN] + x[3 * kN]);
-        float l = 0.0f;
-#pragma unroll 1
-        for (int r0 = 0; r0 < live; r0 += 8) {
-          uint32_t o[8];
-          tc::ld_wait_x8(tL + kN * gr + r0, o);
-#pragma unroll
-          for (int r = 0; r < 8; ++r)
-            if (lane == r0 + r) l = __uint_as_float(o[r]);
-        }
-        return l;
+        return rows <= kFew ? (x[0] + x[kN]) + (x[2 * kN] + x[3 * kN]) : x[0];
       };
       const float* offs = reinterpret_cast<const float*>(smem + L::kOff) + row;
       float f[2] = {0.0f, 0.0f}, all = 0.0f, top = -INFINITY;
