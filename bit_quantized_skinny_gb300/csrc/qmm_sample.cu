@@ -292,14 +292,38 @@ struct Sampler {
   // weights (N u64, kBins / 2).
   template <class N, class In, class Bin>
   __device__ __forceinline__ void histogram(In&& in, Bin&& bin) {
-    N* count = reinterpret_cast<N*>(S.count);
     for (int b = threadIdx.x; b < kBins; b += kThreads) S.count[b] = 0;
-    __syncthreads();
-    each([&](float v, int i) {
-      if (!in(v, i)) return;
-      if constexpr (sizeof(N) == 4) atomicAdd(&count[bin(v)], 1u);
-      else atomicAdd(&count[bin(v)], weight_of(v));
-    });
+    if constexpr (sizeof(N) == 4) {
+      __syncthreads();
+      each([&](float v, int i) {
+        if (in(v, i)) atomicAdd(&S.count[bin(v)], 1u);
+      });
+    } else {
+      // A weight in three parts of 14 bits, which 32 bits of a bin hold the sums of: shared memory adds these by itself, and
+      // 64 bits by a loop of compares (128 rows of 248320 with top_p alone 850 us; parts, with one pass less, see below).
+      constexpr int kHalfBins = kBins / 2;
+      static_assert((int64_t)kMaxRun * kThreads < (1 << 17), "sums of parts");
+      for (int b = threadIdx.x; b < kHalfBins; b += kThreads) S.total[b] = 0;
+      __syncthreads();
+      each([&](float v, int i) {
+        if (!in(v, i)) return;
+        const u64 w = weight_of(v);
+        const int b = bin(v);
+        if (const uint32_t part = (uint32_t)w & 0x3FFFu) atomicAdd(&S.count[b], part);
+        if (const uint32_t part = (uint32_t)(w >> 14) & 0x3FFFu) atomicAdd(&S.count[kHalfBins + b], part);
+        if (const uint32_t part = (uint32_t)(w >> 28)) atomicAdd(&S.total[b], part);
+      });
+      __syncthreads();
+      u64 sum[kHalfBins / kThreads];
+#pragma unroll
+      for (int q = 0; q < kHalfBins / kThreads; ++q) {
+        const int b = q * kThreads + threadIdx.x;
+        sum[q] = S.count[b] + ((u64)S.count[kHalfBins + b] << 14) + ((u64)S.total[b] << 28);
+      }
+      __syncthreads();
+#pragma unroll
+      for (int q = 0; q < kHalfBins / kThreads; ++q) S.mass[q * kThreads + threadIdx.x] = sum[q];
+    }
     join<N>();
   }
   // Counts of bin(v) of one value of each thread, in the same way.
@@ -330,6 +354,15 @@ struct Sampler {
       if (C == 1) total[b] = sum;
     }
     sync();
+  }
+  // All weights, from the cluster's bins.
+  __device__ __forceinline__ u64 mass_of_bins() {
+    constexpr int kMine = kBins / 2 / kThreads;
+    u64 sum = 0, all;
+#pragma unroll
+    for (int q = 0; q < kMine; ++q) sum += S.mass_total[kMine * threadIdx.x + q];
+    block_before(sum, &all);
+    return all;
   }
   // The first bin whose sums reach n >= 1, with those before it.
   template <class N>
@@ -685,27 +718,24 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
     cut = r.lo;
   }
   if (by_p) {
-    u64 all = 0;
-    R.each([&](float v, int i) { if (in(v, i)) all += R.weight_of(v); });
-    all = R.cluster_sum(all);
+    // The top alone weighs 1, so tokens of less than (1 - top_p) / V cannot make up what may go: the border is within
+    // `reach` of the top, and so are all bins but the last one, which has what lies further down too.
+    const float reach = log2f((float)V / (1.0f - fmaxf(p, 0.0f))) * 1.001f / R.c.hi;
+    bins_over(fminf(reach, distance_to(R.floor)));
+    R.histogram<u64>(in, half_bin);
+    const u64 all = R.mass_of_bins();
     bool exact;
     u64 target = fraction_of(fmaxf(p, 0.0f), all, &exact);
     target = max(u64(1), target + !exact);
-    // tokens of less than (1 - top_p) of the sum, divided by their number, cannot make up what may go: the border is above
-    const float spare = fmaxf((float)(all - target), 1.0f) * 0.999f / (float)V, reach = log2f(0x1p42f / spare) / R.c.hi;
-    const Raised now = R.raise_floor(max(cut, key_within(reach)), in);
+    int b;
+    u64 above;
+    R.find<u64>(target, &b, &above);
+    Keys r = R.keys_of(2 * b, 2 * b + 1, distance_bin);
+    r.hi = min(r.hi, top_key);
+    const Raised now = R.raise_floor(max(cut, r.lo), in);
     if (now == kAlone) end_alone(a, R, t, R.listed, p, mp, least, all);
     if (now != kSpread) return;
-    Keys r{R.floor, top_key};
-    u64 above = 0;
-    bins_over(fminf(reach, distance_to(R.floor)));
-    if (per > 0.0f) {
-      int b;
-      R.histogram<u64>(in, half_bin);
-      R.find<u64>(target, &b, &above);
-      r = R.keys_of(2 * b, 2 * b + 1, distance_bin);
-      r.hi = min(r.hi, top_key);
-    }
+    r.lo = max(r.lo, R.floor);
     above += R.narrow<u64>(r, target - above, in);
     const u64 one = max(R.weight_of(float_of(r.lo)), u64(1));
     const int index = R.tie_index(r.lo, (target - above + one - 1) / one, in);
