@@ -60,14 +60,14 @@ constexpr Table make_table() {
 }
 __device__ constexpr Table kTable = make_table();
 
-// log2(e) / T in two fp32 words.
+// log2(e) / T in two fp32 words: the rounded quotient, and what it leaves (a 64-bit division takes 4000 cycles).
 struct Slope {
   float hi, lo;
 };
 __device__ __forceinline__ Slope slope_of(float temperature) {
-  const double c = 1.4426950408889634074 / (double)temperature;
-  const float hi = (float)c;
-  return Slope{hi, hi < INFINITY ? (float)(c - (double)hi) : 0.0f};
+  constexpr float kHi = 1.44269502162933349609375f, kLo = 1.92596299112661746e-8f;   // log2(e)
+  const float hi = __fdiv_rn(kHi, temperature);
+  return Slope{hi, hi > 0.0f && hi < INFINITY ? __fdiv_rn(__fmaf_rn(-hi, temperature, kHi) + kLo, temperature) : 0.0f};
 }
 
 // The weight of logit x (not NaN, not above top) as an integer.
@@ -300,7 +300,7 @@ struct Sampler {
       });
     } else {
       // A weight in three parts of 14 bits, which 32 bits of a bin hold the sums of: shared memory adds these by itself, and
-      // 64 bits by a loop of compares (128 rows of 248320 with top_p alone 850 us; parts, with one pass less, see below).
+      // 64 bits by a loop of compares (13 rows of 32003 with top_p 41 us; in parts, with one pass of weights less, 28).
       constexpr int kHalfBins = kBins / 2;
       static_assert((int64_t)kMaxRun * kThreads < (1 << 17), "sums of parts");
       for (int b = threadIdx.x; b < kHalfBins; b += kThreads) S.total[b] = 0;
@@ -390,26 +390,6 @@ struct Sampler {
     __syncthreads();
   }
 
-  // Narrows a range of keys to the one on which the sums from its highest key down reach n, by bins of 2^shift keys; the sums
-  // before that key.
-  template <class N, class In>
-  __device__ __forceinline__ u64 narrow(Keys& r, u64 n, In&& in) {
-    constexpr int kBits = sizeof(N) == 4 ? kBinBits : kBinBits - 1;
-    u64 sum = 0;
-    while (r.lo < r.hi) {
-      const int shift = max(0, 32 - __clz(r.hi - r.lo) - kBits);
-      int b;
-      u64 before;
-      histogram<N>([&](float v, int i) { const uint32_t key = key_of(v); return key >= r.lo && key <= r.hi && in(v, i); },
-                   [&](float v) { return (int)((r.hi - key_of(v)) >> shift); });
-      find<N>(n - sum, &b, &before);
-      sum += before;
-      r.hi -= (uint32_t)b << shift;
-      r.lo = max(r.lo, r.hi - ((1u << shift) - 1));
-    }
-    return sum;
-  }
-
   // The keys whose value `bin` (which does not rise with the key) puts into b1 .. b2: a warp for each end, 32 keys a step.
   template <class Bin>
   __device__ __forceinline__ Keys keys_of(int b1, int b2, Bin&& bin) {
@@ -435,19 +415,92 @@ struct Sampler {
     return r;
   }
 
-  // Of `r` ties on a key, the index of the last one that stays; INT_MAX if all do.
-  template <class In>
-  __device__ __forceinline__ int tie_index(uint32_t key, u64 r, In&& in) {
-    u64 n = 0, all;
-    each([&](float v, int i) { n += key_of(v) == key && in(v, i); });
-    const u64 before = cluster_before(n, &all);
-    if (all <= r) return 0x7fffffff;
-    u64 at = before, found = 0;
-    if (before < r && before + n >= r)
-      each([&](float v, int i) {
-        if (key_of(v) == key && in(v, i) && ++at == r) found = (u64)i + 1;
-      });
-    return (int)cluster_sum(found) - 1;
+  // The n2 entries of `mass` (a power of two, at most kBins / 2), the highest one first.
+  __device__ __forceinline__ void sort(int n2) {
+    u64* sorted = S.mass;
+    const int tid = threadIdx.x;
+    for (int size = 2; size <= n2; size *= 2) {
+      for (int stride = size / 2; stride > 0; stride /= 2) {
+        if (tid < n2 / 2) {
+          const int i = 2 * stride * (tid / stride) + tid % stride;
+          const u64 u = sorted[i], v = sorted[i + stride];
+          if ((u < v) == ((i & size) == 0)) {
+            sorted[i] = v;
+            sorted[i + stride] = u;
+          }
+        }
+        // (a warp keeps to its own 64 entries while the strides are at most 32)
+        const int next = stride > 1 ? stride / 2 : size;
+        if (stride > 32 || next > 32) __syncthreads();
+        else __syncwarp();
+      }
+    }
+    __syncthreads();
+  }
+
+  // Of the tokens that `in` takes, those with a key in r, the highest first and of equal ones the lowest index: the key and
+  // the index of the one with which their sum reaches n (there is one).  The first CTA sorts them if they are few; more are
+  // told apart by bins of 2^shift keys before, and ties on a key are counted.
+  template <class N, class In>
+  __device__ __forceinline__ void settle(Keys r, u64 n, In&& in, uint32_t* key_out, int* last) {
+    constexpr int kBits = sizeof(N) == 4 ? kBinBits : kBinBits - 1;
+    for (;;) {
+      auto here = [&](float v, int i) { const uint32_t key = key_of(v); return key >= r.lo && key <= r.hi && in(v, i); };
+      u64 mine_n = 0, all, found = 0;
+      each([&](float v, int i) { mine_n += here(v, i); });
+      const u64 before = cluster_before(mine_n, &all);
+      if (all <= (u64)kList) {
+        // keys and places from the end of the row to the first CTA
+        u64 to = before;
+        if (mine_n > 0)
+          each([&](float v, int i) {
+            if (!here(v, i)) return;
+            u64* at = &S.mass[to++];
+            *(C == 1 ? at : cluster.map_shared_rank(at, 0)) = (u64)key_of(v) << 32 | (0xFFFFFFFFu - (uint32_t)i);
+          });
+        sync();
+        if (rank == 0) {
+          int n2 = 2;
+          while (n2 < (int)all) n2 *= 2;
+          for (int e = (int)all + threadIdx.x; e < n2; e += kThreads) S.mass[e] = 0;
+          __syncthreads();
+          sort(n2);
+          u64 w[2] = {0, 0}, sum;
+#pragma unroll
+          for (int q = 0; q < 2; ++q) {
+            const int e = 2 * threadIdx.x + q;
+            if (e < (int)all) w[q] = sizeof(N) == 4 ? u64(1) : weight_of(float_of((uint32_t)(S.mass[e] >> 32)));
+          }
+          const u64 at = block_before(w[0] + w[1], &sum);
+          if (at < n && at + w[0] + w[1] >= n) S.found[0] = S.mass[2 * threadIdx.x + (at + w[0] < n)];
+        }
+        sync();
+        const u64 one = C == 1 ? S.found[0] : *cluster.map_shared_rank(&S.found[0], 0);
+        sync();
+        *key_out = (uint32_t)(one >> 32);
+        *last = (int)(0xFFFFFFFFu - (uint32_t)one);
+        return;
+      }
+      if (r.lo == r.hi) {   // ties, in order of their index
+        const u64 w = sizeof(N) == 4 ? u64(1) : max(weight_of(float_of(r.lo)), u64(1)), count = (n + w - 1) / w;
+        u64 at = before;
+        if (before < count && before + mine_n >= count)
+          each([&](float v, int i) {
+            if (here(v, i) && ++at == count) found = (u64)i + 1;
+          });
+        *key_out = r.lo;
+        *last = (int)cluster_sum(found) - 1;
+        return;
+      }
+      const int shift = max(0, 32 - __clz(r.hi - r.lo) - kBits);
+      int b;
+      u64 above;
+      histogram<N>(here, [&](float v) { return (int)((r.hi - key_of(v)) >> shift); });
+      find<N>(n, &b, &above);
+      n -= above;
+      r.hi -= (uint32_t)b << shift;
+      r.lo = max(r.lo, r.hi - ((1u << shift) - 1));
+    }
   }
 
   // Nothing below `lowest` stays, nor what `in` does not take: the CTA's other tokens into its list, and all lists to the
@@ -543,23 +596,7 @@ __device__ __forceinline__ void end_alone(const qmm_sample_args& a, Sampler& R, 
   for (int e = tid; e < n2; e += kThreads)
     sorted[e] = e < n ? (u64)key_of(R.all_x[e]) << 32 | (0xFFFFFFFFu - (uint32_t)e) : 0;
   __syncthreads();
-  for (int size = 2; size <= n2; size *= 2) {
-    for (int stride = size / 2; stride > 0; stride /= 2) {
-      if (tid < n2 / 2) {
-        const int i = 2 * stride * (tid / stride) + tid % stride;
-        const u64 u = sorted[i], v = sorted[i + stride];
-        if ((u < v) == ((i & size) == 0)) {
-          sorted[i] = v;
-          sorted[i + stride] = u;
-        }
-      }
-      // (a warp keeps to its own 64 entries while the strides are at most 32)
-      const int next = stride > 1 ? stride / 2 : size;
-      if (stride > 32 || next > 32) __syncthreads();
-      else __syncwarp();
-    }
-  }
-  __syncthreads();
+  R.sort(n2);
   u64 w[2] = {0, 0}, sum;
   int place[2];
 #pragma unroll
@@ -713,9 +750,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
     R.histogram<uint32_t>(everything, distance_bin);
     R.find<uint32_t>((u64)k, &b, &above);
     Keys r = R.keys_of(b, b, distance_bin);
-    above += R.narrow<uint32_t>(r, (u64)k - above, everything);
-    last = R.tie_index(r.lo, (u64)k - above, everything);
-    cut = r.lo;
+    R.settle<uint32_t>(r, (u64)k - above, everything, &cut, &last);
   }
   if (by_p) {
     // The top alone weighs 1, so tokens of less than (1 - top_p) / V cannot make up what may go: the border is within
@@ -736,11 +771,11 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
     if (now == kAlone) end_alone(a, R, t, R.listed, p, mp, least, all);
     if (now != kSpread) return;
     r.lo = max(r.lo, R.floor);
-    above += R.narrow<u64>(r, target - above, in);
-    const u64 one = max(R.weight_of(float_of(r.lo)), u64(1));
-    const int index = R.tie_index(r.lo, (target - above + one - 1) / one, in);
-    if (r.lo > cut || index < last) last = index;   // (of those that top_k left on it)
-    cut = r.lo;
+    uint32_t key;
+    int index;
+    R.settle<u64>(r, target - above, in, &key, &index);
+    cut = key;
+    last = index;
   } else if (mp > 0.0f) {
     const Raised now = R.raise_floor(max(cut, key_within(log2f(1.0f / fminf(mp, 1.0f)) / R.c.hi)), in);
     if (now == kAlone) end_alone(a, R, t, R.listed, p, mp, least, 0);
