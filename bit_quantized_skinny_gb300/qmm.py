@@ -659,6 +659,8 @@ def attn_fp4_workspace_bytes(args) -> int:
 def attn_shared_fp4(args, workspace, stream=None) -> None:
     """qmm_attn_shared_fp4: attn_shared() over a 4-bit cache.  `args` from make_attn_fp4(); `workspace`: a device
     tensor of >= attn_fp4_workspace_bytes(args) bytes."""
+    if not workspace.is_cuda or workspace.get_device() != args._device or not workspace.is_contiguous():
+        raise QmmError(2, "workspace")
     _check(load().qmm_attn_shared_fp4(args, workspace.data_ptr(), workspace.numel() * workspace.element_size(),
                                       _handle_on(args._device, stream)), "qmm_attn_shared_fp4")
 
