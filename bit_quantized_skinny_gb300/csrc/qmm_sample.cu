@@ -181,6 +181,22 @@ struct Keys {             // lo <= key <= hi
   uint32_t lo, hi;
 };
 
+// Sum over the threads of the CTA before this one, and over the CTA.  (Out of line, as weight_once() is: a sixth less code, the
+// same times.)
+struct Sums {
+  u64 before, all;
+};
+__device__ __noinline__ Sums block_sums(u64* scan, u64 v) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const u64 upto = warp_upto(v);
+  __syncthreads();
+  if (lane == 31) scan[warp] = upto;
+  __syncthreads();
+  const u64 of = lane < kWarps ? scan[lane] : 0;
+  return Sums{upto - v + warp_sum(lane < warp ? of : 0), warp_sum(of)};
+}
+__device__ __noinline__ u64 weight_once(float x, float top, Slope c, const u64* table) { return weight(x, top, c, table); }
+
 enum Raised { kDone, kSpread, kAlone };   // this CTA has nothing left to do; goes on with the others; has all tokens
 
 struct Sampler {
@@ -213,6 +229,7 @@ struct Sampler {
     }
   }
   __device__ __forceinline__ u64 weight_of(float v) const { return v == -INFINITY ? u64(0) : weight(v, top, c, S.table); }
+  __device__ __forceinline__ u64 weight_of_one(float v) const { return v == -INFINITY ? u64(0) : weight_once(v, top, c, S.table); }
 
   __device__ __forceinline__ void sync() const {
     if (C > 1) cluster.sync();
@@ -271,14 +288,9 @@ struct Sampler {
   }
   // Sum over the threads of the CTA before this one; all: over the CTA.
   __device__ __forceinline__ u64 block_before(u64 v, u64* all) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const u64 upto = warp_upto(v);
-    __syncthreads();
-    if (lane == 31) S.scan[warp] = upto;
-    __syncthreads();
-    const u64 of = lane < kWarps ? S.scan[lane] : 0;
-    *all = warp_sum(of);
-    return upto - v + warp_sum(lane < warp ? of : 0);
+    const Sums sums = block_sums(S.scan, v);
+    *all = sums.all;
+    return sums.before;
   }
   // Sum over the threads of the cluster before this one; all: over the cluster.
   __device__ __forceinline__ u64 cluster_before(u64 v, u64* all) {
@@ -469,7 +481,7 @@ struct Sampler {
 #pragma unroll
           for (int q = 0; q < 2; ++q) {
             const int e = 2 * threadIdx.x + q;
-            if (e < (int)all) w[q] = sizeof(N) == 4 ? u64(1) : weight_of(float_of((uint32_t)(S.mass[e] >> 32)));
+            if (e < (int)all) w[q] = sizeof(N) == 4 ? u64(1) : weight_of_one(float_of((uint32_t)(S.mass[e] >> 32)));
           }
           const u64 at = block_before(w[0] + w[1], &sum);
           if (at < n && at + w[0] + w[1] >= n) S.found[0] = S.mass[2 * threadIdx.x + (at + w[0] < n)];
@@ -482,7 +494,7 @@ struct Sampler {
         return;
       }
       if (r.lo == r.hi) {   // ties, in order of their index
-        const u64 w = sizeof(N) == 4 ? u64(1) : max(weight_of(float_of(r.lo)), u64(1)), count = (n + w - 1) / w;
+        const u64 w = sizeof(N) == 4 ? u64(1) : max(weight_of_one(float_of(r.lo)), u64(1)), count = (n + w - 1) / w;
         u64 at = before;
         if (before < count && before + mine_n >= count)
           each([&](float v, int i) {
@@ -606,7 +618,7 @@ __device__ __forceinline__ void end_alone(const qmm_sample_args& a, Sampler& R, 
     if (e < n) {
       const u64 v = sorted[e];
       place[q] = (int)(0xFFFFFFFFu - (uint32_t)v);
-      if (e < k) w[q] = R.weight_of(float_of((uint32_t)(v >> 32)));
+      if (e < k) w[q] = R.weight_of_one(float_of((uint32_t)(v >> 32)));
     }
   }
   u64 at = R.block_before(w[0] + w[1], &sum);
@@ -807,7 +819,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
       const bool here = j0 + lane < len;
       const float v = here ? R.mine[off + j0 + lane] : -INFINITY;
       const int i = !here ? 0 : R.index ? R.index[off + j0 + lane] : first + j0 + lane;
-      u64 w = here && key_of(v) >= R.floor && in(v, i) ? R.weight_of(v) : 0;
+      u64 w = here && key_of(v) >= R.floor && in(v, i) ? R.weight_of_one(v) : 0;
       if (w < least) w = 0;
       const u64 upto = at + warp_upto(w);
       const uint32_t hit = __ballot_sync(0xffffffffu, upto > goal);
