@@ -58,9 +58,11 @@ constexpr uint32_t kTmemCols = 512;   // lane L: S at 64 L, p at 128 + 64 L and 
 constexpr float kGrow = 8.0f;
 constexpr uint32_t kWaitLimit = 1u << 17;
 constexpr float kLog2e = 1.44269504088896340736f;
+constexpr float kLift = 7.0f;        // (with kGrow, weights of at most 2^15)
 
 struct Params : Common {
   CUtensorMap mapQ, mapK, mapV;
+  const float* factors;   // EXPANDED: of each row and head, in place of scale log2 e; or NULL
 };
 
 template <int D>
@@ -134,7 +136,9 @@ __device__ __noinline__ bool wait_slowly(uint32_t bar, uint32_t parity, uint32_t
   return false;
 }
 
-template <int D, int TYPE>
+// EXPANDED: keys and values are those of a 4-bit cache, which are few bits long, so p keeps more of its own than bf16
+// has: it is fp16, and lifted by 2^kLift, so that a weight loses bits only below 2^-21 of the largest one.
+template <int D, int TYPE, bool EXPANDED>
 __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant__ Params P) {
   extern __shared__ __align__(1024) uint8_t smem[];
   using L = Smem<D>;
@@ -396,7 +400,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
     const uint32_t lanes = (uint32_t)(warp % kLaneWarps) << 21;   // first TMEM lane << 16
     const uint32_t tS = tmem + lanes + kTile * l, tP = tmem + lanes + 2 * kTile + kTile * l;
     const uint32_t tO = tmem + lanes + 4 * kTile;
-    const float c = a.scale * kLog2e;
+    float c = a.scale * kLog2e;
     float2* stats = reinterpret_cast<float2*>(smem + L::kStats);
     uint32_t parity = 0;   // of the next phases of the value stages' full barriers (single, both)
     uint32_t pos = 0, seen = 0, joins = 0, segs = 0, items = 0, ends = 0;
@@ -409,6 +413,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
       const int tok0 = pair ? l * P.tokens : 0;                   // the lane's rows of the block
       const int live = min(P.tokens, g.rows - tok0) * G;          // rows of the tile in use
       const int tok = tok0 + row / G;
+      if constexpr (EXPANDED)
+        if (P.factors) c = row < live ? P.factors[(int64_t)(g.t0 + tok) * a.Hq + g.h * G + row % G] : 0.0f;
       const int sees = g.own ? clampi(g.first_keys + tok, 0, g.keys) : g.keys;
       // Keys that not every row of the block sees.  The same ones for both lanes, also where each has a row
       // tile and they share the value tiles: whichever takes a value out first, the other one's product
@@ -472,7 +478,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
 #pragma unroll
             for (int q = 0; q < 4; ++q)
               mx[q] = fmaxf(mx[q], fmaxf(__uint_as_float(s[k + 2 * q]), __uint_as_float(s[k + 2 * q + 1])));
-          const float now = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c;
+          const float now = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c - (EXPANDED ? kLift : 0.0f);
           const bool grew = now > top + kGrow || (top == -INFINITY && now > -INFINITY);
           if (i > first && __any_sync(0xffffffffu, grew)) {
             // the item before is in O (the one before that is, with S)
@@ -637,30 +643,30 @@ bool tensor_map(CUtensorMap* m, const void* p, int D, int H, int64_t n, int64_t 
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int D, int TYPE>
+template <int D, int TYPE, bool EXPANDED>
 cudaError_t set_smem_attr() {
   static DeviceOnce once;
   int dev = 0;
   const cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   return once.run(dev, cudaSuccess, [] {
-    return cudaFuncSetAttribute(attn_kernel<D, TYPE>, cudaFuncAttributeMaxDynamicSharedMemorySize, Smem<D>::kTotal);
+    return cudaFuncSetAttribute(attn_kernel<D, TYPE, EXPANDED>, cudaFuncAttributeMaxDynamicSharedMemorySize, Smem<D>::kTotal);
   });
 }
 
-template <int D, int TYPE>
-cudaError_t launch(const qmm_attn_args& a, void* workspace, cudaStream_t stream) {
+// The launch ahead of the combine's; *sms: what that one takes.
+template <int D, int TYPE, bool EXPANDED>
+cudaError_t launch_products(Params& P, int* sms_out, cudaStream_t stream) {
+  const qmm_attn_args& a = P.a;
   const int G = a.Hq / a.Hk;
-  Params P;
-  fill(P, a, kRows / G, 2 * (kRows / G), workspace);
   const int per_box = a.page_size < kTile ? a.page_size : kTile;
   if (!tensor_map(&P.mapQ, a.Q, D, a.Hq, a.T, a.ldq, G, P.tokens, TYPE) ||
       !tensor_map(&P.mapK, a.K_cache, D, a.Hk, a.n_slots, (int64_t)a.Hk * D, 1, per_box, TYPE) ||
       !tensor_map(&P.mapV, a.V_cache, D, a.Hk, a.n_slots, (int64_t)a.Hk * D, 1, per_box, TYPE))
     return cudaErrorInvalidValue;
-  cudaError_t e = set_smem_attr<D, TYPE>();
+  const cudaError_t e = set_smem_attr<D, TYPE, EXPANDED>();
   if (e != cudaSuccess) return e;
-  const int sms = sm_count();
+  const int sms = *sms_out = sm_count();
   if (sms < 1) return cudaErrorNoDevice;
   // Both launches may be scheduled while the one before them finishes (programmatic dependent launch);
   // each waits for it before it reads or writes memory.
@@ -674,10 +680,40 @@ cudaError_t launch(const qmm_attn_args& a, void* workspace, cudaStream_t stream)
   at[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, attn_kernel<D, TYPE>, P);
-  if (e != cudaSuccess) return e;
-  return launch_combine<D, TYPE, false>(P, sms, stream);
+  return cudaLaunchKernelEx(&cfg, attn_kernel<D, TYPE, EXPANDED>, P);
 }
+
+void fill_rows(Params& P, const qmm_attn_args& a, void* workspace) {
+  const int tokens = kRows / (a.Hq / a.Hk);
+  fill(P, a, tokens, 2 * tokens, workspace);
+  P.factors = nullptr;
+}
+
+template <int D, int TYPE>
+cudaError_t launch(const qmm_attn_args& a, void* workspace, cudaStream_t stream) {
+  Params P;
+  int sms = 0;
+  fill_rows(P, a, workspace);
+  const cudaError_t e = launch_products<D, TYPE, false>(P, &sms, stream);
+  return e != cudaSuccess ? e : launch_combine<D, TYPE, false>(P, sms, stream);
+}
+
+template <int D>
+cudaError_t launch_expanded(const qmm_attn_fp4_args& f, const qmm_attn_args& view, const float* factors, void* workspace,
+                            cudaStream_t stream) {
+  Params P;
+  int sms = 0;
+  fill_rows(P, view, workspace);
+  P.factors = factors;
+  const cudaError_t e = launch_products<D, QMM_F16, true>(P, &sms, stream);
+  if (e != cudaSuccess) return e;
+  Common C = P;
+  C.a = f.base;
+  C.v_scale = f.v_scale;
+  return f.base.type == QMM_BF16 ? launch_combine<D, QMM_BF16, true>(C, sms, stream)
+                                 : launch_combine<D, QMM_F16, true>(C, sms, stream);
+}
+
 
 }  // namespace
 
@@ -687,6 +723,12 @@ cudaError_t launch_attn(const qmm_attn_args& a, void* workspace, cudaStream_t st
   if (a.D == 64)
     return a.type == QMM_BF16 ? launch<64, QMM_BF16>(a, workspace, stream) : launch<64, QMM_F16>(a, workspace, stream);
   return a.type == QMM_BF16 ? launch<128, QMM_BF16>(a, workspace, stream) : launch<128, QMM_F16>(a, workspace, stream);
+}
+
+cudaError_t launch_attn_expanded(const qmm_attn_fp4_args& f, const qmm_attn_args& view, const float* factors,
+                                 void* workspace, cudaStream_t stream) {
+  return view.D == 64 ? launch_expanded<64>(f, view, factors, workspace, stream)
+                      : launch_expanded<128>(f, view, factors, workspace, stream);
 }
 
 cudaError_t read_and_clear_attn_status(unsigned* out) {

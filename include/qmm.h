@@ -519,10 +519,13 @@ qmm_status qmm_kv_fp4_read(const qmm_kv_fp4_read_args* args_host, cudaStream_t s
 /* qmm_attn_shared over a 4-bit cache: base.K_cache and base.V_cache are packed caches of base.n_slots slots in pages of
  * base.page_size, base.type is the type of Q and O.  Keys and values enter the products as they
  * are stored (a code times its scale is exact in 16 bits), the weights of the values are rounded to fp16.
- * bf16 queries are taken to fp16 with a power of two of their row that makes this exact down to 2^-24
+ * bf16 queries are taken to fp16 with a power of two of their row that makes this exact down to 2^-31
  * of the row's largest value.  A NaN that a row sees makes the 16 values of its block of O NaN (in a key: the whole row).
  * Shapes, errors and everything else as qmm_attn_shared; k_scale and v_scale in [2^-60, 2^60].
- *   workspace_dev: at least qmm_attn_fp4_workspace_bytes(args) bytes, as there. */
+ *   workspace_dev: at least qmm_attn_fp4_workspace_bytes(args) bytes, as there.  With many rows a key (on the average
+ * 160 or more pairs of a row and one of the query heads that share a key's head) the call writes the keys and values
+ * that its rows may see to the workspace in 16 bits first, unless the page lists have room for more than 1 GiB of them;
+ * the size then has room for these, and depends on all sizes in args. */
 typedef struct {
   qmm_attn_args base;
   float k_scale, v_scale;
@@ -644,7 +647,7 @@ size_t qmm_workspace_bytes_held(void);
  * the launches made from now on to `polls` polls of at most `suspend_ns` nanoseconds each
  * (0, 0 restores the default), for every thread and stream of the process: a test hook, which
  * with a bound far below a memory access's latency makes the first wait run out.  The
- * waits of qmm_attn_shared are bounded in the same way and by the same call. */
+ * waits of qmm_attn_shared and qmm_attn_shared_fp4 are bounded in the same way and by the same call. */
 void qmm_set_wait_limit(uint32_t polls, uint32_t suspend_ns);
 
 /* Read and clear the status word that the kernels of this library keep on the current device
