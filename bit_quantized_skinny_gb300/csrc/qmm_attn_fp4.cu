@@ -791,9 +791,9 @@ struct Expanded {
 // again, at HBM's rate) it costs 0.1 ns, and then 0.05 ns for each 128 rows in the 16-bit kernel.  So keys are expanded from
 // kRowsExpanded rows a key on, on the average over the keys that the page lists have room for (the lengths are on the device),
 // unless these are more than the workspace should hold.  Measured, 8 heads of 128 that 5 query heads share, 16 rows a stream
-// behind 32768 keys: 160 rows a key 81.5 us expanded, 79.2 not; 320 rows 104 and 122; 640 rows 130 and 206; 5120 rows (64
-// streams) 638 and 1442.  A prompt of 1000 rows over 8000 keys 161 and 358; 100 rows over them 52 and 63; 60 rows over 300
-// keys 20.1 and 26.5; 30 streams of 3 rows behind 30000 keys with 1000 of their own 148 and 162.
+// behind 32768 keys: 160 rows a key about 79 us either way; 320 rows 99 expanded, 122 not; 640 rows 126 and 206; 5120 rows
+// (64 streams) 632 and 1442.  A prompt of 1000 rows over 8000 keys 153 and 358; 100 rows over them 41 and 63; 60 rows over
+// 300 keys 19.7 and 26.5; 30 streams of 3 rows behind 30000 keys with 1000 of their own 142 and 162.
 constexpr int64_t kRowsExpanded = 160;
 constexpr int64_t kMostExpanded = int64_t(1) << 30;   // bytes
 bool expands(const qmm_attn_args& a) {
@@ -805,17 +805,21 @@ bool expands(const qmm_attn_args& a) {
 struct ExpandParams {
   qmm_attn_args a;
   float c;               // scale k_scale log2 e
-  int64_t n_pre, n_pages, page_ctas;
+  int64_t n_pre, page_ctas;
+  int chunks;            // CTAs of a page's head
   int32_t* ids;
   __half *Q, *K, *V;
   float* factors;
 };
 constexpr int kExpandThreads = 128;
+// Blocks of 16 values of a CTA.  Two a thread: 100 rows over 8000 keys 40.9 us, a page's 128 slots a CTA 51.9; one, four and eight a
+// thread 39.9, 44.8, 49.0, but 64 streams of 16 rows behind 8000 keys 261, 248, 246, two 250.
+constexpr int kExpandBlocks = 2 * kExpandThreads;
 // Scores stay below 2^40, so a factor this small makes all weights 1, as a smaller one would; but 0 times the -inf of a masked
 // key would be NaN.
 constexpr float kLeastFactor = 0x1p-120f;
 
-// A CTA for each page and head, a thread a block of 16 values at a time; behind these, for bf16, a warp for each row and head of
+// A CTA for kExpandBlocks blocks of 16 values of a page's head, keys and values, a thread a block at a time; behind these, for bf16, a warp for each row and head of
 // the queries.
 template <int D, int TYPE>
 __global__ void __launch_bounds__(kExpandThreads) expand_kernel(const __grid_constant__ ExpandParams P) {
@@ -847,9 +851,9 @@ __global__ void __launch_bounds__(kExpandThreads) expand_kernel(const __grid_con
     return;
   }
   constexpr int kBlocks = D / kv4::kBlock;
-  const int64_t p = blockIdx.x / a.Hk;
-  const int h = (int)(blockIdx.x - p * a.Hk);
-  if (h == 0 && threadIdx.x == 0) P.ids[p] = (int32_t)p;
+  const int64_t run_of = blockIdx.x / P.chunks, p = run_of / a.Hk;
+  const int first = (int)(blockIdx.x - run_of * P.chunks) * kExpandBlocks, h = (int)(run_of - p * a.Hk);
+  if (h == 0 && first == 0 && threadIdx.x == 0) P.ids[p] = (int32_t)p;
   int page, live;
   if (p < P.n_pre) {
     page = a.prefix_pages[p];
@@ -858,16 +862,17 @@ __global__ void __launch_bounds__(kExpandThreads) expand_kernel(const __grid_con
     const int64_t own = p - P.n_pre;
     const int b = (int)(own / a.pages_per_stream);
     live = (int)min((int64_t)a.page_size, stream_of(a, b).len - (own - (int64_t)b * a.pages_per_stream) * a.page_size);
-    if (live <= 0) return;
-    page = a.pages[own];
+    page = first < live * kBlocks ? a.pages[own] : 0;
   }
+  const int end = min(live * kBlocks, first + kExpandBlocks);
+  if (first >= end) return;
   if (page < 0 || page >= a.n_slots / a.page_size) {
     if (threadIdx.x == 0) atomicOr(&g_status, kErrIndex);
     page = 0;   // (the rows that see it have unspecified values)
   }
   const int64_t from = kv4::run_at(page, h, a.Hk, a.page_size, D);
-#pragma unroll 1
-  for (int u = threadIdx.x; u < live * kBlocks; u += kExpandThreads) {
+#pragma unroll 2
+  for (int u = first + threadIdx.x; u < end; u += kExpandThreads) {
     const int slot = u / kBlocks, block = u % kBlocks;
     const int64_t to = ((p * a.page_size + slot) * a.Hk + h) * D + block * kv4::kBlock;
 #pragma unroll
@@ -889,7 +894,8 @@ cudaError_t launch_expand(const qmm_attn_fp4_args& f, void* workspace, cudaStrea
   const qmm_attn_args& a = f.base;
   const Expanded at(a);
   uint8_t* ws = static_cast<uint8_t*>(workspace) + (up(reinterpret_cast<uintptr_t>(workspace)) - reinterpret_cast<uintptr_t>(workspace));
-  ExpandParams P{a, a.scale * f.k_scale * kLog2e, at.n_pre, at.n_pages, at.n_pages * a.Hk,
+  const int chunks = (a.page_size * (D / kv4::kBlock) + kExpandBlocks - 1) / kExpandBlocks;
+  ExpandParams P{a, a.scale * f.k_scale * kLog2e, at.n_pre, at.n_pages * a.Hk * chunks, chunks,
                  reinterpret_cast<int32_t*>(ws + at.ids), reinterpret_cast<__half*>(ws + at.Q), reinterpret_cast<__half*>(ws + at.K),
                  reinterpret_cast<__half*>(ws + at.V), reinterpret_cast<float*>(ws + at.factors)};
   constexpr int kRowsOfCta = kExpandThreads / 32;
