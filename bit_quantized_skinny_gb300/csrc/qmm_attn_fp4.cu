@@ -12,8 +12,7 @@
 //     S^T = K Q^T        tcgen05, K (128 keys x D) from tensor memory, where four warps put it, a thread a key
 //     p = 2^(c S + off)  a thread per key, S^T from tensor memory, c = scale k_scale log2 e over the row's power of two
 //     O^T += V^T p^T     tcgen05, V and p^T (both MN-major) from shared memory; four more warps write V
-//     l += 1 p^T         tcgen05, ones from shared memory: the rows' sums of weights (of up to eight rows the softmax adds
-//                        them up itself: these products take as long as half of those before)
+//     l += p 1           tcgen05, 16 columns of ones: the rows' sums of weights, a row a lane
 // so few rows cost little, the exponentials of a row are spread over 128 threads, and no 128-row tile of queries
 // is read again for every tile.  Two groups of softmax warps have the key tiles in turn, with sums of their own that are
 // joined at a segment's end: what a tile costs a group besides its rows (waits, votes, fences) is then paid once for all of them.
@@ -24,8 +23,8 @@
 // 1100 and 700, a group's softmax 3000 for every other tile), a tile 2100: the roles wait for each other at most a third of
 // the time, and each one's instructions wait for their own way to the warp more than for anything else (without the
 // exponentials, without the conversions or with half the products a tile takes 4 to 10 % less).  Measured: 4 streams of 8 rows
-// behind 131072 keys 208 us (0.73 TB/s of packed keys, 10 times that much arithmetic as two rows would need); 24 streams of
-// 19000 to 41000 keys of their own 288 us (2.9 TB/s); 1 stream of 700 keys 17 us with the combine launch.
+// behind 131072 keys 201 us (three blocks of rows, 2.3 TB/s of packed keys in all); 24 streams of 19000 to 41000 keys of
+// their own 292 us (2.8 TB/s); 1 stream of 700 keys 17 us with the combine launch.
 //
 // Keys that a row may not see are set to -inf by position, so their K may hold anything.  Value rows behind the last key
 // are zeroed, and so are NaN blocks among the keys that only some rows of the block see (a draft's last keys);
@@ -53,7 +52,6 @@ constexpr int kTile = 128;           // keys of a key tile
 constexpr int kLead = 8;             // units of a group besides its key tiles: 8 us (4 streams behind 131072 keys 208 us, 6 units 238)
 constexpr int kN = 64;               // rows of a block
 constexpr int kHalf = kN / 2;        // rows up to which the products are half as wide
-constexpr int kFew = 8;              // rows whose weights a softmax thread adds up itself
 // warps: 0-3 and 4-7 softmax, 8 copies, 9 and 11 tensor cores, 10 queries, 12-15 keys and 16-19 values to fp16
 constexpr int kLoadWarp = 8, kScoreWarp = 9, kQWarp = 10, kSumWarp = 11, kKeyWarp = 12, kValueWarp = 16;
 constexpr int kThreads = 20 * 32, kGroupWarps = 4;
@@ -61,7 +59,10 @@ constexpr uint32_t kTmemCols = 512;
 constexpr int kKeyBufs = 3;          // of 64 values of a tile's keys, in tensor memory
 constexpr int kScoreBufs = 4;        // two for each group
 constexpr int kOnesN = 16;           // columns of l, all the same
-constexpr int kPacks = 9;            // packed tiles in shared memory: of keys and of values in turn
+// Packed tiles in shared memory, of keys and of values in turn.  An even number, so that a role's next use of one follows its
+// own last, and its wait takes no phase before that for it.  (Ten fit: 4 streams behind 131072 keys 203 us, 201.)
+constexpr int kPacks = 8;
+static_assert(kPacks % 2 == 0, "a pack is one role's");
 constexpr int kFactorTiles = 8;      // (the softmax is a few query tiles behind)
 constexpr float kGrow = 8.0f;
 constexpr float kLift = 7.0f;        // log2 of the largest weight when off is set
@@ -384,7 +385,6 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fp4_kernel(const __grid_cons
       uint32_t tile = 0, segs = 0;
       bool ok = true;
       while (ok && next_of(walk, P, g)) {
-        const bool sums = g.rows * G > kFew;
         const uint32_t id = g.rows * G > kHalf ? kIdBoth : kIdHalf;
         if (segs > 0) ok = wait(kBarOFree, (segs - 1) & 1);
         ++segs;
@@ -400,7 +400,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fp4_kernel(const __grid_cons
             const uint32_t p = (buf * L::kPBytes + k * 64 * 128) >> 4;
             mma_ss_x4(tmem + T::kO + kN * buf, dv + ((vb * L::kVBytes + k * 64 * 128) >> 4), 128, dp + p, 128, id | kMnMajorA,
                       !fresh || k > 0);
-            if (sums) mma_ss_x4(tmem + T::kL + kOnesN * buf, dpa + p, 128, ones, 0, kIdSum, !fresh || k > 0);
+            mma_ss_x4(tmem + T::kL + kOnesN * buf, dpa + p, 128, ones, 0, kIdSum, !fresh || k > 0);
           }
           tc::commit(bar(kBarO + buf));
           tc::commit(bar(kBarValueEmpty + vb));
@@ -522,7 +522,6 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fp4_kernel(const __grid_cons
       ++segs;
       off[lane] = off[kHalf + lane] = 0.0f;
       __syncwarp();
-      float sum[kFew] = {}, add[kFew] = {};   // of this thread's weights, and in the tile, where there are few rows
       bool first = true, leave = false;   // leave: the whole group knows that a wait gave up
       for (int j = g.j0; j < j1; ++j, ++tile) {
         const uint32_t buf = tile & 1, phase = (tile >> 1) & 1, at = tile % kScoreBufs;
@@ -574,9 +573,6 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fp4_kernel(const __grid_cons
               }
               *reinterpret_cast<uint4*>(p + ((r / 8 + h) ^ (mine & 7)) * 16) = make_uint4(w[0], w[1], w[2], w[3]);
             }
-            if (rows <= kFew)
-#pragma unroll
-              for (int q = 0; q < kFew; ++q) add[q] = x[q];
           }
           return most;
         };
@@ -623,7 +619,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fp4_kernel(const __grid_cons
                   o[r] = __float_as_uint(__uint_as_float(o[r]) * __shfl_sync(0xffffffffu, of, (r0 & (kHalf - 1)) + r));
                 tc::st_x8(tmem + lanes + T::kO + kN * grp + r0, o);
               }
-              if (rows > kFew && wg < 2) {   // (its first column is read in the end)
+              if (wg < 2) {   // (its first column is read in the end)
                 uint32_t l[8];
                 tc::ld_wait_x8(tmem + lanes + T::kL + kOnesN * grp, l);
 #pragma unroll
@@ -631,8 +627,6 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fp4_kernel(const __grid_cons
                 tc::st_x8(tmem + lanes + T::kL + kOnesN * grp, l);
               }
               tc::wait_st();
-#pragma unroll
-              for (int r = 0; r < kFew; ++r) sum[r] *= __shfl_sync(0xffffffffu, keep[0], r);
             }
           }
           const float most = weights();
@@ -640,9 +634,6 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fp4_kernel(const __grid_cons
         }
         if (leave) break;
         first = false;
-        if (rows <= kFew)
-#pragma unroll
-          for (int r = 0; r < kFew; ++r) sum[r] += add[r];
         fence_proxy_async_smem();
         tc::fence_before_sync();
         __syncwarp();
@@ -657,17 +648,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fp4_kernel(const __grid_cons
       // phase for the one after it)
       const uint32_t last = tile - 1 - ((tile - 1 - grp) & 1);
       if (!leave && (n > 1 || last == tile - 1)) ok = wait_w(kBarO + grp, (last >> 1) & 1) && ok;
-      if (rows <= kFew) {
-        float own = 0.0f;   // lane r: row r's over the warp
-#pragma unroll
-        for (int r = 0; r < kFew; ++r) {
-          float v = sum[r];
-#pragma unroll
-          for (int o = 16; o >= 1; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-          if (lane == r) own = v;
-        }
-        red[wg * kN + lane] = own;
-      } else if (wg < 2) {   // lane r: row kHalf wg + r's
+      if (wg < 2) {   // lane r: row kHalf wg + r's
         uint32_t l[8];
         tc::fence_after_sync();
         tc::ld_wait_x8(tmem + lanes + T::kL + kOnesN * grp, l);
@@ -682,7 +663,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fp4_kernel(const __grid_cons
       const uint32_t tO = tmem + lanes + T::kO + c0;
       auto sum_of = [&](int gr) -> float {
         const float* x = reinterpret_cast<const float*>(smem + L::kRed) + gr * kGroupWarps * kN + row;
-        return rows <= kFew ? (x[0] + x[kN]) + (x[2 * kN] + x[3 * kN]) : x[0];
+        return x[0];
       };
       const float* offs = reinterpret_cast<const float*>(smem + L::kOff) + row;
       float f[2] = {0.0f, 0.0f}, all = 0.0f, top = -INFINITY;
