@@ -1,8 +1,8 @@
 // qmm_attn_fp4.cu — attention of several streams' rows over a prefix that they share and over each
 // stream's own keys, in pages of a 4-bit cache (qmm_attn_shared_fp4).
 //
-// Two forms, by the number of rows a key (expands() below): the kernel described here, and, with many rows, a launch that
-// writes keys and values to the workspace in 16 bits and the 16-bit cache's kernel behind it.
+// Two forms, by the number of rows a key and of keys (expands() below): the kernel described here, and, with many rows or few
+// keys, a launch that writes keys and values to the workspace in 16 bits and the 16-bit cache's kernel behind it.
 //
 // Work: equal pieces of the list of all key tiles, joined by a second launch (q4k_attn_parts.cuh).  A block is N / G
 // tokens (at most N rows), a key tile 128 keys.
@@ -24,7 +24,7 @@
 // the time, and each one's instructions wait for their own way to the warp more than for anything else (without the
 // exponentials, without the conversions or with half the products a tile takes 4 to 10 % less).  Measured: 4 streams of 8 rows
 // behind 131072 keys 201 us (three blocks of rows, 2.3 TB/s of packed keys in all); 24 streams of 19000 to 41000 keys of
-// their own 292 us (2.8 TB/s); 1 stream of 700 keys 17 us with the combine launch.
+// their own 292 us (2.8 TB/s).
 //
 // Keys that a row may not see are set to -inf by position, so their K may hold anything.  Value rows behind the last key
 // are zeroed, and so are NaN blocks among the keys that only some rows of the block see (a draft's last keys);
@@ -749,7 +749,7 @@ cudaError_t launch(const qmm_attn_fp4_args& f, void* workspace, cudaStream_t str
   return launch_combine<D, TYPE, true>(P, sms, stream);
 }
 
-// ---- many rows a key: keys and values to 16 bits once, and the 16-bit kernel
+// ---- many rows a key, or few keys: keys and values to 16 bits once, and the 16-bit kernel
 
 // The workspace behind the sums' one.
 struct Expanded {
@@ -777,30 +777,39 @@ struct Expanded {
 // 300 keys 19.7 and 26.5; 30 streams of 3 rows behind 30000 keys with 1000 of their own 142 and 162.
 constexpr int64_t kRowsExpanded = 160;
 constexpr int64_t kMostExpanded = int64_t(1) << 30;   // bytes
+// Where all keys are few, the 16-bit kernel's shorter start is worth the launch ahead of it with any number of rows.  1 stream of 1
+// row: 16 keys 11.6 us expanded, 15.3 not; 700 keys (2.9 MB) 16.0 and 16.7; 4000 (16 MB) 18.6 and 18.6; 8000 (33 MB) 23.8 and
+// 19.7.  4 streams of 8 rows: 700 keys (11 MB) 18.0 and 23.6; 3000 (49 MB) 31.0 and 27.7.  29 ragged streams (18 MB) 23.2 and 26.3;
+// 16 streams of 4 rows and 500 keys (33 MB) 27.7 and 26.2.
+constexpr int64_t kFewExpanded = int64_t(24) << 20;   // bytes
+double expanded_bytes(const qmm_attn_args& a) {
+  return (a.prefix_len + (double)a.B * a.pages_per_stream * a.page_size) * a.Hk * a.D * 4;
+}
 bool expands(const qmm_attn_args& a) {
   const double own = (double)a.pages_per_stream * a.page_size, keys = a.prefix_len + a.B * own;
   const double rows = (double)a.T * (a.Hq / a.Hk) * (a.prefix_len + own);   // times keys
-  return keys > 0 && rows >= kRowsExpanded * keys && keys * a.Hk * a.D * 4 <= (double)kMostExpanded;
+  const double bytes = expanded_bytes(a);
+  return keys > 0 && (bytes <= (double)kFewExpanded || (rows >= kRowsExpanded * keys && bytes <= (double)kMostExpanded));
 }
 
 struct ExpandParams {
   qmm_attn_args a;
   float c;               // scale k_scale log2 e
   int64_t n_pre, page_ctas;
-  int chunks;            // CTAs of a page's head
+  int chunks, blocks;    // CTAs of a page's head, blocks of one
   int32_t* ids;
   __half *Q, *K, *V;
   float* factors;
 };
+// A CTA has a block of 16 values of a page's head a thread, keys and values, or two where keys are many.  64 streams of 16 rows
+// behind 8000 keys 250 us with two, one, four and eight 261, 248, 246; 100 rows over 8000 keys 40.9, 39.9, 44.8, 49.0; 1 row over
+// 2000 19.9 and with one 17.3.
 constexpr int kExpandThreads = 128;
-// Blocks of 16 values of a CTA.  Two a thread: 100 rows over 8000 keys 40.9 us, a page's 128 slots a CTA 51.9; one, four and eight a
-// thread 39.9, 44.8, 49.0, but 64 streams of 16 rows behind 8000 keys 261, 248, 246, two 250.
-constexpr int kExpandBlocks = 2 * kExpandThreads;
 // Scores stay below 2^40, so a factor this small makes all weights 1, as a smaller one would; but 0 times the -inf of a masked
 // key would be NaN.
 constexpr float kLeastFactor = 0x1p-120f;
 
-// A CTA for kExpandBlocks blocks of 16 values of a page's head, keys and values, a thread a block at a time; behind these, for bf16, a warp for each row and head of
+// A CTA for some blocks of 16 values of a page's head, keys and values, a thread a block at a time; behind these, for bf16, a warp for each row and head of
 // the queries.
 template <int D, int TYPE>
 __global__ void __launch_bounds__(kExpandThreads) expand_kernel(const __grid_constant__ ExpandParams P) {
@@ -833,7 +842,7 @@ __global__ void __launch_bounds__(kExpandThreads) expand_kernel(const __grid_con
   }
   constexpr int kBlocks = D / kv4::kBlock;
   const int64_t run_of = blockIdx.x / P.chunks, p = run_of / a.Hk;
-  const int first = (int)(blockIdx.x - run_of * P.chunks) * kExpandBlocks, h = (int)(run_of - p * a.Hk);
+  const int first = (int)(blockIdx.x - run_of * P.chunks) * P.blocks, h = (int)(run_of - p * a.Hk);
   if (h == 0 && first == 0 && threadIdx.x == 0) P.ids[p] = (int32_t)p;
   int page, live;
   if (p < P.n_pre) {
@@ -845,7 +854,7 @@ __global__ void __launch_bounds__(kExpandThreads) expand_kernel(const __grid_con
     live = (int)min((int64_t)a.page_size, stream_of(a, b).len - (own - (int64_t)b * a.pages_per_stream) * a.page_size);
     page = first < live * kBlocks ? a.pages[own] : 0;
   }
-  const int end = min(live * kBlocks, first + kExpandBlocks);
+  const int end = min(live * kBlocks, first + P.blocks);
   if (first >= end) return;
   if (page < 0 || page >= a.n_slots / a.page_size) {
     if (threadIdx.x == 0) atomicOr(&g_status, kErrIndex);
@@ -875,8 +884,9 @@ cudaError_t launch_expand(const qmm_attn_fp4_args& f, void* workspace, cudaStrea
   const qmm_attn_args& a = f.base;
   const Expanded at(a);
   uint8_t* ws = static_cast<uint8_t*>(workspace) + (up(reinterpret_cast<uintptr_t>(workspace)) - reinterpret_cast<uintptr_t>(workspace));
-  const int chunks = (a.page_size * (D / kv4::kBlock) + kExpandBlocks - 1) / kExpandBlocks;
-  ExpandParams P{a, a.scale * f.k_scale * kLog2e, at.n_pre, at.n_pages * a.Hk * chunks, chunks,
+  const int blocks = expanded_bytes(a) <= (double)kFewExpanded ? kExpandThreads : 2 * kExpandThreads;
+  const int chunks = (a.page_size * (D / kv4::kBlock) + blocks - 1) / blocks;
+  ExpandParams P{a, a.scale * f.k_scale * kLog2e, at.n_pre, at.n_pages * a.Hk * chunks, chunks, blocks,
                  reinterpret_cast<int32_t*>(ws + at.ids), reinterpret_cast<__half*>(ws + at.Q), reinterpret_cast<__half*>(ws + at.K),
                  reinterpret_cast<__half*>(ws + at.V), reinterpret_cast<float*>(ws + at.factors)};
   constexpr int kRowsOfCta = kExpandThreads / 32;

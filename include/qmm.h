@@ -524,8 +524,9 @@ qmm_status qmm_kv_fp4_read(const qmm_kv_fp4_read_args* args_host, cudaStream_t s
  * Shapes, errors and everything else as qmm_attn_shared; k_scale and v_scale in [2^-60, 2^60].
  *   workspace_dev: at least qmm_attn_fp4_workspace_bytes(args) bytes, as there.  With many rows a key (on the average
  * 160 or more pairs of a row and one of the query heads that share a key's head) the call writes the keys and values
- * that its rows may see to the workspace in 16 bits first, unless the page lists have room for more than 1 GiB of them;
- * the size then has room for these, and depends on all sizes in args. */
+ * that its rows may see to the workspace in 16 bits first, unless the page lists have room for more than 1 GiB of them,
+ * and with any number of rows if these have room for at most 24 MiB; the size then has room for them, and depends on
+ * all sizes in args. */
 typedef struct {
   qmm_attn_args base;
   float k_scale, v_scale;

@@ -46,8 +46,10 @@ def test_against_the_formula(qmm, rows, lens, prefix, Hq, Hk, D, page, dtype):
     assert qmm.device_status() == 0
 
 
-def test_few_rows_do_not_expand(qmm):
+def test_few_rows_of_many_keys_do_not_expand(qmm):
     c = Case([8] * 4, [90, 8, 500, 129], 2050, 10, 2, 128, 64)
+    assert expands(qmm, c)                                       # few keys
+    c.pages = torch.cat([c.pages, torch.zeros(4, 200, dtype=torch.int32, device="cuda")], 1)
     assert not expands(qmm, c)
 
 
