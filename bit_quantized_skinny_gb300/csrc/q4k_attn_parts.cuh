@@ -55,7 +55,7 @@ struct Stream {
 // The piece of the list of key tiles that a CTA works on.
 struct Piece {
   int64_t w0, w1, per;   // this CTA's units, units of a CTA
-  int64_t scan[16];      // of the warps
+  int64_t scan[32];      // of the warps (a CTA has at most 32), beside what is written while some of them still read it
   int b, rb, h, rows;
   Stream s;           // stream b, if b >= 0
   int64_t unit;       // end of the CTA's units within that group
@@ -175,6 +175,7 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
 // read.  Lengths and row starts that are out of range count as none and are reported.
 template <int THREADS, int TILE, int LEAD>
 __device__ __forceinline__ void deal(const Common& P, Piece& M, unsigned* status) {
+  static_assert(THREADS % 32 == 0 && THREADS / 32 <= (int)(sizeof(M.scan) / sizeof(M.scan[0])), "an entry a warp");
   const qmm_attn_args& a = P.a;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, block = P.block;
   auto units = [](int keys) { return Walker<TILE, LEAD>::units_of(keys); };
