@@ -796,7 +796,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
     R.settle<u64>(r, target - above, in, &key, &index);
     cut = key;
     last = index;
-  } else if (mp > 0.0f) {
+  } else if (mp > 0.0f && R.c.hi > 0.0f) {   // (a slope of 0: all weights are 1, and none is far enough down)
     const Raised now = R.raise_floor(max(cut, key_within(log2f(1.0f / fminf(mp, 1.0f)) / R.c.hi)), in);
     if (now == kAlone) end_alone(a, R, t, R.listed, p, mp, least, 0);
     if (now != kSpread) return;
