@@ -797,7 +797,10 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
     cut = key;
     last = index;
   } else if (mp > 0.0f && R.c.hi > 0.0f) {   // (a slope of 0: all weights are 1, and none is far enough down)
-    const Raised now = R.raise_floor(max(cut, key_within(log2f(1.0f / fminf(mp, 1.0f)) / R.c.hi)), in);
+    // What stays weighs min_p less a weight's rounding at least; a millionth of it less again covers fp32's own in the distance,
+    // which is 0 where min_p is 1.
+    const float lightest = fmaxf(__fmaf_rn(fminf(mp, 1.0f), 1.0f - 0x1p-20f, -0x1p-40f), 0x1p-44f);
+    const Raised now = R.raise_floor(max(cut, key_within(-log2f(lightest) / R.c.hi)), in);
     if (now == kAlone) end_alone(a, R, t, R.listed, p, mp, least, 0);
     if (now != kSpread) return;
   }

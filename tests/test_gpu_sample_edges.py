@@ -45,3 +45,36 @@ def test_infinite_temperature(qmm, V, dtype):
             stays = order[:row[1] or V] if row[3] <= 1 else order[:1]
             token, logprob = of_equal_weights(sorted(stays), u[t].double().item())
             assert tokens[t].item() == token and near(logprobs[t].item(), logprob), (row, t)
+
+
+@pytest.mark.parametrize("top,temperature", [(0.0, 1.0), (0.0, 0.3), (0.0, 7.0), (1e-4, 1.0), (-0.75, 40.0), (20.0, 1.0)])
+def test_min_p_next_to_1(qmm, top, temperature):
+    """Two tokens, the second one on the border that min_p draws, or just below it, by many units of its weight: one stays
+    with the first, the other does not.  (What is picked of the two goes by u = 0.75 of their sum.)"""
+    T, V = 400, 3001
+    g = torch.Generator().manual_seed(11)
+    f32 = lambda v: torch.tensor(v, dtype=torch.float32).item()
+    top, temperature = f32(top), f32(temperature)
+    x, u = torch.full((T, V), top - 9.0 * temperature - 1.0), torch.full((T,), 0.75)
+    x[:, 40] = top
+    rows, want = [], []
+    for t in range(T):
+        low, high = (0.995, 0.999999) if t % 4 else (0.05, 0.995)
+        mp = f32(low + (high - low) * torch.rand((), generator=g).item())
+        border = top + temperature * math.log(mp)
+        at = torch.tensor(border, dtype=torch.float32)
+        steps = torch.tensor(-INF if t % 2 else INF, dtype=torch.float32)
+        while True:   # the next logit on the wanted side whose weight is 2^-38 from min_p
+            w = math.exp((at.item() - top) / temperature)
+            if (w - mp < -2.0 ** -38) if t % 2 else (w - mp > 2.0 ** -38):
+                break
+            at = torch.nextafter(at, steps)
+        x[t, 2000] = at
+        rows.append((temperature, 0, 1.0, mp))
+        if t % 2:
+            want.append((40, 0.0))
+        else:
+            want.append((40, -math.log(1 + w)) if 0.75 * (1 + w) < 1 else (2000, math.log(w / (1 + w))))
+    tokens, logprobs = run(qmm, x.cuda(), rows, u.cuda())
+    for t in range(T):
+        assert tokens[t].item() == want[t][0] and near(logprobs[t].item(), want[t][1]), (t, rows[t], x[t, 2000].item())
