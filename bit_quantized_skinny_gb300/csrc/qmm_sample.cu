@@ -381,15 +381,18 @@ struct Sampler {
     block_before(sum, &all);
     return all;
   }
-  // The first bin whose sums reach n >= 1, with those before it.
+  // The first bin whose sums reach n >= 1, with those before it; false: all of them do not.
   template <class N>
-  __device__ __forceinline__ void find(u64 n, int* bin, u64* before) {
+  __device__ __forceinline__ bool find(u64 n, int* bin, u64* before) {
     constexpr int kMine = kBins * 4 / (int)sizeof(N) / kThreads;
     const N* total = reinterpret_cast<const N*>(S.total) + kMine * threadIdx.x;
     u64 sum = 0, all;
 #pragma unroll
     for (int q = 0; q < kMine; ++q) sum += total[q];
     u64 at = block_before(sum, &all);
+    *bin = 0;
+    *before = 0;
+    if (all < n) return false;
     if (at < n && at + sum >= n) {
 #pragma unroll
       for (int q = 0; q < kMine; ++q) {
@@ -405,6 +408,7 @@ struct Sampler {
     *bin = (int)S.found[0];
     *before = S.found[1];
     __syncthreads();
+    return true;
   }
 
   // The keys whose value `bin` (which does not rise with the key) puts into b1 .. b2: a warp for each end, 32 keys a step.
@@ -768,9 +772,10 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
       bins_over(distance_to(R.floor));
     }
     R.histogram<uint32_t>(everything, distance_bin);
-    R.find<uint32_t>((u64)k, &b, &above);
-    Keys r = R.keys_of(b, b, distance_bin);
-    R.settle<uint32_t>(r, (u64)k - above, everything, &cut, &last);
+    if (R.find<uint32_t>((u64)k, &b, &above)) {   // (an infinite top's floor may leave fewer: all of them stay)
+      Keys r = R.keys_of(b, b, distance_bin);
+      R.settle<uint32_t>(r, (u64)k - above, everything, &cut, &last);
+    }
   }
   if (by_p) {
     // The top alone weighs 1, so tokens of less than (1 - top_p) / V cannot make up what may go: the border is within

@@ -78,3 +78,22 @@ def test_min_p_next_to_1(qmm, top, temperature):
     tokens, logprobs = run(qmm, x.cuda(), rows, u.cuda())
     for t in range(T):
         assert tokens[t].item() == want[t][0] and near(logprobs[t].item(), want[t][1]), (t, rows[t], x[t, 2000].item())
+
+
+@pytest.mark.parametrize("V,n", [(20000, 2000), (20000, 1024), (20000, 1025), (100003, 9000), (248320, 3)])
+def test_many_infinite_logits(qmm, V, n):
+    """+inf logits share the weight; top_k counts them and then the others, which weigh nothing."""
+    x, u = logits(9, V, seed=3)
+    g = torch.Generator(device="cuda").manual_seed(V)
+    at = torch.stack([torch.randperm(V, generator=g, device="cuda")[:n].sort().values for _ in range(9)])
+    x.scatter_(1, at, INF)
+    for k in (0, 1, n - 1, n, n + 1, 5000, V - 1):
+        for p, mp in ((1.0, 0.0), (0.5, 0.0), (1.0, 0.3), (0.25, 1.0)):
+            if k > V:
+                continue
+            tokens, logprobs = run(qmm, x, [(1.0, k, p, mp)], u)
+            for t in range(9):
+                stays = at[t, :k or n].tolist()
+                stays = stays[:math.ceil(p * len(stays))]      # the weights before a token's are less than p of all
+                token, logprob = of_equal_weights(stays, u[t].double().item())
+                assert tokens[t].item() == token and near(logprobs[t].item(), logprob), (k, p, mp, t)
