@@ -65,19 +65,25 @@ constexpr Table make_table() {
 }
 __device__ constexpr Table kTable = make_table();
 
-// log2(e) / T in two fp32 words: the rounded quotient, and what it leaves (a 64-bit division takes 4000 cycles).
+// log2(e) / T in two fp32 words: the rounded quotient, and what it leaves (a 64-bit division takes 4000 cycles).  Logits and
+// temperature are taken in units of 2^64 where T is above that: their differences may leave fp32's range, and the quotient's words
+// its precision, while a weight hangs on nothing of a logit below 2^-42 T.
 struct Slope {
-  float hi, lo;
+  float hi, lo, unit;
 };
 __device__ __forceinline__ Slope slope_of(float temperature) {
+  const float unit = temperature > 0x1p64f ? 0x1p-64f : 1.0f;
+  temperature *= unit;
   constexpr float kHi = 1.44269502162933349609375f, kLo = 1.92596299112661746e-8f;   // log2(e)
   const float hi = __fdiv_rn(kHi, temperature);
-  return Slope{hi, hi > 0.0f && hi < INFINITY ? __fdiv_rn(__fmaf_rn(-hi, temperature, kHi) + kLo, temperature) : 0.0f};
+  return Slope{hi, hi > 0.0f && hi < INFINITY ? __fdiv_rn(__fmaf_rn(-hi, temperature, kHi) + kLo, temperature) : 0.0f, unit};
 }
 
 // The weight of logit x (not NaN, not above top) as an integer.
 __device__ __forceinline__ u64 weight(float x, float top, Slope c, const u64* table) {
   if (x == top) return u64(1) << kUnit;   // (also where both are infinite)
+  x *= c.unit;
+  top *= c.unit;
   const float d = x - top;                // two words: the rounded difference and what it lost
   const float b = d - x, lost = (x - (d - b)) + (-top - b);
   const float th = d * c.hi;
@@ -596,6 +602,8 @@ __device__ __forceinline__ float logprob_of(float v, float top, Slope c, u64 tot
   const float whole = (float)(e - kUnit) + (float)j * (1.0f / kSteps);        // exact
   float th = 0.0f, tl = 0.0f;
   if (v != top) {
+    v *= c.unit;
+    top *= c.unit;
     const float d = v - top, b = d - v, lost = (v - (d - b)) + (-top - b);
     th = d * c.hi;
     tl = __fmaf_rn(d, c.hi, -th) + __fmaf_rn(d, c.lo, lost * c.hi);
@@ -722,6 +730,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
     return;
   }
   R.c = slope_of(temperature);
+  const float slope = R.c.hi * R.c.unit;
   const int k = a.top_k ? a.top_k[t] : 0;
   const float p = a.top_p ? a.top_p[t] : 1.0f, mp = a.min_p ? a.min_p[t] : 0.0f;
   const bool by_k = k > 0 && k < V, by_p = p < 1.0f;
@@ -780,7 +789,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
   if (by_p) {
     // The top alone weighs 1, so tokens of less than (1 - top_p) / V cannot make up what may go: the border is within
     // `reach` of the top, and so are all bins but the last one, which has what lies further down too.
-    const float reach = log2f((float)V / (1.0f - fmaxf(p, 0.0f))) * 1.001f / R.c.hi;
+    const float reach = log2f((float)V / (1.0f - fmaxf(p, 0.0f))) * 1.001f / slope;
     bins_over(fminf(reach, distance_to(R.floor)));
     R.histogram<u64>(in, half_bin);
     const u64 all = R.mass_of_bins();
@@ -801,11 +810,11 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
     R.settle<u64>(r, target - above, in, &key, &index);
     cut = key;
     last = index;
-  } else if (mp > 0.0f && R.c.hi > 0.0f) {   // (a slope of 0: all weights are 1, and none is far enough down)
+  } else if (mp > 0.0f && slope > 0.0f) {   // (a slope of 0: all weights are 1, and none is far enough down)
     // What stays weighs min_p less a weight's rounding at least; a millionth of it less again covers fp32's own in the distance,
     // which is 0 where min_p is 1.
     const float lightest = fmaxf(__fmaf_rn(fminf(mp, 1.0f), 1.0f - 0x1p-20f, -0x1p-40f), 0x1p-44f);
-    const Raised now = R.raise_floor(max(cut, key_within(-log2f(lightest) / R.c.hi)), in);
+    const Raised now = R.raise_floor(max(cut, key_within(-log2f(lightest) / slope)), in);
     if (now == kAlone) end_alone(a, R, t, R.listed, p, mp, least, 0);
     if (now != kSpread) return;
   }

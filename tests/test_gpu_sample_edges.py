@@ -97,3 +97,30 @@ def test_many_infinite_logits(qmm, V, n):
                 stays = stays[:math.ceil(p * len(stays))]      # the weights before a token's are less than p of all
                 token, logprob = of_equal_weights(stays, u[t].double().item())
                 assert tokens[t].item() == token and near(logprobs[t].item(), logprob), (k, p, mp, t)
+
+
+def test_logits_whose_difference_leaves_fp32(qmm):
+    """Logits of both signs near the largest fp32: their difference over a large temperature is an ordinary number."""
+    V = 2000
+    x = torch.full((8, V), -INF)
+    at = [(5, 3e38), (900, -3e38), (901, -2.5e38), (1700, 1e38)]
+    for i, v in at:
+        x[:, i] = v
+    u = (torch.arange(8) + 0.5) / 8
+    for temperature in (INF, 3.4e38, 1e38, 2.0 ** 125):
+        for k, mp in ((0, 0.0), (3, 0.0), (0, 0.05), (4, 0.01)):
+            tokens, logprobs = run(qmm, x.cuda(), [(temperature, k, 1.0, mp)], u.cuda())
+            exact = {i: torch.tensor(v).double().item() for i, v in at}
+            scale = torch.tensor(temperature).double().item()
+            w = {i: math.exp((v - exact[5]) / scale) for i, v in exact.items()}
+            if k:
+                w = {i: w[i] for i in sorted(w, key=lambda i: -exact[i])[:k]}
+            w = {i: w[i] for i in sorted(w) if w[i] >= mp}
+            total = sum(w.values())
+            for t in range(8):
+                upto = 0.0
+                for i in w:
+                    upto += w[i]
+                    if upto > u[t].item() * total:
+                        break
+                assert tokens[t].item() == i and near(logprobs[t].item(), math.log(w[i] / total)), (temperature, k, mp, t)
