@@ -12,19 +12,21 @@
 //     S^T = K Q^T        tcgen05, K (128 keys x D) from tensor memory, where four warps put it, a thread a key
 //     p = 2^(c S + off)  a thread per key, S^T from tensor memory, c = scale k_scale log2 e over the row's power of two
 //     O^T += V^T p^T     tcgen05, V and p^T (both MN-major) from shared memory; four more warps write V
-//     l += p 1           tcgen05, 16 columns of ones: the rows' sums of weights, a row a lane
+//     l += p             the fp32 weights as they are before their rounding, added up over a warp's keys in the softmax
 // so few rows cost little, the exponentials of a row are spread over 128 threads, and no 128-row tile of queries
 // is read again for every tile.  Two groups of softmax warps have the key tiles in turn, with sums of their own that are
 // joined at a segment's end: what a tile costs a group besides its rows (waits, votes, fences) is then paid once for all of them.
 // off moves, and O^T is rescaled, only when a row's maximum grew by more than 8; weights are then at most 2^15, and
-// fp16 holds those down to 2^-21 of the largest at full precision.
+// fp16 holds those down to 2^-21 of the largest at full precision.  (l as a product of the rounded weights with ones took 205 us
+// and 304 us in the calls below, but lse was off by up to 2^-12 where few keys have the weight, and by 2^-15 from the tensor cores' own
+// rounding of long sums.)
 //
 // A role's work for a tile of 60 rows takes some 1300 to 1800 cycles (values to fp16 1400, keys 1300, the products' issue
-// 1100 and 700, a group's softmax 3000 for every other tile), a tile 2100: the roles wait for each other at most a third of
+// 1100 and 700, a group's softmax some 3400 for every other tile), a tile 2250: the roles wait for each other at most a third of
 // the time, and each one's instructions wait for their own way to the warp more than for anything else (without the
-// exponentials, without the conversions or with half the products a tile takes 4 to 10 % less).  Measured: 4 streams of 8 rows
-// behind 131072 keys 201 us (three blocks of rows, 2.3 TB/s of packed keys in all); 24 streams of 19000 to 41000 keys of
-// their own 292 us (2.8 TB/s).
+// exponentials, without the conversions or with half the products a tile takes 4 to 10 % less, without the sums l 7 %).  Measured: 4 streams of 8 rows
+// behind 131072 keys 220 us (three blocks of rows, 2.1 TB/s of packed keys in all); 24 streams of 19000 to 41000 keys of
+// their own 299 us (2.7 TB/s).
 //
 // Keys that a row may not see are set to -inf by position, so their K may hold anything.  Value rows behind the last key
 // are zeroed, and so are NaN blocks among the keys that only some rows of the block see (a draft's last keys);
@@ -58,11 +60,13 @@ constexpr int kThreads = 20 * 32, kGroupWarps = 4;
 constexpr uint32_t kTmemCols = 512;
 constexpr int kKeyBufs = 3;          // of 64 values of a tile's keys, in tensor memory
 constexpr int kScoreBufs = 4;        // two for each group
-constexpr int kOnesN = 16;           // columns of l, all the same
 // Packed tiles in shared memory, of keys and of values in turn.  An even number, so that a role's next use of one follows its
 // own last, and its wait takes no phase before that for it.  (Ten fit: 4 streams behind 131072 keys 203 us, 201.)
 constexpr int kPacks = 8;
 static_assert(kPacks % 2 == 0, "a pack is one role's");
+// A row's weights of a tile are added up over four lanes by exchanges and over eight through shared memory, a run of rows behind
+// the other for each of the eight (a step of 68 floats: no bank conflict either way).
+constexpr int kPartsOf = 8, kPartStep = kN + 4;
 constexpr int kFactorTiles = 8;      // (the softmax is a few query tiles behind)
 constexpr float kGrow = 8.0f;
 constexpr float kLift = 7.0f;        // log2 of the largest weight when off is set
@@ -81,21 +85,20 @@ struct Smem {
   static constexpr int kV = 0;
   static constexpr int kQ = kV + kValueBufs * kVBytes;
   static constexpr int kP = kQ + 2 * kQBytes;
-  static constexpr int kOnes = kP + 2 * kPBytes;         // 64 keys of kOnesN ones
-  static constexpr int kOnesBytes = kOnesN * 128;
-  static constexpr int kPack = kOnes + kOnesBytes;
+  static constexpr int kPack = kP + 2 * kPBytes;
   static constexpr int kFactors = kPack + kPacks * kPackBytes;   // of the rows of the last kFactorTiles query tiles
   static constexpr int kOff = kFactors + kFactorTiles * kN * 4;  // each softmax warp's copy of its group's rows' off
   static constexpr int kRed = kOff + 2 * kGroupWarps * kN * 4;   // the softmax warps' maxima of the rows
-  static constexpr int kMisc = kRed + 2 * kGroupWarps * kN * 4;
+  static constexpr int kParts = kRed + 2 * kGroupWarps * kN * 4; // and the parts of a tile's sums
+  static constexpr int kMisc = kParts + 2 * kGroupWarps * kPartsOf * kPartStep * 4;
   static constexpr int kTotal = kMisc + 1024;
 };
 static_assert(Smem<128>::kTotal <= 227 * 1024 && Smem<64>::kTotal <= 227 * 1024, "shared memory");
 
-// Tensor memory: K at 0, then S^T (tile t's in t % kScoreBufs), O^T and l of each group.  (l has the rows as its lanes.)
+// Tensor memory: K at 0, then S^T (tile t's in t % kScoreBufs), and O^T of each group.
 struct Tmem {
-  static constexpr uint32_t kS = kKeyBufs * 32, kO = kS + kScoreBufs * kN, kL = kO + 2 * kN;
-  static_assert(kL + 2 * kOnesN <= kTmemCols, "tensor memory");
+  static constexpr uint32_t kS = kKeyBufs * 32, kO = kS + kScoreBufs * kN;
+  static_assert(kO + 2 * kN <= kTmemCols, "tensor memory");
 };
 
 // Barriers; a wait tells a phase from the one after it only, and every wait here is for the phase of a tile (or a segment)
@@ -146,6 +149,22 @@ __device__ __forceinline__ bool any_of(bool mine, int id, int threads) {
   asm volatile("{\n .reg .pred p, q;\n setp.ne.b32 p, %1, 0;\n barrier.cta.red.or.pred q, %2, %3, p;\n selp.u32 %0, 1, 0, q;\n}"
                : "=r"(any) : "r"((uint32_t)mine), "r"(id), "r"(threads) : "memory");
   return any != 0;
+}
+
+// Four sums over four lanes each of sixteen values of every lane: lane l has those of values 4 (l / 8) and on, over the lanes that
+// are l modulo 8.  (At each step a lane gives half of what it has to the one across and takes that one's other half.)
+__device__ __forceinline__ float4 sum_over_four(float (&x)[16]) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int n = 8; n >= 4; n /= 2) {
+    const bool upper = lane & 2 * n;
+#pragma unroll
+    for (int q = 0; q < n; ++q) {
+      const float give = upper ? x[q] : x[q + n], keep = upper ? x[q + n] : x[q];
+      x[q] = keep + __shfl_xor_sync(0xffffffffu, give, 2 * n);
+    }
+  }
+  return make_float4(x[0], x[1], x[2], x[3]);
 }
 
 // The wait for a phase that has not completed yet (out of line: the roles' loops stay short).
@@ -208,9 +227,6 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fp4_kernel(const __grid_cons
   }
   // Launched early (behind a launch that allows it), this grid reads what was written before it from
   // here on; the combine launch, which reads the lengths before its own wait, may start from here on.
-  for (int k = threadIdx.x; k < L::kOnesBytes / 4; k += kThreads)
-    reinterpret_cast<uint32_t*>(smem + L::kOnes)[k] = 0x3C003C00u;
-  fence_proxy_async_smem();
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   deal<kThreads, kTile, kLead>(P, M.piece, &g_status);
@@ -372,16 +388,12 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fp4_kernel(const __grid_cons
   } else if (warp == kSumWarp) {
     // ------------------------------------------------------------------ tensor cores, weighted sums
     if (elect_one()) {
-      constexpr uint32_t kMnMajorA = 1u << 15, kMnMajorB = 1u << 16;   // V and p
+      constexpr uint32_t kMnMajorA = 1u << 15, kMnMajorB = 1u << 16;   // V and p^T
       constexpr uint32_t kIdBoth = tc::idesc_16_f32(128, kN, false, false) | kMnMajorB;
       constexpr uint32_t kIdHalf = tc::idesc_16_f32(128, kHalf, false, false) | kMnMajorB;
       const uint64_t dp = tc::smem_desc_sw128(smem_addr(smem + L::kP), 16, 1024);
       // D = 64: O^T has 128 lanes all the same; the upper ones are products with other keys, and nobody reads them
       const uint64_t dv = tc::smem_desc_sw128(smem_addr(smem + L::kV), D == 128 ? L::kVHalf : L::kVHalf / 2, 1024);
-      // l = p 1^T: p as the 128-row operand, whose upper rows (the next eight keys, and 1 KB behind p) nobody reads
-      constexpr uint32_t kIdSum = tc::idesc_16_f32(128, kOnesN, false, false) | kMnMajorA;
-      const uint64_t dpa = tc::smem_desc_sw128(smem_addr(smem + L::kP), 1024, 1024);
-      const uint64_t ones = tc::smem_desc_sw128(smem_addr(smem + L::kOnes), 16, 1024);
       uint32_t tile = 0, segs = 0;
       bool ok = true;
       while (ok && next_of(walk, P, g)) {
@@ -400,7 +412,6 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fp4_kernel(const __grid_cons
             const uint32_t p = (buf * L::kPBytes + k * 64 * 128) >> 4;
             mma_ss_x4(tmem + T::kO + kN * buf, dv + ((vb * L::kVBytes + k * 64 * 128) >> 4), 128, dp + p, 128, id | kMnMajorA,
                       !fresh || k > 0);
-            mma_ss_x4(tmem + T::kL + kOnesN * buf, dpa + p, 128, ones, 0, kIdSum, !fresh || k > 0);
           }
           tc::commit(bar(kBarO + buf));
           tc::commit(bar(kBarValueEmpty + vb));
@@ -512,6 +523,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fp4_kernel(const __grid_cons
     const uint32_t lanes = (uint32_t)wg << 21;        // first TMEM lane << 16
     float* off = reinterpret_cast<float*>(smem + L::kOff) + warp * kN;
     float* red = reinterpret_cast<float*>(smem + L::kRed) + grp * kGroupWarps * kN;
+    float* parts = reinterpret_cast<float*>(smem + L::kParts) + warp * kPartsOf * kPartStep;
     auto any_here = [&](bool x) { return any_of(x, 1 + grp, 32 * kGroupWarps); };
     uint32_t tile = 0, segs = 0;
     bool ok = true;
@@ -522,6 +534,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fp4_kernel(const __grid_cons
       ++segs;
       off[lane] = off[kHalf + lane] = 0.0f;
       __syncwarp();
+      float sum[2] = {0.0f, 0.0f};   // of the warp's weights of rows lane and kHalf + lane
       bool first = true, leave = false;   // leave: the whole group knows that a wait gave up
       for (int j = g.j0; j < j1; ++j, ++tile) {
         const uint32_t buf = tile & 1, phase = (tile >> 1) & 1, at = tile % kScoreBufs;
@@ -573,6 +586,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fp4_kernel(const __grid_cons
               }
               *reinterpret_cast<uint4*>(p + ((r / 8 + h) ^ (mine & 7)) * 16) = make_uint4(w[0], w[1], w[2], w[3]);
             }
+            *reinterpret_cast<float4*>(parts + lane % 8 * kPartStep + r + lane / 8 * 4) = sum_over_four(x);
           }
           return most;
         };
@@ -605,10 +619,11 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fp4_kernel(const __grid_cons
                 const float now = top > -INFINITY && (first || top > kLift + kGrow) ? was - (top - kLift) : was;
                 keep[h] = exp2_fast(now - was);
                 off[r] = now;
+                sum[h] *= keep[h];
               }
             }
             __syncwarp();
-            if (!first) {   // O^T and l: the products of the group's tile before are in them
+            if (!first) {   // O^T: the products of the group's tile before are in it
 #pragma unroll 1
               for (int r0 = 0; r0 < rows; r0 += 8) {
                 uint32_t o[8];
@@ -618,13 +633,6 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fp4_kernel(const __grid_cons
                 for (int r = 0; r < 8; ++r)
                   o[r] = __float_as_uint(__uint_as_float(o[r]) * __shfl_sync(0xffffffffu, of, (r0 & (kHalf - 1)) + r));
                 tc::st_x8(tmem + lanes + T::kO + kN * grp + r0, o);
-              }
-              if (wg < 2) {   // (its first column is read in the end)
-                uint32_t l[8];
-                tc::ld_wait_x8(tmem + lanes + T::kL + kOnesN * grp, l);
-#pragma unroll
-                for (int r = 0; r < 8; ++r) l[r] = __float_as_uint(__uint_as_float(l[r]) * (wg ? keep[1] : keep[0]));
-                tc::st_x8(tmem + lanes + T::kL + kOnesN * grp, l);
               }
               tc::wait_st();
             }
@@ -641,6 +649,16 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fp4_kernel(const __grid_cons
           mbar_arrive(bar(kBarP + buf));
           mbar_arrive(bar(kBarSFree + at));
         }
+        // (the parts were written ahead of the warp's last barrier, and are written again behind its next one)
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+          if (kHalf * h < rows) {
+            const float* x = parts + kHalf * h + lane;
+            float a[kPartsOf / 2];
+#pragma unroll
+            for (int q = 0; q < kPartsOf / 2; ++q) a[q] = x[2 * q * kPartStep] + x[(2 * q + 1) * kPartStep];
+            sum[h] += (a[0] + a[1]) + (a[2] + a[3]);
+          }
       }
 
       // ---- the segment's sums to the workspace
@@ -648,12 +666,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fp4_kernel(const __grid_cons
       // phase for the one after it)
       const uint32_t last = tile - 1 - ((tile - 1 - grp) & 1);
       if (!leave && (n > 1 || last == tile - 1)) ok = wait_w(kBarO + grp, (last >> 1) & 1) && ok;
-      if (wg < 2) {   // lane r: row kHalf wg + r's
-        uint32_t l[8];
-        tc::fence_after_sync();
-        tc::ld_wait_x8(tmem + lanes + T::kL + kOnesN * grp, l);
-        red[kHalf * wg + lane] = __uint_as_float(l[0]);
-      }
+      red[wg * kN + lane] = sum[0];
+      red[wg * kN + kHalf + lane] = sum[1];
       if (any_of(!ok || leave, 3, 64 * kGroupWarps)) break;
       tc::fence_after_sync();
       // Each group joins both groups' sums of half of the rows, from c0 on; lane r has row c0 + r: its sum, its exponent, what
@@ -663,7 +677,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fp4_kernel(const __grid_cons
       const uint32_t tO = tmem + lanes + T::kO + c0;
       auto sum_of = [&](int gr) -> float {
         const float* x = reinterpret_cast<const float*>(smem + L::kRed) + gr * kGroupWarps * kN + row;
-        return x[0];
+        return (x[0] + x[kN]) + (x[2 * kN] + x[3 * kN]);
       };
       const float* offs = reinterpret_cast<const float*>(smem + L::kOff) + row;
       float f[2] = {0.0f, 0.0f}, all = 0.0f, top = -INFINITY;
