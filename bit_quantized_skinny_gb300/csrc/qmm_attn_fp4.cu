@@ -858,14 +858,16 @@ __global__ void __launch_bounds__(kExpandThreads) expand_kernel(const __grid_con
   const int64_t run_of = blockIdx.x / P.chunks, p = run_of / a.Hk;
   const int first = (int)(blockIdx.x - run_of * P.chunks) * P.blocks, h = (int)(run_of - p * a.Hk);
   if (h == 0 && first == 0 && threadIdx.x == 0) P.ids[p] = (int32_t)p;
+  // (Of keys that no row sees, a stream's without rows or a prefix's without any stream's, not even the page is looked at.)
   int page, live;
   if (p < P.n_pre) {
-    page = a.prefix_pages[p];
-    live = (int)min((int64_t)a.page_size, a.prefix_len - p * a.page_size);
+    live = a.B > 0 && a.row_starts[a.B] > 0 ? (int)min((int64_t)a.page_size, a.prefix_len - p * a.page_size) : 0;
+    page = live > 0 ? a.prefix_pages[p] : 0;
   } else {
     const int64_t own = p - P.n_pre;
     const int b = (int)(own / a.pages_per_stream);
-    live = (int)min((int64_t)a.page_size, stream_of(a, b).len - (own - (int64_t)b * a.pages_per_stream) * a.page_size);
+    const Stream s = stream_of(a, b);
+    live = s.m > 0 ? (int)min((int64_t)a.page_size, s.len - (own - (int64_t)b * a.pages_per_stream) * a.page_size) : 0;
     page = first < live * kBlocks ? a.pages[own] : 0;
   }
   const int end = min(live * kBlocks, first + P.blocks);

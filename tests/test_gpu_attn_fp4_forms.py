@@ -96,3 +96,22 @@ def test_both_forms_of_a_call(qmm, rows, lens, prefix, Hq, Hk, D, page, dtype):
     u = torch.finfo(dtype).eps / 2
     assert bool(((c.O.double() - O.double()).abs() <= 2 * u * O.double().abs() + 2.0 ** -10 * S + 2.0 ** -24).all())
     assert qmm.device_status() == 0
+
+
+@pytest.mark.parametrize("wide", [False, True])
+def test_pages_that_no_row_needs_may_hold_anything(qmm, wide):
+    """A stream without rows may have any page numbers, and so may the prefix of a call whose rows are all padding."""
+    c = Case([2, 0, 3], [90, 200, 30], 130, 10, 2, 128, 16)
+    c.pages[1] = torch.tensor([-3, 1 << 30], dtype=torch.int32, device="cuda").repeat(c.pages.shape[1])[:c.pages.shape[1]]
+    c = roomy(c) if wide else c
+    assert expands(qmm, c) is not wide
+    c.run(qmm)
+    assert qmm.device_status() == 0
+    c.pages[1] = 0
+    c.check()
+    c = Case([0, 0], [40, 0], 70, 10, 2, 128, 16, pad_rows=4)
+    c.prefix_pages[:], c.pages[:] = -7, 1 << 30
+    c = roomy(c) if wide else c
+    assert expands(qmm, c) is not wide
+    c.run(qmm)
+    assert qmm.device_status() == 0 and bool((c.O == 0).all()) and bool(c.lse.isneginf().all())
