@@ -54,6 +54,11 @@ qmm_status check_attn_shape(const qmm_attn_args& a) {
 bool valid_page(int n) { return n >= 16 && n <= 4096 && (n & (n - 1)) == 0; }
 // A tensor scale of a 4-bit cache: its products with every E4M3 value, and their reciprocals, are ordinary fp32 numbers.
 bool valid_scale(float s) { return s >= 0x1p-60f && s <= 0x1p60f; }
+// The tensor scales of an attention call.  A key's score in units of its codes is below 2^34.4 (128 products of a query below 2^16 and
+// of 2688) and enters the softmax times scale k_scale log2 e: finite in fp32 up to 2^93.  (0 times an infinite factor would be NaN.)
+bool valid_scales(const qmm_attn_fp4_args& a) {
+  return valid_scale(a.k_scale) && valid_scale(a.v_scale) && (double)a.base.scale * a.k_scale <= 0x1p93;
+}
 
 // What a qmm_norm_rope call may not be, for either cache; QMM_OK for a call without rows as well.
 qmm_status check_norm_rope(const qmm_norm_rope_args& a) {
@@ -509,7 +514,7 @@ qmm_status qmm_attn_shared(const qmm_attn_args* args_host, void* workspace_dev, 
 
 size_t qmm_attn_fp4_workspace_bytes(const qmm_attn_fp4_args* args_host) {
   if (!args_host || check_attn_shape(args_host->base) != QMM_OK) return 0;
-  if (!valid_scale(args_host->k_scale) || !valid_scale(args_host->v_scale)) return 0;
+  if (!valid_scales(*args_host)) return 0;
   return q4k::attn_fp4_workspace_bytes(*args_host);
 }
 
@@ -519,7 +524,7 @@ qmm_status qmm_attn_shared_fp4(const qmm_attn_fp4_args* args_host, void* workspa
   const qmm_attn_fp4_args& a = *args_host;
   qmm_status s = check_attn_shape(a.base);
   if (s != QMM_OK) return s;
-  if (!valid_scale(a.k_scale) || !valid_scale(a.v_scale)) return QMM_ERR_SHAPE;
+  if (!valid_scales(a)) return QMM_ERR_SHAPE;
   if (a.base.T == 0) return QMM_OK;
   s = check_attn_pointers(a.base, workspace_dev);
   if (s != QMM_OK) return s;

@@ -439,8 +439,8 @@ qmm_status qmm_norm_rope(const qmm_norm_rope_args* args_host, cudaStream_t strea
  *   Q, O and the caches are 16-byte aligned, row strides multiples of 8; the int arrays and lse
  *   4-byte aligned.
  * Scores, softmax statistics and sums are fp32; the weights of the values are rounded to `type` for
- * the tensor cores, and O is rounded once.  The result does not depend on the other calls of the
- * stream, and the same arguments give the same bits.
+ * the tensor cores, and O is rounded once.  (So a score of 2^20 is off by some 2^-4; from 2^22 on, weights may be
+ * infinite.)  The result does not depend on the other calls of the stream, and the same arguments give the same bits.
  *   workspace_dev: at least qmm_attn_workspace_bytes(args) bytes (it depends on T, Hq and D only),
  *   16-byte aligned; calls that may overlap need one each.  It needs no initialisation.
  * Errors: QMM_ERR_NULL, QMM_ERR_SHAPE, QMM_ERR_TYPE, QMM_ERR_ALIGN, QMM_ERR_BUFSIZE, QMM_ERR_CUDA. */
@@ -521,7 +521,8 @@ qmm_status qmm_kv_fp4_read(const qmm_kv_fp4_read_args* args_host, cudaStream_t s
  * are stored (a code times its scale is exact in 16 bits), the weights of the values are rounded to fp16.
  * bf16 queries are taken to fp16 with a power of two of their row that makes this exact down to 2^-31
  * of the row's largest value.  A NaN that a row sees makes the 16 values of its block of O NaN (in a key: the whole row).
- * Shapes, errors and everything else as qmm_attn_shared; k_scale and v_scale in [2^-60, 2^60].
+ * Shapes, errors and everything else as qmm_attn_shared; k_scale and v_scale in [2^-60, 2^60], scale * k_scale at most
+ * 2^93.
  *   workspace_dev: at least qmm_attn_fp4_workspace_bytes(args) bytes, as there.  With many rows a key (on the average
  * 160 or more pairs of a row and one of the query heads that share a key's head) the call writes the keys and values
  * that its rows may see to the workspace in 16 bits first, unless the page lists have room for more than 1 GiB of them,

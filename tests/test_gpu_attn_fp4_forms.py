@@ -36,7 +36,7 @@ def expands(qmm, c):
     sums = 2 * T * Hq * (4 * D + 16) + 152 * 256 * (4 * D + 16) + 5 * 256
     values = (c.prefix_pages.numel() + c.pages.numel()) * c.page * c.Hk * D * 4
     need = qmm.attn_fp4_workspace_bytes(c.args(qmm))
-    assert need <= sums or need >= sums - 5 * 256 + values
+    assert 0 < need <= sums or need >= sums - 5 * 256 + values
     return need > sums
 
 
@@ -115,3 +115,19 @@ def test_pages_that_no_row_needs_may_hold_anything(qmm, wide):
     assert expands(qmm, c) is not wide
     c.run(qmm)
     assert qmm.device_status() == 0 and bool((c.O == 0).all()) and bool(c.lse.isneginf().all())
+
+
+@pytest.mark.parametrize("wide", [False, True])
+@pytest.mark.parametrize("dtype", [BF16, F16])
+@pytest.mark.parametrize("product,keys", [(2.0 ** 93, 0.0), (2.0 ** -126, 1.0)])
+def test_scales_at_the_ends_of_their_range(qmm, wide, dtype, product, keys):
+    """The smallest factor between a key's score and the softmax's, and the largest one over keys of zeros: all weights are equal."""
+    c = Case([3, 2], [100, 260], 130, 10, 2, 128, 32, dtype, scales=(2.0 ** -5, 0.055))   # (the product is exactly the range's end)
+    c = roomy(c) if wide else c
+    c.scale = product / c.scales[0]
+    c.Q[1] = 0
+    if keys == 0.0:
+        c.K[:] = 0
+    assert expands(qmm, c) is not wide
+    c.run(qmm).check()
+    assert qmm.device_status() == 0
