@@ -179,82 +179,82 @@ __device__ __forceinline__ void deal(const Common& P, Piece& M, unsigned* status
   const qmm_attn_args& a = P.a;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, block = P.block;
   auto units = [](int keys) { return Walker<TILE, LEAD>::units_of(keys); };
-      // the page tables towards L2 while the pieces are worked out: one 128-byte line a thread
-      const int64_t line = ((int64_t)blockIdx.x * THREADS + threadIdx.x) * 32;
-      const int64_t n_pre = (a.prefix_len + a.page_size - 1) >> P.page_shift, n_own = a.B * a.pages_per_stream;
-      if (line < n_pre) asm volatile("prefetch.global.L2 [%0];" :: "l"(a.prefix_pages + line));
-      if (line < n_own) asm volatile("prefetch.global.L2 [%0];" :: "l"(a.pages + line));
-      constexpr int kPer = (QMM_ATTN_MAX_STREAMS + THREADS - 1) / THREADS;
-      Stream str[kPer];
-      int64_t mine[kPer], sum = 0;
-      bool wrong = false;
-      const int rows = a.B > 0 ? clampi(a.row_starts[a.B], 0, a.T) : 0;
-  #pragma unroll
-      for (int q = 0; q < kPer; ++q) {
-        const int b = threadIdx.x * kPer + q;
-        mine[q] = 0;
-        if (b < a.B) {
-          bool bad;
-          str[q] = stream_of(a, b, &bad);
-          wrong |= bad;
-          for (int rb = 0; rb * block < str[q].m; ++rb)
-            mine[q] += (int64_t)a.Hk * units(keys_of(str[q], rb, block));
-        }
-        sum += mine[q];
-      }
-      if (wrong && blockIdx.x == 0) atomicOr(status, kErrIndex);
-      int64_t upto = sum;
-  #pragma unroll
-      for (int off = 1; off < 32; off <<= 1) {
-        const int64_t v = __shfl_up_sync(0xffffffffu, upto, off);
-        if (lane >= off) upto += v;
-      }
-      if (lane == 31) M.scan[warp] = upto;
-      __syncthreads();
-      int64_t before = upto - sum, own = 0;
-  #pragma unroll
-      for (int w = 0; w < THREADS / 32; ++w) {
-        if (w < warp) before += M.scan[w];
-        own += M.scan[w];
-      }
-      const int punits = units((int)a.prefix_len);
-      const int64_t prefix = (int64_t)((rows + block - 1) / block) * a.Hk * punits;
-      const int64_t W = prefix + own;
-      // equal pieces: no CTA has more than ceil(W / CTAs), whichever way the remainder falls
-      const int64_t per = W < (int64_t(1) << 31) ? (int64_t)(((uint32_t)W + gridDim.x - 1) / gridDim.x)
-                                                 : (W + gridDim.x - 1) / gridDim.x;
-      const int64_t w0 = min(W, blockIdx.x * per), w1 = min(W, w0 + per);
-      const int64_t last = w1 - 1;   // its group is the first one the CTA works on
-      if (threadIdx.x == 0) {
-        M.w0 = w0;
-        M.w1 = w1;
-        M.per = per;
-        M.rows = rows;
-        if (w0 < w1 && last < prefix) {
-          const int64_t g = prefix < (int64_t(1) << 31) ? (int64_t)((uint32_t)last / (uint32_t)punits) : last / punits;
-          M.b = -1;
-          M.rb = (int)((uint32_t)g / (uint32_t)a.Hk);
-          M.h = (int)((uint32_t)g - (uint32_t)M.rb * (uint32_t)a.Hk);
-          M.unit = last - g * punits + 1;
-        }
-      }
-      before += prefix;
-  #pragma unroll
-      for (int q = 0; q < kPer; ++q) {
-        const int b = threadIdx.x * kPer + q;
-        if (b < a.B && w0 < w1 && last >= before && last < before + mine[q]) {
-          int64_t at = last - before;
-          int rb = 0, h = 0, n = units(keys_of(str[q], 0, block));
-          while (at >= (int64_t)a.Hk * n) { at -= (int64_t)a.Hk * n; n = units(keys_of(str[q], ++rb, block)); }
-          while (at >= n) { at -= n; ++h; }
-          M.s = str[q];
-          M.b = b;
-          M.rb = rb;
-          M.h = h;
-          M.unit = at + 1;
-        }
-        before += mine[q];
-      }
+  // the page tables towards L2 while the pieces are worked out: one 128-byte line a thread
+  const int64_t line = ((int64_t)blockIdx.x * THREADS + threadIdx.x) * 32;
+  const int64_t n_pre = (a.prefix_len + a.page_size - 1) >> P.page_shift, n_own = a.B * a.pages_per_stream;
+  if (line < n_pre) asm volatile("prefetch.global.L2 [%0];" :: "l"(a.prefix_pages + line));
+  if (line < n_own) asm volatile("prefetch.global.L2 [%0];" :: "l"(a.pages + line));
+  constexpr int kPer = (QMM_ATTN_MAX_STREAMS + THREADS - 1) / THREADS;
+  Stream str[kPer];
+  int64_t mine[kPer], sum = 0;
+  bool wrong = false;
+  const int rows = a.B > 0 ? clampi(a.row_starts[a.B], 0, a.T) : 0;
+#pragma unroll
+  for (int q = 0; q < kPer; ++q) {
+    const int b = threadIdx.x * kPer + q;
+    mine[q] = 0;
+    if (b < a.B) {
+      bool bad;
+      str[q] = stream_of(a, b, &bad);
+      wrong |= bad;
+      for (int rb = 0; rb * block < str[q].m; ++rb)
+        mine[q] += (int64_t)a.Hk * units(keys_of(str[q], rb, block));
+    }
+    sum += mine[q];
+  }
+  if (wrong && blockIdx.x == 0) atomicOr(status, kErrIndex);
+  int64_t upto = sum;
+#pragma unroll
+  for (int off = 1; off < 32; off <<= 1) {
+    const int64_t v = __shfl_up_sync(0xffffffffu, upto, off);
+    if (lane >= off) upto += v;
+  }
+  if (lane == 31) M.scan[warp] = upto;
+  __syncthreads();
+  int64_t before = upto - sum, own = 0;
+#pragma unroll
+  for (int w = 0; w < THREADS / 32; ++w) {
+    if (w < warp) before += M.scan[w];
+    own += M.scan[w];
+  }
+  const int punits = units((int)a.prefix_len);
+  const int64_t prefix = (int64_t)((rows + block - 1) / block) * a.Hk * punits;
+  const int64_t W = prefix + own;
+  // equal pieces: no CTA has more than ceil(W / CTAs), whichever way the remainder falls
+  const int64_t per = W < (int64_t(1) << 31) ? (int64_t)(((uint32_t)W + gridDim.x - 1) / gridDim.x)
+                                             : (W + gridDim.x - 1) / gridDim.x;
+  const int64_t w0 = min(W, blockIdx.x * per), w1 = min(W, w0 + per);
+  const int64_t last = w1 - 1;   // its group is the first one the CTA works on
+  if (threadIdx.x == 0) {
+    M.w0 = w0;
+    M.w1 = w1;
+    M.per = per;
+    M.rows = rows;
+    if (w0 < w1 && last < prefix) {
+      const int64_t g = prefix < (int64_t(1) << 31) ? (int64_t)((uint32_t)last / (uint32_t)punits) : last / punits;
+      M.b = -1;
+      M.rb = (int)((uint32_t)g / (uint32_t)a.Hk);
+      M.h = (int)((uint32_t)g - (uint32_t)M.rb * (uint32_t)a.Hk);
+      M.unit = last - g * punits + 1;
+    }
+  }
+  before += prefix;
+#pragma unroll
+  for (int q = 0; q < kPer; ++q) {
+    const int b = threadIdx.x * kPer + q;
+    if (b < a.B && w0 < w1 && last >= before && last < before + mine[q]) {
+      int64_t at = last - before;
+      int rb = 0, h = 0, n = units(keys_of(str[q], 0, block));
+      while (at >= (int64_t)a.Hk * n) { at -= (int64_t)a.Hk * n; n = units(keys_of(str[q], ++rb, block)); }
+      while (at >= n) { at -= n; ++h; }
+      M.s = str[q];
+      M.b = b;
+      M.rb = rb;
+      M.h = h;
+      M.unit = at + 1;
+    }
+    before += mine[q];
+  }
 }
 
 // ------------------------------------------------------------------------------------------

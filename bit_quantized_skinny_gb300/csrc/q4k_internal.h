@@ -101,10 +101,10 @@ cudaError_t launch_norm_rope_fp4(const qmm_norm_rope_fp4_args& a, cudaStream_t s
 cudaError_t launch_kv_fp4_read(const qmm_kv_fp4_read_args& a, cudaStream_t stream);
 cudaError_t read_and_clear_kv_fp4_status(unsigned* out);
 cudaError_t launch_attn_fp4(const qmm_attn_fp4_args& a, void* workspace, cudaStream_t stream);
-// f's attention over its keys and values in 16 bits: `view` is f.base with fp16 queries, and with fp16 caches and page lists
-// that f's have been written to.  factors: of each row and head, in place of view.scale log2 e (NULL: none).
-cudaError_t launch_attn_expanded(const qmm_attn_fp4_args& f, const qmm_attn_args& view, const float* factors,
-                                 void* workspace, cudaStream_t stream);
+// The products of a 4-bit cache's attention over its keys and values in 16 bits, ahead of the combine launch: `view` has fp16
+// queries, caches and page lists that the call's have been written to.  factors: of each row and head, in place of
+// view.scale log2 e (NULL: none).  *sms: what the combine launch takes.
+cudaError_t launch_attn_expanded(const qmm_attn_args& view, const float* factors, void* workspace, int* sms, cudaStream_t stream);
 size_t attn_fp4_workspace_bytes(const qmm_attn_fp4_args& a);
 cudaError_t read_and_clear_attn_fp4_status(unsigned* out);
 cudaError_t launch_lora(const qmm_lora_entry* entries, int count, const int32_t* ids, int M, int rank_max,

@@ -699,21 +699,12 @@ cudaError_t launch(const qmm_attn_args& a, void* workspace, cudaStream_t stream)
 }
 
 template <int D>
-cudaError_t launch_expanded(const qmm_attn_fp4_args& f, const qmm_attn_args& view, const float* factors, void* workspace,
-                            cudaStream_t stream) {
+cudaError_t launch_expanded(const qmm_attn_args& view, const float* factors, void* workspace, int* sms, cudaStream_t stream) {
   Params P;
-  int sms = 0;
   fill_rows(P, view, workspace);
   P.factors = factors;
-  const cudaError_t e = launch_products<D, QMM_F16, true>(P, &sms, stream);
-  if (e != cudaSuccess) return e;
-  Common C = P;
-  C.a = f.base;
-  C.v_scale = f.v_scale;
-  return f.base.type == QMM_BF16 ? launch_combine<D, QMM_BF16, true>(C, sms, stream)
-                                 : launch_combine<D, QMM_F16, true>(C, sms, stream);
+  return launch_products<D, QMM_F16, true>(P, sms, stream);
 }
-
 
 }  // namespace
 
@@ -725,10 +716,9 @@ cudaError_t launch_attn(const qmm_attn_args& a, void* workspace, cudaStream_t st
   return a.type == QMM_BF16 ? launch<128, QMM_BF16>(a, workspace, stream) : launch<128, QMM_F16>(a, workspace, stream);
 }
 
-cudaError_t launch_attn_expanded(const qmm_attn_fp4_args& f, const qmm_attn_args& view, const float* factors,
-                                 void* workspace, cudaStream_t stream) {
-  return view.D == 64 ? launch_expanded<64>(f, view, factors, workspace, stream)
-                      : launch_expanded<128>(f, view, factors, workspace, stream);
+cudaError_t launch_attn_expanded(const qmm_attn_args& view, const float* factors, void* workspace, int* sms, cudaStream_t stream) {
+  return view.D == 64 ? launch_expanded<64>(view, factors, workspace, sms, stream)
+                      : launch_expanded<128>(view, factors, workspace, sms, stream);
 }
 
 cudaError_t read_and_clear_attn_status(unsigned* out) {

@@ -917,7 +917,7 @@ cudaError_t launch_expand(const qmm_attn_fp4_args& f, void* workspace, cudaStrea
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, expand_kernel<D, TYPE>, P);
+  cudaError_t e = cudaLaunchKernelEx(&cfg, expand_kernel<D, TYPE>, P);
   if (e != cudaSuccess) return e;
   qmm_attn_args view = a;
   view.type = QMM_F16;
@@ -931,7 +931,14 @@ cudaError_t launch_expand(const qmm_attn_fp4_args& f, void* workspace, cudaStrea
     view.Q = P.Q;
     view.ldq = (int64_t)a.Hq * D;
   }
-  return launch_attn_expanded(f, view, TYPE == QMM_BF16 ? P.factors : nullptr, workspace, stream);
+  int sms = 0;
+  e = launch_attn_expanded(view, TYPE == QMM_BF16 ? P.factors : nullptr, workspace, &sms, stream);
+  if (e != cudaSuccess) return e;
+  Common C;
+  const int tokens = kRows / (a.Hq / a.Hk);   // of that kernel's row tiles, two a block
+  fill(C, a, tokens, 2 * tokens, workspace);
+  C.v_scale = f.v_scale;
+  return launch_combine<D, TYPE, true>(C, sms, stream);
 }
 
 template <int D, int TYPE>
