@@ -17,16 +17,16 @@
 // is read again for every tile.  Two groups of softmax warps have the key tiles in turn, with sums of their own that are
 // joined at a segment's end: what a tile costs a group besides its rows (waits, votes, fences) is then paid once for all of them.
 // off moves, and O^T is rescaled, only when a row's maximum grew by more than 8; weights are then at most 2^15, and
-// fp16 holds those down to 2^-21 of the largest at full precision.  (l as a product of the rounded weights with ones took 205 us
-// and 304 us in the calls below, but lse was off by up to 2^-12 where few keys have the weight, and by 2^-15 from the tensor cores' own
+// fp16 holds those down to 2^-21 of the largest at full precision.  (l as a product of the rounded weights with ones took 201 us
+// and 292 us in the calls below, but lse was off by up to 2^-12 where few keys have the weight, and by 2^-15 from the tensor cores' own
 // rounding of long sums.)
 //
 // A role's work for a tile of 60 rows takes some 1300 to 1800 cycles (values to fp16 1400, keys 1300, the products' issue
-// 1100 and 700, a group's softmax some 3400 for every other tile), a tile 2250: the roles wait for each other at most a third of
+// 1100 and 700, a group's softmax some 3400 for every other tile), a tile 2200: the roles wait for each other at most a third of
 // the time, and each one's instructions wait for their own way to the warp more than for anything else (without the
 // exponentials, without the conversions or with half the products a tile takes 4 to 10 % less, without the sums l 7 %).  Measured: 4 streams of 8 rows
-// behind 131072 keys 220 us (three blocks of rows, 2.1 TB/s of packed keys in all); 24 streams of 19000 to 41000 keys of
-// their own 299 us (2.7 TB/s).
+// behind 131072 keys 213 us (three blocks of rows, 2.1 TB/s of packed keys in all); 24 streams of 19000 to 41000 keys of
+// their own 287 us (2.9 TB/s).
 //
 // Keys that a row may not see are set to -inf by position, so their K may hold anything.  Value rows behind the last key
 // are zeroed, and so are NaN blocks among the keys that only some rows of the block see (a draft's last keys);
@@ -51,7 +51,10 @@ namespace {
 __device__ unsigned g_status;   // this file's kernels' status word
 
 constexpr int kTile = 128;           // keys of a key tile
-constexpr int kLead = 8;             // units of a group besides its key tiles: 8 us (4 streams behind 131072 keys 208 us, 6 units 238)
+// Units of a group besides its key tiles.  With 4, 6, 8, 10 and 12: 4 streams of 8 rows behind 131072 keys 259, 235, 213, 214 and 212 us,
+// behind 60000 149, 130, 113, 115 and 115; 24 streams of 19000 to 41000 keys of their own 288, 288, 287, 288 and 289; 29 ragged ones
+// behind 3001 28, 27, 29, 31 and 33.
+constexpr int kLead = 8;
 constexpr int kN = 64;               // rows of a block
 constexpr int kHalf = kN / 2;        // rows up to which the products are half as wide
 // warps: 0-3 and 4-7 softmax, 8 copies, 9 and 11 tensor cores, 10 queries, 12-15 keys and 16-19 values to fp16
@@ -61,7 +64,7 @@ constexpr uint32_t kTmemCols = 512;
 constexpr int kKeyBufs = 3;          // of 64 values of a tile's keys, in tensor memory
 constexpr int kScoreBufs = 4;        // two for each group
 // Packed tiles in shared memory, of keys and of values in turn.  An even number, so that a role's next use of one follows its
-// own last, and its wait takes no phase before that for it.  (Ten fit: 4 streams behind 131072 keys 203 us, 201.)
+// own last, and its wait takes no phase before that for it.
 constexpr int kPacks = 8;
 static_assert(kPacks % 2 == 0, "a pack is one role's");
 // A row's weights of a tile are added up over four lanes by exchanges and over eight through shared memory, a run of rows behind
@@ -782,19 +785,19 @@ struct Expanded {
   }
 };
 
-// A key costs the kernel above 0.054 ns a head for each 64 rows that see it; to 16 bits (656 bytes read, written and read
+// A key costs the kernel above some 0.07 ns a head for each 64 rows that see it; to 16 bits (656 bytes read, written and read
 // again, at HBM's rate) it costs 0.1 ns, and then 0.05 ns for each 128 rows in the 16-bit kernel.  So keys are expanded from
 // kRowsExpanded rows a key on, on the average over the keys that the page lists have room for (the lengths are on the device),
 // unless these are more than the workspace should hold.  Measured, 8 heads of 128 that 5 query heads share, 16 rows a stream
-// behind 32768 keys: 160 rows a key about 79 us either way; 320 rows 99 expanded, 122 not; 640 rows 126 and 206; 5120 rows
-// (64 streams) 632 and 1442.  A prompt of 1000 rows over 8000 keys 153 and 358; 100 rows over them 41 and 63; 60 rows over
-// 300 keys 19.7 and 26.5; 30 streams of 3 rows behind 30000 keys with 1000 of their own 142 and 162.
+// behind 32768 keys: 160 rows a key 78 us either way; 320 rows 100 expanded, 124 not; 640 rows 128 and 213; 5120 rows
+// (64 streams) 589 and 1547.  A prompt of 1000 rows over 8000 keys 153 and 381; 100 rows over them 40 and 65; 60 rows over
+// 300 keys 18 and 26; 30 streams of 3 rows behind 30000 keys with 1000 of their own 142 and 174.
 constexpr int64_t kRowsExpanded = 160;
 constexpr int64_t kMostExpanded = int64_t(1) << 30;   // bytes
 // Where all keys are few, the 16-bit kernel's shorter start is worth the launch ahead of it with any number of rows.  1 stream of 1
-// row: 16 keys 11.6 us expanded, 15.3 not; 700 keys (2.9 MB) 16.0 and 16.7; 4000 (16 MB) 18.6 and 18.6; 8000 (33 MB) 23.8 and
-// 19.7.  4 streams of 8 rows: 700 keys (11 MB) 18.0 and 23.6; 3000 (49 MB) 31.0 and 27.7.  29 ragged streams (18 MB) 23.2 and 26.3;
-// 16 streams of 4 rows and 500 keys (33 MB) 27.7 and 26.2.
+// row: 16 keys 11.4 us expanded, 14.8 not; 700 keys (2.9 MB) 15.9 and 16.4; 4000 (16 MB) 18.6 and 18.4; 8000 (33 MB) 23.8 and
+// 19.5.  4 streams of 8 rows: 700 keys (11 MB) 18.2 and 23.5; 3000 (49 MB) 31.0 and 27.9.  29 ragged streams (18 MB) 23.9 and 29.4;
+// 16 streams of 4 rows and 500 keys (33 MB) 27.7 and 26.4.
 constexpr int64_t kFewExpanded = int64_t(24) << 20;   // bytes
 double expanded_bytes(const qmm_attn_args& a) {
   return (a.prefix_len + (double)a.B * a.pages_per_stream * a.page_size) * a.Hk * a.D * 4;

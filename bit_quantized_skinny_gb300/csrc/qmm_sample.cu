@@ -9,8 +9,8 @@
 //
 // A row is read once, into the shared memory of a cluster's CTAs, and everything else is passes over it there.  What bounds
 // a call: with few rows the barriers and exchanges between the cluster's CTAs, some 700 cycles each (1 row of 248320 18 us);
-// with many, the rows' passes (128 rows: greedy ones 92 us, top_k 50 185, top_k 1000 298, min_p alone 151, top_p alone, the
-// weights of all tokens twice, 521 and 666).
+// with many, the rows' passes (128 rows: greedy ones 92 us, top_k 50 178, top_k 1000 293, min_p alone 151, top_p alone, the
+// weights of all tokens twice, 526 and 671).
 #include <cstdint>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>

@@ -491,7 +491,7 @@ size_t qmm_kv_fp4_bytes(int64_t n_slots, int Hk, int D);
  * (to the last code: what fp32 leaves open is computed in 64 bits), rounded to binary32 and then as above; a value
  * is rounded as above.  The same operands give the same bits in every call.
  *   As qmm_norm_rope, and: page_size a power of two in [16, 4096], base.n_slots a multiple of it, k_scale and
- *   v_scale in [2^-60, 2^60].
+ *   v_scale in [2^-60, 2^60].  (Heads of 256 can be appended and read back; qmm_attn_shared_fp4 takes heads of 64 and 128.)
  * Errors: as qmm_norm_rope. */
 typedef struct {
   qmm_norm_rope_args base;
@@ -527,7 +527,8 @@ qmm_status qmm_kv_fp4_read(const qmm_kv_fp4_read_args* args_host, cudaStream_t s
  * 160 or more pairs of a row and one of the query heads that share a key's head) the call writes the keys and values
  * that its rows may see to the workspace in 16 bits first, unless the page lists have room for more than 1 GiB of them,
  * and with any number of rows if these have room for at most 24 MiB; the size then has room for them, and depends on
- * all sizes in args. */
+ * all sizes in args.  The two ways sum in different orders: O and lse of a call with wider page lists may differ by their
+ * roundings. */
 typedef struct {
   qmm_attn_args base;
   float k_scale, v_scale;
@@ -586,7 +587,8 @@ qmm_status qmm_run_lora(const qmm_lora_entry* entries_host, int count, const int
  * nothing but its row.  NaN and -inf logits are never taken; with +inf logits, these share the weight.  A row
  * without any logit above -inf gives token -1 and logprob -inf.
  *   temperature, top_p, min_p, uniform (fp32) and top_k (int32): device, one for each row.  temperature, top_k, top_p and
- *   min_p may be NULL (1, off, off, off).  A temperature that is not above 0 picks the first token (logprob 0);
+ *   min_p may be NULL (1, off, off, off).  A temperature that is not above 0 picks the first token (logprob 0), with an infinite
+ *   one all logits above -inf weigh the same;
  *   top_k < 1, top_p >= 1 and min_p <= 0 are off, and so is a NaN; u is taken into [0, 1).
  *   T >= 0 rows, 1 <= V <= QMM_SAMPLE_MAX_V; type: QMM_F32, QMM_BF16 or QMM_F16; ld >= V elements between rows, any
  *   alignment that the type needs.  tokens: T int32.  logprobs: T fp32, or NULL.
