@@ -67,12 +67,13 @@ __device__ constexpr Table kTable = make_table();
 
 // log2(e) / T in two fp32 words: the rounded quotient, and what it leaves (a 64-bit division takes 4000 cycles).  Logits and
 // temperature are taken in units of 2^64 where T is above that: their differences may leave fp32's range, and the quotient's words
-// its precision, while a weight hangs on nothing of a logit below 2^-42 T.
+// its precision, while a weight hangs on nothing of a logit below 2^-42 T.  In the same way in units of 2^-64 where T is below
+// those (a logit that is infinite then differs from every other one by too many T's for a weight).
 struct Slope {
   float hi, lo, unit;
 };
 __device__ __forceinline__ Slope slope_of(float temperature) {
-  const float unit = temperature > 0x1p64f ? 0x1p-64f : 1.0f;
+  const float unit = temperature > 0x1p64f ? 0x1p-64f : temperature < 0x1p-64f ? 0x1p64f : 1.0f;
   temperature *= unit;
   constexpr float kHi = 1.44269502162933349609375f, kLo = 1.92596299112661746e-8f;   // log2(e)
   const float hi = __fdiv_rn(kHi, temperature);
@@ -730,7 +731,6 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
     return;
   }
   R.c = slope_of(temperature);
-  const float slope = R.c.hi * R.c.unit;
   const int k = a.top_k ? a.top_k[t] : 0;
   const float p = a.top_p ? a.top_p[t] : 1.0f, mp = a.min_p ? a.min_p[t] : 0.0f;
   const bool by_k = k > 0 && k < V, by_p = p < 1.0f;
@@ -752,7 +752,10 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
   };
   auto half_bin = [&](float v) { return distance_bin(v) >> 1; };   // of weights
   // the lowest key that a token within d of the top can have
-  auto key_within = [&](float d) { return top < INFINITY ? key_of(top - d * (1.0f + 1e-5f) - fabsf(top) * 1e-6f) : top_key; };
+  // (the last term: where d has few bits)
+  auto key_within = [&](float d) {
+    return top < INFINITY ? key_of(top - d * (1.0f + 1e-5f) - fabsf(top) * 1e-6f - 0x1p-147f) : top_key;
+  };
   // a key that no token of the distance bins up to b lies below; the last bin has all that lies further down.  (keys_of() takes
   // 3000 cycles more for the very key: 1 row 18.3 us, 18.8.)
   auto key_down_to = [&](int b) { return b >= kBins - 1 ? 0u : key_within((float)(b + 1) / per); };
@@ -789,7 +792,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
   if (by_p) {
     // The top alone weighs 1, so tokens of less than (1 - top_p) / V cannot make up what may go: the border is within
     // `reach` of the top, and so are all bins but the last one, which has what lies further down too.
-    const float reach = log2f((float)V / (1.0f - fmaxf(p, 0.0f))) * 1.001f / slope;
+    const float reach = log2f((float)V / (1.0f - fmaxf(p, 0.0f))) * 1.001f / R.c.hi / R.c.unit;
     bins_over(fminf(reach, distance_to(R.floor)));
     R.histogram<u64>(in, half_bin);
     const u64 all = R.mass_of_bins();
@@ -810,11 +813,11 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
     R.settle<u64>(r, target - above, in, &key, &index);
     cut = key;
     last = index;
-  } else if (mp > 0.0f && slope > 0.0f) {   // (a slope of 0: all weights are 1, and none is far enough down)
+  } else if (mp > 0.0f && R.c.hi > 0.0f) {   // (a slope of 0: all weights are 1, and none is far enough down)
     // What stays weighs min_p less a weight's rounding at least; a millionth of it less again covers fp32's own in the distance,
     // which is 0 where min_p is 1.
     const float lightest = fmaxf(__fmaf_rn(fminf(mp, 1.0f), 1.0f - 0x1p-20f, -0x1p-40f), 0x1p-44f);
-    const Raised now = R.raise_floor(max(cut, key_within(-log2f(lightest) / slope)), in);
+    const Raised now = R.raise_floor(max(cut, key_within(-log2f(lightest) / R.c.hi / R.c.unit)), in);
     if (now == kAlone) end_alone(a, R, t, R.listed, p, mp, least, 0);
     if (now != kSpread) return;
   }

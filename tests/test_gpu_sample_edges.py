@@ -124,3 +124,34 @@ def test_logits_whose_difference_leaves_fp32(qmm):
                     if upto > u[t].item() * total:
                         break
                 assert tokens[t].item() == i and near(logprobs[t].item(), math.log(w[i] / total)), (temperature, k, mp, t)
+
+
+@pytest.mark.parametrize("temperature", [2.0 ** -149, 2.0 ** -140, 1e-42, 1e-39, 3e-38, 2.0 ** -70])
+def test_temperatures_and_logits_next_to_zero(qmm, temperature):
+    """Logits that differ by a few of the smallest temperatures, and others that are all far below."""
+    V = 3000
+    T = torch.tensor(temperature).double().item()
+    x = torch.full((8, V), -1.0)
+    x[:, 1::2] = -3e38
+    at = {700: 0.0, 701: -T, 1500: -3 * T, 2500: -T, 2999: -6 * T}
+    for i, v in at.items():
+        x[:, i] = v                                              # (exact: a few bits times a power of two, or rounded as `exact` is)
+    exact = {i: x[0, i].double().item() for i in at}
+    u = (torch.arange(8) + 0.5) / 8
+    for k, p, mp in ((0, 1.0, 0.0), (3, 1.0, 0.0), (0, 1.0, 0.2), (0, 0.8, 0.0), (4, 0.9, 0.01)):
+        tokens, logprobs = run(qmm, x.cuda(), [(temperature, k, p, mp)], u.cuda())
+        w = {i: math.exp(v / T) for i, v in exact.items()}
+        order = sorted(w, key=lambda i: (-exact[i], i))[:k or None]
+        limit, before, stays = torch.tensor(p).item() * sum(w[i] for i in order), 0.0, []
+        for i in order:
+            if (p == 1.0 or before < limit) and w[i] >= mp:
+                stays.append(i)
+            before += w[i]
+        total = sum(w[i] for i in stays)
+        for t in range(8):
+            upto = 0.0
+            for i in sorted(stays):
+                upto += w[i]
+                if upto > u[t].item() * total:
+                    break
+            assert tokens[t].item() == i and near(logprobs[t].item(), math.log(w[i] / total)), (k, p, mp, t)
