@@ -439,7 +439,7 @@ qmm_status qmm_norm_rope(const qmm_norm_rope_args* args_host, cudaStream_t strea
  *   Q, O and the caches are 16-byte aligned, row strides multiples of 8; the int arrays and lse
  *   4-byte aligned.
  * Scores, softmax statistics and sums are fp32; the weights of the values are rounded to `type` for
- * the tensor cores, and O is rounded once.  (So a score of 2^20 is off by some 2^-4; from 2^22 on, weights may be
+ * the tensor cores, and O is rounded once.  (So a score of 2^20 is off by some 2^-4; from 2^26 on, weights may be
  * infinite.)  The result does not depend on the other calls of the stream, and the same arguments give the same bits.
  *   workspace_dev: at least qmm_attn_workspace_bytes(args) bytes (it depends on T, Hq and D only),
  *   16-byte aligned; calls that may overlap need one each.  It needs no initialisation.
